@@ -42,7 +42,9 @@ EXPORTED = ["dg_status_string", "dg_version", "dg_set_device_checks", "dg_device
             "dg_canvas_step_workspace", "dg_canvas_step",
             "dg_lm_weight_packed_bytes", "dg_pack_lm_weight",
             "dg_canvas_step_fp8_workspace", "dg_canvas_step_fp8",
-            "dg_canvas_step_sc_workspace", "dg_canvas_step_sc", "dg_canvas_step_plan"]
+            "dg_canvas_step_sc_workspace", "dg_canvas_step_sc", "dg_canvas_step_plan",
+            "dg_rope_steps", "dg_qk_norm_rope", "dg_paged_append_workspace", "dg_paged_append",
+            "dg_paged_attn_workspace", "dg_paged_attn"]
 
 
 class DgError(RuntimeError):
@@ -83,6 +85,22 @@ class BlockIO(ctypes.Structure):
                 ("canvas", "argmax", "steps_taken", "mean_entropy", "n_accepted_hist")]
 
 
+class HeadParams(ctypes.Structure):
+    """dg_head_params; keeps the tensors it points to alive (see head_params)."""
+    _fields_ = [("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("rope_steps", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class PagedCacheArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("B", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
+
+
 class CanvasStepPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in
                 ("attn_reserved_sms", "attn_pair", "attn_ctas", "attn_splits", "attn_key_tiles",
@@ -105,6 +123,8 @@ def _lib():
         sp, si, bp, bi = (ctypes.POINTER(StepParams), ctypes.POINTER(StepIO),
                           ctypes.POINTER(BlockParams), ctypes.POINTER(BlockIO))
         ip = ctypes.POINTER(ctypes.c_int)
+        i64 = ctypes.c_int64
+        hp, pc = ctypes.POINTER(HeadParams), ctypes.POINTER(PagedCacheArgs)
         sig = {
             "dg_status_string": ([i32], ctypes.c_char_p),
             "dg_version": ([], i32),
@@ -154,6 +174,14 @@ def _lib():
             "dg_canvas_step_sc_workspace": ([sp, i32, i32, i32, i32], sz),
             "dg_canvas_step_sc": ([vp] * 6 + [i32] * 4 + [f32, vp, vp, vp, sp, si, vp, vp, sz, vp],
                                   i32),
+            "dg_rope_steps": ([vp, i32, vp], i32),
+            "dg_qk_norm_rope": ([vp, i64, vp, i64, vp, i64, vp, i64, vp, i32, hp, vp], i32),
+            "dg_paged_append_workspace": ([], sz),
+            "dg_paged_append": ([vp, i64, vp, i64, vp, i64, vp, i64, vp, i32, hp, pc, vp, vp, sz,
+                                 vp], i32),
+            "dg_paged_attn_workspace": ([i32, i32, pc], sz),
+            "dg_paged_attn": ([vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, f32, i32, i32, pc, vp,
+                               sz, vp], i32),
             "dg_canvas_step_plan": ([sp] + [i32] * 5 + [ctypes.POINTER(CanvasStepPlan)], i32),
         }
         for name, (args, res) in sig.items():
@@ -217,6 +245,160 @@ def encoder_append(q, k_cache, v_cache, P, k_new, v_new, out, scale, workspace, 
                                   _p(k_new), _p(v_new), _p(out), B, L, Hq, Hkv, D, float(scale),
                                   _p(workspace), workspace.numel(), _stream(stream))
     _check(rc, "dg_encoder_append")
+
+
+# ---------------------------------------------------------------- paged cache
+def _refuse(what: str, why: str):
+    e = DgError(1, what)
+    e.args = ("%s: %s" % (e.args[0], why),)
+    raise e
+
+
+def _rows(t: torch.Tensor, heads: int, D: int, what: str, T: Optional[int] = None) -> int:
+    """The row stride of a bf16 tensor [T, heads, D] on the current device whose rows are dense."""
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
+        _refuse(what, "a bf16 CUDA tensor is wanted")
+    n, h, d = t.shape
+    if h != heads or d != D or (T is not None and n != T):
+        _refuse(what, "shape %s where [%s, %d, %d] is wanted"
+                % (tuple(t.shape), "T" if T is None else T, heads, D))
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
+        _refuse(what, "the rows of a tensor are not dense")
+    return s0 if n > 1 else 0
+
+
+def _ints(t: torch.Tensor, n: int, what: str):
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        _refuse(what, "a dense int32 CUDA tensor of %d is wanted" % n)
+
+
+def _on_current(device: torch.device, what: str):
+    if device.index != torch.cuda.current_device():
+        _refuse(what, "the tensors are on %s, which is not the current device" % device)
+
+
+def rope_steps(inv_freq, device="cuda") -> torch.Tensor:
+    """dg_rope_steps: frequencies in radians per position (a sequence or CPU
+    tensor, taken in 64 bits) as the int64 tensor head_params takes."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous().reshape(-1)
+    out = torch.empty(f.numel(), dtype=torch.int64)
+    _check(_lib().dg_rope_steps(f.data_ptr(), f.numel(), out.data_ptr()), "dg_rope_steps")
+    return out.to(device)
+
+
+def head_params(Hq, Hkv, D, rope_steps=None, interleaved=False, q_weight=None, k_weight=None,
+                eps=1e-6, weight_offset=0.0) -> HeadParams:
+    """dg_head_params: rope_steps as the function of that name makes it (its
+    length is half the rotated values of a head), weights bf16 [D]."""
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not torch.bfloat16 or w.numel() != D
+                              or not w.is_contiguous()):
+            _refuse("head_params", "norm weights are dense bf16 [D]")
+    if rope_steps is not None and (rope_steps.dtype is not torch.int64
+                                   or not rope_steps.is_contiguous()):
+        _refuse("head_params", "rope_steps is a dense int64 tensor")
+    p = HeadParams(Hq, Hkv, D, 0 if rope_steps is None else 2 * rope_steps.numel(),
+                   1 if interleaved else 0, eps, weight_offset, _p(rope_steps), _p(q_weight),
+                   _p(k_weight))
+    p.tensors = (rope_steps, q_weight, k_weight)
+    p.ref = ctypes.byref(p)
+    return p
+
+
+class PagedCache:
+    """dg_paged_cache: k, v [n_pages, page_size, Hkv, D] bf16 (pages may be
+    strided), page_table [B, max_pages], kv_len [B], q_start [B + 1] int32.
+    The tensors are read when the kernels run: their values may change between
+    calls, the tensors themselves may not (make another PagedCache)."""
+
+    def __init__(self, k, v, page_table, kv_len, q_start):
+        what = "PagedCache"
+        n_pages, page_size, Hkv, D = k.shape
+        if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or not k.is_cuda:
+            _refuse(what, "bf16 CUDA tensors are wanted")
+        if v.shape != k.shape or v.stride() != k.stride():
+            _refuse(what, "k and v differ in shape or strides")
+        if k.stride()[1:] != (Hkv * D, D, 1):
+            _refuse(what, "the tokens of a page are not dense")
+        if page_table.dim() != 2:
+            _refuse(what, "page_table is [B, max_pages]")
+        B, max_pages = page_table.shape
+        _ints(page_table, B * max_pages, what)
+        _ints(kv_len, B, what)
+        _ints(q_start, B + 1, what)
+        if len({t.device for t in (k, v, page_table, kv_len, q_start)}) != 1:
+            _refuse(what, "the tensors are on different devices")
+        self.k, self.v, self.page_table, self.kv_len, self.q_start = (k, v, page_table, kv_len,
+                                                                      q_start)
+        self.device, self.B, self.Hkv, self.D = k.device, B, Hkv, D
+        self.args = PagedCacheArgs(_p(k), _p(v), _p(page_table), _p(kv_len), _p(q_start),
+                                   k.stride(0) if n_pages > 1 else 0, n_pages, page_size,
+                                   max_pages, B, Hkv, D)
+        self.ref = ctypes.byref(self.args)
+
+
+def qk_norm_rope(q, k, q_out, k_out, positions, p: HeadParams, stream=None):
+    """dg_qk_norm_rope: q [T, Hq, D] -> q_out, k [T, Hkv, D] -> k_out (rows may be
+    strided; either pair may be None), positions [T] int32 (None without rotation)."""
+    what = "dg_qk_norm_rope"
+    x = q if q is not None else k
+    T = x.shape[0]
+    _on_current(x.device, what)
+    if positions is not None:
+        _ints(positions, T, what)
+    rc = _lib().dg_qk_norm_rope(
+        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, T),
+        _p(k), 0 if k is None else _rows(k, p.Hkv, p.D, what, T),
+        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, T),
+        _p(k_out), 0 if k_out is None else _rows(k_out, p.Hkv, p.D, what, T),
+        _p(positions), T, p.ref, _stream(stream))
+    _check(rc, what)
+
+
+def paged_append_workspace() -> int:
+    return int(_lib().dg_paged_append_workspace())
+
+
+def paged_append(k, v, cache: PagedCache, p: HeadParams, workspace, q=None, q_out=None,
+                 positions=None, kv_len_out=None, stream=None):
+    """dg_paged_append: k (normed and rotated) and v [T, Hkv, D] into the cache's pages
+    after each sequence's kv_len tokens; q -> q_out [T, Hq, D] in the same pass;
+    kv_len_out [B] int32 receives the new lengths."""
+    what = "dg_paged_append"
+    T = k.shape[0]
+    _on_current(cache.device, what)
+    if positions is not None:
+        _ints(positions, T, what)
+    if kv_len_out is not None:
+        _ints(kv_len_out, cache.B, what)
+    rc = _lib().dg_paged_append(
+        _p(k), _rows(k, p.Hkv, p.D, what), _p(v), _rows(v, p.Hkv, p.D, what, T),
+        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, T),
+        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, T),
+        _p(positions), T, p.ref, cache.ref, _p(kv_len_out), _p(workspace), workspace.numel(),
+        _stream(stream))
+    _check(rc, what)
+
+
+def paged_attn_workspace(T, Hq, cache: PagedCache) -> int:
+    return int(_lib().dg_paged_attn_workspace(T, Hq, cache.ref))
+
+
+def paged_attn(q, cache: PagedCache, out, scale, workspace, k_new=None, v_new=None, causal=True,
+               window=0, stream=None):
+    """dg_paged_attn: q, out [T, Hq, D] over the cache's pages, and over k_new, v_new
+    [T, Hkv, D] when given (rows may be strided)."""
+    what = "dg_paged_attn"
+    T, Hq, _ = q.shape
+    _on_current(cache.device, what)
+    rc = _lib().dg_paged_attn(
+        _p(q), _rows(q, Hq, cache.D, what),
+        _p(k_new), 0 if k_new is None else _rows(k_new, cache.Hkv, cache.D, what, T),
+        _p(v_new), 0 if v_new is None else _rows(v_new, cache.Hkv, cache.D, what, T),
+        _p(out), _rows(out, Hq, cache.D, what, T), T, Hq, scale, 1 if causal else 0, window,
+        cache.ref, _p(workspace), workspace.numel(), _stream(stream))
+    _check(rc, what)
 
 
 # ---------------------------------------------------------------- step

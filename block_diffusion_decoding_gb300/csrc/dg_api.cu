@@ -104,6 +104,12 @@ int current_device_info(DeviceInfo **out)
         DG_CUDA_TRY(cudaFuncSetAttribute(attn_pair_kernel_d256,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          attn_pair_smem_bytes(256)));
+        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_kernel_d128,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         paged_attn_smem_bytes(128)));
+        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_kernel_d256,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         paged_attn_smem_bytes(256)));
         di.attrs_set = true;
     }
     *out = &di;
@@ -871,6 +877,107 @@ int check_moe_params(const dg_moe_params *p)
     return DG_OK;
 }
 
+
+// ---------------------------------------------------------------- paged cache
+// A row stride given by the caller: 0 stands for dense rows.
+int check_stride(int64_t &stride, int64_t dense)
+{
+    if (stride == 0) stride = dense;
+    if (stride < dense) return DG_ERR_INVALID_ARG;
+    return stride % 8 == 0 ? DG_OK : DG_ERR_ALIGNMENT;
+}
+
+int check_paged_cache(const dg_paged_cache *c, int64_t *page_stride)
+{
+    if (c == nullptr) return DG_ERR_INVALID_ARG;
+    if (!c->k || !c->v || !c->page_table || !c->kv_len || !c->q_start) return DG_ERR_INVALID_ARG;
+    if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->B < 1 || c->Hkv < 1)
+        return DG_ERR_INVALID_ARG;
+    if (c->D != 128 && c->D != 256) return DG_ERR_UNSUPPORTED;
+    if (c->page_size % 16 != 0 || c->page_size > 2048) return DG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c->max_pages) * c->page_size > (1LL << 30)) return DG_ERR_UNSUPPORTED;
+    if (c->Hkv > 1024 || c->n_pages > (1 << 30)) return DG_ERR_UNSUPPORTED;
+    *page_stride = c->page_stride;
+    const int rc = check_stride(*page_stride, static_cast<int64_t>(c->page_size) * c->Hkv * c->D);
+    if (rc != DG_OK) return rc;
+    // tensor-map strides are below 2^40 bytes
+    if (*page_stride >= (1LL << 38)) return DG_ERR_UNSUPPORTED;
+    return aligned16(c->k) && aligned16(c->v) ? DG_OK : DG_ERR_ALIGNMENT;
+}
+
+int check_head_params(const dg_head_params *p)
+{
+    if (p == nullptr) return DG_ERR_INVALID_ARG;
+    if (p->Hq < 1 || p->Hkv < 1 || p->D < 1 || p->rot < 0) return DG_ERR_INVALID_ARG;
+    if (p->interleaved != 0 && p->interleaved != 1) return DG_ERR_INVALID_ARG;
+    if (!(p->eps >= 0.f) || !std::isfinite(p->eps) || !std::isfinite(p->weight_offset))
+        return DG_ERR_INVALID_ARG;
+    if (p->rot > 0 && !p->rope_steps) return DG_ERR_INVALID_ARG;
+    if (p->D % 16 != 0 || p->D > 256 || p->rot % 16 != 0 || p->rot > p->D) return DG_ERR_UNSUPPORTED;
+    if (p->Hq > 16384 || p->Hkv > 1024) return DG_ERR_UNSUPPORTED;
+    if ((p->q_weight && !aligned16(p->q_weight)) || (p->k_weight && !aligned16(p->k_weight)))
+        return DG_ERR_ALIGNMENT;
+    return DG_OK;
+}
+
+// The heads' part of a QkvArgs; q_n, k_n, v_n heads of each kind are done.
+void fill_qkv(QkvArgs &a, const dg_head_params *p, int T, int q_n, int k_n, int v_n)
+{
+    a.T = T;
+    a.D = p->D;
+    a.rot = p->rot;
+    a.interleaved = p->interleaved;
+    a.eps = p->eps;
+    a.weight_offset = p->weight_offset;
+    a.steps = p->rope_steps;
+    a.q_weight = p->q_weight;
+    a.k_weight = p->k_weight;
+    a.nq = q_n;
+    a.nk = k_n;
+    a.heads = q_n + k_n + v_n;
+    a.lanes = 1;
+    while (a.lanes * 8 < p->D) a.lanes *= 2;
+}
+
+// Launches the pass over T tokens' heads.
+int launch_qkv(QkvArgs &a, bool paged, int sms, cudaStream_t st)
+{
+    const int64_t singles = static_cast<int64_t>(a.T) * a.heads * a.lanes;   // threads at one head each
+    const bool four = singles > static_cast<int64_t>(sms) * 2048 * 2 && a.heads >= 4;
+    a.chunks = four ? (a.heads + 3) / 4 : a.heads;
+    const int64_t threads = static_cast<int64_t>(a.T) * a.chunks * a.lanes;
+    const int64_t blocks = std::max<int64_t>(1, (threads + kQkvThreads - 1) / kQkvThreads);
+    if (blocks > 0x7FFFFFFF) return DG_ERR_UNSUPPORTED;
+    auto kern = paged ? (four ? paged_append_kernel_4 : paged_append_kernel_1)
+                      : (four ? qk_norm_rope_kernel_4 : qk_norm_rope_kernel_1);
+    DG_CUDA_TRY(launch_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQkvThreads), 0, st,
+                              use_pdl(st), a));
+    DG_LAUNCHED();
+    return DG_OK;
+}
+
+int paged_slot_rows(int T, int G)
+{
+    return static_cast<int>(std::min<int64_t>(128, static_cast<int64_t>(T) * G));
+}
+
+// Workspace of the paged attention for `ctas` CTAs: header | descriptors |
+// (max, sum) of the part rows | part rows (fp32).
+struct PagedWs {
+    size_t desc, ml, o, total;
+};
+
+PagedWs paged_ws(int ctas, int rows, int D)
+{
+    PagedWs w{};
+    const size_t slots = 2 * static_cast<size_t>(ctas) * rows;
+    w.desc = sizeof(WsHeader);
+    w.ml = w.desc + round_up(static_cast<size_t>(ctas) * sizeof(PagedDesc), 256);
+    w.o = w.ml + round_up(slots * sizeof(float2), 256);
+    w.total = w.o + slots * D * sizeof(float);
+    return w;
+}
+
 }  // namespace
 
 int dg::device_checks() { return g_checks.load(std::memory_order_relaxed); }
@@ -939,6 +1046,219 @@ int dg_canvas_attn(const uint16_t *q, const uint16_t *k_prefix, const uint16_t *
 {
     return attn_run(q, k_prefix, v_prefix, k_canvas, v_canvas, out, B, L, P, P, Hq, Hkv, D, scale,
                     0, workspace, workspace_bytes, stream);
+}
+
+int dg_rope_steps(const double *radians, int n, uint64_t *steps)
+{
+    if (n < 0 || (n > 0 && (!radians || !steps))) return DG_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!std::isfinite(radians[i])) return DG_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        double turns = radians[i] / 6.283185307179586476925;
+        turns -= std::floor(turns);                       // in [0, 1]
+        // rounded to 2^-64 of a turn; a whole turn is none
+        steps[i] = turns >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(turns, 64));
+    }
+    return DG_OK;
+}
+
+int dg_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                    uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                    const int32_t *positions, int T, const dg_head_params *p, void *stream)
+{
+    int rc = check_head_params(p);
+    if (rc != DG_OK) return rc;
+    if (T < 0) return DG_ERR_INVALID_ARG;
+    if (T == 0) return DG_OK;
+    if ((!q && !k) || (q && !q_out) || (k && !k_out)) return DG_ERR_INVALID_ARG;
+    if (p->rot > 0 && !positions) return DG_ERR_INVALID_ARG;
+    const int64_t dq = static_cast<int64_t>(p->Hq) * p->D, dk = static_cast<int64_t>(p->Hkv) * p->D;
+    if (q && ((rc = check_stride(q_stride, dq)) != DG_OK ||
+              (rc = check_stride(q_out_stride, dq)) != DG_OK))
+        return rc;
+    if (k && ((rc = check_stride(k_stride, dk)) != DG_OK ||
+              (rc = check_stride(k_out_stride, dk)) != DG_OK))
+        return rc;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out))
+        return DG_ERR_ALIGNMENT;
+    DeviceInfo *di = nullptr;
+    if ((rc = current_device_info(&di)) != DG_OK) return rc;
+    QkvArgs a{};
+    fill_qkv(a, p, T, q ? p->Hq : 0, k ? p->Hkv : 0, 0);
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.qo_stride = q_out_stride;
+    a.ko_stride = k_out_stride;
+    a.positions = positions;
+    return launch_qkv(a, false, di->sms, as_stream(stream));
+}
+
+size_t dg_paged_append_workspace(void) { return sizeof(WsHeader); }
+
+int dg_paged_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                    const uint16_t *q, int64_t q_stride, uint16_t *q_out, int64_t q_out_stride,
+                    const int32_t *positions, int T, const dg_head_params *p,
+                    const dg_paged_cache *c, int32_t *kv_len_out, void *workspace,
+                    size_t workspace_bytes, void *stream)
+{
+    int rc = check_head_params(p);
+    if (rc != DG_OK) return rc;
+    int64_t page_stride = 0;
+    if ((rc = check_paged_cache(c, &page_stride)) != DG_OK) return rc;
+    if (T < 0 || p->Hkv != c->Hkv || p->D != c->D) return DG_ERR_INVALID_ARG;
+    if (T > 0 && (!k || !v || (q != nullptr) != (q_out != nullptr))) return DG_ERR_INVALID_ARG;
+    if (kv_len_out != nullptr && kv_len_out < c->kv_len + c->B && c->kv_len < kv_len_out + c->B)
+        return DG_ERR_INVALID_ARG;
+    const int64_t dq = static_cast<int64_t>(p->Hq) * p->D, dk = static_cast<int64_t>(p->Hkv) * p->D;
+    if ((rc = check_stride(k_stride, dk)) != DG_OK || (rc = check_stride(v_stride, dk)) != DG_OK)
+        return rc;
+    if (q && ((rc = check_stride(q_stride, dq)) != DG_OK ||
+              (rc = check_stride(q_out_stride, dq)) != DG_OK))
+        return rc;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out))
+        return DG_ERR_ALIGNMENT;
+    if (workspace == nullptr || workspace_bytes < dg_paged_append_workspace())
+        return DG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
+    if (T == 0 && kv_len_out == nullptr) return DG_OK;
+    DeviceInfo *di = nullptr;
+    if ((rc = current_device_info(&di)) != DG_OK) return rc;
+    QkvArgs a{};
+    fill_qkv(a, p, T, q ? p->Hq : 0, p->Hkv, p->Hkv);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.qo_stride = q_out_stride;
+    a.positions = positions;
+    a.k_cache = c->k;
+    a.v_cache = c->v;
+    a.page_stride = page_stride;
+    a.page_size = c->page_size;
+    a.n_pages = c->n_pages;
+    a.max_pages = c->max_pages;
+    a.B = c->B;
+    a.page_table = c->page_table;
+    a.kv_len = c->kv_len;
+    a.q_start = c->q_start;
+    a.kv_len_out = kv_len_out;
+    a.ws = static_cast<WsHeader *>(workspace);
+    return launch_qkv(a, true, di->sms, as_stream(stream));
+}
+
+size_t dg_paged_attn_workspace(int T, int Hq, const dg_paged_cache *c)
+{
+    if (c == nullptr || T < 0 || Hq < 1 || c->Hkv < 1 || Hq % c->Hkv != 0) return 0;
+    if ((c->D != 128 && c->D != 256) || Hq / c->Hkv > 128) return 0;
+    return paged_ws(kAssumedMaxSMs, paged_slot_rows(std::max(T, 1), Hq / c->Hkv), c->D).total;
+}
+
+int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
+                  const uint16_t *v_new, int64_t v_stride, uint16_t *out, int64_t out_stride,
+                  int T, int Hq, float scale, int causal, int window, const dg_paged_cache *c,
+                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    int64_t page_stride = 0;
+    int rc = check_paged_cache(c, &page_stride);
+    if (rc != DG_OK) return rc;
+    if (T < 0 || Hq < 1 || window < 0 || (causal != 0 && causal != 1)) return DG_ERR_INVALID_ARG;
+    if (window > 0 && !causal) return DG_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
+    if (Hq % c->Hkv != 0 || Hq / c->Hkv > 128) return DG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(T) * Hq > (1LL << 30)) return DG_ERR_UNSUPPORTED;
+    if (T > 0 && (!q || !out || (k_new != nullptr) != (v_new != nullptr))) return DG_ERR_INVALID_ARG;
+    const int64_t dq = static_cast<int64_t>(Hq) * c->D, dk = static_cast<int64_t>(c->Hkv) * c->D;
+    if ((rc = check_stride(q_stride, dq)) != DG_OK || (rc = check_stride(out_stride, dq)) != DG_OK)
+        return rc;
+    if (k_new && ((rc = check_stride(k_stride, dk)) != DG_OK ||
+                  (rc = check_stride(v_stride, dk)) != DG_OK))
+        return rc;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
+        return DG_ERR_ALIGNMENT;
+    if (workspace == nullptr || workspace_bytes < dg_paged_attn_workspace(T, Hq, c))
+        return DG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
+    if (T == 0) return DG_OK;
+    if (k_new && (k_stride >= (1LL << 38) || v_stride >= (1LL << 38))) return DG_ERR_UNSUPPORTED;
+    DeviceInfo *di = nullptr;
+    if ((rc = current_device_info(&di)) != DG_OK) return rc;
+    if (di->sms > kAssumedMaxSMs) return DG_ERR_UNSUPPORTED;
+    const int D = c->D, bkv = D == 128 ? 128 : 64;
+    // a box of keys stays inside one page and one key tile: its rows divide both
+    int box_rows = c->page_size & -c->page_size;
+    box_rows = std::min(box_rows, bkv);
+
+    CUtensorMap mk, mv, mkn, mvn;
+    auto page_map = [&](CUtensorMap *m, const uint16_t *base) -> int {
+        // pages [n_pages][page_size, Hkv, D] as {D, Hkv, page_size, n_pages}
+        const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c->Hkv),
+                                  static_cast<uint64_t>(c->page_size),
+                                  static_cast<uint64_t>(c->n_pages)};
+        const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(dk) * 2,
+                                     static_cast<uint64_t>(page_stride) * 2};
+        const uint32_t box[4] = {64, 1, static_cast<uint32_t>(box_rows), 1};
+        return make_map_bf16(m, base, 4, dims, strides, box);
+    };
+    auto new_map = [&](CUtensorMap *m, const uint16_t *base, int64_t stride) -> int {
+        const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c->Hkv),
+                                  static_cast<uint64_t>(T)};
+        const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(stride) * 2};
+        const uint32_t box[3] = {64, 1, static_cast<uint32_t>(bkv)};
+        return make_map_bf16(m, base, 3, dims, strides, box);
+    };
+    if ((rc = page_map(&mk, c->k)) != DG_OK || (rc = page_map(&mv, c->v)) != DG_OK) return rc;
+    mkn = mk;
+    mvn = mv;
+    if (k_new && ((rc = new_map(&mkn, k_new, k_stride)) != DG_OK ||
+                  (rc = new_map(&mvn, v_new, v_stride)) != DG_OK))
+        return rc;
+
+    PagedArgs a{};
+    a.q = q;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.T = T;
+    a.B = c->B;
+    a.Hq = Hq;
+    a.Hkv = c->Hkv;
+    a.G = Hq / c->Hkv;
+    a.D = D;
+    a.page_size = c->page_size;
+    a.box_rows = box_rows;
+    a.n_pages = c->n_pages;
+    a.max_pages = c->max_pages;
+    a.page_table = c->page_table;
+    a.kv_len = c->kv_len;
+    a.q_start = c->q_start;
+    a.has_new = k_new != nullptr ? 1 : 0;
+    a.causal = causal;
+    a.window = window;
+    a.checks = g_checks.load(std::memory_order_relaxed);
+    a.scale_log2 = scale * 1.44269502162933349609375f;
+    a.slot_rows = paged_slot_rows(T, a.G);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const PagedWs w = paged_ws(di->sms, a.slot_rows, D);
+    a.ws = reinterpret_cast<WsHeader *>(ws);
+    a.desc = reinterpret_cast<PagedDesc *>(ws + w.desc);
+    a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.o);
+    cudaStream_t st = as_stream(stream);
+    const bool pdl = use_pdl(st);
+    DG_CUDA_TRY(launch_kernel(D == 128 ? paged_attn_kernel_d128 : paged_attn_kernel_d256,
+                              dim3(di->sms), dim3(kPagedThreads), paged_attn_smem_bytes(D), st, pdl,
+                              mk, mv, mkn, mvn, a));
+    DG_LAUNCHED();
+    DG_CUDA_TRY(launch_kernel(paged_merge_kernel, dim3(di->sms, 16), dim3(256), 0, st, pdl, a));
+    DG_LAUNCHED();
+    return DG_OK;
 }
 
 size_t dg_encoder_append_workspace(int B, int L, int P, int Hq, int Hkv, int D)

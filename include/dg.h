@@ -140,6 +140,119 @@ int dg_encoder_append(const uint16_t *q, uint16_t *k_cache, uint16_t *v_cache, i
                       size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Serving over a paged KV cache: the per-head norm of queries and keys with */
+/* the position rotation, the append of a ragged batch's keys and values to  */
+/* the pages, and the attention of its queries over them.  The canvas        */
+/* attention and encoder append above take queries and keys that are already */
+/* position-encoded and caches that are dense [B, P, Hkv, D]; these calls    */
+/* make the former and replace the latter where sequences of unequal,        */
+/* changing lengths share one pool of pages.  "Parallel Denoising From an    */
+/* Autoregressive Checkpoint", section "Finding" (append-only encoder cache, */
+/* canvas attention over it); the paging, the norm and the rotation have no  */
+/* counterpart on the pages.                                                 */
+/* ------------------------------------------------------------------------ */
+
+/* A paged cache and the ragged batch that works on it.                      */
+/* Page p holds page_size tokens: k (and v) + p * page_stride is             */
+/* [page_size, Hkv, D] bf16, dense.  Token j of sequence b is row            */
+/* j % page_size of page page_table[b, j / page_size].  Entries of the table */
+/* past a sequence's last page are never read.  The rows of the batch's      */
+/* tensors ([T, heads, D]) are the sequences' new tokens one after another:  */
+/* rows q_start[b] .. q_start[b + 1] - 1 are sequence b's (possibly none).   */
+/* Rows before q_start[0] or from q_start[B] on (a padded batch) belong to   */
+/* nobody: they are not read into any result and their outputs are left as  */
+/* they were.  The lengths and the table are DEVICE data, read when the      */
+/* kernels run, so a captured graph follows them.  A length or row index     */
+/* outside its tensor is cut to what the tensors hold, a page id outside     */
+/* [0, n_pages) reads as a page of zeros and is not written; either records  */
+/* DG_ERR_DEVICE in the workspace's status word.                             */
+/* Supported: D in {128, 256}; page_size a multiple of 16, 16 .. 2048;       */
+/* max_pages * page_size <= 2^30; page_stride a multiple of 8 and            */
+/* >= page_size * Hkv * D, or 0 for that value.                              */
+typedef struct dg_paged_cache {
+    uint16_t *k, *v;            /* the pages                                  */
+    const int32_t *page_table;  /* [B, max_pages]                             */
+    const int32_t *kv_len;      /* [B] tokens each sequence has in the cache  */
+    const int32_t *q_start;     /* [B + 1] first row of each sequence         */
+    int64_t page_stride;        /* elements from a page to the next           */
+    int n_pages, page_size, max_pages, B, Hkv, D;
+} dg_paged_cache;
+
+/* How heads are normed and rotated.  With x a head of D values:             */
+/*   norm (weight not NULL)  x <- x / sqrt(mean(x^2) + eps)                  */
+/*                                * (weight_offset + weight)                  */
+/*   rotation (rot > 0) of the pairs (x_a, x_b) by position * f_m,           */
+/*   m = 0 .. rot / 2 - 1:  x_a <- x_a cos - x_b sin, x_b <- x_b cos + x_a   */
+/*   sin; (a, b) = (m, m + rot / 2), or (2m, 2m + 1) with interleaved = 1;   */
+/*   values from rot on are not rotated.                                      */
+/* fp32 throughout, rounded to bf16 once.  rope_steps [rot / 2] holds the    */
+/* f_m as dg_rope_steps converts them: turns per position as a 64-bit        */
+/* fraction, so that position * f_m is exact modulo a turn at any position.  */
+/* Supported: D a multiple of 16, <= 256; rot a multiple of 16, <= D.        */
+typedef struct dg_head_params {
+    int Hq, Hkv, D;
+    int rot;                    /* rotated values of each head (0: none)      */
+    int interleaved;            /* pairs: 0 (m, m + rot / 2), 1 (2m, 2m + 1)  */
+    float eps;                  /* >= 0                                       */
+    float weight_offset;        /* 0, or 1 for weights stored around zero     */
+    const uint64_t *rope_steps; /* device, rot / 2; NULL when rot == 0        */
+    const uint16_t *q_weight;   /* device bf16 [D]; NULL: queries not normed  */
+    const uint16_t *k_weight;   /* device bf16 [D]; NULL: keys not normed     */
+} dg_head_params;
+
+/* Host: frequencies in radians per position -> rope_steps (both host, n of  */
+/* them).  DG_ERR_INVALID_ARG for null pointers, n < 0 or a value that is    */
+/* not finite.                                                               */
+int dg_rope_steps(const double *radians, int n, uint64_t *steps);
+
+/* q [T, Hq, D] -> q_out, k [T, Hkv, D] -> k_out, normed and rotated.  Rows  */
+/* are *_stride elements apart (multiples of 8, >= heads * D; 0 for that     */
+/* value), so q and k may be columns of one joint projection.  positions [T] */
+/* int32 (any value; not read when rot == 0).  q or k may be NULL (not       */
+/* computed).  An output may be its input (same pointer and stride); other   */
+/* overlaps are not allowed.  T == 0 is allowed.  Needs no workspace.        */
+int dg_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                    uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                    const int32_t *positions, int T, const dg_head_params *p, void *stream);
+
+/* Appends: key and value of token i of sequence b go, the key normed and    */
+/* rotated, to place kv_len[b] + i of its pages; every other byte of the     */
+/* cache stays.  positions [T] gives the rotation's positions; NULL: that    */
+/* place.  q, q_out (both or neither): the queries are normed and rotated in */
+/* the same pass.  kv_len_out [B] (or NULL; not kv_len itself) receives      */
+/* kv_len[b] + new tokens.  A token whose place lies past the table or whose */
+/* page id is bad is not stored (DG_ERR_DEVICE in the status word).  Two     */
+/* sequences must not append to one place.  workspace: 256 bytes, for the    */
+/* status word.  p->Hkv and p->D equal the cache's.                          */
+size_t dg_paged_append_workspace(void);
+int dg_paged_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                    const uint16_t *q, int64_t q_stride, uint16_t *q_out, int64_t q_out_stride,
+                    const int32_t *positions, int T, const dg_head_params *p,
+                    const dg_paged_cache *c, int32_t *kv_len_out, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* Attention of the new tokens.  Token i of sequence b (n_b new tokens) sees  */
+/* the keys of its sequence: the kv_len[b] cached ones, followed by the new  */
+/* tokens' own k_new, v_new [T, Hkv, D] when those are given.  Without them  */
+/* the new tokens' keys are the last n_b cached ones (appended before).      */
+/* With pos = that token's place among the keys:                             */
+/*   causal = 0: every key (a canvas over its cache);                        */
+/*   causal = 1: keys up to pos, and with window > 0 only those after        */
+/*               pos - window.                                               */
+/*   out[q_start[b] + i, h, :] = softmax_j(scale q . k_j) v_j over those     */
+/*   keys; a token that sees no key gets a row of zeros.                     */
+/* q, out [T, Hq, D]; rows *_stride elements apart as above; out overlaps no */
+/* input.  bf16 in and out, fp32 accumulation, softmax and partial results.  */
+/* The work is divided over the GPU on the device, from the lengths.         */
+/* Supported: Hq % Hkv == 0, Hq / Hkv <= 128; scale > 0; T * Hq <= 2^30;     */
+/* window requires causal.  T == 0 is allowed.                               */
+size_t dg_paged_attn_workspace(int T, int Hq, const dg_paged_cache *c);
+int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
+                  const uint16_t *v_new, int64_t v_stride, uint16_t *out, int64_t out_stride,
+                  int T, int Hq, float scale, int causal, int window, const dg_paged_cache *c,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* One denoising step after the decoder body: LM head -> per-position        */
 /* entropy, Gumbel-max sample and argmax -> entropy-bounded acceptance and    */
 /* uniform renoise -> adaptive stop test.                                     */
