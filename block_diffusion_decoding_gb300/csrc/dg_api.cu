@@ -915,13 +915,13 @@ int check_head_params(const dg_head_params *p)
     if (p->rot > 0 && !p->rope_steps) return DG_ERR_INVALID_ARG;
     if (p->D % 16 != 0 || p->D > 256 || p->rot % 16 != 0 || p->rot > p->D) return DG_ERR_UNSUPPORTED;
     if (p->Hq > 16384 || p->Hkv > 1024) return DG_ERR_UNSUPPORTED;
-    if ((p->q_weight && !aligned16(p->q_weight)) || (p->k_weight && !aligned16(p->k_weight)))
+    if (!aligned16(p->q_weight) || !aligned16(p->k_weight) || !aligned16(p->rope_steps))
         return DG_ERR_ALIGNMENT;
     return DG_OK;
 }
 
-// The heads' part of a QkvArgs; q_n, k_n, v_n heads of each kind are done.
-void fill_qkv(QkvArgs &a, const dg_head_params *p, int T, int q_n, int k_n, int v_n)
+// The heads' part of a QkvArgs; q_n, k_n heads of each kind are done.
+void fill_qkv(QkvArgs &a, const dg_head_params *p, int T, int q_n, int k_n)
 {
     a.T = T;
     a.D = p->D;
@@ -934,22 +934,31 @@ void fill_qkv(QkvArgs &a, const dg_head_params *p, int T, int q_n, int k_n, int 
     a.k_weight = p->k_weight;
     a.nq = q_n;
     a.nk = k_n;
-    a.heads = q_n + k_n + v_n;
+    a.inv_d = 1.f / static_cast<float>(p->D);
     a.lanes = 1;
-    while (a.lanes * 8 < p->D) a.lanes *= 2;
+    while (a.lanes * 8 < p->D) {
+        a.lanes *= 2;
+        ++a.lanes_log2;
+    }
 }
 
 // Launches the pass over T tokens' heads.
 int launch_qkv(QkvArgs &a, bool paged, int sms, cudaStream_t st)
 {
-    const int64_t singles = static_cast<int64_t>(a.T) * a.heads * a.lanes;   // threads at one head each
-    const bool four = singles > static_cast<int64_t>(sms) * 2048 * 2 && a.heads >= 4;
-    a.chunks = four ? (a.heads + 3) / 4 : a.heads;
+    // one head a group spreads few tokens over the GPU; from two full loads of
+    // threads on, kQkvHeads a group save their shared instructions
+    const int64_t heads = a.nq + (paged ? 2 : 1) * static_cast<int64_t>(a.nk);
+    const bool many = a.T * heads * a.lanes > static_cast<int64_t>(sms) * 2048 * 2;
+    const int hpg = many ? kQkvHeads : 1;
+    a.q_chunks = (a.nq + hpg - 1) / hpg;
+    a.k_chunks = (a.nk + hpg - 1) / hpg;
+    a.chunks = a.q_chunks + (paged ? 2 : 1) * a.k_chunks;
     const int64_t threads = static_cast<int64_t>(a.T) * a.chunks * a.lanes;
     const int64_t blocks = std::max<int64_t>(1, (threads + kQkvThreads - 1) / kQkvThreads);
-    if (blocks > 0x7FFFFFFF) return DG_ERR_UNSUPPORTED;
-    auto kern = paged ? (four ? paged_append_kernel_4 : paged_append_kernel_1)
-                      : (four ? qk_norm_rope_kernel_4 : qk_norm_rope_kernel_1);
+    // the kernel counts threads in 32 bits
+    if (blocks * kQkvThreads > 0xFFFFFFFFLL) return DG_ERR_UNSUPPORTED;
+    auto kern = paged ? (many ? paged_append_kernel_n : paged_append_kernel_1)
+                      : (many ? qk_norm_rope_kernel_n : qk_norm_rope_kernel_1);
     DG_CUDA_TRY(launch_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQkvThreads), 0, st,
                               use_pdl(st), a));
     DG_LAUNCHED();
@@ -1084,7 +1093,7 @@ int dg_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int6
     DeviceInfo *di = nullptr;
     if ((rc = current_device_info(&di)) != DG_OK) return rc;
     QkvArgs a{};
-    fill_qkv(a, p, T, q ? p->Hq : 0, k ? p->Hkv : 0, 0);
+    fill_qkv(a, p, T, q ? p->Hq : 0, k ? p->Hkv : 0);
     a.q = q;
     a.k = k;
     a.q_out = q_out;
@@ -1128,7 +1137,7 @@ int dg_paged_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int6
     DeviceInfo *di = nullptr;
     if ((rc = current_device_info(&di)) != DG_OK) return rc;
     QkvArgs a{};
-    fill_qkv(a, p, T, q ? p->Hq : 0, p->Hkv, p->Hkv);
+    fill_qkv(a, p, T, q ? p->Hq : 0, p->Hkv);
     a.q = q;
     a.k = k;
     a.v = v;

@@ -266,9 +266,10 @@ struct QkvArgs {
     const uint16_t *q_weight, *k_weight;
     float eps, weight_offset;
     int T, D, rot, interleaved;
-    int nq, nk, heads;                  // q heads, k heads, all heads of the pass (with v's)
-    int lanes;                          // lanes of a head's group
-    int chunks;                         // groups per token
+    int nq, nk;                         // q heads, k (and v) heads of the pass
+    int lanes, lanes_log2;              // lanes of a head's group
+    float inv_d;                        // 1 / D
+    int chunks, q_chunks, k_chunks;     // groups per token, those for q and for k
     // paged destination
     uint16_t *k_cache, *v_cache;
     int64_t page_stride;                // elements between pages
@@ -278,11 +279,12 @@ struct QkvArgs {
     WsHeader *ws;
 };
 constexpr int kQkvThreads = 256;
+constexpr int kQkvHeads = 4;         // heads per group of the kernels for many tokens
 constexpr int kQkvSeqSmem = 2048;    // sequences whose first rows are staged in shared memory
 __global__ void qk_norm_rope_kernel_1(QkvArgs a);
-__global__ void qk_norm_rope_kernel_4(QkvArgs a);
+__global__ void qk_norm_rope_kernel_n(QkvArgs a);
 __global__ void paged_append_kernel_1(QkvArgs a);
-__global__ void paged_append_kernel_4(QkvArgs a);
+__global__ void paged_append_kernel_n(QkvArgs a);
 
 // ---------------------------------------------------------------- paged attention
 // What a CTA left for the merge: slot 0 holds a part that continues an item

@@ -2,20 +2,24 @@
 // rotation, into dense rows (dg_qk_norm_rope) or, with the values, into the
 // pages of a paged KV cache (dg_paged_append).
 //
-// Both are one read and one write of every value.  A head of D values is
-// held by a group of D / 8 lanes (rounded up to a power of two), 8 values
-// (one 16-byte load) per lane:
+// Both are one read and one write of every value, so what is left to decide
+// is how few instructions a value costs.  A head of D values is held by a
+// group of D / 8 lanes (rounded up to a power of two) as two runs of 4 values
+// a lane, placed so that a rotated pair never leaves its lane:
+//   pairs (m, m + rot / 2)   runs at 4 l and rot / 2 + 4 l for l < rot / 8,
+//                            then the values that are not rotated, 8 a lane;
+//   pairs (2m, 2m + 1)       runs at 8 l and 8 l + 4.
+// So a lane needs 4 angles, computed once for all the heads it works on, and
+// the only shuffles are the norm's sum.
 //   norm      r = 1 / sqrt(mean x^2 + eps) by a shuffle tree of the group,
 //             y = x r (offset + w);
-//   rotation  of the first `rot` values by position x frequency.  The angle
-//             is kept as a fraction of a turn in 64-bit fixed point: the
-//             frequency step is round(2^64 f / 2 pi), so position x step
-//             wraps modulo one turn exactly, and the angle of position
-//             262143 is as accurate as that of position 1; its top 32 bits
-//             give an angle in [-pi, pi) for the fast sine and cosine
-//             (absolute error about 2^-21, far below the half step 2^-9 of
-//             the bf16 result).  Pairs (m, m + rot / 2) exchange values by a
-//             shuffle, pairs (2m, 2m + 1) sit in one lane.
+//   rotation  the angle, position x frequency, is kept as a fraction of a
+//             turn in 64-bit fixed point: the step of a frequency f is
+//             2^64 f / 2 pi, so position x step wraps modulo one turn exactly
+//             and the angle of position 262143 is as accurate as that of
+//             position 1; its top 32 bits give an angle in [-pi, pi) for the
+//             fast sine and cosine (absolute error about 2^-21, far below the
+//             half step 2^-8 of the bf16 result).
 // Everything is fp32 until the one rounding to bf16 at the store.
 #include "dg_kernels.h"
 
@@ -23,36 +27,35 @@ namespace dg {
 
 namespace {
 
-// Not the read-only path: q_out may be q itself.
-DG_DEVICE uint4 ld_stream(const uint16_t *p)
+// 4 bf16 values.  Not the read-only path: q_out may be q itself.
+DG_DEVICE uint2 ld_stream(const uint16_t *p)
 {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y)
                  : "l"(p)
                  : "memory");
     return v;
 }
 
-DG_DEVICE void unpack8(const uint4 &v, float (&x)[8])
+DG_DEVICE float2 unpack2(uint32_t w)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-    }
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-DG_DEVICE uint4 pack8(const float (&x)[8])
+DG_DEVICE uint32_t pack2(float2 v)
 {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t *>(&h2);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&h2);
+}
+
+// cos and sin of position x step (turns in 64-bit fixed point).
+DG_DEVICE void turn(int pos, uint64_t step, float &c, float &s)
+{
+    const uint64_t ph = static_cast<uint64_t>(static_cast<int64_t>(pos)) * step;
+    const float ang = static_cast<float>(static_cast<int32_t>(ph >> 32)) *
+                      1.4629180792671596e-9f;   // 2 pi / 2^32
+    __sincosf(ang, &s, &c);
 }
 
 // The last b with start[b] <= t (-1: none), start non-decreasing, [n].
@@ -69,23 +72,21 @@ DG_DEVICE int last_not_above(const int32_t *start, int n, int t)
 
 }  // namespace
 
-// HPG heads per group: their loads are in flight together and share one set
-// of sines and cosines.
+// A group takes up to HPG consecutive heads of one kind (q, k or v): their
+// loads are in flight together, and they share the lane's addresses, weights,
+// sines and cosines.
 template <bool PAGED, int HPG>
 __device__ __forceinline__ void qkv_body(const QkvArgs &a)
 {
-    __shared__ int32_t s_start[kQkvSeqSmem];
+    __shared__ int32_t s_start[PAGED ? kQkvSeqSmem : 1];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x;
     const int lg = a.lanes;                       // lanes of a group, a power of two
     const int sub = tid & (lg - 1);
-    const int e0 = sub * 8;                       // first value this lane holds
-    const bool in_head = e0 < a.D;
 
     if (PAGED) {
-        const bool staged = a.B < kQkvSeqSmem;
-        if (staged) {
+        if (a.B < kQkvSeqSmem) {
             for (int b = tid; b <= a.B; b += kQkvThreads) s_start[b] = a.q_start[b];
             __syncthreads();
         }
@@ -98,25 +99,36 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
         }
     }
 
-    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kQkvThreads + tid) / lg;
-    const int64_t t64 = unit / a.chunks;
-    const int chunk = static_cast<int>(unit - t64 * a.chunks);
-    const bool live = t64 < a.T;
-    const int t = live ? static_cast<int>(t64) : 0;
+    const uint32_t unit = (blockIdx.x * static_cast<uint32_t>(kQkvThreads) + tid) >> a.lanes_log2;
+    const uint32_t tu = unit / static_cast<uint32_t>(a.chunks);
+    const bool live = tu < static_cast<uint32_t>(a.T);
+    const int t = live ? static_cast<int>(tu) : 0;
+    int c = static_cast<int>(unit - tu * a.chunks);
+    const bool is_q = c < a.q_chunks, is_v = c >= a.q_chunks + a.k_chunks;
+    c -= is_q ? 0 : is_v ? a.q_chunks + a.k_chunks : a.q_chunks;
+    const int h0 = c * HPG;
+    const int count = live ? min(HPG, (is_q ? a.nq : a.nk) - h0) : 0;   // heads of this group
 
-    // ---- this group's heads: chunk, chunk + chunks, ...; q, then k, then v
-    uint4 raw[HPG];
+    // ---- the two runs of this lane: value offsets, angles of its pairs
+    const int rl = a.interleaved ? 0 : a.rot >> 3;    // lanes with split runs
+    const bool split = sub < rl;
+    const int e0 = split ? 4 * sub : a.interleaved ? 8 * sub : a.rot + 8 * (sub - rl);
+    const int gap = split ? (a.rot >> 1) : 4;         // from the first run to the second
+    const bool in_head = sub * 8 < a.D;
+    const bool turns = !is_v && (a.interleaved ? e0 < a.rot : split);
+
+    uint2 lo[HPG], hi[HPG];
+    {
+        const uint16_t *src = (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride
+                                                                  : a.k + t * a.k_stride) +
+                              (h0 * a.D + e0);
 #pragma unroll
-    for (int j = 0; j < HPG; ++j) {
-        const int h = chunk + j * a.chunks;
-        raw[j] = make_uint4(0, 0, 0, 0);
-        if (live && in_head && h < a.heads) {
-            const uint16_t *src =
-                h < a.nq            ? a.q + static_cast<int64_t>(t) * a.q_stride + h * a.D
-                : h < a.nq + a.nk   ? a.k + static_cast<int64_t>(t) * a.k_stride + (h - a.nq) * a.D
-                                    : a.v + static_cast<int64_t>(t) * a.v_stride +
-                                          (h - a.nq - a.nk) * a.D;
-            raw[j] = ld_stream(src + e0);
+        for (int j = 0; j < HPG; ++j, src += a.D) {
+            lo[j] = hi[j] = make_uint2(0, 0);
+            if (in_head && j < count) {
+                lo[j] = ld_stream(src);
+                hi[j] = ld_stream(src + gap);
+            }
         }
     }
 
@@ -132,12 +144,12 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
             if (token) {
                 const int64_t at = static_cast<int64_t>(a.kv_len[b]) + (t - start[b]);
                 pos = a.positions != nullptr ? a.positions[t] : static_cast<int>(at);
-                const int64_t pg = at / a.page_size;
-                if (at >= 0 && pg < a.max_pages) {
+                if (at >= 0 && at < static_cast<int64_t>(a.max_pages) * a.page_size) {
+                    const uint32_t pg = static_cast<uint32_t>(at) / static_cast<uint32_t>(a.page_size);
                     const int page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pg];
                     if (page >= 0 && page < a.n_pages)
-                        row = static_cast<int64_t>(page) * a.page_stride +
-                              (at - pg * a.page_size) * a.nk * a.D;
+                        row = page * a.page_stride +
+                              (at - static_cast<int64_t>(pg) * a.page_size) * a.nk * a.D;
                 }
                 if (row < 0) report_error(a.ws, DG_ERR_DEVICE, 901);
             }
@@ -145,89 +157,109 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
     } else if (live && a.rot > 0) {
         pos = a.positions[t];
     }
-
-    // ---- sines and cosines of this lane's values
-    float cs[8], sn[8];
-    const int half = a.rot >> 1;
-    const bool turns = e0 < a.rot;
-    if (a.rot > 0) {
-        const int m0 = a.interleaved ? e0 >> 1 : (e0 < half ? e0 : e0 - half);
+    float2 cs[2], sn[2], ns[2];   // of the lane's four pairs; ns = -sn
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cs[e] = 1.f;
-            sn[e] = 0.f;
-            if (turns) {
-                const int m = a.interleaved ? m0 + (e >> 1) : m0 + e;
-                if (!a.interleaved || (e & 1) == 0) {
-                    const uint64_t ph =
-                        static_cast<uint64_t>(static_cast<int64_t>(pos)) * __ldg(a.steps + m);
-                    const float ang = static_cast<float>(static_cast<int32_t>(ph >> 32)) *
-                                      1.4629180792671596e-9f;   // 2 pi / 2^32
-                    __sincosf(ang, &sn[e], &cs[e]);
-                } else {
-                    sn[e] = sn[e - 1];
-                    cs[e] = cs[e - 1];
-                }
-            }
-        }
+    for (int e = 0; e < 2; ++e) cs[e] = make_float2(1.f, 1.f), sn[e] = make_float2(0.f, 0.f);
+    if (turns) {
+        // pairs m .. m + 3 either way
+        const ulonglong2 *steps = reinterpret_cast<const ulonglong2 *>(a.steps + 4 * sub);
+        const ulonglong2 s0 = __ldg(steps), s1 = __ldg(steps + 1);
+        turn(pos, s0.x, cs[0].x, sn[0].x);
+        turn(pos, s0.y, cs[0].y, sn[0].y);
+        turn(pos, s1.x, cs[1].x, sn[1].x);
+        turn(pos, s1.y, cs[1].y, sn[1].y);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) ns[e] = make_float2(-sn[e].x, -sn[e].y);
+
+    const uint16_t *wp = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+    float2 w[4];                  // offset + weight of the lane's values
+    if (wp != nullptr && in_head) {
+        const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(wp + e0));
+        const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(wp + e0 + gap));
+        const float2 off = make_float2(a.weight_offset, a.weight_offset);
+        w[0] = add2(unpack2(wa.x), off);
+        w[1] = add2(unpack2(wa.y), off);
+        w[2] = add2(unpack2(wb.x), off);
+        w[3] = add2(unpack2(wb.y), off);
     }
 
+    // ---- norms of all the group's heads together, so that their shuffles
+    // overlap; every lane of the warp takes part in them
+    float rn[HPG];
+    if (a.q_weight != nullptr || a.k_weight != nullptr) {
 #pragma unroll
-    for (int j = 0; j < HPG; ++j) {
-        const int h = chunk + j * a.chunks;
-        const bool have = h < a.heads;
-        const bool is_q = h < a.nq, is_v = h >= a.nq + a.nk;
-        uint4 res = raw[j];
-        float x[8];
-        unpack8(raw[j], x);
-        const uint16_t *w = is_q ? a.q_weight : a.k_weight;
-        // every lane of the warp takes part in the shuffles
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        for (int o = lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (w != nullptr && !is_v) {
-            const float r = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
-            float wv[8];
-            unpack8(in_head ? __ldg(reinterpret_cast<const uint4 *>(w + e0)) : make_uint4(0, 0, 0, 0),
-                    wv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * r * (a.weight_offset + wv[e]);
+        for (int j = 0; j < HPG; ++j) {
+            float2 x = unpack2(lo[j].x);
+            float2 s2 = mul2(x, x);
+            x = unpack2(lo[j].y);
+            s2 = fma2(x, x, s2);
+            x = unpack2(hi[j].x);
+            s2 = fma2(x, x, s2);
+            x = unpack2(hi[j].y);
+            s2 = fma2(x, x, s2);
+            rn[j] = s2.x + s2.y;
         }
-        if (a.rot > 0) {
-            if (a.interleaved) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float p = x[e], q = x[e + 1];
-                    x[e] = p * cs[e] - q * sn[e];
-                    x[e + 1] = q * cs[e] + p * sn[e];
-                }
-            } else {
-                // the pair's other value sits rot / 16 lanes away
-                const int hop = a.rot >> 4;
-                const int other = !turns ? sub : e0 < half ? sub + hop : sub - hop;
+        for (int o = 16; o > 0; o >>= 1) {
+            if (o < lg) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float p = __shfl_sync(0xFFFFFFFFu, x[e], other, lg);
-                    x[e] = e0 < half ? x[e] * cs[e] - p * sn[e] : x[e] * cs[e] + p * sn[e];
-                }
+                for (int j = 0; j < HPG; ++j) rn[j] += __shfl_xor_sync(0xFFFFFFFFu, rn[j], o);
             }
         }
-        if (!is_v && (w != nullptr || turns)) res = pack8(x);   // else the bits as they are
-        if (have && in_head && token) {
-            if (is_q) {
-                *reinterpret_cast<uint4 *>(a.q_out + static_cast<int64_t>(t) * a.qo_stride +
-                                           h * a.D + e0) = res;
-            } else if (PAGED) {
-                if (row >= 0) {
-                    uint16_t *base = is_v ? a.v_cache : a.k_cache;
-                    const int hk = h - a.nq - (is_v ? a.nk : 0);
-                    *reinterpret_cast<uint4 *>(base + row + hk * a.D + e0) = res;
+#pragma unroll
+        for (int j = 0; j < HPG; ++j) rn[j] = rsqrtf(rn[j] * a.inv_d + a.eps);
+    }
+
+    uint16_t *dst;
+    if (is_q)
+        dst = a.q_out + t * a.qo_stride;
+    else if (!PAGED)
+        dst = a.k_out + t * a.ko_stride;
+    else
+        dst = (is_v ? a.v_cache : a.k_cache) + row;
+    dst += h0 * a.D + e0;
+    const int stores = token && in_head && (is_q || !PAGED || row >= 0) ? count : 0;
+    const bool normed = wp != nullptr;
+    if (normed || turns) {        // else the bits go as they are
+#pragma unroll
+        for (int j = 0; j < HPG; ++j) {
+            // x[0], x[1]: the first run, x[2], x[3]: the second
+            float2 x[4] = {unpack2(lo[j].x), unpack2(lo[j].y), unpack2(hi[j].x), unpack2(hi[j].y)};
+            if (normed) {
+                const float2 r2 = make_float2(rn[j], rn[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), w[e]);
+            }
+            if (!turns) {
+                // (also where a value is infinite: no product with a zero sine)
+            } else if (a.interleaved) {
+                // (x.x, x.y) is a pair
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float co = (e & 1) ? cs[e >> 1].y : cs[e >> 1].x;
+                    const float si = (e & 1) ? sn[e >> 1].y : sn[e >> 1].x;
+                    const float2 p = x[e];
+                    x[e] = make_float2(p.x * co - p.y * si, p.y * co + p.x * si);
                 }
             } else {
-                *reinterpret_cast<uint4 *>(a.k_out + static_cast<int64_t>(t) * a.ko_stride +
-                                           (h - a.nq) * a.D + e0) = res;
+                // x[e] pairs with x[e + 2], component by component
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 p = x[e], q = x[e + 2];
+                    x[e] = fma2(q, ns[e], mul2(p, cs[e]));
+                    x[e + 2] = fma2(p, sn[e], mul2(q, cs[e]));
+                }
             }
+            lo[j] = make_uint2(pack2(x[0]), pack2(x[1]));
+            hi[j] = make_uint2(pack2(x[2]), pack2(x[3]));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < HPG; ++j, dst += a.D) {
+        if (j < stores) {
+            *reinterpret_cast<uint2 *>(dst) = lo[j];
+            *reinterpret_cast<uint2 *>(dst + gap) = hi[j];
         }
     }
 }
@@ -236,17 +268,17 @@ __global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_1(QkvArgs a)
 {
     qkv_body<false, 1>(a);
 }
-__global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_4(QkvArgs a)
+__global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_n(QkvArgs a)
 {
-    qkv_body<false, 4>(a);
+    qkv_body<false, kQkvHeads>(a);
 }
 __global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_1(QkvArgs a)
 {
     qkv_body<true, 1>(a);
 }
-__global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_4(QkvArgs a)
+__global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_n(QkvArgs a)
 {
-    qkv_body<true, 4>(a);
+    qkv_body<true, kQkvHeads>(a);
 }
 
 }  // namespace dg

@@ -84,6 +84,19 @@ def test_norm_rope_extremes():
     dg.qk_norm_rope(e, None, e, None, torch.empty(0, dtype=torch.int32, device=DEV), p)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_infinities_outside_the_rotation_stay(interleaved):
+    """A value that is not rotated meets no product with its neighbour: an infinity there stays one value."""
+    D, rot = 128, 64
+    x = heads_of(4, 2, D, 6)
+    x[1, 0, 65], x[2, 1, 127] = float("inf"), float("-inf")
+    pos = torch.arange(4, dtype=torch.int32)
+    p = dg.head_params(2, 1, D, rope_steps=dg.rope_steps(inv_freq(rot), DEV), interleaved=interleaved)
+    out = torch.full_like(x, NAN).to(DEV)
+    dg.qk_norm_rope(x.to(DEV), None, out, None, pos.to(DEV), p)
+    assert torch.equal(out.cpu()[..., rot:], x[..., rot:])
+
+
 # ---------------------------------------------------------------- append
 @pytest.mark.parametrize("n,kv,Hq,Hkv,D,page,rot,interleaved,pad", [
     ([1], [0], 4, 1, 128, 16, 128, False, 0),
