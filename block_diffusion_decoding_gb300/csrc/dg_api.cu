@@ -110,6 +110,12 @@ int current_device_info(DeviceInfo **out)
         DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_kernel_d256,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          paged_attn_smem_bytes(256)));
+        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_pair_kernel_d128,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         paged_pair_smem_bytes(128)));
+        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_pair_kernel_d256,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         paged_pair_smem_bytes(256)));
         di.attrs_set = true;
     }
     *out = &di;
@@ -967,7 +973,18 @@ int launch_qkv(QkvArgs &a, bool paged, int sms, cudaStream_t st)
 
 int paged_slot_rows(int T, int G)
 {
-    return static_cast<int>(std::min<int64_t>(128, static_cast<int64_t>(T) * G));
+    return static_cast<int>(std::min<int64_t>(kPagedPairRows, static_cast<int64_t>(T) * G));
+}
+
+// Whether a batch runs on 2-CTA clusters with query tiles of 256 rows: when its
+// sequences have more than 128 folded rows on average (the lengths themselves
+// are device data).  DG_PAGED_KERNEL=single|pair forces a choice.
+bool paged_pair(int T, int B, int G)
+{
+    const char *env = std::getenv("DG_PAGED_KERNEL");
+    if (env && std::strcmp(env, "single") == 0) return false;
+    if (env && std::strcmp(env, "pair") == 0) return true;
+    return static_cast<int64_t>(T) * G > 128LL * B;
 }
 
 // Workspace of the paged attention for `ctas` CTAs: header | descriptors |
@@ -1199,10 +1216,12 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     DeviceInfo *di = nullptr;
     if ((rc = current_device_info(&di)) != DG_OK) return rc;
     if (di->sms > kAssumedMaxSMs) return DG_ERR_UNSUPPORTED;
-    const int D = c->D, bkv = D == 128 ? 128 : 64;
-    // a box of keys stays inside one page and one key tile: its rows divide both
-    int box_rows = c->page_size & -c->page_size;
-    box_rows = std::min(box_rows, bkv);
+    const int D = c->D;
+    const bool pair = paged_pair(T, c->B, Hq / c->Hkv);
+    // keys of K and of V a CTA loads of a tile, dense; a box of the pages
+    // stays inside one page and one such load: its rows divide both
+    const int k_rows = pair || D == 256 ? 64 : 128, v_rows = pair || D == 128 ? 128 : 64;
+    const int box_rows = std::min(c->page_size & -c->page_size, k_rows);
 
     CUtensorMap mk, mv, mkn, mvn;
     auto page_map = [&](CUtensorMap *m, const uint16_t *base) -> int {
@@ -1215,18 +1234,18 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
         const uint32_t box[4] = {64, 1, static_cast<uint32_t>(box_rows), 1};
         return make_map_bf16(m, base, 4, dims, strides, box);
     };
-    auto new_map = [&](CUtensorMap *m, const uint16_t *base, int64_t stride) -> int {
+    auto new_map = [&](CUtensorMap *m, const uint16_t *base, int64_t stride, int rows) -> int {
         const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c->Hkv),
                                   static_cast<uint64_t>(T)};
         const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(stride) * 2};
-        const uint32_t box[3] = {64, 1, static_cast<uint32_t>(bkv)};
+        const uint32_t box[3] = {64, 1, static_cast<uint32_t>(rows)};
         return make_map_bf16(m, base, 3, dims, strides, box);
     };
     if ((rc = page_map(&mk, c->k)) != DG_OK || (rc = page_map(&mv, c->v)) != DG_OK) return rc;
     mkn = mk;
     mvn = mv;
-    if (k_new && ((rc = new_map(&mkn, k_new, k_stride)) != DG_OK ||
-                  (rc = new_map(&mvn, v_new, v_stride)) != DG_OK))
+    if (k_new && ((rc = new_map(&mkn, k_new, k_stride, k_rows)) != DG_OK ||
+                  (rc = new_map(&mvn, v_new, v_stride, v_rows)) != DG_OK))
         return rc;
 
     PagedArgs a{};
@@ -1253,6 +1272,7 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     a.checks = g_checks.load(std::memory_order_relaxed);
     a.scale_log2 = scale * 1.44269502162933349609375f;
     a.slot_rows = paged_slot_rows(T, a.G);
+    a.out_wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && out_stride % 16 == 0 ? 1 : 0;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const PagedWs w = paged_ws(di->sms, a.slot_rows, D);
     a.ws = reinterpret_cast<WsHeader *>(ws);
@@ -1261,11 +1281,19 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     a.part_o = reinterpret_cast<float *>(ws + w.o);
     cudaStream_t st = as_stream(stream);
     const bool pdl = use_pdl(st);
-    DG_CUDA_TRY(launch_kernel(D == 128 ? paged_attn_kernel_d128 : paged_attn_kernel_d256,
-                              dim3(di->sms), dim3(kPagedThreads), paged_attn_smem_bytes(D), st, pdl,
-                              mk, mv, mkn, mvn, a));
+    const int units = pair ? di->sms / 2 : di->sms;
+    if (pair)
+        DG_CUDA_TRY(launch_kernel(D == 128 ? paged_attn_pair_kernel_d128 : paged_attn_pair_kernel_d256,
+                                  dim3(2 * units), dim3(kPagedPairThreads), paged_pair_smem_bytes(D),
+                                  st, pdl, mk, mv, mkn, mvn, a));
+    else
+        DG_CUDA_TRY(launch_kernel(D == 128 ? paged_attn_kernel_d128 : paged_attn_kernel_d256,
+                                  dim3(units), dim3(kPagedThreads), paged_attn_smem_bytes(D), st,
+                                  pdl, mk, mv, mkn, mvn, a));
     DG_LAUNCHED();
-    DG_CUDA_TRY(launch_kernel(paged_merge_kernel, dim3(di->sms, 16), dim3(256), 0, st, pdl, a));
+    const int merge_y = (a.slot_rows * (D / 16) + kMergeThreads - 1) / kMergeThreads;
+    DG_CUDA_TRY(launch_kernel(paged_merge_kernel, dim3(units, merge_y), dim3(kMergeThreads), 0, st,
+                              pdl, a));
     DG_LAUNCHED();
     return DG_OK;
 }

@@ -174,6 +174,38 @@ DG_DEVICE bool mbar_wait(uint64_t *bar, uint32_t parity, WsHeader *ws, int where
     return mbar_wait_limit(bar, parity, ws, where, kWaitLimitNs);
 }
 
+// The same wait with the clock read only once it has lasted: a wait that a few
+// polls satisfy, as most in a running pipeline are, pays for those alone.
+// CLUSTER: acquires what the other CTA of a pair released.
+template <bool CLUSTER = false>
+DG_DEVICE bool mbar_wait_poll(uint64_t *bar, uint32_t parity, WsHeader *ws, int where,
+                              uint64_t limit_ns = kWaitLimitNs)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        uint32_t ok;
+        if (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity)
+                : "memory");
+        else
+            ok = mbar_try_wait(bar, parity) ? 1u : 0u;
+        if (ok) return true;
+        if ((it & 63u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > limit_ns) {
+                report_error(ws, DG_ERR_TIMEOUT, where);
+                return false;
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor), completion on an mbarrier (complete_tx)
 // ------------------------------------------------------------------------
@@ -275,6 +307,13 @@ DG_DEVICE uint64_t policy_evict_first()
 {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+DG_DEVICE uint64_t policy_evict_normal()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 
@@ -595,6 +634,21 @@ DG_DEVICE void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// True in one lane of a converged warp, the same one every time.  A role whose
+// whole warp runs its loop and only issues under this keeps its operands
+// uniform over the warp, which is how the tensor instructions take them; a
+// role run by one lane alone pays a move and a wait for each operand.
+DG_DEVICE bool elect_lane()
+{
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
 }
 
 // Instruction descriptor, kind::f16: D fp32, A/B bf16, A K-major,

@@ -308,13 +308,14 @@ struct PagedArgs {
     int has_new, causal, window;
     int checks;
     float scale_log2;
+    int out_wide;        // output rows are 32-byte aligned
     int slot_rows;       // rows of a part slot
-    float *part_o;       // [2 CTAs][slot_rows][D] unnormalised rows
+    float *part_o;       // [2 CTAs][D / 4][slot_rows][4] unnormalised rows
     float2 *part_ml;     // [2 CTAs][slot_rows] (reference max in base 2, sum)
     PagedDesc *desc;     // [CTAs]
     WsHeader *ws;
 };
-constexpr int kPagedThreads = 224;   // warps as kAttnThreads
+constexpr int kPagedThreads = 256;   // warps as kAttnThreads, and 7 walks the parts
 __global__ void paged_attn_kernel_d128(const __grid_constant__ CUtensorMap map_k,
                                        const __grid_constant__ CUtensorMap map_v,
                                        const __grid_constant__ CUtensorMap map_kn,
@@ -323,8 +324,21 @@ __global__ void paged_attn_kernel_d256(const __grid_constant__ CUtensorMap map_k
                                        const __grid_constant__ CUtensorMap map_v,
                                        const __grid_constant__ CUtensorMap map_kn,
                                        const __grid_constant__ CUtensorMap map_vn, PagedArgs a);
+constexpr int kMergeThreads = 256;
 __global__ void paged_merge_kernel(PagedArgs a);
 int paged_attn_smem_bytes(int D);
+// Chunks: query tiles of 256 rows on 2-CTA clusters (dg_paged_pair.cu)
+constexpr int kPagedPairThreads = 384;
+constexpr int kPagedPairRows = 256;
+__global__ void paged_attn_pair_kernel_d128(const __grid_constant__ CUtensorMap map_k,
+                                            const __grid_constant__ CUtensorMap map_v,
+                                            const __grid_constant__ CUtensorMap map_kn,
+                                            const __grid_constant__ CUtensorMap map_vn, PagedArgs a);
+__global__ void paged_attn_pair_kernel_d256(const __grid_constant__ CUtensorMap map_k,
+                                            const __grid_constant__ CUtensorMap map_v,
+                                            const __grid_constant__ CUtensorMap map_kn,
+                                            const __grid_constant__ CUtensorMap map_vn, PagedArgs a);
+int paged_pair_smem_bytes(int D);
 
 // ---------------------------------------------------------------- MoE FFN
 constexpr int kMoeMaxExperts = 128;    // routed experts (plus one shared)

@@ -5,8 +5,8 @@
 // one query tile (ROWS folded rows = positions x heads of one kv head) of one
 // kv head of one sequence; it costs a fixed part plus its visible keys.  The
 // items in the order (sequence, kv head, query tile) lie end to end on a line
-// of total cost W, CTA c takes the stretch [W c / n, W (c + 1) / n), and a cut
-// inside an item falls between two of its key tiles.  So the CTAs' work is
+// of total cost W, CTA c takes the stretch from c s to (c + 1) s, s the n-th
+// part of W, and a cut inside an item falls between two of its key tiles.  So the CTAs' work is
 // equal whatever the lengths are, a CTA leaves at most two unfinished parts
 // (one at each end of its stretch), and the parts of an item are those of
 // consecutive CTAs: they are merged in that order, whoever was first.
@@ -89,46 +89,62 @@ DG_BOTH int64_t paged_prefix(const PagedSeq &s, int m)
     return m * s.fixed + k * s.x0 + s.slope * (k * (k + 1) / 2) + (m - k) * s.cap;
 }
 
-struct PagedRange {
-    int64_t W, begin, end;   // the whole line, this CTA's stretch
-    int n;                   // CTAs that have one
-    int b;                   // sequence `begin` falls in
-    int64_t base;            // where that sequence begins
-};
-
-DG_BOTH int64_t paged_bound(int64_t W, int n, int c)
+// Both non-negative; nearly every quotient here is one of 32-bit numbers.
+DG_BOTH int64_t paged_div(int64_t x, int64_t y)
 {
-    return W / n * c + W % n * c / n;
+    if (((x | y) >> 32) == 0)
+        return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
 }
 
-// The CTA whose stretch holds position x.
-DG_BOTH int paged_owner(int64_t W, int n, int64_t x)
-{
-    int c = static_cast<int>(static_cast<float>(x) / static_cast<float>(W) * n);
-    c = paged_min(paged_max(c, 0), n - 1);
-    while (paged_bound(W, n, c) > x) --c;
-    while (paged_bound(W, n, c + 1) <= x) ++c;
-    return c;
-}
-
-// Units (CTAs, or pairs of them) that get a stretch of a line of cost W.
-DG_BOTH int paged_units(const PagedArgs &a, int64_t W, int units)
+// The length of a unit's stretch (a unit: a CTA, or a pair of them) of a line
+// of cost W.
+DG_BOTH int64_t paged_step(const PagedArgs &a, int64_t W, int units)
 {
     const int64_t least = static_cast<int64_t>(a.G) * kPagedMinKeys;
-    return static_cast<int>(paged_min<int64_t>(units, paged_max<int64_t>(W / least, 1)));
+    const int64_t n = paged_min<int64_t>(units, paged_max<int64_t>(paged_div(W, least), 1));
+    return paged_div(W + n - 1, n);
+}
+
+struct PagedRange {
+    int64_t begin, end;      // this unit's stretch (end <= begin: none)
+    int64_t step;
+    int64_t item;            // where the item that `begin` falls in begins
+    int b, g, m;             // that item
+};
+
+// The item of sequence b (which begins at `base`) that position x falls in.
+template <int ROWS, int BKV>
+DG_BOTH void paged_locate(const PagedArgs &a, const PagedSeq &s, int b, int64_t base, int64_t x,
+                          PagedRange &r)
+{
+    const int64_t head = paged_prefix(s, s.mt);
+    int64_t y = x - base;
+    r.b = b;
+    r.g = static_cast<int>(paged_div(y, head));
+    y -= r.g * head;
+    int lo = 0, hi = s.mt - 1;   // the last tile that begins at or before y
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (paged_prefix(s, mid) <= y) lo = mid;
+        else hi = mid - 1;
+    }
+    r.m = lo;
+    r.item = base + r.g * head + paged_prefix(s, lo);
 }
 
 struct PagedScan {
-    int64_t warp_sum[32];
+    int64_t warp_sum[12];    // one a warp
     PagedRange r;
 };
 
-// Unit u of `units` (a CTA, or a pair) of NT threads: its stretch, left in
-// sc.r (end <= begin: nothing to do).  All threads of the CTA call it.
+// Unit u of `units`, in a CTA of NT threads: its stretch, left in sc.r.  All
+// threads of the CTA call it.
 template <int ROWS, int BKV, int NT>
 DG_DEVICE void paged_divide(const PagedArgs &a, int u, int units, PagedScan &sc)
 {
     constexpr int NW = NT / 32;
+    static_assert(NW <= 12, "PagedScan");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ch = (a.B + NT - 1) / NT;
     const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
@@ -156,21 +172,18 @@ DG_DEVICE void paged_divide(const PagedArgs &a, int u, int units, PagedScan &sc)
         if (w < warp) before += sc.warp_sum[w];
         W += sc.warp_sum[w];
     }
-    const int n = paged_units(a, W, units);
-    if (W > 0 && u < n) {
-        const int64_t x = paged_bound(W, n, u);
+    if (mine > 0) {
+        const int64_t step = paged_step(a, W, units), x = u * step;
         if (x >= before && x < before + mine) {
             int64_t base = before;
             for (int b = b0; b < b1; ++b) {
                 const PagedSeq s = paged_seq<ROWS, BKV>(a, b);
                 const int64_t c = a.Hkv * paged_prefix(s, s.mt);
                 if (x < base + c) {
-                    sc.r.W = W;
-                    sc.r.n = n;
+                    paged_locate<ROWS, BKV>(a, s, b, base, x, sc.r);
                     sc.r.begin = x;
-                    sc.r.end = paged_bound(W, n, u + 1);
-                    sc.r.b = b;
-                    sc.r.base = base;
+                    sc.r.end = min(W, x + step);
+                    sc.r.step = step;
                     break;
                 }
                 base += c;
@@ -193,38 +206,26 @@ struct PagedPart {
     bool whole;
 };
 
-// Walks the parts of a stretch.  Every role of the CTA walks its own copy, all
-// the same.
+// Walks the parts of a stretch.
 template <int ROWS, int BKV>
 struct PagedWalk {
     PagedSeq s, ahead;   // this sequence, the next one's lengths (already loaded)
     int b, g, m;
-    int64_t item, begin, end, W;
-    int n;
+    int64_t item, begin, end, step;
 
     DG_BOTH void start(const PagedArgs &a, const PagedRange &r)
     {
         begin = r.begin;
         item = end = r.end;
         if (end <= begin) return;
-        W = r.W;
-        n = r.n;
+        step = r.step;
         b = r.b;
+        g = r.g;
+        m = r.m;
+        item = r.item;
         s = paged_seq<ROWS, BKV>(a, b);
         ahead = s;
         if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV>(a, b + 1);
-        const int64_t head = paged_prefix(s, s.mt);
-        int64_t y = begin - r.base;
-        g = static_cast<int>(y / head);
-        y -= g * head;
-        int lo = 0, hi = s.mt - 1;   // the last tile that begins at or before y
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (paged_prefix(s, mid) <= y) lo = mid;
-            else hi = mid - 1;
-        }
-        m = lo;
-        item = r.base + g * head + paged_prefix(s, m);
     }
 
     // The next part; false: the stretch is done.
@@ -253,11 +254,13 @@ struct PagedWalk {
             }
             p.lo = lo;
             p.nt = paged_max(0, hi - lo);
-            const int64_t span = cost - s.fixed;
+            // a tile is worth its keys: BKV x G of the cost after the fixed
+            // part; what rounding leaves over goes with the last tile
+            const int64_t tile = static_cast<int64_t>(a.G) * BKV;
             auto cut = [&](int64_t x) -> int {   // tiles before cost x of the item
                 if (x <= s.fixed) return 0;
                 if (x >= cost) return p.nt;
-                return static_cast<int>((x - s.fixed) * p.nt / span);
+                return static_cast<int>(paged_min<int64_t>(paged_div(x - s.fixed, tile), p.nt));
             };
             const int64_t from = begin - item, to = end - item;
             p.t0 = cut(from);
@@ -265,7 +268,9 @@ struct PagedWalk {
             p.whole = p.t0 == 0 && p.t1 == p.nt && (p.nt > 0 || from <= 0);
             p.last = -1;
             const bool any = p.t1 > p.t0 || (p.nt == 0 && from <= 0);
-            if (any && p.t0 == 0 && !p.whole) p.last = paged_owner(W, n, item + cost - 1);
+            if (any && p.t0 == 0 && !p.whole)
+                p.last = static_cast<int>(paged_div(
+                    item + paged_min<int64_t>(s.fixed + p.nt * tile, cost) - 1, step));
             item += cost;
             if (++m == s.mt) {
                 m = 0;
@@ -286,5 +291,260 @@ struct PagedWalk {
         return false;
     }
 };
+
+// ---------------------------------------------------------------- parts in shared memory
+// One warp walks the stretch and hands the parts to the other roles through a
+// small ring, so that the walk's arithmetic and its registers are paid once.
+enum : int32_t { kPartWhole = 0, kPartFirst = 1, kPartLater = 2 };
+struct __align__(16) PagedItem {
+    int32_t b, g;
+    int32_t s0, n, kv;       // the sequence: first token, tokens, cached keys
+    int32_t frow0, rows;     // folded rows of the query tile (rows == 0: no more parts)
+    int32_t tv0, tv1;        // key tiles of this part
+    int32_t kind;            // kPart*
+    int32_t last;            // kPartFirst: the unit with the item's last part
+    int32_t pad;
+};
+constexpr int kPagedItems = 4;
+struct PagedRing {
+    PagedItem item[kPagedItems];
+    uint64_t full[kPagedItems], empty[kPagedItems];
+};
+// The walking warp waits for the slowest role, which may be a whole part
+// behind: that takes as long as the part does.
+constexpr uint64_t kPagedWalkLimitNs = 20000000000ull;
+
+// By one thread; `takers` arrivals free an entry.
+DG_DEVICE void paged_ring_init(PagedRing &ring, int takers)
+{
+    for (int e = 0; e < kPagedItems; ++e) {
+        mbar_init(&ring.full[e], 1);
+        mbar_init(&ring.empty[e], takers);
+    }
+}
+
+// The walking warp (all lanes).
+template <class Gm>
+DG_DEVICE void paged_walk(const PagedArgs &a, const PagedRange &range, PagedRing &ring, int where)
+{
+    const bool lead = (threadIdx.x & 31) == 0;
+    PagedWalk<Gm::Rows, Gm::BKV> walk;
+    walk.start(a, range);
+    PagedPart p;
+    for (uint32_t k = 0;; ++k) {
+        const bool more = walk.next(a, p);
+        const int e = static_cast<int>(k % kPagedItems);
+        const bool ok = mbar_wait_poll(&ring.empty[e], ((k / kPagedItems) & 1u) ^ 1u, a.ws, where,
+                                       kPagedWalkLimitNs);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return;
+        if (lead) {
+            PagedItem it{};
+            if (more) {
+                it.b = p.b;
+                it.g = p.g;
+                it.s0 = p.s.s0;
+                it.n = p.s.n;
+                it.kv = p.s.kv;
+                it.frow0 = p.frow0;
+                it.rows = p.rows;
+                it.tv0 = p.lo + p.t0;
+                it.tv1 = p.lo + p.t1;
+                it.kind = p.whole ? kPartWhole : p.last >= 0 ? kPartFirst : kPartLater;
+                it.last = p.last;
+            }
+            ring.item[e] = it;
+            mbar_arrive(&ring.full[e]);
+        }
+        if (!more) return;
+    }
+}
+
+// The k-th part, by every thread of a role's warp (or one thread alone, which
+// then passes alone = true).  False: no more parts, or a wait ran out.
+DG_DEVICE bool paged_take(const PagedArgs &a, PagedRing &ring, uint32_t k, PagedItem &it, bool alone,
+                          int where)
+{
+    const int e = static_cast<int>(k % kPagedItems);
+    bool ok = mbar_wait_poll(&ring.full[e], (k / kPagedItems) & 1u, a.ws, where);
+    if (!alone) ok = __all_sync(0xFFFFFFFFu, ok);
+    if (!ok) return false;
+    it = ring.item[e];
+    if (!alone) __syncwarp();
+    if (alone || (threadIdx.x & 31) == 0) mbar_arrive(&ring.empty[e]);
+    return it.rows > 0;
+}
+
+// Keys of key tile tv that exist, and its first key's place among all keys.
+template <int BKV>
+DG_DEVICE int paged_valid(const PagedItem &p, int tv)
+{
+    const int nkp = (p.kv + BKV - 1) / BKV;
+    return min(BKV, tv < nkp ? p.kv - tv * BKV : p.n - (tv - nkp) * BKV);
+}
+template <int BKV>
+DG_DEVICE int paged_key0(const PagedItem &p, int tv)
+{
+    const int nkp = (p.kv + BKV - 1) / BKV;
+    return tv < nkp ? tv * BKV : p.kv + (tv - nkp) * BKV;
+}
+
+// K steps of 16 keys that the last tile of n keys is multiplied with V in.
+DG_DEVICE int paged_steps(int n, int bkv)
+{
+    return ((n - 1) % bkv + 16) / 16;
+}
+
+// One ring's loads (K or V) over all parts.  The whole warp: lane l loads the
+// box (page piece l / NA, 64-dim atom l % NA) of a tile; the page ids of 32
+// pieces ahead are held one per lane, the next 32 already on their way.
+template <class Gm, int NS>
+__device__ __forceinline__ void paged_ring_producer(uint8_t *buf, uint64_t *full, uint64_t *empty,
+                                                    const CUtensorMap *map_c,
+                                                    const CUtensorMap *map_n, const PagedArgs &a,
+                                                    PagedRing &ring, int where)
+{
+    const int lane = threadIdx.x & 31;
+    const uint64_t pol = policy_evict_first();
+    const int R = a.box_rows, per_tile = Gm::BKV / R, batch = 32 / per_tile;
+    const int box = lane / Gm::NA, at = lane % Gm::NA;
+    uint32_t armed = 0, armed_par = 0;
+    uint32_t it = 0;
+    bool ok = true;
+    PagedItem p;
+    for (uint32_t k = 0; ok && paged_take(a, ring, k, p, false, where + 2); ++k) {
+        const int32_t *table = a.page_table + static_cast<int64_t>(p.b) * a.max_pages;
+        const int nkp = (p.kv + Gm::BKV - 1) / Gm::BKV;
+        auto fetch = [&](int tile) -> int32_t {   // page of piece `lane` from this tile on
+            const int key = tile * Gm::BKV + lane * R;
+            return key < p.kv && tile < p.tv1 ? __ldg(table + key / a.page_size) : 0;
+        };
+        int32_t pages = fetch(p.tv0), ahead = fetch(p.tv0 + batch);
+        int in = 0;
+        for (int tv = p.tv0; tv < p.tv1; ++tv, ++it, ++in) {
+            if (in == batch) {
+                in = 0;
+                pages = ahead;
+                ahead = fetch(tv + batch);
+            }
+            const int s = static_cast<int>(it % NS);
+            const uint32_t use = it / NS;
+            ok = mbar_wait_poll(&empty[s], (use & 1u) ^ 1u, a.ws, where);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = false;
+                break;
+            }
+            uint8_t *dst = buf + s * Gm::KVBytes;
+            if (tv < nkp) {
+                const int key0 = tv * Gm::BKV;
+                const int boxes = (min(Gm::BKV, p.kv - key0) + R - 1) / R;
+                int32_t page = __shfl_sync(0xFFFFFFFFu, pages, in * per_tile + min(box, per_tile - 1));
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(boxes * R * Gm::Dim * 2));
+                __syncwarp();
+                if (box < boxes) {
+                    // a page id outside the cache: the box lies outside the
+                    // tensor, which reads as zeros
+                    if (page < 0 || page >= a.n_pages) {
+                        report_error(a.ws, DG_ERR_DEVICE, 912);
+                        page = a.n_pages;
+                    }
+                    const int key = key0 + box * R;
+                    tma_load_4d(dst + at * Gm::KVAtomBytes + box * R * 128, map_c, &full[s], at * 64,
+                                p.g, key % a.page_size, page, pol);
+                }
+            } else {
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], Gm::KVBytes);
+                __syncwarp();
+                if (lane < Gm::NA)
+                    tma_load_3d(dst + lane * Gm::KVAtomBytes, map_n, &full[s], lane * 64, p.g,
+                                p.s0 + (tv - nkp) * Gm::BKV, pol);
+            }
+            armed |= 1u << s;
+            armed_par = (armed_par & ~(1u << s)) | ((use & 1u) << s);
+        }
+    }
+    // every copy has landed before the CTA leaves
+    for (int s = 0; s < NS; ++s)
+        if (armed >> s & 1u) mbar_wait(&full[s], armed_par >> s & 1u, a.ws, where + 1);
+}
+
+// 16 values of an output row as bf16, 32 bytes (wide: one aligned store, which
+// fills a memory sector; else two).
+DG_DEVICE void store_bf16x16(uint16_t *dst, const float (&v)[16], float f, bool wide)
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e] * f, v[2 * e + 1] * f);
+        w[e] = *reinterpret_cast<const uint32_t *>(&h2);
+    }
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Where a part keeps 4 values (dims c .. c + 3, c a multiple of 4) of a row:
+// [slot][D / 4][slot_rows][4], so that the threads of a warp, which hold
+// neighbouring rows, store and load neighbouring addresses.
+DG_DEVICE float4 *part_at(const PagedArgs &a, int slot, int row, int c)
+{
+    return reinterpret_cast<float4 *>(a.part_o) +
+           (static_cast<int64_t>(slot) * (a.D / 4) + c / 4) * a.slot_rows + row;
+}
+
+// Dims [c0, c1) of a row of O from TMEM: the output row (times f), or the part
+// slot as it is.  All lanes of the warp; only live rows store.
+template <int N>
+DG_DEVICE bool paged_store_row(const PagedArgs &a, uint32_t tmem_row, int c0, bool live, bool whole,
+                               uint16_t *row_out, float f, int slot, int row)
+{
+    bool finite = true;
+#pragma unroll 1
+    for (int c = c0; c < c0 + N; c += 32) {
+        uint32_t o[32];
+        tmem_ld32_nowait(tmem_row + c, o);
+        tmem_wait_ld();
+        if (!live) continue;
+        if (a.checks) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) finite &= isfinite(__uint_as_float(o[e])) != 0;
+        }
+        if (whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[16 * h + e]);
+                store_bf16x16(row_out + c + 16 * h, v, f, a.out_wide != 0);
+            }
+        } else {
+            float4 *dst = part_at(a, slot, row, c);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+                dst[static_cast<int64_t>(e / 4) * a.slot_rows] =
+                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+        }
+    }
+    return finite;
+}
+
+// The rows of a V tile between its last key and the next multiple of 16, up
+// to which it is multiplied: zero, whatever the page holds there.  By the 128
+// threads of a softmax group (t = 0 .. 127), after the tile has landed.
+template <class Gm>
+DG_DEVICE void paged_zero_tail(uint8_t *v_tile, int valid, int t)
+{
+    const int chunks = (((valid + 15) & ~15) - valid) * 8;   // 16-byte pieces of a 64-dim atom
+    for (int c = t; c < chunks * Gm::NA; c += 128)
+        *reinterpret_cast<uint4 *>(v_tile + c / chunks * Gm::KVAtomBytes + valid * 128 +
+                                   c % chunks * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+}
 
 }  // namespace dg

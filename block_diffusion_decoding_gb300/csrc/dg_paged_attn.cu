@@ -14,6 +14,7 @@
 //               (the bf16 P of a tile overwrites the S it came from);
 //   warp 0      TMA: K tiles, one box per page piece, into a 4-stage ring;
 //   warp 6      TMA: V tiles into a 3-stage ring;
+//   warp 7      the walk over the parts;
 //   warp 1      UMMA issuer: S(0), S(1), PV(0), S(2), PV(1), ...;
 //   warps 2-5   Q rows into TMEM, then the softmax, one query row a thread,
 //               with a reference maximum that moves only when a tile exceeds
@@ -29,6 +30,8 @@ namespace dg {
 
 template <int D>
 struct PagedGeom {
+    static constexpr int Dim = D;
+    static constexpr int Rows = 128;                       // query rows per tile
     static constexpr int BKV = (D == 128) ? 128 : 64;      // keys per tile
     static constexpr int NA = D / 64;                      // 64-dim atoms
     static constexpr int KVBytes = BKV * D * 2;            // 32 KB
@@ -43,88 +46,12 @@ struct PagedGeom {
     static constexpr int ColS = D;
     static constexpr int ColQ = D + 2 * BKV;
     static_assert(ColQ + D / 2 <= 512, "TMEM columns");
-    static_assert(Smem + sizeof(PagedScan) <= 232448, "shared memory");
+    static_assert(Smem + sizeof(PagedScan) + sizeof(PagedRing) <= 232448, "shared memory");
 };
 
 int paged_attn_smem_bytes(int D)
 {
     return D == 128 ? PagedGeom<128>::Smem : PagedGeom<256>::Smem;
-}
-
-// One ring's loads (K or V) over all parts.  The whole warp: lane l loads the
-// box (page piece l / NA, 64-dim atom l % NA) of a tile; the page ids of 32
-// pieces ahead are held one per lane, the next 32 already on their way.
-template <int D, int NS>
-__device__ __forceinline__ void paged_ring_producer(uint8_t *ring, uint64_t *full, uint64_t *empty,
-                                                    const CUtensorMap *map_c,
-                                                    const CUtensorMap *map_n, const PagedArgs &a,
-                                                    const PagedRange &range, int where)
-{
-    using Gm = PagedGeom<D>;
-    const int lane = threadIdx.x & 31;
-    const uint64_t pol = policy_evict_first();
-    const int R = a.box_rows, per_tile = Gm::BKV / R, batch = 32 / per_tile;
-    uint32_t armed = 0, armed_par = 0;
-    uint32_t it = 0;
-    bool ok = true;
-    PagedWalk<128, Gm::BKV> walk;
-    walk.start(a, range);
-    PagedPart p;
-    while (ok && walk.next(a, p)) {
-        const int32_t *table = a.page_table + static_cast<int64_t>(p.b) * a.max_pages;
-        const int tv0 = p.lo + p.t0, tv1 = p.lo + p.t1;
-        auto fetch = [&](int tile) -> int32_t {   // page of piece `lane` from this tile on
-            const int key = tile * Gm::BKV + lane * R;
-            return key < p.s.kv && tile < tv1 ? __ldg(table + key / a.page_size) : 0;
-        };
-        int32_t pages = fetch(tv0), ahead = fetch(tv0 + batch);
-        for (int tv = tv0; tv < tv1; ++tv, ++it) {
-            const int in = (tv - tv0) % batch;
-            if (in == 0 && tv > tv0) {
-                pages = ahead;
-                ahead = fetch(tv + batch);
-            }
-            const int s = static_cast<int>(it % NS);
-            const uint32_t use = it / NS;
-            ok = mbar_wait(&empty[s], (use & 1u) ^ 1u, a.ws, where);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-                ok = false;
-                break;
-            }
-            uint8_t *dst = ring + s * Gm::KVBytes;
-            if (tv < p.nkp) {
-                const int key0 = tv * Gm::BKV;
-                const int boxes = (min(Gm::BKV, p.s.kv - key0) + R - 1) / R;
-                const int box = lane / Gm::NA, at = lane % Gm::NA;
-                int32_t page = __shfl_sync(0xFFFFFFFFu, pages, in * per_tile + min(box, per_tile - 1));
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(boxes * R * D * 2));
-                __syncwarp();
-                if (box < boxes) {
-                    // a page id outside the cache: the box lies outside the
-                    // tensor, which reads as zeros
-                    if (page < 0 || page >= a.n_pages) {
-                        report_error(a.ws, DG_ERR_DEVICE, 912);
-                        page = a.n_pages;
-                    }
-                    const int key = key0 + box * R;
-                    tma_load_4d(dst + at * Gm::KVAtomBytes + box * R * 128, map_c, &full[s], at * 64,
-                                p.g, key % a.page_size, page, pol);
-                }
-            } else {
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], Gm::KVBytes);
-                __syncwarp();
-                if (lane < Gm::NA)
-                    tma_load_3d(dst + lane * Gm::KVAtomBytes, map_n, &full[s], lane * 64, p.g,
-                                p.s.s0 + (tv - p.nkp) * Gm::BKV, pol);
-            }
-            armed |= 1u << s;
-            armed_par = (armed_par & ~(1u << s)) | ((use & 1u) << s);
-        }
-    }
-    // every copy has landed before the CTA leaves
-    for (int s = 0; s < NS; ++s)
-        if (armed >> s & 1u) mbar_wait(&full[s], armed_par >> s & 1u, a.ws, where + 1);
 }
 
 template <int D>
@@ -136,6 +63,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     constexpr int BKV = Gm::BKV, NK = Gm::NK, NV = Gm::NV;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PagedScan scan;
+    __shared__ PagedRing ring;
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Gm::OffBar);
@@ -148,7 +76,8 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     uint64_t *p_full = pv_done + 2;          // [2]
     uint64_t *q_ready = p_full + 2;
     uint64_t *o_full = q_ready + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 1);
+    uint64_t *drained = o_full + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
 
     // inputs may come from the previous kernel of the stream; nor is TMEM
     // taken before that kernel has given its own back
@@ -171,6 +100,8 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         }
         mbar_init(q_ready, 4);
         mbar_init(o_full, 1);
+        mbar_init(drained, 1);
+        paged_ring_init(ring, 3 + 4);    // K, V, UMMA, softmax warps
         fence_barrier_init();
         tma_prefetch_desc(map_k);
         tma_prefetch_desc(map_v);
@@ -187,12 +118,13 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     paged_divide<128, BKV, kPagedThreads>(a, blockIdx.x, gridDim.x, scan);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const PagedRange range = scan.r;
 
     if (warp == 0) {
-        paged_ring_producer<D, NK>(smem + Gm::OffK, k_full, k_empty, map_k, map_kn, a, range, 921);
+        paged_ring_producer<Gm, NK>(smem + Gm::OffK, k_full, k_empty, map_k, map_kn, a, ring, 921);
     } else if (warp == 6) {
-        paged_ring_producer<D, NV>(smem + Gm::OffV, v_full, v_empty, map_v, map_vn, a, range, 923);
+        paged_ring_producer<Gm, NV>(smem + Gm::OffV, v_full, v_empty, map_v, map_vn, a, ring, 924);
+    } else if (warp == 7) {
+        paged_walk<Gm>(a, scan.r, ring, 927);
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMA
         if (lane == 0) {
@@ -202,18 +134,16 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
             const uint32_t sv0 = smem_u32(smem + Gm::OffV);
             uint32_t it0 = 0, parts = 0;    // tiles and parts before this part
             bool ok = true;
-            PagedWalk<128, BKV> walk;
-            walk.start(a, range);
-            PagedPart p;
-            while (ok && walk.next(a, p)) {
-                const int nt = p.t1 - p.t0;
+            PagedItem p;
+            for (uint32_t k = 0; ok && paged_take(a, ring, k, p, true, 930); ++k) {
+                const int nt = p.tv1 - p.tv0;
                 if (nt == 0) continue;
-                ok = mbar_wait(q_ready, parts & 1u, a.ws, 931);
+                ok = mbar_wait_poll(q_ready, parts & 1u, a.ws, 931);
                 tc_fence_after();
                 auto issue_s = [&](int j) -> bool {
                     const uint32_t it = it0 + j;
                     const int s = static_cast<int>(it % NK);
-                    if (!mbar_wait(&k_full[s], (it / NK) & 1u, a.ws, 932)) return false;
+                    if (!mbar_wait_poll(&k_full[s], (it / NK) & 1u, a.ws, 932)) return false;
                     tc_fence_after();
                     const uint32_t sk = sk0 + s * Gm::KVBytes;
                     const uint32_t d = tmem + Gm::ColS + (it & 1) * BKV;
@@ -230,15 +160,12 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 auto issue_pv = [&](int j) -> bool {
                     const uint32_t it = it0 + j;
                     const int s = static_cast<int>(it % NV);
-                    if (!mbar_wait(&p_full[it & 1], (it >> 1) & 1u, a.ws, 933)) return false;
-                    if (!mbar_wait(&v_full[s], (it / NV) & 1u, a.ws, 934)) return false;
+                    if (!mbar_wait_poll(&p_full[it & 1], (it >> 1) & 1u, a.ws, 933)) return false;
+                    if (!mbar_wait_poll(&v_full[s], (it / NV) & 1u, a.ws, 934)) return false;
                     tc_fence_after();
                     const uint32_t sv = sv0 + s * Gm::KVBytes;
                     const uint32_t pa = tmem + Gm::ColS + (it & 1) * BKV;
-                    const int tv = p.lo + p.t0 + j;
-                    const int valid = tv < p.nkp ? p.s.kv - tv * BKV
-                                                 : p.s.n - (tv - p.nkp) * BKV;
-                    const int steps = min(BKV, valid + 15) / 16;
+                    const int steps = (paged_valid<BKV>(p, p.tv0 + j) + 15) / 16;
                     for (int kk = 0; kk < steps; ++kk) {
                         const uint64_t bdesc =
                             make_sdesc_sw128(sv + kk * 2048, Gm::KVAtomBytes, 1024);
@@ -256,7 +183,8 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 ++parts;
             }
             // every UMMA and commit is done before the CTA leaves
-            if (parts > 0) mbar_wait(o_full, (parts - 1) & 1u, a.ws, 935);
+            umma_commit(drained);
+            mbar_wait_poll(drained, 0, a.ws, 935);
         }
     } else {
         // -------------------------------------------------------------- softmax
@@ -266,15 +194,13 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         uint32_t it = 0, parts = 0;
         bool ok = true;
         PagedDesc de{-1, 0, 0, 0, 0, 0, {0, 0}};
-        PagedWalk<128, BKV> walk;
-        walk.start(a, range);
-        PagedPart p;
-        while (ok && walk.next(a, p)) {
-            const int nt = p.t1 - p.t0;
+        PagedItem p;
+        for (uint32_t k = 0; ok && paged_take(a, ring, k, p, false, 940); ++k) {
+            const int nt = p.tv1 - p.tv0;
             const bool live = r < p.rows;
             const int frow = p.frow0 + (live ? r : 0);
             const int i = frow / a.G, hj = frow - i * a.G;
-            const int64_t tok = p.s.s0 + i;
+            const int64_t tok = p.s0 + i;
             const int head = p.g * a.G + hj;
             uint16_t *row_out = a.out + tok * a.out_stride + static_cast<int64_t>(head) * D;
             if (nt == 0) {                       // no key to see: a zero row
@@ -311,27 +237,19 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 if (lane == 0) mbar_arrive(q_ready);
             }
             // position of this row, and the keys it sees
-            const int pos = (a.has_new ? p.s.kv : p.s.kv - p.s.n) + i;
+            const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j, ++it) {
                 const int sb = static_cast<int>(it & 1u);
-                const int tv = p.lo + p.t0 + j;
-                const bool paged = tv < p.nkp;
-                const int valid = min(BKV, paged ? p.s.kv - tv * BKV : p.s.n - (tv - p.nkp) * BKV);
-                const int key0 = paged ? tv * BKV : p.s.kv + (tv - p.nkp) * BKV;
+                const int valid = paged_valid<BKV>(p, p.tv0 + j);
+                const int key0 = paged_key0<BKV>(p, p.tv0 + j);
                 if (valid & 15) {
-                    // V rows from the last key to the next multiple of 16: zero
                     const int s = static_cast<int>(it % NV);
-                    ok = mbar_wait(&v_full[s], (it / NV) & 1u, a.ws, 941);
+                    ok = mbar_wait_poll(&v_full[s], (it / NV) & 1u, a.ws, 941);
                     if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                    uint8_t *sv = smem + Gm::OffV + s * Gm::KVBytes;
-                    const int chunks = (((valid + 15) & ~15) - valid) * 8;
-                    for (int c = threadIdx.x - 64; c < chunks * Gm::NA; c += 128)
-                        *reinterpret_cast<uint4 *>(sv + c / chunks * Gm::KVAtomBytes + valid * 128 +
-                                                   c % chunks * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
+                    paged_zero_tail<Gm>(smem + Gm::OffV + s * Gm::KVBytes, valid, threadIdx.x - 64);
                 }
-                ok = mbar_wait(&s_full[sb], (it >> 1) & 1u, a.ws, 942);
+                ok = mbar_wait_poll(&s_full[sb], (it >> 1) & 1u, a.ws, 942);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
                 if (busy) {
@@ -382,7 +300,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     l += acc.x + acc.y;
                     if (__any_sync(0xFFFFFFFFu, rescale)) {
                         // O holds the PVs up to the tile before: wait for the last one
-                        ok = mbar_wait(&pv_done[sb ^ 1], ((it - 1) >> 1) & 1u, a.ws, 943);
+                        ok = mbar_wait_poll(&pv_done[sb ^ 1], ((it - 1) >> 1) & 1u, a.ws, 943);
                         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                         tc_fence_after();
 #pragma unroll 1
@@ -408,54 +326,22 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
             }
             if (!ok) break;
             // ---------------------------------------------------------- epilogue
-            ok = mbar_wait(o_full, parts & 1u, a.ws, 944);
+            ok = mbar_wait_poll(o_full, parts & 1u, a.ws, 944);
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             ++parts;
             tc_fence_after();
-            const int slot = 2 * blockIdx.x + (p.last >= 0 ? 1 : 0);
-            const int64_t prow = static_cast<int64_t>(slot) * a.slot_rows + r;
-            if (!p.whole) {
-                if (p.last >= 0)
-                    de = PagedDesc{p.last, p.rows, p.frow0, p.s.s0, p.g * a.G, de.part0, {0, 0}};
-                else
-                    de.part0 = 1;
-                if (live) a.part_ml[prow] = make_float2(m_ref, l);
-            }
+            const int slot = 2 * blockIdx.x + (p.kind == kPartFirst ? 1 : 0);
+            if (p.kind == kPartFirst)
+                de = PagedDesc{p.last, p.rows, p.frow0, p.s0, p.g * a.G, de.part0, {0, 0}};
+            else if (p.kind == kPartLater)
+                de.part0 = 1;
+            if (p.kind != kPartWhole && live)
+                a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + r] = make_float2(m_ref, l);
             const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
             bool badv = a.checks && live && !isfinite(l);
-            if (busy) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32_nowait(tmem + lane_off + Gm::ColO + c0, o);
-                    tmem_wait_ld();
-                    if (!live) continue;
-                    if (a.checks) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) badv |= !isfinite(__uint_as_float(o[k]));
-                    }
-                    if (p.whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(row_out + c0);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            uint32_t w4[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 h2 = __floats2bfloat162_rn(
-                                    __uint_as_float(o[k + 2 * e]) * inv_l,
-                                    __uint_as_float(o[k + 2 * e + 1]) * inv_l);
-                                w4[e] = *reinterpret_cast<const uint32_t *>(&h2);
-                            }
-                            dst[k >> 3] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                        }
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + prow * D + c0);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            dst[k >> 2] = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                    }
-                }
-            }
+            if (busy)
+                badv |= !paged_store_row<D>(a, tmem + lane_off + Gm::ColO, 0, live,
+                                            p.kind == kPartWhole, row_out, inv_l, slot, r);
             if (badv) report_error(a.ws, DG_ERR_DEVICE, 945);
             tc_fence_before();   // O is read before the next part's first PV
         }
@@ -487,115 +373,112 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_attn_body<256>(&map_k, &map_v, &map_kn, &map_vn, a);
 }
 
-// Joins the parts of the items that were cut: CTA (c, y) takes rows of the
-// item whose first part CTA c left in its slot 1; the others are slot 0 of
-// CTAs c + 1 .. last, taken in that order.  out = sum 2^(m_z - M) O_z /
-// sum 2^(m_z - M) l_z.  Items of few rows (single tokens) give a row to a
-// whole block, its 8 warps each a share of the parts; larger ones a row to a
-// warp.
-__global__ void __launch_bounds__(256) paged_merge_kernel(PagedArgs a)
+// Joins the parts of the items that were cut: the blocks (c, y) take the item
+// whose first part unit c left in its slot 1; the others are slot 0 of units
+// c + 1 .. last, taken in that order.  out = sum 2^(m_z - M) O_z /
+// sum 2^(m_z - M) l_z.  A thread takes 16 dims of a row, neighbouring threads
+// neighbouring rows.  An item too small to fill a block with those (single
+// tokens, whose caches may have parts from every SM) shares its parts out over
+// the block's threads and joins their results in shared memory.
+struct MergeState {
+    float M, den;
+    float acc[16];
+};
+
+DG_DEVICE void merge_add(MergeState &s, float m, float l, const float (&x)[16])
 {
-    __shared__ float s_acc[8][256];
-    __shared__ float2 s_ml[8];
+    if (l == 0.f) return;                    // no visible key there
+    if (m > s.M) {
+        const float f = fast_exp2(s.M - m);  // 0 while M = -inf
+        s.den *= f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s.acc[e] *= f;
+        s.M = m;
+    }
+    const float w = fast_exp2(m - s.M);
+    s.den = fmaf(w, l, s.den);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s.acc[e] = fmaf(w, x[e], s.acc[e]);
+}
+
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedArgs a)
+{
+    __shared__ float s_state[18][kMergeThreads];
     griddep_wait();
     griddep_launch_dependents();
     const int c = blockIdx.x;
     const PagedDesc de = a.desc[c];
     if (de.last < 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = a.D / 32;            // 4 or 8 consecutive dims per lane
-    const bool block_row = de.rows <= static_cast<int>(gridDim.y);
-    for (int r0 = block_row ? blockIdx.y : blockIdx.y * 8; r0 < de.rows;
-         r0 += block_row ? gridDim.y : gridDim.y * 8) {
-        const int r = block_row ? r0 : r0 + warp;
-        const bool live = r < de.rows;
-        float M = -INFINITY, den = 0.f;
-        float acc[8];
+    const int pairs = de.rows * (a.D / 16);
+    // threads that share a pair's parts
+    int share = 1;
+    while (share < 32 && pairs * share * 2 <= kMergeThreads) share *= 2;
+    if (share > 1 && blockIdx.y > 0) return;
+    for (int p0 = blockIdx.y * kMergeThreads; p0 < pairs; p0 += gridDim.y * kMergeThreads) {
+        const int at = p0 + static_cast<int>(threadIdx.x);
+        const int part = share > 1 ? at / pairs : 0;
+        const int pair = at - part * pairs;
+        const bool live = part < share && pair < pairs;
+        const int dg = pair / de.rows, row = pair - dg * de.rows;
+        MergeState s;
+        s.M = -INFINITY;
+        s.den = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        const int step = block_row ? 8 : 1;
+        for (int e = 0; e < 16; ++e) s.acc[e] = 0.f;
         if (live) {
-            for (int z0 = c + (block_row ? warp : 0); z0 <= de.last; z0 += 4 * step) {
-                float2 ml[4];
-                float4 v[4][2];
+            for (int z0 = c + part; z0 <= de.last; z0 += 2 * share) {
+                float2 ml[2];
+                float x[2][16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int z = z0 + k * step;
-                    const bool have = z <= de.last && (z == c || a.desc[z].part0 != 0);
-                    ml[k] = make_float2(-INFINITY, 0.f);
-                    v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (have) {
-                        const int64_t row =
-                            static_cast<int64_t>(2 * z + (z == c ? 1 : 0)) * a.slot_rows + r;
-                        ml[k] = a.part_ml[row];
-                        const float4 *src =
-                            reinterpret_cast<const float4 *>(a.part_o + row * a.D + lane * per);
-                        v[k][0] = src[0];
-                        if (per == 8) v[k][1] = src[1];
+                for (int k = 0; k < 2; ++k) {
+                    const int z = z0 + k * share;
+                    ml[k] = make_float2(0.f, 0.f);
+                    if (z > de.last) continue;
+                    const int slot = 2 * z + (z == c ? 1 : 0);
+                    const bool have = z == c || a.desc[z].part0 != 0;
+                    const float2 v = a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + row];
+                    const float4 *src = part_at(a, slot, row, dg * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 f = src[static_cast<int64_t>(e) * a.slot_rows];
+                        x[k][4 * e] = f.x;
+                        x[k][4 * e + 1] = f.y;
+                        x[k][4 * e + 2] = f.z;
+                        x[k][4 * e + 3] = f.w;
                     }
+                    if (have) ml[k] = v;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (ml[k].y == 0.f) continue;        // no visible key in this part
-                    if (ml[k].x > M) {
-                        const float f = fast_exp2(M - ml[k].x);   // 0 while M = -inf
-                        den *= f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[e] *= f;
-                        M = ml[k].x;
-                    }
-                    const float w = fast_exp2(ml[k].x - M);
-                    den = fmaf(w, ml[k].y, den);
-                    const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
-                                        v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, x[e], acc[e]);
-                }
+                for (int k = 0; k < 2; ++k) merge_add(s, ml[k].x, ml[k].y, x[k]);
             }
         }
-        if (block_row) {
-            __syncthreads();             // the row before has been read
-            if (lane == 0) s_ml[warp] = make_float2(M, den);
+        if (share > 1) {
+            s_state[0][threadIdx.x] = s.M;
+            s_state[1][threadIdx.x] = s.den;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < per) s_acc[warp][lane * per + e] = acc[e];
+            for (int e = 0; e < 16; ++e) s_state[2 + e][threadIdx.x] = s.acc[e];
             __syncthreads();
-            if (warp > 0) continue;
-            float Mt = -INFINITY, dt = 0.f;
-            for (int w = 0; w < 8; ++w)
-                if (s_ml[w].y != 0.f) Mt = fmaxf(Mt, s_ml[w].x);
+            if (part > 0) continue;              // (one round: nothing follows)
+            for (int k = 1; live && k < share; ++k) {
+                const int t = threadIdx.x + k * pairs;
+                float x[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-            for (int w = 0; w < 8; ++w) {
-                const float2 ml = s_ml[w];
-                if (ml.y == 0.f) continue;
-                const float f = fast_exp2(ml.x - Mt);
-                dt = fmaf(f, ml.y, dt);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < per) acc[e] = fmaf(f, s_acc[w][lane * per + e], acc[e]);
+                for (int e = 0; e < 16; ++e) x[e] = s_state[2 + e][t];
+                merge_add(s, s_state[0][t], s_state[1][t], x);
             }
-            den = dt;
         }
         if (!live) continue;
-        const float inv = den == 0.f ? 0.f : 1.f / den;
         if (a.checks) {
-            bool bad = !isfinite(den);
+            bool bad = !isfinite(s.den);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) bad |= !isfinite(acc[e]);
+            for (int e = 0; e < 16; ++e) bad |= !isfinite(s.acc[e]);
             if (bad) report_error(a.ws, DG_ERR_DEVICE, 951);
         }
-        const int frow = de.frow0 + r;
+        const int frow = de.frow0 + row;
         const int i = frow / a.G, hj = frow - i * a.G;
-        uint16_t *dst = a.out + static_cast<int64_t>(de.s0 + i) * a.out_stride +
-                        static_cast<int64_t>(de.head0 + hj) * a.D + lane * per;
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            if (e < per) {
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-                *reinterpret_cast<uint32_t *>(dst + e) = *reinterpret_cast<const uint32_t *>(&h2);
-            }
-        }
+        store_bf16x16(a.out + static_cast<int64_t>(de.s0 + i) * a.out_stride +
+                          static_cast<int64_t>(de.head0 + hj) * a.D + dg * 16,
+                      s.acc, s.den == 0.f ? 0.f : 1.f / s.den, a.out_wide != 0);
     }
 }
 

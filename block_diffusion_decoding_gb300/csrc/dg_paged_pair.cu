@@ -1,0 +1,624 @@
+// dg_paged_pair.cu -- paged attention of chunks: sequences with more folded
+// query rows than one 128-row tile.
+//
+// What dg_paged_attn.cu computes, on 2-CTA clusters that issue 2-SM UMMAs.
+// A query tile has 256 rows, 128 per CTA, and both CTAs share every tile of
+// 128 keys: CTA r stages keys [64 r, 64 r + 64) of K and dims
+// [r D / 2, (r + 1) D / 2) of V, so a key costs each SM half the shared-memory
+// traffic of a single-CTA tile and the tensor cores run at their full rate
+// (2 x 512 cycles a tile at D = 128, 2 x 1024 at D = 256).
+//
+// One warpgroup's softmax of a 128 x 128 tile takes about 1800 cycles from
+// the arrival of S to that of P (TMEM loads 170, maximum 400, exponentials
+// and packing 900, stores and signals 300), more than the UMMAs of a tile.
+// So two warpgroups take the tiles in turn, and S is buffered (3 tiles at
+// D = 128, 2 at D = 256) far enough ahead of them.  The running maximum goes
+// from one to the other through shared memory right after each tile's
+// maximum, long before its exponentials; each keeps the sum of its own tiles.
+//   TMEM        O [128 x D] fp32 | S buffers [128 x 128] fp32 (the bf16 P of a
+//               tile overwrites the S it came from);
+//   warp 0      TMA: K halves;    warp 2   TMA: V halves;    warp 3   the walk;
+//   warp 1      UMMA issuer (even CTA): S runs NS - 1 tiles ahead of PV;
+//   warps 4-7   softmax of the even tiles, a query row a thread; warps 8-11 of
+//               the odd ones; both load Q rows, and each stores half of O.
+// All copies of a tile complete on the even CTA's barrier.  Only where V needs
+// its tail zeroed (see dg_paged_attn.cu) each CTA's half lands on a barrier
+// of its own, and the arrival of P tells that it has been cleaned.
+#include "dg_paged.cuh"
+
+namespace dg {
+
+template <int D>
+struct PairGeom {
+    static constexpr int Dim = D;
+    static constexpr int Rows = kPagedPairRows;
+    static constexpr int BKV = 128;
+    static constexpr int HK = BKV / 2;                     // keys of K this CTA stages
+    static constexpr int NAK = D / 64;                     // 64-dim atoms of a K row
+    static constexpr int NA = D / 128;                     // of this CTA's V half
+    static constexpr int KAtomBytes = HK * 128;
+    static constexpr int KBytes = NAK * KAtomBytes;
+    static constexpr int KVAtomBytes = BKV * 128;          // V
+    static constexpr int VBytes = NA * KVAtomBytes;
+    static constexpr int NS = D == 128 ? 3 : 2;            // S buffers
+    static constexpr int NK = D == 128 ? 6 : 3;
+    static constexpr int NV = D == 128 ? 6 : 2;
+    static constexpr int QAtomBytes = 128 * 128;
+    static constexpr int QBytes = NAK * QAtomBytes;
+    static constexpr int OffQ = 0;
+    static constexpr int OffK = OffQ + QBytes;
+    static constexpr int OffV = OffK + NK * KBytes;
+    static constexpr int OffShared = OffV + NV * VBytes;
+    static constexpr int ColO = 0;
+    static constexpr int ColS = D;
+    static_assert(ColS + NS * BKV <= 512, "TMEM columns");
+};
+
+struct PairShared {
+    PagedScan scan;
+    PagedRing ring;
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_land[6];
+    uint64_t s_full[3], p_full[3];    // by S buffer: P(t + NS) cannot be signalled before
+                                      // the UMMA warp has seen P(t) of both CTAs
+    uint64_t pv_done[2];              // by tile parity
+    uint64_t m_full[2][4];            // by tile parity and lane quadrant
+    uint64_t l_full[2][4];            // by warpgroup and lane quadrant
+    uint64_t q_ready, o_full, o_free, drained;
+    uint32_t tmem;
+    float m[2][128];                  // running maximum after a tile, by its parity
+    float l[2][128];                  // sum of a warpgroup's tiles of a part
+};
+static_assert(PairGeom<128>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
+static_assert(PairGeom<256>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
+
+int paged_pair_smem_bytes(int D)
+{
+    return static_cast<int>((D == 128 ? PairGeom<128>::OffShared : PairGeom<256>::OffShared) +
+                            sizeof(PairShared));
+}
+
+// One ring's loads, as paged_ring_producer, for this CTA's half of every tile.
+template <class Gm, bool IS_V>
+__device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint32_t lead_full, int r,
+                                              const CUtensorMap *map_c, const CUtensorMap *map_n,
+                                              const PagedArgs &a, int where)
+{
+    constexpr int NS = IS_V ? Gm::NV : Gm::NK;
+    constexpr int Bytes = IS_V ? Gm::VBytes : Gm::KBytes;
+    constexpr int Atom = IS_V ? Gm::KVAtomBytes : Gm::KAtomBytes;
+    constexpr int Atoms = IS_V ? Gm::NA : Gm::NAK;
+    constexpr int Keys = IS_V ? Gm::BKV : Gm::HK;          // keys of a tile this CTA loads
+    uint64_t *full = IS_V ? sh.v_full : sh.k_full, *empty = IS_V ? sh.v_empty : sh.k_empty;
+    const int lane = threadIdx.x & 31;
+    const uint64_t pol = policy_evict_normal();
+    const int R = a.box_rows, per_tile = Keys / R, batch = 32 / per_tile;
+    const int box = lane / Atoms, at = lane % Atoms;
+    const int key_off = IS_V ? 0 : r * Gm::HK;             // of this CTA's keys in a tile
+    const int dim0 = (IS_V ? r * Gm::NA : 0) * 64 + at * 64;
+    uint32_t armed = 0, armed_par = 0, landing = 0;        // by stage; landing: parity of v_land
+    int s = 0;
+    uint32_t par = 0;                                      // parity of the stages' use
+    bool ok = true;
+    PagedItem p;
+    for (uint32_t k = 0; ok && paged_take(a, sh.ring, k, p, false, where + 2); ++k) {
+        const int32_t *table = a.page_table + static_cast<int64_t>(p.b) * a.max_pages;
+        const int nkp = (p.kv + Gm::BKV - 1) / Gm::BKV;
+        // page of piece `lane` from this tile on
+        auto fetch = [&](int tile) -> int32_t {
+            const int t = tile + lane / per_tile;
+            const int key = t * Gm::BKV + key_off + lane % per_tile * R;
+            return key < p.kv && t < p.tv1 ? __ldg(table + key / a.page_size) : 0;
+        };
+        int32_t pages = fetch(p.tv0), ahead = fetch(p.tv0 + batch);
+        int in = 0;
+        for (int tv = p.tv0; tv < p.tv1; ++tv, ++in) {
+            if (in == batch) {
+                in = 0;
+                pages = ahead;
+                ahead = fetch(tv + batch);
+            }
+            ok = mbar_wait_poll(&empty[s], par ^ 1u, a.ws, where);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = false;
+                break;
+            }
+            const int valid = paged_valid<Gm::BKV>(p, tv);
+            const bool paged = tv < nkp;
+            const bool own = IS_V && (valid & 15) != 0;    // lands on this CTA's own barrier
+            const int mine = paged ? (max(0, min(Keys, valid - key_off)) + R - 1) / R : 0;   // boxes
+            if (lane == 0) {
+                // what both halves bring, or this one alone
+                const uint32_t tile_bytes =
+                    paged ? static_cast<uint32_t>((valid + R - 1) / R * R * Gm::Dim * 2)
+                          : static_cast<uint32_t>(Gm::BKV * Gm::Dim * 2);
+                if (own) {
+                    mbar_arrive_expect_tx(&sh.v_land[s], tile_bytes / 2);
+                    if (r == 0) mbar_arrive(&full[s]);
+                } else if (r == 0) {
+                    mbar_arrive_expect_tx(&full[s], tile_bytes);
+                }
+            }
+            const int32_t piece = __shfl_sync(0xFFFFFFFFu, pages, in * per_tile + min(box, per_tile - 1));
+            const uint32_t bar = own ? mapa_shared(smem_u32(&sh.v_land[s]), r) : lead_full + s * 8;
+            uint8_t *dst = buf + s * Bytes + at * Atom;
+            if (paged) {
+                if (box < mine) {
+                    // a page id outside the cache: the box lies outside the
+                    // tensor, which reads as zeros
+                    int32_t page = piece;
+                    if (page < 0 || page >= a.n_pages) {
+                        report_error(a.ws, DG_ERR_DEVICE, 912);
+                        page = a.n_pages;
+                    }
+                    const int key = tv * Gm::BKV + key_off + box * R;
+                    tma_load_4d_pair(dst + box * R * 128, map_c, bar, dim0, p.g, key % a.page_size,
+                                     page, pol);
+                }
+            } else if (box == 0) {
+                tma_load_3d_pair(dst, map_n, bar, dim0, p.g, p.s0 + (tv - nkp) * Gm::BKV + key_off,
+                                 pol);
+            }
+            if (own) landing ^= 1u << s;
+            armed |= 1u << s;
+            armed_par = (armed_par & ~(1u << s)) | (par << s);
+            if (++s == NS) {
+                s = 0;
+                par ^= 1u;
+            }
+        }
+    }
+    // every copy has landed before the closing cluster barrier lets either
+    // CTA leave: the even CTA's barriers tell of both CTAs' copies
+    for (int e = 0; e < NS; ++e) {
+        if (r == 0 && (armed >> e & 1u)) mbar_wait_poll(&full[e], armed_par >> e & 1u, a.ws, where + 1);
+        if (IS_V) {
+            // `landing` toggles with every use, so its last phase has parity
+            // landing ^ 1 (before any use: the phase before the first, over)
+            mbar_wait_poll(&sh.v_land[e], (landing >> e & 1u) ^ 1u, a.ws, where + 1);
+        }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const CUtensorMap *map_v,
+                                                const CUtensorMap *map_kn,
+                                                const CUtensorMap *map_vn, const PagedArgs &a)
+{
+    using Gm = PairGeom<D>;
+    constexpr int BKV = Gm::BKV, NK = Gm::NK, NV = Gm::NV, NS = Gm::NS;
+    // no room to round the base up: nothing else is in shared memory, so it
+    // starts where the swizzled tiles need it
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PairShared &sh = *reinterpret_cast<PairShared *>(smem + Gm::OffShared);
+    if (smem_u32(smem) & 1023u) {
+        report_error(a.ws, DG_ERR_DEVICE, 1000);
+        return;
+    }
+
+    // inputs may come from the previous kernel of the stream; nor is TMEM
+    // taken before that kernel has given its own back
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = static_cast<int>(cluster_ctarank());
+    const int unit = static_cast<int>(cluster_id_x());
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < NK; ++s) {
+            mbar_init(&sh.k_full[s], 1);
+            mbar_init(&sh.k_empty[s], 1);
+        }
+        for (int s = 0; s < NV; ++s) {
+            mbar_init(&sh.v_full[s], 1);
+            mbar_init(&sh.v_empty[s], 1);
+            mbar_init(&sh.v_land[s], 1);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&sh.s_full[s], 1);
+            mbar_init(&sh.p_full[s], 8);             // a warpgroup of each CTA
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&sh.pv_done[h], 1);
+            for (int q = 0; q < 4; ++q) {
+                mbar_init(&sh.m_full[h][q], 1);
+                mbar_init(&sh.l_full[h][q], 1);
+            }
+        }
+        mbar_init(&sh.q_ready, 16);                  // the softmax warps of both CTAs
+        mbar_init(&sh.o_full, 1);
+        mbar_init(&sh.o_free, 16);
+        mbar_init(&sh.drained, 1);
+        paged_ring_init(sh.ring, r == 0 ? 11 : 10);  // K, V, softmax warps; UMMA (even CTA)
+        fence_barrier_init();
+        tma_prefetch_desc(map_k);
+        tma_prefetch_desc(map_v);
+        if (a.has_new) {
+            tma_prefetch_desc(map_kn);
+            tma_prefetch_desc(map_vn);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&sh.tmem, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    paged_divide<Gm::Rows, BKV, kPagedPairThreads>(a, unit, static_cast<int>(num_clusters_x()),
+                                                   sh.scan);
+    tc_fence_after();
+    // both CTAs' barriers exist before either signals the other
+    cluster_sync_all();
+    const uint32_t tmem = sh.tmem;
+    auto lead_of = [&](const uint64_t *bar) -> uint32_t { return mapa_shared(smem_u32(bar), 0); };
+
+    if (warp == 0) {
+        pair_producer<Gm, false>(smem + Gm::OffK, sh, lead_of(sh.k_full), r, map_k, map_kn, a, 1001);
+    } else if (warp == 2) {
+        pair_producer<Gm, true>(smem + Gm::OffV, sh, lead_of(sh.v_full), r, map_v, map_vn, a, 1004);
+    } else if (warp == 3) {
+        paged_walk<Gm>(a, sh.scan.r, sh.ring, 1007);
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMA
+        // (the whole warp of the even CTA, see elect_lane)
+        if (r == 0) {
+            const uint32_t idesc_s = make_idesc_bf16(256, BKV, 0);
+            const uint32_t idesc_o = make_idesc_bf16(256, D, 1);
+            // descriptors of the buffers' first tiles; the address sits in
+            // the low bits in units of 16 bytes
+            const uint64_t dq = make_sdesc_sw128(smem_u32(smem + Gm::OffQ), 16, 1024);
+            const uint64_t dk0 = make_sdesc_sw128(smem_u32(smem + Gm::OffK), 16, 1024);
+            const uint64_t dv0 = make_sdesc_sw128(smem_u32(smem + Gm::OffV), Gm::KVAtomBytes, 1024);
+            int ks = 0, vs = 0, ss = 0, ps = 0;      // stages of K, V, S (written), S (read as P)
+            uint32_t kpar = 0, vpar = 0, ppar = 0;
+            uint32_t pv = 0, parts = 0;              // tiles multiplied with V, parts
+            bool ok = true;
+            const bool lead = elect_lane();
+            PagedItem p;
+            for (uint32_t k = 0; ok && paged_take(a, sh.ring, k, p, false, 1010); ++k) {
+                const int nt = p.tv1 - p.tv0;
+                if (nt == 0) continue;
+                ok = mbar_wait_poll<true>(&sh.q_ready, parts & 1u, a.ws, 1011);
+                ++parts;
+                const int steps_kv = paged_steps(p.kv, BKV), steps_new = paged_steps(p.n, BKV);
+                const int j_kv = (p.kv + BKV - 1) / BKV - 1 - p.tv0;   // last tile of the pages
+                const int j_new = j_kv + (p.n + BKV - 1) / BKV;        // of the new tokens
+                for (int j = 0; j < nt + NS - 1 && ok; ++j) {
+                    if (j < nt) {
+                        ok = mbar_wait_poll(&sh.k_full[ks], kpar, a.ws, 1012);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dk = dk0 + ks * (Gm::KBytes >> 4);
+                        const uint32_t d = tmem + Gm::ColS + ss * BKV;
+                        if (lead) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma_bf16_pair(
+                                    d, dq + (((kk >> 2) * Gm::QAtomBytes + (kk & 3) * 32) >> 4),
+                                    dk + (((kk >> 2) * Gm::KAtomBytes + (kk & 3) * 32) >> 4), idesc_s,
+                                    kk != 0);
+                            umma_commit_pair(&sh.s_full[ss], 0x3);
+                            umma_commit_pair(&sh.k_empty[ks], 0x3);
+                        }
+                        if (++ss == NS) ss = 0;
+                        if (++ks == NK) {
+                            ks = 0;
+                            kpar ^= 1u;
+                        }
+                    }
+                    const int jp = j - (NS - 1);
+                    if (jp >= 0) {
+                        // both CTAs' softmax warps have written P
+                        // (and read the O of the part before this one)
+                        ok = mbar_wait_poll(&sh.v_full[vs], vpar, a.ws, 1014) &&
+                             mbar_wait_poll<true>(&sh.p_full[ps], ppar, a.ws, 1013) &&
+                             (jp > 0 || parts < 2 ||
+                              mbar_wait_poll<true>(&sh.o_free, parts & 1u, a.ws, 1016));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int steps = jp == j_kv ? steps_kv : jp == j_new ? steps_new : BKV / 16;
+                        const uint64_t dv = dv0 + vs * (Gm::VBytes >> 4);
+                        const uint32_t pa = tmem + Gm::ColS + ps * BKV;
+                        if (lead) {
+                            umma_bf16_pair_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
+                            if (steps == BKV / 16) {
+#pragma unroll
+                                for (int kk = 1; kk < BKV / 16; ++kk)
+                                    umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
+                                                      idesc_o, 1);
+                            } else {
+                                for (int kk = 1; kk < steps; ++kk)
+                                    umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
+                                                      idesc_o, 1);
+                            }
+                            umma_commit_pair(&sh.v_empty[vs], 0x3);
+                            umma_commit_pair(&sh.pv_done[pv & 1], 0x3);
+                            if (jp + 1 == nt) umma_commit_pair(&sh.o_full, 0x3);
+                        }
+                        ++pv;
+                        if (++ps == NS) {
+                            ps = 0;
+                            ppar ^= 1u;
+                        }
+                        if (++vs == NV) {
+                            vs = 0;
+                            vpar ^= 1u;
+                        }
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+            }
+            // every UMMA and commit is done before the cluster leaves
+            if (lead) umma_commit_pair(&sh.drained, 0x3);
+            __syncwarp();
+            mbar_wait_poll(&sh.drained, 0, a.ws, 1015);
+        }
+    } else {
+        // -------------------------------------------------------------- softmax
+        const int wg = (warp - 4) >> 2;          // 0: even tiles, 1: odd tiles
+        const int q = warp & 3;                  // TMEM lane quadrant of the warp
+        const int rr = q * 32 + lane;            // row within this CTA's 128
+        const int row = r * 128 + rr;            // row within the query tile
+        const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+        const uint32_t to = tmem + lane_off + Gm::ColO;
+        uint32_t it = 0, parts = 0;              // tiles and parts before this part
+        uint32_t landing = 0;                    // parity of v_land by stage
+        bool ok = true;
+        PagedDesc de{-1, 0, 0, 0, 0, 0, {0, 0}};
+
+        // The query rows of an item into shared memory, 16-byte chunks swizzled
+        // as TMA would (rows past the tile's last are zero).  A warp loads its
+        // 32 rows, each warpgroup half of every row; the lanes of a load lie
+        // along the rows.
+        auto load_q = [&](const PagedItem &p) {
+            if (r * 128 + q * 32 < p.rows) {
+                constexpr int CPR = D / 16, RPL = 32 / CPR;   // chunks of a half row, rows per load
+                const int frow = p.frow0 + min(row, p.rows - 1);
+                const int i = frow / a.G;
+                const int64_t off = static_cast<int64_t>(p.s0 + i) * a.q_stride +
+                                    static_cast<int64_t>(p.g * a.G + frow - i * a.G) * D;
+                const int c = wg * CPR + lane % CPR;
+                uint4 v[CPR];
+#pragma unroll
+                for (int n = 0; n < CPR; ++n) {
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, n * RPL + lane / CPR);
+                    v[n] = __ldg(reinterpret_cast<const uint4 *>(a.q + o) + c);
+                }
+#pragma unroll
+                for (int n = 0; n < CPR; ++n) {
+                    const int rw = q * 32 + n * RPL + lane / CPR;   // row within this CTA's 128
+                    if (r * 128 + rw >= p.rows) v[n] = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(smem + Gm::OffQ + rw * 128 + (c >> 3) * Gm::QAtomBytes +
+                                               (((c & 7) ^ (rw & 7)) << 4)) = v[n];
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_of(&sh.q_ready));
+        };
+
+        PagedItem p;
+        uint32_t k = 0;
+        bool more = paged_take(a, sh.ring, k, p, false, 1020);
+        if (more && p.tv1 > p.tv0) load_q(p);
+        while (more && ok) {
+            const int nt = p.tv1 - p.tv0;
+            const bool live = row < p.rows;
+            if (p.kind == kPartFirst)
+                de = PagedDesc{p.last, p.rows, p.frow0, p.s0, p.g * a.G, de.part0, {0, 0}};
+            else if (p.kind == kPartLater)
+                de.part0 = 1;
+            const int frow = p.frow0 + (live ? row : 0);
+            const int i = frow / a.G;
+            const bool busy = r * 128 + q * 32 < p.rows;   // the warp has a live row
+            float m_ref = -INFINITY, l = 0.f;    // reference of, and sum over, this group's tiles
+            const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
+            // the part's tiles whose V has a tail: the last of the pages, the
+            // last of the new tokens
+            const int nkp = (p.kv + BKV - 1) / BKV;
+            int j_kv = (p.kv & 15) ? nkp - 1 - p.tv0 : -1;
+            int j_new = a.has_new && (p.n & 15) ? nkp + (p.n - 1) / BKV - p.tv0 : -1;
+            if (j_kv >= nt) j_kv = -1;
+            if (j_new >= nt) j_new = -1;
+            for (int j = static_cast<int>((it ^ wg) & 1u); j < nt; j += 2) {
+                const uint32_t t = it + j;       // tile of the CTA; its parity is wg
+                const int valid = paged_valid<BKV>(p, p.tv0 + j);
+                const int ss = static_cast<int>(t % NS);
+                // first and last visible column
+                const int key0 = paged_key0<BKV>(p, p.tv0 + j);
+                const int c_hi = a.causal ? min(valid - 1, pos - key0) : valid - 1;
+                const int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
+                const bool masked = __any_sync(0xFFFFFFFFu, c_hi < BKV - 1 || c_lo > 0);
+                // a wait that runs out is noticed at the tile's end: what is
+                // computed until then reaches no memory but the outputs
+                ok = mbar_wait_poll(&sh.s_full[ss], (t / NS) & 1u, a.ws, 1022);
+                tc_fence_after();
+                const uint32_t ts = tmem + lane_off + Gm::ColS + ss * BKV;
+                if (busy) {
+                    uint32_t sr[BKV];
+#pragma unroll
+                    for (int c0 = 0; c0 < BKV; c0 += 32)
+                        tmem_ld32_nowait(ts + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
+                    tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < BKV; ++c)
+                            if (c > c_hi || c < c_lo) sr[c] = __float_as_uint(-INFINITY);
+                    }
+                    // the scale is positive, so the scaled maximum is the maximum scaled
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < BKV; c += 8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = max3(mx[e], __uint_as_float(sr[c + 2 * e]),
+                                         __uint_as_float(sr[c + 2 * e + 1]));
+                    }
+                    const float tmax = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
+                    // the reference moves when a tile exceeds it by 2^8
+                    float m_in = -INFINITY;
+                    if (j > 0) {
+                        ok &= mbar_wait_poll(&sh.m_full[wg ^ 1][q], ((t - 1) >> 1) & 1u, a.ws, 1023);
+                        m_in = sh.m[wg ^ 1][rr];
+                    }
+                    const float m_new = m_in == -INFINITY || tmax > m_in + 8.f ? tmax : m_in;
+                    sh.m[wg][rr] = m_new;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.m_full[wg][q]);
+                    if (__any_sync(0xFFFFFFFFu, m_new != m_ref)) {
+                        // a part's first tiles, and few others
+                        if (m_ref != m_new && m_ref != -INFINITY) l *= fast_exp2(m_ref - m_new);
+                        const bool moved = m_new != m_in && m_in != -INFINITY;
+                        m_ref = m_new;
+                        if (__any_sync(0xFFFFFFFFu, moved)) {
+                            // O holds the PVs up to the tile before: wait for that one
+                            const float factor = moved ? fast_exp2(m_in - m_new) : 1.f;
+                            ok &= mbar_wait_poll(&sh.pv_done[wg ^ 1], ((t - 1) >> 1) & 1u, a.ws, 1024);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_issue(to + c0, o);
+                                tmem_wait_ld16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+                                tmem_st16(to + c0, o);
+                            }
+                        }
+                    }
+                    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+                    const float mexp = (m_ref == -INFINITY) ? 0.f : m_ref;
+                    const float2 nm2 = make_float2(-mexp, -mexp);
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c0 = 0; c0 < BKV; c0 += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 d2 = fma2(make_float2(__uint_as_float(sr[c0 + c]),
+                                                               __uint_as_float(sr[c0 + c + 1])),
+                                                   sc2, nm2);
+                            const float2 p2 = make_float2(fast_exp2(d2.x), fast_exp2(d2.y));
+                            acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], p2);
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p2.x, p2.y);
+                            pk[c >> 1] = *reinterpret_cast<const uint32_t *>(&h2);
+                        }
+                        tmem_st16(ts + c0 / 2, pk);
+                    }
+                    l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                    tmem_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(&sh.m_full[wg][q]);      // its phases count the tiles
+                }
+                if (valid & 15) {
+                    const int vs = static_cast<int>(t % NV);
+                    // (the same stage may have landed so earlier in the part)
+                    const bool again = j == j_new && j_kv >= 0 && j_kv < j &&
+                                       static_cast<int>((it + j_kv) % NV) == vs;
+                    ok &= mbar_wait_poll(&sh.v_land[vs], (landing >> vs & 1u) ^ (again ? 1u : 0u), a.ws,
+                                         1025);
+                    paged_zero_tail<Gm>(smem + Gm::OffV + vs * Gm::VBytes, valid, threadIdx.x & 127);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(lead_of(&sh.p_full[ss]));
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(lead_of(&sh.p_full[ss]));
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+            }
+            if (!ok) break;
+            if (j_kv >= 0) landing ^= 1u << ((it + j_kv) % NV);
+            if (j_new >= 0) landing ^= 1u << ((it + j_new) % NV);
+            // ---------------------------------------------------------- next query, epilogue
+            const PagedItem done = p;
+            if (nt > 0) {
+                // every S of this part is done: its last tile's arrived
+                const uint32_t t = it + nt - 1;
+                ok = mbar_wait_poll(&sh.s_full[t % NS], (t / NS) & 1u, a.ws, 1026);
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                it += nt;
+            }
+            more = paged_take(a, sh.ring, ++k, p, false, 1020);
+            if (more && p.tv1 > p.tv0) load_q(p);
+            const int slot = 2 * unit + (done.kind == kPartFirst ? 1 : 0);
+            const int head = done.g * a.G + frow - i * a.G;
+            uint16_t *row_out = a.out + static_cast<int64_t>(done.s0 + i) * a.out_stride +
+                                static_cast<int64_t>(head) * D;
+            constexpr int Half = D / 2;          // dims each warpgroup stores
+            if (nt == 0) {                       // no key to see: a zero row
+                if (live) {
+#pragma unroll 1
+                    for (int c = 0; c < Half / 8; ++c)
+                        reinterpret_cast<uint4 *>(row_out + wg * Half)[c] = make_uint4(0, 0, 0, 0);
+                }
+                continue;
+            }
+            ok = mbar_wait_poll(&sh.o_full, parts & 1u, a.ws, 1027);
+            if (busy && ok) {
+                // this group's sum in the reference of the last tile, which
+                // the other group may have set; then both groups' together.
+                // (Its slot has been read: O is whole only after every warp
+                // was through with the part before.)
+                const uint32_t t = it - 1;
+                const int last = static_cast<int>(t & 1u);
+                float m_last = m_ref;
+                if (last != wg) {
+                    ok = mbar_wait_poll(&sh.m_full[last][q], (t >> 1) & 1u, a.ws, 1028);
+                    m_last = sh.m[last][rr];
+                }
+                if (l != 0.f && m_ref != m_last) l *= fast_exp2(m_ref - m_last);
+                m_ref = m_last;
+                sh.l[wg][rr] = l;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.l_full[wg][q]);
+            ok = ok && mbar_wait_poll(&sh.l_full[wg ^ 1][q], parts & 1u, a.ws, 1029);
+            if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+            ++parts;
+            tc_fence_after();
+            l += sh.l[wg ^ 1][rr];
+            if (done.kind != kPartWhole && live && wg == 0)
+                a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + row] = make_float2(m_ref, l);
+            const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
+            bool badv = a.checks && live && !isfinite(l);
+            if (busy)
+                badv |= !paged_store_row<Half>(a, to, wg * Half, live, done.kind == kPartWhole, row_out,
+                                               inv_l, slot, row);
+            if (badv) report_error(a.ws, DG_ERR_DEVICE, 1030);
+            tc_fence_before();   // O is read before the next part's first PV
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(lead_of(&sh.o_free));
+        }
+        if (r == 0 && threadIdx.x == 128) a.desc[unit] = de;
+    }
+    tc_fence_before();
+    __syncthreads();
+    // no CTA releases its TMEM or leaves while the pair's UMMAs, copies,
+    // commits or remote arrivals may still reach it
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPagedPairThreads, 1)
+    paged_attn_pair_kernel_d128(const __grid_constant__ CUtensorMap map_k,
+                                const __grid_constant__ CUtensorMap map_v,
+                                const __grid_constant__ CUtensorMap map_kn,
+                                const __grid_constant__ CUtensorMap map_vn, PagedArgs a)
+{
+    paged_pair_body<128>(&map_k, &map_v, &map_kn, &map_vn, a);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPagedPairThreads, 1)
+    paged_attn_pair_kernel_d256(const __grid_constant__ CUtensorMap map_k,
+                                const __grid_constant__ CUtensorMap map_v,
+                                const __grid_constant__ CUtensorMap map_kn,
+                                const __grid_constant__ CUtensorMap map_vn, PagedArgs a)
+{
+    paged_pair_body<256>(&map_k, &map_v, &map_kn, &map_vn, a);
+}
+
+}  // namespace dg

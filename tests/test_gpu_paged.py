@@ -204,12 +204,18 @@ def check_attn(n, kv, Hq, Hkv, D, page, causal, window, fresh, pad=0, strided=Fa
     return b, out
 
 
+@pytest.fixture(params=["single", "pair"])
+def kernel(request, monkeypatch):
+    """Query tiles of 128 rows on one CTA, or of 256 on two."""
+    monkeypatch.setenv("DG_PAGED_KERNEL", request.param)
+
+
 MASKS = [(False, 0, False), (False, 0, True), (True, 0, False), (True, 0, True), (True, 5, False), (True, 130, True)]
 
 
 @pytest.mark.parametrize("causal,window,fresh", MASKS)
 @pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 128), (6, 2, 256), (5, 1, 128), (4, 4, 256)])
-def test_attention_small_and_ragged(Hq, Hkv, D, causal, window, fresh):
+def test_attention_small_and_ragged(kernel, Hq, Hkv, D, causal, window, fresh):
     """Lengths around tiles, pages and nothing: empty sequences, empty caches, one token, tails of a tile."""
     n = [1, 0, 7, 33, 1, 2, 1]
     kv = [1, 9, 0, 40, 129, 64, 0]
@@ -222,7 +228,7 @@ def test_attention_small_and_ragged(Hq, Hkv, D, causal, window, fresh):
 @pytest.mark.parametrize("causal,window,fresh", MASKS)
 @pytest.mark.parametrize("page", [16, 64, 256])
 @pytest.mark.parametrize("D", [128, 256])
-def test_attention_cut_between_ctas(D, page, causal, window, fresh):
+def test_attention_cut_between_ctas(kernel, D, page, causal, window, fresh):
     """Long caches and several query tiles: items cut between CTAs and merged."""
     n, kv = [70, 1, 130], [900, 2500, 333]
     if not fresh:
@@ -241,20 +247,20 @@ def test_attention_one_long_sequence(D, Hkv):
     check_attn([1], [20000], 2 * Hkv, Hkv, D, 64, True, 0, False, seed=5)
 
 
-def test_rows_that_see_nothing_are_zero():
+def test_rows_that_see_nothing_are_zero(kernel):
     """Causal, with more new tokens than cached keys (their keys were not all appended): the first rows see none."""
     b, out = check_attn([12, 3], [5, 0], 4, 2, 128, 16, True, 0, False, seed=6)
     assert (out[:7] == 0).all() and (out[12:] == 0).all()
 
 
-def test_many_sequences():
+def test_many_sequences(kernel):
     g = torch.Generator().manual_seed(8)
     n = torch.randint(0, 4, (531,), generator=g).tolist()
     kv = [int(x) + m for x, m in zip(torch.randint(0, 90, (531,), generator=g), n)]
     check_attn(n, kv, 2, 1, 128, 16, True, 0, False, seed=8)
 
 
-def test_scores_far_apart():
+def test_scores_far_apart(kernel):
     """Scores from -1000 to 1000 in an order that moves the reference maximum late, and large negative ones only."""
     b = Batch([40], [600], [600], 2, 1, 128, 64, seed=10)
     ramp = torch.linspace(-1, 1, 640)
@@ -290,7 +296,7 @@ def test_results_do_not_depend_on_pages_or_repeats():
         assert same_bits(o, outs[0])
 
 
-def test_attention_reports_bad_pages_and_lengths():
+def test_attention_reports_bad_pages_and_lengths(kernel):
     b = Batch([2, 2], [40, 20], [40, 20], 2, 1, 128, 16, seed=12)
     c = b.cache()
     ws = dg.workspace(dg.paged_attn_workspace(b.T, 2, c), DEV)

@@ -35,17 +35,20 @@ int check(const PagedArgs &a, int units)
         base[b + 1] = base[b] + a.Hkv * paged_prefix(s, s.mt);
     }
     const int64_t W = base[a.B];
-    const int n = paged_units(a, W, units);
+    if (W == 0) return 0;
+    const int64_t step = paged_step(a, W, units);
+    const int n = static_cast<int>((W + step - 1) / step);
+    if (n > units) FAIL("%d units of %d", n, units);
     // per item: the tiles so far, the unit promised the last part
     std::map<std::tuple<int, int, int>, std::pair<int, int>> items;
-    for (int u = 0; u < n && W > 0; ++u) {
+    for (int u = 0; u < n; ++u) {
         PagedRange r{};
-        r.W = W;
-        r.n = n;
-        r.begin = paged_bound(W, n, u);
-        r.end = paged_bound(W, n, u + 1);
-        while (base[r.b + 1] <= r.begin) ++r.b;
-        r.base = base[r.b];
+        r.begin = u * step;
+        r.end = r.begin + step < W ? r.begin + step : W;
+        r.step = step;
+        int b = 0;
+        while (base[b + 1] <= r.begin) ++b;
+        paged_locate<ROWS, BKV>(a, paged_seq<ROWS, BKV>(a, b), b, base[b], r.begin, r);
         PagedWalk<ROWS, BKV> walk;
         walk.start(a, r);
         PagedPart p;
