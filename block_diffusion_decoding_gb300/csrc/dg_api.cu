@@ -116,6 +116,13 @@ int current_device_info(DeviceInfo **out)
         DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_pair_kernel_d256,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          paged_pair_smem_bytes(256)));
+        // its warps share the launch's registers out anew: fewer than they were
+        // counted on would be waited for forever
+        for (auto kern : {paged_attn_pair_kernel_d128, paged_attn_pair_kernel_d256}) {
+            cudaFuncAttributes fa;
+            DG_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+            if (fa.numRegs < kPagedPairRegs) return DG_ERR_CUDA;
+        }
         di.attrs_set = true;
     }
     *out = &di;

@@ -471,6 +471,22 @@ DG_DEVICE void umma_commit_pair(uint64_t *bar, uint16_t cta_mask)
 }
 
 // ------------------------------------------------------------------------
+// Registers per thread of a warpgroup (4 warps, all of which execute it):
+// raised from, or given back to, those the block was launched with.
+// ------------------------------------------------------------------------
+template <int N>
+DG_DEVICE void reg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+DG_DEVICE void reg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ------------------------------------------------------------------------
 // Paired fp32 arithmetic (two lanes of a 64-bit register pair per
 // instruction) and a three-input maximum.
 // ------------------------------------------------------------------------

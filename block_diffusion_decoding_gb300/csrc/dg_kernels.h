@@ -330,6 +330,7 @@ int paged_attn_smem_bytes(int D);
 // Chunks: query tiles of 256 rows on 2-CTA clusters (dg_paged_pair.cu)
 constexpr int kPagedPairThreads = 384;
 constexpr int kPagedPairRows = 256;
+constexpr int kPagedPairRegs = 168;   // registers a thread it is launched with
 __global__ void paged_attn_pair_kernel_d128(const __grid_constant__ CUtensorMap map_k,
                                             const __grid_constant__ CUtensorMap map_v,
                                             const __grid_constant__ CUtensorMap map_kn,

@@ -71,6 +71,12 @@ struct PairShared {
 static_assert(PairGeom<128>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
 static_assert(PairGeom<256>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
 
+// Of the registers that the launch has: kPagedPairRegs a thread, which the host
+// makes sure of before it launches.
+constexpr int kPairOtherRegs = 88, kPairSoftmaxRegs = 208;
+static_assert(128 * kPairOtherRegs + 256 * kPairSoftmaxRegs <= kPagedPairThreads * kPagedPairRegs,
+              "registers");
+
 int paged_pair_smem_bytes(int D)
 {
     return static_cast<int>((D == 128 ? PairGeom<128>::OffShared : PairGeom<256>::OffShared) +
@@ -249,108 +255,114 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
     const uint32_t tmem = sh.tmem;
     auto lead_of = [&](const uint64_t *bar) -> uint32_t { return mapa_shared(smem_u32(bar), 0); };
 
-    if (warp == 0) {
-        pair_producer<Gm, false>(smem + Gm::OffK, sh, lead_of(sh.k_full), r, map_k, map_kn, a, 1001);
-    } else if (warp == 2) {
-        pair_producer<Gm, true>(smem + Gm::OffV, sh, lead_of(sh.v_full), r, map_v, map_vn, a, 1004);
-    } else if (warp == 3) {
-        paged_walk<Gm>(a, sh.scan.r, sh.ring, 1007);
-    } else if (warp == 1) {
-        // -------------------------------------------------------------- MMA
-        // (the whole warp of the even CTA, see elect_lane)
-        if (r == 0) {
-            const uint32_t idesc_s = make_idesc_bf16(256, BKV, 0);
-            const uint32_t idesc_o = make_idesc_bf16(256, D, 1);
-            // descriptors of the buffers' first tiles; the address sits in
-            // the low bits in units of 16 bytes
-            const uint64_t dq = make_sdesc_sw128(smem_u32(smem + Gm::OffQ), 16, 1024);
-            const uint64_t dk0 = make_sdesc_sw128(smem_u32(smem + Gm::OffK), 16, 1024);
-            const uint64_t dv0 = make_sdesc_sw128(smem_u32(smem + Gm::OffV), Gm::KVAtomBytes, 1024);
-            int ks = 0, vs = 0, ss = 0, ps = 0;      // stages of K, V, S (written), S (read as P)
-            uint32_t kpar = 0, vpar = 0, ppar = 0;
-            uint32_t pv = 0, parts = 0;              // tiles multiplied with V, parts
-            bool ok = true;
-            const bool lead = elect_lane();
-            PagedItem p;
-            for (uint32_t k = 0; ok && paged_take(a, sh.ring, k, p, false, 1010); ++k) {
-                const int nt = p.tv1 - p.tv0;
-                if (nt == 0) continue;
-                ok = mbar_wait_poll<true>(&sh.q_ready, parts & 1u, a.ws, 1011);
-                ++parts;
-                const int steps_kv = paged_steps(p.kv, BKV), steps_new = paged_steps(p.n, BKV);
-                const int j_kv = (p.kv + BKV - 1) / BKV - 1 - p.tv0;   // last tile of the pages
-                const int j_new = j_kv + (p.n + BKV - 1) / BKV;        // of the new tokens
-                for (int j = 0; j < nt + NS - 1 && ok; ++j) {
-                    if (j < nt) {
-                        ok = mbar_wait_poll(&sh.k_full[ks], kpar, a.ws, 1012);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t dk = dk0 + ks * (Gm::KBytes >> 4);
-                        const uint32_t d = tmem + Gm::ColS + ss * BKV;
-                        if (lead) {
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                umma_bf16_pair(
-                                    d, dq + (((kk >> 2) * Gm::QAtomBytes + (kk & 3) * 32) >> 4),
-                                    dk + (((kk >> 2) * Gm::KAtomBytes + (kk & 3) * 32) >> 4), idesc_s,
-                                    kk != 0);
-                            umma_commit_pair(&sh.s_full[ss], 0x3);
-                            umma_commit_pair(&sh.k_empty[ks], 0x3);
-                        }
-                        if (++ss == NS) ss = 0;
-                        if (++ks == NK) {
-                            ks = 0;
-                            kpar ^= 1u;
-                        }
-                    }
-                    const int jp = j - (NS - 1);
-                    if (jp >= 0) {
-                        // both CTAs' softmax warps have written P
-                        // (and read the O of the part before this one)
-                        ok = mbar_wait_poll(&sh.v_full[vs], vpar, a.ws, 1014) &&
-                             mbar_wait_poll<true>(&sh.p_full[ps], ppar, a.ws, 1013) &&
-                             (jp > 0 || parts < 2 ||
-                              mbar_wait_poll<true>(&sh.o_free, parts & 1u, a.ws, 1016));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const int steps = jp == j_kv ? steps_kv : jp == j_new ? steps_new : BKV / 16;
-                        const uint64_t dv = dv0 + vs * (Gm::VBytes >> 4);
-                        const uint32_t pa = tmem + Gm::ColS + ps * BKV;
-                        if (lead) {
-                            umma_bf16_pair_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
-                            if (steps == BKV / 16) {
-#pragma unroll
-                                for (int kk = 1; kk < BKV / 16; ++kk)
-                                    umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
-                                                      idesc_o, 1);
-                            } else {
-                                for (int kk = 1; kk < steps; ++kk)
-                                    umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
-                                                      idesc_o, 1);
+    // A softmax thread holds 128 scores: its warps take registers from the
+    // other four.
+    if (warp < 4) {
+        reg_dec<kPairOtherRegs>();
+        if (warp == 0) {
+            pair_producer<Gm, false>(smem + Gm::OffK, sh, lead_of(sh.k_full), r, map_k, map_kn, a, 1001);
+        } else if (warp == 2) {
+            pair_producer<Gm, true>(smem + Gm::OffV, sh, lead_of(sh.v_full), r, map_v, map_vn, a, 1004);
+        } else if (warp == 3) {
+            paged_walk<Gm>(a, sh.scan.r, sh.ring, 1007);
+        } else if (warp == 1) {
+            // -------------------------------------------------------------- MMA
+            // (the whole warp of the even CTA, see elect_lane)
+            if (r == 0) {
+                const uint32_t idesc_s = make_idesc_bf16(256, BKV, 0);
+                const uint32_t idesc_o = make_idesc_bf16(256, D, 1);
+                // descriptors of the buffers' first tiles; the address sits in
+                // the low bits in units of 16 bytes
+                const uint64_t dq = make_sdesc_sw128(smem_u32(smem + Gm::OffQ), 16, 1024);
+                const uint64_t dk0 = make_sdesc_sw128(smem_u32(smem + Gm::OffK), 16, 1024);
+                const uint64_t dv0 = make_sdesc_sw128(smem_u32(smem + Gm::OffV), Gm::KVAtomBytes, 1024);
+                int ks = 0, vs = 0, ss = 0, ps = 0;      // stages of K, V, S (written), S (read as P)
+                uint32_t kpar = 0, vpar = 0, ppar = 0;
+                uint32_t pv = 0, parts = 0;              // tiles multiplied with V, parts
+                bool ok = true;
+                const bool lead = elect_lane();
+                PagedItem p;
+                for (uint32_t k = 0; ok && paged_take(a, sh.ring, k, p, false, 1010); ++k) {
+                    const int nt = p.tv1 - p.tv0;
+                    if (nt == 0) continue;
+                    ok = mbar_wait_poll<true>(&sh.q_ready, parts & 1u, a.ws, 1011);
+                    ++parts;
+                    const int steps_kv = paged_steps(p.kv, BKV), steps_new = paged_steps(p.n, BKV);
+                    const int j_kv = (p.kv + BKV - 1) / BKV - 1 - p.tv0;   // last tile of the pages
+                    const int j_new = j_kv + (p.n + BKV - 1) / BKV;        // of the new tokens
+                    for (int j = 0; j < nt + NS - 1 && ok; ++j) {
+                        if (j < nt) {
+                            ok = mbar_wait_poll(&sh.k_full[ks], kpar, a.ws, 1012);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t dk = dk0 + ks * (Gm::KBytes >> 4);
+                            const uint32_t d = tmem + Gm::ColS + ss * BKV;
+                            if (lead) {
+    #pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk)
+                                    umma_bf16_pair(
+                                        d, dq + (((kk >> 2) * Gm::QAtomBytes + (kk & 3) * 32) >> 4),
+                                        dk + (((kk >> 2) * Gm::KAtomBytes + (kk & 3) * 32) >> 4), idesc_s,
+                                        kk != 0);
+                                umma_commit_pair(&sh.s_full[ss], 0x3);
+                                umma_commit_pair(&sh.k_empty[ks], 0x3);
                             }
-                            umma_commit_pair(&sh.v_empty[vs], 0x3);
-                            umma_commit_pair(&sh.pv_done[pv & 1], 0x3);
-                            if (jp + 1 == nt) umma_commit_pair(&sh.o_full, 0x3);
+                            if (++ss == NS) ss = 0;
+                            if (++ks == NK) {
+                                ks = 0;
+                                kpar ^= 1u;
+                            }
                         }
-                        ++pv;
-                        if (++ps == NS) {
-                            ps = 0;
-                            ppar ^= 1u;
-                        }
-                        if (++vs == NV) {
-                            vs = 0;
-                            vpar ^= 1u;
+                        const int jp = j - (NS - 1);
+                        if (jp >= 0) {
+                            // both CTAs' softmax warps have written P
+                            // (and read the O of the part before this one)
+                            ok = mbar_wait_poll(&sh.v_full[vs], vpar, a.ws, 1014) &&
+                                 mbar_wait_poll<true>(&sh.p_full[ps], ppar, a.ws, 1013) &&
+                                 (jp > 0 || parts < 2 ||
+                                  mbar_wait_poll<true>(&sh.o_free, parts & 1u, a.ws, 1016));
+                            if (!ok) break;
+                            tc_fence_after();
+                            const int steps = jp == j_kv ? steps_kv : jp == j_new ? steps_new : BKV / 16;
+                            const uint64_t dv = dv0 + vs * (Gm::VBytes >> 4);
+                            const uint32_t pa = tmem + Gm::ColS + ps * BKV;
+                            if (lead) {
+                                umma_bf16_pair_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
+                                if (steps == BKV / 16) {
+    #pragma unroll
+                                    for (int kk = 1; kk < BKV / 16; ++kk)
+                                        umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
+                                                          idesc_o, 1);
+                                } else {
+                                    for (int kk = 1; kk < steps; ++kk)
+                                        umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
+                                                          idesc_o, 1);
+                                }
+                                umma_commit_pair(&sh.v_empty[vs], 0x3);
+                                umma_commit_pair(&sh.pv_done[pv & 1], 0x3);
+                                if (jp + 1 == nt) umma_commit_pair(&sh.o_full, 0x3);
+                            }
+                            ++pv;
+                            if (++ps == NS) {
+                                ps = 0;
+                                ppar ^= 1u;
+                            }
+                            if (++vs == NV) {
+                                vs = 0;
+                                vpar ^= 1u;
+                            }
                         }
                     }
+                    ok = __all_sync(0xFFFFFFFFu, ok);
                 }
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                // every UMMA and commit is done before the cluster leaves
+                if (lead) umma_commit_pair(&sh.drained, 0x3);
+                __syncwarp();
+                mbar_wait_poll(&sh.drained, 0, a.ws, 1015);
             }
-            // every UMMA and commit is done before the cluster leaves
-            if (lead) umma_commit_pair(&sh.drained, 0x3);
-            __syncwarp();
-            mbar_wait_poll(&sh.drained, 0, a.ws, 1015);
         }
     } else {
+        reg_inc<kPairSoftmaxRegs>();
         // -------------------------------------------------------------- softmax
         const int wg = (warp - 4) >> 2;          // 0: even tiles, 1: odd tiles
         const int q = warp & 3;                  // TMEM lane quadrant of the warp
