@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "dg_kernels.h"
+#include "dg_paged.cuh"
 #include "dg_plan.h"
 
 using namespace dg;
@@ -22,6 +23,7 @@ namespace {
 
 // ---------------------------------------------------------------- small utilities
 constexpr int kAssumedMaxSMs = 256;  // workspace queries do not touch the GPU
+static_assert(kAssumedMaxSMs <= kMergeThreads, "paged merge: a thread per unit");
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -908,7 +910,7 @@ int check_paged_cache(const dg_paged_cache *c, int64_t *page_stride)
         return DG_ERR_INVALID_ARG;
     if (c->D != 128 && c->D != 256) return DG_ERR_UNSUPPORTED;
     if (c->page_size % 16 != 0 || c->page_size > 2048) return DG_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(c->max_pages) * c->page_size > (1LL << 30)) return DG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c->max_pages) * c->page_size > (1LL << 29)) return DG_ERR_UNSUPPORTED;
     if (c->Hkv > 1024 || c->n_pages > (1 << 30)) return DG_ERR_UNSUPPORTED;
     *page_stride = c->page_stride;
     const int rc = check_stride(*page_stride, static_cast<int64_t>(c->page_size) * c->Hkv * c->D);
@@ -1205,7 +1207,8 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     if (window > 0 && !causal) return DG_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
     if (Hq % c->Hkv != 0 || Hq / c->Hkv > 128) return DG_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(T) * Hq > (1LL << 30)) return DG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(T) * Hq > (1LL << 29)) return DG_ERR_UNSUPPORTED;
+    window = std::min(window, 1 << 30);   // no sequence has as many keys
     if (T > 0 && (!q || !out || (k_new != nullptr) != (v_new != nullptr))) return DG_ERR_INVALID_ARG;
     const int64_t dq = static_cast<int64_t>(Hq) * c->D, dk = static_cast<int64_t>(c->Hkv) * c->D;
     if ((rc = check_stride(q_stride, dq)) != DG_OK || (rc = check_stride(out_stride, dq)) != DG_OK)
@@ -1276,6 +1279,7 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     a.has_new = k_new != nullptr ? 1 : 0;
     a.causal = causal;
     a.window = window;
+    a.small = paged_small(T, c->B, c->Hkv, a.G, static_cast<int64_t>(c->max_pages) * c->page_size) ? 1 : 0;
     a.checks = g_checks.load(std::memory_order_relaxed);
     a.scale_log2 = scale * 1.44269502162933349609375f;
     a.slot_rows = paged_slot_rows(T, a.G);
@@ -1298,9 +1302,9 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
                                   dim3(units), dim3(kPagedThreads), paged_attn_smem_bytes(D), st,
                                   pdl, mk, mv, mkn, mvn, a));
     DG_LAUNCHED();
-    const int merge_y = (a.slot_rows * (D / 16) + kMergeThreads - 1) / kMergeThreads;
-    DG_CUDA_TRY(launch_kernel(paged_merge_kernel, dim3(units, merge_y), dim3(kMergeThreads), 0, st,
-                              pdl, a));
+    const int jobs = (a.slot_rows * (D / 16) + kMergeThreads - 1) / kMergeThreads;   // of an item
+    DG_CUDA_TRY(launch_kernel(paged_merge_kernel, dim3(std::min(2 * di->sms, units * jobs)),
+                              dim3(kMergeThreads), 0, st, pdl, a, units));
     DG_LAUNCHED();
     return DG_OK;
 }

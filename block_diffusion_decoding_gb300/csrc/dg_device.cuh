@@ -176,8 +176,10 @@ DG_DEVICE bool mbar_wait(uint64_t *bar, uint32_t parity, WsHeader *ws, int where
 
 // The same wait with the clock read only once it has lasted: a wait that a few
 // polls satisfy, as most in a running pipeline are, pays for those alone.
-// CLUSTER: acquires what the other CTA of a pair released.
-template <bool CLUSTER = false>
+// CLUSTER: acquires what the other CTA of a pair released.  SLEEP: nanoseconds
+// between polls, for roles with time to spare whose polls would take issue
+// slots from the others of their SM.
+template <bool CLUSTER = false, int SLEEP = 0>
 DG_DEVICE bool mbar_wait_poll(uint64_t *bar, uint32_t parity, WsHeader *ws, int where,
                               uint64_t limit_ns = kWaitLimitNs)
 {
@@ -195,6 +197,7 @@ DG_DEVICE bool mbar_wait_poll(uint64_t *bar, uint32_t parity, WsHeader *ws, int 
         else
             ok = mbar_try_wait(bar, parity) ? 1u : 0u;
         if (ok) return true;
+        if (SLEEP > 0) __nanosleep(SLEEP);
         if ((it & 63u) == 0) {
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
@@ -523,6 +526,12 @@ DG_DEVICE float max3(float a, float b, float c)
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// __syncthreads() that the warps of a block may reach in different places.
+DG_DEVICE void cta_sync()
+{
+    asm volatile("bar.sync 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------

@@ -306,6 +306,7 @@ struct PagedArgs {
     int page_size, box_rows, n_pages, max_pages;
     const int32_t *page_table, *kv_len, *q_start;
     int has_new, causal, window;
+    int small;           // the division of the work fits 32-bit integers
     int checks;
     float scale_log2;
     int out_wide;        // output rows are 32-byte aligned
@@ -324,8 +325,9 @@ __global__ void paged_attn_kernel_d256(const __grid_constant__ CUtensorMap map_k
                                        const __grid_constant__ CUtensorMap map_v,
                                        const __grid_constant__ CUtensorMap map_kn,
                                        const __grid_constant__ CUtensorMap map_vn, PagedArgs a);
-constexpr int kMergeThreads = 256;
-__global__ void paged_merge_kernel(PagedArgs a);
+constexpr int kMergeThreads = 256;   // at least as many as there are units
+constexpr int kMergeParts = 2;       // parts whose loads a thread has in flight
+__global__ void paged_merge_kernel(PagedArgs a, int units);
 int paged_attn_smem_bytes(int D);
 // Chunks: query tiles of 256 rows on 2-CTA clusters (dg_paged_pair.cu)
 constexpr int kPagedPairThreads = 384;

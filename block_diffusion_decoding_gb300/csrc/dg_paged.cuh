@@ -1,7 +1,7 @@
 // dg_paged.cuh -- how the paged attention kernels divide their work.
 //
 // The lengths of the sequences are device data, so the division is made on
-// the device, by every CTA for itself, from the lengths alone.  An item is
+// the device, by one warp of every CTA for itself, from the lengths alone.  An item is
 // one query tile (ROWS folded rows = positions x heads of one kv head) of one
 // kv head of one sequence; it costs a fixed part plus its visible keys.  The
 // items in the order (sequence, kv head, query tile) lie end to end on a line
@@ -42,19 +42,23 @@ DG_BOTH T paged_max(T a, T b)
 constexpr int kPagedItemKeys = 256;    // an item's fixed cost, in keys
 constexpr int kPagedMinKeys = 512;     // least cost of a CTA's stretch, in keys
 
+// I: the integers the line is measured in, 32-bit where the host has seen that
+// no line of these tensors is longer (PagedArgs::small): the walk is on the
+// path to every CTA's first load.
+template <class I>
 struct PagedSeq {
     int s0, n, kv;      // first token, tokens, cached keys
     int mt;             // query tiles of a kv head
     int mc;             // tiles whose key count still grows with the tile index
-    int64_t x0, slope, cap, fixed;
+    I x0, slope, cap, fixed;
 };
 
 // Bounds every length by what the tensors hold, so that no later index can
 // leave them; *bad is set when something had to be cut.
-template <int ROWS, int BKV>
-DG_BOTH PagedSeq paged_seq(const PagedArgs &a, int b, bool *bad = nullptr)
+template <int ROWS, int BKV, class I>
+DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool *bad = nullptr)
 {
-    PagedSeq s;
+    PagedSeq<I> s;
     const int r0 = paged_load(a.q_start + b), r1 = paged_load(a.q_start + b + 1);
     const int k0 = paged_load(a.kv_len + b);
     s.s0 = paged_min(paged_max(r0, 0), a.T);
@@ -62,64 +66,72 @@ DG_BOTH PagedSeq paged_seq(const PagedArgs &a, int b, bool *bad = nullptr)
     s.kv = paged_min(paged_max(k0, 0), a.max_pages * a.page_size);
     if (bad != nullptr) *bad = r0 != s.s0 || r1 != s.s0 + s.n || k0 != s.kv;
     s.mt = (s.n * a.G + ROWS - 1) / ROWS;
-    const int64_t G = a.G;
+    const I G = a.G;
     s.fixed = G * kPagedItemKeys + 1;
-    s.cap = INT64_MAX / 4;
+    s.cap = 0;
+    s.mc = s.mt;
     if (!a.causal) {
         s.slope = 0;
-        s.x0 = G * (static_cast<int64_t>(s.kv) + (a.has_new ? s.n : 0));
-        s.mc = s.mt;
+        s.x0 = G * (s.kv + (a.has_new ? s.n : 0));
     } else {
         s.slope = ROWS;
         s.x0 = G * paged_max(0, a.has_new ? s.kv : s.kv - s.n);
-        s.mc = s.mt;
         if (a.window > 0) {
-            s.cap = G * (static_cast<int64_t>(a.window) + BKV) + ROWS;
-            const int64_t k = s.cap < s.x0 ? 0 : (s.cap - s.x0) / ROWS;
-            s.mc = static_cast<int>(paged_min(k, static_cast<int64_t>(s.mt)));
+            s.cap = G * (paged_min(a.window, s.kv + s.n) + BKV) + ROWS;
+            const I k = s.cap < s.x0 ? 0 : (s.cap - s.x0) / ROWS;
+            s.mc = static_cast<int>(paged_min<I>(k, s.mt));
         }
     }
     return s;
 }
 
 // Cost of the first m query tiles of one kv head.
-DG_BOTH int64_t paged_prefix(const PagedSeq &s, int m)
+template <class I>
+DG_BOTH I paged_prefix(const PagedSeq<I> &s, int m)
 {
-    const int64_t k = paged_min(m, s.mc);
+    const I k = paged_min(m, s.mc);
     return m * s.fixed + k * s.x0 + s.slope * (k * (k + 1) / 2) + (m - k) * s.cap;
 }
 
-// Both non-negative; nearly every quotient here is one of 32-bit numbers.
-DG_BOTH int64_t paged_div(int64_t x, int64_t y)
+// No negative operands.
+template <class I>
+DG_BOTH I paged_div(I x, I y)
 {
-    if (((x | y) >> 32) == 0)
-        return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return x / y;
+    return sizeof(I) == 4 ? static_cast<I>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
+
+// Host: whether every line of these tensors can be measured in 32 bits.
+inline bool paged_small(int T, int B, int Hkv, int G, int64_t max_kv)
+{
+    const int64_t items = static_cast<int64_t>(Hkv) * (static_cast<int64_t>(T) * G / 128 + B);
+    const int64_t cost = G * (max_kv + 2 * static_cast<int64_t>(T) + kPagedItemKeys + 256) + 1024;
+    return cost < (1 << 30) && items < (1 << 30) / cost;
 }
 
 // The length of a unit's stretch (a unit: a CTA, or a pair of them) of a line
 // of cost W.
-DG_BOTH int64_t paged_step(const PagedArgs &a, int64_t W, int units)
+template <class I>
+DG_BOTH I paged_step(const PagedArgs &a, I W, int units)
 {
-    const int64_t least = static_cast<int64_t>(a.G) * kPagedMinKeys;
-    const int64_t n = paged_min<int64_t>(units, paged_max<int64_t>(paged_div(W, least), 1));
-    return paged_div(W + n - 1, n);
+    const I least = static_cast<I>(a.G) * kPagedMinKeys;
+    const I n = paged_min<I>(units, paged_max<I>(paged_div(W, least), 1));
+    return paged_div<I>(W + n - 1, n);
 }
 
+template <class I>
 struct PagedRange {
-    int64_t begin, end;      // this unit's stretch (end <= begin: none)
-    int64_t step;
-    int64_t item;            // where the item that `begin` falls in begins
+    I begin, end;            // this unit's stretch (end <= begin: none)
+    I step;
+    I item;                  // where the item that `begin` falls in begins
     int b, g, m;             // that item
 };
 
 // The item of sequence b (which begins at `base`) that position x falls in.
-template <int ROWS, int BKV>
-DG_BOTH void paged_locate(const PagedArgs &a, const PagedSeq &s, int b, int64_t base, int64_t x,
-                          PagedRange &r)
+template <class I>
+DG_BOTH void paged_locate(const PagedSeq<I> &s, int b, I base, I x, PagedRange<I> &r)
 {
-    const int64_t head = paged_prefix(s, s.mt);
-    int64_t y = x - base;
+    const I head = paged_prefix(s, s.mt);
+    I y = x - base;
     r.b = b;
     r.g = static_cast<int>(paged_div(y, head));
     y -= r.g * head;
@@ -133,69 +145,63 @@ DG_BOTH void paged_locate(const PagedArgs &a, const PagedSeq &s, int b, int64_t 
     r.item = base + r.g * head + paged_prefix(s, lo);
 }
 
-struct PagedScan {
-    int64_t warp_sum[12];    // one a warp
-    PagedRange r;
-};
-
-// Unit u of `units`, in a CTA of NT threads: its stretch, left in sc.r.  All
-// threads of the CTA call it.
-template <int ROWS, int BKV, int NT>
-DG_DEVICE void paged_divide(const PagedArgs &a, int u, int units, PagedScan &sc)
+// Unit u of `units`: its stretch.  By one warp, a sequence a lane and 32 at a
+// time: once over all of them for the line's cost, and again up to the one that
+// the stretch begins in (a batch of up to 32 keeps its costs in registers).
+template <int ROWS, int BKV, class I>
+DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units)
 {
-    constexpr int NW = NT / 32;
-    static_assert(NW <= 12, "PagedScan");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ch = (a.B + NT - 1) / NT;
-    const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
-    int64_t mine = 0;
+    const int lane = threadIdx.x & 31;
+    PagedRange<I> r{};
     bool bad = false;
-    for (int b = b0; b < b1; ++b) {
+    auto cost_of = [&](int b, bool look) -> I {
+        if (b >= a.B) return 0;
         bool cut;
-        const PagedSeq s = paged_seq<ROWS, BKV>(a, b, &cut);
-        bad |= cut;
-        mine += a.Hkv * paged_prefix(s, s.mt);
-    }
-    if (bad && u == 0) report_error(a.ws, DG_ERR_DEVICE, 911);
-    int64_t incl = mine;
+        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b, &cut);
+        if (look) bad |= cut;
+        return a.Hkv * paged_prefix(s, s.mt);
+    };
+    I mine = cost_of(lane, true), W = mine;
+#pragma unroll 4
+    for (int b0 = 32; b0 < a.B; b0 += 32) W += cost_of(b0 + lane, true);
+    I incl = 0;
+    auto scan = [&](I v) {
+        incl = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) sc.warp_sum[warp] = incl;
-    if (tid == 0) sc.r.begin = sc.r.end = 0;
-    __syncthreads();
-    int64_t W = 0, before = incl - mine;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += sc.warp_sum[w];
-        W += sc.warp_sum[w];
-    }
-    if (mine > 0) {
-        const int64_t step = paged_step(a, W, units), x = u * step;
-        if (x >= before && x < before + mine) {
-            int64_t base = before;
-            for (int b = b0; b < b1; ++b) {
-                const PagedSeq s = paged_seq<ROWS, BKV>(a, b);
-                const int64_t c = a.Hkv * paged_prefix(s, s.mt);
-                if (x < base + c) {
-                    paged_locate<ROWS, BKV>(a, s, b, base, x, sc.r);
-                    sc.r.begin = x;
-                    sc.r.end = min(W, x + step);
-                    sc.r.step = step;
-                    break;
-                }
-                base += c;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const I p = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += p;
         }
+    };
+    scan(W);
+    W = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    if (bad && u == 0) report_error(a.ws, DG_ERR_DEVICE, 911);
+    if (W == 0) return r;
+    const I step = paged_step(a, W, units), x = u * step;
+    if (x >= W) return r;
+    I base = 0;
+    for (int b0 = 0;; b0 += 32) {
+        if (a.B > 32) {
+            if (b0 > 0) mine = cost_of(b0 + lane, false);
+            scan(mine);
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + incl > x);
+        if (past != 0) {
+            const int at = __ffs(past) - 1;
+            base += __shfl_sync(0xFFFFFFFFu, incl - mine, at);
+            paged_locate(paged_seq<ROWS, BKV, I>(a, b0 + at), b0 + at, base, x, r);
+            r.begin = x;
+            r.end = min(W, x + step);
+            r.step = step;
+            return r;
+        }
+        base += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    __syncthreads();
 }
 
 // One stretch's share of an item.
 struct PagedPart {
-    PagedSeq s;
+    int s0, n, kv;       // the sequence
     int b, g;
     int frow0, rows;     // folded rows of the query tile
     int nkp;             // key tiles of the pages (further ones: the chunk's own keys)
@@ -207,13 +213,13 @@ struct PagedPart {
 };
 
 // Walks the parts of a stretch.
-template <int ROWS, int BKV>
+template <int ROWS, int BKV, class I>
 struct PagedWalk {
-    PagedSeq s, ahead;   // this sequence, the next one's lengths (already loaded)
+    PagedSeq<I> s, ahead;   // this sequence, the next one's lengths (already loaded)
     int b, g, m;
-    int64_t item, begin, end, step;
+    I item, begin, end, step;
 
-    DG_BOTH void start(const PagedArgs &a, const PagedRange &r)
+    DG_BOTH void start(const PagedArgs &a, const PagedRange<I> &r)
     {
         begin = r.begin;
         item = end = r.end;
@@ -223,31 +229,33 @@ struct PagedWalk {
         g = r.g;
         m = r.m;
         item = r.item;
-        s = paged_seq<ROWS, BKV>(a, b);
+        s = paged_seq<ROWS, BKV, I>(a, b);
         ahead = s;
-        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV>(a, b + 1);
+        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1);
     }
 
     // The next part; false: the stretch is done.
     DG_BOTH bool next(const PagedArgs &a, PagedPart &p)
     {
         while (item < end) {
-            const int64_t cost = paged_prefix(s, m + 1) - paged_prefix(s, m);
-            p.s = s;
+            const I cost = paged_prefix(s, m + 1) - paged_prefix(s, m);
+            p.s0 = s.s0;
+            p.n = s.n;
+            p.kv = s.kv;
             p.b = b;
             p.g = g;
             p.frow0 = m * ROWS;
             p.rows = paged_min(ROWS, s.n * a.G - p.frow0);
-            const int i0 = p.frow0 / a.G, i1 = (p.frow0 + p.rows - 1) / a.G;
             p.nkp = (s.kv + BKV - 1) / BKV;
             int hi, lo = 0;
-            if (!a.causal)
+            if (!a.causal) {
                 hi = p.nkp + (a.has_new ? (s.n + BKV - 1) / BKV : 0);
-            else if (a.has_new)
-                hi = p.nkp + i1 / BKV + 1;
-            else
-                hi = paged_max(0, (s.kv - s.n + i1 + BKV) / BKV);
+            } else {
+                const int i1 = (p.frow0 + p.rows - 1) / a.G;
+                hi = a.has_new ? p.nkp + i1 / BKV + 1 : paged_max(0, (s.kv - s.n + i1 + BKV) / BKV);
+            }
             if (a.window > 0) {
+                const int i0 = p.frow0 / a.G;
                 const int first = (a.has_new ? s.kv : s.kv - s.n) + i0 - a.window + 1;
                 if (first > 0)
                     lo = a.has_new && first >= s.kv ? p.nkp + (first - s.kv) / BKV : first / BKV;
@@ -256,21 +264,21 @@ struct PagedWalk {
             p.nt = paged_max(0, hi - lo);
             // a tile is worth its keys: BKV x G of the cost after the fixed
             // part; what rounding leaves over goes with the last tile
-            const int64_t tile = static_cast<int64_t>(a.G) * BKV;
-            auto cut = [&](int64_t x) -> int {   // tiles before cost x of the item
+            const I tile = static_cast<I>(a.G) * BKV;
+            auto cut = [&](I x) -> int {   // tiles before cost x of the item
                 if (x <= s.fixed) return 0;
                 if (x >= cost) return p.nt;
-                return static_cast<int>(paged_min<int64_t>(paged_div(x - s.fixed, tile), p.nt));
+                return static_cast<int>(paged_min<I>(paged_div<I>(x - s.fixed, tile), p.nt));
             };
-            const int64_t from = begin - item, to = end - item;
+            const I from = begin - item, to = end - item;
             p.t0 = cut(from);
             p.t1 = cut(to);
             p.whole = p.t0 == 0 && p.t1 == p.nt && (p.nt > 0 || from <= 0);
             p.last = -1;
             const bool any = p.t1 > p.t0 || (p.nt == 0 && from <= 0);
             if (any && p.t0 == 0 && !p.whole)
-                p.last = static_cast<int>(paged_div(
-                    item + paged_min<int64_t>(s.fixed + p.nt * tile, cost) - 1, step));
+                p.last = static_cast<int>(
+                    paged_div<I>(item + paged_min<I>(s.fixed + p.nt * tile, cost) - 1, step));
             item += cost;
             if (++m == s.mt) {
                 m = 0;
@@ -282,7 +290,7 @@ struct PagedWalk {
                             break;
                         }
                         s = ahead;
-                        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV>(a, b + 1);
+                        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1);
                     } while (s.n == 0);
                 }
             }
@@ -306,6 +314,7 @@ struct __align__(16) PagedItem {
     int32_t pad;
 };
 constexpr int kPagedItems = 4;
+constexpr int kPagedLoadSleep = 60;    // ns between a load warp's looks at a full ring
 struct PagedRing {
     PagedItem item[kPagedItems];
     uint64_t full[kPagedItems], empty[kPagedItems];
@@ -323,28 +332,31 @@ DG_DEVICE void paged_ring_init(PagedRing &ring, int takers)
     }
 }
 
-// The walking warp (all lanes).
-template <class Gm>
-DG_DEVICE void paged_walk(const PagedArgs &a, const PagedRange &range, PagedRing &ring, int where)
+// The walking warp (all lanes), for unit u of `units`.  It divides the work
+// while the rest of the CTA sets up; `ready` returns once the ring may be used.
+template <class Gm, class I, class Ready>
+DG_DEVICE void paged_walk_in(const PagedArgs &a, int u, int units, PagedRing &ring, int where,
+                             Ready ready)
 {
     const bool lead = (threadIdx.x & 31) == 0;
-    PagedWalk<Gm::Rows, Gm::BKV> walk;
-    walk.start(a, range);
+    PagedWalk<Gm::Rows, Gm::BKV, I> walk;
+    walk.start(a, paged_divide<Gm::Rows, Gm::BKV, I>(a, u, units));
     PagedPart p;
+    bool more = walk.next(a, p);
+    ready();
     for (uint32_t k = 0;; ++k) {
-        const bool more = walk.next(a, p);
         const int e = static_cast<int>(k % kPagedItems);
-        const bool ok = mbar_wait_poll(&ring.empty[e], ((k / kPagedItems) & 1u) ^ 1u, a.ws, where,
-                                       kPagedWalkLimitNs);
+        const bool ok = mbar_wait_poll<false, 400>(&ring.empty[e], ((k / kPagedItems) & 1u) ^ 1u, a.ws,
+                                                   where, kPagedWalkLimitNs);
         if (!__all_sync(0xFFFFFFFFu, ok)) return;
         if (lead) {
             PagedItem it{};
             if (more) {
                 it.b = p.b;
                 it.g = p.g;
-                it.s0 = p.s.s0;
-                it.n = p.s.n;
-                it.kv = p.s.kv;
+                it.s0 = p.s0;
+                it.n = p.n;
+                it.kv = p.kv;
                 it.frow0 = p.frow0;
                 it.rows = p.rows;
                 it.tv0 = p.lo + p.t0;
@@ -356,7 +368,15 @@ DG_DEVICE void paged_walk(const PagedArgs &a, const PagedRange &range, PagedRing
             mbar_arrive(&ring.full[e]);
         }
         if (!more) return;
+        more = walk.next(a, p);
     }
+}
+
+template <class Gm, class Ready>
+DG_DEVICE void paged_walk(const PagedArgs &a, int u, int units, PagedRing &ring, int where, Ready ready)
+{
+    if (a.small) paged_walk_in<Gm, int32_t>(a, u, units, ring, where, ready);
+    else paged_walk_in<Gm, int64_t>(a, u, units, ring, where, ready);
 }
 
 // The k-th part, by every thread of a role's warp (or one thread alone, which
@@ -428,7 +448,7 @@ __device__ __forceinline__ void paged_ring_producer(uint8_t *buf, uint64_t *full
             }
             const int s = static_cast<int>(it % NS);
             const uint32_t use = it / NS;
-            ok = mbar_wait_poll(&empty[s], (use & 1u) ^ 1u, a.ws, where);
+            ok = mbar_wait_poll<false, kPagedLoadSleep>(&empty[s], (use & 1u) ^ 1u, a.ws, where);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;

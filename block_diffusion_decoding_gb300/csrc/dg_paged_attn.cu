@@ -46,7 +46,7 @@ struct PagedGeom {
     static constexpr int ColS = D;
     static constexpr int ColQ = D + 2 * BKV;
     static_assert(ColQ + D / 2 <= 512, "TMEM columns");
-    static_assert(Smem + sizeof(PagedScan) + sizeof(PagedRing) <= 232448, "shared memory");
+    static_assert(Smem + sizeof(PagedRing) <= 232448, "shared memory");
 };
 
 int paged_attn_smem_bytes(int D)
@@ -62,7 +62,6 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     using Gm = PagedGeom<D>;
     constexpr int BKV = Gm::BKV, NK = Gm::NK, NV = Gm::NV;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ PagedScan scan;
     __shared__ PagedRing ring;
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -79,10 +78,6 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     uint64_t *drained = o_full + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
 
-    // inputs may come from the previous kernel of the stream; nor is TMEM
-    // taken before that kernel has given its own back
-    griddep_wait();
-    griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < NK; ++s) {
@@ -110,21 +105,26 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
             tma_prefetch_desc(map_vn);
         }
     }
+    // inputs may come from the previous kernel of the stream; nor is TMEM
+    // taken before that kernel has given its own back
+    griddep_wait();
+    griddep_launch_dependents();
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
-    paged_divide<128, BKV, kPagedThreads>(a, blockIdx.x, gridDim.x, scan);
+    if (warp != 7) cta_sync();           // warp 7: once it has divided the work
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) {
+    if (warp == 7) {
+        paged_walk<Gm>(a, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), ring, 927,
+                       [] { cta_sync(); });
+    } else if (warp == 0) {
         paged_ring_producer<Gm, NK>(smem + Gm::OffK, k_full, k_empty, map_k, map_kn, a, ring, 921);
     } else if (warp == 6) {
         paged_ring_producer<Gm, NV>(smem + Gm::OffV, v_full, v_empty, map_v, map_vn, a, ring, 924);
-    } else if (warp == 7) {
-        paged_walk<Gm>(a, scan.r, ring, 927);
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMA
         if (lane == 0) {
@@ -373,13 +373,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_attn_body<256>(&map_k, &map_v, &map_kn, &map_vn, a);
 }
 
-// Joins the parts of the items that were cut: the blocks (c, y) take the item
-// whose first part unit c left in its slot 1; the others are slot 0 of units
-// c + 1 .. last, taken in that order.  out = sum 2^(m_z - M) O_z /
-// sum 2^(m_z - M) l_z.  A thread takes 16 dims of a row, neighbouring threads
-// neighbouring rows.  An item too small to fill a block with those (single
-// tokens, whose caches may have parts from every SM) shares its parts out over
-// the block's threads and joins their results in shared memory.
+// Joins the parts of the items that were cut.  An item's first part is in slot 1
+// of unit c, which describes it; the others are in slot 0 of units c + 1 ..
+// last, taken in that order: out = sum 2^(m_z - M) O_z / sum 2^(m_z - M) l_z.
+// A thread takes 16 dims of a row, neighbouring threads neighbouring rows, with
+// the loads of kMergeParts parts in flight; a block takes the next 256 of those
+// in all the items.  An item too small to fill a block (single tokens, whose
+// caches may have parts from every SM) shares its parts out over the block's
+// threads and joins their results in shared memory.
+// Bound by latency, not bytes: the descriptors, then all of a thread's parts,
+// then the row.  A block per possible row group instead (2432 of them for one
+// 256-token canvas, most with nothing to do) took 12.4 us against this one's
+// few.
 struct MergeState {
     float M, den;
     float acc[16];
@@ -401,21 +406,46 @@ DG_DEVICE void merge_add(MergeState &s, float m, float l, const float (&x)[16])
     for (int e = 0; e < 16; ++e) s.acc[e] = fmaf(w, x[e], s.acc[e]);
 }
 
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedArgs a)
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedArgs a, int units)
 {
     __shared__ float s_state[18][kMergeThreads];
+    __shared__ int s_end[kMergeThreads];     // blocks of work up to and with unit t's item
+    __shared__ int s_warp[kMergeThreads / 32];
+    __shared__ int s_part0[kMergeThreads];
     griddep_wait();
     griddep_launch_dependents();
-    const int c = blockIdx.x;
-    const PagedDesc de = a.desc[c];
-    if (de.last < 0) return;
-    const int pairs = de.rows * (a.D / 16);
-    // threads that share a pair's parts
-    int share = 1;
-    while (share < 32 && pairs * share * 2 <= kMergeThreads) share *= 2;
-    if (share > 1 && blockIdx.y > 0) return;
-    for (int p0 = blockIdx.y * kMergeThreads; p0 < pairs; p0 += gridDim.y * kMergeThreads) {
-        const int at = p0 + static_cast<int>(threadIdx.x);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    {
+        int n = 0;
+        if (tid < units) {
+            const PagedDesc de = a.desc[tid];
+            if (de.last >= 0) n = (de.rows * (a.D / 16) + kMergeThreads - 1) / kMergeThreads;
+            s_part0[tid] = de.part0;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, n, o);
+            if (lane >= o) n += v;
+        }
+        if (lane == 31) s_warp[warp] = n;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) n += s_warp[w];
+        s_end[tid] = n;
+        __syncthreads();
+    }
+    const int total = s_end[kMergeThreads - 1];
+    for (int job = blockIdx.x; job < total; job += gridDim.x) {
+        int c = 0;                               // the first unit with s_end > job
+#pragma unroll
+        for (int o = kMergeThreads / 2; o > 0; o >>= 1)
+            if (s_end[c + o - 1] <= job) c += o;
+        const PagedDesc de = a.desc[c];
+        const int p0 = (job - (c > 0 ? s_end[c - 1] : 0)) * kMergeThreads;
+        const int pairs = de.rows * (a.D / 16);
+        // threads that share a pair's parts
+        int share = 1;
+        while (share < 32 && pairs * share * 2 <= kMergeThreads) share *= 2;
+        const int at = p0 + tid;
         const int part = share > 1 ? at / pairs : 0;
         const int pair = at - part * pairs;
         const bool live = part < share && pair < pairs;
@@ -426,41 +456,44 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedArgs a)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s.acc[e] = 0.f;
         if (live) {
-            for (int z0 = c + part; z0 <= de.last; z0 += 2 * share) {
-                float2 ml[2];
-                float x[2][16];
+            for (int z0 = c + part; z0 <= de.last; z0 += kMergeParts * share) {
+                float2 ml[kMergeParts];
+                float4 x[kMergeParts][4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < kMergeParts; ++k) {
                     const int z = z0 + k * share;
                     ml[k] = make_float2(0.f, 0.f);
-                    if (z > de.last) continue;
+                    if (z > de.last || (z > c && s_part0[z] == 0)) continue;
                     const int slot = 2 * z + (z == c ? 1 : 0);
-                    const bool have = z == c || a.desc[z].part0 != 0;
-                    const float2 v = a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + row];
+                    ml[k] = a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + row];
                     const float4 *src = part_at(a, slot, row, dg * 16);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 f = src[static_cast<int64_t>(e) * a.slot_rows];
-                        x[k][4 * e] = f.x;
-                        x[k][4 * e + 1] = f.y;
-                        x[k][4 * e + 2] = f.z;
-                        x[k][4 * e + 3] = f.w;
-                    }
-                    if (have) ml[k] = v;
+                    for (int e = 0; e < 4; ++e) x[k][e] = src[static_cast<int64_t>(e) * a.slot_rows];
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) merge_add(s, ml[k].x, ml[k].y, x[k]);
+                for (int k = 0; k < kMergeParts; ++k) {
+                    float v[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[4 * e] = x[k][e].x;
+                        v[4 * e + 1] = x[k][e].y;
+                        v[4 * e + 2] = x[k][e].z;
+                        v[4 * e + 3] = x[k][e].w;
+                    }
+                    merge_add(s, ml[k].x, ml[k].y, v);
+                }
             }
         }
         if (share > 1) {
-            s_state[0][threadIdx.x] = s.M;
-            s_state[1][threadIdx.x] = s.den;
+            __syncthreads();                     // the job before has been read
+            s_state[0][tid] = s.M;
+            s_state[1][tid] = s.den;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s_state[2 + e][threadIdx.x] = s.acc[e];
+            for (int e = 0; e < 16; ++e) s_state[2 + e][tid] = s.acc[e];
             __syncthreads();
-            if (part > 0) continue;              // (one round: nothing follows)
+            if (part > 0) continue;
             for (int k = 1; live && k < share; ++k) {
-                const int t = threadIdx.x + k * pairs;
+                const int t = tid + k * pairs;
                 float x[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] = s_state[2 + e][t];

@@ -18,7 +18,8 @@
 //   TMEM        O [128 x D] fp32 | S buffers [128 x 128] fp32 (the bf16 P of a
 //               tile overwrites the S it came from);
 //   warp 0      TMA: K halves;    warp 2   TMA: V halves;    warp 3   the walk;
-//   warp 1      UMMA issuer (even CTA): S runs NS - 1 tiles ahead of PV;
+//   warp 1      UMMA issuer (even CTA): S runs NS - 1 tiles ahead of PV; the odd
+//               CTA's passes on that its query rows are in place;
 //   warps 4-7   softmax of the even tiles, a query row a thread; warps 8-11 of
 //               the odd ones; both load Q rows, and each stores half of O.
 // All copies of a tile complete on the even CTA's barrier.  Only where V needs
@@ -55,7 +56,6 @@ struct PairGeom {
 };
 
 struct PairShared {
-    PagedScan scan;
     PagedRing ring;
     uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_land[6];
     uint64_t s_full[3], p_full[3];    // by S buffer: P(t + NS) cannot be signalled before
@@ -123,7 +123,7 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
                 pages = ahead;
                 ahead = fetch(tv + batch);
             }
-            ok = mbar_wait_poll(&empty[s], par ^ 1u, a.ws, where);
+            ok = mbar_wait_poll<false, kPagedLoadSleep>(&empty[s], par ^ 1u, a.ws, where);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
@@ -201,10 +201,6 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         return;
     }
 
-    // inputs may come from the previous kernel of the stream; nor is TMEM
-    // taken before that kernel has given its own back
-    griddep_wait();
-    griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = static_cast<int>(cluster_ctarank());
     const int unit = static_cast<int>(cluster_id_x());
@@ -229,11 +225,11 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 mbar_init(&sh.l_full[h][q], 1);
             }
         }
-        mbar_init(&sh.q_ready, 16);                  // the softmax warps of both CTAs
+        mbar_init(&sh.q_ready, r == 0 ? 9 : 8);      // its softmax warps; the other CTA's all at once
         mbar_init(&sh.o_full, 1);
         mbar_init(&sh.o_free, 16);
         mbar_init(&sh.drained, 1);
-        paged_ring_init(sh.ring, r == 0 ? 11 : 10);  // K, V, softmax warps; UMMA (even CTA)
+        paged_ring_init(sh.ring, 11);                // K, V, UMMA, softmax warps
         fence_barrier_init();
         tma_prefetch_desc(map_k);
         tma_prefetch_desc(map_v);
@@ -242,32 +238,41 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
             tma_prefetch_desc(map_vn);
         }
     }
+    // inputs may come from the previous kernel of the stream; nor is TMEM
+    // taken before that kernel has given its own back
+    griddep_wait();
+    griddep_launch_dependents();
     if (warp == 1) {
         tmem_alloc_pair(&sh.tmem, 512);
         tmem_relinquish_pair();
     }
-    tc_fence_before();
-    paged_divide<Gm::Rows, BKV, kPagedPairThreads>(a, unit, static_cast<int>(num_clusters_x()),
-                                                   sh.scan);
-    tc_fence_after();
-    // both CTAs' barriers exist before either signals the other
-    cluster_sync_all();
-    const uint32_t tmem = sh.tmem;
+    // both CTAs' barriers exist before either signals the other; the walking
+    // warp comes to it when it has divided the work
+    auto together = [&]() -> uint32_t {
+        tc_fence_before();
+        cluster_sync_all();
+        tc_fence_after();
+        return sh.tmem;
+    };
     auto lead_of = [&](const uint64_t *bar) -> uint32_t { return mapa_shared(smem_u32(bar), 0); };
 
     // A softmax thread holds 128 scores: its warps take registers from the
     // other four.
     if (warp < 4) {
         reg_dec<kPairOtherRegs>();
-        if (warp == 0) {
+        if (warp == 3) {
+            paged_walk<Gm>(a, unit, static_cast<int>(num_clusters_x()), sh.ring, 1007,
+                           [&] { together(); });
+        } else if (warp == 0) {
+            together();
             pair_producer<Gm, false>(smem + Gm::OffK, sh, lead_of(sh.k_full), r, map_k, map_kn, a, 1001);
         } else if (warp == 2) {
+            together();
             pair_producer<Gm, true>(smem + Gm::OffV, sh, lead_of(sh.v_full), r, map_v, map_vn, a, 1004);
-        } else if (warp == 3) {
-            paged_walk<Gm>(a, sh.scan.r, sh.ring, 1007);
         } else if (warp == 1) {
             // -------------------------------------------------------------- MMA
             // (the whole warp of the even CTA, see elect_lane)
+            const uint32_t tmem = together();
             if (r == 0) {
                 const uint32_t idesc_s = make_idesc_bf16(256, BKV, 0);
                 const uint32_t idesc_o = make_idesc_bf16(256, D, 1);
@@ -359,10 +364,24 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 if (lead) umma_commit_pair(&sh.drained, 0x3);
                 __syncwarp();
                 mbar_wait_poll(&sh.drained, 0, a.ws, 1015);
+            } else {
+                // the odd CTA's: passes on that its query rows are in place (one
+                // arrival ordered over the cluster, by a warp with no memory
+                // traffic of its own to wait for)
+                uint32_t parts = 0;
+                PagedItem p;
+                for (uint32_t k = 0; paged_take(a, sh.ring, k, p, false, 1017); ++k) {
+                    if (p.tv1 == p.tv0) continue;
+                    bool ok = mbar_wait_poll<false, 100>(&sh.q_ready, parts & 1u, a.ws, 1018);
+                    ++parts;
+                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                    if (lane == 0) mbar_arrive_cluster(lead_of(&sh.q_ready));
+                }
             }
         }
     } else {
         reg_inc<kPairSoftmaxRegs>();
+        const uint32_t tmem = together();
         // -------------------------------------------------------------- softmax
         const int wg = (warp - 4) >> 2;          // 0: even tiles, 1: odd tiles
         const int q = warp & 3;                  // TMEM lane quadrant of the warp
@@ -403,7 +422,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_of(&sh.q_ready));
+            if (lane == 0) mbar_arrive(&sh.q_ready);
         };
 
         PagedItem p;
@@ -530,7 +549,10 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                     paged_zero_tail<Gm>(smem + Gm::OffV + vs * Gm::VBytes, valid, threadIdx.x & 127);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(lead_of(&sh.p_full[ss]));
+                    if (lane == 0) {
+                        if (r == 0) mbar_arrive(&sh.p_full[ss]);
+                        else mbar_arrive_cluster(lead_of(&sh.p_full[ss]));
+                    }
                 } else {
                     tc_fence_before();
                     __syncwarp();
@@ -611,7 +633,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
     cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
+        tmem_dealloc_pair(sh.tmem, 512);
     }
 }
 

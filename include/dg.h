@@ -167,7 +167,7 @@ int dg_encoder_append(const uint16_t *q, uint16_t *k_cache, uint16_t *v_cache, i
 /* [0, n_pages) reads as a page of zeros and is not written; either records  */
 /* DG_ERR_DEVICE in the workspace's status word.                             */
 /* Supported: D in {128, 256}; page_size a multiple of 16, 16 .. 2048;       */
-/* max_pages * page_size <= 2^30; page_stride a multiple of 8 and            */
+/* max_pages * page_size <= 2^29; page_stride a multiple of 8 and            */
 /* >= page_size * Hkv * D, or 0 for that value.                              */
 typedef struct dg_paged_cache {
     uint16_t *k, *v;            /* the pages                                  */
@@ -244,7 +244,7 @@ int dg_paged_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int6
 /* q, out [T, Hq, D]; rows *_stride elements apart as above; out overlaps no */
 /* input.  bf16 in and out, fp32 accumulation, softmax and partial results.  */
 /* The work is divided over the GPU on the device, from the lengths.         */
-/* Supported: Hq % Hkv == 0, Hq / Hkv <= 128; scale > 0; T * Hq <= 2^30;     */
+/* Supported: Hq % Hkv == 0, Hq / Hkv <= 128; scale > 0; T * Hq <= 2^29;     */
 /* window requires causal.  T == 0 is allowed.                               */
 size_t dg_paged_attn_workspace(int T, int Hq, const dg_paged_cache *c);
 int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, int64_t k_stride,

@@ -24,46 +24,46 @@ using namespace dg;
 
 #define FAIL(...) do { printf(__VA_ARGS__); printf("\n"); return 1; } while (0)
 
-template <int ROWS, int BKV>
+template <int ROWS, int BKV, class I>
 int check(const PagedArgs &a, int units)
 {
-    std::vector<int64_t> base(a.B + 1, 0);
+    std::vector<I> base(a.B + 1, 0);
     for (int b = 0; b < a.B; ++b) {
-        const PagedSeq s = paged_seq<ROWS, BKV>(a, b);
+        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b);
         if (s.s0 < 0 || s.n < 0 || s.s0 + s.n > a.T || s.kv < 0 || s.kv > a.max_pages * a.page_size)
             FAIL("lengths not cut");
         base[b + 1] = base[b] + a.Hkv * paged_prefix(s, s.mt);
     }
-    const int64_t W = base[a.B];
+    const I W = base[a.B];
     if (W == 0) return 0;
-    const int64_t step = paged_step(a, W, units);
+    const I step = paged_step(a, W, units);
     const int n = static_cast<int>((W + step - 1) / step);
     if (n > units) FAIL("%d units of %d", n, units);
     // per item: the tiles so far, the unit promised the last part
     std::map<std::tuple<int, int, int>, std::pair<int, int>> items;
     for (int u = 0; u < n; ++u) {
-        PagedRange r{};
+        PagedRange<I> r{};
         r.begin = u * step;
         r.end = r.begin + step < W ? r.begin + step : W;
         r.step = step;
         int b = 0;
         while (base[b + 1] <= r.begin) ++b;
-        paged_locate<ROWS, BKV>(a, paged_seq<ROWS, BKV>(a, b), b, base[b], r.begin, r);
-        PagedWalk<ROWS, BKV> walk;
+        paged_locate(paged_seq<ROWS, BKV, I>(a, b), b, base[b], r.begin, r);
+        PagedWalk<ROWS, BKV, I> walk;
         walk.start(a, r);
         PagedPart p;
         int slot0 = 0, slot1 = 0;
         while (walk.next(a, p)) {
             // the definition, from the lengths alone
             int lo = 1 << 30, hi = 0;
-            const int keys = p.s.kv + (a.has_new ? p.s.n : 0);
+            const int keys = p.kv + (a.has_new ? p.n : 0);
             for (int row = p.frow0; row < p.frow0 + p.rows; ++row) {
-                const int pos = keys - p.s.n + row / a.G;
+                const int pos = keys - p.n + row / a.G;
                 const int last = a.causal ? pos : keys - 1;
                 const int first = a.window ? (pos - a.window + 1 > 0 ? pos - a.window + 1 : 0) : 0;
                 if (last < first) continue;
                 auto tile = [&](int key) {
-                    return key < p.s.kv ? key / BKV : p.nkp + (key - p.s.kv) / BKV;
+                    return key < p.kv ? key / BKV : p.nkp + (key - p.kv) / BKV;
                 };
                 if (tile(first) < lo) lo = tile(first);
                 if (tile(last) + 1 > hi) hi = tile(last) + 1;
@@ -94,7 +94,7 @@ int check(const PagedArgs &a, int units)
         }
     }
     for (int b = 0; b < a.B; ++b) {
-        const PagedSeq s = paged_seq<ROWS, BKV>(a, b);
+        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b);
         for (int g = 0; g < a.Hkv; ++g)
             for (int m = 0; m < s.mt; ++m)
                 if (!items.count(std::make_tuple(b, g, m * ROWS))) FAIL("item (%d %d %d) missing", b, g, m);
@@ -105,7 +105,7 @@ int check(const PagedArgs &a, int units)
 int main()
 {
     int T, B, Hkv, G, page, width, fresh, causal, window, units, bkv, rows;
-    long line = 0;
+    long line = 0, small = 0;
     while (scanf("%d %d %d %d %d %d %d %d %d %d %d %d", &T, &B, &Hkv, &G, &page, &width, &fresh, &causal,
                  &window, &units, &bkv, &rows) == 12) {
         std::vector<int32_t> start(B + 1), kv(B);
@@ -115,12 +115,17 @@ int main()
         a.T = T; a.B = B; a.Hkv = Hkv; a.G = G; a.page_size = page; a.max_pages = width;
         a.has_new = fresh; a.causal = causal; a.window = window;
         a.q_start = start.data(); a.kv_len = kv.data();
-        const int rc = rows == 256 ? check<256, 128>(a, units)
-                       : bkv == 128 ? check<128, 128>(a, units) : check<128, 64>(a, units);
+        int rc = rows == 256 ? check<256, 128, int64_t>(a, units)
+                 : bkv == 128 ? check<128, 128, int64_t>(a, units) : check<128, 64, int64_t>(a, units);
+        if (!rc && paged_small(T, B, Hkv, G, static_cast<int64_t>(width) * page)) {
+            rc = rows == 256 ? check<256, 128, int32_t>(a, units)
+                 : bkv == 128 ? check<128, 128, int32_t>(a, units) : check<128, 64, int32_t>(a, units);
+            ++small;
+        }
         if (rc) { printf("case %ld\n", line); return 1; }
         ++line;
     }
-    printf("%ld cases\n", line);
+    printf("%ld cases, %ld of them also in 32 bits\n", line, small);
     return 0;
 }
 """
@@ -173,3 +178,5 @@ def test_every_visible_tile_goes_to_one_cta(harness):
     where = int(r.stdout.split()[-1]) if "case " in r.stdout and r.returncode else None
     assert r.returncode == 0, (r.stdout[-300:], cases[where][:12] if where is not None else r.stderr[-300:])
     assert "1500 cases" in r.stdout
+    small = int(r.stdout.split()[2])
+    assert 500 < small < 1500, r.stdout     # both kinds, and lines too long for 32 bits
