@@ -204,8 +204,11 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: torch.cuda.current_stream() makes a Stream object
+    # around it, which takes longer than a small kernel's launch
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(rc: int, what: str):
@@ -274,7 +277,7 @@ def _ints(t: torch.Tensor, n: int, what: str):
 
 
 def _on_current(device: torch.device, what: str):
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         _refuse(what, "the tensors are on %s, which is not the current device" % device)
 
 

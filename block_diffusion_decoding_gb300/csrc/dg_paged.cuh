@@ -147,9 +147,10 @@ DG_BOTH void paged_locate(const PagedSeq<I> &s, int b, I base, I x, PagedRange<I
 
 // Unit u of `units`: its stretch.  By one warp, a sequence a lane and 32 at a
 // time: once over all of them for the line's cost, and again up to the one that
-// the stretch begins in (a batch of up to 32 keeps its costs in registers).
+// the stretch begins in (a batch of up to 32 keeps its costs in registers), whose
+// lengths are left in s.
 template <int ROWS, int BKV, class I>
-DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units)
+DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, PagedSeq<I> &s)
 {
     const int lane = threadIdx.x & 31;
     PagedRange<I> r{};
@@ -189,7 +190,8 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units)
         if (past != 0) {
             const int at = __ffs(past) - 1;
             base += __shfl_sync(0xFFFFFFFFu, incl - mine, at);
-            paged_locate(paged_seq<ROWS, BKV, I>(a, b0 + at), b0 + at, base, x, r);
+            s = paged_seq<ROWS, BKV, I>(a, b0 + at);
+            paged_locate(s, b0 + at, base, x, r);
             r.begin = x;
             r.end = min(W, x + step);
             r.step = step;
@@ -219,7 +221,8 @@ struct PagedWalk {
     int b, g, m;
     I item, begin, end, step;
 
-    DG_BOTH void start(const PagedArgs &a, const PagedRange<I> &r)
+    // first: the lengths of the sequence the stretch begins in
+    DG_BOTH void start(const PagedArgs &a, const PagedRange<I> &r, const PagedSeq<I> &first)
     {
         begin = r.begin;
         item = end = r.end;
@@ -229,8 +232,7 @@ struct PagedWalk {
         g = r.g;
         m = r.m;
         item = r.item;
-        s = paged_seq<ROWS, BKV, I>(a, b);
-        ahead = s;
+        s = ahead = first;
         if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1);
     }
 
@@ -340,7 +342,17 @@ DG_DEVICE void paged_walk_in(const PagedArgs &a, int u, int units, PagedRing &ri
 {
     const bool lead = (threadIdx.x & 31) == 0;
     PagedWalk<Gm::Rows, Gm::BKV, I> walk;
-    walk.start(a, paged_divide<Gm::Rows, Gm::BKV, I>(a, u, units));
+    PagedSeq<I> first{};
+    const PagedRange<I> range = paged_divide<Gm::Rows, Gm::BKV, I>(a, u, units, first);
+    if (range.end > range.begin) {
+        // the load warps will want the pages of the first keys next
+        const I key = paged_div<I>(paged_max<I>(range.begin - range.item, first.fixed) - first.fixed, a.G);
+        const int page = static_cast<int>(key) / a.page_size + (static_cast<int>(threadIdx.x) & 31) * 32;
+        if (page < a.max_pages)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                a.page_table + static_cast<int64_t>(range.b) * a.max_pages + page));
+    }
+    walk.start(a, range, first);
     PagedPart p;
     bool more = walk.next(a, p);
     ready();

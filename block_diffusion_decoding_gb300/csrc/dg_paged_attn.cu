@@ -127,65 +127,86 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         paged_ring_producer<Gm, NV>(smem + Gm::OffV, v_full, v_empty, map_v, map_vn, a, ring, 924);
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMA
-        if (lane == 0) {
-            const uint32_t idesc_s = make_idesc_bf16(128, BKV, 0);
-            const uint32_t idesc_o = make_idesc_bf16(128, D, 1);
-            const uint32_t sk0 = smem_u32(smem + Gm::OffK);
-            const uint32_t sv0 = smem_u32(smem + Gm::OffV);
-            uint32_t it0 = 0, parts = 0;    // tiles and parts before this part
-            bool ok = true;
-            PagedItem p;
-            for (uint32_t k = 0; ok && paged_take(a, ring, k, p, true, 930); ++k) {
-                const int nt = p.tv1 - p.tv0;
-                if (nt == 0) continue;
-                ok = mbar_wait_poll(q_ready, parts & 1u, a.ws, 931);
-                tc_fence_after();
-                auto issue_s = [&](int j) -> bool {
-                    const uint32_t it = it0 + j;
-                    const int s = static_cast<int>(it % NK);
-                    if (!mbar_wait_poll(&k_full[s], (it / NK) & 1u, a.ws, 932)) return false;
+        // (the whole warp, see elect_lane)
+        const uint32_t idesc_s = make_idesc_bf16(128, BKV, 0);
+        const uint32_t idesc_o = make_idesc_bf16(128, D, 1);
+        // descriptors of the rings' first tiles; the address sits in the low
+        // bits in units of 16 bytes
+        const uint64_t dk0 = make_sdesc_sw128(smem_u32(smem + Gm::OffK), 16, 1024);
+        const uint64_t dv0 = make_sdesc_sw128(smem_u32(smem + Gm::OffV), Gm::KVAtomBytes, 1024);
+        const bool lead = elect_lane();
+        int ks = 0, vs = 0;                  // ring stages and their parities
+        uint32_t kpar = 0, vpar = 0;
+        uint32_t ns = 0, np = 0, parts = 0;  // S and PV tiles issued, parts
+        bool ok = true;
+        PagedItem p;
+        for (uint32_t k = 0; ok && paged_take(a, ring, k, p, false, 930); ++k) {
+            const int nt = p.tv1 - p.tv0;
+            if (nt == 0) continue;
+            ok = mbar_wait_poll(q_ready, parts & 1u, a.ws, 931);
+            ++parts;
+            const int steps_kv = paged_steps(p.kv, BKV), steps_new = paged_steps(p.n, BKV);
+            const int j_kv = (p.kv + BKV - 1) / BKV - 1 - p.tv0;   // last tile of the pages
+            const int j_new = j_kv + (p.n + BKV - 1) / BKV;        // of the new tokens
+            for (int j = 0; j <= nt && ok; ++j) {
+                if (j < nt) {
+                    // S(j) overwrites the buffer of P(j - 2), whose PV was issued before
+                    ok = mbar_wait_poll(&k_full[ks], kpar, a.ws, 932);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sk = sk0 + s * Gm::KVBytes;
-                    const uint32_t d = tmem + Gm::ColS + (it & 1) * BKV;
+                    const uint64_t dk = dk0 + ks * (Gm::KVBytes >> 4);
+                    const uint32_t d = tmem + Gm::ColS + (ns & 1) * BKV;
+                    if (lead) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t bdesc = make_sdesc_sw128(
-                            sk + (kk >> 2) * Gm::KVAtomBytes + (kk & 3) * 32, 16, 1024);
-                        umma_bf16_ts(d, tmem + Gm::ColQ + kk * 8, bdesc, idesc_s, kk != 0);
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma_bf16_ts(d, tmem + Gm::ColQ + kk * 8,
+                                         dk + (((kk >> 2) * Gm::KVAtomBytes + (kk & 3) * 32) >> 4),
+                                         idesc_s, kk != 0);
+                        umma_commit(&k_empty[ks]);
+                        umma_commit(&s_full[ns & 1]);
                     }
-                    umma_commit(&k_empty[s]);
-                    umma_commit(&s_full[it & 1]);
-                    return true;
-                };
-                auto issue_pv = [&](int j) -> bool {
-                    const uint32_t it = it0 + j;
-                    const int s = static_cast<int>(it % NV);
-                    if (!mbar_wait_poll(&p_full[it & 1], (it >> 1) & 1u, a.ws, 933)) return false;
-                    if (!mbar_wait_poll(&v_full[s], (it / NV) & 1u, a.ws, 934)) return false;
+                    ++ns;
+                    if (++ks == NK) {
+                        ks = 0;
+                        kpar ^= 1u;
+                    }
+                }
+                if (j > 0) {
+                    const int jp = j - 1;
+                    ok = mbar_wait_poll(&v_full[vs], vpar, a.ws, 934) &&
+                         mbar_wait_poll(&p_full[np & 1], (np >> 1) & 1u, a.ws, 933);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sv = sv0 + s * Gm::KVBytes;
-                    const uint32_t pa = tmem + Gm::ColS + (it & 1) * BKV;
-                    const int steps = (paged_valid<BKV>(p, p.tv0 + j) + 15) / 16;
-                    for (int kk = 0; kk < steps; ++kk) {
-                        const uint64_t bdesc =
-                            make_sdesc_sw128(sv + kk * 2048, Gm::KVAtomBytes, 1024);
-                        umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, bdesc, idesc_o, (j | kk) != 0);
+                    const int steps = jp == j_kv ? steps_kv : jp == j_new ? steps_new : BKV / 16;
+                    const uint64_t dv = dv0 + vs * (Gm::KVBytes >> 4);
+                    const uint32_t pa = tmem + Gm::ColS + (np & 1) * BKV;
+                    if (lead) {
+                        umma_bf16_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
+                        if (steps == BKV / 16) {
+#pragma unroll
+                            for (int kk = 1; kk < BKV / 16; ++kk)
+                                umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o, 1);
+                        } else {
+                            for (int kk = 1; kk < steps; ++kk)
+                                umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o, 1);
+                        }
+                        umma_commit(&v_empty[vs]);
+                        umma_commit(&pv_done[np & 1]);
+                        if (jp + 1 == nt) umma_commit(o_full);
                     }
-                    umma_commit(&v_empty[s]);
-                    umma_commit(&pv_done[it & 1]);
-                    return true;
-                };
-                if (ok) ok = issue_s(0);
-                for (int j = 1; j < nt && ok; ++j) ok = issue_s(j) && issue_pv(j - 1);
-                if (ok) ok = issue_pv(nt - 1);
-                umma_commit(o_full);
-                it0 += nt;
-                ++parts;
+                    ++np;
+                    if (++vs == NV) {
+                        vs = 0;
+                        vpar ^= 1u;
+                    }
+                }
             }
-            // every UMMA and commit is done before the CTA leaves
-            umma_commit(drained);
-            mbar_wait_poll(drained, 0, a.ws, 935);
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
+        // every UMMA and commit is done before the CTA leaves
+        if (lead) umma_commit(drained);
+        __syncwarp();
+        mbar_wait_poll(drained, 0, a.ws, 935);
     } else {
         // -------------------------------------------------------------- softmax
         const int q = warp & 3;                  // TMEM lane quadrant of the warp

@@ -50,7 +50,7 @@ int check(const PagedArgs &a, int units)
         while (base[b + 1] <= r.begin) ++b;
         paged_locate(paged_seq<ROWS, BKV, I>(a, b), b, base[b], r.begin, r);
         PagedWalk<ROWS, BKV, I> walk;
-        walk.start(a, r);
+        walk.start(a, r, paged_seq<ROWS, BKV, I>(a, b));
         PagedPart p;
         int slot0 = 0, slot1 = 0;
         while (walk.next(a, p)) {
