@@ -10,6 +10,10 @@
 // equal whatever the lengths are, a CTA leaves at most two unfinished parts
 // (one at each end of its stretch), and the parts of an item are those of
 // consecutive CTAs: they are merged in that order, whoever was first.
+//
+// A cut has a price: a part's unfinished rows are written and read again in
+// fp32, by a second kernel.  Where whole items spread almost as evenly, as many
+// to each CTA as to any other, they are left whole.
 #pragma once
 
 #include "dg_kernels.h"
@@ -39,8 +43,17 @@ DG_BOTH T paged_max(T a, T b)
     return a > b ? a : b;
 }
 
-constexpr int kPagedItemKeys = 256;    // an item's fixed cost, in keys
-constexpr int kPagedMinKeys = 512;     // least cost of a CTA's stretch, in keys
+// In keys, by the rows of a query tile (128: one CTA, 256: a pair of them): an
+// item's fixed cost (its queries, pipeline fill, epilogue); what cutting a
+// batch's items costs every unit (parts and merge); the least a unit is given.
+// From sweeps over the chunk and single-token batches of the benchmarks: the
+// pair's epilogue and merge move 256 rows in fp32, about 8 us, 7 key tiles.
+template <int ROWS>
+struct PagedCost {
+    static constexpr int Item = ROWS == 256 ? 768 : 512;
+    static constexpr int Cut = ROWS == 256 ? 1024 : 512;
+    static constexpr int Least = 512;
+};
 
 // I: the integers the line is measured in, 32-bit where the host has seen that
 // no line of these tensors is longer (PagedArgs::small): the walk is on the
@@ -55,8 +68,9 @@ struct PagedSeq {
 
 // Bounds every length by what the tensors hold, so that no later index can
 // leave them; *bad is set when something had to be cut.
+// whole: items are not cut, each costs 1.
 template <int ROWS, int BKV, class I>
-DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool *bad = nullptr)
+DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool whole, bool *bad = nullptr)
 {
     PagedSeq<I> s;
     const int r0 = paged_load(a.q_start + b), r1 = paged_load(a.q_start + b + 1);
@@ -67,10 +81,13 @@ DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool *bad = nullptr)
     if (bad != nullptr) *bad = r0 != s.s0 || r1 != s.s0 + s.n || k0 != s.kv;
     s.mt = (s.n * a.G + ROWS - 1) / ROWS;
     const I G = a.G;
-    s.fixed = G * kPagedItemKeys + 1;
+    s.fixed = G * PagedCost<ROWS>::Item + 1;
     s.cap = 0;
     s.mc = s.mt;
-    if (!a.causal) {
+    if (whole) {
+        s.fixed = 1;
+        s.x0 = s.slope = 0;
+    } else if (!a.causal) {
         s.slope = 0;
         s.x0 = G * (s.kv + (a.has_new ? s.n : 0));
     } else {
@@ -104,18 +121,29 @@ DG_BOTH I paged_div(I x, I y)
 inline bool paged_small(int T, int B, int Hkv, int G, int64_t max_kv)
 {
     const int64_t items = static_cast<int64_t>(Hkv) * (static_cast<int64_t>(T) * G / 128 + B);
-    const int64_t cost = G * (max_kv + 2 * static_cast<int64_t>(T) + kPagedItemKeys + 256) + 1024;
+    const int64_t cost = G * (max_kv + 2 * static_cast<int64_t>(T) + PagedCost<256>::Item + 256) + 1024;
     return cost < (1 << 30) && items < (1 << 30) / cost;
 }
 
 // The length of a unit's stretch (a unit: a CTA, or a pair of them) of a line
 // of cost W.
-template <class I>
-DG_BOTH I paged_step(const PagedArgs &a, I W, int units)
+template <int ROWS, class I>
+DG_BOTH I paged_step(const PagedArgs &a, I W, int units, bool whole)
 {
-    const I least = static_cast<I>(a.G) * kPagedMinKeys;
+    const I least = whole ? 1 : static_cast<I>(a.G) * PagedCost<ROWS>::Least;
     const I n = paged_min<I>(units, paged_max<I>(paged_div(W, least), 1));
     return paged_div<I>(W + n - 1, n);
+}
+
+// Whether a line of cost W, with `items` items of cost `most` at most, is left
+// uncut: when the unit with most items is done before the cuts would pay.
+template <int ROWS, class I>
+DG_BOTH bool paged_whole(const PagedArgs &a, I W, I items, I most, int units)
+{
+    const I rounds = paged_div<I>(items + units - 1, units);
+    // (in 64 bits: rounds x most may be longer than the line)
+    return static_cast<int64_t>(rounds) * most <=
+           static_cast<int64_t>(paged_div<I>(W, units)) + static_cast<int64_t>(a.G) * PagedCost<ROWS>::Cut;
 }
 
 template <class I>
@@ -124,6 +152,7 @@ struct PagedRange {
     I step;
     I item;                  // where the item that `begin` falls in begins
     int b, g, m;             // that item
+    bool whole;
 };
 
 // The item of sequence b (which begins at `base`) that position x falls in.
@@ -155,16 +184,39 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
     const int lane = threadIdx.x & 31;
     PagedRange<I> r{};
     bool bad = false;
-    auto cost_of = [&](int b, bool look) -> I {
+    auto cost_of = [&](int b) -> I {
         if (b >= a.B) return 0;
-        bool cut;
-        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b, &cut);
-        if (look) bad |= cut;
-        return a.Hkv * paged_prefix(s, s.mt);
+        const PagedSeq<I> q = paged_seq<ROWS, BKV, I>(a, b, r.whole);
+        return a.Hkv * paged_prefix(q, q.mt);
     };
-    I mine = cost_of(lane, true), W = mine;
+    // this lane's sequences: cost, items, the dearest item
+    I mine = 0, W = 0, items = 0, most = 0;
 #pragma unroll 4
-    for (int b0 = 32; b0 < a.B; b0 += 32) W += cost_of(b0 + lane, true);
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        if (b0 + lane >= a.B) continue;
+        bool cut;
+        const PagedSeq<I> q = paged_seq<ROWS, BKV, I>(a, b0 + lane, false, &cut);
+        bad |= cut;
+        mine = a.Hkv * paged_prefix(q, q.mt);
+        W += mine;
+        items += a.Hkv * q.mt;
+        if (q.mt > 0) most = max(most, paged_prefix(q, q.mt) - paged_prefix(q, q.mt - 1));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        W += __shfl_xor_sync(0xFFFFFFFFu, W, o);
+        items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    }
+    if (bad && u == 0) report_error(a.ws, DG_ERR_DEVICE, 911);
+    if (W == 0) return r;
+    r.whole = paged_whole<ROWS>(a, W, items, most, units);
+    if (r.whole) {
+        W = items;
+        mine = cost_of(lane);
+    }
+    const I step = paged_step<ROWS>(a, W, units, r.whole), x = u * step;
+    if (x >= W) return r;
     I incl = 0;
     auto scan = [&](I v) {
         incl = v;
@@ -174,23 +226,15 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
             if (lane >= o) incl += p;
         }
     };
-    scan(W);
-    W = __shfl_sync(0xFFFFFFFFu, incl, 31);
-    if (bad && u == 0) report_error(a.ws, DG_ERR_DEVICE, 911);
-    if (W == 0) return r;
-    const I step = paged_step(a, W, units), x = u * step;
-    if (x >= W) return r;
     I base = 0;
     for (int b0 = 0;; b0 += 32) {
-        if (a.B > 32) {
-            if (b0 > 0) mine = cost_of(b0 + lane, false);
-            scan(mine);
-        }
+        if (a.B > 32) mine = cost_of(b0 + lane);
+        scan(mine);
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + incl > x);
         if (past != 0) {
             const int at = __ffs(past) - 1;
             base += __shfl_sync(0xFFFFFFFFu, incl - mine, at);
-            s = paged_seq<ROWS, BKV, I>(a, b0 + at);
+            s = paged_seq<ROWS, BKV, I>(a, b0 + at, r.whole);
             paged_locate(s, b0 + at, base, x, r);
             r.begin = x;
             r.end = min(W, x + step);
@@ -220,6 +264,7 @@ struct PagedWalk {
     PagedSeq<I> s, ahead;   // this sequence, the next one's lengths (already loaded)
     int b, g, m;
     I item, begin, end, step;
+    bool whole;
 
     // first: the lengths of the sequence the stretch begins in
     DG_BOTH void start(const PagedArgs &a, const PagedRange<I> &r, const PagedSeq<I> &first)
@@ -232,8 +277,9 @@ struct PagedWalk {
         g = r.g;
         m = r.m;
         item = r.item;
+        whole = r.whole;
         s = ahead = first;
-        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1);
+        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1, whole);
     }
 
     // The next part; false: the stretch is done.
@@ -268,8 +314,8 @@ struct PagedWalk {
             // part; what rounding leaves over goes with the last tile
             const I tile = static_cast<I>(a.G) * BKV;
             auto cut = [&](I x) -> int {   // tiles before cost x of the item
-                if (x <= s.fixed) return 0;
                 if (x >= cost) return p.nt;
+                if (x <= s.fixed) return 0;
                 return static_cast<int>(paged_min<I>(paged_div<I>(x - s.fixed, tile), p.nt));
             };
             const I from = begin - item, to = end - item;
@@ -292,7 +338,7 @@ struct PagedWalk {
                             break;
                         }
                         s = ahead;
-                        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1);
+                        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1, whole);
                     } while (s.n == 0);
                 }
             }

@@ -6,6 +6,7 @@ one is the part that holds its last key tile.  Lengths outside the tensors
 are cut to them."""
 import os
 import random
+import re
 import subprocess
 
 import pytest
@@ -21,6 +22,7 @@ HARNESS = r"""
 #include <vector>
 #include "dg_paged.cuh"
 using namespace dg;
+static long wholes = 0;
 
 #define FAIL(...) do { printf(__VA_ARGS__); printf("\n"); return 1; } while (0)
 
@@ -28,15 +30,30 @@ template <int ROWS, int BKV, class I>
 int check(const PagedArgs &a, int units)
 {
     std::vector<I> base(a.B + 1, 0);
+    I items_n = 0, most = 0;
+    bool whole = false;
     for (int b = 0; b < a.B; ++b) {
-        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b);
+        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b, false);
         if (s.s0 < 0 || s.n < 0 || s.s0 + s.n > a.T || s.kv < 0 || s.kv > a.max_pages * a.page_size)
             FAIL("lengths not cut");
         base[b + 1] = base[b] + a.Hkv * paged_prefix(s, s.mt);
+        items_n += a.Hkv * s.mt;
+        for (int m = 0; m < s.mt; ++m) {
+            const I c = paged_prefix(s, m + 1) - paged_prefix(s, m);
+            if (c > most) most = c;
+        }
     }
-    const I W = base[a.B];
+    I W = base[a.B];
     if (W == 0) return 0;
-    const I step = paged_step(a, W, units);
+    whole = paged_whole<ROWS>(a, W, items_n, most, units);
+    if (whole) {
+        for (int b = 0; b < a.B; ++b)
+            base[b + 1] = base[b] + a.Hkv * paged_prefix(paged_seq<ROWS, BKV, I>(a, b, true), paged_seq<ROWS, BKV, I>(a, b, true).mt);
+        W = base[a.B];
+        if (W != items_n) FAIL("whole items");
+        ++wholes;
+    }
+    const I step = paged_step<ROWS>(a, W, units, whole);
     const int n = static_cast<int>((W + step - 1) / step);
     if (n > units) FAIL("%d units of %d", n, units);
     // per item: the tiles so far, the unit promised the last part
@@ -48,9 +65,10 @@ int check(const PagedArgs &a, int units)
         r.step = step;
         int b = 0;
         while (base[b + 1] <= r.begin) ++b;
-        paged_locate(paged_seq<ROWS, BKV, I>(a, b), b, base[b], r.begin, r);
+        paged_locate(paged_seq<ROWS, BKV, I>(a, b, whole), b, base[b], r.begin, r);
+        r.whole = whole;
         PagedWalk<ROWS, BKV, I> walk;
-        walk.start(a, r, paged_seq<ROWS, BKV, I>(a, b));
+        walk.start(a, r, paged_seq<ROWS, BKV, I>(a, b, whole));
         PagedPart p;
         int slot0 = 0, slot1 = 0;
         while (walk.next(a, p)) {
@@ -91,10 +109,11 @@ int check(const PagedArgs &a, int units)
             }
             if (p.t1 == p.nt) it->second.first = p.nt;
             if (p.rows < 1 || p.rows > ROWS) FAIL("rows");
+            if (whole && !p.whole) FAIL("a whole item cut");
         }
     }
     for (int b = 0; b < a.B; ++b) {
-        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b);
+        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b, whole);
         for (int g = 0; g < a.Hkv; ++g)
             for (int m = 0; m < s.mt; ++m)
                 if (!items.count(std::make_tuple(b, g, m * ROWS))) FAIL("item (%d %d %d) missing", b, g, m);
@@ -125,7 +144,7 @@ int main()
         if (rc) { printf("case %ld\n", line); return 1; }
         ++line;
     }
-    printf("%ld cases, %ld of them also in 32 bits\n", line, small);
+    printf("%ld cases, %ld of them also in 32 bits, %ld divisions left whole\n", line, small, wholes);
     return 0;
 }
 """
@@ -178,5 +197,6 @@ def test_every_visible_tile_goes_to_one_cta(harness):
     where = int(r.stdout.split()[-1]) if "case " in r.stdout and r.returncode else None
     assert r.returncode == 0, (r.stdout[-300:], cases[where][:12] if where is not None else r.stderr[-300:])
     assert "1500 cases" in r.stdout
-    small = int(r.stdout.split()[2])
-    assert 500 < small < 1500, r.stdout     # both kinds, and lines too long for 32 bits
+    # both integer widths, and both ways of dividing, are among them
+    cases_, small, wholes = (int(x) for x in re.findall(r"(\d+) (?:cases|of them|divisions)", r.stdout))
+    assert 500 < small < 1500 and 200 < wholes < cases_ + small - 200, r.stdout
