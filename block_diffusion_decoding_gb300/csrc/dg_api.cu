@@ -1276,6 +1276,13 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     a.page_table = c->page_table;
     a.kv_len = c->kv_len;
     a.q_start = c->q_start;
+    a.k_pages = c->k;
+    a.v_pages = c->v;
+    a.page_stride = page_stride;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
     a.has_new = k_new != nullptr ? 1 : 0;
     a.causal = causal;
     a.window = window;

@@ -545,6 +545,12 @@ DG_DEVICE uint32_t mapa_shared(uint32_t addr, uint32_t rank)
     return r;
 }
 
+// A word of shared memory given by its cluster address.
+DG_DEVICE void st_cluster(uint32_t cluster_addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
 // Arrive (release at cluster scope) on an mbarrier given by its cluster address.
 DG_DEVICE void mbar_arrive_cluster(uint32_t cluster_addr)
 {

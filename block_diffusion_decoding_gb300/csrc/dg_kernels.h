@@ -305,6 +305,9 @@ struct PagedArgs {
     int T, B, Hq, Hkv, G, D;
     int page_size, box_rows, n_pages, max_pages;
     const int32_t *page_table, *kv_len, *q_start;
+    // the tensors behind the maps, for what is read outside the tiles
+    const uint16_t *k_pages, *v_pages, *k_new, *v_new;
+    int64_t page_stride, k_stride, v_stride;
     int has_new, causal, window;
     int small;           // the division of the work fits 32-bit integers
     int checks;

@@ -612,6 +612,166 @@ DG_DEVICE bool paged_store_row(const PagedArgs &a, uint32_t tmem_row, int c0, bo
     return finite;
 }
 
+// ---------------------------------------------------------------- values hidden from some rows
+// A key that a mask hides from a row gets the weight 0 there, and 0 times an
+// infinity or a NaN in its values would be a NaN in a row that must not know of
+// it.  Only tiles with a key that some row of the query tile sees and another
+// does not (those on a causal or window border) can hold one that matters:
+// where a row sees all or nothing of a key, the products are right as they are.
+// In those tiles the softmax threads look at a key's values each; a key with a
+// value that is not finite has its values set to zero before the product, and
+// the epilogue adds it to the rows that do see it (paged_add_hidden).
+
+// First and last position of a part's rows, and whether some of them see a key
+// of tile tv that others do not.
+struct PagedEdge {
+    int pos0, pos1;
+};
+DG_DEVICE PagedEdge paged_edge(const PagedArgs &a, const PagedItem &p)
+{
+    const int base = a.has_new ? p.kv : p.kv - p.n;
+    return {base + p.frow0 / a.G, base + (p.frow0 + p.rows - 1) / a.G};
+}
+DG_DEVICE bool paged_border(const PagedArgs &a, const PagedEdge &e, int key0, int valid)
+{
+    return a.causal && (key0 + valid - 1 > e.pos0 || (a.window > 0 && key0 <= e.pos1 - a.window));
+}
+
+// The tiles of a part that are not whole and seen by all of its rows, by their
+// index in the part: the first `lo` and those from `hi` on (borders), and the last
+// of the pages and of the new tokens where it is not full (-1: none here).
+struct PagedSpecial {
+    int lo, hi, kv, fresh;
+    DG_DEVICE bool at(int j) const { return j < lo || j >= hi || j == kv || j == fresh; }
+    // Calls f with every such tile before tile `end`.
+    template <class F>
+    DG_DEVICE void each(int end, F f) const
+    {
+        for (int j = 0; j < min(lo, end); ++j) f(j);
+        if (kv >= 0 && kv < end && kv >= lo && kv < hi) f(kv);
+        if (fresh >= 0 && fresh < end && fresh >= lo && fresh < hi) f(fresh);
+        for (int j = max(lo, hi); j < end; ++j) f(j);
+    }
+};
+template <int BKV>
+DG_DEVICE PagedSpecial paged_special(const PagedArgs &a, const PagedItem &p, const PagedEdge &e)
+{
+    const int nt = p.tv1 - p.tv0, nkp = (p.kv + BKV - 1) / BKV;
+    PagedSpecial s;
+    s.lo = 0;
+    s.hi = nt;
+    if (a.causal) {
+        // what is hidden lies within a query tile's positions of either end
+        if (a.window > 0)
+            while (s.lo < nt && paged_key0<BKV>(p, p.tv0 + s.lo) <= e.pos1 - a.window) ++s.lo;
+        while (s.hi > s.lo && paged_key0<BKV>(p, p.tv0 + s.hi - 1) +
+                                      paged_valid<BKV>(p, p.tv0 + s.hi - 1) - 1 > e.pos0)
+            --s.hi;
+    }
+    s.kv = p.kv % BKV ? nkp - 1 - p.tv0 : -1;
+    s.fresh = a.has_new && p.n % BKV ? nkp + (p.n - 1) / BKV - p.tv0 : -1;
+    if (s.kv >= nt) s.kv = -1;
+    if (s.fresh >= nt) s.fresh = -1;
+    return s;
+}
+
+// Whether any of 2 N bf16 values is infinite or NaN: the largest magnitude as
+// integers.
+DG_DEVICE uint32_t magnitude_max(uint32_t m, const uint4 &v)
+{
+    m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+    return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+}
+DG_DEVICE bool not_finite(uint32_t m) { return (m & 0xFFFFu) >= 0x7F80u || (m >> 16) >= 0x7F80u; }
+
+// Thread t's key of a landed V tile: true, and its values zeroed, if one of
+// them is not finite.
+template <class Gm>
+DG_DEVICE bool paged_look(uint8_t *v_tile, int valid, int t)
+{
+    if (t >= valid) return false;
+    uint32_t m = 0;
+#pragma unroll
+    for (int at = 0; at < Gm::NA; ++at) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(v_tile + at * Gm::KVAtomBytes + t * 128);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m = magnitude_max(m, row[(c + t) & 7]);   // (each piece; spread over banks)
+    }
+    if (!not_finite(m)) return false;
+    for (int at = 0; at < Gm::NA; ++at)
+        for (int c = 0; c < 8; ++c)
+            reinterpret_cast<uint4 *>(v_tile + at * Gm::KVAtomBytes + t * 128)[c] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    return true;
+}
+
+// Adds to a row of O (dims [c0, c0 + N), in TMEM, with reference m_ref) the keys
+// that paged_look zeroed and the row sees.  The whole warp, lane = row (live:
+// it exists); nothing here is fast, nor need it be.
+template <int BKV, int N>
+DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t tmem_row, int c0,
+                                bool live, int64_t q_off, int pos, float m_ref)
+{
+    const PagedEdge e = paged_edge(a, p);
+    const int nkp = (p.kv + BKV - 1) / BKV;
+#pragma unroll 1
+    for (int tv = p.tv0; tv < p.tv1; ++tv) {
+        const int valid = paged_valid<BKV>(p, tv), key0 = paged_key0<BKV>(p, tv);
+        if (!paged_border(a, e, key0, valid)) continue;
+#pragma unroll 1
+        for (int c = 0; c < valid; ++c) {
+            int64_t ko, vo;
+            const uint16_t *kb = a.k_new, *vb = a.v_new;
+            if (tv < nkp) {
+                const int page = a.page_table[static_cast<int64_t>(p.b) * a.max_pages +
+                                              (key0 + c) / a.page_size];
+                if (page < 0 || page >= a.n_pages) continue;
+                ko = vo = page * a.page_stride +
+                          static_cast<int64_t>((key0 + c) % a.page_size) * a.Hkv * a.D;
+                kb = a.k_pages;
+                vb = a.v_pages;
+            } else {
+                const int64_t row = p.s0 + (tv - nkp) * BKV + c;
+                ko = row * a.k_stride;
+                vo = row * a.v_stride;
+            }
+            const uint16_t *v = vb + vo + p.g * a.D + c0, *kr = kb + ko + p.g * a.D;
+            uint32_t m = 0;
+#pragma unroll 1
+            for (int d = 0; d < N; d += 8) m = magnitude_max(m, *reinterpret_cast<const uint4 *>(v + d));
+            if (!not_finite(m)) continue;
+            const int key = key0 + c;
+            const bool sees = live && key <= pos && (a.window == 0 || key > pos - a.window);
+            float w = 0.f;
+            if (sees) {
+                float s = 0.f;
+#pragma unroll 1
+                for (int d = 0; d < a.D; ++d)
+                    s = fmaf(__uint_as_float(static_cast<uint32_t>(a.q[q_off + d]) << 16),
+                             __uint_as_float(static_cast<uint32_t>(kr[d]) << 16), s);
+                w = fast_exp2(fmaf(s, a.scale_log2, -m_ref));
+            }
+#pragma unroll 1
+            for (int d = 0; d < N; d += 16) {
+                uint32_t o[16];
+                tmem_ld16_issue(tmem_row + c0 + d, o);
+                tmem_wait_ld16(o);
+                if (sees) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        o[x] = __float_as_uint(
+                            fmaf(w, __uint_as_float(static_cast<uint32_t>(v[d + x]) << 16),
+                                 __uint_as_float(o[x])));
+                }
+                tmem_st16(tmem_row + c0 + d, o);
+                tmem_wait_st();
+            }
+        }
+    }
+}
+
 // The rows of a V tile between its last key and the next multiple of 16, up
 // to which it is multiplied: zero, whatever the page holds there.  By the 128
 // threads of a softmax group (t = 0 .. 127), after the tile has landed.

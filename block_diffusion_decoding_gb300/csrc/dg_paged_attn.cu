@@ -46,7 +46,7 @@ struct PagedGeom {
     static constexpr int ColS = D;
     static constexpr int ColQ = D + 2 * BKV;
     static_assert(ColQ + D / 2 <= 512, "TMEM columns");
-    static_assert(Smem + sizeof(PagedRing) <= 232448, "shared memory");
+    static_assert(Smem + sizeof(PagedRing) + 16 <= 232448, "shared memory");
 };
 
 int paged_attn_smem_bytes(int D)
@@ -63,6 +63,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     constexpr int BKV = Gm::BKV, NK = Gm::NK, NV = Gm::NV;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PagedRing ring;
+    __shared__ uint32_t zeroed[3];           // by part modulo 3: a hidden value was zeroed
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Gm::OffBar);
@@ -96,6 +97,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         mbar_init(q_ready, 4);
         mbar_init(o_full, 1);
         mbar_init(drained, 1);
+        zeroed[0] = zeroed[1] = zeroed[2] = 0;
         paged_ring_init(ring, 3 + 4);    // K, V, UMMA, softmax warps
         fence_barrier_init();
         tma_prefetch_desc(map_k);
@@ -259,16 +261,21 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
             }
             // position of this row, and the keys it sees
             const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
+            const PagedEdge edge = paged_edge(a, p);
+            const int buf = static_cast<int>(parts % 3u);
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j, ++it) {
                 const int sb = static_cast<int>(it & 1u);
                 const int valid = paged_valid<BKV>(p, p.tv0 + j);
                 const int key0 = paged_key0<BKV>(p, p.tv0 + j);
-                if (valid & 15) {
+                const bool border = paged_border(a, edge, key0, valid);
+                if ((valid & 15) != 0 || border) {
                     const int s = static_cast<int>(it % NV);
+                    uint8_t *v_tile = smem + Gm::OffV + s * Gm::KVBytes;
                     ok = mbar_wait_poll(&v_full[s], (it / NV) & 1u, a.ws, 941);
                     if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                    paged_zero_tail<Gm>(smem + Gm::OffV + s * Gm::KVBytes, valid, threadIdx.x - 64);
+                    if (valid & 15) paged_zero_tail<Gm>(v_tile, valid, threadIdx.x - 64);
+                    if (border && paged_look<Gm>(v_tile, valid, threadIdx.x - 64)) zeroed[buf] = 1;
                 }
                 ok = mbar_wait_poll(&s_full[sb], (it >> 1) & 1u, a.ws, 942);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
@@ -358,6 +365,11 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 de.part0 = 1;
             if (p.kind != kPartWhole && live)
                 a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + r] = make_float2(m_ref, l);
+            if (busy && zeroed[buf] != 0)
+                paged_add_hidden<BKV, D>(
+                    a, p, tmem + lane_off + Gm::ColO, 0, live,
+                    tok * a.q_stride + static_cast<int64_t>(head) * D, pos, m_ref);
+            if (threadIdx.x == 64) zeroed[(buf + 2) % 3] = 0;
             const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
             bool badv = a.checks && live && !isfinite(l);
             if (busy)

@@ -22,9 +22,11 @@
 //               CTA's passes on that its query rows are in place;
 //   warps 4-7   softmax of the even tiles, a query row a thread; warps 8-11 of
 //               the odd ones; both load Q rows, and each stores half of O.
-// All copies of a tile complete on the even CTA's barrier.  Only where V needs
-// its tail zeroed (see dg_paged_attn.cu) each CTA's half lands on a barrier
-// of its own, and the arrival of P tells that it has been cleaned.
+// All copies of a tile complete on the even CTA's barrier.  Only where V is
+// looked at before its product (its tail, see dg_paged_attn.cu, and values hidden
+// from some rows, dg_paged.cuh) each CTA's half lands on a barrier of its own,
+// and the arrival of P tells that it has been seen and is clean.  (With every
+// V half landing so the prompt chunks took 7% longer.)
 #include "dg_paged.cuh"
 
 namespace dg {
@@ -67,6 +69,9 @@ struct PairShared {
     uint32_t tmem;
     float m[2][128];                  // running maximum after a tile, by its parity
     float l[2][128];                  // sum of a warpgroup's tiles of a part
+    // by part modulo 3 and half of the dims: a hidden value of that half was
+    // zeroed (told to both CTAs; cleared a part later, two before it is used again)
+    uint32_t zeroed[3][2];
 };
 static_assert(PairGeom<128>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
 static_assert(PairGeom<256>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
@@ -101,7 +106,7 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
     const int box = lane / Atoms, at = lane % Atoms;
     const int key_off = IS_V ? 0 : r * Gm::HK;             // of this CTA's keys in a tile
     const int dim0 = (IS_V ? r * Gm::NA : 0) * 64 + at * 64;
-    uint32_t armed = 0, armed_par = 0, landing = 0;        // by stage; landing: parity of v_land
+    uint32_t armed = 0, armed_par = 0, landing = 0;        // by stage; landing: uses of v_land
     int s = 0;
     uint32_t par = 0;                                      // parity of the stages' use
     bool ok = true;
@@ -115,6 +120,7 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
             const int key = t * Gm::BKV + key_off + lane % per_tile * R;
             return key < p.kv && t < p.tv1 ? __ldg(table + key / a.page_size) : 0;
         };
+        const PagedSpecial special = paged_special<Gm::BKV>(a, p, paged_edge(a, p));
         int32_t pages = fetch(p.tv0), ahead = fetch(p.tv0 + batch);
         int in = 0;
         for (int tv = p.tv0; tv < p.tv1; ++tv, ++in) {
@@ -130,8 +136,8 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
             }
             const int valid = paged_valid<Gm::BKV>(p, tv);
             const bool paged = tv < nkp;
-            const bool own = IS_V && (valid & 15) != 0;    // lands on this CTA's own barrier
             const int mine = paged ? (max(0, min(Keys, valid - key_off)) + R - 1) / R : 0;   // boxes
+            const bool own = IS_V && special.at(tv - p.tv0);   // lands on this CTA's own barrier
             if (lane == 0) {
                 // what both halves bring, or this one alone
                 const uint32_t tile_bytes =
@@ -177,11 +183,9 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
     // CTA leave: the even CTA's barriers tell of both CTAs' copies
     for (int e = 0; e < NS; ++e) {
         if (r == 0 && (armed >> e & 1u)) mbar_wait_poll(&full[e], armed_par >> e & 1u, a.ws, where + 1);
-        if (IS_V) {
-            // `landing` toggles with every use, so its last phase has parity
-            // landing ^ 1 (before any use: the phase before the first, over)
-            mbar_wait_poll(&sh.v_land[e], (landing >> e & 1u) ^ 1u, a.ws, where + 1);
-        }
+        // `landing` toggles with every use, so the last phase has parity
+        // landing ^ 1 (before any use: the phase before the first, over)
+        if (IS_V) mbar_wait_poll(&sh.v_land[e], (landing >> e & 1u) ^ 1u, a.ws, where + 1);
     }
 }
 
@@ -230,6 +234,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         mbar_init(&sh.o_free, 16);
         mbar_init(&sh.drained, 1);
         paged_ring_init(sh.ring, 11);                // K, V, UMMA, softmax warps
+        for (int s = 0; s < 3; ++s) sh.zeroed[s][0] = sh.zeroed[s][1] = 0;
         fence_barrier_init();
         tma_prefetch_desc(map_k);
         tma_prefetch_desc(map_v);
@@ -390,7 +395,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
         const uint32_t to = tmem + lane_off + Gm::ColO;
         uint32_t it = 0, parts = 0;              // tiles and parts before this part
-        uint32_t landing = 0;                    // parity of v_land by stage
+        uint32_t landing = 0;                    // uses of v_land before this part, by stage
         bool ok = true;
         PagedDesc de{-1, 0, 0, 0, 0, 0, {0, 0}};
 
@@ -441,22 +446,12 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
             const bool busy = r * 128 + q * 32 < p.rows;   // the warp has a live row
             float m_ref = -INFINITY, l = 0.f;    // reference of, and sum over, this group's tiles
             const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
-            // the part's tiles whose V has a tail: the last of the pages, the
-            // last of the new tokens
-            const int nkp = (p.kv + BKV - 1) / BKV;
-            int j_kv = (p.kv & 15) ? nkp - 1 - p.tv0 : -1;
-            int j_new = a.has_new && (p.n & 15) ? nkp + (p.n - 1) / BKV - p.tv0 : -1;
-            if (j_kv >= nt) j_kv = -1;
-            if (j_new >= nt) j_new = -1;
+            const PagedSpecial special = paged_special<BKV>(a, p, paged_edge(a, p));
+            const int buf = static_cast<int>(parts % 3u);
             for (int j = static_cast<int>((it ^ wg) & 1u); j < nt; j += 2) {
                 const uint32_t t = it + j;       // tile of the CTA; its parity is wg
-                const int valid = paged_valid<BKV>(p, p.tv0 + j);
                 const int ss = static_cast<int>(t % NS);
-                // first and last visible column
-                const int key0 = paged_key0<BKV>(p, p.tv0 + j);
-                const int c_hi = a.causal ? min(valid - 1, pos - key0) : valid - 1;
-                const int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-                const bool masked = __any_sync(0xFFFFFFFFu, c_hi < BKV - 1 || c_lo > 0);
+                const bool odd = special.at(j);  // else whole, and seen by every row
                 // a wait that runs out is noticed at the tile's end: what is
                 // computed until then reaches no memory but the outputs
                 ok = mbar_wait_poll(&sh.s_full[ss], (t / NS) & 1u, a.ws, 1022);
@@ -468,7 +463,12 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                     for (int c0 = 0; c0 < BKV; c0 += 32)
                         tmem_ld32_nowait(ts + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
                     tmem_wait_ld();
-                    if (masked) {
+                    if (odd) {
+                        // first and last visible column
+                        const int valid = paged_valid<BKV>(p, p.tv0 + j);
+                        const int at = pos - paged_key0<BKV>(p, p.tv0 + j);
+                        const int c_hi = a.causal ? min(valid - 1, at) : valid - 1;
+                        const int c_lo = a.window > 0 ? at - a.window + 1 : 0;
 #pragma unroll
                         for (int c = 0; c < BKV; ++c)
                             if (c > c_hi || c < c_lo) sr[c] = __float_as_uint(-INFINITY);
@@ -539,18 +539,27 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 } else if (lane == 0) {
                     mbar_arrive(&sh.m_full[wg][q]);      // its phases count the tiles
                 }
-                if (valid & 15) {
+                if (odd) {
+                    const int valid = paged_valid<BKV>(p, p.tv0 + j);
                     const int vs = static_cast<int>(t % NV);
-                    // (the same stage may have landed so earlier in the part)
-                    const bool again = j == j_new && j_kv >= 0 && j_kv < j &&
-                                       static_cast<int>((it + j_kv) % NV) == vs;
-                    ok &= mbar_wait_poll(&sh.v_land[vs], (landing >> vs & 1u) ^ (again ? 1u : 0u), a.ws,
-                                         1025);
-                    paged_zero_tail<Gm>(smem + Gm::OffV + vs * Gm::VBytes, valid, threadIdx.x & 127);
+                    uint8_t *v_tile = smem + Gm::OffV + vs * Gm::VBytes;
+                    uint32_t uses = landing >> vs;
+                    special.each(j, [&](int x) { uses += static_cast<int>((it + x) % NV) == vs; });
+                    ok &= mbar_wait_poll(&sh.v_land[vs], uses & 1u, a.ws, 1025);
+                    bool wrote = (valid & 15) != 0;
+                    if (wrote) paged_zero_tail<Gm>(v_tile, valid, threadIdx.x & 127);
+                    if (paged_border(a, paged_edge(a, p), paged_key0<BKV>(p, p.tv0 + j), valid) &&
+                        paged_look<Gm>(v_tile, valid, threadIdx.x & 127)) {
+                        wrote = true;
+                        sh.zeroed[buf][r] = 1;
+                        st_cluster(mapa_shared(smem_u32(&sh.zeroed[buf][r]), r ^ 1), 1);
+                    }
+                    wrote = __any_sync(0xFFFFFFFFu, wrote);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (r == 0) mbar_arrive(&sh.p_full[ss]);
+                        if (!wrote) mbar_arrive_cluster_relaxed(lead_of(&sh.p_full[ss]));
+                        else if (r == 0) mbar_arrive(&sh.p_full[ss]);
                         else mbar_arrive_cluster(lead_of(&sh.p_full[ss]));
                     }
                 } else {
@@ -562,8 +571,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 if (!ok) break;
             }
             if (!ok) break;
-            if (j_kv >= 0) landing ^= 1u << ((it + j_kv) % NV);
-            if (j_new >= 0) landing ^= 1u << ((it + j_new) % NV);
+            special.each(nt, [&](int x) { landing ^= 1u << ((it + x) % NV); });
             // ---------------------------------------------------------- next query, epilogue
             const PagedItem done = p;
             if (nt > 0) {
@@ -614,6 +622,13 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
             l += sh.l[wg ^ 1][rr];
             if (done.kind != kPartWhole && live && wg == 0)
                 a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + row] = make_float2(m_ref, l);
+            // the sums are both groups'; so is the reference, for what is added now
+            if (busy && sh.zeroed[buf][wg] != 0)
+                paged_add_hidden<BKV, Half>(
+                    a, done, to, wg * Half, live,
+                    static_cast<int64_t>(done.s0 + i) * a.q_stride + static_cast<int64_t>(head) * D, pos,
+                    m_ref);
+            if (q == 0 && lane == 0) sh.zeroed[(buf + 2) % 3][wg] = 0;
             const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
             bool badv = a.checks && live && !isfinite(l);
             if (busy)

@@ -260,6 +260,43 @@ def test_many_sequences(kernel):
     check_attn(n, kv, 2, 1, 128, 16, True, 0, False, seed=8)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,page", [(128, 2, 1, 16), (256, 6, 2, 64), (128, 1, 1, 48), (256, 4, 4, 128)])
+@pytest.mark.parametrize("window,fresh", [(0, False), (0, True), (130, True), (70, False)])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(kernel, D, Hq, Hkv, page, window, fresh):
+    """Infinities and NaN in the keys and values of some tokens: the rows that do not see such a token are as if it
+    were not there; the others get what the definition gives (an infinite value: that infinity; a NaN: NaN)."""
+    n, kv = [150, 1, 90, 300], [700, 300, 0, 33]
+    if not fresh:
+        kv = [k + m for k, m in zip(kv, n)]
+    b = Batch(n, kv, kv, Hq, Hkv, D, page, seed=50, strided=True)
+
+    def put(s, key, dim, value, which):
+        """A value into key `key` (of all the sequence's keys) of sequence s."""
+        if key < kv[s]:
+            pages = b.k if which == "k" else b.v
+            pages[b.table[s, key // page], key % page, 0, dim] = value
+        else:
+            (b.kn if which == "k" else b.vn)[int(b.q_start[s]) + key - kv[s], 0, dim] = value
+
+    total = [k + (m if fresh else 0) for k, m in zip(kv, n)]
+    inf = float("inf")
+    put(0, total[0] - 20, 3, inf, "v")              # a late token: hidden from the rows before it
+    put(0, total[0] - 60, D - 1, -inf, "v")
+    put(0, total[0] - 100, 1, NAN, "k")             # a key: its score is NaN where it is seen
+    put(0, total[0] - 200, D // 2, NAN, "v")        # behind the window of the later rows, where there is one
+    put(2, 40, 0, NAN, "v")
+    put(3, total[3] - 1, D // 2 + 1, inf, "v")      # the last token: only its own row sees it
+    put(3, total[3] - 299, 5, -inf, "v")
+    out = run_attn(b, True, window, fresh, kv).cpu().double()
+    want, bound = attention(b, True, window, fresh, kv)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    ends = torch.isinf(want)
+    assert torch.equal(out[ends], want[ends]) and ends.any() and torch.isnan(want).any()
+    fine = torch.isfinite(want)
+    off = (out[fine] - want[fine]).abs() - bound[fine]
+    assert torch.isfinite(out[fine]).all() and (off <= 0).all(), off.max()
+
+
 def test_scores_far_apart(kernel):
     """Scores from -1000 to 1000 in an order that moves the reference maximum late, and large negative ones only."""
     b = Batch([40], [600], [600], 2, 1, 128, 64, seed=10)
