@@ -278,9 +278,9 @@ struct QkvArgs {
     int32_t *kv_len_out;
     WsHeader *ws;
 };
-constexpr int kQkvThreads = 256;
+constexpr int kQkvThreads = 128;
 constexpr int kQkvHeads = 4;         // heads per group of the kernels for many tokens
-constexpr int kQkvSeqSmem = 2048;    // sequences whose first rows are staged in shared memory
+constexpr int kQkvSeqSmem = 512;    // sequences whose first rows are staged in shared memory
 __global__ void qk_norm_rope_kernel_1(QkvArgs a);
 __global__ void qk_norm_rope_kernel_n(QkvArgs a);
 __global__ void paged_append_kernel_1(QkvArgs a);

@@ -109,7 +109,7 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
     uint32_t armed = 0, armed_par = 0, landing = 0;        // by stage; landing: uses of v_land
     int s = 0;
     uint32_t par = 0;                                      // parity of the stages' use
-    bool ok = true;
+    bool ok = true, first = true;
     PagedItem p;
     for (uint32_t k = 0; ok && paged_take(a, sh.ring, k, p, false, where + 2); ++k) {
         const int32_t *table = a.page_table + static_cast<int64_t>(p.b) * a.max_pages;
@@ -130,6 +130,11 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
                 ahead = fetch(tv + batch);
             }
             ok = mbar_wait_poll<false, kPagedLoadSleep>(&empty[s], par ^ 1u, a.ws, where);
+            if (Gm::Dim == 256 && first && (IS_V || tv > p.tv0)) {
+                // the first tiles wait for nothing but the queries and K's first
+                ok &= mbar_wait_poll(&sh.q_ready, 0, a.ws, where);
+                first = false;
+            }
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
