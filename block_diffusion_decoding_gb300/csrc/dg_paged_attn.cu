@@ -11,7 +11,7 @@
 // CTA works through its parts with its K and V rings running ahead across
 // parts, so the memory stream does not stop at an item's end.  Per part:
 //   TMEM        O [128 x D] fp32 | S0, S1 [128 x BKV] fp32 | Q [128 x D] bf16
-//               (the bf16 P of a tile overwrites the S it came from);
+//               (P overwrites the S it came from, as two bf16 halves, see below);
 //   warp 0      TMA: K tiles, one box per page piece, into a 4-stage ring;
 //   warp 6      TMA: V tiles into a 3-stage ring;
 //   warp 7      the walk over the parts;
@@ -20,6 +20,10 @@
 //               with a reference maximum that moves only when a tile exceeds
 //               it by 2^8; then the output row, or the unnormalised fp32 row
 //               with its maximum and sum for paged_merge_kernel.
+// P is multiplied as hi + lo, each bf16: hi = the bf16 below the one that p is cut
+// off to, lo = bf16(p - hi): neither is negative, nor zero where p is not, so that
+// an infinite value stays the infinity it is.  This kernel serves few rows, whose time is the memory's, so the second product is free, and the output
+// is off by little more than its own rounding (with one bf16 P by sqrt 2 of that).
 // A tile whose end is past the last key is loaded, and multiplied with P,
 // only up to the next multiple of 16 keys; the softmax warps zero the V rows
 // between the last key and there, so that whatever bits the page holds behind
@@ -184,13 +188,17 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     const uint32_t pa = tmem + Gm::ColS + (np & 1) * BKV;
                     if (lead) {
                         umma_bf16_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
+                        umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2, dv, idesc_o, 1);
+                        auto both = [&](int kk) {
+                            umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o, 1);
+                            umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2 + kk * 8, dv + kk * 128, idesc_o,
+                                         1);
+                        };
                         if (steps == BKV / 16) {
 #pragma unroll
-                            for (int kk = 1; kk < BKV / 16; ++kk)
-                                umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o, 1);
+                            for (int kk = 1; kk < BKV / 16; ++kk) both(kk);
                         } else {
-                            for (int kk = 1; kk < steps; ++kk)
-                                umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o, 1);
+                            for (int kk = 1; kk < steps; ++kk) both(kk);
                         }
                         umma_commit(&v_empty[vs]);
                         umma_commit(&pv_done[np & 1]);
@@ -314,18 +322,6 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
                     const float mexp = (m_ref == -INFINITY) ? 0.f : m_ref;
                     const float2 nm2 = make_float2(-mexp, -mexp);
-                    float2 acc = make_float2(0.f, 0.f);
-                    uint32_t pk[BKV / 2];
-#pragma unroll
-                    for (int c = 0; c < BKV; c += 2) {
-                        const float2 d2 = fma2(
-                            make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nm2);
-                        const float2 p2 = make_float2(fast_exp2(d2.x), fast_exp2(d2.y));
-                        acc = add2(acc, p2);
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(p2.x, p2.y);
-                        pk[c >> 1] = *reinterpret_cast<const uint32_t *>(&h2);
-                    }
-                    l += acc.x + acc.y;
                     if (__any_sync(0xFFFFFFFFu, rescale)) {
                         // O holds the PVs up to the tile before: wait for the last one
                         ok = mbar_wait_poll(&pv_done[sb ^ 1], ((it - 1) >> 1) & 1u, a.ws, 943);
@@ -343,9 +339,29 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                             tmem_st32(ta, o);
                         }
                     }
+                    float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int c0 = 0; c0 < BKV / 2; c0 += 32)
-                        tmem_st32(ts + c0, *reinterpret_cast<const uint32_t(*)[32]>(&pk[c0]));
+                    for (int c0 = 0; c0 < BKV; c0 += 32) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 d2 = fma2(make_float2(__uint_as_float(sr[c0 + c]),
+                                                               __uint_as_float(sr[c0 + c + 1])),
+                                                   sc2, nm2);
+                            const float2 p2 = make_float2(fast_exp2(d2.x), fast_exp2(d2.y));
+                            acc = add2(acc, p2);
+                            // p down to the bf16 below the one it is cut off to
+                            const int px = __viaddmax_s32(__float_as_int(p2.x), -0x10000, 0) & ~0xFFFF;
+                            const int py = __viaddmax_s32(__float_as_int(p2.y), -0x10000, 0) & ~0xFFFF;
+                            hi[c >> 1] = __byte_perm(px, py, 0x7632);
+                            const float2 r2 = add2(p2, make_float2(-__int_as_float(px), -__int_as_float(py)));
+                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(r2.x, r2.y);
+                            lo[c >> 1] = *reinterpret_cast<const uint32_t *>(&l2);
+                        }
+                        tmem_st16(ts + c0 / 2, hi);
+                        tmem_st16(ts + BKV / 2 + c0 / 2, lo);
+                    }
+                    l += acc.x + acc.y;
                     tmem_wait_st();
                 }
                 tc_fence_before();

@@ -382,7 +382,8 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 PagedItem p;
                 for (uint32_t k = 0; paged_take(a, sh.ring, k, p, false, 1017); ++k) {
                     if (p.tv1 == p.tv0) continue;
-                    bool ok = mbar_wait_poll<false, 100>(&sh.q_ready, parts & 1u, a.ws, 1018);
+                    bool ok = mbar_wait_poll<false, 100>(&sh.q_ready, parts & 1u, a.ws, 1018,
+                                                         kPagedWalkLimitNs);   // a whole part
                     ++parts;
                     if (!__all_sync(0xFFFFFFFFu, ok)) break;
                     if (lane == 0) mbar_arrive_cluster(lead_of(&sh.q_ready));
