@@ -798,6 +798,15 @@ DG_DEVICE void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
         : "memory");
 }
 
+// 32 lanes x 32 bit, 8 consecutive columns per thread.
+DG_DEVICE void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
 DG_DEVICE void tmem_wait_st()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

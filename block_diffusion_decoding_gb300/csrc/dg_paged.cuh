@@ -707,12 +707,48 @@ DG_DEVICE bool paged_look(uint8_t *v_tile, int valid, int t)
     return true;
 }
 
+// Where a part's key is: its offset in the pages or, from tile nkp on, among the
+// new tokens (k, v: the arrays' own strides); false: its page does not exist.
+struct PagedKey {
+    const uint16_t *k, *v;
+};
+DG_DEVICE bool paged_key(const PagedArgs &a, const PagedItem &p, bool fresh, int key, PagedKey &at)
+{
+    if (fresh) {
+        const int64_t row = p.s0 + key - p.kv;
+        at = PagedKey{a.k_new + row * a.k_stride + p.g * a.D, a.v_new + row * a.v_stride + p.g * a.D};
+        return true;
+    }
+    const int page = a.page_table[static_cast<int64_t>(p.b) * a.max_pages + key / a.page_size];
+    if (page < 0 || page >= a.n_pages) return false;
+    const int64_t off = page * a.page_stride +
+                        static_cast<int64_t>(key % a.page_size) * a.Hkv * a.D + p.g * a.D;
+    at = PagedKey{a.k_pages + off, a.v_pages + off};
+    return true;
+}
+// The weight of a key for the row at q_off, whose reference is m_ref.
+DG_DEVICE float paged_weight(const PagedArgs &a, const uint16_t *k, int64_t q_off, float m_ref)
+{
+    float s = 0.f;
+#pragma unroll 1
+    for (int d = 0; d < a.D; ++d)
+        s = fmaf(__uint_as_float(static_cast<uint32_t>(a.q[q_off + d]) << 16),
+                 __uint_as_float(static_cast<uint32_t>(k[d]) << 16), s);
+    return fast_exp2(fmaf(s, a.scale_log2, -m_ref));
+}
+DG_DEVICE bool paged_sees(const PagedArgs &a, int pos, int key)
+{
+    return (!a.causal || key <= pos) && (a.window == 0 || key > pos - a.window);
+}
+
 // Adds to a row of O (dims [c0, c0 + N), in TMEM, with reference m_ref) the keys
-// that paged_look zeroed and the row sees.  The whole warp, lane = row (live:
-// it exists); nothing here is fast, nor need it be.
+// that paged_look zeroed and the row sees, those in columns [first, end) of their
+// tiles.  The whole warp, lane = row (live: it exists); nothing here is fast, nor
+// need it be.
 template <int BKV, int N>
 DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t tmem_row, int c0,
-                                bool live, int64_t q_off, int pos, float m_ref)
+                                bool live, int64_t q_off, int pos, float m_ref, int first = 0,
+                                int end = BKV)
 {
     const PagedEdge e = paged_edge(a, p);
     const int nkp = (p.kv + BKV - 1) / BKV;
@@ -721,38 +757,16 @@ DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t
         const int valid = paged_valid<BKV>(p, tv), key0 = paged_key0<BKV>(p, tv);
         if (!paged_border(a, e, key0, valid)) continue;
 #pragma unroll 1
-        for (int c = 0; c < valid; ++c) {
-            int64_t ko, vo;
-            const uint16_t *kb = a.k_new, *vb = a.v_new;
-            if (tv < nkp) {
-                const int page = a.page_table[static_cast<int64_t>(p.b) * a.max_pages +
-                                              (key0 + c) / a.page_size];
-                if (page < 0 || page >= a.n_pages) continue;
-                ko = vo = page * a.page_stride +
-                          static_cast<int64_t>((key0 + c) % a.page_size) * a.Hkv * a.D;
-                kb = a.k_pages;
-                vb = a.v_pages;
-            } else {
-                const int64_t row = p.s0 + (tv - nkp) * BKV + c;
-                ko = row * a.k_stride;
-                vo = row * a.v_stride;
-            }
-            const uint16_t *v = vb + vo + p.g * a.D + c0, *kr = kb + ko + p.g * a.D;
+        for (int c = first; c < min(valid, end); ++c) {
+            PagedKey at;
+            if (!paged_key(a, p, tv >= nkp, key0 + c, at)) continue;
+            const uint16_t *v = at.v + c0;
             uint32_t m = 0;
 #pragma unroll 1
             for (int d = 0; d < N; d += 8) m = magnitude_max(m, *reinterpret_cast<const uint4 *>(v + d));
             if (!not_finite(m)) continue;
-            const int key = key0 + c;
-            const bool sees = live && key <= pos && (a.window == 0 || key > pos - a.window);
-            float w = 0.f;
-            if (sees) {
-                float s = 0.f;
-#pragma unroll 1
-                for (int d = 0; d < a.D; ++d)
-                    s = fmaf(__uint_as_float(static_cast<uint32_t>(a.q[q_off + d]) << 16),
-                             __uint_as_float(static_cast<uint32_t>(kr[d]) << 16), s);
-                w = fast_exp2(fmaf(s, a.scale_log2, -m_ref));
-            }
+            const bool sees = live && paged_sees(a, pos, key0 + c);
+            const float w = sees ? paged_weight(a, at.k, q_off, m_ref) : 0.f;
 #pragma unroll 1
             for (int d = 0; d < N; d += 16) {
                 uint32_t o[16];
@@ -767,6 +781,35 @@ DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t
                 }
                 tmem_st16(tmem_row + c0 + d, o);
                 tmem_wait_st();
+            }
+        }
+    }
+}
+
+// Sets those of a row's 16 dims from c0 on for which a key that it sees has a
+// value that is not finite to the sum of these products.  (Every lane by itself.)
+template <int BKV>
+DG_DEVICE void paged_sum_infinite(const PagedArgs &a, const PagedItem &p, int c0, int64_t q_off, int pos,
+                                  float m_ref, float (&o)[16])
+{
+    const int nkp = (p.kv + BKV - 1) / BKV;
+    uint32_t found = 0;
+#pragma unroll 1
+    for (int tv = p.tv0; tv < p.tv1; ++tv) {
+        const int valid = paged_valid<BKV>(p, tv), key0 = paged_key0<BKV>(p, tv);
+#pragma unroll 1
+        for (int key = key0; key < key0 + valid; ++key) {
+            PagedKey at;
+            if (!paged_sees(a, pos, key) || !paged_key(a, p, tv >= nkp, key, at)) continue;
+            const uint4 *v = reinterpret_cast<const uint4 *>(at.v + c0);
+            if (!not_finite(magnitude_max(magnitude_max(0, v[0]), v[1]))) continue;
+            const float w = paged_weight(a, at.k, q_off, m_ref);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float x = __uint_as_float(static_cast<uint32_t>(at.v[c0 + e]) << 16);
+                if (isfinite(x)) continue;
+                o[e] = (found >> e & 1u) ? fmaf(w, x, o[e]) : w * x;
+                found |= 1u << e;
             }
         }
     }

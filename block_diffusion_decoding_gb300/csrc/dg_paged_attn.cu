@@ -12,7 +12,7 @@
 // parts, so the memory stream does not stop at an item's end.  Per part:
 //   TMEM        O [128 x D] fp32 | S0, S1 [128 x BKV] fp32 | Q [128 x D] bf16
 //               (P overwrites the S it came from, as two bf16 halves, see below);
-//   warp 0      TMA: K tiles, one box per page piece, into a 4-stage ring;
+//   warp 0      TMA: K tiles, one box per page piece, into a 3-stage ring;
 //   warp 6      TMA: V tiles into a 3-stage ring;
 //   warp 7      the walk over the parts;
 //   warp 1      UMMA issuer: S(0), S(1), PV(0), S(2), PV(1), ...;
@@ -20,6 +20,11 @@
 //               with a reference maximum that moves only when a tile exceeds
 //               it by 2^8; then the output row, or the unnormalised fp32 row
 //               with its maximum and sum for paged_merge_kernel.
+// Items of up to 16 rows (8 at head dim 256), as nearly all single tokens are,
+// would keep one warp busy with 128 columns a row while three idle.  There every
+// warp has a copy of the rows in its own TMEM lanes and takes a quarter of each
+// tile's columns, with a maximum, a sum and an O of its own (its P is zero in the
+// others' columns); at the end they exchange their rows through shared memory.
 // P is multiplied as hi + lo, each bf16: hi = the bf16 below the one that p is cut
 // off to, lo = bf16(p - hi): neither is negative, nor zero where p is not, so that
 // an infinite value stays the infinity it is.  This kernel serves few rows, whose time is the memory's, so the second product is free, and the output
@@ -40,11 +45,17 @@ struct PagedGeom {
     static constexpr int NA = D / 64;                      // 64-dim atoms
     static constexpr int KVBytes = BKV * D * 2;            // 32 KB
     static constexpr int KVAtomBytes = BKV * 128;
-    static constexpr int NK = 4;
+    static constexpr int NK = 3;
     static constexpr int NV = 3;
+    // items of few rows (see below): rows, and the buffer in which the four warps
+    // exchange theirs: 12 x D / 4 dims x FewRows fp32, and (maximum, sum) pairs
+    static constexpr int FewRows = (D == 128) ? 16 : 8;
+    static constexpr int XBytes = 12 * (D / 4) * FewRows * 4;
     static constexpr int OffK = 0;
     static constexpr int OffV = OffK + NK * KVBytes;
-    static constexpr int OffBar = OffV + NV * KVBytes;
+    static constexpr int OffX = OffV + NV * KVBytes;
+    static constexpr int OffXml = OffX + XBytes;
+    static constexpr int OffBar = OffXml + 4 * FewRows * 8;
     static constexpr int Smem = OffBar + 256 + 1024;
     static constexpr int ColO = 0;
     static constexpr int ColS = D;
@@ -56,6 +67,13 @@ struct PagedGeom {
 int paged_attn_smem_bytes(int D)
 {
     return D == 128 ? PagedGeom<128>::Smem : PagedGeom<256>::Smem;
+}
+
+template <int N>
+DG_DEVICE void tmem_put(uint32_t taddr, const uint32_t (&r)[N])
+{
+    if constexpr (N == 16) tmem_st16(taddr, r);
+    else tmem_st8(taddr, r);
 }
 
 template <int D>
@@ -81,7 +99,8 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     uint64_t *q_ready = p_full + 2;
     uint64_t *o_full = q_ready + 1;
     uint64_t *drained = o_full + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+    uint64_t *x_full = drained + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_full + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
@@ -101,6 +120,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         mbar_init(q_ready, 4);
         mbar_init(o_full, 1);
         mbar_init(drained, 1);
+        mbar_init(x_full, 4);
         zeroed[0] = zeroed[1] = zeroed[2] = 0;
         paged_ring_init(ring, 3 + 4);    // K, V, UMMA, softmax warps
         fence_barrier_init();
@@ -220,14 +240,17 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     } else {
         // -------------------------------------------------------------- softmax
         const int q = warp & 3;                  // TMEM lane quadrant of the warp
-        const int r = q * 32 + lane;             // row within the query tile
         const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-        uint32_t it = 0, parts = 0;
+        const uint32_t to = tmem + lane_off + Gm::ColO;
+        constexpr int CH = BKV / 4;              // columns of a warp with few rows
+        uint32_t it = 0, parts = 0, swaps = 0;
         bool ok = true;
         PagedDesc de{-1, 0, 0, 0, 0, 0, {0, 0}};
         PagedItem p;
         for (uint32_t k = 0; ok && paged_take(a, ring, k, p, false, 940); ++k) {
             const int nt = p.tv1 - p.tv0;
+            const bool few = p.rows <= Gm::FewRows;
+            const int r = few ? lane : q * 32 + lane;   // row within the query tile
             const bool live = r < p.rows;
             const int frow = p.frow0 + (live ? r : 0);
             const int i = frow / a.G, hj = frow - i * a.G;
@@ -242,13 +265,13 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 }
                 continue;
             }
-            const bool busy = q * 32 < p.rows;   // the warp has a live row
+            const bool busy = few || q * 32 < p.rows;   // the warp has a live row
             {
                 // Q row into TMEM (rows past the tile's last are zero)
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     a.q + tok * a.q_stride + static_cast<int64_t>(head) * D);
                 if (busy) {
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < D / 2; c0 += 32) {
                         uint32_t w[32];
 #pragma unroll
@@ -272,6 +295,52 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
             const PagedEdge edge = paged_edge(a, p);
             const int buf = static_cast<int>(parts % 3u);
             float m_ref = -INFINITY, l = 0.f;
+
+            // Moves the reference to a tile's maximum if that exceeds it by 2^8;
+            // false: a wait ran out.
+            auto refer = [&](float tmax) -> bool {
+                float factor = 1.f;
+                bool rescale = false;
+                if (m_ref == -INFINITY) {
+                    m_ref = tmax;
+                } else if (tmax > m_ref + 8.f) {
+                    factor = fast_exp2(m_ref - tmax);
+                    l *= factor;
+                    m_ref = tmax;
+                    rescale = true;
+                }
+                if (!__any_sync(0xFFFFFFFFu, rescale)) return true;
+                // O holds the PVs up to the tile before: wait for the last one
+                const bool done = mbar_wait_poll(&pv_done[(it & 1u) ^ 1u], ((it - 1) >> 1) & 1u, a.ws, 943);
+                if (!__all_sync(0xFFFFFFFFu, done)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32_nowait(to + c0, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+                    tmem_st32(to + c0, o);
+                }
+                return true;
+            };
+            // P of a pair of columns as hi + lo; their sum joins acc
+            auto weigh = [&](uint32_t s0, uint32_t s1, float nm, float2 &acc, uint32_t &hi, uint32_t &lo) {
+                const float2 d2 = fma2(make_float2(__uint_as_float(s0), __uint_as_float(s1)),
+                                       make_float2(a.scale_log2, a.scale_log2), make_float2(nm, nm));
+                const float2 p2 = make_float2(fast_exp2(d2.x), fast_exp2(d2.y));
+                acc = add2(acc, p2);
+                // p down to the bf16 below the one it is cut off to
+                const int px = __viaddmax_s32(__float_as_int(p2.x), -0x10000, 0) & ~0xFFFF;
+                const int py = __viaddmax_s32(__float_as_int(p2.y), -0x10000, 0) & ~0xFFFF;
+                hi = __byte_perm(px, py, 0x7632);
+                const float2 r2 = add2(p2, make_float2(-__int_as_float(px), -__int_as_float(py)));
+                const __nv_bfloat162 l2 = __floats2bfloat162_rn(r2.x, r2.y);
+                lo = *reinterpret_cast<const uint32_t *>(&l2);
+            };
+
             for (int j = 0; j < nt; ++j, ++it) {
                 const int sb = static_cast<int>(it & 1u);
                 const int valid = paged_valid<BKV>(p, p.tv0 + j);
@@ -285,19 +354,54 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     if (valid & 15) paged_zero_tail<Gm>(v_tile, valid, threadIdx.x - 64);
                     if (border && paged_look<Gm>(v_tile, valid, threadIdx.x - 64)) zeroed[buf] = 1;
                 }
+                // first and last visible column
+                const int c_hi = a.causal ? min(valid - 1, pos - key0) : valid - 1;
+                const int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
                 ok = mbar_wait_poll(&s_full[sb], (it >> 1) & 1u, a.ws, 942);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
-                if (busy) {
-                    const uint32_t ts = tmem + lane_off + Gm::ColS + sb * BKV;
+                const uint32_t ts = tmem + lane_off + Gm::ColS + sb * BKV;
+                if (few) {
+                    uint32_t sr[CH];
+                    if (CH == 32) {
+                        tmem_ld32_nowait(ts + q * CH, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                        tmem_wait_ld();
+                    } else {
+                        tmem_ld16_issue(ts + q * CH, *reinterpret_cast<uint32_t(*)[16]>(&sr[0]));
+                        tmem_wait_ld16(*reinterpret_cast<uint32_t(*)[16]>(&sr[0]));
+                    }
+                    float rmax = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        if (q * CH + c > c_hi || q * CH + c < c_lo) sr[c] = __float_as_uint(-INFINITY);
+                        rmax = fmaxf(rmax, __uint_as_float(sr[c]));
+                    }
+                    ok = refer(rmax * a.scale_log2);
+                    if (!ok) break;
+                    const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+                    float2 acc = make_float2(0.f, 0.f);
+                    uint32_t hi[CH / 2], lo[CH / 2], none[CH / 2];
+#pragma unroll
+                    for (int c = 0; c < CH / 2; ++c) {
+                        weigh(sr[2 * c], sr[2 * c + 1], nm, acc, hi[c], lo[c]);
+                        none[c] = 0u;
+                    }
+                    l += acc.x + acc.y;
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {   // the other warps' columns: none of this one's
+                        if (h == q) continue;
+                        tmem_put<CH / 2>(ts + h * (CH / 2), none);
+                        tmem_put<CH / 2>(ts + BKV / 2 + h * (CH / 2), none);
+                    }
+                    tmem_put<CH / 2>(ts + q * (CH / 2), hi);
+                    tmem_put<CH / 2>(ts + BKV / 2 + q * (CH / 2), lo);
+                    tmem_wait_st();
+                } else if (busy) {
                     uint32_t sr[BKV];
 #pragma unroll
                     for (int c0 = 0; c0 < BKV; c0 += 32)
                         tmem_ld32_nowait(ts + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
                     tmem_wait_ld();
-                    // first and last visible column
-                    const int c_hi = a.causal ? min(valid - 1, pos - key0) : valid - 1;
-                    const int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
                     if (__any_sync(0xFFFFFFFFu, c_hi < BKV - 1 || c_lo > 0)) {
 #pragma unroll
                         for (int c = 0; c < BKV; ++c)
@@ -308,56 +412,16 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
 #pragma unroll
                     for (int c = 0; c < BKV; c += 2)
                         rmax = max3(rmax, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-                    const float tmax = rmax * a.scale_log2;
-                    float factor = 1.f;
-                    bool rescale = false;
-                    if (m_ref == -INFINITY) {
-                        m_ref = tmax;
-                    } else if (tmax > m_ref + 8.f) {
-                        factor = fast_exp2(m_ref - tmax);
-                        l *= factor;
-                        m_ref = tmax;
-                        rescale = true;
-                    }
-                    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
-                    const float mexp = (m_ref == -INFINITY) ? 0.f : m_ref;
-                    const float2 nm2 = make_float2(-mexp, -mexp);
-                    if (__any_sync(0xFFFFFFFFu, rescale)) {
-                        // O holds the PVs up to the tile before: wait for the last one
-                        ok = mbar_wait_poll(&pv_done[sb ^ 1], ((it - 1) >> 1) & 1u, a.ws, 943);
-                        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            const uint32_t ta = tmem + lane_off + Gm::ColO + c0;
-                            tmem_ld32_nowait(ta, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * factor);
-                            tmem_st32(ta, o);
-                        }
-                    }
+                    ok = refer(rmax * a.scale_log2);
+                    if (!ok) break;
+                    const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
                     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int c0 = 0; c0 < BKV; c0 += 32) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float2 d2 = fma2(make_float2(__uint_as_float(sr[c0 + c]),
-                                                               __uint_as_float(sr[c0 + c + 1])),
-                                                   sc2, nm2);
-                            const float2 p2 = make_float2(fast_exp2(d2.x), fast_exp2(d2.y));
-                            acc = add2(acc, p2);
-                            // p down to the bf16 below the one it is cut off to
-                            const int px = __viaddmax_s32(__float_as_int(p2.x), -0x10000, 0) & ~0xFFFF;
-                            const int py = __viaddmax_s32(__float_as_int(p2.y), -0x10000, 0) & ~0xFFFF;
-                            hi[c >> 1] = __byte_perm(px, py, 0x7632);
-                            const float2 r2 = add2(p2, make_float2(-__int_as_float(px), -__int_as_float(py)));
-                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(r2.x, r2.y);
-                            lo[c >> 1] = *reinterpret_cast<const uint32_t *>(&l2);
-                        }
+                        for (int c = 0; c < 16; ++c)
+                            weigh(sr[c0 + 2 * c], sr[c0 + 2 * c + 1], nm, acc, hi[c], lo[c]);
                         tmem_st16(ts + c0 / 2, hi);
                         tmem_st16(ts + BKV / 2 + c0 / 2, lo);
                     }
@@ -379,19 +443,118 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 de = PagedDesc{p.last, p.rows, p.frow0, p.s0, p.g * a.G, de.part0, {0, 0}};
             else if (p.kind == kPartLater)
                 de.part0 = 1;
-            if (p.kind != kPartWhole && live)
-                a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + r] = make_float2(m_ref, l);
             if (busy && zeroed[buf] != 0)
                 paged_add_hidden<BKV, D>(
-                    a, p, tmem + lane_off + Gm::ColO, 0, live,
-                    tok * a.q_stride + static_cast<int64_t>(head) * D, pos, m_ref);
+                    a, p, to, 0, live, tok * a.q_stride + static_cast<int64_t>(head) * D, pos, m_ref,
+                    few ? q * CH : 0, few ? (q + 1) * CH : BKV);
             if (threadIdx.x == 64) zeroed[(buf + 2) % 3] = 0;
-            const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
-            bool badv = a.checks && live && !isfinite(l);
-            if (busy)
-                badv |= !paged_store_row<D>(a, tmem + lane_off + Gm::ColO, 0, live,
-                                            p.kind == kPartWhole, row_out, inv_l, slot, r);
-            if (badv) report_error(a.ws, DG_ERR_DEVICE, 945);
+            const bool whole = p.kind == kPartWhole;
+            bool bad = false;
+            if (few) {
+                // Each warp has the rows over its own columns: warp q gathers
+                // dims [q D / 4, (q + 1) D / 4) of all four.
+                constexpr int Q4 = D / 4;
+                float4 *x = reinterpret_cast<float4 *>(smem + Gm::OffX);
+                float2 *xml = reinterpret_cast<float2 *>(smem + Gm::OffXml);
+                auto at = [&](int from, int dst, int c) -> float4 * {   // 4 dims c .. of row `lane`
+                    return x + ((from * 3 + dst - (dst > from ? 1 : 0)) * (Q4 / 4) + c / 4) * Gm::FewRows +
+                           lane;
+                };
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {
+                    if (h == q) continue;
+#pragma unroll 1
+                    for (int c = 0; c < Q4; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16_issue(to + h * Q4 + c, o);
+                        tmem_wait_ld16(o);
+                        if (live) {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *at(q, h, c + e) =
+                                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (live) xml[q * Gm::FewRows + lane] = make_float2(m_ref, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_full);
+                ok = mbar_wait_poll(x_full, swaps & 1u, a.ws, 946);
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                ++swaps;
+                float f[4] = {0.f, 0.f, 0.f, 0.f};   // of the four warps' rows
+                m_ref = -INFINITY;
+                l = 0.f;
+                if (live) {
+                    float2 ml[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        ml[h] = xml[h * Gm::FewRows + lane];
+                        if (ml[h].y != 0.f) m_ref = fmaxf(m_ref, ml[h].x);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if (ml[h].y == 0.f) continue;
+                        f[h] = fast_exp2(ml[h].x - m_ref);
+                        l = fmaf(f[h], ml[h].y, l);
+                    }
+                }
+                const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;
+#pragma unroll 1
+                for (int c = 0; c < Q4; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16_issue(to + q * Q4 + c, o);
+                    tmem_wait_ld16(o);
+                    float v[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if (f[h] == 0.f) continue;   // (no key of its columns, or none that counts)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 t = h == q ? make_float4(__uint_as_float(o[e]),
+                                                                  __uint_as_float(o[e + 1]),
+                                                                  __uint_as_float(o[e + 2]),
+                                                                  __uint_as_float(o[e + 3]))
+                                                    : *at(h, q, c + e);
+                            v[e] = fmaf(f[h], t.x, v[e]);
+                            v[e + 1] = fmaf(f[h], t.y, v[e + 1]);
+                            v[e + 2] = fmaf(f[h], t.z, v[e + 2]);
+                            v[e + 3] = fmaf(f[h], t.w, v[e + 3]);
+                        }
+                    }
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) odd |= !isfinite(v[e]);
+                    if (odd && live) {
+                        // an infinite value times the other warps' zeros is NaN
+                        paged_sum_infinite<BKV>(a, p, q * Q4 + c,
+                                                tok * a.q_stride + static_cast<int64_t>(head) * D, pos,
+                                                m_ref, v);
+                        bad = true;
+                    }
+                    if (!live) {
+                    } else if (whole) {
+                        store_bf16x16(row_out + q * Q4 + c, v, inv_l, a.out_wide != 0);
+                    } else {
+                        float4 *dst = part_at(a, slot, r, q * Q4 + c);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            dst[static_cast<int64_t>(e / 4) * a.slot_rows] =
+                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
+                if (busy) bad = !paged_store_row<D>(a, to, 0, live, whole, row_out, inv_l, slot, r);
+            }
+            if (!whole && live && (!few || q == 0))
+                a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + r] = make_float2(m_ref, l);
+            if (a.checks && live && (bad || !isfinite(l))) report_error(a.ws, DG_ERR_DEVICE, 945);
             tc_fence_before();   // O is read before the next part's first PV
         }
         if (threadIdx.x == 64) a.desc[blockIdx.x] = de;

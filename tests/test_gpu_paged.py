@@ -297,6 +297,37 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(kernel, D, 
     assert torch.isfinite(out[fine]).all() and (off <= 0).all(), off.max()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,page", [(128, 2, 1, 16), (256, 8, 1, 64), (128, 16, 1, 48), (256, 4, 4, 128)])
+@pytest.mark.parametrize("window,causal", [(0, True), (0, False), (200, True)])
+def test_infinite_values_that_single_tokens_see(kernel, D, Hq, Hkv, page, window, causal):
+    """Infinities and NaN among the values in every part of a tile: the dims that have them get what the
+    definition gives, the other dims and the other sequences their sums."""
+    kv = [513, 128, 300, 77, 64]
+    b = Batch([1] * 5, kv, kv, Hq, Hkv, D, page, seed=57, strided=True)
+    at = {}
+
+    def put(s, key, dim, value):
+        assert b.v[b.table[s, key // page], key % page, 0, dim].isfinite() and (s, dim) not in at
+        b.v[b.table[s, key // page], key % page, 0, dim] = value
+        at[s, dim] = value
+
+    inf = float("inf")
+    for j, key in enumerate((512, 500, 470, 440, 410)):       # each quarter of a tile, and its last, short one
+        put(0, key, 7 + 17 * j, inf if j & 1 else -inf)
+    put(0, 400, 127, NAN)
+    put(0, 3, 126, inf)                                       # behind the window, where there is one
+    put(2, 299, 0, -inf)
+    put(3, 0, D - 1, inf)
+    put(3, 76, D - 2, NAN)
+    out = run_attn(b, causal, window, False, kv).cpu().double()
+    want, bound = attention(b, causal, window, False, kv)
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.isnan(want).any()
+    ends = torch.isinf(want)
+    assert torch.equal(out[ends], want[ends]) and ends.any()
+    fine = torch.isfinite(want)
+    assert torch.isfinite(out[fine]).all() and ((out[fine] - want[fine]).abs() <= bound[fine]).all()
+
+
 def test_scores_far_apart(kernel):
     """Scores from -1000 to 1000 in an order that moves the reference maximum late, and large negative ones only."""
     b = Batch([40], [600], [600], 2, 1, 128, 64, seed=10)
