@@ -64,6 +64,22 @@ struct PagedSeq {
     int mt;             // query tiles of a kv head
     int mc;             // tiles whose key count still grows with the tile index
     I x0, slope, cap, fixed;
+
+    // Items that are not cut cost 1 each.
+    DG_BOTH void uncut()
+    {
+        mc = mt;
+        fixed = 1;
+        x0 = slope = cap = 0;
+    }
+#ifdef __CUDACC__
+    // Lane `at`'s.
+    DG_DEVICE PagedSeq from(int at) const
+    {
+        auto get = [&](auto v) { return __shfl_sync(0xFFFFFFFFu, v, at); };
+        return PagedSeq{get(s0), get(n), get(kv), get(mt), get(mc), get(x0), get(slope), get(cap), get(fixed)};
+    }
+#endif
 };
 
 // Bounds every length by what the tensors hold, so that no later index can
@@ -85,8 +101,7 @@ DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool whole, bool *bad =
     s.cap = 0;
     s.mc = s.mt;
     if (whole) {
-        s.fixed = 1;
-        s.x0 = s.slope = 0;
+        s.uncut();
     } else if (!a.causal) {
         s.slope = 0;
         s.x0 = G * (s.kv + (a.has_new ? s.n : 0));
@@ -191,11 +206,12 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
     };
     // this lane's sequences: cost, items, the dearest item
     I mine = 0, W = 0, items = 0, most = 0;
-#pragma unroll 4
+    PagedSeq<I> q{};
+#pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         if (b0 + lane >= a.B) continue;
         bool cut;
-        const PagedSeq<I> q = paged_seq<ROWS, BKV, I>(a, b0 + lane, false, &cut);
+        q = paged_seq<ROWS, BKV, I>(a, b0 + lane, false, &cut);
         bad |= cut;
         mine = a.Hkv * paged_prefix(q, q.mt);
         W += mine;
@@ -213,7 +229,8 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
     r.whole = paged_whole<ROWS>(a, W, items, most, units);
     if (r.whole) {
         W = items;
-        mine = cost_of(lane);
+        q.uncut();
+        mine = a.Hkv * q.mt;   // (a batch of up to 32)
     }
     const I step = paged_step<ROWS>(a, W, units, r.whole), x = u * step;
     if (x >= W) return r;
@@ -234,7 +251,8 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
         if (past != 0) {
             const int at = __ffs(past) - 1;
             base += __shfl_sync(0xFFFFFFFFu, incl - mine, at);
-            s = paged_seq<ROWS, BKV, I>(a, b0 + at, r.whole);
+            if (a.B > 32) q = paged_seq<ROWS, BKV, I>(a, min(b0 + lane, a.B - 1), r.whole);
+            s = q.from(at);
             paged_locate(s, b0 + at, base, x, r);
             r.begin = x;
             r.end = min(W, x + step);
@@ -786,13 +804,17 @@ DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t
     }
 }
 
-// Sets those of a row's 16 dims from c0 on for which a key that it sees has a
-// value that is not finite to the sum of these products.  (Every lane by itself.)
+// Sets those of 4 dims (from c0 on) of row `row` of the query tile for which a key
+// that the row sees has a value that is not finite to the sum of these products.
+// Every lane by itself.
 template <int BKV>
-DG_DEVICE void paged_sum_infinite(const PagedArgs &a, const PagedItem &p, int c0, int64_t q_off, int pos,
-                                  float m_ref, float (&o)[16])
+DG_DEVICE void paged_sum_infinite(const PagedArgs &a, const PagedItem &p, int row, int c0,
+                                                float m_ref, float (&o)[4])
 {
-    const int nkp = (p.kv + BKV - 1) / BKV;
+    const int nkp = (p.kv + BKV - 1) / BKV, frow = p.frow0 + row, i = frow / a.G;
+    const int64_t q_off = (p.s0 + i) * a.q_stride +
+                          static_cast<int64_t>(p.g * a.G + frow - i * a.G) * a.D;
+    const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
     uint32_t found = 0;
 #pragma unroll 1
     for (int tv = p.tv0; tv < p.tv1; ++tv) {
@@ -801,11 +823,11 @@ DG_DEVICE void paged_sum_infinite(const PagedArgs &a, const PagedItem &p, int c0
         for (int key = key0; key < key0 + valid; ++key) {
             PagedKey at;
             if (!paged_sees(a, pos, key) || !paged_key(a, p, tv >= nkp, key, at)) continue;
-            const uint4 *v = reinterpret_cast<const uint4 *>(at.v + c0);
-            if (!not_finite(magnitude_max(magnitude_max(0, v[0]), v[1]))) continue;
+            const uint2 v = *reinterpret_cast<const uint2 *>(at.v + c0);
+            if (!not_finite(magnitude_max(0, make_uint4(v.x, v.y, 0, 0)))) continue;
             const float w = paged_weight(a, at.k, q_off, m_ref);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 const float x = __uint_as_float(static_cast<uint32_t>(at.v[c0 + e]) << 16);
                 if (isfinite(x)) continue;
                 o[e] = (found >> e & 1u) ? fmaf(w, x, o[e]) : w * x;

@@ -48,9 +48,9 @@ struct PagedGeom {
     static constexpr int NK = 3;
     static constexpr int NV = 3;
     // items of few rows (see below): rows, and the buffer in which the four warps
-    // exchange theirs: 12 x D / 4 dims x FewRows fp32, and (maximum, sum) pairs
+    // exchange theirs: [warp][row][D] fp32, and (maximum, sum) pairs
     static constexpr int FewRows = (D == 128) ? 16 : 8;
-    static constexpr int XBytes = 12 * (D / 4) * FewRows * 4;
+    static constexpr int XBytes = 4 * FewRows * D * 4;
     static constexpr int OffK = 0;
     static constexpr int OffV = OffK + NK * KVBytes;
     static constexpr int OffX = OffV + NV * KVBytes;
@@ -452,31 +452,26 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
             bool bad = false;
             if (few) {
                 // Each warp has the rows over its own columns: warp q gathers
-                // dims [q D / 4, (q + 1) D / 4) of all four.
-                constexpr int Q4 = D / 4;
+                // dims [q D / 4, (q + 1) D / 4) of all four, 4 dims a lane.
+                constexpr int P4 = D / 16;       // pieces of 4 dims that a warp gathers of a row
                 float4 *x = reinterpret_cast<float4 *>(smem + Gm::OffX);
                 float2 *xml = reinterpret_cast<float2 *>(smem + Gm::OffXml);
-                auto at = [&](int from, int dst, int c) -> float4 * {   // 4 dims c .. of row `lane`
-                    return x + ((from * 3 + dst - (dst > from ? 1 : 0)) * (Q4 / 4) + c / 4) * Gm::FewRows +
-                           lane;
+                auto at = [&](int from, int row, int piece) -> float4 * {   // (spread over the banks)
+                    return x + (from * Gm::FewRows + row) * (D / 4) + (piece ^ (row & 7));
                 };
 #pragma unroll 1
-                for (int h = 0; h < 4; ++h) {
-                    if (h == q) continue;
-#pragma unroll 1
-                    for (int c = 0; c < Q4; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16_issue(to + h * Q4 + c, o);
-                        tmem_wait_ld16(o);
-                        if (live) {
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32_nowait(to + c, o);
+                    tmem_wait_ld();
+                    if (live) {
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4)
-                                *at(q, h, c + e) =
-                                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                        }
-                        __syncwarp();
+                        for (int e = 0; e < 32; e += 4)
+                            *at(q, lane, (c + e) / 4) =
+                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                     }
+                    __syncwarp();
                 }
                 if (live) xml[q * Gm::FewRows + lane] = make_float2(m_ref, l);
                 __syncwarp();
@@ -484,77 +479,61 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 ok = mbar_wait_poll(x_full, swaps & 1u, a.ws, 946);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 ++swaps;
-                float f[4] = {0.f, 0.f, 0.f, 0.f};   // of the four warps' rows
-                m_ref = -INFINITY;
-                l = 0.f;
-                if (live) {
-                    float2 ml[4];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        ml[h] = xml[h * Gm::FewRows + lane];
-                        if (ml[h].y != 0.f) m_ref = fmaxf(m_ref, ml[h].x);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        if (ml[h].y == 0.f) continue;
-                        f[h] = fast_exp2(ml[h].x - m_ref);
-                        l = fmaf(f[h], ml[h].y, l);
-                    }
-                }
-                const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;
+                const int64_t first = tok * a.out_stride + static_cast<int64_t>(head) * D;
 #pragma unroll 1
-                for (int c = 0; c < Q4; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16_issue(to + q * Q4 + c, o);
-                    tmem_wait_ld16(o);
-                    float v[16];
+                for (int row0 = 0; row0 < p.rows; row0 += 32 / P4) {
+                    const int row = row0 + lane / P4, piece = q * P4 + lane % P4;
+                    const int64_t row_first = __shfl_sync(0xFFFFFFFFu, first, row & 31);
+                    if (row < p.rows) {
+                        float2 ml[4];
+                        float m = -INFINITY, sum = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        if (f[h] == 0.f) continue;   // (no key of its columns, or none that counts)
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 t = h == q ? make_float4(__uint_as_float(o[e]),
-                                                                  __uint_as_float(o[e + 1]),
-                                                                  __uint_as_float(o[e + 2]),
-                                                                  __uint_as_float(o[e + 3]))
-                                                    : *at(h, q, c + e);
-                            v[e] = fmaf(f[h], t.x, v[e]);
-                            v[e + 1] = fmaf(f[h], t.y, v[e + 1]);
-                            v[e + 2] = fmaf(f[h], t.z, v[e + 2]);
-                            v[e + 3] = fmaf(f[h], t.w, v[e + 3]);
+                        for (int h = 0; h < 4; ++h) {
+                            ml[h] = xml[h * Gm::FewRows + row];
+                            if (ml[h].y != 0.f) m = fmaxf(m, ml[h].x);
                         }
-                    }
-                    bool odd = false;
+                        float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) odd |= !isfinite(v[e]);
-                    if (odd && live) {
-                        // an infinite value times the other warps' zeros is NaN
-                        paged_sum_infinite<BKV>(a, p, q * Q4 + c,
-                                                tok * a.q_stride + static_cast<int64_t>(head) * D, pos,
-                                                m_ref, v);
-                        bad = true;
-                    }
-                    if (!live) {
-                    } else if (whole) {
-                        store_bf16x16(row_out + q * Q4 + c, v, inv_l, a.out_wide != 0);
-                    } else {
-                        float4 *dst = part_at(a, slot, r, q * Q4 + c);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            dst[static_cast<int64_t>(e / 4) * a.slot_rows] =
-                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        for (int h = 0; h < 4; ++h) {
+                            if (ml[h].y == 0.f) continue;   // no key of its columns
+                            const float f = fast_exp2(ml[h].x - m);
+                            const float4 t = *at(h, row, piece);
+                            sum = fmaf(f, ml[h].y, sum);
+                            if (f == 0.f) continue;         // (nor one that counts)
+                            v[0] = fmaf(f, t.x, v[0]);
+                            v[1] = fmaf(f, t.y, v[1]);
+                            v[2] = fmaf(f, t.z, v[2]);
+                            v[3] = fmaf(f, t.w, v[3]);
+                        }
+                        if (!(fabsf(v[0]) + fabsf(v[1]) + fabsf(v[2]) + fabsf(v[3]) < INFINITY)) {
+                            // an infinite value times the other warps' zeros is NaN
+                            paged_sum_infinite<BKV>(a, p, row, piece * 4, m, v);
+                            bad = true;
+                        }
+                        if (whole) {
+                            const float inv = (sum > 0.f) ? 1.f / sum : sum == 0.f ? 0.f : sum;
+                            const __nv_bfloat162 lo2 = __floats2bfloat162_rn(v[0] * inv, v[1] * inv);
+                            const __nv_bfloat162 hi2 = __floats2bfloat162_rn(v[2] * inv, v[3] * inv);
+                            *reinterpret_cast<uint2 *>(a.out + row_first + piece * 4) =
+                                make_uint2(*reinterpret_cast<const uint32_t *>(&lo2),
+                                           *reinterpret_cast<const uint32_t *>(&hi2));
+                        } else {
+                            *part_at(a, slot, row, piece * 4) = make_float4(v[0], v[1], v[2], v[3]);
+                            if (piece == 0)
+                                a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + row] = make_float2(m, sum);
+                        }
+                        bad |= !isfinite(sum);
                     }
                     __syncwarp();
                 }
+                if (a.checks && bad) report_error(a.ws, DG_ERR_DEVICE, 945);
             } else {
                 const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
                 if (busy) bad = !paged_store_row<D>(a, to, 0, live, whole, row_out, inv_l, slot, r);
+                if (!whole && live)
+                    a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + r] = make_float2(m_ref, l);
+                if (a.checks && live && (bad || !isfinite(l))) report_error(a.ws, DG_ERR_DEVICE, 945);
             }
-            if (!whole && live && (!few || q == 0))
-                a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + r] = make_float2(m_ref, l);
-            if (a.checks && live && (bad || !isfinite(l))) report_error(a.ws, DG_ERR_DEVICE, 945);
             tc_fence_before();   // O is read before the next part's first PV
         }
         if (threadIdx.x == 64) a.desc[blockIdx.x] = de;
