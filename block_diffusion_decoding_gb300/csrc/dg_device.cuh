@@ -174,41 +174,6 @@ DG_DEVICE bool mbar_wait(uint64_t *bar, uint32_t parity, WsHeader *ws, int where
     return mbar_wait_limit(bar, parity, ws, where, kWaitLimitNs);
 }
 
-// The same wait with the clock read only once it has lasted: a wait that a few
-// polls satisfy, as most in a running pipeline are, pays for those alone.
-// CLUSTER: acquires what the other CTA of a pair released.  SLEEP: nanoseconds
-// between polls, for roles with time to spare whose polls would take issue
-// slots from the others of their SM.
-template <bool CLUSTER = false, int SLEEP = 0>
-DG_DEVICE bool mbar_wait_poll(uint64_t *bar, uint32_t parity, WsHeader *ws, int where,
-                              uint64_t limit_ns = kWaitLimitNs)
-{
-    uint64_t t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        uint32_t ok;
-        if (CLUSTER)
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(ok)
-                : "r"(smem_u32(bar)), "r"(parity)
-                : "memory");
-        else
-            ok = mbar_try_wait(bar, parity) ? 1u : 0u;
-        if (ok) return true;
-        if (SLEEP > 0) __nanosleep(SLEEP);
-        if ((it & 63u) == 0) {
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > limit_ns) {
-                report_error(ws, DG_ERR_TIMEOUT, where);
-                return false;
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor), completion on an mbarrier (complete_tx)
 // ------------------------------------------------------------------------
@@ -310,13 +275,6 @@ DG_DEVICE uint64_t policy_evict_first()
 {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-
-DG_DEVICE uint64_t policy_evict_normal()
-{
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 
@@ -474,22 +432,6 @@ DG_DEVICE void umma_commit_pair(uint64_t *bar, uint16_t cta_mask)
 }
 
 // ------------------------------------------------------------------------
-// Registers per thread of a warpgroup (4 warps, all of which execute it):
-// raised from, or given back to, those the block was launched with.
-// ------------------------------------------------------------------------
-template <int N>
-DG_DEVICE void reg_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-template <int N>
-DG_DEVICE void reg_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// ------------------------------------------------------------------------
 // Paired fp32 arithmetic (two lanes of a 64-bit register pair per
 // instruction) and a three-input maximum.
 // ------------------------------------------------------------------------
@@ -528,12 +470,6 @@ DG_DEVICE float max3(float a, float b, float c)
     return d;
 }
 
-// __syncthreads() that the warps of a block may reach in different places.
-DG_DEVICE void cta_sync()
-{
-    asm volatile("bar.sync 0;" ::: "memory");
-}
-
 // ------------------------------------------------------------------------
 // Thread-block clusters
 // ------------------------------------------------------------------------
@@ -543,12 +479,6 @@ DG_DEVICE uint32_t mapa_shared(uint32_t addr, uint32_t rank)
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
-}
-
-// A word of shared memory given by its cluster address.
-DG_DEVICE void st_cluster(uint32_t cluster_addr, uint32_t v)
-{
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
 // Arrive (release at cluster scope) on an mbarrier given by its cluster address.
@@ -667,21 +597,6 @@ DG_DEVICE void cluster_sync_all()
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// True in one lane of a converged warp, the same one every time.  A role whose
-// whole warp runs its loop and only issues under this keeps its operands
-// uniform over the warp, which is how the tensor instructions take them; a
-// role run by one lane alone pays a move and a wait for each operand.
-DG_DEVICE bool elect_lane()
-{
-    uint32_t e;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xFFFFFFFF;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(e));
-    return e != 0;
-}
-
 // Instruction descriptor, kind::f16: D fp32, A/B bf16, A K-major,
 // B K-major (b_mn_major = 0) or MN-major (1), shape M x N.
 __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, int b_mn_major)
@@ -795,15 +710,6 @@ DG_DEVICE void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
         "r"(r[15])
-        : "memory");
-}
-
-// 32 lanes x 32 bit, 8 consecutive columns per thread.
-DG_DEVICE void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
 

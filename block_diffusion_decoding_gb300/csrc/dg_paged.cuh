@@ -16,7 +16,8 @@
 // to each CTA as to any other, they are left whole.
 #pragma once
 
-#include "dg_kernels.h"
+#include "dg_paged_device.cuh"
+#include "dg_paged_kernels.h"
 
 namespace dg {
 

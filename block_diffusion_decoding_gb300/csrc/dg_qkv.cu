@@ -21,7 +21,7 @@
 //             fast sine and cosine (absolute error about 2^-21, far below the
 //             half step 2^-8 of the bf16 result).
 // Everything is fp32 until the one rounding to bf16 at the store.
-#include "dg_kernels.h"
+#include "dg_paged_kernels.h"
 
 namespace dg {
 
