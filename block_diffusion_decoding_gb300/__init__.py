@@ -257,28 +257,47 @@ def _refuse(what: str, why: str):
     raise e
 
 
-def _rows(t: torch.Tensor, heads: int, D: int, what: str, T: Optional[int] = None) -> int:
-    """The row stride of a bf16 tensor [T, heads, D] on the current device whose rows are dense."""
-    if t.dtype is not torch.bfloat16 or not t.is_cuda:
-        _refuse(what, "a bf16 CUDA tensor is wanted")
+def _rows(t: torch.Tensor, heads: int, D: int, what: str, device: int, T: Optional[int] = None) -> int:
+    """The row stride of a bf16 tensor [T, heads, D] on the device whose rows are dense and apart."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != device:
+        _refuse(what, "a bf16 tensor on the current device is wanted")
+    if t.dim() != 3:
+        _refuse(what, "a tensor [T, heads, D] is wanted")
     n, h, d = t.shape
     if h != heads or d != D or (T is not None and n != T):
         _refuse(what, "shape %s where [%s, %d, %d] is wanted"
                 % (tuple(t.shape), "T" if T is None else T, heads, D))
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
+    if n > 0 and ((s2 != 1 and D > 1) or (s1 != D and heads > 1)):
         _refuse(what, "the rows of a tensor are not dense")
+    if n > 1 and s0 < heads * D:   # (an expanded one: 0 means dense to the library)
+        _refuse(what, "the rows of a tensor overlap")
     return s0 if n > 1 else 0
 
 
-def _ints(t: torch.Tensor, n: int, what: str):
-    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        _refuse(what, "a dense int32 CUDA tensor of %d is wanted" % n)
+def _ints(t: torch.Tensor, n: int, what: str, device: int):
+    if (t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous()
+            or t.get_device() != device):
+        _refuse(what, "a dense int32 tensor of %d on the others' device is wanted" % n)
 
 
-def _on_current(device: torch.device, what: str):
-    if device.index != torch._C._cuda_getDevice():
-        _refuse(what, "the tensors are on %s, which is not the current device" % device)
+def _on_current(t: torch.Tensor, what: str) -> int:
+    """The current device, which the tensor has to be on."""
+    device = torch._C._cuda_getDevice() if t.is_cuda else -1
+    if device < 0 or t.get_device() != device:
+        _refuse(what, "the tensors are on %s, which is not the current device" % t.device)
+    return device
+
+
+def _heads_on(p: HeadParams, what: str, device: int):
+    if p.device is not None and p.device != device:
+        _refuse(what, "rope_steps and the norm weights are not on the current device")
+
+
+def _scratch(t: torch.Tensor, what: str, device: int) -> int:
+    if t.get_device() != device or not t.is_contiguous():
+        _refuse(what, "a dense workspace on the current device is wanted")
+    return t.numel()
 
 
 def rope_steps(inv_freq, device="cuda") -> torch.Tensor:
@@ -305,6 +324,10 @@ def head_params(Hq, Hkv, D, rope_steps=None, interleaved=False, q_weight=None, k
                    1 if interleaved else 0, eps, weight_offset, _p(rope_steps), _p(q_weight),
                    _p(k_weight))
     p.tensors = (rope_steps, q_weight, k_weight)
+    devices = {t.get_device() for t in p.tensors if t is not None}
+    if len(devices) > 1:
+        _refuse("head_params", "the tensors are on different devices")
+    p.device = devices.pop() if devices else None
     p.ref = ctypes.byref(p)
     return p
 
@@ -317,21 +340,26 @@ class PagedCache:
 
     def __init__(self, k, v, page_table, kv_len, q_start):
         what = "PagedCache"
-        n_pages, page_size, Hkv, D = k.shape
         if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or not k.is_cuda:
             _refuse(what, "bf16 CUDA tensors are wanted")
+        if k.dim() != 4:
+            _refuse(what, "k and v are [n_pages, page_size, Hkv, D]")
+        n_pages, page_size, Hkv, D = k.shape
         if v.shape != k.shape or v.stride() != k.stride():
             _refuse(what, "k and v differ in shape or strides")
         if k.stride()[1:] != (Hkv * D, D, 1):
             _refuse(what, "the tokens of a page are not dense")
+        if n_pages > 1 and k.stride(0) < page_size * Hkv * D:
+            _refuse(what, "the pages overlap")
         if page_table.dim() != 2:
             _refuse(what, "page_table is [B, max_pages]")
         B, max_pages = page_table.shape
-        _ints(page_table, B * max_pages, what)
-        _ints(kv_len, B, what)
-        _ints(q_start, B + 1, what)
-        if len({t.device for t in (k, v, page_table, kv_len, q_start)}) != 1:
-            _refuse(what, "the tensors are on different devices")
+        device = k.get_device()
+        if v.get_device() != device:
+            _refuse(what, "k and v are on different devices")
+        _ints(page_table, B * max_pages, what, device)
+        _ints(kv_len, B, what, device)
+        _ints(q_start, B + 1, what, device)
         self.k, self.v, self.page_table, self.kv_len, self.q_start = (k, v, page_table, kv_len,
                                                                       q_start)
         self.device, self.B, self.Hkv, self.D = k.device, B, Hkv, D
@@ -346,15 +374,18 @@ def qk_norm_rope(q, k, q_out, k_out, positions, p: HeadParams, stream=None):
     strided; either pair may be None), positions [T] int32 (None without rotation)."""
     what = "dg_qk_norm_rope"
     x = q if q is not None else k
+    if x is None:
+        _refuse(what, "neither q nor k is given")
     T = x.shape[0]
-    _on_current(x.device, what)
+    dev = _on_current(x, what)
+    _heads_on(p, what, dev)
     if positions is not None:
-        _ints(positions, T, what)
+        _ints(positions, T, what, dev)
     rc = _lib().dg_qk_norm_rope(
-        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, T),
-        _p(k), 0 if k is None else _rows(k, p.Hkv, p.D, what, T),
-        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, T),
-        _p(k_out), 0 if k_out is None else _rows(k_out, p.Hkv, p.D, what, T),
+        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, dev, T),
+        _p(k), 0 if k is None else _rows(k, p.Hkv, p.D, what, dev, T),
+        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, dev, T),
+        _p(k_out), 0 if k_out is None else _rows(k_out, p.Hkv, p.D, what, dev, T),
         _p(positions), T, p.ref, _stream(stream))
     _check(rc, what)
 
@@ -370,17 +401,18 @@ def paged_append(k, v, cache: PagedCache, p: HeadParams, workspace, q=None, q_ou
     kv_len_out [B] int32 receives the new lengths."""
     what = "dg_paged_append"
     T = k.shape[0]
-    _on_current(cache.device, what)
+    dev = _on_current(cache.k, what)
+    _heads_on(p, what, dev)
     if positions is not None:
-        _ints(positions, T, what)
+        _ints(positions, T, what, dev)
     if kv_len_out is not None:
-        _ints(kv_len_out, cache.B, what)
+        _ints(kv_len_out, cache.B, what, dev)
     rc = _lib().dg_paged_append(
-        _p(k), _rows(k, p.Hkv, p.D, what), _p(v), _rows(v, p.Hkv, p.D, what, T),
-        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, T),
-        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, T),
-        _p(positions), T, p.ref, cache.ref, _p(kv_len_out), _p(workspace), workspace.numel(),
-        _stream(stream))
+        _p(k), _rows(k, p.Hkv, p.D, what, dev), _p(v), _rows(v, p.Hkv, p.D, what, dev, T),
+        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, dev, T),
+        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, dev, T),
+        _p(positions), T, p.ref, cache.ref, _p(kv_len_out), _p(workspace),
+        _scratch(workspace, what, dev), _stream(stream))
     _check(rc, what)
 
 
@@ -393,14 +425,15 @@ def paged_attn(q, cache: PagedCache, out, scale, workspace, k_new=None, v_new=No
     """dg_paged_attn: q, out [T, Hq, D] over the cache's pages, and over k_new, v_new
     [T, Hkv, D] when given (rows may be strided)."""
     what = "dg_paged_attn"
-    T, Hq, _ = q.shape
-    _on_current(cache.device, what)
+    T, Hq = q.shape[:2]
+    dev = _on_current(cache.k, what)
     rc = _lib().dg_paged_attn(
-        _p(q), _rows(q, Hq, cache.D, what),
-        _p(k_new), 0 if k_new is None else _rows(k_new, cache.Hkv, cache.D, what, T),
-        _p(v_new), 0 if v_new is None else _rows(v_new, cache.Hkv, cache.D, what, T),
-        _p(out), _rows(out, Hq, cache.D, what, T), T, Hq, scale, 1 if causal else 0, window,
-        cache.ref, _p(workspace), workspace.numel(), _stream(stream))
+        _p(q), _rows(q, Hq, cache.D, what, dev),
+        _p(k_new), 0 if k_new is None else _rows(k_new, cache.Hkv, cache.D, what, dev, T),
+        _p(v_new), 0 if v_new is None else _rows(v_new, cache.Hkv, cache.D, what, dev, T),
+        _p(out), _rows(out, Hq, cache.D, what, dev, T), T, Hq, scale, 1 if causal else 0,
+        min(window, 1 << 30), cache.ref, _p(workspace), _scratch(workspace, what, dev),
+        _stream(stream))
     _check(rc, what)
 
 
