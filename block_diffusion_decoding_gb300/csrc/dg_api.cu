@@ -1205,7 +1205,7 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     if (rc != DG_OK) return rc;
     if (T < 0 || Hq < 1 || window < 0 || (causal != 0 && causal != 1)) return DG_ERR_INVALID_ARG;
     if (window > 0 && !causal) return DG_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale * 2.f)) return DG_ERR_INVALID_ARG;
     if (Hq % c->Hkv != 0 || Hq / c->Hkv > 128) return DG_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(T) * Hq > (1LL << 29)) return DG_ERR_UNSUPPORTED;
     window = std::min(window, 1 << 30);   // no sequence has as many keys

@@ -84,10 +84,10 @@ struct PagedSeq {
 };
 
 // Bounds every length by what the tensors hold, so that no later index can
-// leave them; *bad is set when something had to be cut.
+// leave them; *bad: 1 when something had to be cut, 2 when q_start decreases.
 // whole: items are not cut, each costs 1.
 template <int ROWS, int BKV, class I>
-DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool whole, bool *bad = nullptr)
+DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool whole, int *bad = nullptr)
 {
     PagedSeq<I> s;
     const int r0 = paged_load(a.q_start + b), r1 = paged_load(a.q_start + b + 1);
@@ -95,7 +95,7 @@ DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool whole, bool *bad =
     s.s0 = paged_min(paged_max(r0, 0), a.T);
     s.n = paged_min(paged_max(r1, s.s0), a.T) - s.s0;
     s.kv = paged_min(paged_max(k0, 0), a.max_pages * a.page_size);
-    if (bad != nullptr) *bad = r0 != s.s0 || r1 != s.s0 + s.n || k0 != s.kv;
+    if (bad != nullptr) *bad = r1 < r0 ? 2 : r0 != s.s0 || r1 != s.s0 + s.n || k0 != s.kv ? 1 : 0;
     s.mt = (s.n * a.G + ROWS - 1) / ROWS;
     const I G = a.G;
     s.fixed = G * PagedCost<ROWS>::Item + 1;
@@ -199,7 +199,7 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
 {
     const int lane = threadIdx.x & 31;
     PagedRange<I> r{};
-    bool bad = false;
+    int bad = 0;
     auto cost_of = [&](int b) -> I {
         if (b >= a.B) return 0;
         const PagedSeq<I> q = paged_seq<ROWS, BKV, I>(a, b, r.whole);
@@ -211,7 +211,7 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
 #pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         if (b0 + lane >= a.B) continue;
-        bool cut;
+        int cut;
         q = paged_seq<ROWS, BKV, I>(a, b0 + lane, false, &cut);
         bad |= cut;
         mine = a.Hkv * paged_prefix(q, q.mt);
@@ -225,7 +225,10 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
         items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     }
-    if (bad && u == 0) report_error(a.ws, DG_ERR_DEVICE, 911);
+    if (bad != 0 && u == 0) report_error(a.ws, DG_ERR_DEVICE, 911);
+    // rows of several sequences may be longer than any line that was counted
+    // on: nothing is computed
+    if (__any_sync(0xFFFFFFFFu, bad & 2)) return r;
     if (W == 0) return r;
     r.whole = paged_whole<ROWS>(a, W, items, most, units);
     if (r.whole) {

@@ -164,8 +164,9 @@ int dg_encoder_append(const uint16_t *q, uint16_t *k_cache, uint16_t *v_cache, i
 /* they were.  The lengths and the table are DEVICE data, read when the      */
 /* kernels run, so a captured graph follows them.  A length or row index     */
 /* outside its tensor is cut to what the tensors hold, a page id outside     */
-/* [0, n_pages) reads as a page of zeros and is not written; either records  */
-/* DG_ERR_DEVICE in the workspace's status word.                             */
+/* [0, n_pages) reads as a page of zeros and is not written; where q_start   */
+/* decreases the attention computes nothing; each records DG_ERR_DEVICE in   */
+/* the workspace's status word.                                              */
 /* Supported: D in {128, 256}; page_size a multiple of 16, 16 .. 2048;       */
 /* max_pages * page_size <= 2^29; page_stride a multiple of 8 and            */
 /* >= page_size * Hkv * D, or 0 for that value.                              */

@@ -388,6 +388,95 @@ def test_attention_reports_bad_pages_and_lengths(kernel):
     assert status() == 0 and same_bits(out, good)
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_rows_that_decrease_compute_nothing(kernel, D):
+    """q_start must not decrease: the sequences' rows could add up to more than the division of the work was
+    measured for.  Reported, and the output is left as it was; the workspace then serves a good batch."""
+    B = 40
+    b = Batch([3] * B, [50] * B, [50] * B, 4, 2, D, 16, seed=13)
+    c, d = b.cache(), b.cache()
+    d.q_start.copy_(torch.tensor([(0, b.T)[i & 1] for i in range(B + 1)], dtype=torch.int32))
+    ws = dg.workspace(dg.paged_attn_workspace(b.T, 4, c), DEV)
+    out = torch.full_like(b.q, 5.0).to(DEV)
+    dg.paged_attn(b.q.to(DEV), d, out, b.scale, ws)
+    assert dg.read_device_status(ws, clear=True) == 7 and (out == 5).all()
+    dg.paged_attn(b.q.to(DEV), c, out, b.scale, ws)
+    status_ok(ws)
+    want, bound = attention(b, True, 0, False, b.kv)
+    close(out, want, bound)
+
+
+def test_rows_before_the_first_sequence_are_left(kernel):
+    """q_start[0] > 0: a batch whose first rows belong to nobody."""
+    b = Batch([4, 1, 9], [80, 33, 200], [80, 33, 200], 4, 2, 128, 16, seed=21)
+    want, bound = attention(b, True, 0, False, b.kv)
+    lead = torch.full((5, 4, 128), float("nan"), dtype=torch.bfloat16)
+    c = b.cache()
+    c.q_start += 5
+    q = torch.cat([lead, b.q]).to(DEV)
+    out = torch.full_like(q, 5.0)
+    ws = dg.workspace(dg.paged_attn_workspace(len(q), 4, c), DEV)
+    dg.paged_attn(q, c, out, b.scale, ws)
+    status_ok(ws)
+    close(out[5:], want, bound)
+    assert (out[:5] == 5).all()
+    # the append's rows likewise: the same tokens as from row 0 on
+    k, v = (torch.cat([lead[:, :2], t]).to(DEV) for t in (b.kn, b.vn))
+    d, p, wa = b.cache([76, 32, 191]), dg.head_params(4, 2, 128), dg.workspace(256, DEV)
+    e = b.cache([76, 32, 191])
+    dg.paged_append(b.kn.to(DEV), b.vn.to(DEV), e, p, wa)
+    d.q_start += 5
+    qo = torch.full_like(q, 5.0)
+    dg.paged_append(k, v, d, p, wa, q=q, q_out=qo)
+    status_ok(wa)
+    assert same_bits(d.k.cpu(), e.k.cpu()) and same_bits(d.v.cpu(), e.v.cpu())
+    assert same_bits(qo[5:].cpu(), b.q) and (qo[:5] == 5).all()
+
+
+@pytest.mark.parametrize("page", [2048, 2032])
+def test_the_largest_pages(kernel, page):
+    for D, causal, window, fresh in ((128, True, 0, False), (256, False, 0, True), (256, True, 900, False)):
+        check_attn([1, 140, 3], [2500, 4100, 2047], 4, 2, D, page, causal, window, fresh, seed=22)
+
+
+def test_expanded_tensors_are_refused():
+    b = Batch([1, 1], [20, 20], [20, 20], 2, 1, 128, 16, seed=23)
+    c, ws = b.cache(), dg.workspace(1 << 22, DEV)
+    q, out = b.q.to(DEV), torch.empty_like(b.q, device=DEV)
+    with pytest.raises(dg.DgError):
+        dg.paged_attn(q[:1].expand(2, 2, 128), c, out, b.scale, ws)
+    with pytest.raises(dg.DgError):
+        dg.paged_attn(q, c, out, b.scale, ws.cpu())
+    with pytest.raises(dg.DgError):
+        dg.qk_norm_rope(q, None, out, None, torch.zeros(2, dtype=torch.int32, device=DEV),
+                        dg.head_params(2, 1, 128, rope_steps=dg.rope_steps([1.0] * 8, "cpu")))
+    with pytest.raises(dg.DgError):
+        dg.PagedCache(c.k[:1].expand_as(c.k), c.v[:1].expand_as(c.v), c.page_table, c.kv_len, c.q_start)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("n,kv", [([1, 1, 1], [300, 5000, 64]), ([40, 200, 1], [300, 5000, 64])])
+def test_device_checks(kernel, D, n, kv):
+    """With dg_set_device_checks on, finite inputs report nothing and give the same bits; an infinite query is
+    reported (and goes unreported with the checks off)."""
+    b = Batch(n, kv, kv, 4, 2, D, 64, seed=24)
+    plain = run_attn(b, True, 0, False, kv)
+    c, out = b.cache(), torch.empty_like(b.q, device=DEV)
+    ws = dg.workspace(dg.paged_attn_workspace(b.T, 4, c), DEV)
+    q = b.q.to(DEV)
+    odd = q.clone()
+    odd[n[0], 1, 3] = float("inf")
+    for x, on, status in ((q, True, 0), (odd, True, 7), (odd, False, 0)):
+        dg.set_device_checks(on)
+        try:
+            dg.paged_attn(x, c, out, b.scale, ws)
+        finally:
+            dg.set_device_checks(False)
+        assert dg.read_device_status(ws, clear=True) == status
+        if x is q:
+            assert same_bits(out.cpu(), plain.cpu())
+
+
 # ---------------------------------------------------------------- streams, graphs, the chain
 def test_captured_graph_follows_lengths_and_table():
     """One captured append + attention, replayed as the sequences grow, on another stream's capture; two graphs

@@ -76,7 +76,7 @@ def test_attention_refuses(lib):
     for kw, code in ((dict(q=None), INVALID), (dict(out=None), INVALID), (dict(kn=GOOD), INVALID),
                      (dict(vn=GOOD), INVALID), (dict(T=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hq=3), UNSUPPORTED),
                      (dict(Hq=2 * 129), UNSUPPORTED), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
-                     (dict(scale=math.nan), INVALID), (dict(causal=2), INVALID), (dict(window=-1), INVALID),
+                     (dict(scale=math.nan), INVALID), (dict(scale=3e38), INVALID), (dict(causal=2), INVALID), (dict(window=-1), INVALID),
                      (dict(causal=0, window=4), INVALID), (dict(qs=4 * 128 - 8), INVALID), (dict(qs=516), ALIGNMENT),
                      (dict(os=8), INVALID), (dict(kn=GOOD, vn=GOOD, ks=264 - 4), ALIGNMENT),
                      (dict(kn=GOOD, vn=GOOD, vs=128), INVALID), (dict(q=GOOD + 2), ALIGNMENT),
