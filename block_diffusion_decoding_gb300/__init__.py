@@ -257,22 +257,27 @@ def _refuse(what: str, why: str):
     raise e
 
 
+_BF16 = torch.bfloat16
+
+
 def _rows(t: torch.Tensor, heads: int, D: int, what: str, device: int, T: Optional[int] = None) -> int:
     """The row stride of a bf16 tensor [T, heads, D] on the device whose rows are dense and apart."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != device:
+    if t.dtype is not _BF16 or t.get_device() != device:
         _refuse(what, "a bf16 tensor on the current device is wanted")
-    if t.dim() != 3:
+    try:
+        (n, h, d), (s0, s1, s2) = t.shape, t.stride()
+    except ValueError:
         _refuse(what, "a tensor [T, heads, D] is wanted")
-    n, h, d = t.shape
     if h != heads or d != D or (T is not None and n != T):
         _refuse(what, "shape %s where [%s, %d, %d] is wanted"
                 % (tuple(t.shape), "T" if T is None else T, heads, D))
-    s0, s1, s2 = t.stride()
     if n > 0 and ((s2 != 1 and D > 1) or (s1 != D and heads > 1)):
         _refuse(what, "the rows of a tensor are not dense")
-    if n > 1 and s0 < heads * D:   # (an expanded one: 0 means dense to the library)
+    if n < 2:
+        return 0
+    if s0 < heads * D:   # (an expanded one: 0 means dense to the library)
         _refuse(what, "the rows of a tensor overlap")
-    return s0 if n > 1 else 0
+    return s0
 
 
 def _ints(t: torch.Tensor, n: int, what: str, device: int):
