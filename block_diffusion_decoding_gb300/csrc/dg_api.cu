@@ -23,6 +23,7 @@ namespace {
 
 // ---------------------------------------------------------------- small utilities
 constexpr int kAssumedMaxSMs = 256;  // workspace queries do not touch the GPU
+static_assert(kAssumedMaxSMs <= kPagedUnits, "paged attention: units");
 static_assert(kAssumedMaxSMs <= kMergeThreads, "paged merge: a thread per unit");
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

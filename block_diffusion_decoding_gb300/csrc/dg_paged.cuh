@@ -13,8 +13,19 @@
 //
 // A cut has a price: a part's unfinished rows are written and read again in
 // fp32, by a second kernel.  Where whole items spread almost as evenly, as many
-// to each CTA as to any other, they are left whole.
+// to each CTA as to any other, they are left whole, item i to CTA i modulo their
+// number.
+//
+// Chunks of many query tiles do both: CTA pair u takes the items u, u + units, ...
+// whole while that leaves more than one for each, and the line's rest is cut so
+// that all have the same in the end.  So the pairs at work at one time are at
+// neighbouring items, which share a few heads' keys and values, and find them in
+// L2: in stretches of the whole line, four 2000-token chunks over 16384 keys had
+// every head of every sequence in use at once and read 2.4 GB from HBM of which
+// 0.29 GB is distinct.
 #pragma once
+
+#include <type_traits>
 
 #include "dg_paged_device.cuh"
 #include "dg_paged_kernels.h"
@@ -66,13 +77,6 @@ struct PagedSeq {
     int mc;             // tiles whose key count still grows with the tile index
     I x0, slope, cap, fixed;
 
-    // Items that are not cut cost 1 each.
-    DG_BOTH void uncut()
-    {
-        mc = mt;
-        fixed = 1;
-        x0 = slope = cap = 0;
-    }
 #ifdef __CUDACC__
     // Lane `at`'s.
     DG_DEVICE PagedSeq from(int at) const
@@ -85,9 +89,8 @@ struct PagedSeq {
 
 // Bounds every length by what the tensors hold, so that no later index can
 // leave them; *bad: 1 when something had to be cut, 2 when q_start decreases.
-// whole: items are not cut, each costs 1.
 template <int ROWS, int BKV, class I>
-DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool whole, int *bad = nullptr)
+DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, int *bad = nullptr)
 {
     PagedSeq<I> s;
     const int r0 = paged_load(a.q_start + b), r1 = paged_load(a.q_start + b + 1);
@@ -101,9 +104,7 @@ DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, bool whole, int *bad = 
     s.fixed = G * PagedCost<ROWS>::Item + 1;
     s.cap = 0;
     s.mc = s.mt;
-    if (whole) {
-        s.uncut();
-    } else if (!a.causal) {
+    if (!a.causal) {
         s.slope = 0;
         s.x0 = G * (s.kv + (a.has_new ? s.n : 0));
     } else {
@@ -144,9 +145,9 @@ inline bool paged_small(int T, int B, int Hkv, int G, int64_t max_kv)
 // The length of a unit's stretch (a unit: a CTA, or a pair of them) of a line
 // of cost W.
 template <int ROWS, class I>
-DG_BOTH I paged_step(const PagedArgs &a, I W, int units, bool whole)
+DG_BOTH I paged_step(const PagedArgs &a, I W, int units)
 {
-    const I least = whole ? 1 : static_cast<I>(a.G) * PagedCost<ROWS>::Least;
+    const I least = static_cast<I>(a.G) * PagedCost<ROWS>::Least;
     const I n = paged_min<I>(units, paged_max<I>(paged_div(W, least), 1));
     return paged_div<I>(W + n - 1, n);
 }
@@ -162,13 +163,32 @@ DG_BOTH bool paged_whole(const PagedArgs &a, I W, I items, I most, int units)
            static_cast<int64_t>(paged_div<I>(W, units)) + static_cast<int64_t>(a.G) * PagedCost<ROWS>::Cut;
 }
 
+// Whole items that every unit takes before the line's rest is cut (0: all of it
+// is).  Where a sequence's heads have few query tiles the pairs do not meet at a
+// head's keys, and the sums would cost more than they bring.
+template <int ROWS>
+DG_BOTH int paged_rounds(const PagedArgs &a, int64_t items, int units)
+{
+    return ROWS == 256 && items >= 2 * units && items >= 16LL * a.B ? static_cast<int>(items / units) - 1 : 0;
+}
+// ... and whether they leave those who have most with no more than their share
+// (and a sixteenth) of a line of cost W.
+template <class I>
+DG_BOTH bool paged_even(I W, int units, I most)
+{
+    const I share = W / units;
+    return most <= share + share / 16;
+}
+
 template <class I>
 struct PagedRange {
-    I begin, end;            // this unit's stretch (end <= begin: none)
-    I step;
-    I item;                  // where the item that `begin` falls in begins
+    int waves;               // whole items: u, u + units, ...
+    int units;
+    I at;                    // waves > 0: item u's place among those of sequence b
+    I begin, end;            // this unit's stretch of the line (end <= begin: none)
+    I step;                  // every unit's, or 0: they differ
+    I item;                  // waves == 0: where the item that `begin` falls in begins
     int b, g, m;             // that item
-    bool whole;
 };
 
 // The item of sequence b (which begins at `base`) that position x falls in.
@@ -190,21 +210,96 @@ DG_BOTH void paged_locate(const PagedSeq<I> &s, int b, I base, I x, PagedRange<I
     r.item = base + r.g * head + paged_prefix(s, lo);
 }
 
-// Unit u of `units`: its stretch.  By one warp, a sequence a lane and 32 at a
-// time: once over all of them for the line's cost, and again up to the one that
-// the stretch begins in (a batch of up to 32 keeps its costs in registers), whose
-// lengths are left in s.
+constexpr int kPagedUnits = 256;     // units there may be of single CTAs; half of that of pairs
+template <int ROWS>
+constexpr int kPagedBounds = kPagedUnits / (ROWS / 128) / 32;   // units a lane keeps the bound of
+
+// The line's rest after `rounds` whole items of every unit, cut so that all have
+// the same: false if the whole ones are too unequal.  By one warp; q: its
+// sequences' lengths in a batch of up to 32; bound: where the stretches of this
+// lane's units begin; sums: shared memory, an I per unit.  (Apart from the rest
+// of the division, which every small batch runs from a cold instruction cache.)
 template <int ROWS, int BKV, class I>
-DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, PagedSeq<I> &s)
+__device__ __noinline__ bool paged_take_rounds(const PagedArgs &a, int rounds, int units, I W,
+                                               PagedSeq<I> q, I (&bound)[kPagedBounds<ROWS>], void *sums)
+{
+    using Sum = std::conditional_t<sizeof(I) == 4, unsigned, unsigned long long>;
+    constexpr int K = kPagedBounds<ROWS>;
+    constexpr uint32_t all = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31;
+    // what the whole items of every unit cost, an item a lane
+    Sum *sum = static_cast<Sum *>(sums);
+    for (int e = lane; e < units; e += 32) sum[e] = 0;
+    __syncwarp();
+    const I end = static_cast<I>(rounds) * units;
+    I first = 0;                                 // item of the sequence
+    for (int b0 = 0; first < end; b0 += 32) {
+        if (a.B > 32) q = paged_seq<ROWS, BKV, I>(a, min(b0 + lane, a.B - 1));
+        for (int j = 0; j < min(32, a.B - b0) && first < end; ++j) {
+            const PagedSeq<I> t = q.from(j);
+            if (t.mt == 0) continue;
+            const I n = static_cast<I>(a.Hkv) * t.mt;
+            int m = lane % t.mt, to = static_cast<int>((first + lane) % units);
+            const int dm = 32 % t.mt, dto = 32 % units;
+            for (I e = lane; e < n && first + e < end; e += 32) {
+                atomicAdd(&sum[to], static_cast<Sum>(paged_prefix(t, m + 1) - paged_prefix(t, m)));
+                m += dm;
+                if (m >= t.mt) m -= t.mt;
+                to += dto;
+                if (to >= units) to -= units;
+            }
+            __syncwarp();
+            first += n;
+        }
+    }
+    I dearest = 0, taken = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int e = lane * K + k;
+        bound[k] = e < units ? static_cast<I>(sum[e]) : 0;
+        dearest = max(dearest, bound[k]);
+        taken += bound[k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        dearest = max(dearest, __shfl_xor_sync(all, dearest, o));
+        taken += __shfl_xor_sync(all, taken, o);
+    }
+    if (!paged_even(W, units, dearest)) return false;
+    // each gets what it is short of its share of the line
+    const I share = (W + units - 1) / units;
+    I at = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const I left = lane * K + k < units ? max(share - bound[k], I(0)) : 0;
+        bound[k] = at;
+        at += left;
+    }
+    I incl = at;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const I v = __shfl_up_sync(all, incl, o);
+        if (lane >= o) incl += v;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) bound[k] = min(W, taken + incl - at + bound[k]);
+    return true;
+}
+
+// Unit u of `units`: its share.  By one warp, a sequence a lane and 32 at a
+// time: once over all of them for the line's cost, and again up to the one that
+// the stretch begins in (a batch of up to 32 keeps its lengths in registers),
+// whose lengths are left in s.  bound: where the stretches of this lane's units
+// begin, if they differ.  sums: shared memory, an I per pair.
+template <int ROWS, int BKV, class I>
+DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, PagedSeq<I> &s,
+                                     I (&bound)[kPagedBounds<ROWS>], void *sums)
 {
     const int lane = threadIdx.x & 31;
+    constexpr uint32_t all = 0xFFFFFFFFu;
     PagedRange<I> r{};
+    r.units = units;
     int bad = 0;
-    auto cost_of = [&](int b) -> I {
-        if (b >= a.B) return 0;
-        const PagedSeq<I> q = paged_seq<ROWS, BKV, I>(a, b, r.whole);
-        return a.Hkv * paged_prefix(q, q.mt);
-    };
     // this lane's sequences: cost, items, the dearest item
     I mine = 0, W = 0, items = 0, most = 0;
     PagedSeq<I> q{};
@@ -212,7 +307,7 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         if (b0 + lane >= a.B) continue;
         int cut;
-        q = paged_seq<ROWS, BKV, I>(a, b0 + lane, false, &cut);
+        q = paged_seq<ROWS, BKV, I>(a, b0 + lane, &cut);
         bad |= cut;
         mine = a.Hkv * paged_prefix(q, q.mt);
         W += mine;
@@ -221,49 +316,66 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        W += __shfl_xor_sync(0xFFFFFFFFu, W, o);
-        items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
-        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        W += __shfl_xor_sync(all, W, o);
+        items += __shfl_xor_sync(all, items, o);
+        most = max(most, __shfl_xor_sync(all, most, o));
     }
     if (bad != 0 && u == 0) report_error(a.ws, DG_ERR_DEVICE, 911);
     // rows of several sequences may be longer than any line that was counted
     // on: nothing is computed
-    if (__any_sync(0xFFFFFFFFu, bad & 2)) return r;
+    if (__any_sync(all, bad & 2)) return r;
     if (W == 0) return r;
-    r.whole = paged_whole<ROWS>(a, W, items, most, units);
-    if (r.whole) {
-        W = items;
-        q.uncut();
-        mine = a.Hkv * q.mt;   // (a batch of up to 32)
+    if (paged_whole<ROWS>(a, W, items, most, units)) {
+        if (u >= items) return r;
+        r.waves = static_cast<int>(paged_div<I>(items - u + units - 1, units));
+    } else {
+        r.step = paged_step<ROWS>(a, W, units);
+        r.begin = u * r.step;
+        r.end = min(W, r.begin + r.step);
     }
-    const I step = paged_step<ROWS>(a, W, units, r.whole), x = u * step;
-    if (x >= W) return r;
-    I incl = 0;
-    auto scan = [&](I v) {
-        incl = v;
+    if constexpr (ROWS == 256) {
+        const int rounds = paged_rounds<ROWS>(a, items, units);
+        if (rounds > 0 && r.waves == 0 && paged_take_rounds<ROWS, BKV, I>(a, rounds, units, W, q, bound, sums)) {
+            constexpr int K = kPagedBounds<ROWS>;
+            r.begin = r.end = W;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const I p = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += p;
+            for (int k = 0; k < K; ++k) {
+                const I begin = __shfl_sync(all, bound[k], u / K);
+                if (k == u % K) r.begin = begin;
+                const I end = __shfl_sync(all, bound[k], (u + 1) / K);
+                if (k == (u + 1) % K && u + 1 < units) r.end = end;
+            }
+            r.step = 0;
+            r.waves = rounds;
         }
-    };
+    }
+    if (r.waves == 0 && r.begin >= r.end) return r;
+    // the first item: by its number, or by the place on the line
+    const I x = r.waves > 0 ? u : r.begin;
     I base = 0;
     for (int b0 = 0;; b0 += 32) {
-        if (a.B > 32) mine = cost_of(b0 + lane);
-        scan(mine);
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, base + incl > x);
+        if (a.B > 32) {
+            q = paged_seq<ROWS, BKV, I>(a, min(b0 + lane, a.B - 1));
+            if (b0 + lane >= a.B) q.mt = 0;
+        }
+        mine = a.Hkv * (r.waves > 0 ? q.mt : paged_prefix(q, q.mt));
+        I incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const I v = __shfl_up_sync(all, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const uint32_t past = __ballot_sync(all, base + incl > x);
         if (past != 0) {
             const int at = __ffs(past) - 1;
-            base += __shfl_sync(0xFFFFFFFFu, incl - mine, at);
-            if (a.B > 32) q = paged_seq<ROWS, BKV, I>(a, min(b0 + lane, a.B - 1), r.whole);
+            base += __shfl_sync(all, incl - mine, at);
             s = q.from(at);
-            paged_locate(s, b0 + at, base, x, r);
-            r.begin = x;
-            r.end = min(W, x + step);
-            r.step = step;
+            r.b = b0 + at;
+            r.at = x - base;
+            if (r.waves == 0) paged_locate(s, r.b, base, x, r);
             return r;
         }
-        base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        base += __shfl_sync(all, incl, 31);
     }
 }
 
@@ -280,58 +392,110 @@ struct PagedPart {
     bool whole;
 };
 
-// Walks the parts of a stretch.
+// Walks a unit's whole items, then the parts of its stretch.
 template <int ROWS, int BKV, class I>
 struct PagedWalk {
     PagedSeq<I> s, ahead;   // this sequence, the next one's lengths (already loaded)
     int b, g, m;
-    I item, begin, end, step;
-    bool whole;
+    I at;                   // whole items: the next one's place in the sequence
+    int waves;              // how many are left
+    I item, begin, end;
+    PagedRange<I> r;
 
-    // first: the lengths of the sequence the stretch begins in
-    DG_BOTH void start(const PagedArgs &a, const PagedRange<I> &r, const PagedSeq<I> &first)
+    // first: the lengths of sequence r.b
+    DG_BOTH void start(const PagedArgs &a, const PagedRange<I> &range, const PagedSeq<I> &first)
+    {
+        r = range;
+        waves = r.waves;
+        b = r.b;
+        at = r.at;
+        s = first;
+        item = end = r.end;
+        if (waves == 0 && r.begin < r.end) stretch(a);
+    }
+
+    // On to the sequence that item `at` is of.
+    DG_BOTH void settle(const PagedArgs &a)
+    {
+        while (at >= static_cast<I>(a.Hkv) * s.mt && b + 1 < a.B) {
+            at -= static_cast<I>(a.Hkv) * s.mt;
+            s = paged_seq<ROWS, BKV, I>(a, ++b);
+        }
+    }
+
+    DG_BOTH void stretch(const PagedArgs &a)
     {
         begin = r.begin;
-        item = end = r.end;
-        if (end <= begin) return;
-        step = r.step;
-        b = r.b;
         g = r.g;
         m = r.m;
         item = r.item;
-        whole = r.whole;
-        s = ahead = first;
-        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1, whole);
+        ahead = s;
+        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1);
     }
 
-    // The next part; false: the stretch is done.
-    DG_BOTH bool next(const PagedArgs &a, PagedPart &p)
+    // To where the stretch begins.
+    DG_BOTH void find(const PagedArgs &a)
     {
+        I base = 0;
+        for (b = 0;; ++b) {
+            s = paged_seq<ROWS, BKV, I>(a, b);
+            const I all = static_cast<I>(a.Hkv) * paged_prefix(s, s.mt);
+            if (base + all > r.begin || b + 1 == a.B) break;
+            base += all;
+        }
+        paged_locate(s, b, base, r.begin, r);
+        stretch(a);
+    }
+
+    // What a part has of its item: all but its share of the tiles.
+    DG_BOTH void fill(const PagedArgs &a, PagedPart &p) const
+    {
+        p.s0 = s.s0;
+        p.n = s.n;
+        p.kv = s.kv;
+        p.b = b;
+        p.g = g;
+        p.frow0 = m * ROWS;
+        p.rows = paged_min(ROWS, s.n * a.G - p.frow0);
+        p.nkp = (s.kv + BKV - 1) / BKV;
+        int hi, lo = 0;
+        if (!a.causal) {
+            hi = p.nkp + (a.has_new ? (s.n + BKV - 1) / BKV : 0);
+        } else {
+            const int i1 = (p.frow0 + p.rows - 1) / a.G;
+            hi = a.has_new ? p.nkp + i1 / BKV + 1 : paged_max(0, (s.kv - s.n + i1 + BKV) / BKV);
+        }
+        if (a.window > 0) {
+            const int i0 = p.frow0 / a.G;
+            const int first = (a.has_new ? s.kv : s.kv - s.n) + i0 - a.window + 1;
+            if (first > 0)
+                lo = a.has_new && first >= s.kv ? p.nkp + (first - s.kv) / BKV : first / BKV;
+        }
+        p.lo = lo;
+        p.nt = paged_max(0, hi - lo);
+    }
+
+    // The next part; false: there are no more.  unit_of(x): the unit whose
+    // stretch has place x of the line.
+    template <class UnitOf>
+    DG_BOTH bool next(const PagedArgs &a, PagedPart &p, UnitOf unit_of)
+    {
+        if (waves > 0) {
+            g = static_cast<int>(paged_div<I>(at, s.mt));
+            m = static_cast<int>(at) - g * s.mt;
+            fill(a, p);
+            p.t0 = 0;
+            p.t1 = p.nt;
+            p.last = -1;
+            p.whole = true;
+            at += r.units;
+            if (--waves > 0) settle(a);
+            else if (r.begin < r.end) find(a);
+            return true;
+        }
         while (item < end) {
             const I cost = paged_prefix(s, m + 1) - paged_prefix(s, m);
-            p.s0 = s.s0;
-            p.n = s.n;
-            p.kv = s.kv;
-            p.b = b;
-            p.g = g;
-            p.frow0 = m * ROWS;
-            p.rows = paged_min(ROWS, s.n * a.G - p.frow0);
-            p.nkp = (s.kv + BKV - 1) / BKV;
-            int hi, lo = 0;
-            if (!a.causal) {
-                hi = p.nkp + (a.has_new ? (s.n + BKV - 1) / BKV : 0);
-            } else {
-                const int i1 = (p.frow0 + p.rows - 1) / a.G;
-                hi = a.has_new ? p.nkp + i1 / BKV + 1 : paged_max(0, (s.kv - s.n + i1 + BKV) / BKV);
-            }
-            if (a.window > 0) {
-                const int i0 = p.frow0 / a.G;
-                const int first = (a.has_new ? s.kv : s.kv - s.n) + i0 - a.window + 1;
-                if (first > 0)
-                    lo = a.has_new && first >= s.kv ? p.nkp + (first - s.kv) / BKV : first / BKV;
-            }
-            p.lo = lo;
-            p.nt = paged_max(0, hi - lo);
+            fill(a, p);
             // a tile is worth its keys: BKV x G of the cost after the fixed
             // part; what rounding leaves over goes with the last tile
             const I tile = static_cast<I>(a.G) * BKV;
@@ -347,8 +511,7 @@ struct PagedWalk {
             p.last = -1;
             const bool any = p.t1 > p.t0 || (p.nt == 0 && from <= 0);
             if (any && p.t0 == 0 && !p.whole)
-                p.last = static_cast<int>(
-                    paged_div<I>(item + paged_min<I>(s.fixed + p.nt * tile, cost) - 1, step));
+                p.last = unit_of(item + paged_min<I>(s.fixed + p.nt * tile, cost) - 1);
             item += cost;
             if (++m == s.mt) {
                 m = 0;
@@ -360,7 +523,7 @@ struct PagedWalk {
                             break;
                         }
                         s = ahead;
-                        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1, whole);
+                        if (b + 1 < a.B) ahead = paged_seq<ROWS, BKV, I>(a, b + 1);
                     } while (s.n == 0);
                 }
             }
@@ -406,23 +569,34 @@ DG_DEVICE void paged_ring_init(PagedRing &ring, int takers)
 // while the rest of the CTA sets up; `ready` returns once the ring may be used.
 template <class Gm, class I, class Ready>
 DG_DEVICE void paged_walk_in(const PagedArgs &a, int u, int units, PagedRing &ring, int where,
-                             Ready ready)
+                             void *sums, Ready ready)
 {
     const bool lead = (threadIdx.x & 31) == 0;
     PagedWalk<Gm::Rows, Gm::BKV, I> walk;
     PagedSeq<I> first{};
-    const PagedRange<I> range = paged_divide<Gm::Rows, Gm::BKV, I>(a, u, units, first);
-    if (range.end > range.begin) {
+    I bound[kPagedBounds<Gm::Rows>];
+    const PagedRange<I> range = paged_divide<Gm::Rows, Gm::BKV, I>(a, u, units, first, bound, sums);
+    if (range.waves > 0 || range.end > range.begin) {
         // the load warps will want the pages of the first keys next
-        const I key = paged_div<I>(paged_max<I>(range.begin - range.item, first.fixed) - first.fixed, a.G);
+        const I key = range.waves > 0 ? 0
+                                      : paged_div<I>(paged_max<I>(range.begin - range.item, first.fixed) -
+                                                         first.fixed, a.G);
         const int page = static_cast<int>(key) / a.page_size + (static_cast<int>(threadIdx.x) & 31) * 32;
         if (page < a.max_pages)
             asm volatile("prefetch.global.L1 [%0];" ::"l"(
                 a.page_table + static_cast<int64_t>(range.b) * a.max_pages + page));
     }
     walk.start(a, range, first);
+    auto unit_of = [&](I x) -> int {
+        if (range.step > 0) return static_cast<int>(paged_div<I>(x, range.step));
+        int n = 0;               // bounds that are not above
+        for (int k = 0; k < kPagedBounds<Gm::Rows>; ++k)
+            n += __popc(__ballot_sync(0xFFFFFFFFu, (static_cast<int>(threadIdx.x) & 31) * kPagedBounds<Gm::Rows> +
+                                                               k < units && bound[k] <= x));
+        return n - 1;
+    };
     PagedPart p;
-    bool more = walk.next(a, p);
+    bool more = walk.next(a, p, unit_of);
     ready();
     for (uint32_t k = 0;; ++k) {
         const int e = static_cast<int>(k % kPagedItems);
@@ -448,15 +622,16 @@ DG_DEVICE void paged_walk_in(const PagedArgs &a, int u, int units, PagedRing &ri
             mbar_arrive(&ring.full[e]);
         }
         if (!more) return;
-        more = walk.next(a, p);
+        more = walk.next(a, p, unit_of);
     }
 }
 
 template <class Gm, class Ready>
-DG_DEVICE void paged_walk(const PagedArgs &a, int u, int units, PagedRing &ring, int where, Ready ready)
+DG_DEVICE void paged_walk(const PagedArgs &a, int u, int units, PagedRing &ring, int where, void *sums,
+                          Ready ready)
 {
-    if (a.small) paged_walk_in<Gm, int32_t>(a, u, units, ring, where, ready);
-    else paged_walk_in<Gm, int64_t>(a, u, units, ring, where, ready);
+    if (a.small) paged_walk_in<Gm, int32_t>(a, u, units, ring, where, sums, ready);
+    else paged_walk_in<Gm, int64_t>(a, u, units, ring, where, sums, ready);
 }
 
 // The k-th part, by every thread of a role's warp (or one thread alone, which

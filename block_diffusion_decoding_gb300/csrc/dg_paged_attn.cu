@@ -145,7 +145,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 7) {
-        paged_walk<Gm>(a, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), ring, 927,
+        paged_walk<Gm>(a, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), ring, 927, nullptr,
                        [] { cta_sync(); });
     } else if (warp == 0) {
         paged_ring_producer<Gm, NK>(smem + Gm::OffK, k_full, k_empty, map_k, map_kn, a, ring, 921);

@@ -67,12 +67,13 @@ struct PairShared {
     uint64_t l_full[2][4];            // by warpgroup and lane quadrant
     uint64_t q_ready, o_full, o_free, drained;
     uint32_t tmem;
-    float m[2][128];                  // running maximum after a tile, by its parity
+    alignas(8) float m[2][128];       // running maximum after a tile, by its parity
     float l[2][128];                  // sum of a warpgroup's tiles of a part
     // by part modulo 3 and half of the dims: a hidden value of that half was
     // zeroed (told to both CTAs; cleared a part later, two before it is used again)
     uint32_t zeroed[3][2];
 };
+static_assert(sizeof(PairShared::m) >= kPagedUnits / 2 * sizeof(int64_t), "the division's sums");
 static_assert(PairGeom<128>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
 static_assert(PairGeom<256>::OffShared + sizeof(PairShared) <= 232448, "shared memory");
 
@@ -271,7 +272,8 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
     if (warp < 4) {
         reg_dec<kPairOtherRegs>();
         if (warp == 3) {
-            paged_walk<Gm>(a, unit, static_cast<int>(num_clusters_x()), sh.ring, 1007,
+            // (the maxima's place is free until the first part is known)
+            paged_walk<Gm>(a, unit, static_cast<int>(num_clusters_x()), sh.ring, 1007, sh.m,
                            [&] { together(); });
         } else if (warp == 0) {
             together();

@@ -236,6 +236,18 @@ def test_attention_cut_between_ctas(kernel, D, page, causal, window, fresh):
     check_attn(n, kv, 4, 2, D, page, causal, window, fresh, seed=3)
 
 
+@pytest.mark.parametrize("causal,window,fresh", MASKS)
+@pytest.mark.parametrize("n,kv,Hq,Hkv,D", [([640, 600], [2600, 1500], 32, 8, 128), ([0, 1500, 1], [40, 900, 7], 24, 8, 256)])
+def test_attention_whole_items_then_a_cut_rest(n, kv, Hq, Hkv, D, causal, window, fresh):
+    """More than two query tiles for every CTA pair, of unequal cost: whole ones in turn, then the cut rest."""
+    tiles = sum(-(-m * (Hq // Hkv) // 256) * Hkv for m in n)
+    units = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    assert tiles >= max(16 * len(n), 2 * units)
+    if not fresh:
+        kv = [k + m for k, m in zip(kv, n)]
+    check_attn(n, kv, Hq, Hkv, D, 64, causal, window, fresh, seed=9)
+
+
 @pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 1), (256, 16, 8), (128, 128, 1), (256, 40, 2)])
 def test_attention_single_tokens(D, Hq, Hkv):
     check_attn([1] * 9, [1, 2, 17, 128, 700, 1500, 64, 31, 4100], Hq, Hkv, D, 32, True, 0, False, seed=4)

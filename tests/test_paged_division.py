@@ -22,7 +22,8 @@ HARNESS = r"""
 #include <vector>
 #include "dg_paged.cuh"
 using namespace dg;
-static long wholes = 0;
+static long wholes = 0, rounds_n = 0;
+static double worst = 0;
 
 #define FAIL(...) do { printf(__VA_ARGS__); printf("\n"); return 1; } while (0)
 
@@ -33,7 +34,7 @@ int check(const PagedArgs &a, int units)
     I items_n = 0, most = 0;
     bool whole = false;
     for (int b = 0; b < a.B; ++b) {
-        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b, false);
+        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b);
         if (s.s0 < 0 || s.n < 0 || s.s0 + s.n > a.T || s.kv < 0 || s.kv > a.max_pages * a.page_size)
             FAIL("lengths not cut");
         base[b + 1] = base[b] + a.Hkv * paged_prefix(s, s.mt);
@@ -43,35 +44,83 @@ int check(const PagedArgs &a, int units)
             if (c > most) most = c;
         }
     }
-    I W = base[a.B];
+    const I W = base[a.B];
     if (W == 0) return 0;
     whole = paged_whole<ROWS>(a, W, items_n, most, units);
+    const I step = paged_step<ROWS>(a, W, units);
+    int n = units;
+    std::vector<I> bound(units + 1, W), sum(units, 0);
+    int waves = 0;
     if (whole) {
-        for (int b = 0; b < a.B; ++b)
-            base[b + 1] = base[b] + a.Hkv * paged_prefix(paged_seq<ROWS, BKV, I>(a, b, true), paged_seq<ROWS, BKV, I>(a, b, true).mt);
-        W = base[a.B];
-        if (W != items_n) FAIL("whole items");
         ++wholes;
+    } else {
+        n = static_cast<int>((W + step - 1) / step);
+        if (n > units) FAIL("%d units of %d", n, units);
+        waves = paged_rounds<ROWS>(a, items_n, units);
+        if (waves) {
+            I i = 0, taken = 0, dearest = 0;
+            for (int b = 0; b < a.B; ++b) {
+                const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b);
+                for (int e = 0; e < a.Hkv * s.mt; ++e, ++i)
+                    if (i < static_cast<I>(waves) * units)
+                        sum[i % units] += paged_prefix(s, e % s.mt + 1) - paged_prefix(s, e % s.mt);
+            }
+            for (I x : sum) taken += x, dearest = x > dearest ? x : dearest;
+            if (!paged_even(W, units, dearest)) {
+                waves = 0;
+            } else {
+                ++rounds_n;
+                n = units;
+                const I share = (W + units - 1) / units;
+                I at = taken;
+                for (int u = 0; u < units; ++u) {
+                    bound[u] = at < W ? at : W;
+                    at += share > sum[u] ? share - sum[u] : 0;
+                    const double cost = static_cast<double>(sum[u] + (at < W ? at : W) - bound[u]) / share;
+                    if (cost > worst) worst = cost;
+                }
+                if (at < W) FAIL("the line is not given out");
+            }
+        }
     }
-    const I step = paged_step<ROWS>(a, W, units, whole);
-    const int n = static_cast<int>((W + step - 1) / step);
-    if (n > units) FAIL("%d units of %d", n, units);
+    auto unit_of = [&](I x) -> int {
+        if (!waves) return static_cast<int>(x / step);
+        int k = 0;
+        while (k < units && bound[k] <= x) ++k;
+        return k - 1;
+    };
     // per item: the tiles so far, the unit promised the last part
     std::map<std::tuple<int, int, int>, std::pair<int, int>> items;
     for (int u = 0; u < n; ++u) {
         PagedRange<I> r{};
-        r.begin = u * step;
-        r.end = r.begin + step < W ? r.begin + step : W;
-        r.step = step;
-        int b = 0;
-        while (base[b + 1] <= r.begin) ++b;
-        paged_locate(paged_seq<ROWS, BKV, I>(a, b, whole), b, base[b], r.begin, r);
-        r.whole = whole;
+        r.units = units;
+        PagedSeq<I> first{};
+        r.waves = waves;
+        if (whole) {
+            r.waves = u < items_n ? static_cast<int>((items_n - u + units - 1) / units) : 0;
+        } else {
+            r.begin = waves ? bound[u] : u * step;
+            r.end = waves ? bound[u + 1] : r.begin + step < W ? r.begin + step : W;
+            r.step = waves ? 0 : step;
+        }
+        if (r.waves) {
+            I i = u;
+            for (;; ++r.b) {
+                first = paged_seq<ROWS, BKV, I>(a, r.b);
+                if (i < a.Hkv * first.mt) break;
+                i -= a.Hkv * first.mt;
+            }
+            r.at = i;
+        } else if (r.begin < r.end) {
+            while (base[r.b + 1] <= r.begin) ++r.b;
+            first = paged_seq<ROWS, BKV, I>(a, r.b);
+            paged_locate(first, r.b, base[r.b], r.begin, r);
+        }
         PagedWalk<ROWS, BKV, I> walk;
-        walk.start(a, r, paged_seq<ROWS, BKV, I>(a, b, whole));
+        walk.start(a, r, first);
         PagedPart p;
         int slot0 = 0, slot1 = 0;
-        while (walk.next(a, p)) {
+        while (walk.next(a, p, unit_of)) {
             // the definition, from the lengths alone
             int lo = 1 << 30, hi = 0;
             const int keys = p.kv + (a.has_new ? p.n : 0);
@@ -113,7 +162,7 @@ int check(const PagedArgs &a, int units)
         }
     }
     for (int b = 0; b < a.B; ++b) {
-        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b, whole);
+        const PagedSeq<I> s = paged_seq<ROWS, BKV, I>(a, b);
         for (int g = 0; g < a.Hkv; ++g)
             for (int m = 0; m < s.mt; ++m)
                 if (!items.count(std::make_tuple(b, g, m * ROWS))) FAIL("item (%d %d %d) missing", b, g, m);
@@ -144,7 +193,8 @@ int main()
         if (rc) { printf("case %ld\n", line); return 1; }
         ++line;
     }
-    printf("%ld cases, %ld of them also in 32 bits, %ld divisions left whole\n", line, small, wholes);
+    printf("%ld cases, %ld of them also in 32 bits, %ld divisions left whole, %ld in rounds, %.0f at most\n", line, small,
+           wholes, rounds_n, 1000 * worst);
     return 0;
 }
 """
@@ -198,5 +248,7 @@ def test_every_visible_tile_goes_to_one_cta(harness):
     assert r.returncode == 0, (r.stdout[-300:], cases[where][:12] if where is not None else r.stderr[-300:])
     assert "1500 cases" in r.stdout
     # both integer widths, and both ways of dividing, are among them
-    cases_, small, wholes = (int(x) for x in re.findall(r"(\d+) (?:cases|of them|divisions)", r.stdout))
-    assert 500 < small < 1500 and 200 < wholes < cases_ + small - 200, r.stdout
+    cases_, small, wholes, rounds, worst = (int(x) for x in re.findall(r"(\d+) (?:cases|of them|divisions|in|at)", r.stdout))
+    assert 500 < small < 1500 and 200 < wholes < cases_ + small - 200 and rounds > 50, r.stdout
+    # whole items first leave no unit with more than a sixteenth above its share (in thousandths)
+    assert 900 < worst <= 1063, r.stdout
