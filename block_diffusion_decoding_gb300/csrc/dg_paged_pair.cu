@@ -115,21 +115,32 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
     for (uint32_t k = 0; ok && paged_take(a, sh.ring, k, p, false, where + 2); ++k) {
         const int32_t *table = a.page_table + static_cast<int64_t>(p.b) * a.max_pages;
         const int nkp = (p.kv + Gm::BKV - 1) / Gm::BKV;
-        // page of piece `lane` from this tile on
-        auto fetch = [&](int tile) -> int32_t {
+        // page of piece `lane` from this tile on, and its first row in that page
+        int32_t page_row[2] = {0, 0};
+        auto fetch = [&](int tile, int32_t &row) -> int32_t {
             const int t = tile + lane / per_tile;
             const int key = t * Gm::BKV + key_off + lane % per_tile * R;
-            return key < p.kv && t < p.tv1 ? __ldg(table + key / a.page_size) : 0;
+            const int at_page = key / a.page_size;
+            row = key - at_page * a.page_size;
+            return key < p.kv && t < p.tv1 ? __ldg(table + at_page) : 0;
         };
         const PagedSpecial special = paged_special<Gm::BKV>(a, p, paged_edge(a, p));
-        int32_t pages = fetch(p.tv0), ahead = fetch(p.tv0 + batch);
-        int in = 0;
-        for (int tv = p.tv0; tv < p.tv1; ++tv, ++in) {
-            if (in == batch) {
-                in = 0;
+        // tiles whose keys are all in pages and seen by every row: nearly all
+        // of a long part's
+        const int plain0 = IS_V ? p.tv0 + special.lo : p.tv0;
+        const int plain1 = min(IS_V ? p.tv0 + special.hi : p.tv1, p.kv / Gm::BKV);
+        int32_t pages = fetch(p.tv0, page_row[0]), ahead = fetch(p.tv0 + batch, page_row[1]);
+        int piece = min(box, per_tile - 1);                // this lane's of the tile
+        for (int tv = p.tv0; tv < p.tv1; ++tv, piece += per_tile) {
+            if (piece >= batch * per_tile) {
+                piece -= batch * per_tile;
                 pages = ahead;
-                ahead = fetch(tv + batch);
+                page_row[0] = page_row[1];
+                ahead = fetch(tv + batch, page_row[1]);
             }
+            int32_t page = __shfl_sync(0xFFFFFFFFu, pages, piece);
+            const int32_t row = __shfl_sync(0xFFFFFFFFu, page_row[0], piece);
+            if (page < 0 || page >= a.n_pages) page = a.n_pages;   // (reported below)
             ok = mbar_wait_poll<false, kPagedLoadSleep>(&empty[s], par ^ 1u, a.ws, where);
             if (Gm::Dim == 256 && first && (IS_V || tv > p.tv0)) {
                 // the first tiles wait for nothing but the queries and K's first
@@ -139,6 +150,25 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 ok = false;
                 break;
+            }
+            uint8_t *dst = buf + s * Bytes + at * Atom;
+            armed |= 1u << s;
+            armed_par = (armed_par & ~(1u << s)) | (par << s);
+            if (tv >= plain0 && tv < plain1) {
+                if (lane == 0 && r == 0) mbar_arrive_expect_tx(&full[s], Gm::BKV * Gm::Dim * 2);
+                __syncwarp();
+                if (box < per_tile) {
+                    // a page id outside the cache: the box lies outside the
+                    // tensor, which reads as zeros
+                    if (page == a.n_pages) report_error(a.ws, DG_ERR_DEVICE, 912);
+                    tma_load_4d_pair(dst + box * R * 128, map_c, lead_full + s * 8, dim0, p.g, row, page,
+                                     pol);
+                }
+                if (++s == NS) {
+                    s = 0;
+                    par ^= 1u;
+                }
+                continue;
             }
             const int valid = paged_valid<Gm::BKV>(p, tv);
             const bool paged = tv < nkp;
@@ -156,29 +186,18 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
                     mbar_arrive_expect_tx(&full[s], tile_bytes);
                 }
             }
-            const int32_t piece = __shfl_sync(0xFFFFFFFFu, pages, in * per_tile + min(box, per_tile - 1));
+            __syncwarp();
             const uint32_t bar = own ? mapa_shared(smem_u32(&sh.v_land[s]), r) : lead_full + s * 8;
-            uint8_t *dst = buf + s * Bytes + at * Atom;
             if (paged) {
                 if (box < mine) {
-                    // a page id outside the cache: the box lies outside the
-                    // tensor, which reads as zeros
-                    int32_t page = piece;
-                    if (page < 0 || page >= a.n_pages) {
-                        report_error(a.ws, DG_ERR_DEVICE, 912);
-                        page = a.n_pages;
-                    }
-                    const int key = tv * Gm::BKV + key_off + box * R;
-                    tma_load_4d_pair(dst + box * R * 128, map_c, bar, dim0, p.g, key % a.page_size,
-                                     page, pol);
+                    if (page == a.n_pages) report_error(a.ws, DG_ERR_DEVICE, 912);
+                    tma_load_4d_pair(dst + box * R * 128, map_c, bar, dim0, p.g, row, page, pol);
                 }
             } else if (box == 0) {
                 tma_load_3d_pair(dst, map_n, bar, dim0, p.g, p.s0 + (tv - nkp) * Gm::BKV + key_off,
                                  pol);
             }
             if (own) landing ^= 1u << s;
-            armed |= 1u << s;
-            armed_par = (armed_par & ~(1u << s)) | (par << s);
             if (++s == NS) {
                 s = 0;
                 par ^= 1u;
