@@ -18,7 +18,7 @@
 //   TMEM        O [128 x D] fp32 | S buffers [128 x 128] fp32 (the bf16 P of a
 //               tile overwrites the S it came from);
 //   warp 0      TMA: K halves;    warp 2   TMA: V halves;    warp 3   the walk;
-//   warp 1      UMMA issuer (even CTA): S runs NS - 1 tiles ahead of PV; the odd
+//   warp 1      UMMA issuer (even CTA): S runs NS tiles ahead of PV; the odd
 //               CTA's passes on that its query rows are in place;
 //   warps 4-7   softmax of the even tiles, a query row a thread; warps 8-11 of
 //               the odd ones; both load Q rows, and each stores half of O.
@@ -326,68 +326,72 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                     const int steps_kv = paged_steps(p.kv, BKV), steps_new = paged_steps(p.n, BKV);
                     const int j_kv = (p.kv + BKV - 1) / BKV - 1 - p.tv0;   // last tile of the pages
                     const int j_new = j_kv + (p.n + BKV - 1) / BKV;        // of the new tokens
-                    for (int j = 0; j < nt + NS - 1 && ok; ++j) {
-                        if (j < nt) {
-                            ok = mbar_wait_poll(&sh.k_full[ks], kpar, a.ws, 1012);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t dk = dk0 + ks * (Gm::KBytes >> 4);
-                            const uint32_t d = tmem + Gm::ColS + ss * BKV;
-                            if (lead) {
-    #pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk)
-                                    umma_bf16_pair(
-                                        d, dq + (((kk >> 2) * Gm::QAtomBytes + (kk & 3) * 32) >> 4),
-                                        dk + (((kk >> 2) * Gm::KAtomBytes + (kk & 3) * 32) >> 4), idesc_s,
-                                        kk != 0);
-                                umma_commit_pair(&sh.s_full[ss], 0x3);
-                                umma_commit_pair(&sh.k_empty[ks], 0x3);
-                            }
-                            if (++ss == NS) ss = 0;
-                            if (++ks == NK) {
-                                ks = 0;
-                                kpar ^= 1u;
-                            }
+                    auto score = [&] {                   // S of the next tile
+                        const uint64_t dk = dk0 + ks * (Gm::KBytes >> 4);
+                        const uint32_t d = tmem + Gm::ColS + ss * BKV;
+                        if (lead) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma_bf16_pair(
+                                    d, dq + (((kk >> 2) * Gm::QAtomBytes + (kk & 3) * 32) >> 4),
+                                    dk + (((kk >> 2) * Gm::KAtomBytes + (kk & 3) * 32) >> 4), idesc_s,
+                                    kk != 0);
+                            umma_commit_pair(&sh.s_full[ss], 0x3);
+                            umma_commit_pair(&sh.k_empty[ks], 0x3);
                         }
-                        const int jp = j - (NS - 1);
-                        if (jp >= 0) {
-                            // both CTAs' softmax warps have written P
-                            // (and read the O of the part before this one)
-                            ok = mbar_wait_poll(&sh.v_full[vs], vpar, a.ws, 1014) &&
-                                 mbar_wait_poll<true>(&sh.p_full[ps], ppar, a.ws, 1013) &&
-                                 (jp > 0 || parts < 2 ||
-                                  mbar_wait_poll<true>(&sh.o_free, parts & 1u, a.ws, 1016));
-                            if (!ok) break;
-                            tc_fence_after();
-                            const int steps = jp == j_kv ? steps_kv : jp == j_new ? steps_new : BKV / 16;
-                            const uint64_t dv = dv0 + vs * (Gm::VBytes >> 4);
-                            const uint32_t pa = tmem + Gm::ColS + ps * BKV;
-                            if (lead) {
-                                umma_bf16_pair_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
-                                if (steps == BKV / 16) {
-    #pragma unroll
-                                    for (int kk = 1; kk < BKV / 16; ++kk)
-                                        umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
-                                                          idesc_o, 1);
-                                } else {
-                                    for (int kk = 1; kk < steps; ++kk)
-                                        umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128,
-                                                          idesc_o, 1);
-                                }
-                                umma_commit_pair(&sh.v_empty[vs], 0x3);
-                                umma_commit_pair(&sh.pv_done[pv & 1], 0x3);
-                                if (jp + 1 == nt) umma_commit_pair(&sh.o_full, 0x3);
-                            }
-                            ++pv;
-                            if (++ps == NS) {
-                                ps = 0;
-                                ppar ^= 1u;
-                            }
-                            if (++vs == NV) {
-                                vs = 0;
-                                vpar ^= 1u;
-                            }
+                        if (++ss == NS) ss = 0;
+                        if (++ks == NK) {
+                            ks = 0;
+                            kpar ^= 1u;
                         }
+                    };
+                    for (int j = 0; j < min(NS, nt) && ok; ++j) {
+                        ok = mbar_wait_poll(&sh.k_full[ks], kpar, a.ws, 1012);
+                        if (!ok) break;
+                        tc_fence_after();
+                        score();
+                    }
+                    for (int j = 0; j < nt && ok; ++j) {
+                        // all that the tile's PV and the S behind it need first,
+                        // P last: both CTAs' softmax warps have written it (and
+                        // read the O of the part before this one)
+                        const bool more = j + NS < nt;
+                        ok = (!more || mbar_wait_poll(&sh.k_full[ks], kpar, a.ws, 1012)) &&
+                             mbar_wait_poll(&sh.v_full[vs], vpar, a.ws, 1014) &&
+                             (j > 0 || parts < 2 ||
+                              mbar_wait_poll<true>(&sh.o_free, parts & 1u, a.ws, 1016)) &&
+                             mbar_wait_poll<true>(&sh.p_full[ps], ppar, a.ws, 1013);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int steps = j == j_kv ? steps_kv : j == j_new ? steps_new : BKV / 16;
+                        const uint64_t dv = dv0 + vs * (Gm::VBytes >> 4);
+                        const uint32_t pa = tmem + Gm::ColS + ps * BKV;
+                        if (lead) {
+                            umma_bf16_pair_ts(tmem + Gm::ColO, pa, dv, idesc_o, j != 0);
+                            if (steps == BKV / 16) {
+#pragma unroll
+                                for (int kk = 1; kk < BKV / 16; ++kk)
+                                    umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o,
+                                                      1);
+                            } else {
+                                for (int kk = 1; kk < steps; ++kk)
+                                    umma_bf16_pair_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o,
+                                                      1);
+                            }
+                            umma_commit_pair(&sh.v_empty[vs], 0x3);
+                            umma_commit_pair(&sh.pv_done[pv & 1], 0x3);
+                            if (j + 1 == nt) umma_commit_pair(&sh.o_full, 0x3);
+                        }
+                        ++pv;
+                        if (++ps == NS) {
+                            ps = 0;
+                            ppar ^= 1u;
+                        }
+                        if (++vs == NV) {
+                            vs = 0;
+                            vpar ^= 1u;
+                        }
+                        if (more) score();               // into the buffer of this tile's P
                     }
                     ok = __all_sync(0xFFFFFFFFu, ok);
                 }
@@ -481,7 +485,14 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 const bool odd = special.at(j);  // else whole, and seen by every row
                 // a wait that runs out is noticed at the tile's end: what is
                 // computed until then reaches no memory but the outputs
-                ok = mbar_wait_poll(&sh.s_full[ss], (t / NS) & 1u, a.ws, 1022);
+                // (the other group's maximum is there before its next scores are)
+                float m_in = -INFINITY;
+                ok = true;
+                if (busy && j > 0) {
+                    ok = mbar_wait_poll(&sh.m_full[wg ^ 1][q], ((t - 1) >> 1) & 1u, a.ws, 1023);
+                    m_in = sh.m[wg ^ 1][rr];
+                }
+                ok &= mbar_wait_poll(&sh.s_full[ss], (t / NS) & 1u, a.ws, 1022);
                 tc_fence_after();
                 const uint32_t ts = tmem + lane_off + Gm::ColS + ss * BKV;
                 if (busy) {
@@ -511,11 +522,6 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                     }
                     const float tmax = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
                     // the reference moves when a tile exceeds it by 2^8
-                    float m_in = -INFINITY;
-                    if (j > 0) {
-                        ok &= mbar_wait_poll(&sh.m_full[wg ^ 1][q], ((t - 1) >> 1) & 1u, a.ws, 1023);
-                        m_in = sh.m[wg ^ 1][rr];
-                    }
                     const float m_new = m_in == -INFINITY || tmax > m_in + 8.f ? tmax : m_in;
                     sh.m[wg][rr] = m_new;
                     __syncwarp();
