@@ -214,6 +214,12 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
     }
 }
 
+// The lowest n bits, n limited to 0 .. 32.
+DG_DEVICE uint32_t column_bits(int n)
+{
+    return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 template <int D>
 __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const CUtensorMap *map_v,
                                                 const CUtensorMap *map_kn,
@@ -503,13 +509,19 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                     tmem_wait_ld();
                     if (odd) {
                         // first and last visible column
-                        const int valid = paged_valid<BKV>(p, p.tv0 + j);
-                        const int at = pos - paged_key0<BKV>(p, p.tv0 + j);
+                        const int valid = paged_valid<BKV>(p, p.tv0 + j), key0 = paged_key0<BKV>(p, p.tv0 + j);
+                        const int at = pos - key0;
                         const int c_hi = a.causal ? min(valid - 1, at) : valid - 1;
-                        const int c_lo = a.window > 0 ? at - a.window + 1 : 0;
+                        const int c_lo = a.window > 0 ? max(at - a.window + 1, 0) : 0;
 #pragma unroll
-                        for (int c = 0; c < BKV; ++c)
-                            if (c > c_hi || c < c_lo) sr[c] = __float_as_uint(-INFINITY);
+                        for (int c0 = 0; c0 < BKV; c0 += 32) {
+                            // 32 columns' visibility, a bit each
+                            const uint32_t seen = column_bits(c_hi - c0 + 1) & ~column_bits(c_lo - c0);
+                            if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) continue;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(seen >> c & 1u)) sr[c0 + c] = __float_as_uint(-INFINITY);
+                        }
                     }
                     // the scale is positive, so the scaled maximum is the maximum scaled
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

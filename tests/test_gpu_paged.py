@@ -236,8 +236,9 @@ def test_attention_cut_between_ctas(kernel, D, page, causal, window, fresh):
     check_attn(n, kv, 4, 2, D, page, causal, window, fresh, seed=3)
 
 
-@pytest.mark.parametrize("causal,window,fresh", MASKS)
-@pytest.mark.parametrize("n,kv,Hq,Hkv,D", [([640, 600], [2600, 1500], 32, 8, 128), ([0, 1500, 1], [40, 900, 7], 24, 8, 256)])
+@pytest.mark.parametrize("n,kv,Hq,Hkv,D,causal,window,fresh",
+                         [([640, 600], [1200, 500], 32, 8, 128, *m) for m in MASKS[:4] + [(True, 300, False)]]
+                         + [([0, 1500, 1], [40, 500, 7], 24, 8, 256, True, 0, True)])
 def test_attention_whole_items_then_a_cut_rest(n, kv, Hq, Hkv, D, causal, window, fresh):
     """More than two query tiles for every CTA pair, of unequal cost: whole ones in turn, then the cut rest."""
     tiles = sum(-(-m * (Hq // Hkv) // 256) * Hkv for m in n)
