@@ -27,12 +27,22 @@
 // others' columns); at the end they exchange their rows through shared memory.
 // P is multiplied as hi + lo, each bf16: hi = the bf16 below the one that p is cut
 // off to, lo = bf16(p - hi): neither is negative, nor zero where p is not, so that
-// an infinite value stays the infinity it is.  This kernel serves few rows, whose time is the memory's, so the second product is free, and the output
-// is off by little more than its own rounding (with one bf16 P by sqrt 2 of that).
+// an infinite value stays the infinity it is.  This kernel serves few rows, whose
+// time is the memory's, so the second product is free, and the output is off by
+// little more than its own rounding (with one bf16 P by sqrt 2 of that).
 // A tile whose end is past the last key is loaded, and multiplied with P,
 // only up to the next multiple of 16 keys; the softmax warps zero the V rows
 // between the last key and there, so that whatever bits the page holds behind
 // the sequence (0 x NaN) cannot reach the output.
+//
+// Bound by HBM: every key and value of a sequence is read once, by bulk copies
+// that run up to three tiles of each ahead (192 KB in flight per SM).  64 single
+// tokens over caches of 16000 tokens and less (16 query heads on 8, D = 128,
+// 2.2 GB): 318-329 us, 6.7-6.9 TB/s, 98-102% of a plain copy's rate; with the
+// columns of a tile in one warp it took 340.  One token over 300 keys takes
+// 12.4-12.8 us, a chain of latencies: launch, the division of the work (1.7 us),
+// the queries (1.5 us), the first K tile, three tiles of softmax, the join of the
+// four warps' rows (1.5 us) and the merge kernel, which finds nothing to do.
 #include "dg_paged.cuh"
 
 namespace dg {
@@ -573,9 +583,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 // caches may have parts from every SM) shares its parts out over the block's
 // threads and joins their results in shared memory.
 // Bound by latency, not bytes: the descriptors, then all of a thread's parts,
-// then the row.  A block per possible row group instead (2432 of them for one
-// 256-token canvas, most with nothing to do) took 12.4 us against this one's
-// few.
+// then the row.  One 256-token canvas over 4096 keys at D = 256, 16 items in about
+// 90 parts (22 MB, from L2 and HBM): 10 us from cold caches, about 6 behind the
+// kernel that wrote them.  A block per possible row group instead (2432 of them
+// there, most with nothing to do) took 12.4; 3, 4 and 6 parts in flight no less
+// than 2.
 struct MergeState {
     float M, den;
     float acc[16];

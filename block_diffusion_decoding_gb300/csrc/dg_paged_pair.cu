@@ -9,12 +9,16 @@
 // (2 x 512 cycles a tile at D = 128, 2 x 1024 at D = 256).
 //
 // One warpgroup's softmax of a 128 x 128 tile takes about 1800 cycles from
-// the arrival of S to that of P (TMEM loads 170, maximum 400, exponentials
-// and packing 900, stores and signals 300), more than the UMMAs of a tile.
+// the arrival of S to that of P (TMEM loads and maximum 450, the exchange of the
+// maximum 300, exponentials and packing 1000), more than the UMMAs of a tile.
 // So two warpgroups take the tiles in turn, and S is buffered (3 tiles at
 // D = 128, 2 at D = 256) far enough ahead of them.  The running maximum goes
 // from one to the other through shared memory right after each tile's
 // maximum, long before its exponentials; each keeps the sum of its own tiles.
+// P is rounded to one bf16 each (the sum keeps fp32): the tensor cores bound this
+// kernel, and a second half as in dg_paged_attn.cu would add half to their work.
+// The output is then off by sqrt 2 of its own rounding (2.3e-3 of its size against
+// 1.7e-3).
 //   TMEM        O [128 x D] fp32 | S buffers [128 x 128] fp32 (the bf16 P of a
 //               tile overwrites the S it came from);
 //   warp 0      TMA: K halves;    warp 2   TMA: V halves;    warp 3   the walk;
@@ -27,6 +31,19 @@
 // from some rows, dg_paged.cuh) each CTA's half lands on a barrier of its own,
 // and the arrival of P tells that it has been seen and is clean.  (With every
 // V half landing so the prompt chunks took 7% longer.)
+//
+// Four chunks of 723 to 2000 tokens over 9905 to 16384 keys (16 query heads on 8,
+// D = 128, causal, 0.69 TFLOP): 411 us at 1.7 PFLOP/s from a cool GPU, the tensor
+// pipe active 85% of the time; 446-480 us under load, where the power cap holds
+// the clock at about 1.65 GHz (a large library product sustains 1.72 PFLOP/s there,
+// 404 us).  What made the difference, in us under load: softmax on two
+// warpgroups in turn 675 -> 546, registers moved to them 533, whole query tiles in
+// turn so that K and V stay in L2 (dg_paged.cuh) 576 -> 505, load warps without
+// divisions 455, scores queued right behind the product that frees their buffer
+// 446.  Without the exponentials it was no faster, nor without the maximum.
+// Short work is a chain of latencies: one 256-token canvas over 4096 keys at
+// D = 256 takes 32.5 us, of which the tensor pipe is active a quarter: division
+// and first queries 6, first keys 3, 9 tiles 11, part rows out 3, merge 6.
 #include "dg_paged.cuh"
 
 namespace dg {

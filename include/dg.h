@@ -42,10 +42,12 @@
  *     count).  For testing and tuning, the environment variables
  *     DG_LM_KERNEL (single | duo | fused), DG_LM_BN (tile width),
  *     DG_LM_EPI (8 | 16: epilogue warps of the 2-SM kernel, bf16 operands),
- *     DG_ATTN_KERNEL (single | pair), DG_ATTN_SPLITS (key splits) and
- *     DG_ATTN_RESERVE (SMs kept for the attention in dg_canvas_step) force a
- *     choice; a choice the shapes do not allow is ignored.  Results do not
- *     depend on the choice beyond floating-point summation order.
+ *     DG_ATTN_KERNEL (single | pair), DG_ATTN_SPLITS (key splits),
+ *     DG_ATTN_RESERVE (SMs kept for the attention in dg_canvas_step) and
+ *     DG_PAGED_KERNEL (single | pair) force a choice; a choice the shapes do
+ *     not allow is ignored.  Results do not depend on the choice beyond
+ *     floating-point summation order (paged attention: and the rounding of the
+ *     softmax weights, one bf16 in the pair kernel, two in the single one).
  */
 #ifndef DG_H
 #define DG_H
@@ -78,9 +80,9 @@ int dg_version(void);
 /* no failure handling).  When on, the combine / acceptance kernels check    */
 /* every sampled and argmax index against [0, V), every entropy and the      */
 /* canvas total for finiteness and every rank of the acceptance's ordered    */
-/* positions against their count; the attention                               */
-/* kernels and the split merge check each row's softmax sum and outputs for  */
-/* finiteness; the MoE routing checks expert ids, positions and the token    */
+/* positions against their count; the attention kernels (paged ones          */
+/* included) and the split merges check each row's softmax sum and outputs   */
+/* for finiteness; the MoE routing checks expert ids, positions and the token */
 /* count.  A failed check records DG_ERR_DEVICE (and a location code) in the */
 /* call's workspace status word, read with dg_read_device_status (or        */
 /* dg_noalloc_read_device_status), and an out-of-range index is replaced by  */
