@@ -132,7 +132,6 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         mbar_init(drained, 1);
         mbar_init(x_full, 4);
         zeroed[0] = zeroed[1] = zeroed[2] = 0;
-        paged_ring_init(ring, 3 + 4);    // K, V, UMMA, softmax warps
         fence_barrier_init();
         tma_prefetch_desc(map_k);
         tma_prefetch_desc(map_v);
@@ -149,14 +148,24 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    tc_fence_before();
-    if (warp != 7) cta_sync();           // warp 7: once it has divided the work
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    // the walking warp needs nothing that the others set up, and they its ring
+    if (warp == 7) {
+        if (lane == 0) {
+            paged_ring_init(ring, 3 + 4);    // K, V, UMMA, softmax warps
+            fence_barrier_init();
+        }
+        __syncwarp();
+        start_arrive<kPagedThreads>();
+    } else {
+        tc_fence_before();
+        start_sync<kPagedThreads>();
+        tc_fence_after();
+    }
+    const uint32_t tmem = *tmem_slot;    // (not the walking warp's)
 
     if (warp == 7) {
         paged_walk<Gm>(a, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), ring, 927, nullptr,
-                       [] { cta_sync(); });
+                       [] {});
     } else if (warp == 0) {
         paged_ring_producer<Gm, NK>(smem + Gm::OffK, k_full, k_empty, map_k, map_kn, a, ring, 921);
     } else if (warp == 6) {

@@ -61,10 +61,29 @@ DG_DEVICE void reg_dec()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// __syncthreads() that the warps of a block may reach in different places.
-DG_DEVICE void cta_sync()
+// A barrier of THREADS threads, apart from __syncthreads()'s: those that wait at
+// it, and those that only arrive.
+template <int THREADS>
+DG_DEVICE void start_sync()
 {
-    asm volatile("bar.sync 0;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+template <int THREADS>
+DG_DEVICE void start_arrive()
+{
+    asm volatile("bar.arrive 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+// cluster_sync_all() in two halves.
+DG_DEVICE void cluster_arrive_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+DG_DEVICE void cluster_wait_all()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // A word of shared memory given by its cluster address.

@@ -300,7 +300,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         tmem_relinquish_pair();
     }
     // both CTAs' barriers exist before either signals the other; the walking
-    // warp comes to it when it has divided the work
+    // warp looks for that when it has divided the work
     auto together = [&]() -> uint32_t {
         tc_fence_before();
         cluster_sync_all();
@@ -315,8 +315,9 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         reg_dec<kPairOtherRegs>();
         if (warp == 3) {
             // (the maxima's place is free until the first part is known)
+            cluster_arrive_all();
             paged_walk<Gm>(a, unit, static_cast<int>(num_clusters_x()), sh.ring, 1007, sh.m,
-                           [&] { together(); });
+                           [] { cluster_wait_all(); });
         } else if (warp == 0) {
             together();
             pair_producer<Gm, false>(smem + Gm::OffK, sh, lead_of(sh.k_full), r, map_k, map_kn, a, 1001);

@@ -260,6 +260,32 @@ def test_attention_one_long_sequence(D, Hkv):
     check_attn([1], [20000], 2 * Hkv, Hkv, D, 64, True, 0, False, seed=5)
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_whole_items_of_many_sequences(wide, monkeypatch):
+    """More than 32 sequences with 16 items each and more, on CTA pairs; wide: a table of so many pages that the
+    work is divided in 64 bits."""
+    monkeypatch.setenv("DG_PAGED_KERNEL", "pair")
+    g = torch.Generator().manual_seed(31)
+    n = torch.randint(10, 40, (33,), generator=g).tolist()[:-2] + [140, 150]
+    kv = [m + int(k) for m, k in zip(n, torch.randint(10, 200, (33,), generator=g))]
+    check_attn_wide(n, kv, 32, 16, 128, 2048 if wide else 16, 1 << 14 if wide else 0)
+
+
+@pytest.mark.parametrize("n,kv,Hq,Hkv,D", [([1, 3, 1], [900, 64, 1], 16, 8, 128), ([90, 1, 200], [900, 64, 700], 6, 2, 256)])
+def test_division_in_64_bits(kernel, n, kv, Hq, Hkv, D):
+    """The same work with a table of 2^25 tokens' pages and with one that just fits: the same bits."""
+    kv = [max(k, m) for k, m in zip(kv, n)]
+    assert same_bits(check_attn_wide(n, kv, Hq, Hkv, D, 64, 1 << 19), check_attn_wide(n, kv, Hq, Hkv, D, 64, 0))
+
+
+def check_attn_wide(n, kv, Hq, Hkv, D, page, extra):
+    b = Batch(n, kv, kv, Hq, Hkv, D, page, seed=32, extra_width=extra)
+    out = run_attn(b, True, 0, False, kv)
+    want, bound = attention(b, True, 0, False, kv)
+    close(out, want, bound)
+    return out.cpu()
+
+
 def test_rows_that_see_nothing_are_zero(kernel):
     """Causal, with more new tokens than cached keys (their keys were not all appended): the first rows see none."""
     b, out = check_attn([12, 3], [5, 0], 4, 2, 128, 16, True, 0, False, seed=6)
