@@ -260,24 +260,21 @@ def _refuse(what: str, why: str):
 _BF16 = torch.bfloat16
 
 
-def _rows(t: torch.Tensor, heads: int, D: int, what: str, device: int, T: Optional[int] = None) -> int:
-    """The row stride of a bf16 tensor [T, heads, D] on the device whose rows are dense and apart."""
-    if t.dtype is not _BF16 or t.get_device() != device:
-        _refuse(what, "a bf16 tensor on the current device is wanted")
-    try:
-        (n, h, d), (s0, s1, s2) = t.shape, t.stride()
-    except ValueError:
-        _refuse(what, "a tensor [T, heads, D] is wanted")
-    if h != heads or d != D or (T is not None and n != T):
-        _refuse(what, "shape %s where [%s, %d, %d] is wanted"
-                % (tuple(t.shape), "T" if T is None else T, heads, D))
-    if n > 0 and ((s2 != 1 and D > 1) or (s1 != D and heads > 1)):
+def _rows(t: torch.Tensor, shape, what: str, device: int):
+    """Address and row stride of a bf16 tensor `shape` = (T, heads, D) on the device, whose rows
+    are dense and apart."""
+    if t.dtype is not _BF16 or t.get_device() != device or t.shape != shape:
+        _refuse(what, "a bf16 tensor %s on the current device is wanted, not %s %s on %s"
+                % (shape, t.dtype, tuple(t.shape), t.device))
+    n, heads, D = shape
+    s0, s1, s2 = t.stride()
+    if (s1 != D or s2 != 1) and n > 0 and ((s2 != 1 and D > 1) or (s1 != D and heads > 1)):
         _refuse(what, "the rows of a tensor are not dense")
     if n < 2:
-        return 0
+        return t.data_ptr(), 0
     if s0 < heads * D:   # (an expanded one: 0 means dense to the library)
         _refuse(what, "the rows of a tensor overlap")
-    return s0
+    return t.data_ptr(), s0
 
 
 def _ints(t: torch.Tensor, n: int, what: str, device: int):
@@ -299,10 +296,19 @@ def _heads_on(p: HeadParams, what: str, device: int):
         _refuse(what, "rope_steps and the norm weights are not on the current device")
 
 
-def _scratch(t: torch.Tensor, what: str, device: int) -> int:
+def _scratch(t: torch.Tensor, what: str, device: int):
+    """Address and size of a workspace."""
     if t.get_device() != device or not t.is_contiguous():
         _refuse(what, "a dense workspace on the current device is wanted")
-    return t.numel()
+    return t.data_ptr(), t.numel()
+
+
+def _stream_on(stream, device: int):
+    """_stream for a call whose device is known to be the current one."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+_NONE = (None, 0)   # address and stride of a tensor that is not given
 
 
 def rope_steps(inv_freq, device="cuda") -> torch.Tensor:
@@ -386,12 +392,13 @@ def qk_norm_rope(q, k, q_out, k_out, positions, p: HeadParams, stream=None):
     _heads_on(p, what, dev)
     if positions is not None:
         _ints(positions, T, what, dev)
+    q_shape, k_shape = (T, p.Hq, p.D), (T, p.Hkv, p.D)
     rc = _lib().dg_qk_norm_rope(
-        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, dev, T),
-        _p(k), 0 if k is None else _rows(k, p.Hkv, p.D, what, dev, T),
-        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, dev, T),
-        _p(k_out), 0 if k_out is None else _rows(k_out, p.Hkv, p.D, what, dev, T),
-        _p(positions), T, p.ref, _stream(stream))
+        *(_NONE if q is None else _rows(q, q_shape, what, dev)),
+        *(_NONE if k is None else _rows(k, k_shape, what, dev)),
+        *(_NONE if q_out is None else _rows(q_out, q_shape, what, dev)),
+        *(_NONE if k_out is None else _rows(k_out, k_shape, what, dev)),
+        _p(positions), T, p.ref, _stream_on(stream, dev))
     _check(rc, what)
 
 
@@ -412,12 +419,13 @@ def paged_append(k, v, cache: PagedCache, p: HeadParams, workspace, q=None, q_ou
         _ints(positions, T, what, dev)
     if kv_len_out is not None:
         _ints(kv_len_out, cache.B, what, dev)
+    q_shape, k_shape = (T, p.Hq, p.D), (T, p.Hkv, p.D)
     rc = _lib().dg_paged_append(
-        _p(k), _rows(k, p.Hkv, p.D, what, dev), _p(v), _rows(v, p.Hkv, p.D, what, dev, T),
-        _p(q), 0 if q is None else _rows(q, p.Hq, p.D, what, dev, T),
-        _p(q_out), 0 if q_out is None else _rows(q_out, p.Hq, p.D, what, dev, T),
-        _p(positions), T, p.ref, cache.ref, _p(kv_len_out), _p(workspace),
-        _scratch(workspace, what, dev), _stream(stream))
+        *_rows(k, k_shape, what, dev), *_rows(v, k_shape, what, dev),
+        *(_NONE if q is None else _rows(q, q_shape, what, dev)),
+        *(_NONE if q_out is None else _rows(q_out, q_shape, what, dev)),
+        _p(positions), T, p.ref, cache.ref, _p(kv_len_out), *_scratch(workspace, what, dev),
+        _stream_on(stream, dev))
     _check(rc, what)
 
 
@@ -432,13 +440,13 @@ def paged_attn(q, cache: PagedCache, out, scale, workspace, k_new=None, v_new=No
     what = "dg_paged_attn"
     T, Hq = q.shape[:2]
     dev = _on_current(cache.k, what)
+    q_shape, k_shape = (T, Hq, cache.D), (T, cache.Hkv, cache.D)
     rc = _lib().dg_paged_attn(
-        _p(q), _rows(q, Hq, cache.D, what, dev),
-        _p(k_new), 0 if k_new is None else _rows(k_new, cache.Hkv, cache.D, what, dev, T),
-        _p(v_new), 0 if v_new is None else _rows(v_new, cache.Hkv, cache.D, what, dev, T),
-        _p(out), _rows(out, Hq, cache.D, what, dev, T), T, Hq, scale, 1 if causal else 0,
-        min(window, 1 << 30), cache.ref, _p(workspace), _scratch(workspace, what, dev),
-        _stream(stream))
+        *_rows(q, q_shape, what, dev),
+        *(_NONE if k_new is None else _rows(k_new, k_shape, what, dev)),
+        *(_NONE if v_new is None else _rows(v_new, k_shape, what, dev)),
+        *_rows(out, q_shape, what, dev), T, Hq, scale, 1 if causal else 0, min(window, 1 << 30),
+        cache.ref, *_scratch(workspace, what, dev), _stream_on(stream, dev))
     _check(rc, what)
 
 

@@ -40,7 +40,7 @@
 // tokens over caches of 16000 tokens and less (16 query heads on 8, D = 128,
 // 2.2 GB): 318-329 us, 6.7-6.9 TB/s, 98-102% of a plain copy's rate; with the
 // columns of a tile in one warp it took 340.  One token over 300 keys takes
-// 12.4-12.8 us, a chain of latencies: launch, the division of the work (1.7 us),
+// 12.0-12.6 us, a chain of latencies: launch, the division of the work (1.7 us),
 // the queries (1.5 us), the first K tile, three tiles of softmax, the join of the
 // four warps' rows (1.5 us) and the merge kernel, which finds nothing to do.
 #include "dg_paged.cuh"

@@ -42,7 +42,7 @@
 // divisions 455, scores queued right behind the product that frees their buffer
 // 446.  Without the exponentials it was no faster, nor without the maximum.
 // Short work is a chain of latencies: one 256-token canvas over 4096 keys at
-// D = 256 takes 32.5 us, of which the tensor pipe is active a quarter: division
+// D = 256 takes 32.8 us, of which the tensor pipe is active a quarter: division
 // and first queries 6, first keys 3, 9 tiles 11, part rows out 3, merge 6.
 #include "dg_paged.cuh"
 

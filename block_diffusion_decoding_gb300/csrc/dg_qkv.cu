@@ -29,8 +29,8 @@
 // used): with a value's pair in another lane, and sines by shuffles, they were
 // first and the same pass took 265 us.  2, 3, 6 and 8 heads a group and blocks of
 // 256 and 512 threads were slower, as were the loads behind the staging of
-// q_start.  A few tokens are bound by the launch: 1.9 us on the GPU, 7.4 for the
-// call through the Python binding.
+// q_start.  A few tokens are bound by the launch: 1.9 us on the GPU, 7.4 for
+// the call through the Python binding.
 #include "dg_paged_kernels.h"
 
 namespace dg {

@@ -157,15 +157,21 @@ def test_binding_refuses_rows_that_overlap_and_other_devices(lib):
     """The library takes a row stride of 0 for dense rows: an expanded tensor must not reach it.  Tensors that
     stay on the host are refused where a call would hand their addresses to a kernel."""
     x = torch.zeros(1, 4, 128, dtype=torch.bfloat16)
-    assert dg._rows(x, 4, 128, "x", -1) == 0 and dg._rows(x.repeat(3, 1, 1), 4, 128, "x", -1, 3) == 512
-    assert dg._rows(torch.zeros(3, 1024, dtype=torch.bfloat16)[:, 512:].view(3, 4, 128), 4, 128, "x", -1) == 1024
-    for bad in (x.expand(3, 4, 128), torch.zeros(1, 1, 128, dtype=torch.bfloat16).expand(1, 4, 128),
+
+    def stride(t, T):
+        address, s0 = dg._rows(t, (T, 4, 128), "x", -1)
+        assert address == t.data_ptr()
+        return s0
+
+    assert stride(x, 1) == 0 and stride(x.repeat(3, 1, 1), 3) == 512 and stride(x[:0], 0) == 0
+    assert stride(torch.zeros(3, 1024, dtype=torch.bfloat16)[:, 512:].view(3, 4, 128), 3) == 1024
+    for bad in (x.expand(3, 4, 128), torch.zeros(3, 1, 128, dtype=torch.bfloat16).expand(3, 4, 128),
                 torch.zeros(3 * 512, dtype=torch.bfloat16).as_strided((3, 4, 128), (256, 128, 1)),
-                x.float(), x[0], x.view(1, 8, 64)):
+                torch.zeros(3, 128, 4, dtype=torch.bfloat16).mT, torch.zeros(3, 4, 128), x[0], x.view(1, 8, 64), x):
         with pytest.raises(dg.DgError):
-            dg._rows(bad, 4, 128, "x", -1)
+            stride(bad, 3)
     with pytest.raises(dg.DgError):
-        dg._rows(x, 4, 128, "x", 0)                  # not on that device
+        dg._rows(x, (1, 4, 128), "x", 0)             # not on that device
     with pytest.raises(dg.DgError):
         dg._ints(torch.zeros(4, dtype=torch.int32), 4, "x", 0)
     p = dg.head_params(4, 2, 128, rope_steps=dg.rope_steps([1.0] * 32, "cpu"))
