@@ -965,11 +965,12 @@ int launch_qkv(QkvArgs &a, bool paged, int sms, cudaStream_t st)
     // threads on, kQkvHeads a group save their shared instructions
     const int64_t heads = a.nq + (paged ? 2 : 1) * static_cast<int64_t>(a.nk);
     const bool many = a.T * heads * a.lanes > static_cast<int64_t>(sms) * 2048 * 2;
-    const int hpg = many ? kQkvHeads : 1;
+    const int hpg = many ? kQkvHeads * kQkvBatches : 1;
     a.q_chunks = (a.nq + hpg - 1) / hpg;
     a.k_chunks = (a.nk + hpg - 1) / hpg;
     a.chunks = a.q_chunks + (paged ? 2 : 1) * a.k_chunks;
-    const int64_t threads = static_cast<int64_t>(a.T) * a.chunks * a.lanes;
+    const int64_t gpw = 32 / a.lanes;   // groups of a warp, each of its own token
+    const int64_t threads = (a.T + gpw - 1) / gpw * a.chunks * 32;
     const int64_t blocks = std::max<int64_t>(1, (threads + kQkvThreads - 1) / kQkvThreads);
     // the kernel counts threads in 32 bits
     if (blocks * kQkvThreads > 0xFFFFFFFFLL) return DG_ERR_UNSUPPORTED;

@@ -30,7 +30,8 @@ struct QkvArgs {
     WsHeader *ws;
 };
 constexpr int kQkvThreads = 128;
-constexpr int kQkvHeads = 4;         // heads per group of the kernels for many tokens
+constexpr int kQkvHeads = 4;        // kernels for many tokens: heads whose loads a group has
+constexpr int kQkvBatches = 2;      // in flight, and how many times as many it takes
 constexpr int kQkvSeqSmem = 512;    // sequences whose first rows are staged in shared memory
 __global__ void qk_norm_rope_kernel_1(QkvArgs a);
 __global__ void qk_norm_rope_kernel_n(QkvArgs a);

@@ -82,10 +82,11 @@ DG_DEVICE int last_not_above(const int32_t *start, int n, int t)
 
 }  // namespace
 
-// A group takes up to HPG consecutive heads of one kind (q, k or v): their
-// loads are in flight together, and they share the lane's addresses, weights,
-// sines and cosines.
-template <bool PAGED, int HPG>
+// A group takes up to HPG x BATCH consecutive heads of one kind (q, k or v):
+// they share the lane's addresses, weights, sines and cosines, and the loads of
+// HPG of them are in flight together; without pages, those of the next HPG
+// behind them (into pages that took 15% longer where nothing is normed).
+template <bool PAGED, int HPG, int BATCH>
 __device__ __forceinline__ void qkv_body(const QkvArgs &a)
 {
     __shared__ int32_t s_start[PAGED ? kQkvSeqSmem : 1];
@@ -109,15 +110,18 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
         }
     }
 
-    const uint32_t unit = (blockIdx.x * static_cast<uint32_t>(kQkvThreads) + tid) >> a.lanes_log2;
-    const uint32_t tu = unit / static_cast<uint32_t>(a.chunks);
+    // the groups of a warp have the same heads of neighbouring tokens, so that
+    // all of it norms and rotates, or none
+    const uint32_t warp = (blockIdx.x * static_cast<uint32_t>(kQkvThreads) + tid) >> 5;
+    const uint32_t tw = warp / static_cast<uint32_t>(a.chunks);
+    const uint32_t tu = (tw << (5 - a.lanes_log2)) + ((tid & 31u) >> a.lanes_log2);
     const bool live = tu < static_cast<uint32_t>(a.T);
     const int t = live ? static_cast<int>(tu) : 0;
-    int c = static_cast<int>(unit - tu * a.chunks);
+    int c = static_cast<int>(warp - tw * a.chunks);
     const bool is_q = c < a.q_chunks, is_v = c >= a.q_chunks + a.k_chunks;
     c -= is_q ? 0 : is_v ? a.q_chunks + a.k_chunks : a.q_chunks;
-    const int h0 = c * HPG;
-    const int count = live ? min(HPG, (is_q ? a.nq : a.nk) - h0) : 0;   // heads of this group
+    const int h0 = c * (HPG * BATCH);
+    const int count = live ? min(HPG * BATCH, (is_q ? a.nq : a.nk) - h0) : 0;   // heads of this group
 
     // ---- the two runs of this lane: value offsets, angles of its pairs
     const int rl = a.interleaved ? 0 : a.rot >> 3;    // lanes with split runs
@@ -128,19 +132,20 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
     const bool turns = !is_v && (a.interleaved ? e0 < a.rot : split);
 
     uint2 lo[HPG], hi[HPG];
-    {
-        const uint16_t *src = (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride
-                                                                  : a.k + t * a.k_stride) +
-                              (h0 * a.D + e0);
+    const uint16_t *src = (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride
+                                                              : a.k + t * a.k_stride) +
+                          (h0 * a.D + e0);
+    auto load = [&](int first, uint2 (&l)[HPG], uint2 (&h)[HPG]) {
 #pragma unroll
         for (int j = 0; j < HPG; ++j, src += a.D) {
-            lo[j] = hi[j] = make_uint2(0, 0);
-            if (in_head && j < count) {
-                lo[j] = ld_stream(src);
-                hi[j] = ld_stream(src + gap);
+            l[j] = h[j] = make_uint2(0, 0);
+            if (in_head && first + j < count) {
+                l[j] = ld_stream(src);
+                h[j] = ld_stream(src + gap);
             }
         }
-    }
+    };
+    load(0, lo, hi);
 
     // ---- position, and the row of the cache that takes the token
     int pos = 0;
@@ -194,33 +199,6 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
         w[3] = add2(unpack2(wb.y), off);
     }
 
-    // ---- norms of all the group's heads together, so that their shuffles
-    // overlap; every lane of the warp takes part in them
-    float rn[HPG];
-    if (a.q_weight != nullptr || a.k_weight != nullptr) {
-#pragma unroll
-        for (int j = 0; j < HPG; ++j) {
-            float2 x = unpack2(lo[j].x);
-            float2 s2 = mul2(x, x);
-            x = unpack2(lo[j].y);
-            s2 = fma2(x, x, s2);
-            x = unpack2(hi[j].x);
-            s2 = fma2(x, x, s2);
-            x = unpack2(hi[j].y);
-            s2 = fma2(x, x, s2);
-            rn[j] = s2.x + s2.y;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            if (o < lg) {
-#pragma unroll
-                for (int j = 0; j < HPG; ++j) rn[j] += __shfl_xor_sync(0xFFFFFFFFu, rn[j], o);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < HPG; ++j) rn[j] = rsqrtf(rn[j] * a.inv_d + a.eps);
-    }
-
     uint16_t *dst;
     if (is_q)
         dst = a.q_out + t * a.qo_stride;
@@ -231,64 +209,103 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
     dst += h0 * a.D + e0;
     const int stores = token && in_head && (is_q || !PAGED || row >= 0) ? count : 0;
     const bool normed = wp != nullptr;
-    if (normed || turns) {        // else the bits go as they are
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+        uint2 next_lo[HPG], next_hi[HPG];
+        if (!PAGED && b + 1 < BATCH) load((b + 1) * HPG, next_lo, next_hi);
+        // ---- norms of all the group's heads together, so that their shuffles
+        // overlap; every lane of the warp takes part in them
+        float rn[HPG];
+        if (__any_sync(0xFFFFFFFFu, normed)) {
+#pragma unroll
+            for (int j = 0; j < HPG; ++j) {
+                float2 x = unpack2(lo[j].x);
+                float2 s2 = mul2(x, x);
+                x = unpack2(lo[j].y);
+                s2 = fma2(x, x, s2);
+                x = unpack2(hi[j].x);
+                s2 = fma2(x, x, s2);
+                x = unpack2(hi[j].y);
+                s2 = fma2(x, x, s2);
+                rn[j] = s2.x + s2.y;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                if (o < lg) {
+#pragma unroll
+                    for (int j = 0; j < HPG; ++j) rn[j] += __shfl_xor_sync(0xFFFFFFFFu, rn[j], o);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < HPG; ++j) rn[j] = rsqrtf(rn[j] * a.inv_d + a.eps);
+        }
+        if (normed || turns) {        // else the bits go as they are
+#pragma unroll
+            for (int j = 0; j < HPG; ++j) {
+                // x[0], x[1]: the first run, x[2], x[3]: the second
+                float2 x[4] = {unpack2(lo[j].x), unpack2(lo[j].y), unpack2(hi[j].x), unpack2(hi[j].y)};
+                if (normed) {
+                    const float2 r2 = make_float2(rn[j], rn[j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), w[e]);
+                }
+                if (!turns) {
+                    // (also where a value is infinite: no product with a zero sine)
+                } else if (a.interleaved) {
+                    // (x.x, x.y) is a pair
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float co = (e & 1) ? cs[e >> 1].y : cs[e >> 1].x;
+                        const float si = (e & 1) ? sn[e >> 1].y : sn[e >> 1].x;
+                        const float2 p = x[e];
+                        x[e] = make_float2(p.x * co - p.y * si, p.y * co + p.x * si);
+                    }
+                } else {
+                    // x[e] pairs with x[e + 2], component by component
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 p = x[e], q = x[e + 2];
+                        x[e] = fma2(q, ns[e], mul2(p, cs[e]));
+                        x[e + 2] = fma2(p, sn[e], mul2(q, cs[e]));
+                    }
+                }
+                lo[j] = make_uint2(pack2(x[0]), pack2(x[1]));
+                hi[j] = make_uint2(pack2(x[2]), pack2(x[3]));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < HPG; ++j, dst += a.D) {
+            if (b * HPG + j < stores) {
+                *reinterpret_cast<uint2 *>(dst) = lo[j];
+                *reinterpret_cast<uint2 *>(dst + gap) = hi[j];
+            }
+        }
+        if (PAGED && b + 1 < BATCH) load((b + 1) * HPG, lo, hi);
 #pragma unroll
         for (int j = 0; j < HPG; ++j) {
-            // x[0], x[1]: the first run, x[2], x[3]: the second
-            float2 x[4] = {unpack2(lo[j].x), unpack2(lo[j].y), unpack2(hi[j].x), unpack2(hi[j].y)};
-            if (normed) {
-                const float2 r2 = make_float2(rn[j], rn[j]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), w[e]);
+            if (!PAGED && b + 1 < BATCH) {
+                lo[j] = next_lo[j];
+                hi[j] = next_hi[j];
             }
-            if (!turns) {
-                // (also where a value is infinite: no product with a zero sine)
-            } else if (a.interleaved) {
-                // (x.x, x.y) is a pair
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float co = (e & 1) ? cs[e >> 1].y : cs[e >> 1].x;
-                    const float si = (e & 1) ? sn[e >> 1].y : sn[e >> 1].x;
-                    const float2 p = x[e];
-                    x[e] = make_float2(p.x * co - p.y * si, p.y * co + p.x * si);
-                }
-            } else {
-                // x[e] pairs with x[e + 2], component by component
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 p = x[e], q = x[e + 2];
-                    x[e] = fma2(q, ns[e], mul2(p, cs[e]));
-                    x[e + 2] = fma2(p, sn[e], mul2(q, cs[e]));
-                }
-            }
-            lo[j] = make_uint2(pack2(x[0]), pack2(x[1]));
-            hi[j] = make_uint2(pack2(x[2]), pack2(x[3]));
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < HPG; ++j, dst += a.D) {
-        if (j < stores) {
-            *reinterpret_cast<uint2 *>(dst) = lo[j];
-            *reinterpret_cast<uint2 *>(dst + gap) = hi[j];
         }
     }
 }
 
 __global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_1(QkvArgs a)
 {
-    qkv_body<false, 1>(a);
+    qkv_body<false, 1, 1>(a);
 }
 __global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_n(QkvArgs a)
 {
-    qkv_body<false, kQkvHeads>(a);
+    qkv_body<false, kQkvHeads, kQkvBatches>(a);
 }
 __global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_1(QkvArgs a)
 {
-    qkv_body<true, 1>(a);
+    qkv_body<true, 1, 1>(a);
 }
 __global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_n(QkvArgs a)
 {
-    qkv_body<true, kQkvHeads>(a);
+    qkv_body<true, kQkvHeads, kQkvBatches>(a);
 }
 
 }  // namespace dg
