@@ -23,14 +23,15 @@
 // Everything is fp32 until the one rounding to bf16 at the store.
 //
 // Bound by HBM where there are many tokens: 32768 tokens' 16 + 8 heads of 256
-// (0.8 GB read and written) take 132.7 us, 90% of a plain copy's rate; the append
-// of thirteen prompts' keys and values, 42185 tokens of 8 heads of 128, 57.6 us
-// (89%).  Issue slots come second (70%
-// used): with a value's pair in another lane, and sines by shuffles, they were
-// first and the same pass took 265 us.  2, 3, 6 and 8 heads a group and blocks of
-// 256 and 512 threads were slower, as were the loads behind the staging of
-// q_start.  A few tokens are bound by the launch: 1.9 us on the GPU, 7.4 for
-// the call through the Python binding.
+// (0.8 GB read and written) take 127.8 us, 93% of a plain copy's rate; the append
+// of thirteen prompts' keys and values, 42185 tokens of 8 heads of 128, 55.1 us
+// (93%); of 16 blocks of 256 with their queries, 134 MB, 25.6 us.  Issue slots come
+// second: with a value's pair in another lane, and sines by shuffles, the first of
+// these took 265 us, and with a position, a row and angles for every four heads
+// instead of eight 133 (the blocks 29.4).  Twelve heads a group, or four batches of
+// four or two, were slower, as were blocks of 256 and 512 threads, and the loads
+// behind the staging of q_start.  A few tokens are bound by the launch: 1.9 us on the
+// GPU, 7.4 for the call through the Python binding.
 #include "dg_paged_kernels.h"
 
 namespace dg {
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_1(QkvArgs a)
 {
     qkv_body<true, 1, 1>(a);
 }
-__global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_n(QkvArgs a)
+__global__ void __launch_bounds__(kQkvThreads, 8) paged_append_kernel_n(QkvArgs a)
 {
     qkv_body<true, kQkvHeads, kQkvBatches>(a);
 }
