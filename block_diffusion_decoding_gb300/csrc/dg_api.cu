@@ -961,11 +961,19 @@ void fill_qkv(QkvArgs &a, const dg_head_params *p, int T, int q_n, int k_n)
 // Launches the pass over T tokens' heads.
 int launch_qkv(QkvArgs &a, bool paged, int sms, cudaStream_t st)
 {
-    // one head a group spreads few tokens over the GPU; from two full loads of
-    // threads on, kQkvHeads a group save their shared instructions
-    const int64_t heads = a.nq + (paged ? 2 : 1) * static_cast<int64_t>(a.nk);
-    const bool many = a.T * heads * a.lanes > static_cast<int64_t>(sms) * 2048 * 2;
-    const int hpg = many ? kQkvHeads * kQkvBatches : 1;
+    // One head a group spreads few tokens over the GPU; more save their shared
+    // instructions.  By the threads that one head a group would take, in loads
+    // of the GPU's: four heads from 3/4 of a load on, into pages from half of one
+    // (norm of 16 + 8 heads, half a load: 2.98 us with one, 3.31 with four; a whole
+    // one: 4.64, 4.01; append 4.46, 4.21 and 7.49, 5.17), eight from 8 on where they fill their groups at
+    // least by half (norm, 4 loads: 9.89 with four, 10.8 with eight; 8: 16.7,
+    // 16.8; 80: 133, 128; append 10.8, 11.2; 17.5, 17.0; 13 loads: 28.4, 25.8.
+    // 4 + 1 heads, 8 loads: 25.6 with one, 22.2, 34.7).
+    const int kinds = paged ? 2 : 1;     // k, and v
+    const int64_t heads = a.nq + kinds * static_cast<int64_t>(a.nk);
+    const int64_t threads_1 = a.T * heads * a.lanes, load = static_cast<int64_t>(sms) * 2048;
+    const int64_t slots_8 = ((a.nq + 7) / 8 + kinds * static_cast<int64_t>((a.nk + 7) / 8)) * 8;
+    const int hpg = threads_1 > 8 * load && 2 * heads >= slots_8 ? 8 : 4 * threads_1 > (paged ? 2 : 3) * load ? 4 : 1;
     a.q_chunks = (a.nq + hpg - 1) / hpg;
     a.k_chunks = (a.nk + hpg - 1) / hpg;
     a.chunks = a.q_chunks + (paged ? 2 : 1) * a.k_chunks;
@@ -974,8 +982,12 @@ int launch_qkv(QkvArgs &a, bool paged, int sms, cudaStream_t st)
     const int64_t blocks = std::max<int64_t>(1, (threads + kQkvThreads - 1) / kQkvThreads);
     // the kernel counts threads in 32 bits
     if (blocks * kQkvThreads > 0xFFFFFFFFLL) return DG_ERR_UNSUPPORTED;
-    auto kern = paged ? (many ? paged_append_kernel_n : paged_append_kernel_1)
-                      : (many ? qk_norm_rope_kernel_n : qk_norm_rope_kernel_1);
+    auto kern = paged ? (hpg == 8   ? paged_append_kernel_8
+                         : hpg == 4 ? paged_append_kernel_4
+                                    : paged_append_kernel_1)
+                      : (hpg == 8   ? qk_norm_rope_kernel_8
+                         : hpg == 4 ? qk_norm_rope_kernel_4
+                                    : qk_norm_rope_kernel_1);
     DG_CUDA_TRY(launch_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQkvThreads), 0, st,
                               use_pdl(st), a));
     DG_LAUNCHED();

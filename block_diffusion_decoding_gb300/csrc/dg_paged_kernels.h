@@ -30,13 +30,14 @@ struct QkvArgs {
     WsHeader *ws;
 };
 constexpr int kQkvThreads = 128;
-constexpr int kQkvHeads = 4;        // kernels for many tokens: heads whose loads a group has
-constexpr int kQkvBatches = 2;      // in flight, and how many times as many it takes
 constexpr int kQkvSeqSmem = 512;    // sequences whose first rows are staged in shared memory
+// by the heads of a group
 __global__ void qk_norm_rope_kernel_1(QkvArgs a);
-__global__ void qk_norm_rope_kernel_n(QkvArgs a);
+__global__ void qk_norm_rope_kernel_4(QkvArgs a);
+__global__ void qk_norm_rope_kernel_8(QkvArgs a);
 __global__ void paged_append_kernel_1(QkvArgs a);
-__global__ void paged_append_kernel_n(QkvArgs a);
+__global__ void paged_append_kernel_4(QkvArgs a);
+__global__ void paged_append_kernel_8(QkvArgs a);
 
 // ---------------------------------------------------------------- paged attention
 // What a CTA left for the merge: slot 0 holds a part that continues an item

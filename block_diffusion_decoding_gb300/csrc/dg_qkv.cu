@@ -296,17 +296,25 @@ __global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_1(QkvArgs a)
 {
     qkv_body<false, 1, 1>(a);
 }
-__global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_n(QkvArgs a)
+__global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_4(QkvArgs a)
 {
-    qkv_body<false, kQkvHeads, kQkvBatches>(a);
+    qkv_body<false, 4, 1>(a);
+}
+__global__ void __launch_bounds__(kQkvThreads) qk_norm_rope_kernel_8(QkvArgs a)
+{
+    qkv_body<false, 4, 2>(a);
 }
 __global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_1(QkvArgs a)
 {
     qkv_body<true, 1, 1>(a);
 }
-__global__ void __launch_bounds__(kQkvThreads, 8) paged_append_kernel_n(QkvArgs a)
+__global__ void __launch_bounds__(kQkvThreads) paged_append_kernel_4(QkvArgs a)
 {
-    qkv_body<true, kQkvHeads, kQkvBatches>(a);
+    qkv_body<true, 4, 1>(a);
+}
+__global__ void __launch_bounds__(kQkvThreads, 8) paged_append_kernel_8(QkvArgs a)
+{
+    qkv_body<true, 4, 2>(a);
 }
 
 }  // namespace dg

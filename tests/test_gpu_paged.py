@@ -29,6 +29,8 @@ def heads_of(T, H, D, seed):
     (5, 16, 8, 128, 0, False, True, 0.0),
     (3, 2, 1, 48, 16, False, True, 0.0),
     (9001, 9, 3, 128, 96, False, True, 0.0),     # several heads a lane group, not a multiple of them
+    (3500, 17, 8, 256, 256, False, True, 1.0),   # twice as many
+    (7001, 17, 8, 128, 64, True, True, 1.0),
 ])
 @pytest.mark.parametrize("strided", [False, True])
 def test_norm_rope(T, Hq, Hkv, D, rot, interleaved, normed, offset, strided):
@@ -103,7 +105,9 @@ def test_infinities_outside_the_rotation_stay(interleaved):
     ([1, 1, 1, 1], [15, 16, 300, 31], 4, 2, 128, 16, 64, True, 3),
     ([5, 0, 40, 17], [0, 20, 47, 90], 16, 8, 256, 48, 256, False, 2),
     ([300, 1], [700, 63], 3, 1, 256, 64, 32, True, 0),
+    ([400, 1, 700], [10, 0, 77], 6, 2, 256, 32, 128, False, 0),
     ([2500, 1, 900, 4000], [13, 2047, 5, 0], 16, 8, 128, 128, 128, False, 1),
+    ([1700, 1200], [100, 0], 11, 9, 256, 64, 64, True, 2),
 ])
 @pytest.mark.parametrize("strided", [False, True])
 def test_append(n, kv, Hq, Hkv, D, page, rot, interleaved, pad, strided):
