@@ -1004,7 +1004,7 @@ int paged_slot_rows(int T, int G)
 // are device data): up to there the single CTA's query tile holds them.  16
 // sequences over 2000 keys, 16 heads on 8, single / pair, us: 128 rows 37.0 / 46.0
 // (D = 256: 54.4 / 68.1), 160 rows 69.0 / 46.7 (102.7 / 69.3); one sequence over
-// 4000: within 7% of each other from 32 to 160 rows.  DG_PAGED_KERNEL=single|pair
+// 4000: within 10% of each other from 32 to 160 rows.  DG_PAGED_KERNEL=single|pair
 // forces a choice.
 bool paged_pair(int T, int B, int G)
 {
