@@ -34,7 +34,7 @@
 //
 // Four chunks of 723 to 2000 tokens over 9905 to 16384 keys (16 query heads on 8,
 // D = 128, causal, 0.69 TFLOP): 411 us at 1.7 PFLOP/s from a cool GPU, the tensor
-// pipe active 85% of the time; 446-462 us under load, where the power cap holds
+// pipe active 85% of the time; 446-466 us under load, where the power cap holds
 // the clock at about 1.65 GHz (a large library product sustains 1.72 PFLOP/s there,
 // 404 us).  What made the difference, in us under load: softmax on two
 // warpgroups in turn 675 -> 546, registers moved to them 533, whole query tiles in
