@@ -83,6 +83,8 @@ struct PairShared {
     uint64_t m_full[2][4];            // by tile parity and lane quadrant
     uint64_t l_full[2][4];            // by warpgroup and lane quadrant
     uint64_t q_ready, o_full, o_free, drained;
+    uint64_t q_first;                 // the unit's first queries, once: a load warp may come to
+                                      // it any number of parts later
     uint32_t tmem;
     alignas(8) float m[2][128];       // running maximum after a tile, by its parity
     float l[2][128];                  // sum of a warpgroup's tiles of a part
@@ -161,7 +163,10 @@ __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint
             ok = mbar_wait_poll<false, kPagedLoadSleep>(&empty[s], par ^ 1u, a.ws, where);
             if (Gm::Dim == 256 && first && (IS_V || tv > p.tv0)) {
                 // the first tiles wait for nothing but the queries and K's first
-                ok &= mbar_wait_poll(&sh.q_ready, 0, a.ws, where);
+                // (not on q_ready: its phases go on with the parts, those of one
+                // tile have no second one to wait with, and a parity that has
+                // come round again would hold back what its next phase needs)
+                ok &= mbar_wait_poll(&sh.q_first, 0, a.ws, where);
                 first = false;
             }
             if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -278,6 +283,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
             }
         }
         mbar_init(&sh.q_ready, r == 0 ? 9 : 8);      // its softmax warps; the other CTA's all at once
+        mbar_init(&sh.q_first, 8);
         mbar_init(&sh.o_full, 1);
         mbar_init(&sh.o_free, 16);
         mbar_init(&sh.drained, 1);
@@ -482,7 +488,10 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_ready);
+            if (lane == 0) {
+                mbar_arrive(&sh.q_ready);
+                if (D == 256 && it == 0) mbar_arrive(&sh.q_first);   // (no tiles before: once)
+            }
         };
 
         PagedItem p;
