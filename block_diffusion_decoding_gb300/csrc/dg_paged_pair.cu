@@ -29,8 +29,9 @@
 // All copies of a tile complete on the even CTA's barrier.  Only where V is
 // looked at before its product (its tail, see dg_paged_attn.cu, and values hidden
 // from some rows, dg_paged.cuh) each CTA's half lands on a barrier of its own,
-// and the arrival of P tells that it has been seen and is clean.  (With every
-// V half landing so the prompt chunks took 7% longer.)
+// and the arrival of P tells that it has been seen and is clean: there it
+// releases memory, elsewhere it only tells of tcgen05 stores that have been waited
+// for.  (With every V half landing so the prompt chunks took 7% longer.)
 //
 // Four chunks of 723 to 2000 tokens over 9905 to 16384 keys (16 query heads on 8,
 // D = 128, causal, 0.69 TFLOP): 411 us at 1.7 PFLOP/s from a cool GPU, the tensor
@@ -88,8 +89,9 @@ struct PairShared {
     uint32_t tmem;
     alignas(8) float m[2][128];       // running maximum after a tile, by its parity
     float l[2][128];                  // sum of a warpgroup's tiles of a part
-    // by part modulo 3 and half of the dims: a hidden value of that half was
-    // zeroed (told to both CTAs; cleared a part later, two before it is used again)
+    // by part modulo 3 and half of the dims: the number (from 1) of the last part
+    // of which a hidden value of that half was zeroed (told to both CTAs; never
+    // cleared, which would have to be ordered with the other CTA's next word)
     uint32_t zeroed[3][2];
 };
 static_assert(sizeof(PairShared::m) >= kPagedUnits / 2 * sizeof(int64_t), "the division's sums");
@@ -618,20 +620,22 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                     uint32_t uses = landing >> vs;
                     special.each(j, [&](int x) { uses += static_cast<int>((it + x) % NV) == vs; });
                     ok &= mbar_wait_poll(&sh.v_land[vs], uses & 1u, a.ws, 1025);
-                    bool wrote = (valid & 15) != 0;
-                    if (wrote) paged_zero_tail<Gm>(v_tile, valid, threadIdx.x & 127);
+                    bool hid = false;                    // a value of this thread's key
+                    if (valid & 15) paged_zero_tail<Gm>(v_tile, valid, threadIdx.x & 127);
                     if (paged_border(a, paged_edge(a, p), paged_key0<BKV>(p, p.tv0 + j), valid) &&
                         paged_look<Gm>(v_tile, valid, threadIdx.x & 127)) {
-                        wrote = true;
-                        sh.zeroed[buf][r] = 1;
-                        st_cluster(mapa_shared(smem_u32(&sh.zeroed[buf][r]), r ^ 1), 1);
+                        hid = true;
+                        sh.zeroed[buf][r] = parts + 1;
+                        st_cluster(mapa_shared(smem_u32(&sh.zeroed[buf][r]), r ^ 1), parts + 1);
                     }
-                    wrote = __any_sync(0xFFFFFFFFu, wrote);
+                    hid = __any_sync(0xFFFFFFFFu, hid);
                     tc_fence_before();
                     __syncwarp();
+                    // Released: the landed V, zeros over it, and the word that
+                    // the other CTA is told by.  What stays in the even CTA needs
+                    // no more than its own scope.
                     if (lane == 0) {
-                        if (!wrote) mbar_arrive_cluster_relaxed(lead_of(&sh.p_full[ss]));
-                        else if (r == 0) mbar_arrive(&sh.p_full[ss]);
+                        if (r == 0 && !hid) mbar_arrive(&sh.p_full[ss]);
                         else mbar_arrive_cluster(lead_of(&sh.p_full[ss]));
                     }
                 } else {
@@ -668,7 +672,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                 }
                 continue;
             }
-            ok = mbar_wait_poll(&sh.o_full, parts & 1u, a.ws, 1027);
+            ok = mbar_wait_poll<true>(&sh.o_full, parts & 1u, a.ws, 1027);   // (and zeroed's words)
             if (busy && ok) {
                 // this group's sum in the reference of the last tile, which
                 // the other group may have set; then both groups' together.
@@ -695,12 +699,11 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
             if (done.kind != kPartWhole && live && wg == 0)
                 a.part_ml[static_cast<int64_t>(slot) * a.slot_rows + row] = make_float2(m_ref, l);
             // the sums are both groups'; so is the reference, for what is added now
-            if (busy && sh.zeroed[buf][wg] != 0)
+            if (busy && sh.zeroed[buf][wg] == parts)
                 paged_add_hidden<BKV, Half>(
                     a, done, to, wg * Half, live,
                     static_cast<int64_t>(done.s0 + i) * a.q_stride + static_cast<int64_t>(head) * D, pos,
                     m_ref);
-            if (q == 0 && lane == 0) sh.zeroed[(buf + 2) % 3][wg] = 0;
             const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
             bool badv = a.checks && live && !isfinite(l);
             if (busy)

@@ -29,3 +29,37 @@ def test_units_of_many_parts_at_head_dim_256(monkeypatch, causal, window, fresh,
     if not fresh:
         kv = [k + m for k, m in zip(kv, n)]
     check_attn(n, kv, 2, 2, 256, 16, causal, window, fresh, seed=62)
+
+
+@pytest.mark.parametrize("D,window,fresh", [(128, 0, True), (256, 0, True), (128, 90, False), (256, 300, True)])
+def test_hidden_values_in_every_border_tile(monkeypatch, D, window, fresh):
+    """Units of several parts, all of whose border tiles hold values that some rows must not know of, in either
+    CTA's half of the dims; in the next batch over the same workspace there are none.  The same bits every time."""
+    monkeypatch.setenv("DG_PAGED_KERNEL", "pair")
+    n, kv = [37 + 61 * (i % 5) for i in range(24)], [50 + 77 * (i % 7) for i in range(24)]
+    if not fresh:
+        kv = [k + m for k, m in zip(kv, n)]
+    clean = Batch(n, kv, kv, 2, 2, D, 16, seed=63)
+    b = Batch(n, kv, kv, 2, 2, D, 16, seed=63)
+    for i in range(24):
+        total = kv[i] + (n[i] if fresh else 0)
+        for key in range(total - n[i] + 3, total, 29):     # seen by the rows from there on only
+            for head in (0, 1):
+                dim = (key * 7 + head) % (D // 2) + (D // 2 if (key + head) % 2 else 0)
+                if key < kv[i]:
+                    b.v[b.table[i, key // 16], key % 16, head, dim] = float("inf")
+                else:
+                    b.vn[int(b.q_start[i]) + key - kv[i], head, dim] = float("inf")
+    want, bound = attention(b, True, window, fresh, kv)
+    ws = dg.workspace(dg.paged_attn_workspace(b.T, 2, b.cache(kv)), DEV)
+    first = None
+    for turn in range(6):
+        out = run_attn(b, True, window, fresh, kv, ws=ws)
+        ends = torch.isinf(want)
+        assert torch.equal(out.cpu().double()[ends], want[ends]) and ends.any()
+        fine = torch.isfinite(want)
+        assert ((out.cpu().double()[fine] - want[fine]).abs() <= bound[fine]).all()
+        first = out if first is None else first
+        assert same_bits(out, first)
+        if turn == 0:
+            close(run_attn(clean, True, window, fresh, kv, ws=ws), *attention(clean, True, window, fresh, kv))

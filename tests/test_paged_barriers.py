@@ -30,3 +30,19 @@ def test_a_wait_for_a_fixed_phase_is_on_a_barrier_that_is_used_once(name):
     fixed = {b for b, p in found if p.isdigit()}
     counted = {b for b, p in found if not p.isdigit()}
     assert not fixed & counted, fixed & counted
+
+
+def test_tiles_that_land_on_both_ctas_are_released_to_the_products():
+    """Where a V half lands on its own CTA's barrier, the arrival of P is the only sign to the even CTA's products
+    that the other half is there and clean, and that a value was zeroed: it has to release memory, in the odd CTA
+    and wherever a word was stored to the other one, at cluster scope."""
+    text = source("dg_paged_pair.cu")
+    landed = text[text.index("mbar_wait_poll(&sh.v_land[vs]"):]
+    tile = landed[:landed.index("} else {")]
+    assert "sh.p_full" in tile and "st_cluster(" in tile
+    assert "mbar_arrive_cluster(lead_of(&sh.p_full" in tile
+    assert "relaxed" not in tile
+    local = re.search(r"if \(([^()]*)\) mbar_arrive\(&sh\.p_full", tile)
+    assert local is None or local.group(1) == "r == 0 && !hid"
+    # the words stored to the other CTA are read behind a wait that acquires at that scope
+    assert "mbar_wait_poll<true>(&sh.o_full" in text
