@@ -54,6 +54,9 @@ inline uint64_t d2u(double f)
 struct DeviceInfo {
     int sms = 0;
     bool attrs_set = false;
+    // the paged attention's two kernels may be launched; no other call is
+    // refused where one may not
+    bool paged_single = false, paged_pair = false;
 };
 
 std::mutex g_mu;
@@ -107,25 +110,25 @@ int current_device_info(DeviceInfo **out)
         DG_CUDA_TRY(cudaFuncSetAttribute(attn_pair_kernel_d256,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          attn_pair_smem_bytes(256)));
-        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_kernel_d128,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         paged_attn_smem_bytes(128)));
-        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_kernel_d256,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         paged_attn_smem_bytes(256)));
-        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_pair_kernel_d128,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         paged_pair_smem_bytes(128)));
-        DG_CUDA_TRY(cudaFuncSetAttribute(paged_attn_pair_kernel_d256,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         paged_pair_smem_bytes(256)));
-        // its warps share the launch's registers out anew: fewer than they were
-        // counted on would be waited for forever
-        for (auto kern : {paged_attn_pair_kernel_d128, paged_attn_pair_kernel_d256}) {
+        auto smem = [](auto kern, int bytes) {
+            const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 bytes) == cudaSuccess;
+            if (!ok) (void)cudaGetLastError();
+            return ok;
+        };
+        // the pair's warps share the launch's registers out anew: fewer than
+        // they were counted on would be waited for forever
+        auto regs = [](auto kern) {
             cudaFuncAttributes fa;
-            DG_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
-            if (fa.numRegs < kPagedPairRegs) return DG_ERR_CUDA;
-        }
+            const bool ok = cudaFuncGetAttributes(&fa, kern) == cudaSuccess;
+            if (!ok) (void)cudaGetLastError();
+            return ok && fa.numRegs >= kPagedPairRegs;
+        };
+        di.paged_single = smem(paged_attn_kernel_d128, paged_attn_smem_bytes(128)) &&
+                          smem(paged_attn_kernel_d256, paged_attn_smem_bytes(256));
+        di.paged_pair = smem(paged_attn_pair_kernel_d128, paged_pair_smem_bytes(128)) &&
+                        smem(paged_attn_pair_kernel_d256, paged_pair_smem_bytes(256)) &&
+                        regs(paged_attn_pair_kernel_d128) && regs(paged_attn_pair_kernel_d256);
         di.attrs_set = true;
     }
     *out = &di;
@@ -1005,9 +1008,11 @@ int paged_slot_rows(int T, int G)
 // sequences over 2000 keys, 16 heads on 8, single / pair, us: 128 rows 37.0 / 46.0
 // (D = 256: 54.4 / 68.1), 160 rows 69.0 / 46.7 (102.7 / 69.3); one sequence over
 // 4000: within 10% of each other from 32 to 160 rows.  DG_PAGED_KERNEL=single|pair
-// forces a choice.
-bool paged_pair(int T, int B, int G)
+// forces a choice.  Where the pair kernel may not be launched the single one takes
+// every batch.
+bool paged_pair(const DeviceInfo &di, int T, int B, int G)
 {
+    if (!di.paged_pair) return false;
     const char *env = std::getenv("DG_PAGED_KERNEL");
     if (env && std::strcmp(env, "single") == 0) return false;
     if (env && std::strcmp(env, "pair") == 0) return true;
@@ -1245,7 +1250,8 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     if ((rc = current_device_info(&di)) != DG_OK) return rc;
     if (di->sms > kAssumedMaxSMs) return DG_ERR_UNSUPPORTED;
     const int D = c->D;
-    const bool pair = paged_pair(T, c->B, Hq / c->Hkv);
+    const bool pair = paged_pair(*di, T, c->B, Hq / c->Hkv);
+    if (!pair && !di->paged_single) return DG_ERR_CUDA;
     // keys of K and of V a CTA loads of a tile, dense; a box of the pages
     // stays inside one page and one such load: its rows divide both
     const int k_rows = pair || D == 256 ? 64 : 128, v_rows = pair || D == 128 ? 128 : 64;
