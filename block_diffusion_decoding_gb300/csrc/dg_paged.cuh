@@ -984,37 +984,64 @@ DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t
     }
 }
 
-// Sets those of 4 dims (from c0 on) of row `row` of the query tile for which a key
-// that the row sees has a value that is not finite to the sum of these products.
-// Every lane by itself.
-template <int BKV>
-DG_DEVICE void paged_sum_infinite(const PagedArgs &a, const PagedItem &p, int row, int c0,
-                                                float m_ref, float (&o)[4])
+// Which of N dims (from c0 on; a bit each) have an infinity of either sign, or a
+// NaN, in the value of a key of this part that token i of its rows sees.  A
+// softmax's weights are positive, so that is all that such values bring to a sum;
+// a key that is not finite itself has a score that is not, and makes NaN of them.
+struct PagedMarks {
+    uint64_t pos, neg, nan;
+};
+// The whole warp, a key a lane, so that a cache full of them (a sequence whose
+// values have overflowed) does not hold up the other sequences: 2000 such keys of 16
+// heads of 128 took 57 ms with each lane by itself and their weights worked out, so
+// that 40000 outlasted the other warps' waits; they take 0.7.
+template <int BKV, int N>
+__device__ __noinline__ PagedMarks paged_marks(const PagedArgs &a, const PagedItem &p, int i, int c0)
 {
-    const int nkp = (p.kv + BKV - 1) / BKV, frow = p.frow0 + row, i = frow / a.G;
-    const int64_t q_off = (p.s0 + i) * a.q_stride +
-                          static_cast<int64_t>(p.g * a.G + frow - i * a.G) * a.D;
+    PagedMarks m{0, 0, 0};
+    const int lane = threadIdx.x & 31;
+    const int nkp = (p.kv + BKV - 1) / BKV;
     const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
-    uint32_t found = 0;
 #pragma unroll 1
     for (int tv = p.tv0; tv < p.tv1; ++tv) {
         const int valid = paged_valid<BKV>(p, tv), key0 = paged_key0<BKV>(p, tv);
 #pragma unroll 1
-        for (int key = key0; key < key0 + valid; ++key) {
+        for (int c = lane; c < valid; c += 32) {
             PagedKey at;
-            if (!paged_sees(a, pos, key) || !paged_key(a, p, tv >= nkp, key, at)) continue;
-            const uint2 v = *reinterpret_cast<const uint2 *>(at.v + c0);
-            if (!not_finite(magnitude_max(0, make_uint4(v.x, v.y, 0, 0)))) continue;
-            const float w = paged_weight(a, at.k, q_off, m_ref);
+            if (!paged_sees(a, pos, key0 + c) || !paged_key(a, p, tv >= nkp, key0 + c, at)) continue;
+            uint32_t v = 0, k = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = __uint_as_float(static_cast<uint32_t>(at.v[c0 + e]) << 16);
-                if (isfinite(x)) continue;
-                o[e] = (found >> e & 1u) ? fmaf(w, x, o[e]) : w * x;
-                found |= 1u << e;
+            for (int d = 0; d < N; d += 8) v = magnitude_max(v, *reinterpret_cast<const uint4 *>(at.v + c0 + d));
+            if (!not_finite(v)) continue;
+#pragma unroll 1
+            for (int d = 0; d < a.D; d += 8) k = magnitude_max(k, *reinterpret_cast<const uint4 *>(at.k + d));
+            const bool no_weight = not_finite(k);
+#pragma unroll 1
+            for (int d = 0; d < N; ++d) {
+                const uint32_t x = at.v[c0 + d];
+                if ((x & 0x7F80u) != 0x7F80u) continue;
+                const uint64_t bit = 1ull << d;
+                if (no_weight || (x & 0x7Fu)) m.nan |= bit;
+                else if (x >> 15) m.neg |= bit;
+                else m.pos |= bit;
             }
         }
     }
+    auto any = [](uint64_t x) -> uint64_t {
+        return static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(x >> 32))) << 32 |
+               __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(x));
+    };
+    m.pos = any(m.pos);
+    m.neg = any(m.neg);
+    m.nan = any(m.nan);
+    return m;
+}
+// The sum's value in dim d (of those marked): else x.
+DG_DEVICE float paged_marked(const PagedMarks &m, int d, float x)
+{
+    const bool pos = m.pos >> d & 1u, neg = m.neg >> d & 1u;
+    if ((m.nan >> d & 1u) || (pos && neg)) return __int_as_float(0x7FC00000);
+    return pos ? INFINITY : neg ? -INFINITY : x;
 }
 
 // The rows of a V tile between its last key and the next multiple of 16, up

@@ -499,19 +499,21 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 ++swaps;
                 const int64_t first = tok * a.out_stride + static_cast<int64_t>(head) * D;
+                PagedMarks marks{0, 0, 0};
+                int marked = -1;                 // the token they are of
 #pragma unroll 1
                 for (int row0 = 0; row0 < p.rows; row0 += 32 / P4) {
                     const int row = row0 + lane / P4, piece = q * P4 + lane % P4;
                     const int64_t row_first = __shfl_sync(0xFFFFFFFFu, first, row & 31);
+                    float m = -INFINITY, sum = 0.f;
+                    float v[4] = {0.f, 0.f, 0.f, 0.f};
                     if (row < p.rows) {
                         float2 ml[4];
-                        float m = -INFINITY, sum = 0.f;
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             ml[h] = xml[h * Gm::FewRows + row];
                             if (ml[h].y != 0.f) m = fmaxf(m, ml[h].x);
                         }
-                        float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             if (ml[h].y == 0.f) continue;   // no key of its columns
@@ -524,11 +526,26 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                             v[2] = fmaf(f, t.z, v[2]);
                             v[3] = fmaf(f, t.w, v[3]);
                         }
-                        if (!(fabsf(v[0]) + fabsf(v[1]) + fabsf(v[2]) + fabsf(v[3]) < INFINITY)) {
-                            // an infinite value times the other warps' zeros is NaN
-                            paged_sum_infinite<BKV>(a, p, row, piece * 4, m, v);
-                            bad = true;
+                    }
+                    // an infinite value times the other warps' zeros is NaN
+                    const uint32_t odd = __ballot_sync(
+                        0xFFFFFFFFu, !(fabsf(v[0]) + fabsf(v[1]) + fabsf(v[2]) + fabsf(v[3]) < INFINITY));
+                    if (odd != 0) {
+                        bad = true;
+#pragma unroll 1
+                        for (int h = 0; h < 32 / P4; ++h) {   // the rows of this turn
+                            if ((odd >> (h * P4) & ((1u << P4) - 1u)) == 0) continue;
+                            const int i_h = (p.frow0 + row0 + h) / a.G;
+                            if (i_h != marked) {
+                                marks = paged_marks<BKV, D / 4>(a, p, i_h, q * (D / 4));
+                                marked = i_h;
+                            }
+                            if (lane / P4 != h) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = paged_marked(marks, lane % P4 * 4 + e, v[e]);
                         }
+                    }
+                    if (row < p.rows) {
                         if (whole) {
                             const float inv = (sum > 0.f) ? 1.f / sum : sum == 0.f ? 0.f : sum;
                             const __nv_bfloat162 lo2 = __floats2bfloat162_rn(v[0] * inv, v[1] * inv);

@@ -5,7 +5,7 @@ import torch
 import block_diffusion_decoding_gb300 as dg
 from tests._helpers import status_ok
 from tests._paged import DEV, NAN, Batch, attention, close
-from tests.test_gpu_paged import check_attn, run_attn, same_bits
+from tests.test_gpu_paged import check_attn, kernel, run_attn, same_bits  # noqa: F401 (kernel: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,86 @@ def test_hidden_values_in_every_border_tile(monkeypatch, D, window, fresh):
         assert same_bits(out, first)
         if turn == 0:
             close(run_attn(clean, True, window, fresh, kv, ws=ws), *attention(clean, True, window, fresh, kv))
+
+
+@pytest.mark.parametrize("D,Hq", [(256, 8), (128, 16), (128, 2)])
+def test_a_sequence_whose_values_have_overflowed_leaves_the_others_alone(monkeypatch, D, Hq):
+    """One sequence of a decode batch, 40000 keys long, with nothing but NaN, or infinities, in its values: the
+    others, whose parts the same CTAs work on, get the bits they get without it, and no wait runs out."""
+    monkeypatch.setenv("DG_PAGED_KERNEL", "single")
+    B, page, kv = 160, 64, 40000
+    P = kv // page
+    g = torch.Generator(device=DEV).manual_seed(71)
+    k = torch.randn(2 * P, page, 1, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    v = torch.randn(2 * P, page, 1, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    table = torch.arange(P, device=DEV, dtype=torch.int32).repeat(B, 1)
+    table[5] += P                               # the others share their pages
+    c = dg.PagedCache(k, v, table, torch.full((B,), kv, device=DEV, dtype=torch.int32),
+                      torch.arange(B + 1, device=DEV, dtype=torch.int32))
+    q = torch.randn(B, Hq, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    ws = dg.workspace(dg.paged_attn_workspace(B, Hq, c), DEV)
+
+    def run():
+        out = torch.full_like(q, 5.0)
+        dg.paged_attn(q, c, out, D ** -0.5, ws)
+        status_ok(ws)
+        return out
+
+    clean = run()
+    others = torch.arange(B, device=DEV) != 5
+    good = v[P:].clone()
+    inf = float("inf")
+    for fill, want in ((NAN, NAN), (inf, inf), (-inf, -inf)):
+        v[P:] = fill
+        got = run()
+        assert same_bits(got[others], clean[others])
+        row = got[5].float()
+        assert torch.isnan(row).all() if want != want else (row == want).all()
+    v[P:] = inf
+    v[P + 100, 7] = -inf
+    assert torch.isnan(run()[5]).all()
+    v[P:] = good
+    v[P + 3, 9, 0, 5], v[2 * P - 1, 63, 0, D - 1], v[P, 0, 0, D - 1], v[P + 9, 1, 0, D // 2] = inf, inf, -inf, NAN
+    got = run()
+    keep = torch.ones(D, dtype=torch.bool, device=DEV)
+    keep[[5, D // 2, D - 1]] = False
+    assert same_bits(got[others], clean[others]) and same_bits(got[5][:, keep], clean[5][:, keep])
+    assert (got[5][:, 5] == inf).all() and torch.isnan(got[5][:, [D // 2, D - 1]]).all()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 1), (256, 2, 1), (128, 6, 3)])
+@pytest.mark.parametrize("window,fresh", [(0, False), (0, True), (40, True)])
+def test_infinite_values_that_some_tokens_of_a_few_see(kernel, D, Hq, Hkv, window, fresh):
+    """Items of few rows but several tokens: infinities among the tokens' own values, which the earlier ones do
+    not see, and among the cached ones; and a key that is infinite itself, whose value is too."""
+    n, kv = [3, 2, 4, 1], [300, 7, 129, 500]
+    if not fresh:
+        kv = [k + m for k, m in zip(kv, n)]
+    b = Batch(n, kv, kv, Hq, Hkv, D, 32, seed=64, strided=True)
+    inf = float("inf")
+
+    def put(s, back, dim, value, which="v"):
+        """Into the key `back` before the last of sequence s."""
+        key = kv[s] + (n[s] if fresh else 0) - 1 - back
+        if key < kv[s]:
+            (b.k if which == "k" else b.v)[b.table[s, key // 32], key % 32, 0, dim] = value
+        else:
+            (b.kn if which == "k" else b.vn)[int(b.q_start[s]) + key - kv[s], 0, dim] = value
+
+    put(0, 0, 3, inf)
+    put(0, 1, D - 1, -inf)
+    put(0, 30, 17, inf)
+    put(0, 2, 17, -inf)
+    put(1, 1, D // 2, NAN)
+    put(2, 0, 40, -inf)
+    put(2, 3, 41, inf)
+    put(3, 20, 9, inf)
+    put(3, 20, 1, inf, "k")
+    out = run_attn(b, True, window, fresh, kv).cpu().double()
+    want, bound = attention(b, True, window, fresh, kv)
+    # sequence 3's row has an infinite score: NaN, or (minus infinity) no weight, times an infinite value
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.isnan(want).any()
+    ends = torch.isinf(want)
+    assert torch.equal(out[ends], want[ends]) and ends.any()
+    fine = torch.isfinite(want)
+    assert torch.isfinite(out[fine]).all() and ((out[fine] - want[fine]).abs() <= bound[fine]).all()
