@@ -106,7 +106,9 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
         for (int64_t b = static_cast<int64_t>(blockIdx.x) * kQkvThreads + tid; b < a.B;
              b += static_cast<int64_t>(gridDim.x) * kQkvThreads) {
             const int r0 = a.q_start[b], r1 = a.q_start[b + 1], kv = a.kv_len[b];
-            if (a.kv_len_out != nullptr) a.kv_len_out[b] = kv + r1 - r0;
+            // its rows as the attention counts them: those that the batch has
+            const int first = min(max(r0, 0), a.T), n = max(min(r1, a.T) - first, 0);
+            if (a.kv_len_out != nullptr) a.kv_len_out[b] = kv < 0 ? kv : kv + min(n, 0x7FFFFFFF - kv);
             if (r0 < 0 || r1 < r0 || r1 > a.T || kv < 0) report_error(a.ws, DG_ERR_DEVICE, 902);
         }
     }
@@ -158,9 +160,10 @@ __device__ __forceinline__ void qkv_body(const QkvArgs &a)
             const int b = last_not_above(start, a.B + 1, t);
             token = b >= 0 && b < a.B && t >= start[b] && t < start[b + 1];
             if (token) {
-                const int64_t at = static_cast<int64_t>(a.kv_len[b]) + (t - start[b]);
+                const int kv = a.kv_len[b];
+                const int64_t at = static_cast<int64_t>(kv) + (t - max(start[b], 0));
                 pos = a.positions != nullptr ? a.positions[t] : static_cast<int>(at);
-                if (at >= 0 && at < static_cast<int64_t>(a.max_pages) * a.page_size) {
+                if (kv >= 0 && at < static_cast<int64_t>(a.max_pages) * a.page_size) {
                     const uint32_t pg = static_cast<uint32_t>(at) / static_cast<uint32_t>(a.page_size);
                     const int page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pg];
                     if (page >= 0 && page < a.n_pages)

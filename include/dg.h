@@ -223,10 +223,12 @@ int dg_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int6
 /* cache stays.  positions [T] gives the rotation's positions; NULL: that    */
 /* place.  q, q_out (both or neither): the queries are normed and rotated in */
 /* the same pass.  kv_len_out [B] (or NULL; not kv_len itself) receives      */
-/* kv_len[b] + new tokens.  A token whose place lies past the table or whose */
-/* page id is bad is not stored (DG_ERR_DEVICE in the status word).  Two     */
-/* sequences must not append to one place.  workspace: 256 bytes, for the    */
-/* status word.  p->Hkv and p->D equal the cache's.                          */
+/* kv_len[b] + new tokens (those whose rows the batch has).  A token whose   */
+/* place lies past the table or whose page id is bad is not stored; nor is   */
+/* any of a sequence whose kv_len is negative, which it keeps (DG_ERR_DEVICE */
+/* in the status word each).  Two sequences must not append to one place.    */
+/* workspace: 256 bytes, for the status word.  p->Hkv and p->D equal the     */
+/* cache's.                                                                  */
 size_t dg_paged_append_workspace(void);
 int dg_paged_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
                     const uint16_t *q, int64_t q_stride, uint16_t *q_out, int64_t q_out_stride,

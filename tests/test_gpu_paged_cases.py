@@ -146,3 +146,35 @@ def test_infinite_values_that_some_tokens_of_a_few_see(kernel, D, Hq, Hkv, windo
     assert torch.equal(out[ends], want[ends]) and ends.any()
     fine = torch.isfinite(want)
     assert torch.isfinite(out[fine]).all() and ((out[fine] - want[fine]).abs() <= bound[fine]).all()
+
+
+@pytest.mark.parametrize("start,kv", [([-4, 2, 8], [14, 3]), ([0, 4, 90], [14, 3]), ([3, 6, 1000], [0, 20]),
+                                      ([-10 ** 9, 8, 8], [5, 7]), ([0, 12, 12], [-3, 9]), ([0, 6, 2], [4, 9]),
+                                      ([0, 4, 8], [2 ** 31 - 2, 1])])
+def test_append_cuts_its_rows_as_the_attention_does(start, kv):
+    """Row starts that leave the batch and lengths that cannot be: reported; the tokens there are lie where the
+    attention looks for them, the new lengths count those, and a negative length stores nothing and stays."""
+    T, page, cap = 12, 16, 48
+    b = Batch([6, 6], [18, 30], [48, 48], 2, 1, 128, page, seed=65)
+    c = b.cache(kv)
+    c.q_start.copy_(torch.tensor(start, dtype=torch.int32))
+    k0, v0 = c.k.cpu(), c.v.cpu()
+    ws = dg.workspace(256, DEV)
+    lens = torch.full((2,), 77, dtype=torch.int32, device=DEV)
+    dg.paged_append(b.kn.to(DEV), b.vn.to(DEV), c, dg.head_params(2, 1, 128), ws, kv_len_out=lens)
+    assert dg.read_device_status(ws, clear=True) == 7
+    after = []
+    for s in range(2):
+        first = min(max(start[s], 0), T)
+        end = max(min(start[s + 1], T), first)
+        if kv[s] < 0:
+            after.append(kv[s])
+            continue
+        after.append(min(kv[s] + end - first, 2 ** 31 - 1))
+        for t in range(first, end):
+            at = kv[s] + t - first
+            if at < cap:
+                k0[b.table[s, at // page], at % page] = b.kn[t]
+                v0[b.table[s, at // page], at % page] = b.vn[t]
+    assert lens.tolist() == after
+    assert same_bits(c.k, k0) and same_bits(c.v, v0)
