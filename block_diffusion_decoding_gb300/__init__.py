@@ -356,10 +356,15 @@ class PagedCache:
         if k.dim() != 4:
             _refuse(what, "k and v are [n_pages, page_size, Hkv, D]")
         n_pages, page_size, Hkv, D = k.shape
-        if v.shape != k.shape or v.stride() != k.stride():
-            _refuse(what, "k and v differ in shape or strides")
-        if k.stride()[1:] != (Hkv * D, D, 1):
-            _refuse(what, "the tokens of a page are not dense")
+        if v.shape != k.shape:
+            _refuse(what, "k and v differ in shape")
+        for t in (k, v):
+            # (strides of dimensions of one element say nothing)
+            if any(n > 1 and t.stride(i) != s
+                   for i, n, s in ((1, page_size, Hkv * D), (2, Hkv, D), (3, D, 1))):
+                _refuse(what, "the tokens of a page are not dense")
+        if n_pages > 1 and v.stride(0) != k.stride(0):
+            _refuse(what, "the pages of k and v are not equally far apart")
         if n_pages > 1 and k.stride(0) < page_size * Hkv * D:
             _refuse(what, "the pages overlap")
         if page_table.dim() != 2:

@@ -178,3 +178,31 @@ def test_append_cuts_its_rows_as_the_attention_does(start, kv):
                 v0[b.table[s, at // page], at % page] = b.vn[t]
     assert lens.tolist() == after
     assert same_bits(c.k, k0) and same_bits(c.v, v0)
+
+
+def test_page_layouts_that_are_dense_all_the_same():
+    """Dimensions of one element have strides that say nothing: one kv head taken from a pool laid out by heads,
+    a pool of one page.  They work; pools that are not dense are refused as before."""
+    n, kv, page, D = [1, 5], [40, 17], 16, 128
+    b = Batch(n, kv, kv, 4, 1, D, page, seed=66)
+    want = run_attn(b, True, 0, False, kv)
+    c = b.cache()
+    by_head = [torch.empty(b.n_pages, 1, page, D, dtype=torch.bfloat16, device=DEV).copy_(t.transpose(1, 2))
+               .transpose(1, 2) for t in (c.k, c.v)]
+    by_head[0] = by_head[0].as_strided(by_head[0].shape, (page * D, D, 12345, 1))
+    assert by_head[0].stride() != c.k.stride() and by_head[0].stride() != by_head[1].stride()
+    ws = dg.workspace(dg.paged_attn_workspace(b.T, 4, c), DEV)
+    out = torch.empty_like(b.q, device=DEV)
+    dg.paged_attn(b.q.to(DEV), dg.PagedCache(*by_head, c.page_table, c.kv_len, c.q_start), out, b.scale, ws)
+    status_ok(ws)
+    assert same_bits(out, want)
+    one = [t[2:3].as_strided((1, page, 1, D), (s, D, D, 1)) for t, s in ((c.k, 8), (c.v, 16 * D))]
+    dg.PagedCache(*one, c.page_table, c.kv_len, c.q_start)
+    for bad in ([c.k, c.v[::2]], [c.k, c.v.float()], [c.k[..., ::2], c.v[..., ::2]],
+                [c.k[:, ::2], c.v[:, ::2]],
+                [c.k[::2], c.v[:c.k[::2].shape[0]]], [c.k[:1].expand_as(c.k), c.v[:1].expand_as(c.v)]):
+        with pytest.raises(dg.DgError):
+            dg.PagedCache(*bad, c.page_table, c.kv_len, c.q_start)
+    two = torch.empty(b.n_pages, 2, page, D, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
+    with pytest.raises(dg.DgError):      # two heads laid out by heads: not a token's row
+        dg.PagedCache(two, two, c.page_table, c.kv_len, c.q_start)
