@@ -997,9 +997,11 @@ int launch_qkv(QkvArgs &a, bool paged, int sms, cudaStream_t st)
     return DG_OK;
 }
 
-int paged_slot_rows(int T, int G)
+// Rows of a part slot: a query tile's, or all there are.
+int paged_slot_rows(bool pair, int T, int G)
 {
-    return static_cast<int>(std::min<int64_t>(kPagedPairRows, static_cast<int64_t>(T) * G));
+    return static_cast<int>(std::min<int64_t>(pair ? kPagedPairRows : kPagedPairRows / 2,
+                                              static_cast<int64_t>(T) * G));
 }
 
 // Whether a batch runs on 2-CTA clusters with query tiles of 256 rows: when its
@@ -1019,18 +1021,19 @@ bool paged_pair(const DeviceInfo &di, int T, int B, int G)
     return static_cast<int64_t>(T) * G > 128LL * B;
 }
 
-// Workspace of the paged attention for `ctas` CTAs: header | descriptors |
-// (max, sum) of the part rows | part rows (fp32).
+// Workspace of the paged attention for `units` CTAs, or pairs of them: header |
+// descriptors | (max, sum) of the part rows | part rows (fp32).  Pairs are half as
+// many with at most twice the rows, so that of the CTAs holds theirs too.
 struct PagedWs {
     size_t desc, ml, o, total;
 };
 
-PagedWs paged_ws(int ctas, int rows, int D)
+PagedWs paged_ws(int units, int rows, int D)
 {
     PagedWs w{};
-    const size_t slots = 2 * static_cast<size_t>(ctas) * rows;
+    const size_t slots = 2 * static_cast<size_t>(units) * rows;
     w.desc = sizeof(WsHeader);
-    w.ml = w.desc + round_up(static_cast<size_t>(ctas) * sizeof(PagedDesc), 256);
+    w.ml = w.desc + round_up(static_cast<size_t>(units) * sizeof(PagedDesc), 256);
     w.o = w.ml + round_up(slots * sizeof(float2), 256);
     w.total = w.o + slots * D * sizeof(float);
     return w;
@@ -1215,7 +1218,7 @@ size_t dg_paged_attn_workspace(int T, int Hq, const dg_paged_cache *c)
 {
     if (c == nullptr || T < 0 || Hq < 1 || c->Hkv < 1 || Hq % c->Hkv != 0) return 0;
     if ((c->D != 128 && c->D != 256) || Hq / c->Hkv > 128) return 0;
-    return paged_ws(kAssumedMaxSMs, paged_slot_rows(std::max(T, 1), Hq / c->Hkv), c->D).total;
+    return paged_ws(kAssumedMaxSMs, paged_slot_rows(false, std::max(T, 1), Hq / c->Hkv), c->D).total;
 }
 
 int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
@@ -1313,17 +1316,17 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     a.small = paged_small(T, c->B, c->Hkv, a.G, static_cast<int64_t>(c->max_pages) * c->page_size) ? 1 : 0;
     a.checks = g_checks.load(std::memory_order_relaxed);
     a.scale_log2 = scale * 1.44269502162933349609375f;
-    a.slot_rows = paged_slot_rows(T, a.G);
+    a.slot_rows = paged_slot_rows(pair, T, a.G);
     a.out_wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && out_stride % 16 == 0 ? 1 : 0;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const PagedWs w = paged_ws(di->sms, a.slot_rows, D);
+    const int units = pair ? di->sms / 2 : di->sms;
+    const PagedWs w = paged_ws(units, a.slot_rows, D);
     a.ws = reinterpret_cast<WsHeader *>(ws);
     a.desc = reinterpret_cast<PagedDesc *>(ws + w.desc);
     a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
     a.part_o = reinterpret_cast<float *>(ws + w.o);
     cudaStream_t st = as_stream(stream);
     const bool pdl = use_pdl(st);
-    const int units = pair ? di->sms / 2 : di->sms;
     if (pair)
         DG_CUDA_TRY(launch_kernel(D == 128 ? paged_attn_pair_kernel_d128 : paged_attn_pair_kernel_d256,
                                   dim3(2 * units), dim3(kPagedPairThreads), paged_pair_smem_bytes(D),

@@ -206,3 +206,19 @@ def test_page_layouts_that_are_dense_all_the_same():
     two = torch.empty(b.n_pages, 2, page, D, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
     with pytest.raises(dg.DgError):      # two heads laid out by heads: not a token's row
         dg.PagedCache(two, two, c.page_table, c.kv_len, c.q_start)
+
+
+@pytest.mark.parametrize("D,n,kv", [(128, [300], [5000]), (256, [300], [5000]), (128, [1], [9000]), (256, [3], [9000]),
+                                    (128, [60], [4000]), (256, [64, 64], [3000, 4000])])
+def test_workspace_of_the_queried_size_is_enough(kernel, D, n, kv):
+    """Items cut between all the CTAs: nothing behind the workspace is written."""
+    b = Batch(n, kv, kv, 4, 2, D, 64, seed=67)
+    c = b.cache()
+    need = dg.paged_attn_workspace(b.T, 4, c)
+    room = dg.workspace(need + (1 << 20), DEV)
+    room[need:] = 0xA5
+    out = torch.empty_like(b.q, device=DEV)
+    dg.paged_attn(b.q.to(DEV), c, out, b.scale, room[:need])
+    status_ok(room)
+    assert (room[need:] == 0xA5).all()
+    close(out, *attention(b, True, 0, False, kv))
