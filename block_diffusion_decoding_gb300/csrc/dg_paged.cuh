@@ -380,6 +380,19 @@ DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, Paged
     }
 }
 
+// The unit whose stretch has place x of the line.  All lanes of the warp that
+// divided it.
+template <int ROWS, class I>
+DG_DEVICE int paged_unit_of(const PagedRange<I> &r, const I (&bound)[kPagedBounds<ROWS>], I x)
+{
+    if (r.step > 0) return static_cast<int>(paged_div<I>(x, r.step));
+    int n = 0;               // bounds that are not above
+    for (int k = 0; k < kPagedBounds<ROWS>; ++k)
+        n += __popc(__ballot_sync(0xFFFFFFFFu, (static_cast<int>(threadIdx.x) & 31) * kPagedBounds<ROWS> + k <
+                                                       r.units && bound[k] <= x));
+    return n - 1;
+}
+
 // One stretch's share of an item.
 struct PagedPart {
     int s0, n, kv;       // the sequence
@@ -588,14 +601,7 @@ DG_DEVICE void paged_walk_in(const PagedArgs &a, int u, int units, PagedRing &ri
                 a.page_table + static_cast<int64_t>(range.b) * a.max_pages + page));
     }
     walk.start(a, range, first);
-    auto unit_of = [&](I x) -> int {
-        if (range.step > 0) return static_cast<int>(paged_div<I>(x, range.step));
-        int n = 0;               // bounds that are not above
-        for (int k = 0; k < kPagedBounds<Gm::Rows>; ++k)
-            n += __popc(__ballot_sync(0xFFFFFFFFu, (static_cast<int>(threadIdx.x) & 31) * kPagedBounds<Gm::Rows> +
-                                                               k < units && bound[k] <= x));
-        return n - 1;
-    };
+    auto unit_of = [&](I x) -> int { return paged_unit_of<Gm::Rows>(range, bound, x); };
     PagedPart p;
     bool more = walk.next(a, p, unit_of);
     ready();
