@@ -20,9 +20,10 @@
 // whole while that leaves more than one for each, and the line's rest is cut so
 // that all have the same in the end.  So the pairs at work at one time are at
 // neighbouring items, which share a few heads' keys and values, and find them in
-// L2: in stretches of the whole line, four 2000-token chunks over 16384 keys had
-// every head of every sequence in use at once and read 2.4 GB from HBM of which
-// 0.29 GB is distinct, and took 576 us; so they read 0.29 GB and took 505.
+// L2: in stretches of the whole line, four chunks of up to 2000 tokens over up to
+// 16384 keys had every head of every sequence in use at once and read 2.4 GB from
+// HBM of which 0.29 GB is distinct, and took 576 us; so they read 0.29 GB and took
+// 505 (both with that build's slower load warps: dg_paged_pair.cu).
 #pragma once
 
 #include <type_traits>
@@ -59,8 +60,9 @@ DG_BOTH T paged_max(T a, T b)
 // item's fixed cost (its queries, pipeline fill, epilogue); what cutting a
 // batch's items costs every unit (parts and merge); the least a unit is given.
 // From sweeps over chunk and single-token batches: the pair's epilogue and merge
-// move 256 rows in fp32, about 8 us, 7 key tiles.  (Item 1152 or 1536 for the
-// pair: one canvas 33.9 us instead of 32.7; Cut 1536: no difference.)
+// move 256 rows in fp32, about 8 us, 7 key tiles.  (Item for the pair, by one
+// canvas of 256 tokens over 4096 keys alone: 1152 or 1536 33.9 us instead of 32.7.
+// Cut 1536: no difference.)
 template <int ROWS>
 struct PagedCost {
     static constexpr int Item = ROWS == 256 ? 768 : 512;
@@ -166,7 +168,8 @@ DG_BOTH bool paged_whole(const PagedArgs &a, I W, I items, I most, int units)
 
 // Whole items that every unit takes before the line's rest is cut (0: all of it
 // is).  Where a sequence's heads have few query tiles the pairs do not meet at a
-// head's keys, and the sums would cost more than they bring.
+// head's keys, and the sums would cost more than they bring.  (16 items a sequence,
+// and the sixteenth below, are estimates: neither was swept.)
 template <int ROWS>
 DG_BOTH int paged_rounds(const PagedArgs &a, int64_t items, int units)
 {
@@ -567,7 +570,8 @@ struct PagedRing {
     uint64_t full[kPagedItems], empty[kPagedItems];
 };
 // The walking warp waits for the slowest role, which may be a whole part
-// behind: that takes as long as the part does.
+// behind: that takes as long as the part does.  (So does the odd CTA's warp that
+// passes its queries on.  All other waits end after kWaitLimitNs.)
 constexpr uint64_t kPagedWalkLimitNs = 20000000000ull;
 
 // By one thread; `takers` arrivals free an entry.

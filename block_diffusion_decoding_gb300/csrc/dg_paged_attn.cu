@@ -38,7 +38,7 @@
 // Bound by HBM: every key and value of a sequence is read once, by bulk copies
 // that run up to three tiles of each ahead (192 KB in flight per SM).  64 single
 // tokens over caches of 16000 tokens and less (16 query heads on 8, D = 128,
-// 2.2 GB): 318-329 us, 6.7-6.9 TB/s, 98-102% of a plain copy's rate; with the
+// 2.2 GB): 326-329 us, 6.7 TB/s, 98-99% of a plain copy's rate; with the
 // columns of a tile in one warp it took 340.  One token over 300 keys takes
 // 12.0-12.6 us, a chain of latencies: launch, the division of the work (1.7 us),
 // the queries (1.5 us), the first K tile, three tiles of softmax, the join of the

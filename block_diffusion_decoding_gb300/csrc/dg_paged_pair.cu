@@ -34,17 +34,19 @@
 // for.  (With every V half landing so the prompt chunks took 7% longer.)
 //
 // Four chunks of 723 to 2000 tokens over 9905 to 16384 keys (16 query heads on 8,
-// D = 128, causal, 0.69 TFLOP): 411 us at 1.7 PFLOP/s from a cool GPU, the tensor
-// pipe active 85% of the time; 446-466 us under load, where the power cap holds
-// the clock at about 1.65 GHz (a large library product sustains 1.72 PFLOP/s there,
-// 404 us).  What made the difference, in us under load: softmax on two
+// D = 128, causal, 0.69 TFLOP): 443-470 us, 1.5 PFLOP/s, under load, where the power
+// cap holds the clock at about 1.65 GHz (a large library product sustains 1.72 there,
+// 404 us); profiled once, from a cool GPU, the tensor pipe was active 85% of 410 us.
+// What made the difference, in us under load: softmax on two
 // warpgroups in turn 675 -> 546, registers moved to them 533, whole query tiles in
 // turn so that K and V stay in L2 (dg_paged.cuh) 576 -> 505, load warps without
 // divisions 455, scores queued right behind the product that frees their buffer
 // 446.  Without the exponentials it was no faster, nor without the maximum.
 // Short work is a chain of latencies: one 256-token canvas over 4096 keys at
-// D = 256 takes 32.8 us, of which the tensor pipe is active a quarter: division
-// and first queries 6, first keys 3, 9 tiles 11, part rows out 3, merge 6.
+// D = 256 takes 32.7-33.7 us, of which the tensor pipe is active a quarter: division
+// and first queries 6, first keys 3, 9 tiles 11, part rows out 3, merge 6.  Five
+// blocks through a window of 1024 take 34.9-36.0; 0.7 of it since the tiles that
+// land on both CTAs release memory (relaxed, the products could have missed them).
 #include "dg_paged.cuh"
 
 namespace dg {

@@ -31,7 +31,7 @@
 // instead of eight 133 (the blocks 29.4).  Twelve heads a group, or four batches of
 // four or two, were slower, as were blocks of 256 and 512 threads, and the loads
 // behind the staging of q_start.  A few tokens are bound by the launch: 1.9 us on the
-// GPU, 7.4 for the call through the Python binding.
+// GPU, 7.0-7.6 for the call through the Python binding.
 #include "dg_paged_kernels.h"
 
 namespace dg {

@@ -47,7 +47,10 @@
  *     DG_PAGED_KERNEL (single | pair) force a choice; a choice the shapes do
  *     not allow is ignored.  Results do not depend on the choice beyond
  *     floating-point summation order (paged attention: and the rounding of the
- *     softmax weights, one bf16 in the pair kernel, two in the single one).
+ *     softmax weights, one bf16 in the pair kernel, two in the single one; the
+ *     pair kernel takes batches of more than 128 rows of a kv head, tokens x
+ *     its query heads, a sequence on average, so the last bits of a token's
+ *     row depend on what else is in its batch).
  */
 #ifndef DG_H
 #define DG_H
@@ -245,7 +248,8 @@ int dg_paged_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int6
 /*   causal = 1: keys up to pos, and with window > 0 only those after        */
 /*               pos - window.                                               */
 /*   out[q_start[b] + i, h, :] = softmax_j(scale q . k_j) v_j over those     */
-/*   keys; a token that sees no key gets a row of zeros.                     */
+/*   keys; a token that sees no key gets a row of zeros (as does one all of  */
+/*   whose scores are minus infinity).                                       */
 /* q, out [T, Hq, D]; rows *_stride elements apart as above; out overlaps no */
 /* input.  bf16 in and out, fp32 accumulation, softmax and partial results.  */
 /* The work is divided over the GPU on the device, from the lengths.         */
