@@ -54,9 +54,8 @@ inline uint64_t d2u(double f)
 struct DeviceInfo {
     int sms = 0;
     bool attrs_set = false;
-    // the paged attention's two kernels may be launched; no other call is
-    // refused where one may not
-    bool paged_single = false, paged_pair = false;
+    // the paged attention's two kernels (paged_kernels)
+    bool paged_single = false, paged_asked = false, paged_pair = false;
 };
 
 std::mutex g_mu;
@@ -110,29 +109,41 @@ int current_device_info(DeviceInfo **out)
         DG_CUDA_TRY(cudaFuncSetAttribute(attn_pair_kernel_d256,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          attn_pair_smem_bytes(256)));
-        auto smem = [](auto kern, int bytes) {
-            const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 bytes) == cudaSuccess;
-            if (!ok) (void)cudaGetLastError();
-            return ok;
-        };
-        // the pair's warps share the launch's registers out anew: fewer than
-        // they were counted on would be waited for forever
-        auto regs = [](auto kern) {
-            cudaFuncAttributes fa;
-            const bool ok = cudaFuncGetAttributes(&fa, kern) == cudaSuccess;
-            if (!ok) (void)cudaGetLastError();
-            return ok && fa.numRegs >= kPagedPairRegs;
-        };
-        di.paged_single = smem(paged_attn_kernel_d128, paged_attn_smem_bytes(128)) &&
-                          smem(paged_attn_kernel_d256, paged_attn_smem_bytes(256));
-        di.paged_pair = smem(paged_attn_pair_kernel_d128, paged_pair_smem_bytes(128)) &&
-                        smem(paged_attn_pair_kernel_d256, paged_pair_smem_bytes(256)) &&
-                        regs(paged_attn_pair_kernel_d128) && regs(paged_attn_pair_kernel_d256);
         di.attrs_set = true;
     }
     *out = &di;
     return DG_OK;
+}
+
+// Readies the paged attention's kernels, apart from the others', so that no other
+// call is refused where one of them may not be launched.  *pair: whether the pair
+// kernel may.  What the runtime refuses is asked for again at the next call.
+int paged_kernels(DeviceInfo &di, bool *pair)
+{
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto ok = [](cudaError_t e) {
+        if (e != cudaSuccess) (void)cudaGetLastError();
+        return e == cudaSuccess;
+    };
+    auto smem = [&](auto kern, int bytes) {
+        return ok(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    };
+    if (!di.paged_asked && smem(paged_attn_pair_kernel_d128, paged_pair_smem_bytes(128)) &&
+        smem(paged_attn_pair_kernel_d256, paged_pair_smem_bytes(256))) {
+        // its warps share the launch's registers out anew: fewer than they were
+        // counted on would be waited for forever
+        cudaFuncAttributes f128, f256;
+        if (ok(cudaFuncGetAttributes(&f128, paged_attn_pair_kernel_d128)) &&
+            ok(cudaFuncGetAttributes(&f256, paged_attn_pair_kernel_d256))) {
+            di.paged_asked = true;
+            di.paged_pair = f128.numRegs >= kPagedPairRegs && f256.numRegs >= kPagedPairRegs;
+        }
+    }
+    if (!di.paged_single)
+        di.paged_single = smem(paged_attn_kernel_d128, paged_attn_smem_bytes(128)) &&
+                          smem(paged_attn_kernel_d256, paged_attn_smem_bytes(256));
+    *pair = di.paged_pair;
+    return di.paged_single ? DG_OK : DG_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -1012,9 +1023,9 @@ int paged_slot_rows(bool pair, int T, int G)
 // 4000: within 10% of each other from 32 to 160 rows.  DG_PAGED_KERNEL=single|pair
 // forces a choice.  Where the pair kernel may not be launched the single one takes
 // every batch.
-bool paged_pair(const DeviceInfo &di, int T, int B, int G)
+bool paged_pair(bool possible, int T, int B, int G)
 {
-    if (!di.paged_pair) return false;
+    if (!possible) return false;
     const char *env = std::getenv("DG_PAGED_KERNEL");
     if (env && std::strcmp(env, "single") == 0) return false;
     if (env && std::strcmp(env, "pair") == 0) return true;
@@ -1253,8 +1264,9 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
     if ((rc = current_device_info(&di)) != DG_OK) return rc;
     if (di->sms > kAssumedMaxSMs) return DG_ERR_UNSUPPORTED;
     const int D = c->D;
-    const bool pair = paged_pair(*di, T, c->B, Hq / c->Hkv);
-    if (!pair && !di->paged_single) return DG_ERR_CUDA;
+    bool pair = false;
+    if ((rc = paged_kernels(*di, &pair)) != DG_OK) return rc;
+    pair = paged_pair(pair, T, c->B, Hq / c->Hkv);
     // keys of K and of V a CTA loads of a tile, dense; a box of the pages
     // stays inside one page and one such load: its rows divide both
     const int k_rows = pair || D == 256 ? 64 : 128, v_rows = pair || D == 128 ? 128 : 64;

@@ -43,7 +43,7 @@
 // divisions 455, scores queued right behind the product that frees their buffer
 // 446.  Without the exponentials it was no faster, nor without the maximum.
 // Short work is a chain of latencies: one 256-token canvas over 4096 keys at
-// D = 256 takes 32.7-33.7 us, of which the tensor pipe is active a quarter: division
+// D = 256 takes 32.7-33.9 us, of which the tensor pipe is active a quarter: division
 // and first queries 6, first keys 3, 9 tiles 11, part rows out 3, merge 6.  Five
 // blocks through a window of 1024 take 34.9-36.0; 0.7 of it since the tiles that
 // land on both CTAs release memory (relaxed, the products could have missed them).

@@ -129,3 +129,17 @@ def test_no_paged_kernel_at_all(fake_lib):
     lib = fake_lib(168, "paged_attn")
     assert others(lib) == [0, 0]
     assert attn(lib, 5) == (5, [])
+
+
+def test_a_refusal_of_the_runtime_does_not_last(fake_lib, monkeypatch):
+    """What failed once (while the runtime was busy with a capture, say) is asked for again."""
+    monkeypatch.delenv("DG_PAGED_KERNEL", raising=False)
+    lib = fake_lib(168, "paged_attn_pair_kernel_d256")
+    assert "paged_attn_kernel_d128" in attn(lib, 3000)[1][0][0]
+    lib.fake_set(168, b"")
+    for _ in range(2):
+        assert "paged_attn_pair_kernel_d128" in attn(lib, 3000)[1][0][0]
+    lib = fake_lib(168, "paged_attn")
+    assert attn(lib, 3000)[0] == 5
+    lib.fake_set(168, b"")
+    assert attn(lib, 3000)[0] == 0
