@@ -291,8 +291,6 @@ def _prepare_sample(s, c, gen, seed):
     s["u"] = torch.rand(R, generator=gen, device=DEV)
     s["token"] = torch.empty(R, device=DEV, dtype=torch.int32)
     s["logprob"] = torch.empty(R, device=DEV)
-    if own:
-        s["ws"] = dg.workspace(dg.sample_logits_workspace(R, V, s["logits"].dtype), DEV)
 
 
 def _prepare_commit(s, c, gen, seed):
@@ -420,7 +418,7 @@ def _run_attn(s):
 
 def _run_sample(s):
     if own:
-        dg.sample_logits(s["logits"], s["token"], s["u"], s["ws"], temperature=s["temperature"], top_k=s["top_k"],
+        dg.sample_logits(s["logits"], s["token"], s["u"], temperature=s["temperature"], top_k=s["top_k"],
                          top_p=s["top_p"], min_p=s["min_p"], logprob=s["logprob"])
         return {"token": s["token"], "logprob": s["logprob"]}
     x = s["logits"].float()
