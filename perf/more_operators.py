@@ -494,7 +494,7 @@ def _run_fork(s):
     src, dst, table = s["src"].long(), s["dst"].long(), s["table"]
     m = torch.arange(table.shape[1], device=DEV)
     # release
-    gone = m < (s["kv_len"][dst, None] + page - 1) // page
+    gone = table[dst] >= 0
     before = s["refs"] > 0
     s["refs"].index_add_(0, table[dst].long().clamp(min=0).flatten(), -gone.flatten().int())
     freed = before & (s["refs"] == 0)
@@ -503,6 +503,7 @@ def _run_fork(s):
     pad[place] = torch.arange(n_pages, device=DEV, dtype=torch.int32)
     s["free"].copy_(pad[:n_pages])
     s["n_free"] += freed.sum().int()
+    table[dst] = -1
     # fork
     kv = s["kv_len"][src]
     full, rest = (kv // page)[:, None], (kv % page)[:, None]
@@ -512,7 +513,7 @@ def _run_fork(s):
     place = s["n_free"].long() - need.cumsum(0)[:, 0]
     new = torch.where(need[:, 0], s["free"][place.clamp(min=0)], 0)
     old = table[src].gather(1, full.long())[:, 0].clamp(min=0).long()
-    table[dst] = torch.where(shared, table[src], torch.where((m == full) & need, new[:, None], table[dst]))
+    table[dst] = torch.where(shared, table[src], torch.where((m == full) & need, new[:, None], -1))
     s["refs"].index_add_(0, new.long(), need[:, 0].int())
     to = torch.where(need[:, 0], new.long(), old)            # (nothing to copy: a page onto itself)
     row = (torch.arange(page, device=DEV) < rest)[None, :, :, None, None]
