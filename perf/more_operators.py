@@ -219,7 +219,9 @@ def prepare(case, seed):
 
 
 def _prepare_plan(s, c, gen, seed):
-    n, kv = _lengths(c)
+    n, _ = _lengths(c)
+    r = random.Random(int(seed))
+    kv = [r.randrange(c["kv_max"] + 1000) for _ in n]
     page = 16
     n_pages, _ = _pages(gen, s, kv, page, c["B"])
     s["parents"] = _i32([p for tree in _trees(c, n, int(seed)) for p in tree])
