@@ -44,7 +44,12 @@ EXPORTED = ["dg_status_string", "dg_version", "dg_set_device_checks", "dg_device
             "dg_canvas_step_fp8_workspace", "dg_canvas_step_fp8",
             "dg_canvas_step_sc_workspace", "dg_canvas_step_sc", "dg_canvas_step_plan",
             "dg_rope_steps", "dg_qk_norm_rope", "dg_paged_append_workspace", "dg_paged_append",
-            "dg_paged_attn_workspace", "dg_paged_attn"]
+            "dg_paged_attn_workspace", "dg_paged_attn",
+            "dg_tree_plan_workspace", "dg_tree_plan", "dg_paged_tree_attn_workspace",
+            "dg_paged_tree_attn", "dg_paged_tree_commit_workspace", "dg_paged_tree_commit",
+            "dg_sample_logits", "dg_paged_reserve_workspace", "dg_paged_reserve",
+            "dg_paged_fork_workspace", "dg_paged_fork", "dg_paged_release_workspace",
+            "dg_paged_release"]
 
 
 class DgError(RuntimeError):
@@ -101,6 +106,11 @@ class PagedCacheArgs(ctypes.Structure):
                 ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
 
 
+class PagePoolArgs(ctypes.Structure):
+    _fields_ = [("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
+
+
 class CanvasStepPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in
                 ("attn_reserved_sms", "attn_pair", "attn_ctas", "attn_splits", "attn_key_tiles",
@@ -125,6 +135,7 @@ def _lib():
         ip = ctypes.POINTER(ctypes.c_int)
         i64 = ctypes.c_int64
         hp, pc = ctypes.POINTER(HeadParams), ctypes.POINTER(PagedCacheArgs)
+        pp = ctypes.POINTER(PagePoolArgs)
         sig = {
             "dg_status_string": ([i32], ctypes.c_char_p),
             "dg_version": ([], i32),
@@ -182,6 +193,21 @@ def _lib():
             "dg_paged_attn_workspace": ([i32, i32, pc], sz),
             "dg_paged_attn": ([vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, f32, i32, i32, pc, vp,
                                sz, vp], i32),
+            "dg_tree_plan_workspace": ([], sz),
+            "dg_tree_plan": ([vp, i32, i32, i32, vp, i32, vp, pc, vp, sz, vp], i32),
+            "dg_paged_tree_attn_workspace": ([i32, i32, pc], sz),
+            "dg_paged_tree_attn": ([vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, f32, i32, vp, i32,
+                                    vp, pc, vp, sz, vp], i32),
+            "dg_paged_tree_commit_workspace": ([], sz),
+            "dg_paged_tree_commit": ([vp, vp, vp, i32, i32, i64, pc, vp, i32, vp, vp, vp, vp, sz,
+                                      vp], i32),
+            "dg_sample_logits": ([vp, i32, i64, i32, i32] + [vp] * 8, i32),
+            "dg_paged_reserve_workspace": ([], sz),
+            "dg_paged_reserve": ([pp, pc, vp, sz, vp], i32),
+            "dg_paged_fork_workspace": ([i32], sz),
+            "dg_paged_fork": ([pp, pc, i32, i64, vp, vp, i32, vp, sz, vp], i32),
+            "dg_paged_release_workspace": ([], sz),
+            "dg_paged_release": ([pp, pc, vp, i32, vp, sz, vp], i32),
             "dg_canvas_step_plan": ([sp] + [i32] * 5 + [ctypes.POINTER(CanvasStepPlan)], i32),
         }
         for name, (args, res) in sig.items():
@@ -452,6 +478,195 @@ def paged_attn(q, cache: PagedCache, out, scale, workspace, k_new=None, v_new=No
         *(_NONE if v_new is None else _rows(v_new, k_shape, what, dev)),
         *_rows(out, q_shape, what, dev), T, Hq, scale, 1 if causal else 0, min(window, 1 << 30),
         cache.ref, *_scratch(workspace, what, dev), _stream_on(stream, dev))
+    _check(rc, what)
+
+
+# ---------------------------------------------------------------- drafted trees
+def tree_plan_workspace() -> int:
+    return int(_lib().dg_tree_plan_workspace())
+
+
+def _mask(mask: torch.Tensor, T: int, what: str, device: int):
+    """Address and words of a tree mask, a dense int32 tensor [T, words]."""
+    if (mask.dim() != 2 or mask.shape[0] != T or mask.dtype is not torch.int32
+            or not mask.is_contiguous() or mask.get_device() != device):
+        _refuse(what, "a dense int32 mask [%d, words] on the current device is wanted" % T)
+    return mask.data_ptr(), mask.shape[1]
+
+
+def tree_plan(parents, cache: PagedCache, mask, workspace, positions=None, window=0, appended=False,
+              stream=None):
+    """dg_tree_plan: parents [T] int32 -> mask [T, words] int32 (32 nodes a word) and
+    positions [T] int32; appended: the cache's kv_len counts the nodes."""
+    what = "dg_tree_plan"
+    T = parents.shape[0]
+    dev = _on_current(cache.k, what)
+    _ints(parents, T, what, dev)
+    if positions is not None:
+        _ints(positions, T, what, dev)
+    bits, words = _mask(mask, T, what, dev)
+    rc = _lib().dg_tree_plan(_p(parents), T, min(window, 1 << 30), 1 if appended else 0, bits, words,
+                             _p(positions), cache.ref, *_scratch(workspace, what, dev),
+                             _stream_on(stream, dev))
+    _check(rc, what)
+
+
+def paged_tree_attn_workspace(T, Hq, cache: PagedCache) -> int:
+    return int(_lib().dg_paged_tree_attn_workspace(T, Hq, cache.ref))
+
+
+def paged_tree_attn(q, cache: PagedCache, out, scale, workspace, mask, k_new=None, v_new=None,
+                    positions=None, window=0, stream=None):
+    """dg_paged_tree_attn: q, out [T, Hq, D] over the cache's pages, and over k_new, v_new
+    [T, Hkv, D] when given (rows may be strided); mask and positions as tree_plan makes
+    them (positions are needed with a window)."""
+    what = "dg_paged_tree_attn"
+    T, Hq = q.shape[:2]
+    dev = _on_current(cache.k, what)
+    q_shape, k_shape = (T, Hq, cache.D), (T, cache.Hkv, cache.D)
+    if positions is not None:
+        _ints(positions, T, what, dev)
+    rc = _lib().dg_paged_tree_attn(
+        *_rows(q, q_shape, what, dev),
+        *(_NONE if k_new is None else _rows(k_new, k_shape, what, dev)),
+        *(_NONE if v_new is None else _rows(v_new, k_shape, what, dev)),
+        *_rows(out, q_shape, what, dev), T, Hq, scale, min(window, 1 << 30),
+        *_mask(mask, T, what, dev), _p(positions), cache.ref, *_scratch(workspace, what, dev),
+        _stream_on(stream, dev))
+    _check(rc, what)
+
+
+def _layers(layers, cache: PagedCache, what: str):
+    """Number and distance of the layers of a pair of tensors [layers, n_pages, page_size,
+    Hkv, D] whose first is the cache's (None: the cache's alone)."""
+    if layers is None:
+        return 1, 0
+    for t, first in zip(layers, (cache.k, cache.v)):
+        if t.dtype is not _BF16 or t.dim() != 5 or t.shape[1:] != first.shape or t.shape[0] < 1:
+            _refuse(what, "bf16 layers [layers, n_pages, page_size, Hkv, D] of the cache's shape are wanted")
+        if t.data_ptr() != first.data_ptr() or t.stride()[1:] != first.stride():
+            _refuse(what, "the first layer is not the cache")
+    k, v = layers
+    if k.shape[0] != v.shape[0] or (k.shape[0] > 1 and k.stride(0) != v.stride(0)):
+        _refuse(what, "k's and v's layers are not alike")
+    return k.shape[0], k.stride(0) if k.shape[0] > 1 else 0
+
+
+def paged_tree_commit_workspace() -> int:
+    return int(_lib().dg_paged_tree_commit_workspace())
+
+
+def paged_tree_commit(tokens, parents, sampled, cache: PagedCache, path, n_path, next, kv_len_out,
+                      workspace, layers=None, stream=None):
+    """dg_paged_tree_commit: tokens, parents, sampled [T] int32 -> path [B, path_max],
+    n_path, next, kv_len_out [B] int32, the accepted nodes' keys and values moved in all
+    layers (see _layers)."""
+    what = "dg_paged_tree_commit"
+    T, B = tokens.shape[0], cache.B
+    dev = _on_current(cache.k, what)
+    for t in (tokens, parents, sampled):
+        _ints(t, T, what, dev)
+    for t in (n_path, next, kv_len_out):
+        _ints(t, B, what, dev)
+    if path.dim() != 2:
+        _refuse(what, "path is [B, path_max]")
+    path_max = path.shape[1]
+    _ints(path, B * path_max, what, dev)
+    n, apart = _layers(layers, cache, what)
+    rc = _lib().dg_paged_tree_commit(
+        _p(tokens), _p(parents), _p(sampled), T, n, apart, cache.ref, _p(path), path_max, _p(n_path),
+        _p(next), _p(kv_len_out), *_scratch(workspace, what, dev), _stream_on(stream, dev))
+    _check(rc, what)
+
+
+# ---------------------------------------------------------------- draws from logits
+def _floats(t, n: int, what: str, device: int):
+    if t is not None and (t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous()
+                          or t.get_device() != device):
+        _refuse(what, "a dense fp32 tensor of %d on the logits' device is wanted" % n)
+
+
+def sample_logits(logits, token, u, temperature=None, top_k=None, top_p=None, min_p=None,
+                  logprob=None, stream=None):
+    """dg_sample_logits: logits [R, V] bf16 or fp32 (rows may be strided) -> token [R]
+    int32, logprob [R] fp32; u, temperature, top_p, min_p [R] fp32, top_k [R] int32."""
+    what = "dg_sample_logits"
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        _refuse(what, "bf16 or fp32 logits [R, V] are wanted")
+    R, V = logits.shape
+    dev = _on_current(logits, what)
+    if V > 1 and logits.stride(1) != 1:
+        _refuse(what, "the rows of logits are not dense")
+    if R > 1 and logits.stride(0) < V:
+        _refuse(what, "the rows of logits overlap")
+    _ints(token, R, what, dev)
+    if top_k is not None:
+        _ints(top_k, R, what, dev)
+    for t in (u, temperature, top_p, min_p, logprob):
+        _floats(t, R, what, dev)
+    rc = _lib().dg_sample_logits(
+        logits.data_ptr(), 0 if logits.dtype is _BF16 else 1, logits.stride(0) if R > 1 else 0, R, V,
+        _p(temperature), _p(top_k), _p(top_p), _p(min_p), _p(u), _p(token), _p(logprob),
+        _stream_on(stream, dev))
+    _check(rc, what)
+
+
+# ---------------------------------------------------------------- page pool
+class PagePool:
+    """dg_page_pool of a cache: free_pages and refs [n_pages], n_free [1] int32.  The
+    calls write these, and the cache's page_table and kv_len."""
+
+    def __init__(self, cache: PagedCache, free_pages, n_free, refs):
+        what, n, dev = "PagePool", cache.k.shape[0], cache.k.get_device()
+        _ints(free_pages, n, what, dev)
+        _ints(refs, n, what, dev)
+        _ints(n_free, 1, what, dev)
+        self.cache, self.free_pages, self.n_free, self.refs = cache, free_pages, n_free, refs
+        self.args = PagePoolArgs(_p(free_pages), _p(n_free), _p(refs))
+        self.ref = ctypes.byref(self.args)
+
+
+def paged_reserve_workspace() -> int:
+    return int(_lib().dg_paged_reserve_workspace())
+
+
+def paged_reserve(pool: PagePool, workspace, stream=None):
+    """dg_paged_reserve: pages for the tokens of the cache's q_start behind its kv_len."""
+    what = "dg_paged_reserve"
+    dev = _on_current(pool.cache.k, what)
+    rc = _lib().dg_paged_reserve(pool.ref, pool.cache.ref, *_scratch(workspace, what, dev),
+                                 _stream_on(stream, dev))
+    _check(rc, what)
+
+
+def paged_fork_workspace(n: int) -> int:
+    return int(_lib().dg_paged_fork_workspace(n))
+
+
+def paged_fork(pool: PagePool, src, dst, workspace, layers=None, stream=None):
+    """dg_paged_fork: sequences dst [n] int32 become copies of sequences src [n]."""
+    what = "dg_paged_fork"
+    dev = _on_current(pool.cache.k, what)
+    n = src.numel()
+    _ints(src, n, what, dev)
+    _ints(dst, n, what, dev)
+    count, apart = _layers(layers, pool.cache, what)
+    rc = _lib().dg_paged_fork(pool.ref, pool.cache.ref, count, apart, _p(src), _p(dst), n,
+                              *_scratch(workspace, what, dev), _stream_on(stream, dev))
+    _check(rc, what)
+
+
+def paged_release_workspace() -> int:
+    return int(_lib().dg_paged_release_workspace())
+
+
+def paged_release(pool: PagePool, seqs, workspace, stream=None):
+    """dg_paged_release: the pages of sequences seqs [n] int32 are given back."""
+    what = "dg_paged_release"
+    dev = _on_current(pool.cache.k, what)
+    _ints(seqs, seqs.numel(), what, dev)
+    rc = _lib().dg_paged_release(pool.ref, pool.cache.ref, _p(seqs), seqs.numel(),
+                                 *_scratch(workspace, what, dev), _stream_on(stream, dev))
     _check(rc, what)
 
 

@@ -16,6 +16,7 @@
 #include "dg_kernels.h"
 #include "dg_paged.cuh"
 #include "dg_plan.h"
+#include "dg_serve_kernels.h"
 
 using namespace dg;
 
@@ -55,7 +56,10 @@ struct DeviceInfo {
     int sms = 0;
     bool attrs_set = false;
     // the paged attention's two kernels (paged_kernels)
-    bool paged_single = false, paged_asked = false, paged_pair = false;
+    struct Paged {
+        bool single = false, asked = false, pair = false;
+    } paged, tree;
+    bool sample_set = false;
 };
 
 std::mutex g_mu;
@@ -115,10 +119,22 @@ int current_device_info(DeviceInfo **out)
     return DG_OK;
 }
 
-// Readies the paged attention's kernels, apart from the others', so that no other
-// call is refused where one of them may not be launched.  *pair: whether the pair
-// kernel may.  What the runtime refuses is asked for again at the next call.
-int paged_kernels(DeviceInfo &di, bool *pair)
+// Readies the paged attention's kernels (a trees' or the others' four), apart from
+// the others', so that no other call is refused where one of them may not be
+// launched.  *pair: whether the pair kernel may.  What the runtime refuses is asked
+// for again at the next call.
+template <class Args>
+struct PagedKernels {
+    using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Args);
+    Kernel single[2], pair[2];           // by head dim: 128, 256
+};
+const PagedKernels<PagedArgs> kPagedKernels{{paged_attn_kernel_d128, paged_attn_kernel_d256},
+                                            {paged_attn_pair_kernel_d128, paged_attn_pair_kernel_d256}};
+const PagedKernels<PagedTreeArgs> kTreeKernels{{paged_tree_kernel_d128, paged_tree_kernel_d256},
+                                               {paged_tree_pair_kernel_d128, paged_tree_pair_kernel_d256}};
+
+template <class Args>
+int paged_kernels(const PagedKernels<Args> &kernels, DeviceInfo::Paged &di, bool *pair)
 {
     std::lock_guard<std::mutex> lk(g_mu);
     auto ok = [](cudaError_t e) {
@@ -128,22 +144,22 @@ int paged_kernels(DeviceInfo &di, bool *pair)
     auto smem = [&](auto kern, int bytes) {
         return ok(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
     };
-    if (!di.paged_asked && smem(paged_attn_pair_kernel_d128, paged_pair_smem_bytes(128)) &&
-        smem(paged_attn_pair_kernel_d256, paged_pair_smem_bytes(256))) {
+    if (!di.asked && smem(kernels.pair[0], paged_pair_smem_bytes(128)) &&
+        smem(kernels.pair[1], paged_pair_smem_bytes(256))) {
         // its warps share the launch's registers out anew: fewer than they were
         // counted on would be waited for forever
         cudaFuncAttributes f128, f256;
-        if (ok(cudaFuncGetAttributes(&f128, paged_attn_pair_kernel_d128)) &&
-            ok(cudaFuncGetAttributes(&f256, paged_attn_pair_kernel_d256))) {
-            di.paged_asked = true;
-            di.paged_pair = f128.numRegs >= kPagedPairRegs && f256.numRegs >= kPagedPairRegs;
+        if (ok(cudaFuncGetAttributes(&f128, kernels.pair[0])) &&
+            ok(cudaFuncGetAttributes(&f256, kernels.pair[1]))) {
+            di.asked = true;
+            di.pair = f128.numRegs >= kPagedPairRegs && f256.numRegs >= kPagedPairRegs;
         }
     }
-    if (!di.paged_single)
-        di.paged_single = smem(paged_attn_kernel_d128, paged_attn_smem_bytes(128)) &&
-                          smem(paged_attn_kernel_d256, paged_attn_smem_bytes(256));
-    *pair = di.paged_pair;
-    return di.paged_single ? DG_OK : DG_ERR_CUDA;
+    if (!di.single)
+        di.single = smem(kernels.single[0], paged_attn_smem_bytes(128)) &&
+                    smem(kernels.single[1], paged_attn_smem_bytes(256));
+    *pair = di.pair;
+    return di.single ? DG_OK : DG_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -1050,6 +1066,212 @@ PagedWs paged_ws(int units, int rows, int D)
     return w;
 }
 
+// ---------------------------------------------------------------- drafted trees, page pool
+constexpr int kMaskWords = 128;
+
+int check_status_ws(const void *workspace, size_t bytes, size_t need = sizeof(WsHeader))
+{
+    if (workspace == nullptr || bytes < need) return DG_ERR_WORKSPACE;
+    return aligned16(workspace) ? DG_OK : DG_ERR_ALIGNMENT;
+}
+
+// Layers whose pages lie layer_stride elements apart, none over another's: layer
+// after layer, or the layers of a page side by side.
+int check_layers(const dg_paged_cache *c, int64_t page_stride, int layers, int64_t layer_stride)
+{
+    if (layers < 1 || layer_stride < 0) return DG_ERR_INVALID_ARG;
+    if (layers > (1 << 16) || layer_stride > (1LL << 46)) return DG_ERR_UNSUPPORTED;
+    if (layer_stride % 8 != 0) return DG_ERR_ALIGNMENT;
+    if (layers == 1) return DG_OK;
+    using wide = unsigned __int128;
+    const wide page = static_cast<wide>(c->page_size) * c->Hkv * c->D, apart = static_cast<wide>(layer_stride);
+    const wide stride = static_cast<wide>(page_stride);
+    const bool after = apart >= stride * static_cast<wide>(c->n_pages - 1) + page;
+    const bool beside = apart >= page && (c->n_pages == 1 || stride >= apart * static_cast<wide>(layers - 1) + page);
+    return after || beside ? DG_OK : DG_ERR_INVALID_ARG;
+}
+
+int pool_args(PagePoolArgs &a, const dg_page_pool *pool, const dg_paged_cache *c, void *workspace, size_t bytes,
+              size_t need)
+{
+    const int rc = check_paged_cache(c, &a.page_stride);
+    if (rc != DG_OK) return rc;
+    if (!pool || !pool->free_pages || !pool->n_free || !pool->refs) return DG_ERR_INVALID_ARG;
+    a.free_pages = pool->free_pages;
+    a.n_free = pool->n_free;
+    a.refs = pool->refs;
+    a.page_table = const_cast<int32_t *>(c->page_table);
+    a.kv_len = const_cast<int32_t *>(c->kv_len);
+    a.q_start = c->q_start;
+    a.n_pages = c->n_pages;
+    a.max_pages = c->max_pages;
+    a.page_size = c->page_size;
+    a.B = c->B;
+    a.k = c->k;
+    a.v = c->v;
+    a.row = c->Hkv * c->D;
+    a.ws = static_cast<WsHeader *>(workspace);
+    return check_status_ws(workspace, bytes, need);
+}
+
+// ---------------------------------------------------------------- draws from logits
+constexpr int kSampleMaxV = 393216;      // 2^19 tokens' weights fit the sums
+
+int sample_kernels(DeviceInfo &di)
+{
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (di.sample_set) return DG_OK;
+    for (auto kern : {sample_bf16_kernel, sample_fp32_kernel}) {
+        DG_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         sample_smem_bytes(kSampleRows)));
+        DG_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    }
+    di.sample_set = true;
+    return DG_OK;
+}
+
+// CTAs that share a row, and the 512-byte pieces a warp of theirs keeps: few enough
+// that three CTAs' rows fit an SM, so that one's loads run beside the others' passes;
+// more where the rows would leave SMs idle.
+int sample_cluster(int type, int64_t stride, int R, int V, int sms, int *rows_warp)
+{
+    const int per = type == DG_LOGITS_BF16 ? 8 : 4;
+    const int skew = stride % per == 0 ? 0 : per - 1;
+    const int vecs = (V + skew + per - 1) / per;
+    auto rows = [&](int ctas) { return (vecs + ctas * kSampleThreads - 1) / (ctas * kSampleThreads); };
+    int ctas = 1;
+    while (ctas < kSampleCluster && rows(ctas) > 8) ctas *= 2;
+    while (ctas < 8 && rows(ctas) > 1 && static_cast<int64_t>(R) * ctas * 2 <= sms) ctas *= 2;
+    *rows_warp = rows(ctas);
+    return ctas;
+}
+
+// ---------------------------------------------------------------- paged attention
+// dg_paged_attn (Args: PagedArgs) and dg_paged_tree_attn (PagedTreeArgs); `a`: what
+// the two do not share, filled in already.
+template <class Args>
+int paged_attn_run(Args a, const PagedKernels<Args> &kernels, DeviceInfo::Paged DeviceInfo::*ready,
+                          const uint16_t *q, int64_t q_stride, const uint16_t *k_new,
+                          int64_t k_stride, const uint16_t *v_new, int64_t v_stride, uint16_t *out,
+                          int64_t out_stride, int T, int Hq, float scale, int causal, int window,
+                          const dg_paged_cache *c, void *workspace, size_t workspace_bytes,
+                          void *stream)
+{
+    int64_t page_stride = 0;
+    int rc = check_paged_cache(c, &page_stride);
+    if (rc != DG_OK) return rc;
+    if (T < 0 || Hq < 1 || window < 0 || (causal != 0 && causal != 1)) return DG_ERR_INVALID_ARG;
+    if (window > 0 && !causal && !kPagedTree<Args>) return DG_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale * 2.f)) return DG_ERR_INVALID_ARG;
+    if (Hq % c->Hkv != 0 || Hq / c->Hkv > 128) return DG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(T) * Hq > (1LL << 29)) return DG_ERR_UNSUPPORTED;
+    window = std::min(window, 1 << 30);   // no sequence has as many keys
+    if (T > 0 && (!q || !out || (k_new != nullptr) != (v_new != nullptr))) return DG_ERR_INVALID_ARG;
+    const int64_t dq = static_cast<int64_t>(Hq) * c->D, dk = static_cast<int64_t>(c->Hkv) * c->D;
+    if ((rc = check_stride(q_stride, dq)) != DG_OK || (rc = check_stride(out_stride, dq)) != DG_OK)
+        return rc;
+    if (k_new && ((rc = check_stride(k_stride, dk)) != DG_OK ||
+                  (rc = check_stride(v_stride, dk)) != DG_OK))
+        return rc;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
+        return DG_ERR_ALIGNMENT;
+    if (workspace == nullptr || workspace_bytes < dg_paged_attn_workspace(T, Hq, c))
+        return DG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
+    if (T == 0) return DG_OK;
+    if (k_new && (k_stride >= (1LL << 38) || v_stride >= (1LL << 38))) return DG_ERR_UNSUPPORTED;
+    DeviceInfo *di = nullptr;
+    if ((rc = current_device_info(&di)) != DG_OK) return rc;
+    if (di->sms > kAssumedMaxSMs) return DG_ERR_UNSUPPORTED;
+    const int D = c->D;
+    bool pair = false;
+    if ((rc = paged_kernels(kernels, di->*ready, &pair)) != DG_OK) return rc;
+    pair = paged_pair(pair, T, c->B, Hq / c->Hkv);
+    // keys of K and of V a CTA loads of a tile, dense; a box of the pages
+    // stays inside one page and one such load: its rows divide both
+    const int k_rows = pair || D == 256 ? 64 : 128, v_rows = pair || D == 128 ? 128 : 64;
+    const int box_rows = std::min(c->page_size & -c->page_size, k_rows);
+
+    CUtensorMap mk, mv, mkn, mvn;
+    auto page_map = [&](CUtensorMap *m, const uint16_t *base) -> int {
+        // pages [n_pages][page_size, Hkv, D] as {D, Hkv, page_size, n_pages}
+        const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c->Hkv),
+                                  static_cast<uint64_t>(c->page_size),
+                                  static_cast<uint64_t>(c->n_pages)};
+        const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(dk) * 2,
+                                     static_cast<uint64_t>(page_stride) * 2};
+        const uint32_t box[4] = {64, 1, static_cast<uint32_t>(box_rows), 1};
+        return make_map_bf16(m, base, 4, dims, strides, box);
+    };
+    auto new_map = [&](CUtensorMap *m, const uint16_t *base, int64_t stride, int rows) -> int {
+        const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c->Hkv),
+                                  static_cast<uint64_t>(T)};
+        const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(stride) * 2};
+        const uint32_t box[3] = {64, 1, static_cast<uint32_t>(rows)};
+        return make_map_bf16(m, base, 3, dims, strides, box);
+    };
+    if ((rc = page_map(&mk, c->k)) != DG_OK || (rc = page_map(&mv, c->v)) != DG_OK) return rc;
+    mkn = mk;
+    mvn = mv;
+    if (k_new && ((rc = new_map(&mkn, k_new, k_stride, k_rows)) != DG_OK ||
+                  (rc = new_map(&mvn, v_new, v_stride, v_rows)) != DG_OK))
+        return rc;
+
+    a.q = q;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.T = T;
+    a.B = c->B;
+    a.Hq = Hq;
+    a.Hkv = c->Hkv;
+    a.G = Hq / c->Hkv;
+    a.D = D;
+    a.page_size = c->page_size;
+    a.box_rows = box_rows;
+    a.n_pages = c->n_pages;
+    a.max_pages = c->max_pages;
+    a.page_table = c->page_table;
+    a.kv_len = c->kv_len;
+    a.q_start = c->q_start;
+    a.k_pages = c->k;
+    a.v_pages = c->v;
+    a.page_stride = page_stride;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.has_new = k_new != nullptr ? 1 : 0;
+    a.causal = causal;
+    a.window = window;
+    a.small = paged_small(T, c->B, c->Hkv, a.G, static_cast<int64_t>(c->max_pages) * c->page_size) ? 1 : 0;
+    a.checks = g_checks.load(std::memory_order_relaxed);
+    a.scale_log2 = scale * 1.44269502162933349609375f;
+    a.slot_rows = paged_slot_rows(pair, T, a.G);
+    a.out_wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && out_stride % 16 == 0 ? 1 : 0;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int units = pair ? di->sms / 2 : di->sms;
+    const PagedWs w = paged_ws(units, a.slot_rows, D);
+    a.ws = reinterpret_cast<WsHeader *>(ws);
+    a.desc = reinterpret_cast<PagedDesc *>(ws + w.desc);
+    a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.o);
+    cudaStream_t st = as_stream(stream);
+    const bool pdl = use_pdl(st);
+    if (pair)
+        DG_CUDA_TRY(launch_kernel(kernels.pair[D == 128 ? 0 : 1], dim3(2 * units),
+                                  dim3(kPagedPairThreads), paged_pair_smem_bytes(D), st, pdl, mk, mv, mkn, mvn, a));
+    else
+        DG_CUDA_TRY(launch_kernel(kernels.single[D == 128 ? 0 : 1], dim3(units), dim3(kPagedThreads), paged_attn_smem_bytes(D), st,
+                                  pdl, mk, mv, mkn, mvn, a));
+    DG_LAUNCHED();
+    const int jobs = (a.slot_rows * (D / 16) + kMergeThreads - 1) / kMergeThreads;   // of an item
+    DG_CUDA_TRY(launch_kernel(paged_merge_kernel, dim3(std::min(2 * di->sms, units * jobs)),
+                              dim3(kMergeThreads), 0, st, pdl, static_cast<const PagedArgs &>(a), units));
+    DG_LAUNCHED();
+    return DG_OK;
+}
+
 }  // namespace
 
 int dg::device_checks() { return g_checks.load(std::memory_order_relaxed); }
@@ -1237,120 +1459,236 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
                   int T, int Hq, float scale, int causal, int window, const dg_paged_cache *c,
                   void *workspace, size_t workspace_bytes, void *stream)
 {
+    return paged_attn_run(PagedArgs{}, kPagedKernels, &DeviceInfo::paged, q, q_stride, k_new, k_stride,
+                          v_new, v_stride, out, out_stride, T, Hq, scale, causal, window, c, workspace,
+                          workspace_bytes, stream);
+}
+
+size_t dg_paged_tree_attn_workspace(int T, int Hq, const dg_paged_cache *c)
+{
+    return dg_paged_attn_workspace(T, Hq, c);
+}
+
+int dg_paged_tree_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
+                       const uint16_t *v_new, int64_t v_stride, uint16_t *out, int64_t out_stride,
+                       int T, int Hq, float scale, int window, const uint32_t *mask, int mask_words,
+                       const int32_t *positions, const dg_paged_cache *c, void *workspace,
+                       size_t workspace_bytes, void *stream)
+{
+    if (mask_words < 1) return DG_ERR_INVALID_ARG;
+    if (mask_words > kMaskWords) return DG_ERR_UNSUPPORTED;
+    if (T > 0 && (!mask || (window > 0 && !positions))) return DG_ERR_INVALID_ARG;
+    PagedTreeArgs a{};
+    a.mask = mask;
+    a.words = mask_words;
+    a.positions = positions;
+    return paged_attn_run(a, kTreeKernels, &DeviceInfo::tree, q, q_stride, k_new, k_stride, v_new,
+                          v_stride, out, out_stride, T, Hq, scale, 0, window, c, workspace,
+                          workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------- drafted trees, page pool
+size_t dg_tree_plan_workspace(void) { return sizeof(WsHeader); }
+
+int dg_tree_plan(const int32_t *parents, int T, int window, int appended, uint32_t *mask,
+                 int mask_words, int32_t *positions, const dg_paged_cache *c, void *workspace,
+                 size_t workspace_bytes, void *stream)
+{
     int64_t page_stride = 0;
     int rc = check_paged_cache(c, &page_stride);
     if (rc != DG_OK) return rc;
-    if (T < 0 || Hq < 1 || window < 0 || (causal != 0 && causal != 1)) return DG_ERR_INVALID_ARG;
-    if (window > 0 && !causal) return DG_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || !std::isfinite(scale * 2.f)) return DG_ERR_INVALID_ARG;
-    if (Hq % c->Hkv != 0 || Hq / c->Hkv > 128) return DG_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(T) * Hq > (1LL << 29)) return DG_ERR_UNSUPPORTED;
-    window = std::min(window, 1 << 30);   // no sequence has as many keys
-    if (T > 0 && (!q || !out || (k_new != nullptr) != (v_new != nullptr))) return DG_ERR_INVALID_ARG;
-    const int64_t dq = static_cast<int64_t>(Hq) * c->D, dk = static_cast<int64_t>(c->Hkv) * c->D;
-    if ((rc = check_stride(q_stride, dq)) != DG_OK || (rc = check_stride(out_stride, dq)) != DG_OK)
-        return rc;
-    if (k_new && ((rc = check_stride(k_stride, dk)) != DG_OK ||
-                  (rc = check_stride(v_stride, dk)) != DG_OK))
-        return rc;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
-        return DG_ERR_ALIGNMENT;
-    if (workspace == nullptr || workspace_bytes < dg_paged_attn_workspace(T, Hq, c))
-        return DG_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
+    if (T < 0 || window < 0 || (appended != 0 && appended != 1) || mask_words < 1) return DG_ERR_INVALID_ARG;
+    if (mask_words > kMaskWords || T > (1 << 29)) return DG_ERR_UNSUPPORTED;
+    if (T > 0 && (!parents || !mask)) return DG_ERR_INVALID_ARG;
+    if ((rc = check_status_ws(workspace, workspace_bytes)) != DG_OK) return rc;
     if (T == 0) return DG_OK;
-    if (k_new && (k_stride >= (1LL << 38) || v_stride >= (1LL << 38))) return DG_ERR_UNSUPPORTED;
-    DeviceInfo *di = nullptr;
-    if ((rc = current_device_info(&di)) != DG_OK) return rc;
-    if (di->sms > kAssumedMaxSMs) return DG_ERR_UNSUPPORTED;
-    const int D = c->D;
-    bool pair = false;
-    if ((rc = paged_kernels(*di, &pair)) != DG_OK) return rc;
-    pair = paged_pair(pair, T, c->B, Hq / c->Hkv);
-    // keys of K and of V a CTA loads of a tile, dense; a box of the pages
-    // stays inside one page and one such load: its rows divide both
-    const int k_rows = pair || D == 256 ? 64 : 128, v_rows = pair || D == 128 ? 128 : 64;
-    const int box_rows = std::min(c->page_size & -c->page_size, k_rows);
-
-    CUtensorMap mk, mv, mkn, mvn;
-    auto page_map = [&](CUtensorMap *m, const uint16_t *base) -> int {
-        // pages [n_pages][page_size, Hkv, D] as {D, Hkv, page_size, n_pages}
-        const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c->Hkv),
-                                  static_cast<uint64_t>(c->page_size),
-                                  static_cast<uint64_t>(c->n_pages)};
-        const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(dk) * 2,
-                                     static_cast<uint64_t>(page_stride) * 2};
-        const uint32_t box[4] = {64, 1, static_cast<uint32_t>(box_rows), 1};
-        return make_map_bf16(m, base, 4, dims, strides, box);
-    };
-    auto new_map = [&](CUtensorMap *m, const uint16_t *base, int64_t stride, int rows) -> int {
-        const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c->Hkv),
-                                  static_cast<uint64_t>(T)};
-        const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(stride) * 2};
-        const uint32_t box[3] = {64, 1, static_cast<uint32_t>(rows)};
-        return make_map_bf16(m, base, 3, dims, strides, box);
-    };
-    if ((rc = page_map(&mk, c->k)) != DG_OK || (rc = page_map(&mv, c->v)) != DG_OK) return rc;
-    mkn = mk;
-    mvn = mv;
-    if (k_new && ((rc = new_map(&mkn, k_new, k_stride, k_rows)) != DG_OK ||
-                  (rc = new_map(&mvn, v_new, v_stride, v_rows)) != DG_OK))
-        return rc;
-
-    PagedArgs a{};
-    a.q = q;
-    a.out = out;
-    a.q_stride = q_stride;
-    a.out_stride = out_stride;
+    TreePlanArgs a{};
+    a.parents = parents;
+    a.q_start = c->q_start;
+    a.kv_len = c->kv_len;
     a.T = T;
     a.B = c->B;
-    a.Hq = Hq;
-    a.Hkv = c->Hkv;
-    a.G = Hq / c->Hkv;
-    a.D = D;
+    a.max_kv = c->max_pages * c->page_size;
+    a.window = window;
+    a.appended = appended;
+    a.words = mask_words;
+    a.mask = mask;
+    a.positions = positions;
+    a.ws = static_cast<WsHeader *>(workspace);
+    cudaStream_t st = as_stream(stream);
+    const int rows = std::max(T, c->B);
+    DG_CUDA_TRY(launch_kernel(tree_plan_kernel, dim3((rows + kTreePlanThreads - 1) / kTreePlanThreads),
+                              dim3(kTreePlanThreads), 0, st, use_pdl(st), a));
+    DG_LAUNCHED();
+    return DG_OK;
+}
+
+size_t dg_paged_tree_commit_workspace(void) { return sizeof(WsHeader); }
+
+int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const int32_t *sampled,
+                         int T, int layers, int64_t layer_stride, const dg_paged_cache *c,
+                         int32_t *path, int path_max, int32_t *n_path, int32_t *next,
+                         int32_t *kv_len_out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int64_t page_stride = 0;
+    int rc = check_paged_cache(c, &page_stride);
+    if (rc != DG_OK) return rc;
+    if (T < 0 || path_max < 1 || !path || !n_path || !next || !kv_len_out) return DG_ERR_INVALID_ARG;
+    if (T > 0 && (!tokens || !parents || !sampled)) return DG_ERR_INVALID_ARG;
+    if (T > (1 << 29) || path_max > (1 << 20)) return DG_ERR_UNSUPPORTED;
+    if ((rc = check_layers(c, page_stride, layers, layer_stride)) != DG_OK) return rc;
+    if (kv_len_out != c->kv_len && kv_len_out < c->kv_len + c->B && c->kv_len < kv_len_out + c->B)
+        return DG_ERR_INVALID_ARG;
+    if ((rc = check_status_ws(workspace, workspace_bytes)) != DG_OK) return rc;
+    DeviceInfo *di = nullptr;
+    if ((rc = current_device_info(&di)) != DG_OK) return rc;
+    TreeCommitArgs a{};
+    a.tokens = tokens;
+    a.parents = parents;
+    a.sampled = sampled;
+    a.q_start = c->q_start;
+    a.kv_len = c->kv_len;
+    a.page_table = c->page_table;
+    a.T = T;
+    a.B = c->B;
+    a.max_kv = c->max_pages * c->page_size;
+    a.path = path;
+    a.n_path = n_path;
+    a.next = next;
+    a.kv_out = kv_len_out;
+    a.path_max = path_max;
+    a.k = c->k;
+    a.v = c->v;
+    a.page_stride = page_stride;
+    a.layer_stride = layer_stride;
     a.page_size = c->page_size;
-    a.box_rows = box_rows;
     a.n_pages = c->n_pages;
     a.max_pages = c->max_pages;
-    a.page_table = c->page_table;
-    a.kv_len = c->kv_len;
-    a.q_start = c->q_start;
-    a.k_pages = c->k;
-    a.v_pages = c->v;
-    a.page_stride = page_stride;
-    a.k_new = k_new;
-    a.v_new = v_new;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.has_new = k_new != nullptr ? 1 : 0;
-    a.causal = causal;
-    a.window = window;
-    a.small = paged_small(T, c->B, c->Hkv, a.G, static_cast<int64_t>(c->max_pages) * c->page_size) ? 1 : 0;
-    a.checks = g_checks.load(std::memory_order_relaxed);
-    a.scale_log2 = scale * 1.44269502162933349609375f;
-    a.slot_rows = paged_slot_rows(pair, T, a.G);
-    a.out_wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && out_stride % 16 == 0 ? 1 : 0;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int units = pair ? di->sms / 2 : di->sms;
-    const PagedWs w = paged_ws(units, a.slot_rows, D);
-    a.ws = reinterpret_cast<WsHeader *>(ws);
-    a.desc = reinterpret_cast<PagedDesc *>(ws + w.desc);
-    a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
-    a.part_o = reinterpret_cast<float *>(ws + w.o);
+    a.layers = layers;
+    a.row = c->Hkv * c->D;
+    a.ws = static_cast<WsHeader *>(workspace);
     cudaStream_t st = as_stream(stream);
     const bool pdl = use_pdl(st);
-    if (pair)
-        DG_CUDA_TRY(launch_kernel(D == 128 ? paged_attn_pair_kernel_d128 : paged_attn_pair_kernel_d256,
-                                  dim3(2 * units), dim3(kPagedPairThreads), paged_pair_smem_bytes(D),
-                                  st, pdl, mk, mv, mkn, mvn, a));
-    else
-        DG_CUDA_TRY(launch_kernel(D == 128 ? paged_attn_kernel_d128 : paged_attn_kernel_d256,
-                                  dim3(units), dim3(kPagedThreads), paged_attn_smem_bytes(D), st,
-                                  pdl, mk, mv, mkn, mvn, a));
+    const int64_t walks = (static_cast<int64_t>(c->B) * 32 + kTreeWalkThreads - 1) / kTreeWalkThreads;
+    DG_CUDA_TRY(launch_kernel(tree_walk_kernel, dim3(static_cast<unsigned>(walks)), dim3(kTreeWalkThreads), 0,
+                              st, pdl, a));
     DG_LAUNCHED();
-    const int jobs = (a.slot_rows * (D / 16) + kMergeThreads - 1) / kMergeThreads;   // of an item
-    DG_CUDA_TRY(launch_kernel(paged_merge_kernel, dim3(std::min(2 * di->sms, units * jobs)),
-                              dim3(kMergeThreads), 0, st, pdl, a, units));
+    const int64_t units = 2LL * c->B * layers * ((a.row / 8 + kTreeMoveThreads - 1) / kTreeMoveThreads);
+    DG_CUDA_TRY(launch_kernel(tree_move_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(units, 16 * di->sms))),
+                              dim3(kTreeMoveThreads), 0, st, pdl, a));
+    DG_LAUNCHED();
+    return DG_OK;
+}
+
+int dg_sample_logits(const void *logits, int type, int64_t row_stride, int R, int V,
+                     const float *temperature, const int32_t *top_k, const float *top_p,
+                     const float *min_p, const float *u, int32_t *token, float *logprob,
+                     void *stream)
+{
+    if (R < 0 || V < 1 || row_stride < 0 || (type != DG_LOGITS_BF16 && type != DG_LOGITS_FP32))
+        return DG_ERR_INVALID_ARG;
+    if (row_stride == 0) row_stride = V;
+    if (row_stride < V) return DG_ERR_INVALID_ARG;
+    if (V > kSampleMaxV || R > (1 << 26) || row_stride > (1LL << 40)) return DG_ERR_UNSUPPORTED;
+    if (R == 0) return DG_OK;
+    if (!logits || !u || !token) return DG_ERR_INVALID_ARG;
+    if (!aligned16(logits)) return DG_ERR_ALIGNMENT;
+    DeviceInfo *di = nullptr;
+    int rc = current_device_info(&di);
+    if (rc != DG_OK) return rc;
+    if ((rc = sample_kernels(*di)) != DG_OK) return rc;
+    SampleArgs a{};
+    a.logits = logits;
+    a.stride = row_stride;
+    a.R = R;
+    a.V = V;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.u = u;
+    a.token = token;
+    a.logprob = logprob;
+    const int cluster = sample_cluster(type, row_stride, R, V, di->sms, &a.rows_warp);
+    cudaStream_t st = as_stream(stream);
+    DG_CUDA_TRY(launch_clusters(type == DG_LOGITS_BF16 ? sample_bf16_kernel : sample_fp32_kernel,
+                                dim3(static_cast<unsigned>(R) * cluster), dim3(kSampleThreads), cluster,
+                                sample_smem_bytes(a.rows_warp), st, use_pdl(st), a));
+    DG_LAUNCHED();
+    return DG_OK;
+}
+
+size_t dg_paged_reserve_workspace(void) { return sizeof(WsHeader); }
+
+int dg_paged_reserve(const dg_page_pool *pool, const dg_paged_cache *c, void *workspace,
+                     size_t workspace_bytes, void *stream)
+{
+    PagePoolArgs a{};
+    int rc = pool_args(a, pool, c, workspace, workspace_bytes, sizeof(WsHeader));
+    if (rc != DG_OK) return rc;
+    cudaStream_t st = as_stream(stream);
+    DG_CUDA_TRY(launch_kernel(paged_reserve_kernel, dim3(1), dim3(kPoolThreads), 0, st, use_pdl(st), a));
+    DG_LAUNCHED();
+    return DG_OK;
+}
+
+size_t dg_paged_fork_workspace(int n)
+{
+    return n < 0 || n > kPoolThreads ? 0 : sizeof(WsHeader) + static_cast<size_t>(n) * sizeof(PageForkJob);
+}
+
+int dg_paged_fork(const dg_page_pool *pool, const dg_paged_cache *c, int layers,
+                  int64_t layer_stride, const int32_t *src, const int32_t *dst, int n,
+                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (n < 0) return DG_ERR_INVALID_ARG;
+    if (n > kPoolThreads) return DG_ERR_UNSUPPORTED;
+    PagePoolArgs a{};
+    int rc = pool_args(a, pool, c, workspace, workspace_bytes, dg_paged_fork_workspace(n));
+    if (rc != DG_OK) return rc;
+    if ((rc = check_layers(c, a.page_stride, layers, layer_stride)) != DG_OK) return rc;
+    if (n == 0) return DG_OK;
+    if (!src || !dst) return DG_ERR_INVALID_ARG;
+    DeviceInfo *di = nullptr;
+    if ((rc = current_device_info(&di)) != DG_OK) return rc;
+    a.src = src;
+    a.dst = dst;
+    a.n = n;
+    a.layers = layers;
+    a.layer_stride = layer_stride;
+    a.jobs = reinterpret_cast<PageForkJob *>(static_cast<uint8_t *>(workspace) + sizeof(WsHeader));
+    cudaStream_t st = as_stream(stream);
+    const bool pdl = use_pdl(st);
+    DG_CUDA_TRY(launch_kernel(paged_fork_kernel, dim3(1), dim3(kPoolThreads), 0, st, pdl, a));
+    DG_LAUNCHED();
+    const int64_t chunks = (static_cast<int64_t>(a.page_size) * a.row * 2 + kForkBytes - 1) / kForkBytes;
+    const int64_t units = n + 2LL * n * layers * chunks;
+    DG_CUDA_TRY(launch_kernel(paged_fork_copy_kernel,
+                              dim3(static_cast<unsigned>(std::min<int64_t>(units, 16 * di->sms))),
+                              dim3(kForkThreads), 0, st, pdl, a));
+    DG_LAUNCHED();
+    return DG_OK;
+}
+
+size_t dg_paged_release_workspace(void) { return sizeof(WsHeader); }
+
+int dg_paged_release(const dg_page_pool *pool, const dg_paged_cache *c, const int32_t *seqs, int n,
+                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (n < 0) return DG_ERR_INVALID_ARG;
+    if (n > (1 << 20)) return DG_ERR_UNSUPPORTED;
+    PagePoolArgs a{};
+    const int rc = pool_args(a, pool, c, workspace, workspace_bytes, sizeof(WsHeader));
+    if (rc != DG_OK) return rc;
+    if (n == 0) return DG_OK;
+    if (!seqs) return DG_ERR_INVALID_ARG;
+    a.dst = seqs;
+    a.n = n;
+    cudaStream_t st = as_stream(stream);
+    const bool pdl = use_pdl(st);
+    DG_CUDA_TRY(launch_kernel(paged_release_kernel, dim3(n), dim3(kReleaseThreads), 0, st, pdl, a));
+    DG_LAUNCHED();
+    DG_CUDA_TRY(launch_kernel(paged_collect_kernel, dim3(1), dim3(kPoolThreads), 0, st, pdl, a));
     DG_LAUNCHED();
     return DG_OK;
 }

@@ -90,10 +90,14 @@ struct PagedSeq {
 #endif
 };
 
+// Whether the new tokens are drafted trees.
+template <class Args>
+constexpr bool kPagedTree = std::is_same<Args, PagedTreeArgs>::value;
+
 // Bounds every length by what the tensors hold, so that no later index can
 // leave them; *bad: 1 when something had to be cut, 2 when q_start decreases.
-template <int ROWS, int BKV, class I>
-DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, int *bad = nullptr)
+template <int ROWS, int BKV, class I, class Args>
+DG_BOTH PagedSeq<I> paged_seq(const Args &a, int b, int *bad = nullptr)
 {
     PagedSeq<I> s;
     const int r0 = paged_load(a.q_start + b), r1 = paged_load(a.q_start + b + 1);
@@ -107,7 +111,12 @@ DG_BOTH PagedSeq<I> paged_seq(const PagedArgs &a, int b, int *bad = nullptr)
     s.fixed = G * PagedCost<ROWS>::Item + 1;
     s.cap = 0;
     s.mc = s.mt;
-    if (!a.causal) {
+    if constexpr (kPagedTree<Args>) {
+        // every tile the same: all keys but those before any row's window
+        const int keys = s.kv + (a.has_new ? s.n : 0);
+        s.slope = 0;
+        s.x0 = G * (a.window > 0 ? paged_min(keys, s.n + a.window + BKV) : keys);
+    } else if (!a.causal) {
         s.slope = 0;
         s.x0 = G * (s.kv + (a.has_new ? s.n : 0));
     } else {
@@ -223,8 +232,8 @@ constexpr int kPagedBounds = kPagedUnits / (ROWS / 128) / 32;   // units a lane 
 // sequences' lengths in a batch of up to 32; bound: where the stretches of this
 // lane's units begin; sums: shared memory, an I per unit.  (Apart from the rest
 // of the division, which every small batch runs from a cold instruction cache.)
-template <int ROWS, int BKV, class I>
-__device__ __noinline__ bool paged_take_rounds(const PagedArgs &a, int rounds, int units, I W,
+template <int ROWS, int BKV, class I, class Args>
+__device__ __noinline__ bool paged_take_rounds(const Args &a, int rounds, int units, I W,
                                                PagedSeq<I> q, I (&bound)[kPagedBounds<ROWS>], void *sums)
 {
     using Sum = std::conditional_t<sizeof(I) == 4, unsigned, unsigned long long>;
@@ -295,8 +304,8 @@ __device__ __noinline__ bool paged_take_rounds(const PagedArgs &a, int rounds, i
 // the stretch begins in (a batch of up to 32 keeps its lengths in registers),
 // whose lengths are left in s.  bound: where the stretches of this lane's units
 // begin, if they differ.  sums: shared memory, an I per pair.
-template <int ROWS, int BKV, class I>
-DG_DEVICE PagedRange<I> paged_divide(const PagedArgs &a, int u, int units, PagedSeq<I> &s,
+template <int ROWS, int BKV, class I, class Args>
+DG_DEVICE PagedRange<I> paged_divide(const Args &a, int u, int units, PagedSeq<I> &s,
                                      I (&bound)[kPagedBounds<ROWS>], void *sums)
 {
     const int lane = threadIdx.x & 31;
@@ -420,7 +429,8 @@ struct PagedWalk {
     PagedRange<I> r;
 
     // first: the lengths of sequence r.b
-    DG_BOTH void start(const PagedArgs &a, const PagedRange<I> &range, const PagedSeq<I> &first)
+    template <class Args>
+    DG_BOTH void start(const Args &a, const PagedRange<I> &range, const PagedSeq<I> &first)
     {
         r = range;
         waves = r.waves;
@@ -432,7 +442,8 @@ struct PagedWalk {
     }
 
     // On to the sequence that item `at` is of.
-    DG_BOTH void settle(const PagedArgs &a)
+    template <class Args>
+    DG_BOTH void settle(const Args &a)
     {
         while (at >= static_cast<I>(a.Hkv) * s.mt && b + 1 < a.B) {
             at -= static_cast<I>(a.Hkv) * s.mt;
@@ -440,7 +451,8 @@ struct PagedWalk {
         }
     }
 
-    DG_BOTH void stretch(const PagedArgs &a)
+    template <class Args>
+    DG_BOTH void stretch(const Args &a)
     {
         begin = r.begin;
         g = r.g;
@@ -451,7 +463,8 @@ struct PagedWalk {
     }
 
     // To where the stretch begins.
-    DG_BOTH void find(const PagedArgs &a)
+    template <class Args>
+    DG_BOTH void find(const Args &a)
     {
         I base = 0;
         for (b = 0;; ++b) {
@@ -465,7 +478,8 @@ struct PagedWalk {
     }
 
     // What a part has of its item: all but its share of the tiles.
-    DG_BOTH void fill(const PagedArgs &a, PagedPart &p) const
+    template <class Args>
+    DG_BOTH void fill(const Args &a, PagedPart &p) const
     {
         p.s0 = s.s0;
         p.n = s.n;
@@ -476,14 +490,15 @@ struct PagedWalk {
         p.rows = paged_min(ROWS, s.n * a.G - p.frow0);
         p.nkp = (s.kv + BKV - 1) / BKV;
         int hi, lo = 0;
-        if (!a.causal) {
+        if (kPagedTree<Args> || !a.causal) {
             hi = p.nkp + (a.has_new ? (s.n + BKV - 1) / BKV : 0);
         } else {
             const int i1 = (p.frow0 + p.rows - 1) / a.G;
             hi = a.has_new ? p.nkp + i1 / BKV + 1 : paged_max(0, (s.kv - s.n + i1 + BKV) / BKV);
         }
         if (a.window > 0) {
-            const int i0 = p.frow0 / a.G;
+            // (a tree's rows may all be its root's, the first position)
+            const int i0 = kPagedTree<Args> ? 0 : p.frow0 / a.G;
             const int first = (a.has_new ? s.kv : s.kv - s.n) + i0 - a.window + 1;
             if (first > 0)
                 lo = a.has_new && first >= s.kv ? p.nkp + (first - s.kv) / BKV : first / BKV;
@@ -494,8 +509,8 @@ struct PagedWalk {
 
     // The next part; false: there are no more.  unit_of(x): the unit whose
     // stretch has place x of the line.
-    template <class UnitOf>
-    DG_BOTH bool next(const PagedArgs &a, PagedPart &p, UnitOf unit_of)
+    template <class Args, class UnitOf>
+    DG_BOTH bool next(const Args &a, PagedPart &p, UnitOf unit_of)
     {
         if (waves > 0) {
             g = static_cast<int>(paged_div<I>(at, s.mt));
@@ -585,8 +600,8 @@ DG_DEVICE void paged_ring_init(PagedRing &ring, int takers)
 
 // The walking warp (all lanes), for unit u of `units`.  It divides the work
 // while the rest of the CTA sets up; `ready` returns once the ring may be used.
-template <class Gm, class I, class Ready>
-DG_DEVICE void paged_walk_in(const PagedArgs &a, int u, int units, PagedRing &ring, int where,
+template <class Gm, class I, class Args, class Ready>
+DG_DEVICE void paged_walk_in(const Args &a, int u, int units, PagedRing &ring, int where,
                              void *sums, Ready ready)
 {
     const bool lead = (threadIdx.x & 31) == 0;
@@ -637,8 +652,8 @@ DG_DEVICE void paged_walk_in(const PagedArgs &a, int u, int units, PagedRing &ri
     }
 }
 
-template <class Gm, class Ready>
-DG_DEVICE void paged_walk(const PagedArgs &a, int u, int units, PagedRing &ring, int where, void *sums,
+template <class Gm, class Args, class Ready>
+DG_DEVICE void paged_walk(const Args &a, int u, int units, PagedRing &ring, int where, void *sums,
                           Ready ready)
 {
     if (a.small) paged_walk_in<Gm, int32_t>(a, u, units, ring, where, sums, ready);
@@ -835,14 +850,18 @@ DG_DEVICE bool paged_store_row(const PagedArgs &a, uint32_t tmem_row, int c0, bo
 struct PagedEdge {
     int pos0, pos1;
 };
-DG_DEVICE PagedEdge paged_edge(const PagedArgs &a, const PagedItem &p)
+template <class Args>
+DG_DEVICE PagedEdge paged_edge(const Args &a, const PagedItem &p)
 {
     const int base = a.has_new ? p.kv : p.kv - p.n;
+    // any node of a tree may be hidden from any row, and any row be the root
+    if constexpr (kPagedTree<Args>) return {base - 1, base + p.n - 1};
     return {base + p.frow0 / a.G, base + (p.frow0 + p.rows - 1) / a.G};
 }
-DG_DEVICE bool paged_border(const PagedArgs &a, const PagedEdge &e, int key0, int valid)
+template <class Args>
+DG_DEVICE bool paged_border(const Args &a, const PagedEdge &e, int key0, int valid)
 {
-    return a.causal && (key0 + valid - 1 > e.pos0 || (a.window > 0 && key0 <= e.pos1 - a.window));
+    return (kPagedTree<Args> || a.causal) && (key0 + valid - 1 > e.pos0 || (a.window > 0 && key0 <= e.pos1 - a.window));
 }
 
 // The tiles of a part that are not whole and seen by all of its rows, by their
@@ -861,14 +880,14 @@ struct PagedSpecial {
         for (int j = max(lo, hi); j < end; ++j) f(j);
     }
 };
-template <int BKV>
-DG_DEVICE PagedSpecial paged_special(const PagedArgs &a, const PagedItem &p, const PagedEdge &e)
+template <int BKV, class Args>
+DG_DEVICE PagedSpecial paged_special(const Args &a, const PagedItem &p, const PagedEdge &e)
 {
     const int nt = p.tv1 - p.tv0, nkp = (p.kv + BKV - 1) / BKV;
     PagedSpecial s;
     s.lo = 0;
     s.hi = nt;
-    if (a.causal) {
+    if (kPagedTree<Args> || a.causal) {
         // what is hidden lies within a query tile's positions of either end
         if (a.window > 0)
             while (s.lo < nt && paged_key0<BKV>(p, p.tv0 + s.lo) <= e.pos1 - a.window) ++s.lo;
@@ -944,8 +963,35 @@ DG_DEVICE float paged_weight(const PagedArgs &a, const uint16_t *k, int64_t q_of
                  __uint_as_float(static_cast<uint32_t>(k[d]) << 16), s);
     return fast_exp2(fmaf(s, a.scale_log2, -m_ref));
 }
-DG_DEVICE bool paged_sees(const PagedArgs &a, int pos, int key)
+// Token i of a part's sequence: its place among the keys, or (with a window) its
+// position in the tree, which lies among those of the tree's nodes.
+template <class Args>
+DG_DEVICE int paged_pos(const Args &a, const PagedItem &p, int i)
 {
+    const int base = a.has_new ? p.kv : p.kv - p.n;
+    if constexpr (kPagedTree<Args>)
+        if (a.window > 0) return min(max(__ldg(a.positions + p.s0 + i), base), base + p.n - 1);
+    return base + i;
+}
+// Whether token i sees nodes node .. node + 31 of its tree, a bit each; those
+// before the tree (node < 0) are cached keys.
+DG_DEVICE uint32_t paged_nodes(const PagedTreeArgs &a, const PagedItem &p, int i, int node)
+{
+    const uint32_t *row = a.mask + static_cast<int64_t>(p.s0 + i) * a.words;
+    auto word = [&](int k) -> uint32_t { return k < a.words ? __ldg(row + k) : 0u; };
+    if (node <= -32) return 0xFFFFFFFFu;
+    if (node < 0) return word(0) << -node | ((1u << -node) - 1u);
+    return node & 31 ? __funnelshift_r(word(node >> 5), word((node >> 5) + 1), node & 31) : word(node >> 5);
+}
+// Whether token i, at paged_pos `pos`, sees a key.
+template <class Args>
+DG_DEVICE bool paged_sees(const Args &a, const PagedItem &p, int i, int pos, int key)
+{
+    if constexpr (kPagedTree<Args>) {
+        const int base = a.has_new ? p.kv : p.kv - p.n;
+        if (key >= base) return paged_nodes(a, p, i, key - base) & 1u;
+        return a.window == 0 || key > pos - a.window;
+    }
     return (!a.causal || key <= pos) && (a.window == 0 || key > pos - a.window);
 }
 
@@ -953,9 +999,9 @@ DG_DEVICE bool paged_sees(const PagedArgs &a, int pos, int key)
 // that paged_look zeroed and the row sees, those in columns [first, end) of their
 // tiles.  The whole warp, lane = row (live: it exists); nothing here is fast, nor
 // need it be.
-template <int BKV, int N>
-DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t tmem_row, int c0,
-                                bool live, int64_t q_off, int pos, float m_ref, int first = 0,
+template <int BKV, int N, class Args>
+DG_DEVICE void paged_add_hidden(const Args &a, const PagedItem &p, uint32_t tmem_row, int c0,
+                                bool live, int64_t q_off, int i, int pos, float m_ref, int first = 0,
                                 int end = BKV)
 {
     const PagedEdge e = paged_edge(a, p);
@@ -973,7 +1019,7 @@ DG_DEVICE void paged_add_hidden(const PagedArgs &a, const PagedItem &p, uint32_t
 #pragma unroll 1
             for (int d = 0; d < N; d += 8) m = magnitude_max(m, *reinterpret_cast<const uint4 *>(v + d));
             if (!not_finite(m)) continue;
-            const bool sees = live && paged_sees(a, pos, key0 + c);
+            const bool sees = live && paged_sees(a, p, i, pos, key0 + c);
             const float w = sees ? paged_weight(a, at.k, q_off, m_ref) : 0.f;
 #pragma unroll 1
             for (int d = 0; d < N; d += 16) {
@@ -1005,20 +1051,20 @@ struct PagedMarks {
 // values have overflowed) does not hold up the other sequences: 2000 such keys of 16
 // heads of 128 took 57 ms with each lane by itself and their weights worked out, so
 // that 40000 outlasted the other warps' waits; they take 0.7.
-template <int BKV, int N>
-__device__ __noinline__ PagedMarks paged_marks(const PagedArgs &a, const PagedItem &p, int i, int c0)
+template <int BKV, int N, class Args>
+__device__ __noinline__ PagedMarks paged_marks(const Args &a, const PagedItem &p, int i, int c0)
 {
     PagedMarks m{0, 0, 0};
     const int lane = threadIdx.x & 31;
     const int nkp = (p.kv + BKV - 1) / BKV;
-    const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
+    const int pos = paged_pos(a, p, i);
 #pragma unroll 1
     for (int tv = p.tv0; tv < p.tv1; ++tv) {
         const int valid = paged_valid<BKV>(p, tv), key0 = paged_key0<BKV>(p, tv);
 #pragma unroll 1
         for (int c = lane; c < valid; c += 32) {
             PagedKey at;
-            if (!paged_sees(a, pos, key0 + c) || !paged_key(a, p, tv >= nkp, key0 + c, at)) continue;
+            if (!paged_sees(a, p, i, pos, key0 + c) || !paged_key(a, p, tv >= nkp, key0 + c, at)) continue;
             uint32_t v = 0, k = 0;
 #pragma unroll
             for (int d = 0; d < N; d += 8) v = magnitude_max(v, *reinterpret_cast<const uint4 *>(at.v + c0 + d));

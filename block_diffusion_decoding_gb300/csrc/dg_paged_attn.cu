@@ -86,10 +86,10 @@ DG_DEVICE void tmem_put(uint32_t taddr, const uint32_t (&r)[N])
     else tmem_st8(taddr, r);
 }
 
-template <int D>
+template <int D, class Args>
 __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const CUtensorMap *map_v,
                                                 const CUtensorMap *map_kn,
-                                                const CUtensorMap *map_vn, const PagedArgs &a)
+                                                const CUtensorMap *map_vn, const Args &a)
 {
     using Gm = PagedGeom<D>;
     constexpr int BKV = Gm::BKV, NK = Gm::NK, NV = Gm::NV;
@@ -310,7 +310,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 if (lane == 0) mbar_arrive(q_ready);
             }
             // position of this row, and the keys it sees
-            const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
+            const int pos = paged_pos(a, p, i);
             const PagedEdge edge = paged_edge(a, p);
             const int buf = static_cast<int>(parts % 3u);
             float m_ref = -INFINITY, l = 0.f;
@@ -374,8 +374,20 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     if (border && paged_look<Gm>(v_tile, valid, threadIdx.x - 64)) zeroed[buf] = 1;
                 }
                 // first and last visible column
-                const int c_hi = a.causal ? min(valid - 1, pos - key0) : valid - 1;
-                const int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
+                const int c_hi = !kPagedTree<Args> && a.causal ? min(valid - 1, pos - key0) : valid - 1;
+                int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
+                // a tree's columns beyond that, a bit each (those of this warp, with few rows)
+                uint32_t nodes[BKV / 32];
+                if constexpr (kPagedTree<Args>) {
+                    // (the window cuts the cached keys alone)
+                    const int node0 = key0 - (a.has_new ? p.kv : p.kv - p.n);
+                    c_lo = min(c_lo, max(0, -node0));
+#pragma unroll
+                    for (int w = 0; w < BKV / 32; ++w)
+                        nodes[w] = !border ? 0xFFFFFFFFu
+                                           : few ? (w == 0 ? paged_nodes(a, p, i, node0 + q * CH) : 0u)
+                                                 : paged_nodes(a, p, i, node0 + 32 * w);
+                }
                 ok = mbar_wait_poll(&s_full[sb], (it >> 1) & 1u, a.ws, 942);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
@@ -393,6 +405,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         if (q * CH + c > c_hi || q * CH + c < c_lo) sr[c] = __float_as_uint(-INFINITY);
+                        if (kPagedTree<Args> && !(nodes[0] >> c & 1u)) sr[c] = __float_as_uint(-INFINITY);
                         rmax = fmaxf(rmax, __uint_as_float(sr[c]));
                     }
                     ok = refer(rmax * a.scale_log2);
@@ -425,6 +438,13 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
 #pragma unroll
                         for (int c = 0; c < BKV; ++c)
                             if (c > c_hi || c < c_lo) sr[c] = __float_as_uint(-INFINITY);
+                    }
+                    if constexpr (kPagedTree<Args>) {
+                        if (border) {
+#pragma unroll
+                            for (int c = 0; c < BKV; ++c)
+                                if (!(nodes[c / 32] >> (c & 31) & 1u)) sr[c] = __float_as_uint(-INFINITY);
+                        }
                     }
                     // the scale is positive, so the scaled maximum is the maximum scaled
                     float rmax = -INFINITY;
@@ -464,7 +484,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 de.part0 = 1;
             if (busy && zeroed[buf] != 0)
                 paged_add_hidden<BKV, D>(
-                    a, p, to, 0, live, tok * a.q_stride + static_cast<int64_t>(head) * D, pos, m_ref,
+                    a, p, to, 0, live, tok * a.q_stride + static_cast<int64_t>(head) * D, i, pos, m_ref,
                     few ? q * CH : 0, few ? (q + 1) * CH : BKV);
             if (threadIdx.x == 64) zeroed[(buf + 2) % 3] = 0;
             const bool whole = p.kind == kPartWhole;
@@ -596,6 +616,24 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
                            const __grid_constant__ CUtensorMap map_v,
                            const __grid_constant__ CUtensorMap map_kn,
                            const __grid_constant__ CUtensorMap map_vn, PagedArgs a)
+{
+    paged_attn_body<256>(&map_k, &map_v, &map_kn, &map_vn, a);
+}
+
+__global__ void __launch_bounds__(kPagedThreads, 1)
+    paged_tree_kernel_d128(const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v,
+                           const __grid_constant__ CUtensorMap map_kn,
+                           const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a)
+{
+    paged_attn_body<128>(&map_k, &map_v, &map_kn, &map_vn, a);
+}
+
+__global__ void __launch_bounds__(kPagedThreads, 1)
+    paged_tree_kernel_d256(const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v,
+                           const __grid_constant__ CUtensorMap map_kn,
+                           const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a)
 {
     paged_attn_body<256>(&map_k, &map_v, &map_kn, &map_vn, a);
 }

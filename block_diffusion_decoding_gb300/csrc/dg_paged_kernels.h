@@ -72,6 +72,13 @@ struct PagedArgs {
     PagedDesc *desc;     // [CTAs]
     WsHeader *ws;
 };
+// Drafted trees: of the new tokens a row sees those that its bits name, and every
+// cached key before them (with a window: after its position - window).
+struct PagedTreeArgs : PagedArgs {
+    const uint32_t *mask;       // [T, words]
+    const int32_t *positions;   // [T], read with a window
+    int words;
+};
 constexpr int kPagedThreads = 256;   // warps as kAttnThreads, and 7 walks the parts
 __global__ void paged_attn_kernel_d128(const __grid_constant__ CUtensorMap map_k,
                                        const __grid_constant__ CUtensorMap map_v,
@@ -81,6 +88,14 @@ __global__ void paged_attn_kernel_d256(const __grid_constant__ CUtensorMap map_k
                                        const __grid_constant__ CUtensorMap map_v,
                                        const __grid_constant__ CUtensorMap map_kn,
                                        const __grid_constant__ CUtensorMap map_vn, PagedArgs a);
+__global__ void paged_tree_kernel_d128(const __grid_constant__ CUtensorMap map_k,
+                                       const __grid_constant__ CUtensorMap map_v,
+                                       const __grid_constant__ CUtensorMap map_kn,
+                                       const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a);
+__global__ void paged_tree_kernel_d256(const __grid_constant__ CUtensorMap map_k,
+                                       const __grid_constant__ CUtensorMap map_v,
+                                       const __grid_constant__ CUtensorMap map_kn,
+                                       const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a);
 constexpr int kMergeThreads = 256;   // at least as many as there are units
 constexpr int kMergeParts = 2;       // parts whose loads a thread has in flight
 __global__ void paged_merge_kernel(PagedArgs a, int units);
@@ -97,6 +112,14 @@ __global__ void paged_attn_pair_kernel_d256(const __grid_constant__ CUtensorMap 
                                             const __grid_constant__ CUtensorMap map_v,
                                             const __grid_constant__ CUtensorMap map_kn,
                                             const __grid_constant__ CUtensorMap map_vn, PagedArgs a);
+__global__ void paged_tree_pair_kernel_d128(const __grid_constant__ CUtensorMap map_k,
+                                            const __grid_constant__ CUtensorMap map_v,
+                                            const __grid_constant__ CUtensorMap map_kn,
+                                            const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a);
+__global__ void paged_tree_pair_kernel_d256(const __grid_constant__ CUtensorMap map_k,
+                                            const __grid_constant__ CUtensorMap map_v,
+                                            const __grid_constant__ CUtensorMap map_kn,
+                                            const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a);
 int paged_pair_smem_bytes(int D);
 
 }  // namespace dg

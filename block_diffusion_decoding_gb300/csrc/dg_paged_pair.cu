@@ -113,10 +113,10 @@ int paged_pair_smem_bytes(int D)
 }
 
 // One ring's loads, as paged_ring_producer, for this CTA's half of every tile.
-template <class Gm, bool IS_V>
+template <class Gm, bool IS_V, class Args>
 __device__ __forceinline__ void pair_producer(uint8_t *buf, PairShared &sh, uint32_t lead_full, int r,
                                               const CUtensorMap *map_c, const CUtensorMap *map_n,
-                                              const PagedArgs &a, int where)
+                                              const Args &a, int where)
 {
     constexpr int NS = IS_V ? Gm::NV : Gm::NK;
     constexpr int Bytes = IS_V ? Gm::VBytes : Gm::KBytes;
@@ -246,10 +246,10 @@ DG_DEVICE uint32_t column_bits(int n)
     return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-template <int D>
+template <int D, class Args>
 __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const CUtensorMap *map_v,
                                                 const CUtensorMap *map_kn,
-                                                const CUtensorMap *map_vn, const PagedArgs &a)
+                                                const CUtensorMap *map_vn, const Args &a)
 {
     using Gm = PairGeom<D>;
     constexpr int BKV = Gm::BKV, NK = Gm::NK, NV = Gm::NV, NS = Gm::NS;
@@ -513,13 +513,21 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
             const int i = frow / a.G;
             const bool busy = r * 128 + q * 32 < p.rows;   // the warp has a live row
             float m_ref = -INFINITY, l = 0.f;    // reference of, and sum over, this group's tiles
-            const int pos = (a.has_new ? p.kv : p.kv - p.n) + i;
+            const int pos = paged_pos(a, p, i);
             const PagedSpecial special = paged_special<BKV>(a, p, paged_edge(a, p));
             const int buf = static_cast<int>(parts % 3u);
             for (int j = static_cast<int>((it ^ wg) & 1u); j < nt; j += 2) {
                 const uint32_t t = it + j;       // tile of the CTA; its parity is wg
                 const int ss = static_cast<int>(t % NS);
                 const bool odd = special.at(j);  // else whole, and seen by every row
+                uint32_t nodes[BKV / 32];        // a tree's columns, a bit each
+                if constexpr (kPagedTree<Args>) {
+                    const int node0 =
+                        paged_key0<BKV>(p, p.tv0 + j) - (a.has_new ? p.kv : p.kv - p.n);
+#pragma unroll
+                    for (int w = 0; w < BKV / 32; ++w)
+                        nodes[w] = odd ? paged_nodes(a, p, i, node0 + 32 * w) : 0xFFFFFFFFu;
+                }
                 // a wait that runs out is noticed at the tile's end: what is
                 // computed until then reaches no memory but the outputs
                 // (the other group's maximum is there before its next scores are)
@@ -542,12 +550,16 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                         // first and last visible column
                         const int valid = paged_valid<BKV>(p, p.tv0 + j), key0 = paged_key0<BKV>(p, p.tv0 + j);
                         const int at = pos - key0;
-                        const int c_hi = a.causal ? min(valid - 1, at) : valid - 1;
-                        const int c_lo = a.window > 0 ? max(at - a.window + 1, 0) : 0;
+                        const int c_hi = !kPagedTree<Args> && a.causal ? min(valid - 1, at) : valid - 1;
+                        int c_lo = a.window > 0 ? max(at - a.window + 1, 0) : 0;
+                        // (a tree's window cuts the cached keys alone)
+                        if (kPagedTree<Args>)
+                            c_lo = min(c_lo, max(0, (a.has_new ? p.kv : p.kv - p.n) - key0));
 #pragma unroll
                         for (int c0 = 0; c0 < BKV; c0 += 32) {
                             // 32 columns' visibility, a bit each
-                            const uint32_t seen = column_bits(c_hi - c0 + 1) & ~column_bits(c_lo - c0);
+                            uint32_t seen = column_bits(c_hi - c0 + 1) & ~column_bits(c_lo - c0);
+                            if constexpr (kPagedTree<Args>) seen &= nodes[c0 / 32];
                             if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) continue;
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
@@ -704,7 +716,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
             if (busy && sh.zeroed[buf][wg] == parts)
                 paged_add_hidden<BKV, Half>(
                     a, done, to, wg * Half, live,
-                    static_cast<int64_t>(done.s0 + i) * a.q_stride + static_cast<int64_t>(head) * D, pos,
+                    static_cast<int64_t>(done.s0 + i) * a.q_stride + static_cast<int64_t>(head) * D, i, pos,
                     m_ref);
             const float inv_l = (l > 0.f) ? 1.f / l : l == 0.f ? 0.f : l;   // no visible key: zero; NaN stays
             bool badv = a.checks && live && !isfinite(l);
@@ -743,6 +755,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPagedPairThreads, 1
                                 const __grid_constant__ CUtensorMap map_v,
                                 const __grid_constant__ CUtensorMap map_kn,
                                 const __grid_constant__ CUtensorMap map_vn, PagedArgs a)
+{
+    paged_pair_body<256>(&map_k, &map_v, &map_kn, &map_vn, a);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPagedPairThreads, 1)
+    paged_tree_pair_kernel_d128(const __grid_constant__ CUtensorMap map_k,
+                                const __grid_constant__ CUtensorMap map_v,
+                                const __grid_constant__ CUtensorMap map_kn,
+                                const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a)
+{
+    paged_pair_body<128>(&map_k, &map_v, &map_kn, &map_vn, a);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPagedPairThreads, 1)
+    paged_tree_pair_kernel_d256(const __grid_constant__ CUtensorMap map_k,
+                                const __grid_constant__ CUtensorMap map_v,
+                                const __grid_constant__ CUtensorMap map_kn,
+                                const __grid_constant__ CUtensorMap map_vn, PagedTreeArgs a)
 {
     paged_pair_body<256>(&map_k, &map_v, &map_kn, &map_vn, a);
 }

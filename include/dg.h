@@ -262,6 +262,153 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
                   void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Drafted trees over the paged cache.  Where one causal forward checks a    */
+/* drafted tree of continuations of every sequence (the pages' causal encoder */
+/* run over guesses), a step is: pages for the nodes (dg_paged_reserve), the  */
+/* trees' plan, the append of the nodes' keys and values at the plan's        */
+/* positions (dg_paged_append), their attention in every layer, a draw from   */
+/* every node's logits (dg_sample_logits), and the commit of each sequence's  */
+/* accepted path.  The pages have no counterpart of these calls.              */
+/*                                                                            */
+/* The new tokens of sequence b (rows q_start[b] .. q_start[b + 1] - 1) are   */
+/* the nodes 0 .. n_b - 1 of its tree; parents [T] holds each one's parent by */
+/* its index in the tree, lower than its own, or -1.  Node 0 is the root.     */
+/* ------------------------------------------------------------------------ */
+
+/* The plan, once for all layers.  With the sequence's keys before the tree   */
+/* counted as base = kv_len[b] - (appended ? n_b : 0) (appended: kv_len       */
+/* counts the nodes already):                                                 */
+/*   depth of node i   the edges from it up to a node whose parent is -1      */
+/*   positions[q_start[b] + i] = base + depth   (positions may be NULL)       */
+/*   mask[(q_start[b] + i) * mask_words + j / 32], bit j % 32: whether node i  */
+/*     attends to node j: its ancestors and itself, with window > 0 only those */
+/*     fewer than `window` edges away.                                         */
+/* mask [T, mask_words] and positions [T], device.  Rows of nobody stay as    */
+/* they were.  A parent that is not a lower index or -1 counts as -1; a node  */
+/* past 32 mask_words is not in the mask (not seen by itself either); lengths */
+/* and rows are cut as the attention cuts them; each records DG_ERR_DEVICE.   */
+/* workspace: 256 bytes, for the status word.                                 */
+/* Supported: 1 <= mask_words <= 128; T == 0 is allowed.                      */
+size_t dg_tree_plan_workspace(void);
+int dg_tree_plan(const int32_t *parents, int T, int window, int appended, uint32_t *mask,
+                 int mask_words, int32_t *positions, const dg_paged_cache *c, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
+/* dg_paged_attn for trees: node i of sequence b sees the keys before the     */
+/* tree, with window > 0 those at places after positions[q_start[b] + i] -     */
+/* window, and of the tree's own keys those whose bit is set in its row of    */
+/* mask (bits from n_b on are ignored; nodes past 32 mask_words are seen by    */
+/* nobody; the window does not look at the bits).  The tree's keys are k_new,  */
+/* v_new, or without them the last n_b cached ones.  A node that sees no key   */
+/* gets a row of zeros.  positions are read with a window alone (else may be  */
+/* NULL); one outside [base, base + n_b) counts as the nearest inside.        */
+/* Everything else, and what is supported, as dg_paged_attn;                  */
+/* 1 <= mask_words <= 128.                                                    */
+size_t dg_paged_tree_attn_workspace(int T, int Hq, const dg_paged_cache *c);
+int dg_paged_tree_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, int64_t k_stride,
+                       const uint16_t *v_new, int64_t v_stride, uint16_t *out, int64_t out_stride,
+                       int T, int Hq, float scale, int window, const uint32_t *mask, int mask_words,
+                       const int32_t *positions, const dg_paged_cache *c, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* The commit.  kv_len[b] counts the nodes, which are the last n_b cached     */
+/* tokens.  The accepted path of sequence b begins with the root; from a node */
+/* i on it goes to the lowest node whose parent is i and whose token is        */
+/* sampled[i], while there is one and the path is shorter than path_max.      */
+/*   path [B, path_max]   the accepted nodes, 0 past their end                 */
+/*   n_path [B]           how many (0: the sequence has no new tokens)         */
+/*   next [B]             what was sampled at the last one (-1: none)          */
+/*   kv_len_out [B]       base + n_path, the cache's new length; may be kv_len */
+/* Keys and values of the accepted nodes move to the places base .. base +     */
+/* n_path - 1 of the sequence's pages, in all layers: layer l's pages are k +  */
+/* l * layer_stride and v + l * layer_stride.  Every other byte of the cache   */
+/* stays.  A sequence of fewer cached tokens than nodes keeps what it has      */
+/* (n_path 0); a page id that does not exist is read as zeros and not written; */
+/* each records DG_ERR_DEVICE.  No page of a sequence's tree may be another    */
+/* one's too.  tokens, sampled, parents [T] int32.  workspace: 256 bytes.      */
+/* Supported: layers >= 1; path_max >= 1; layer_stride a multiple of 8, such   */
+/* that no two layers' pages overlap: at least all pages of a layer, or layers */
+/* interleaved in each page_stride.                                            */
+size_t dg_paged_tree_commit_workspace(void);
+int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const int32_t *sampled,
+                         int T, int layers, int64_t layer_stride, const dg_paged_cache *c,
+                         int32_t *path, int path_max, int32_t *n_path, int32_t *next,
+                         int32_t *kv_len_out, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* Draws a token from each row of logits.  With x the row's logits, m the     */
+/* largest, w_i = exp((x_i - m) / T), and its tokens in the order (logit       */
+/* falling, index rising), kept are the tokens in all of                       */
+/*   the first top_k of the order (top_k <= 0: all);                           */
+/*   the shortest prefix of those whose weight is at least top_p of theirs     */
+/*     (top_p >= 1: all; <= 0: the first token);                               */
+/*   those with w_i >= min_p (<= 0: all; at least 1: those that equal m).      */
+/* The token is the first, in the order of the vocabulary, up to and with      */
+/* which the kept weight exceeds u of it all (u >= 1: the last that counts);   */
+/* logprob = ln(its weight / the kept weight).  T <= 0 or NaN: the first token */
+/* of the order; T is cut to 2^-100 .. 2^100.  Tokens whose logit is minus     */
+/* infinity or NaN are never drawn (a row of them alone: token -1, logprob     */
+/* minus infinity); where m is infinite, the tokens that have it are all alike. */
+/* logits [R, V] fp32 or bf16, rows row_stride elements apart (>= V, 0: V);    */
+/* temperature, top_k, top_p, min_p [R], each NULL for 1, 0, 1, 0; u [R] fp32   */
+/* in [0, 1); token [R] int32, logprob [R] fp32 or NULL.  All device; logits    */
+/* 16-byte aligned (its rows need not be).  Weights and their sums are 64-bit   */
+/* fixed-point numbers, 2^-43 of the largest, weights with a relative error of  */
+/* 2^-28: results do not depend on the order of any sum.  Needs no workspace.   */
+/* Supported: R * 16 < 2^31; V <= 393216.  R == 0 is allowed.                   */
+#define DG_LOGITS_BF16 0
+#define DG_LOGITS_FP32 1
+int dg_sample_logits(const void *logits, int type, int64_t row_stride, int R, int V,
+                     const float *temperature, const int32_t *top_k, const float *top_p,
+                     const float *min_p, const float *u, int32_t *token, float *logprob,
+                     void *stream);
+
+/* A pool of the cache's pages, shared by its sequences.  free_pages [n_pages] */
+/* holds the ids of the pages of nobody in its first *n_free places, a stack;  */
+/* refs [n_pages] how many sequences hold a page.  All device, int32; the      */
+/* cache's page_table and kv_len are written too.  A sequence holds the pages  */
+/* of the first places of its row of the table, the places behind them are     */
+/* negative.  The calls keep to the order of their arguments, so that the same */
+/* calls hand out the same pages.                                              */
+/* n_free outside 0 .. n_pages, lengths that do not fit the table, a page id    */
+/* that does not exist: cut or skipped, and DG_ERR_DEVICE recorded.  workspace: */
+/* 256 bytes, for the status word (dg_paged_fork: its query).  Calls on one     */
+/* pool are ordered on one stream.                                              */
+typedef struct dg_page_pool {
+    int32_t *free_pages, *n_free, *refs;
+} dg_page_pool;
+
+/* Pages for the tokens of the coming append: sequence b gets what it does not  */
+/* hold yet of the pages of its places kv_len[b] .. kv_len[b] + q_start[b + 1]  */
+/* - q_start[b] - 1, from the end of the free ones, with refs 1.  Where the     */
+/* pool runs short, that sequence and all later ones that want pages get none,  */
+/* and where the table does, none past it (DG_ERR_DEVICE each).                 */
+size_t dg_paged_reserve_workspace(void);
+int dg_paged_reserve(const dg_page_pool *pool, const dg_paged_cache *c, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Forks: sequence dst[i] becomes a copy of sequence src[i] (device, [n]).  It  */
+/* shares the full pages (refs + 1 each); the last, unfinished one is copied,   */
+/* the tokens in use of it and in all layers (as dg_paged_tree_commit), to a    */
+/* page from the end of the free ones.  kv_len[dst[i]] = kv_len[src[i]].  A     */
+/* fork to a sequence that is not empty (kv_len 0, no page held), to its own    */
+/* source or to an earlier fork's dst, of indices outside [0, B), or with no page left for its  */
+/* copy is not made, and recorded; the others are.  All lengths are those       */
+/* before the call.  Supported: 1 <= layers; n <= 1024 (0 is allowed).          */
+size_t dg_paged_fork_workspace(int n);
+int dg_paged_fork(const dg_page_pool *pool, const dg_paged_cache *c, int layers,
+                  int64_t layer_stride, const int32_t *src, const int32_t *dst, int n,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Takes back the pages of sequences seqs [n] (device): refs - 1 each, their    */
+/* places in the table -1, kv_len 0.  Pages that nobody holds any more join the */
+/* free ones at the end, the lowest id first.  An index outside [0, B) or given */
+/* before is skipped, and recorded.  n == 0 is allowed.                         */
+size_t dg_paged_release_workspace(void);
+int dg_paged_release(const dg_page_pool *pool, const dg_paged_cache *c, const int32_t *seqs, int n,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* One denoising step after the decoder body: LM head -> per-position        */
 /* entropy, Gumbel-max sample and argmax -> entropy-bounded acceptance and    */
 /* uniform renoise -> adaptive stop test.                                     */
