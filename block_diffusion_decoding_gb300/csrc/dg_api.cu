@@ -1123,16 +1123,15 @@ int sample_kernels(DeviceInfo &di)
     if (di.sample_set) return DG_OK;
     for (auto kern : {sample_bf16_kernel, sample_fp32_kernel}) {
         DG_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         sample_smem_bytes(kSampleRows)));
+                                         sample_smem_bytes()));
         DG_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     }
     di.sample_set = true;
     return DG_OK;
 }
 
-// CTAs that share a row, and the 512-byte pieces a warp of theirs keeps: few enough
-// that three CTAs' rows fit an SM, so that one's loads run beside the others' passes;
-// more where the rows would leave SMs idle.
+// CTAs that share a row, and the 512-byte pieces of it that a warp of theirs reads:
+// as many as fill the GPU, two a SM, and have a piece for every warp.
 int sample_cluster(int type, int64_t stride, int R, int V, int sms, int *rows_warp)
 {
     const int per = type == DG_LOGITS_BF16 ? 8 : 4;
@@ -1140,8 +1139,10 @@ int sample_cluster(int type, int64_t stride, int R, int V, int sms, int *rows_wa
     const int vecs = (V + skew + per - 1) / per;
     auto rows = [&](int ctas) { return (vecs + ctas * kSampleThreads - 1) / (ctas * kSampleThreads); };
     int ctas = 1;
-    while (ctas < kSampleCluster && rows(ctas) > 8) ctas *= 2;
-    while (ctas < 8 && rows(ctas) > 1 && static_cast<int64_t>(R) * ctas * 2 <= sms) ctas *= 2;
+    const char *env = std::getenv("DG_SAMPLE_CTAS");
+    if (env) ctas = std::max(1, std::min(16, std::atoi(env)));
+    else
+    while (ctas < 8 && rows(ctas) > 1 && static_cast<int64_t>(R) * ctas * 2 <= 2 * sms) ctas *= 2;
     *rows_warp = rows(ctas);
     return ctas;
 }
@@ -1609,11 +1610,11 @@ int dg_sample_logits(const void *logits, int type, int64_t row_stride, int R, in
     a.u = u;
     a.token = token;
     a.logprob = logprob;
-    const int cluster = sample_cluster(type, row_stride, R, V, di->sms, &a.rows_warp);
+    a.ctas = sample_cluster(type, row_stride, R, V, di->sms, &a.rows_warp);
     cudaStream_t st = as_stream(stream);
     DG_CUDA_TRY(launch_clusters(type == DG_LOGITS_BF16 ? sample_bf16_kernel : sample_fp32_kernel,
-                                dim3(static_cast<unsigned>(R) * cluster), dim3(kSampleThreads), cluster,
-                                sample_smem_bytes(a.rows_warp), st, use_pdl(st), a));
+                                dim3(static_cast<unsigned>(R) * a.ctas), dim3(kSampleThreads), a.ctas,
+                                sample_smem_bytes(), st, use_pdl(st), a));
     DG_LAUNCHED();
     return DG_OK;
 }

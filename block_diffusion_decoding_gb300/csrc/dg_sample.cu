@@ -3,17 +3,31 @@
 //
 // What is kept of a row is a prefix of its tokens in the order (logit falling, index
 // rising): all above a value, the cut, and the first few of those that equal it.  So
-// nothing is sorted.  The cut is found by counting: the tokens fall into 1024 bins by
-// their distance from the maximum, those of the bin it lies in into 1024 again, then
-// by their bits.  For top-k the bins count tokens, for top-p their weights, rounded,
-// and the exact sums decide afterwards whether the cut found so is the one, or its
-// neighbour.
+// a vocabulary is not sorted.  Every way to the token begins with one pass over the
+// row, in which a thread takes the maximum of each of its kGroups groups of tokens.
+//   no filter    the weights are summed, a stretch of the row a warp; the token is
+//                looked for in the stretch that the random number falls into;
+//   few kept     (top-k of up to kListMost, what min-p leaves, a small nucleus) the
+//                groups whose maximum reaches a value that the cut lies above are read
+//                again for the tokens above it, which are sorted and summed by one CTA.
+//                For top-k the value is the k-th largest of the groups' maxima;
+//   top-p        the weights, rounded, are summed in bins of 1/32 of a factor of 2; the
+//                tokens of the bin that holds the cut (or of a part of it) are sorted, as
+//                above, beside the exact sum of what lies above it; then as without a
+//                filter;
+//   the rest     (a larger k, cuts that lie elsewhere) the cut is found by counting: the
+//                tokens fall into 1024 bins by their distance from the maximum, those
+//                of the bin it lies in into 1024 again, then by their bits; the exact
+//                sums decide whether it is the one found or a neighbour.
+// A row is a cluster's; its CTAs exchange maxima, bins and sums through each other's
+// shared memory.
 //
-// A cluster of CTAs has the row in shared memory, so that the memory is read once,
-// however many passes the row takes.  The exact weights exp((x - max) / T) are 64-bit
-// fixed-point numbers with a relative error of about 2^-29 (see Weights): a token's
-// place among the sums of a whole vocabulary would be lost in 32 bits, and sums of
-// integers do not depend on their order.
+// The exact weights exp((x - max) / T) are 64-bit fixed-point numbers with a relative
+// error of about 2^-29 (see Weights): a token's place among the sums of a whole
+// vocabulary would be lost in 32 bits, and sums of integers do not depend on their
+// order.
+#include <cstddef>
+
 #include "dg_paged_device.cuh"
 #include "dg_serve_kernels.h"
 
@@ -22,10 +36,15 @@ namespace dg {
 namespace {
 
 constexpr int kBins = 1024;
-constexpr float kBinsLog2 = 16.f;        // bins to a factor of 2 in weight
-constexpr int kLaneBits = 54;            // a weight of 1 in a lane's sums; a lane has at most
-                                         // 24 x 8 tokens
-constexpr int kSumBits = 43;             // in all others: up to 2^19 tokens
+constexpr int kBinsThread = kBins / kSampleThreads;
+constexpr float kBinsLog2 = 16.f;        // of the search by counting: bins to a factor of 2 in weight
+constexpr float kMassLog2 = 32.f;        // of top-p's bins of weights
+constexpr float kMassOne = 8192.f;       // a weight at its bin's upper end, in these
+constexpr int kGroups = 8;               // groups of a thread's tokens
+constexpr int kList = 1536;              // tokens that are sorted at most
+constexpr int kListMost = 1024;          // of which top-k's k
+constexpr int kLaneBits = 53;            // a weight of 1 in a lane's sums: up to 1600 tokens
+constexpr int kSumBits = 43;             // in all others: up to 2^19
 constexpr int kDrop = kLaneBits - kSumBits;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // Neighbours that top-p's cut is moved over at most.  The rounded weights put it
@@ -35,27 +54,51 @@ constexpr int kMoves = 1 << 14;
 struct Found {
     int bin;                             // -1: the target lies past the last one
     uint32_t count, before;              // tokens in it, and above it
-    float mass, target;                  // weight above it, and the weight that was looked for
+    float mass;                          // weight above it
+    bool reached;                        // (with rounded weights: else the last one with a token)
 };
 
+struct Cut {
+    float v;                             // -inf: none
+    uint32_t first;                      // how many of the tokens at v are kept
+    uint32_t ties;                       // tokens at v
+};
+
+constexpr int kSegments = kSampleCluster * kSampleWarps;
 struct alignas(16) SampleShared {
     uint32_t hist[2][kBins];
-    uint64_t gather[2][kSampleCluster];
-    uint64_t above[2][kSampleCluster * kSampleWarps];   // by segment: weight above the cut,
-    uint64_t whole[2][kSampleCluster * kSampleWarps];   // above top-k's,
-    uint32_t ties[2][kSampleCluster * kSampleWarps];    // tokens at the cut
+    uint64_t list[kList];                 // (the first CTA's) tokens: falling value, index
+    uint64_t mass[kList];                 // their weights in that order
+    uint64_t gather[2][kSegments];
+    union {
+        struct {
+            uint64_t above[2][kSegments];   // by segment: weight above the cut
+            uint32_t ties[2][kSegments];    // and tokens at it
+            uint64_t row_above[kSampleRows];
+            uint32_t row_ties[kSampleRows];
+            float group[kGroups][kSampleThreads];   // maxima
+        };
+        uint64_t moved[kList];            // the list while it is sorted
+    };
     uint64_t red[kSampleWarps];
-    uint64_t totals[3];
-    uint64_t row_above[kSampleRows + 8];
-    uint32_t row_ties[kSampleRows + 8];
     uint32_t table[32];
     float scan_f[kSampleWarps];
     uint32_t scan_u[kSampleWarps];
     Found found;
+    Cut cut;
     int claim, last;
     int seg, tie_prefix;
-    uint64_t rem;
+    uint64_t rem, all;
+    uint32_t listed, base, todo;
+    float min_value;
 };
+
+// (what is written and read 64 and 128 bits wide through cluster addresses)
+static_assert(offsetof(SampleShared, hist) % 16 == 0 && offsetof(SampleShared, list) % 8 == 0 &&
+                  offsetof(SampleShared, gather) % 8 == 0 && offsetof(SampleShared, above) % 8 == 0 &&
+                  offsetof(SampleShared, rem) % 8 == 0 && offsetof(SampleShared, all) % 8 == 0 &&
+                  offsetof(SampleShared, cut) % 4 == 0,
+              "alignment");
 
 // round(2^(30 + j / 32))
 __constant__ uint32_t kExpTable[32] = {
@@ -72,10 +115,25 @@ DG_DEVICE void st_cluster32(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-DG_DEVICE uint2 ld_cluster2(uint32_t addr)
+DG_DEVICE uint32_t ld_cluster32(uint32_t addr)
 {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+DG_DEVICE uint32_t add_cluster32(uint32_t addr, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+    return old;
+}
+DG_DEVICE uint4 ld_cluster4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -102,6 +160,15 @@ struct Vec<float> {
         x[2] = __uint_as_float(v.z);
         x[3] = __uint_as_float(v.w);
     }
+    using Most = float;
+    DG_DEVICE static Most none() { return -INFINITY; }
+    DG_DEVICE static void most(Most &m, const uint4 &v)
+    {
+        m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v.x)), __uint_as_float(v.y)),
+                  fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    DG_DEVICE static float value(Most m) { return m; }
+    DG_DEVICE static float widen(float x) { return x; }
 };
 template <>
 struct Vec<uint16_t> {
@@ -115,6 +182,15 @@ struct Vec<uint16_t> {
             x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
         }
     }
+    using Most = __nv_bfloat162;
+    DG_DEVICE static Most none() { return __floats2bfloat162_rn(-INFINITY, -INFINITY); }
+    DG_DEVICE static void most(Most &m, const uint4 &v)
+    {
+        const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&v);
+        m = __hmax2(__hmax2(m, x[0]), __hmax2(x[1], __hmax2(x[2], x[3])));
+    }
+    DG_DEVICE static float value(Most m) { return fmaxf(__low2float(m), __high2float(m)); }
+    DG_DEVICE static float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 };
 
 // floor(f S) for f in [0, 1), a float's 24 bits times 64 (up: the next whole number
@@ -138,7 +214,7 @@ DG_DEVICE uint64_t part_of(uint64_t S, float f, bool up)
     return q + (up && rest != 0 ? 1 : 0);
 }
 
-// Weights 2^(c x - reference), c = log2 e / T, as 64-bit integers, 2^54 for 1.
+// Weights 2^(c x - reference), c = log2 e / T, as 64-bit integers, 2^53 for 1.
 // c x is taken in units of 1/32: P, its nearest whole number, comes out of one
 // multiply-add with a large constant, exactly; what is left of it, |r| <= 1/64, of a
 // second, rounded at 2^-31, and c's low half with it.  Then 2^(j / 32) from a table
@@ -151,28 +227,39 @@ struct Weights {
     int ref;
     bool wide;
     float m;
-    double c;
 
+    // (Arithmetic in 64 bits is slow here, and every thread goes through this: c, to
+    // 2^-46 of itself, from two divisions in 32.)
     DG_DEVICE void init(float max, float t)
     {
         m = max;
-        c = 1.4426950408889634 / static_cast<double>(t);
-        ch = static_cast<float>(c);
-        cl = static_cast<float>(c - static_cast<double>(ch));
+        ch = 1.442695041f / t;
+        cl = (fmaf(-ch, t, 1.442695041f) + 1.92596299e-8f) / t;   // log2 e in two parts
         floor = max - 60.f / ch;
         ref = __float_as_int(fmaf(max, ch, 393216.f));   // 1.5 x 2^18: a unit in the last place is 1/32
         wide = !(fabsf(max) * ch < 65536.f);
     }
-    // ln of what a weight of 2^54 stands for beside exp((x - max) / T) = 1
+    DG_DEVICE double c() const { return static_cast<double>(ch) + static_cast<double>(cl); }
+    // ln of what a weight of 2^53 stands for beside exp((x - max) / T) = 1
     DG_DEVICE double shift() const
     {
         if (wide) return 0.;
         const double at = static_cast<double>(__int_as_float(ref) - 393216.f);
-        return (at - static_cast<double>(m) * c) * 0.6931471805599453;
+        return (at - static_cast<double>(m) * c()) * 0.6931471805599453;
+    }
+    // The maximum's weight beside its reference (2^53), a factor next to 1.
+    DG_DEVICE float most() const
+    {
+        if (wide) return 1.f;
+        const float P = __int_as_float(ref) - 393216.f;
+        return exp2f(fmaf(m, cl, fmaf(m, ch, -P)));
     }
     DG_DEVICE uint64_t operator()(float x, const uint32_t *table) const
     {
-        if (wide) return in_double(x);
+        return wide ? in_double(x) : fast(x, table);
+    }
+    DG_DEVICE uint64_t fast(float x, const uint32_t *table) const
+    {
         const float y = fmaxf(x, floor);
         const float P = fmaf(y, ch, 393216.f);
         const float Pf = P - 393216.f;
@@ -186,12 +273,12 @@ struct Weights {
         const uint32_t T = table[i & 31];
         const int yi = __float_as_int(B) - __float_as_int(0.046875f);
         const uint32_t w = T + static_cast<uint32_t>(__mulhi(static_cast<int>(T), yi << 4));
-        return static_cast<uint64_t>(w) << 24 >> min(-(i >> 5), 63);
+        return static_cast<uint64_t>(w) << (kLaneBits - 30) >> (31 - i >> 5);   // (0 .. 61)
     }
     DG_DEVICE uint64_t in_double(float x) const
     {
-        const double t = (static_cast<double>(x) - static_cast<double>(m)) * c;
-        return t > -60. ? static_cast<uint64_t>(exp2(t) * 18014398509481984.) : 0;
+        const double t = (static_cast<double>(x) - static_cast<double>(m)) * c();
+        return t > -60. ? static_cast<uint64_t>(exp2(t) * 9007199254740992.) : 0;
     }
 };
 
@@ -200,20 +287,18 @@ struct Sampler {
     static constexpr int E = Vec<T>::N;
     const SampleArgs &a;
     SampleShared &sh;
-    const uint4 *data;
+    const T *base = nullptr;             // the row, from the 16 bytes on that it begins in
+    int skew = 0;                        // where in them
     const int warp, lane, rank, ctas;
-    int turn = 0, hist_turn = 0;
+    int turn = 0, hist_turn = 0, sum_turn = 0;
     Weights weight;
     float m = 0.f;
     bool flat = false;                   // the maximum is infinite: those tokens alone, alike
 
-    DG_DEVICE Sampler(const SampleArgs &args, SampleShared &s, const uint4 *d)
-        : a(args), sh(s), data(d), warp(threadIdx.x >> 5), lane(threadIdx.x & 31),
-          rank(static_cast<int>(cluster_ctarank())), ctas(0)
+    DG_DEVICE Sampler(const SampleArgs &args, SampleShared &s)
+        : a(args), sh(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31),
+          rank(static_cast<int>(cluster_ctarank())), ctas(args.ctas)
     {
-        uint32_t n;
-        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-        const_cast<int &>(ctas) = static_cast<int>(n);
     }
 
     DG_DEVICE uint64_t w_of(float x) const
@@ -226,50 +311,121 @@ struct Sampler {
         return n * (w >> kDrop) + (n * (w & ((1u << kDrop) - 1)) >> kDrop);
     }
 
-    // f(x) for each of this thread's tokens (places past the row hold -inf).
-    template <class F>
-    DG_DEVICE void each(F f) const
+    // A barrier of the row's threads.
+    DG_DEVICE void sync() const
     {
-        for (int r = 0; r < a.rows_warp; ++r) {
-            float x[E];
-            Vec<T>::unpack(data[(warp * a.rows_warp + r) * 32 + lane], x);
-#pragma unroll
-            for (int e = 0; e < E; ++e) f(x[e], r, e);
-        }
+        if (ctas == 1) __syncthreads();
+        else cluster_sync_all();
     }
-    // The place of a token in its row, `skew` places early.
+
+    // 16 bytes of the row (-inf past its ends).
+    DG_DEVICE uint4 load(int w, int r, int l) const
+    {
+        constexpr uint32_t Low = E == 8 ? 0xFF80FF80u : 0xFF800000u;
+        const int first = place(w, r, l, 0);
+        if (first >= skew && first + E <= a.V + skew) return __ldg(reinterpret_cast<const uint4 *>(base + first));
+        uint4 v = make_uint4(Low, Low, Low, Low);
+        if (first + E > skew && first < a.V + skew) {
+            alignas(16) T x[E];
+            *reinterpret_cast<uint4 *>(x) = v;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (first + e >= skew && first + e < a.V + skew) x[e] = base[first + e];
+            v = *reinterpret_cast<const uint4 *>(x);
+        }
+        return v;
+    }
+    // The first token of 16 bytes, `skew` early.
     DG_DEVICE int place(int w, int r, int l, int e) const
     {
         return (((rank * kSampleWarps + w) * a.rows_warp + r) * 32 + l) * E + e;
     }
+    DG_DEVICE int rows_group() const { return (a.rows_warp + kGroups - 1) / kGroups; }
 
-    // The largest of two values over the cluster.
+    // f(16 bytes, row of the warp) for rows r0 .. r1 - 1.
+    template <int N, class F>
+    DG_DEVICE void rows(int r0, int r1, F f) const
+    {
+#pragma unroll 1
+        for (int r = r0; r < r1; r += N) {
+            uint4 v[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (r + e < r1) v[e] = load(warp, r + e, lane);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (r + e < r1) f(v[e], r + e);
+        }
+    }
+    // f(x, row of the warp, number in the 16 bytes) for each of this thread's tokens.
+    template <class F>
+    DG_DEVICE void each(F f) const
+    {
+        rows<4>(0, a.rows_warp, [&](const uint4 &v, int r) {
+            float x[E];
+            Vec<T>::unpack(v, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) f(x[e], r, e);
+        });
+    }
+    // f(16 bytes, warp, row, lane) for those of the groups whose maximum is wanted,
+    // shared out evenly over the CTA's threads.  Once a row; all of them.
+    template <class W, class F>
+    DG_DEVICE void each_of(W wanted, F f)
+    {
+        constexpr int N = 4;
+        uint16_t *todo = reinterpret_cast<uint16_t *>(sh.mass);
+        static_assert(sizeof(sh.mass) >= kGroups * kSampleThreads * sizeof(uint16_t), "a place for every group");
+#pragma unroll 1
+        for (int g = 0; g < kGroups; ++g)
+            if (wanted(sh.group[g][threadIdx.x]))
+                todo[atomicAdd(&sh.todo, 1u)] = static_cast<uint16_t>(g * kSampleThreads + threadIdx.x);
+        __syncthreads();
+        const int rg = rows_group(), n = static_cast<int>(sh.todo) * rg;
+#pragma unroll 1
+        for (int x0 = threadIdx.x; x0 < n; x0 += N * kSampleThreads) {
+            uint4 v[N];
+            int w[N], r[N], l[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int x = x0 + e * kSampleThreads;
+                r[e] = a.rows_warp;
+                if (x >= n) continue;
+                const int at = x / rg, id = todo[at];
+                r[e] = id / kSampleThreads * rg + x - at * rg;
+                w[e] = id % kSampleThreads / 32;
+                l[e] = id % 32;
+                if (r[e] < a.rows_warp) v[e] = load(w[e], r[e], l[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (r[e] < a.rows_warp) f(v[e], w[e], r[e], l[e]);
+        }
+    }
+
+    // The largest of two values over the row's threads.
     DG_DEVICE uint2 largest(uint32_t x, uint32_t y)
     {
         x = __reduce_max_sync(kAll, x);
         y = __reduce_max_sync(kAll, y);
-        if (lane == 0) sh.red[warp] = static_cast<uint64_t>(y) << 32 | x;
-        __syncthreads();
-        const int buf = turn++ & 1;
-        if (warp == 0) {
-            const uint64_t v = sh.red[lane & (kSampleWarps - 1)];
-            x = __reduce_max_sync(kAll, static_cast<uint32_t>(v));
-            y = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
-            if (lane < ctas)
-                st_cluster64(mapa_shared(smem_u32(&sh.gather[buf][rank]), lane),
-                             static_cast<uint64_t>(y) << 32 | x);
+        uint64_t *got = sh.gather[turn++ & 1];
+        const int at = rank * kSampleWarps + warp;
+        const uint64_t both = static_cast<uint64_t>(y) << 32 | x;
+        if (ctas == 1) {
+            if (lane == 0) got[at] = both;
+        } else if (lane < ctas) {
+            st_cluster64(mapa_shared(smem_u32(got + at), lane), both);
         }
-        cluster_sync_all();
-        uint2 got = make_uint2(0, 0);
-        for (int k = 0; k < ctas; ++k) {
-            const uint64_t v = sh.gather[buf][k];
-            got.x = max(got.x, static_cast<uint32_t>(v));
-            got.y = max(got.y, static_cast<uint32_t>(v >> 32));
+        sync();
+        x = y = 0;
+        for (int k = lane; k < ctas * kSampleWarps; k += 32) {
+            x = max(x, static_cast<uint32_t>(got[k]));
+            y = max(y, static_cast<uint32_t>(got[k] >> 32));
         }
-        return got;
+        return make_uint2(__reduce_max_sync(kAll, x), __reduce_max_sync(kAll, y));
     }
 
-    // ------------------------------------------------------------ a histogram over the cluster
+    // ------------------------------------------------------------ a histogram over the row
     DG_DEVICE uint32_t *clear()
     {
         uint32_t *hist = sh.hist[hist_turn & 1];
@@ -277,83 +433,94 @@ struct Sampler {
         __syncthreads();
         return hist;
     }
-    // The bin in which the tokens reach `target` in number, or with `mass` (counts
-    // weighed by of_bin) want.target in weight, or that part of it all less `less`.
-    // Where rounded sums stay short of that, the last one that is not empty.
-    template <class F>
-    DG_DEVICE Found find(bool mass, uint32_t target, float target_mass, float part, float less, F of_bin)
+    // The bin in which the tokens reach `target` in number, or with `Mass` (counts
+    // weighed by of_bin) target_mass in weight; where rounded sums stay short of that,
+    // the last one that is not empty.
+    template <bool Mass, class F>
+    DG_DEVICE Found find(uint32_t target, float target_mass, F of_bin)
     {
         const int buf = hist_turn++ & 1;
         if (threadIdx.x == 0) {
             sh.claim = kSampleThreads;
             sh.last = -1;
         }
-        cluster_sync_all();
-        const int b = 2 * threadIdx.x;
-        uint32_t n0 = 0, n1 = 0;
+        sync();
+        const int b = kBinsThread * threadIdx.x;
+        uint32_t n[kBinsThread];
+        float f[kBinsThread];
+#pragma unroll
+        for (int e = 0; e < kBinsThread; ++e) n[e] = 0;
         for (int k = 0; k < ctas; ++k) {
-            const uint2 v = ld_cluster2(mapa_shared(smem_u32(&sh.hist[buf][b]), k));
-            n0 += v.x;
-            n1 += v.y;
+            uint4 v;
+            if (ctas == 1) v = *reinterpret_cast<const uint4 *>(&sh.hist[buf][b]);
+            else v = ld_cluster4(mapa_shared(smem_u32(&sh.hist[buf][b]), k));
+            n[0] += v.x;
+            n[1] += v.y;
+            n[2] += v.z;
+            n[3] += v.w;
         }
-        const float f0 = mass ? n0 * of_bin(b) : 0.f, f1 = mass ? n1 * of_bin(b + 1) : 0.f;
-        uint32_t n = n0 + n1;
-        float f = f0 + f1;
+        uint32_t n_sum = 0;
+        float f_sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < kBinsThread; ++e) {
+            f[e] = Mass && n[e] > 0 ? n[e] * of_bin(b + e) : 0.f;
+            n_sum += n[e];
+            f_sum += f[e];
+        }
+        uint32_t n_end = n_sum;
+        float f_end = f_sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t un = __shfl_up_sync(kAll, n, o);
-            const float uf = __shfl_up_sync(kAll, f, o);
+            const uint32_t un = __shfl_up_sync(kAll, n_end, o);
+            const float uf = __shfl_up_sync(kAll, f_end, o);
             if (lane >= o) {
-                n += un;
-                f += uf;
+                n_end += un;
+                f_end += uf;
             }
         }
         if (lane == 31) {
-            sh.scan_u[warp] = n;
-            sh.scan_f[warp] = f;
+            sh.scan_u[warp] = n_end;
+            sh.scan_f[warp] = f_end;
         }
         __syncthreads();
-        uint32_t n_all = 0;
-        float f_all = 0.f;
-        for (int w = 0; w < kSampleWarps; ++w) {
-            if (w == warp) {
-                n += n_all;
-                f += f_all;
-            }
-            n_all += sh.scan_u[w];
-            f_all += sh.scan_f[w];
+        for (int w = 0; w < warp; ++w) {
+            n_end += sh.scan_u[w];
+            f_end += sh.scan_f[w];
         }
-        if (part > 0.f) target_mass = part * (f_all - less);
-        if (n0 + n1 > 0) {
-            if (mass ? f >= target_mass : n >= target) atomicMin(&sh.claim, static_cast<int>(threadIdx.x));
-            atomicMax(&sh.last, static_cast<int>(threadIdx.x));
+        if (n_sum > 0) {
+            if (Mass ? f_end >= target_mass : n_end >= target) atomicMin(&sh.claim, static_cast<int>(threadIdx.x));
+            if (Mass) atomicMax(&sh.last, static_cast<int>(threadIdx.x));
         }
         __syncthreads();
         const bool reached = sh.claim < kSampleThreads;
         if (static_cast<int>(threadIdx.x) == (reached ? sh.claim : max(sh.last, 0))) {
-            bool second = n0 == 0;
-            if (n0 > 0 && n1 > 0) second = !reached || (mass ? f - f1 < target_mass : n - n1 < target);
-            sh.found = Found{reached || mass ? (second ? b + 1 : b) : -1, second ? n1 : n0,
-                             second ? n - n1 : n - n0 - n1, second ? f - f1 : f - f0 - f1, target_mass};
-            if (sh.last < 0) sh.found.bin = -1;
+            Found got{-1, 0, 0, 0.f, reached};
+            uint32_t n_before = n_end - n_sum;
+            float f_before = f_end - f_sum;
+            bool stop = false;
+#pragma unroll
+            for (int e = 0; e < kBinsThread; ++e) {
+                if (n[e] > 0 && !stop) {
+                    got = Found{b + e, n[e], n_before, f_before, reached};
+                    stop = reached && (Mass ? f_before + f[e] >= target_mass : n_before + n[e] >= target);
+                }
+                n_before += n[e];
+                f_before += f[e];
+            }
+            if (!reached && !Mass) got.bin = -1;
+            sh.found = got;
         }
         __syncthreads();
         return sh.found;
     }
 
-    // ------------------------------------------------------------ the cut
-    struct Cut {
-        float v;                          // -inf: none
-        uint32_t first;                   // how many of the tokens at v are kept
-        uint32_t ties;                    // tokens at v
-    };
-
-    // Where the tokens reach k in number or, with `mass`, the part p of the weight of
-    // those that `least` keeps.  Tokens of weight 0 do not count; none: there are too
-    // few.  With `mass` it may be one of the cut's neighbours (the weights are rounded).
-    DG_DEVICE Cut select(bool mass, uint32_t k, float p, const Cut &least)
+    // Where the tokens reach k in number or, with `Mass`, `target` in weight, of those
+    // from `floor_v` on.  Tokens of weight 0 do not count; none: there are too few.
+    // With `Mass` it may be one of the cut's neighbours (the weights are rounded).
+    template <bool Mass>
+    DG_DEVICE Cut select(uint32_t k, float target, float floor_v)
     {
-        const float s1 = weight.ch * kBinsLog2, floor_v = least.v;
+        const float s1 = weight.ch * kBinsLog2;
         auto y_of = [&](float x) -> float { return (m - x) * s1; };
         uint32_t *hist = clear();
         each([&](float x, int, int) {
@@ -361,18 +528,15 @@ struct Sampler {
             if (!(x >= floor_v) || !(y < static_cast<float>(kBins))) return;
             const int b = static_cast<int>(y);
             uint32_t inc = 1;
-            if (mass) {
+            if (Mass) {
                 // its weight beside that of the bin's upper end, 2^(-f / 16)
                 const float f = y - static_cast<float>(b);
-                inc = static_cast<uint32_t>(fmaf(f, fmaf(f, 9.3838e-4f, -0.0433217f), 1.f) * 65536.f);
+                inc = static_cast<uint32_t>(fmaf(fmaf(f, fmaf(f, 9.3838e-4f, -0.0433217f), 1.f), kMassOne, 0.5f));
             }
             atomicAdd(hist + b, inc);
         });
-        const float less = mass && floor_v > -INFINITY
-                               ? static_cast<float>(least.ties - least.first) * exp2f(-y_of(floor_v) / kBinsLog2)
-                               : 0.f;
-        const Found f1 = find(mass, k, 0.f, p, less,
-                              [&](int b) -> float { return exp2f(-b / kBinsLog2) * (1.f / 65536.f); });
+        const Found f1 =
+            find<Mass>(k, target, [&](int b) -> float { return exp2f(-b / kBinsLog2) * (1.f / kMassOne); });
         if (f1.bin < 0) return Cut{-INFINITY, 0, 0};
         // that bin's tokens by their place in it
         const float b1 = static_cast<float>(f1.bin);
@@ -385,9 +549,9 @@ struct Sampler {
             const float y = y_of(x);
             if (inside(x, y)) atomicAdd(hist + y2_of(y), 1u);
         });
-        uint32_t before = mass ? 0 : f1.before;
+        uint32_t before = Mass ? 0 : f1.before;
         float above = f1.mass;
-        const Found f2 = find(mass, k - before, f1.target - above, 0.f, 0.f, [&](int b) -> float {
+        const Found f2 = find<Mass>(k - before, target - above, [&](int b) -> float {
             return exp2f(-(b1 + (static_cast<float>(b) + 0.5f) * (1.f / kBins)) / kBinsLog2);
         });
         if (f2.bin < 0) return Cut{-INFINITY, 0, 0};
@@ -413,7 +577,7 @@ struct Sampler {
                 const uint32_t o = order_of(x);
                 if (o <= hi && o >= lo) atomicAdd(hist + ((hi - o) >> shift), 1u);
             });
-            const Found f3 = find(mass, k - before, f1.target - above, 0.f, 0.f, [&](int b) -> float {
+            const Found f3 = find<Mass>(k - before, target - above, [&](int b) -> float {
                 const uint64_t mid = (static_cast<uint64_t>(b) << shift) + (1u << shift >> 1);
                 return exp2f(-y_of(of_order(mid < hi - lo ? hi - static_cast<uint32_t>(mid) : lo)) / kBinsLog2);
             });
@@ -425,80 +589,76 @@ struct Sampler {
             if (hi - lo > (1u << shift) - 1) lo = hi - ((1u << shift) - 1);
             if (shift == 0) break;
         }
-        return Cut{of_order(hi), mass ? ties : k - before, ties};
+        return Cut{of_order(hi), Mass ? ties : k - before, ties};
     }
 
     // ------------------------------------------------------------ exact sums
     struct Sums {
-        uint64_t above, whole;            // weight above the cut, above top-k's
+        uint64_t above;                   // weight above the cut
         uint32_t ties;                    // tokens at the cut
         int buf;
     };
-    int sum_turn = 0;
-    DG_DEVICE Sums sums(float v, float floor_v, bool with_whole)
+    // Hands a lane's sums out by segment (a warp's stretch of the row) and adds them up.
+    DG_DEVICE Sums gather(uint64_t above, uint32_t ties)
     {
-        uint64_t above = 0, whole = 0;
-        uint32_t ties = 0;
-        const float least = with_whole ? fminf(v, floor_v) : v;
-        for (int r = 0; r < a.rows_warp; ++r) {
-            float x[E];
-            Vec<T>::unpack(data[(warp * a.rows_warp + r) * 32 + lane], x);
-            bool any = false;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                any |= x[e] > least;
-                ties += x[e] == v ? 1u : 0u;
-            }
-            if (!__any_sync(kAll, any)) continue;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (!(x[e] > least)) continue;
-                const uint64_t w = w_of(x[e]);
-                if (x[e] > v) above += w;
-                if (x[e] > floor_v) whole += w;
-            }
-        }
         above >>= kDrop;
-        whole >>= kDrop;
-        if (v == -INFINITY) ties = 0;     // (those past the row's end)
         ties = __reduce_add_sync(kAll, ties);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             above += __shfl_xor_sync(kAll, above, o);
-            whole += __shfl_xor_sync(kAll, whole, o);
         }
         const int buf = sum_turn++ & 1;
+        const int at = rank * kSampleWarps + warp;
         if (lane < ctas) {
-            const int at = rank * kSampleWarps + warp;
             st_cluster64(mapa_shared(smem_u32(&sh.above[buf][at]), lane), above);
-            st_cluster64(mapa_shared(smem_u32(&sh.whole[buf][at]), lane), whole);
             st_cluster32(mapa_shared(smem_u32(&sh.ties[buf][at]), lane), ties);
         }
-        cluster_sync_all();
-        if (warp == 0) {
-            above = whole = 0;
-            ties = 0;
-            for (int k = lane; k < ctas * kSampleWarps; k += 32) {
-                above += sh.above[buf][k];
-                whole += sh.whole[buf][k];
-                ties += sh.ties[buf][k];
-            }
-            ties = __reduce_add_sync(kAll, ties);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                above += __shfl_xor_sync(kAll, above, o);
-                whole += __shfl_xor_sync(kAll, whole, o);
-            }
-            if (lane == 0) {
-                sh.totals[0] = above;
-                sh.totals[1] = whole;
-                sh.totals[2] = ties;
-            }
+        sync();
+        above = 0;
+        ties = 0;
+        for (int k = lane; k < ctas * kSampleWarps; k += 32) {
+            above += sh.above[buf][k];
+            ties += sh.ties[buf][k];
         }
-        __syncthreads();
-        const Sums s{sh.totals[0], sh.totals[1], static_cast<uint32_t>(sh.totals[2]), buf};
-        __syncthreads();
-        return s;
+        ties = __reduce_add_sync(kAll, ties);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            above += __shfl_xor_sync(kAll, above, o);
+        }
+        return Sums{above, ties, buf};
+    }
+    // Of the whole row.
+    DG_DEVICE Sums sums_all()
+    {
+        uint64_t above = 0;
+        if (flat || weight.wide) {
+            each([&](float x, int, int) { above += w_of(x); });
+        } else {
+            rows<2>(0, a.rows_warp, [&](const uint4 &v, int) {
+                float x[E];
+                Vec<T>::unpack(v, x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) above += weight.fast(x[e], sh.table);
+            });
+        }
+        return gather(above, 0);
+    }
+    // Above v; and the tokens at v.
+    DG_DEVICE Sums sums(float v)
+    {
+        uint64_t above = 0;
+        uint32_t ties = 0;
+        rows<2>(0, a.rows_warp, [&](const uint4 &raw, int) {
+            float x[E];
+            Vec<T>::unpack(raw, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                ties += x[e] == v ? 1u : 0u;
+                if (x[e] > v) above += w_of(x[e]);
+            }
+        });
+        if (v == -INFINITY) ties = 0;     // (those past the row's end)
+        return gather(above, ties);
     }
 
     // The first of up to 32 parts, a lane's each (of weight `above` and `ties` tokens at
@@ -522,43 +682,54 @@ struct Sampler {
             if (lane >= o) end += x;
         }
         const uint32_t past = __ballot_sync(kAll, end > rem && mine > 0), any = __ballot_sync(kAll, mine > 0);
-        int at = past != 0 ? __ffs(past) - 1 : any != 0 ? 31 - __clz(any) : 0;
+        const int at = past != 0 ? __ffs(past) - 1 : any != 0 ? 31 - __clz(any) : 0;
         const uint64_t begin = __shfl_sync(kAll, end - mine, at), size = __shfl_sync(kAll, mine, at);
         rem = past != 0 ? rem - begin : size > 0 ? size - 1 : 0;     // (sums round off: the last one)
         tie_prefix += __shfl_sync(kAll, before, at);
         return at;
     }
-
-    // The token in which `rem` of the kept weight falls, in the order of the vocabulary:
-    // by the CTA that has it.
-    DG_DEVICE void draw(float v, int64_t kept, const Sums &s, uint64_t rem, int row, int skew, double log_all)
+    // The same of up to 1024 parts, a lane taking a stretch of them first.
+    DG_DEVICE int locate_of(const uint64_t *aboves, const uint32_t *tie_counts, int n, uint64_t w, int64_t kept,
+                            uint64_t &rem, int &tie_prefix)
     {
-        const uint64_t wv = v > -INFINITY ? w_of(v) : 0;
+        const int per = (n + 31) / 32;
+        uint64_t above = 0;
+        uint32_t ties = 0;
+        for (int k = lane * per; k < min(n, (lane + 1) * per); ++k) {
+            above += aboves[k];
+            ties += tie_counts[k];
+        }
+        const int at = per > 1 ? locate(above, ties, w, kept, rem, tie_prefix) : 0;
+        const int k = at * per + lane;
+        const bool mine = (per == 1 || lane < per) && k < n;
+        return at * per + locate(mine ? aboves[k] : 0, mine ? tie_counts[k] : 0, w, kept, rem, tie_prefix);
+    }
+
+    // The token in which `rem` of the kept weight `all` falls, in the order of the
+    // vocabulary: by the CTA that has it.  kept: how many of those at v are.
+    DG_DEVICE void draw(float v, int64_t kept, const Sums &s, uint64_t rem, uint64_t all, int row)
+    {
         if (warp == 0) {
-            // the segment: a lane takes `per` of them
-            const int n = ctas * kSampleWarps, per = (n + 31) / 32;
-            uint64_t above = 0;
-            uint32_t ties = 0;
-            for (int k = lane * per; k < min(n, (lane + 1) * per); ++k) {
-                above += sh.above[s.buf][k];
-                ties += sh.ties[s.buf][k];
-            }
+            const uint64_t wv = v > -INFINITY ? w_of(v) : 0;
             int prefix = 0;
-            const int at = locate(above, ties, wv, kept, rem, prefix);
-            const int k = at * per + lane;
-            const bool mine = lane < per && k < n;
-            const int in = locate(mine ? sh.above[s.buf][k] : 0, mine ? sh.ties[s.buf][k] : 0, wv, kept, rem, prefix);
+            const int seg = locate_of(sh.above[s.buf], sh.ties[s.buf], ctas * kSampleWarps, wv, kept, rem, prefix);
             if (lane == 0) {
-                sh.seg = at * per + in;
+                sh.seg = seg;
                 sh.rem = rem;
                 sh.tie_prefix = prefix;
             }
         }
         __syncthreads();
+        draw_segment(v, kept, all, row);
+    }
+    // The rest of it, once segment, remainder and ties before are in shared memory.
+    DG_DEVICE void draw_segment(float v, int64_t kept, uint64_t all, int row)
+    {
         if (sh.seg / kSampleWarps != rank) return;
+        const uint64_t wv = v > -INFINITY ? w_of(v) : 0;
         const int seg = sh.seg % kSampleWarps;
         auto row_of = [&](int r, uint64_t &above, uint32_t &ties, float (&x)[E]) {
-            Vec<T>::unpack(data[(seg * a.rows_warp + r) * 32 + lane], x);
+            Vec<T>::unpack(load(seg, r, lane), x);
             above = 0;
             ties = 0;
 #pragma unroll
@@ -583,10 +754,9 @@ struct Sampler {
         }
         __syncthreads();
         if (warp != 0) return;
-        rem = sh.rem;
+        uint64_t rem = sh.rem;
         int prefix = sh.tie_prefix;
-        const bool mine = lane < a.rows_warp;
-        const int r = locate(mine ? sh.row_above[lane] : 0, mine ? sh.row_ties[lane] : 0, wv, kept, rem, prefix);
+        const int r = locate_of(sh.row_above, sh.row_ties, a.rows_warp, wv, kept, rem, prefix);
         uint64_t above;
         uint32_t ties;
         float x[E];
@@ -611,7 +781,7 @@ struct Sampler {
             // (parts too small to count beside the rest: the segment's last kept token)
             prefix = sh.tie_prefix;
             for (int k = 0; k < a.rows_warp * 32; ++k) {
-                Vec<T>::unpack(data[seg * a.rows_warp * 32 + k], x);
+                Vec<T>::unpack(load(seg, k / 32, k % 32), x);
                 for (int e = 0; e < E; ++e) {
                     const bool tie = x[e] == v && v > -INFINITY;
                     if (x[e] > v || (tie && prefix < kept)) {
@@ -622,49 +792,386 @@ struct Sampler {
                 }
             }
         }
-        say(row, token, value, log_all);
+        say(row, token, value, all);
     }
 
-    DG_DEVICE void say(int row, int token, float value, double log_all) const
+    // The draw from all that lies above v and `kept` of the tokens at v, summed by s.
+    DG_DEVICE void draw_from(float v, int64_t kept, const Sums &s, float u, int row)
+    {
+        const uint64_t all = s.above + times(v > -INFINITY ? w_of(v) : 0, kept);
+        const uint64_t rem = min(u < 1.f ? part_of(all, u, false) : all - 1, all - 1);
+        if (rem > 0) {
+            draw(v, kept, s, rem, all, row);
+            return;
+        }
+        // the first that is kept, however light
+        uint32_t best = 0;
+        float value = 0.f;
+        each([&](float x, int r, int e) {
+            const uint32_t at = ~static_cast<uint32_t>(place(warp, r, lane, e));
+            if ((x > v || (x == v && kept > 0)) && at > best) {
+                best = at;
+                value = x;
+            }
+        });
+        const uint32_t mine = best;
+        best = largest(best, 0).x;
+        if (mine == best && best != 0) say(row, static_cast<int>(~best) - skew, value, all);   // (one thread has it)
+    }
+
+    DG_DEVICE void say(int row, int token, float value, uint64_t all) const
     {
         a.token[row] = token;
         if (a.logprob != nullptr) {
-            const double at = flat ? 0. : (static_cast<double>(value) - static_cast<double>(m)) * weight.c * 0.6931471805599453;
-            a.logprob[row] = static_cast<float>(at - log_all);
+            const double at = flat ? 0. : (static_cast<double>(value) - static_cast<double>(m)) * weight.c() * 0.6931471805599453;
+            a.logprob[row] = static_cast<float>(at - (log(static_cast<double>(all)) - kSumBits * 0.6931471805599453 +
+                                                      (flat ? 0. : weight.shift())));
         }
     }
 
-    DG_DEVICE void row(int row, uint4 *keep)
+    // ------------------------------------------------------------ few tokens
+    // Sums up to and with each thread's, over the block; *all: of all threads.
+    DG_DEVICE uint64_t scan(uint64_t v, uint64_t *all)
     {
-        constexpr uint32_t Low = E == 8 ? 0xFF80FF80u : 0xFF800000u;
-        const int64_t at = row * a.stride;
-        const int skew = static_cast<int>(at & (E - 1));     // the row begins inside 16 bytes
-        const T *base = static_cast<const T *>(a.logits) + (at - skew);
-        cluster_arrive_all();                                // (the others' shared memory: only once they run)
-        m = -INFINITY;
-#pragma unroll 4
-        for (int r = 0; r < a.rows_warp; ++r) {
-            const int first = place(warp, r, lane, 0);
-            uint4 v = make_uint4(Low, Low, Low, Low);
-            if (first >= skew && first + E <= a.V + skew) {
-                v = __ldg(reinterpret_cast<const uint4 *>(base + first));
-            } else if (first + E > skew && first < a.V + skew) {
-                T x[E];
-                *reinterpret_cast<uint4 *>(x) = v;
-                for (int e = 0; e < E; ++e)
-                    if (first + e >= skew && first + e < a.V + skew) x[e] = base[first + e];
-                v = *reinterpret_cast<const uint4 *>(x);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t x = __shfl_up_sync(kAll, v, o);
+            if (lane >= o) v += x;
+        }
+        __syncthreads();
+        if (lane == 31) sh.red[warp] = v;
+        __syncthreads();
+        uint64_t sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSampleWarps; ++w) {
+            if (w == warp) v += sum;
+            sum += sh.red[w];
+        }
+        *all = sum;
+        return v;
+    }
+
+    // The n keys of the list in rising order: counted into bins (bin_of rises with the
+    // key), put there, and each to its place among its bin's.
+    template <class F>
+    DG_DEVICE void sort(int n, F bin_of)
+    {
+        uint32_t *end = sh.hist[0];
+        for (int k = threadIdx.x; k < kBins; k += kSampleThreads) end[k] = 0;
+        __syncthreads();
+        for (int e = threadIdx.x; e < n; e += kSampleThreads) atomicAdd(end + bin_of(sh.list[e]), 1u);
+        __syncthreads();
+        uint32_t c[kBinsThread], sum = 0;
+#pragma unroll
+        for (int e = 0; e < kBinsThread; ++e) {
+            c[e] = end[kBinsThread * threadIdx.x + e];
+            sum += c[e];
+        }
+        uint64_t ignored;
+        uint32_t at = static_cast<uint32_t>(scan(sum, &ignored)) - sum;
+#pragma unroll
+        for (int e = 0; e < kBinsThread; ++e) {
+            end[kBinsThread * threadIdx.x + e] = at;
+            at += c[e];
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < n; e += kSampleThreads) {
+            const uint64_t key = sh.list[e];
+            sh.moved[atomicAdd(end + bin_of(key), 1u)] = key;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < n; e += kSampleThreads) {
+            const uint64_t key = sh.moved[e];
+            const int b = bin_of(key);
+            const uint32_t first = b > 0 ? end[b - 1] : 0, last = end[b];
+            uint32_t rank_in = first;
+            for (uint32_t o = first; o < last; ++o) rank_in += sh.moved[o] < key ? 1 : 0;
+            sh.list[rank_in] = key;
+        }
+        __syncthreads();
+    }
+    DG_DEVICE static float value_of(uint64_t key) { return of_order(~static_cast<uint32_t>(key >> 32)); }
+    // ... of n listed tokens: falling value, rising index.
+    DG_DEVICE void sort_values(int n)
+    {
+        uint32_t hi = 0, lo = 0;
+        for (int e = threadIdx.x; e < n; e += kSampleThreads) {
+            const uint32_t o = ~static_cast<uint32_t>(sh.list[e] >> 32);
+            hi = max(hi, o);
+            lo = max(lo, ~o);
+        }
+        hi = __reduce_max_sync(kAll, hi);
+        lo = __reduce_max_sync(kAll, lo);
+        if (lane == 0) sh.red[warp] = static_cast<uint64_t>(lo) << 32 | hi;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSampleWarps; ++w) {
+            hi = max(hi, static_cast<uint32_t>(sh.red[w]));
+            lo = max(lo, static_cast<uint32_t>(sh.red[w] >> 32));
+        }
+        const float top = of_order(hi), scale = static_cast<float>(kBins) / (top - of_order(~lo));
+        sort(n, [&](uint64_t key) -> int {       // (equal ones only: 0 x infinity, the first bin)
+            return min(max(static_cast<int>((top - value_of(key)) * scale), 0), kBins - 1);
+        });
+    }
+
+    // The draw from the n listed tokens, which hold all that is kept, by one CTA: of the
+    // first k (k > 0), top-p's part p of their weight or (k == 0) of `all`, and not below
+    // `least`.
+    DG_DEVICE void draw_listed(int n, int k, float p, uint64_t all, float least, float u, int row)
+    {
+        sort_values(n);
+        const int most = k > 0 ? min(k, n) : n;
+        // the weights in that order and their sums; a thread has `per` neighbours
+        int per = (most + kSampleThreads - 1) / kSampleThreads, first = threadIdx.x * per;
+        uint64_t sum = 0, listed, part;
+        for (int e = first; e < min(first + per, most); ++e) {
+            const uint64_t w = w_of(value_of(sh.list[e])) >> kDrop;
+            sh.mass[e] = w;
+            sum += w;
+        }
+        uint64_t before = scan(sum, &listed) - sum;
+        const uint64_t need = p < 1.f ? part_of(k > 0 ? listed : all, p, true) : ~0ull;
+        // how many of them are kept, and what those weigh
+        uint64_t mine = 0, count = 0;
+        for (int e = first; e < min(first + per, most); ++e) {
+            if (e == 0 || (before < need && value_of(sh.list[e]) >= least)) {
+                ++count;
+                mine += sh.mass[e];
             }
-            keep[(warp * a.rows_warp + r) * 32 + lane] = v;
+            before += sh.mass[e];
+        }
+        scan(mine, &part);
+        uint64_t number;
+        scan(count, &number);
+        const int kept = static_cast<int>(number);
+        uint64_t rem = min(u < 1.f ? part_of(part, u, false) : part - 1, part - 1);
+        // in the vocabulary's order: an index, the place in the first order beside it
+        for (int e = threadIdx.x; e < kept; e += kSampleThreads)
+            sh.list[e] = sh.list[e] << 32 | static_cast<uint32_t>(e);
+        __syncthreads();
+        const float per_bin = static_cast<float>(kBins) / static_cast<float>(a.V + E);
+        sort(kept, [&](uint64_t key) -> int {
+            return min(static_cast<int>(static_cast<float>(static_cast<uint32_t>(key >> 32)) * per_bin), kBins - 1);
+        });
+        per = (kept + kSampleThreads - 1) / kSampleThreads;
+        first = threadIdx.x * per;
+        sum = 0;
+        for (int e = first; e < min(first + per, kept); ++e) sum += sh.mass[static_cast<uint32_t>(sh.list[e])];
+        uint64_t at = scan(sum, &listed) - sum;
+        for (int e = first; e < min(first + per, kept); ++e) {
+            const uint64_t w = sh.mass[static_cast<uint32_t>(sh.list[e])];
+            // (rem == 0: the first one, however light)
+            if (rem == 0 ? e == 0 : at <= rem && rem < at + w) {
+                const int place = static_cast<int>(sh.list[e] >> 32);
+                say(row, place - skew, Vec<T>::widen(base[place]), part);
+            }
+            at += w;
+        }
+    }
+
+    // Lists a thread's hits among 16 bytes' tokens.
+    DG_DEVICE void list(const float (&x)[E], uint32_t hits, int w, int r, int l)
+    {
+        if (hits == 0) return;
+        uint32_t slot = atomicAdd(&sh.listed, static_cast<uint32_t>(__popc(hits)));
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (!(hits >> e & 1u)) continue;
+            if (slot < kList)
+                sh.list[slot] = static_cast<uint64_t>(~order_of(x[e])) << 32 | static_cast<uint32_t>(place(w, r, l, e));
+            ++slot;
+        }
+    }
+    // All that the row's CTAs have listed to the first one; how many that are (more than
+    // kList: they are not all there).
+    DG_DEVICE int join_lists()
+    {
+        __syncthreads();
+        if (ctas == 1) return static_cast<int>(sh.listed);
+        const uint32_t to_count = mapa_shared(smem_u32(&sh.listed), 0);
+        if (rank != 0) {
+            const uint32_t n = sh.listed;
+            if (threadIdx.x == 0) sh.base = add_cluster32(to_count, n);
+            __syncthreads();
+            const uint32_t to_list = mapa_shared(smem_u32(sh.list), 0), at = sh.base;
+            for (uint32_t e = threadIdx.x; e < min(n, static_cast<uint32_t>(kList)); e += kSampleThreads)
+                if (at + e < kList) st_cluster64(to_list + 8 * (at + e), sh.list[e]);
+        }
+        __syncwarp();
+        cluster_sync_all();
+        return static_cast<int>(ld_cluster32(to_count));
+    }
+
+    // ------------------------------------------------------------ top-p alone
+    // The cut of the part p of the whole weight `all`, whose bins of weights are in the
+    // histogram: its tokens and those next to it are listed and sorted by the first CTA,
+    // beside the exact weight of those above.  False: the row has to go the long way.
+    DG_DEVICE bool draw_nucleus(float p, uint64_t all, float u, int row)
+    {
+        constexpr float kSlack = 2e-4f;          // (the bins' weights are off by less than 1e-4)
+        const float s1 = weight.ch * kMassLog2;
+        const float target = p * (static_cast<float>(all) * (1.f / 8796093022208.f) / weight.most());
+        auto of_bin = [](int b) -> float { return exp2f(-b / kMassLog2) * (1.f / kMassOne); };
+        const Found hi = find<true>(0, target * (1.f + kSlack), of_bin);
+        if (!hi.reached) return false;
+        const float below = static_cast<float>(hi.bin + 1);
+        auto upto = [&](float x) -> bool { return x > -INFINITY && !((m - x) * s1 >= below); };
+        if (hi.before + hi.count < static_cast<uint32_t>(kMassOne * 0.9f * kList)) {
+            each_of(upto, [&](const uint4 &v, int w, int r, int l) {
+                float x[E];
+                Vec<T>::unpack(v, x);
+                uint32_t hits = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) hits |= upto(x[e]) ? 1u << e : 0u;
+                list(x, hits, w, r, l);
+            });
+            const int n = join_lists();
+            if (n > kList) return false;
+            if (rank == 0) draw_listed(n, 0, p, all, -INFINITY, u, row);
+            return true;
+        }
+        --hist_turn;                             // (once more in the same histogram)
+        const Found lo = find<true>(0, target * (1.f - kSlack), of_bin);
+        const float from = static_cast<float>(lo.bin), scale = static_cast<float>(kBins) / (below - from);
+        auto sub_bin = [&](float y) -> int { return min(static_cast<int>((y - from) * scale), kBins - 1); };
+        int first_bin = 0, last_bin = kBins - 1;
+        if (hi.before + hi.count - lo.before > static_cast<uint32_t>(kMassOne * 0.8f * kList)) {
+            // too many: the same once more for these alone
+            uint32_t *hist = clear();
+            each([&](float x, int, int) {
+                const float y = (m - x) * s1;
+                if (y >= from && y < below) atomicAdd(hist + sub_bin(y), 1u);
+            });
+            auto of_sub = [&](int b) -> float {
+                return exp2f(-(from + (static_cast<float>(b) + 0.5f) / scale) / kMassLog2);
+            };
+            const Found hi2 = find<true>(0, target * (1.f + kSlack) - lo.mass, of_sub);
+            --hist_turn;
+            const Found lo2 = find<true>(0, target * (1.f - kSlack) - lo.mass, of_sub);
+            if (!hi2.reached || hi2.before + hi2.count - lo2.before > kList) return false;
+            first_bin = lo2.bin;
+            last_bin = hi2.bin;
+        }
+        uint64_t above = 0;
+        rows<2>(0, a.rows_warp, [&](const uint4 &v, int r) {
             float x[E];
             Vec<T>::unpack(v, x);
+            uint32_t hits = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) m = fmaxf(m, x[e]);
+            for (int e = 0; e < E; ++e) {
+                const float y = (m - x[e]) * s1;
+                if (!(y < below)) continue;
+                const int b = y >= from ? sub_bin(y) : -1;
+                if (b >= first_bin && b <= last_bin) hits |= 1u << e;
+                else if (b < first_bin) above += w_of(x[e]);
+            }
+            list(x, hits, warp, r, lane);
+        });
+        const Sums s = gather(above, 0);
+        const int n = join_lists();
+        if (n > kList || n == 0) return false;
+        const uint64_t need = part_of(all, p, true);
+        if (rank == 0) {
+            // the segments' weights are kept where the sort leaves them
+            uint64_t *segment = sh.gather[0];
+            for (int k = threadIdx.x; k < ctas * kSampleWarps; k += kSampleThreads) segment[k] = sh.above[s.buf][k];
+            if (threadIdx.x == 0) sh.cut = Cut{-INFINITY, 0, 0};
+            sort_values(n);
+            const int per = (n + kSampleThreads - 1) / kSampleThreads, first = threadIdx.x * per;
+            uint64_t sum = 0, listed;
+            for (int e = first; e < min(first + per, n); ++e) sum += w_of(value_of(sh.list[e])) >> kDrop;
+            uint64_t before = s.above + scan(sum, &listed) - sum;
+            for (int e = first; e < min(first + per, n); ++e) {
+                const float x = value_of(sh.list[e]);
+                const uint64_t w = w_of(x) >> kDrop;
+                if (before < need && before + w >= need) {
+                    uint32_t ties = 1;
+                    for (int o = e - 1; o >= 0 && value_of(sh.list[o]) == x; --o) ++ties;
+                    sh.cut = Cut{x, ties, static_cast<uint32_t>(e + 1)};   // (and how many of the list are kept)
+                    sh.all = before + w;
+                }
+                before += w;
+            }
+            __syncthreads();
+            const Cut cut = sh.cut;
+            const int kept = static_cast<int>(cut.ties), size = E * 32 * a.rows_warp;
+            for (int e = threadIdx.x; e < kept; e += kSampleThreads)
+                atomicAdd(reinterpret_cast<unsigned long long *>(segment) + static_cast<uint32_t>(sh.list[e]) / size,
+                          static_cast<unsigned long long>(w_of(value_of(sh.list[e])) >> kDrop));
+            __syncthreads();
+            if (warp == 0 && kept > 0) {
+                const uint64_t kept_all = sh.all;
+                uint64_t rem = min(u < 1.f ? part_of(kept_all, u, false) : kept_all - 1, kept_all - 1);
+                const bool light = rem == 0;     // (the first that is kept, however light: looked for below)
+                int prefix = 0;
+                const int seg = locate_of(segment, sh.ties[0], ctas * kSampleWarps, 0, 0, rem, prefix);
+                // tokens at the cut before that segment
+                prefix = 0;
+                for (int e = kept - static_cast<int>(cut.first);; e += 32) {
+                    const bool tie = e + lane < n && value_of(sh.list[min(e + lane, n - 1)]) == cut.v;
+                    prefix += __popc(__ballot_sync(kAll, tie && static_cast<uint32_t>(sh.list[min(e + lane, n - 1)]) <
+                                                                    static_cast<uint32_t>(seg * size)));
+                    if (!__all_sync(kAll, tie)) break;
+                }
+                if (lane < ctas) {
+                    const uint32_t to = mapa_shared(smem_u32(&sh.cut), lane);
+                    st_cluster32(to, __float_as_uint(cut.v));            // (a Cut is 4-byte aligned)
+                    st_cluster32(to + 4, cut.first);
+                    st_cluster32(to + 8, light ? 2u : 1u);
+                    st_cluster32(mapa_shared(smem_u32(&sh.seg), lane), seg);
+                    st_cluster32(mapa_shared(smem_u32(&sh.tie_prefix), lane), prefix);
+                    st_cluster64(mapa_shared(smem_u32(&sh.rem), lane), rem);
+                    st_cluster64(mapa_shared(smem_u32(&sh.all), lane), kept_all);
+                }
+            } else if (warp == 0 && lane < ctas) {
+                st_cluster32(mapa_shared(smem_u32(&sh.cut), lane) + 8, 0);
+            }
         }
+        __syncwarp();
+        sync();
+        const Cut cut = sh.cut;
+        if (cut.ties == 0) return false;
+        if (cut.ties == 2) draw_from(cut.v, cut.first, sums(cut.v), u, row);
+        else draw_segment(cut.v, cut.first, sh.all, row);
+        return true;
+    }
+
+    // ------------------------------------------------------------ a row
+    // False: this CTA has nothing left to do for its row, and nobody looks at its
+    // shared memory again.
+    DG_DEVICE bool row(int row)
+    {
+        const int64_t at = row * a.stride;
+        skew = static_cast<int>(at & (E - 1));
+        base = static_cast<const T *>(a.logits) + (at - skew);
+        float t = a.temperature != nullptr ? __ldg(a.temperature + row) : 1.f;
+        const int k = a.top_k != nullptr ? __ldg(a.top_k + row) : 0;
+        const float p = a.top_p != nullptr ? __ldg(a.top_p + row) : 1.f;
+        const float low = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.f;
+        const float u = __ldg(a.u + row);
+        if (threadIdx.x == 0) sh.listed = sh.todo = 0;
         if (threadIdx.x < 32) sh.table[threadIdx.x] = kExpTable[threadIdx.x];
         __syncwarp();
-        cluster_wait_all();
-        m = of_order(largest(order_of(m), 0).x);
+        if (ctas > 1) cluster_arrive_all();                  // (the others' shared memory: only once they run)
+        uint32_t hi = 0, lo = 0;
+        typename Vec<T>::Most most = Vec<T>::none();
+        int g = 0, left = rows_group();
+        rows<8>(0, a.rows_warp, [&](const uint4 &v, int r) {
+            Vec<T>::most(most, v);
+            if (--left > 0 && r + 1 < a.rows_warp) return;
+            const float x = Vec<T>::value(most);
+            sh.group[g++][threadIdx.x] = x;
+            hi = max(hi, order_of(x));
+            if (x > -INFINITY) lo = max(lo, ~order_of(x));
+            most = Vec<T>::none();
+            left = rows_group();
+        });
+        for (; g < kGroups; ++g) sh.group[g][threadIdx.x] = -INFINITY;
+        __syncwarp();
+        if (ctas > 1) cluster_wait_all();
+        const uint2 ends = largest(hi, lo);
+        m = of_order(ends.x);
 
         const bool lead = rank == 0 && threadIdx.x == 0;
         if (m == -INFINITY) {                                // no token
@@ -672,48 +1179,123 @@ struct Sampler {
                 a.token[row] = -1;
                 if (a.logprob != nullptr) a.logprob[row] = -INFINITY;
             }
-            return;
+            return true;
         }
-        float t = a.temperature != nullptr ? __ldg(a.temperature + row) : 1.f;
-        const int k = a.top_k != nullptr ? __ldg(a.top_k + row) : 0;
-        const float p = a.top_p != nullptr ? __ldg(a.top_p + row) : 1.f;
-        const float low = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.f;
         if (!(t > 0.f) || k == 1 || p <= 0.f) {              // the first of the largest
             uint32_t best = 0;
-            each([&](float x, int r, int e) {
-                if (x == m) best = max(best, ~static_cast<uint32_t>(place(warp, r, lane, e)));
+            each_of([&](float x) -> bool { return x == m; }, [&](const uint4 &v, int w, int r, int l) {
+                float x[E];
+                Vec<T>::unpack(v, x);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (x[e] == m) best = max(best, ~static_cast<uint32_t>(place(w, r, l, e)));
             });
+            __syncwarp();
             best = largest(best, 0).x;
             if (lead) {
                 a.token[row] = static_cast<int>(~best) - skew;
                 if (a.logprob != nullptr) a.logprob[row] = 0.f;
             }
-            return;
+            return true;
         }
         flat = m == INFINITY;
         t = fminf(fmaxf(t, 7.8886091e-31f), 1.2676506e30f);  // 2^-100, 2^100
         if (!flat) weight.init(m, t);
-        // top-k's cut, min-p's, top-p's: the highest is the one
-        Cut by_k{-INFINITY, 0, 0};
-        const bool some = k > 0 && k < a.V;
-        if (flat) by_k = Cut{m, some ? static_cast<uint32_t>(k) : ~0u, 0};
-        else if (some) by_k = select(false, k, 0.f, by_k);
-        float least = by_k.v;
-        if (low > 0.f && !flat)
-            least = fmaxf(least, fminf(m, __double2float_ru(static_cast<double>(m) +
-                                                            static_cast<double>(t) * log(static_cast<double>(low)))));
+        const bool some = k > 0 && k < a.V, part = p < 1.f;
+        if (!some && !part && !(low > 0.f)) {
+            draw_from(-INFINITY, 0, sums_all(), u, row);
+            return true;
+        }
+        float min_value = -INFINITY;
+        if (low > 0.f && !flat) {
+            if (threadIdx.x == 0)
+                sh.min_value = fminf(m, __double2float_ru(static_cast<double>(m) +
+                                                          static_cast<double>(t) * log(static_cast<double>(low))));
+            __syncthreads();
+            min_value = sh.min_value;
+        }
+        // few tokens: above the k-th largest of the groups' maxima, or above min-p's value
+        const bool list_k = some && k <= kListMost;
+        const bool list_min = !list_k && low > 0.f && !(part && some);
+        if (!flat && (list_k || list_min)) {
+            uint64_t all = 0;
+            if (part && !some) all = sums_all().above;
+            float scale = 0.f, limit = INFINITY;
+            if (list_k) {
+                scale = static_cast<float>(kBins) / (m - of_order(~ends.y));
+                uint32_t *hist = clear();
+#pragma unroll 1
+                for (int g = 0; g < kGroups; ++g) {
+                    const float x = sh.group[g][threadIdx.x];
+                    if (x > -INFINITY) atomicAdd(hist + max(0, min(static_cast<int>((m - x) * scale), kBins - 1)), 1u);
+                }
+                const Found f = find<false>(k, 0.f, [](int) -> float { return 0.f; });
+                if (f.bin >= 0 && f.bin < kBins - 1) limit = static_cast<float>(f.bin + 1);
+                else scale = 0.f;                            // (all of them)
+            }
+            const float from = list_min ? min_value : -INFINITY;
+            auto wanted = [&](float x) -> bool {
+                return x >= from && x > -INFINITY && !((m - x) * scale >= limit);
+            };
+            each_of(wanted, [&](const uint4 &v, int w, int r, int l) {
+                float x[E];
+                Vec<T>::unpack(v, x);
+                uint32_t hits = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) hits |= wanted(x[e]) ? 1u << e : 0u;
+                list(x, hits, w, r, l);
+            });
+            const int n = join_lists();
+            if (n <= kList) {
+                if (rank != 0) return false;
+                draw_listed(n, some ? k : 0, p, all, min_value, u, row);
+                return true;
+            }
+        }
+        if (!flat && part && !some && !(low > 0.f)) {
+            // the whole weight, and its bins
+            const float s1 = weight.ch * kMassLog2;
+            uint32_t *hist = clear();
+            uint64_t all = 0;
+            each([&](float x, int, int) {
+                all += w_of(x);
+                const float y = (m - x) * s1;
+                if (!(y < static_cast<float>(kBins))) return;
+                const int b = static_cast<int>(y);
+                const float f = y - static_cast<float>(b);
+                atomicAdd(hist + b, static_cast<uint32_t>(fmaf(fmaf(f, fmaf(f, 2.3459e-4f, -0.0216608f), 1.f), kMassOne, 0.5f)));
+            });
+            if (draw_nucleus(p, gather(all, 0).above, u, row)) return true;
+        }
+        draw_counted(k, some, p, min_value, u, row);
+        return true;
+    }
+
+    // The cuts by counting: top-k's, min-p's, top-p's; the highest is the one.
+    DG_DEVICE void draw_counted(int k, bool some, float p, float min_value, float u, int row)
+    {
         const bool part = p < 1.f;
+        Cut by_k{-INFINITY, 0, 0};
+        if (flat) by_k = Cut{m, some ? static_cast<uint32_t>(k) : ~0u, 0};
+        else if (some) by_k = select<false>(k, 0.f, -INFINITY);
+        const float least = fmaxf(by_k.v, min_value);
         float v = least;
-        if (part && !flat) v = fmaxf(v, select(true, 0, p, by_k).v);
-        Sums s = sums(v, by_k.v, part);
+        uint64_t whole = 0;                                  // what top-p is the part of
+        if (part) {
+            const Sums s = sums(by_k.v);
+            whole = s.above;
+            if (by_k.v > -INFINITY) whole += times(w_of(by_k.v), min(by_k.first, s.ties));
+            if (!flat)
+                v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 8796093022208.f) / weight.most()),
+                                          by_k.v).v);
+        }
+        Sums s = sums(v);
         int64_t kept;
         for (int moves = 0;; ++moves) {
             const uint64_t wv = v > -INFINITY ? w_of(v) : 0;
             kept = v == by_k.v ? min(by_k.first, s.ties) : s.ties;
             if (!part || moves == kMoves) break;
-            uint64_t all = s.whole;
-            if (by_k.v > -INFINITY) all += times(w_of(by_k.v), flat ? min(by_k.first, s.ties) : by_k.first);
-            const uint64_t need = part_of(all, p, true);
+            const uint64_t need = part_of(whole, p, true);
             if (s.above >= need && s.above > 0) {            // reached before: one up
                 uint32_t up = 0;
                 each([&](float x, int, int) {
@@ -737,33 +1319,9 @@ struct Sampler {
                 if (down == 0 || of_order(down) == -INFINITY) break;
                 v = of_order(down);
             }
-            s = sums(v, by_k.v, part);
+            s = sums(v);
         }
-        const uint64_t all = s.above + times(v > -INFINITY ? w_of(v) : 0, kept);
-        const float u = __ldg(a.u + row);
-        const uint64_t rem = u < 1.f ? part_of(all, u, false) : all - 1;
-        const double log_all = log(static_cast<double>(all)) - kSumBits * 0.6931471805599453 +
-                               (flat ? 0. : weight.shift());
-        if (rem == 0) {                                      // the first that is kept, however light
-            uint32_t best = 0;
-            each([&](float x, int r, int e) {
-                if (x > v || (x == v && kept > 0)) best = max(best, ~static_cast<uint32_t>(place(warp, r, lane, e)));
-            });
-            const uint32_t mine = best;
-            best = largest(best, 0).x;
-            if (mine == best && best != 0) {
-                const int at = static_cast<int>(~best);      // (one thread has it)
-                float x[E];
-                Vec<T>::unpack(data[at / E - rank * kSampleWarps * a.rows_warp * 32], x);
-                float value = x[0];
-#pragma unroll
-                for (int e = 1; e < E; ++e)
-                    if (at % E == e) value = x[e];
-                say(row, at - skew, value, log_all);
-            }
-            return;
-        }
-        draw(v, kept, s, min(rem, all - 1), row, skew, log_all);
+        draw_from(v, kept, s, u, row);
     }
 };
 
@@ -771,24 +1329,28 @@ template <class T>
 __device__ __forceinline__ void sample_body(const SampleArgs &a)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    SampleShared &sh = *reinterpret_cast<SampleShared *>(smem);
-    uint4 *keep = reinterpret_cast<uint4 *>(smem + sizeof(SampleShared));
     griddep_wait();
     griddep_launch_dependents();
-    Sampler<T> s(a, sh, keep);
-    s.row(static_cast<int>(cluster_id_x()), keep);
+    Sampler<T> s(a, *reinterpret_cast<SampleShared *>(smem));
+    const bool stays = s.row(static_cast<int>(blockIdx.x) / a.ctas);
+    if (a.ctas == 1) return;
+    // nobody leaves while its shared memory may be read
     __syncwarp();
-    cluster_sync_all();                  // nobody leaves while its shared memory may be read
+    cluster_arrive_all();
+    if (stays) cluster_wait_all();
 }
 
 }  // namespace
 
-int sample_smem_bytes(int rows_warp)
-{
-    return static_cast<int>(sizeof(SampleShared)) + rows_warp * kSampleThreads * 16;
-}
+int sample_smem_bytes() { return static_cast<int>(sizeof(SampleShared)); }
 
-__global__ void __launch_bounds__(kSampleThreads, 2) sample_bf16_kernel(SampleArgs a) { sample_body<uint16_t>(a); }
-__global__ void __launch_bounds__(kSampleThreads, 2) sample_fp32_kernel(SampleArgs a) { sample_body<float>(a); }
+__global__ void __launch_bounds__(kSampleThreads, kSampleCtas) sample_bf16_kernel(SampleArgs a)
+{
+    sample_body<uint16_t>(a);
+}
+__global__ void __launch_bounds__(kSampleThreads, kSampleCtas) sample_fp32_kernel(SampleArgs a)
+{
+    sample_body<float>(a);
+}
 
 }  // namespace dg

@@ -12,16 +12,18 @@ struct SampleArgs {
     const void *logits;             // [R, V], rows `stride` elements apart
     int64_t stride;
     int R, V;
-    int rows_warp;                  // 512-byte rows of a logits row that a warp keeps
+    int ctas;                       // a row's CTAs, a cluster
+    int rows_warp;                  // 512-byte pieces of a row that a warp reads
     const float *temperature, *top_p, *min_p, *u;   // [R]; null (but u): not applied
     const int32_t *top_k;
     int32_t *token;
     float *logprob;                 // may be null
 };
-constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
+constexpr int kSampleThreads = 256, kSampleWarps = kSampleThreads / 32;
+constexpr int kSampleCtas = 4;        // CTAs of an SM
 constexpr int kSampleCluster = 16;    // CTAs of a row at most
-constexpr int kSampleRows = 24;       // rows_warp at most
-int sample_smem_bytes(int rows_warp);
+constexpr int kSampleRows = 400;      // rows_warp at most
+int sample_smem_bytes();
 __global__ void sample_bf16_kernel(SampleArgs a);
 __global__ void sample_fp32_kernel(SampleArgs a);
 
