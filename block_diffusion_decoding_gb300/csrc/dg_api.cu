@@ -1130,19 +1130,28 @@ int sample_kernels(DeviceInfo &di)
     return DG_OK;
 }
 
-// CTAs that share a row, and the 512-byte pieces of it that a warp of theirs reads:
-// as many as fill the GPU, two a SM, and have a piece for every warp.
+// CTAs that share a row, and the 512-byte pieces of it that a warp of theirs reads.
+// Two things count: a row's time by itself, which more CTAs shorten while each warp has
+// a few pieces to read at once (one row of 151643 bf16 logits, no filter: 57 us with 1,
+// 36 with 2, 25 with 4, 20 with 8), and the clusters that are at work at a time, which
+// take turns from where they fill the GPU (1024 such rows: 246, 235, 260, 355; long
+// rows that are not shared leave fewer threads to each SM's memory traffic and more
+// of them in L2 at a time).  DG_SAMPLE_CTAS forces a number.
 int sample_cluster(int type, int64_t stride, int R, int V, int sms, int *rows_warp)
 {
     const int per = type == DG_LOGITS_BF16 ? 8 : 4;
     const int skew = stride % per == 0 ? 0 : per - 1;
     const int vecs = (V + skew + per - 1) / per;
     auto rows = [&](int ctas) { return (vecs + ctas * kSampleThreads - 1) / (ctas * kSampleThreads); };
-    int ctas = 1;
     const char *env = std::getenv("DG_SAMPLE_CTAS");
-    if (env) ctas = std::max(1, std::min(16, std::atoi(env)));
-    else
-    while (ctas < 8 && rows(ctas) > 1 && static_cast<int64_t>(R) * ctas * 2 <= 2 * sms) ctas *= 2;
+    int ctas = 1;
+    if (env) {
+        while (ctas < kSampleCluster && ctas < std::atoi(env)) ctas *= 2;
+    } else {
+        while (rows(ctas) > 64) ctas *= 2;
+        while (ctas < 8 && rows(2 * ctas) > 2 && 2LL * R * ctas <= kSampleCtas * sms) ctas *= 2;
+        if (ctas == 8 && rows(16) >= 12 && 16LL * R <= sms) ctas = 16;
+    }
     *rows_warp = rows(ctas);
     return ctas;
 }

@@ -214,6 +214,14 @@ DG_DEVICE uint64_t part_of(uint64_t S, float f, bool up)
     return q + (up && rest != 0 ? 1 : 0);
 }
 
+// A weight in 64-bit arithmetic (kept out of line: it is seldom called, and long).
+__device__ __noinline__ uint64_t weight_in_double(float x, float m, float ch, float cl)
+{
+    const double t = (static_cast<double>(x) - static_cast<double>(m)) *
+                     (static_cast<double>(ch) + static_cast<double>(cl));
+    return t > -60. ? static_cast<uint64_t>(exp2(t) * 9007199254740992.) : 0;
+}
+
 // Weights 2^(c x - reference), c = log2 e / T, as 64-bit integers, 2^53 for 1.
 // c x is taken in units of 1/32: P, its nearest whole number, comes out of one
 // multiply-add with a large constant, exactly; what is left of it, |r| <= 1/64, of a
@@ -275,31 +283,83 @@ struct Weights {
         const uint32_t w = T + static_cast<uint32_t>(__mulhi(static_cast<int>(T), yi << 4));
         return static_cast<uint64_t>(w) << (kLaneBits - 30) >> (31 - i >> 5);   // (0 .. 61)
     }
-    DG_DEVICE uint64_t in_double(float x) const
-    {
-        const double t = (static_cast<double>(x) - static_cast<double>(m)) * c();
-        return t > -60. ? static_cast<uint64_t>(exp2(t) * 9007199254740992.) : 0;
-    }
+    DG_DEVICE uint64_t in_double(float x) const { return weight_in_double(x, m, ch, cl); }
 };
+
+// A drawn token's logprob: (x - m) / T less ln of `all`, of which 2^kSumBits stands for
+// e^shift of the largest weight.  (Once a row, by one thread.)
+__device__ __noinline__ float logprob_of(float x, float m, float ch, float cl, uint64_t all, double shift)
+{
+    const double at = (static_cast<double>(x) - static_cast<double>(m)) *
+                      (static_cast<double>(ch) + static_cast<double>(cl));
+    return static_cast<float>(at * 0.6931471805599453 - (log(static_cast<double>(all)) - kSumBits * 0.6931471805599453 + shift));
+}
+
+// What a row's CTA hands on to the out-of-line end of its way to a token.
+struct Row {
+    int row;
+    float m, t;                          // its maximum, its temperature within the range
+    int turns;                           // parities of the exchange buffers
+};
+template <class T>
+struct Sampler;
+// The ends, out of line: a row takes one of them, and the passes of them all in one
+// body are more than its registers hold.
+template <class T>
+__device__ __noinline__ void end_draw(const SampleArgs &a, SampleShared &sh, Row row, float v, int64_t kept,
+                                      uint64_t above, uint32_t ties, int buf, float u)
+{
+    Sampler<T>(a, sh, row).draw_from(v, kept, {above, ties, buf}, u);
+}
+template <class T>
+__device__ __noinline__ void end_listed(const SampleArgs &a, SampleShared &sh, Row row, int n, int k, float p,
+                                        uint64_t all, float least, float u)
+{
+    Sampler<T>(a, sh, row).draw_listed(n, k, p, all, least, u);
+}
+template <class T>
+__device__ __noinline__ void end_counted(const SampleArgs &a, SampleShared &sh, Row row, int k, float p,
+                                         float min_value, float u)
+{
+    Sampler<T>(a, sh, row).draw_counted(k, p, min_value, u);
+}
+template <class T>
+__device__ __noinline__ void end_nucleus(const SampleArgs &a, SampleShared &sh, Row row, float p, float u)
+{
+    Sampler<T> s(a, sh, row);
+    if (!s.draw_nucleus(p, u)) end_counted<T>(a, sh, s.handed(), 0, p, -INFINITY, u);
+}
 
 template <class T>
 struct Sampler {
     static constexpr int E = Vec<T>::N;
     const SampleArgs &a;
     SampleShared &sh;
-    const T *base = nullptr;             // the row, from the 16 bytes on that it begins in
-    int skew = 0;                        // where in them
+    const T *base;                       // the row, from the 16 bytes on that it begins in
+    int skew;                            // where in them
     const int warp, lane, rank, ctas;
-    int turn = 0, hist_turn = 0, sum_turn = 0;
+    int turn, hist_turn, sum_turn;
     Weights weight;
-    float m = 0.f;
-    bool flat = false;                   // the maximum is infinite: those tokens alone, alike
+    const int row;
+    float m, t;
+    bool flat;                           // the maximum is infinite: those tokens alone, alike
 
-    DG_DEVICE Sampler(const SampleArgs &args, SampleShared &s)
+    DG_DEVICE Sampler(const SampleArgs &args, SampleShared &s, const Row &r)
         : a(args), sh(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31),
-          rank(static_cast<int>(cluster_ctarank())), ctas(args.ctas)
+          rank(static_cast<int>(cluster_ctarank())), ctas(args.ctas), turn(r.turns & 1), hist_turn(r.turns >> 1 & 1),
+          sum_turn(r.turns >> 2 & 1), row(r.row), m(r.m), t(r.t)
     {
+        const int64_t at = row * a.stride;
+        skew = static_cast<int>(at & (E - 1));
+        base = static_cast<const T *>(a.logits) + (at - skew);
+        ready();
     }
+    DG_DEVICE void ready()
+    {
+        flat = m == INFINITY;
+        if (!flat) weight.init(m, t);
+    }
+    DG_DEVICE Row handed() const { return Row{row, m, t, (turn & 1) | (hist_turn & 1) << 1 | (sum_turn & 1) << 2}; }
 
     DG_DEVICE uint64_t w_of(float x) const
     {
@@ -361,7 +421,7 @@ struct Sampler {
     template <class F>
     DG_DEVICE void each(F f) const
     {
-        rows<4>(0, a.rows_warp, [&](const uint4 &v, int r) {
+        rows<2>(0, a.rows_warp, [&](const uint4 &v, int r) {
             float x[E];
             Vec<T>::unpack(v, x);
 #pragma unroll
@@ -707,7 +767,7 @@ struct Sampler {
 
     // The token in which `rem` of the kept weight `all` falls, in the order of the
     // vocabulary: by the CTA that has it.  kept: how many of those at v are.
-    DG_DEVICE void draw(float v, int64_t kept, const Sums &s, uint64_t rem, uint64_t all, int row)
+    DG_DEVICE void draw(float v, int64_t kept, const Sums &s, uint64_t rem, uint64_t all)
     {
         if (warp == 0) {
             const uint64_t wv = v > -INFINITY ? w_of(v) : 0;
@@ -720,10 +780,10 @@ struct Sampler {
             }
         }
         __syncthreads();
-        draw_segment(v, kept, all, row);
+        draw_segment(v, kept, all);
     }
     // The rest of it, once segment, remainder and ties before are in shared memory.
-    DG_DEVICE void draw_segment(float v, int64_t kept, uint64_t all, int row)
+    DG_DEVICE void draw_segment(float v, int64_t kept, uint64_t all)
     {
         if (sh.seg / kSampleWarps != rank) return;
         const uint64_t wv = v > -INFINITY ? w_of(v) : 0;
@@ -792,16 +852,16 @@ struct Sampler {
                 }
             }
         }
-        say(row, token, value, all);
+        say(token, value, all);
     }
 
     // The draw from all that lies above v and `kept` of the tokens at v, summed by s.
-    DG_DEVICE void draw_from(float v, int64_t kept, const Sums &s, float u, int row)
+    DG_DEVICE void draw_from(float v, int64_t kept, const Sums &s, float u)
     {
         const uint64_t all = s.above + times(v > -INFINITY ? w_of(v) : 0, kept);
         const uint64_t rem = min(u < 1.f ? part_of(all, u, false) : all - 1, all - 1);
         if (rem > 0) {
-            draw(v, kept, s, rem, all, row);
+            draw(v, kept, s, rem, all);
             return;
         }
         // the first that is kept, however light
@@ -816,17 +876,15 @@ struct Sampler {
         });
         const uint32_t mine = best;
         best = largest(best, 0).x;
-        if (mine == best && best != 0) say(row, static_cast<int>(~best) - skew, value, all);   // (one thread has it)
+        if (mine == best && best != 0) say(static_cast<int>(~best) - skew, value, all);   // (one thread has it)
     }
 
-    DG_DEVICE void say(int row, int token, float value, uint64_t all) const
+    DG_DEVICE void say(int token, float value, uint64_t all) const
     {
         a.token[row] = token;
-        if (a.logprob != nullptr) {
-            const double at = flat ? 0. : (static_cast<double>(value) - static_cast<double>(m)) * weight.c() * 0.6931471805599453;
-            a.logprob[row] = static_cast<float>(at - (log(static_cast<double>(all)) - kSumBits * 0.6931471805599453 +
-                                                      (flat ? 0. : weight.shift())));
-        }
+        if (a.logprob == nullptr) return;
+        if (flat) a.logprob[row] = logprob_of(0.f, 0.f, 0.f, 0.f, all, 0.);
+        else a.logprob[row] = logprob_of(value, m, weight.ch, weight.cl, all, weight.shift());
     }
 
     // ------------------------------------------------------------ few tokens
@@ -918,7 +976,7 @@ struct Sampler {
     // The draw from the n listed tokens, which hold all that is kept, by one CTA: of the
     // first k (k > 0), top-p's part p of their weight or (k == 0) of `all`, and not below
     // `least`.
-    DG_DEVICE void draw_listed(int n, int k, float p, uint64_t all, float least, float u, int row)
+    DG_DEVICE void draw_listed(int n, int k, float p, uint64_t all, float least, float u)
     {
         sort_values(n);
         const int most = k > 0 ? min(k, n) : n;
@@ -964,7 +1022,7 @@ struct Sampler {
             // (rem == 0: the first one, however light)
             if (rem == 0 ? e == 0 : at <= rem && rem < at + w) {
                 const int place = static_cast<int>(sh.list[e] >> 32);
-                say(row, place - skew, Vec<T>::widen(base[place]), part);
+                say(place - skew, Vec<T>::widen(base[place]), part);
             }
             at += w;
         }
@@ -1004,13 +1062,25 @@ struct Sampler {
     }
 
     // ------------------------------------------------------------ top-p alone
-    // The cut of the part p of the whole weight `all`, whose bins of weights are in the
-    // histogram: its tokens and those next to it are listed and sorted by the first CTA,
-    // beside the exact weight of those above.  False: the row has to go the long way.
-    DG_DEVICE bool draw_nucleus(float p, uint64_t all, float u, int row)
+    // The part p of the row's weight: the cut's tokens and those next to it, by their bin,
+    // are listed and sorted by the first CTA, beside the exact weight of those above.
+    // False: the row has to go the long way.
+    DG_DEVICE bool draw_nucleus(float p, float u)
     {
         constexpr float kSlack = 2e-4f;          // (the bins' weights are off by less than 1e-4)
         const float s1 = weight.ch * kMassLog2;
+        uint32_t *hist = clear();
+        uint64_t all = 0;
+        each([&](float x, int, int) {
+            all += w_of(x);
+            const float y = (m - x) * s1;
+            if (!(y < static_cast<float>(kBins))) return;
+            const int b = static_cast<int>(y);
+            const float f = y - static_cast<float>(b);
+            // (its weight beside that of the bin's upper end, 2^(-f / 32))
+            atomicAdd(hist + b, static_cast<uint32_t>(fmaf(fmaf(f, fmaf(f, 2.3459e-4f, -0.0216608f), 1.f), kMassOne, 0.5f)));
+        });
+        all = gather(all, 0).above;
         const float target = p * (static_cast<float>(all) * (1.f / 8796093022208.f) / weight.most());
         auto of_bin = [](int b) -> float { return exp2f(-b / kMassLog2) * (1.f / kMassOne); };
         const Found hi = find<true>(0, target * (1.f + kSlack), of_bin);
@@ -1028,7 +1098,7 @@ struct Sampler {
             });
             const int n = join_lists();
             if (n > kList) return false;
-            if (rank == 0) draw_listed(n, 0, p, all, -INFINITY, u, row);
+            if (rank == 0) end_listed<T>(a, sh, handed(), n, 0, p, all, -INFINITY, u);
             return true;
         }
         --hist_turn;                             // (once more in the same histogram)
@@ -1038,7 +1108,7 @@ struct Sampler {
         int first_bin = 0, last_bin = kBins - 1;
         if (hi.before + hi.count - lo.before > static_cast<uint32_t>(kMassOne * 0.8f * kList)) {
             // too many: the same once more for these alone
-            uint32_t *hist = clear();
+            hist = clear();
             each([&](float x, int, int) {
                 const float y = (m - x) * s1;
                 if (y >= from && y < below) atomicAdd(hist + sub_bin(y), 1u);
@@ -1132,20 +1202,21 @@ struct Sampler {
         sync();
         const Cut cut = sh.cut;
         if (cut.ties == 0) return false;
-        if (cut.ties == 2) draw_from(cut.v, cut.first, sums(cut.v), u, row);
-        else draw_segment(cut.v, cut.first, sh.all, row);
+        if (cut.ties == 2) {
+            const Sums all_of = sums(cut.v);
+            end_draw<T>(a, sh, handed(), cut.v, cut.first, all_of.above, all_of.ties, all_of.buf, u);
+        } else {
+            draw_segment(cut.v, cut.first, sh.all);
+        }
         return true;
     }
 
     // ------------------------------------------------------------ a row
     // False: this CTA has nothing left to do for its row, and nobody looks at its
     // shared memory again.
-    DG_DEVICE bool row(int row)
+    DG_DEVICE bool run()
     {
-        const int64_t at = row * a.stride;
-        skew = static_cast<int>(at & (E - 1));
-        base = static_cast<const T *>(a.logits) + (at - skew);
-        float t = a.temperature != nullptr ? __ldg(a.temperature + row) : 1.f;
+        t = a.temperature != nullptr ? __ldg(a.temperature + row) : 1.f;
         const int k = a.top_k != nullptr ? __ldg(a.top_k + row) : 0;
         const float p = a.top_p != nullptr ? __ldg(a.top_p + row) : 1.f;
         const float low = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.f;
@@ -1198,12 +1269,12 @@ struct Sampler {
             }
             return true;
         }
-        flat = m == INFINITY;
         t = fminf(fmaxf(t, 7.8886091e-31f), 1.2676506e30f);  // 2^-100, 2^100
-        if (!flat) weight.init(m, t);
+        ready();
         const bool some = k > 0 && k < a.V, part = p < 1.f;
         if (!some && !part && !(low > 0.f)) {
-            draw_from(-INFINITY, 0, sums_all(), u, row);
+            const Sums s = sums_all();
+            end_draw<T>(a, sh, handed(), -INFINITY, 0, s.above, s.ties, s.buf, u);
             return true;
         }
         float min_value = -INFINITY;
@@ -1224,10 +1295,15 @@ struct Sampler {
             if (list_k) {
                 scale = static_cast<float>(kBins) / (m - of_order(~ends.y));
                 uint32_t *hist = clear();
-#pragma unroll 1
-                for (int g = 0; g < kGroups; ++g) {
-                    const float x = sh.group[g][threadIdx.x];
+                auto count = [&](float x) {
                     if (x > -INFINITY) atomicAdd(hist + max(0, min(static_cast<int>((m - x) * scale), kBins - 1)), 1u);
+                };
+                // (below half of the maxima there are many more tokens than maxima)
+                if (2 * k <= ctas * kSampleThreads * min(kGroups, a.rows_warp)) {
+#pragma unroll 1
+                    for (int g = 0; g < kGroups; ++g) count(sh.group[g][threadIdx.x]);
+                } else {
+                    each([&](float x, int, int) { count(x); });
                 }
                 const Found f = find<false>(k, 0.f, [](int) -> float { return 0.f; });
                 if (f.bin >= 0 && f.bin < kBins - 1) limit = static_cast<float>(f.bin + 1);
@@ -1248,36 +1324,25 @@ struct Sampler {
             const int n = join_lists();
             if (n <= kList) {
                 if (rank != 0) return false;
-                draw_listed(n, some ? k : 0, p, all, min_value, u, row);
+                end_listed<T>(a, sh, handed(), n, some ? k : 0, p, all, min_value, u);
                 return true;
             }
         }
         if (!flat && part && !some && !(low > 0.f)) {
-            // the whole weight, and its bins
-            const float s1 = weight.ch * kMassLog2;
-            uint32_t *hist = clear();
-            uint64_t all = 0;
-            each([&](float x, int, int) {
-                all += w_of(x);
-                const float y = (m - x) * s1;
-                if (!(y < static_cast<float>(kBins))) return;
-                const int b = static_cast<int>(y);
-                const float f = y - static_cast<float>(b);
-                atomicAdd(hist + b, static_cast<uint32_t>(fmaf(fmaf(f, fmaf(f, 2.3459e-4f, -0.0216608f), 1.f), kMassOne, 0.5f)));
-            });
-            if (draw_nucleus(p, gather(all, 0).above, u, row)) return true;
+            end_nucleus<T>(a, sh, handed(), p, u);
+            return true;
         }
-        draw_counted(k, some, p, min_value, u, row);
+        end_counted<T>(a, sh, handed(), some ? k : 0, p, min_value, u);
         return true;
     }
 
     // The cuts by counting: top-k's, min-p's, top-p's; the highest is the one.
-    DG_DEVICE void draw_counted(int k, bool some, float p, float min_value, float u, int row)
+    DG_DEVICE void draw_counted(int k, float p, float min_value, float u)
     {
         const bool part = p < 1.f;
         Cut by_k{-INFINITY, 0, 0};
-        if (flat) by_k = Cut{m, some ? static_cast<uint32_t>(k) : ~0u, 0};
-        else if (some) by_k = select<false>(k, 0.f, -INFINITY);
+        if (flat) by_k = Cut{m, k > 0 ? static_cast<uint32_t>(k) : ~0u, 0};
+        else if (k > 0) by_k = select<false>(k, 0.f, -INFINITY);
         const float least = fmaxf(by_k.v, min_value);
         float v = least;
         uint64_t whole = 0;                                  // what top-p is the part of
@@ -1321,7 +1386,7 @@ struct Sampler {
             }
             s = sums(v);
         }
-        draw_from(v, kept, s, u, row);
+        end_draw<T>(a, sh, handed(), v, kept, s.above, s.ties, s.buf, u);
     }
 };
 
@@ -1331,8 +1396,8 @@ __device__ __forceinline__ void sample_body(const SampleArgs &a)
     extern __shared__ __align__(16) uint8_t smem[];
     griddep_wait();
     griddep_launch_dependents();
-    Sampler<T> s(a, *reinterpret_cast<SampleShared *>(smem));
-    const bool stays = s.row(static_cast<int>(blockIdx.x) / a.ctas);
+    const bool stays = Sampler<T>(a, *reinterpret_cast<SampleShared *>(smem),
+                                  Row{static_cast<int>(blockIdx.x) / a.ctas, 0.f, 1.f, 0}).run();
     if (a.ctas == 1) return;
     // nobody leaves while its shared memory may be read
     __syncwarp();
@@ -1344,11 +1409,11 @@ __device__ __forceinline__ void sample_body(const SampleArgs &a)
 
 int sample_smem_bytes() { return static_cast<int>(sizeof(SampleShared)); }
 
-__global__ void __launch_bounds__(kSampleThreads, kSampleCtas) sample_bf16_kernel(SampleArgs a)
+__global__ void __launch_bounds__(kSampleThreads, kSampleCtas) sample_bf16_kernel(const __grid_constant__ SampleArgs a)
 {
     sample_body<uint16_t>(a);
 }
-__global__ void __launch_bounds__(kSampleThreads, kSampleCtas) sample_fp32_kernel(SampleArgs a)
+__global__ void __launch_bounds__(kSampleThreads, kSampleCtas) sample_fp32_kernel(const __grid_constant__ SampleArgs a)
 {
     sample_body<float>(a);
 }

@@ -24,8 +24,8 @@ constexpr int kSampleCtas = 4;        // CTAs of an SM
 constexpr int kSampleCluster = 16;    // CTAs of a row at most
 constexpr int kSampleRows = 400;      // rows_warp at most
 int sample_smem_bytes();
-__global__ void sample_bf16_kernel(SampleArgs a);
-__global__ void sample_fp32_kernel(SampleArgs a);
+__global__ void sample_bf16_kernel(const __grid_constant__ SampleArgs a);
+__global__ void sample_fp32_kernel(const __grid_constant__ SampleArgs a);
 
 // ---------------------------------------------------------------- drafted trees
 struct TreePlanArgs {
