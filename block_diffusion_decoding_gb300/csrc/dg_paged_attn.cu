@@ -30,6 +30,13 @@
 // an infinite value stays the infinity it is.  This kernel serves few rows, whose
 // time is the memory's, so the second product is free, and the output is off by
 // little more than its own rounding (with one bf16 P by sqrt 2 of that).
+// Trees take neither way: their items are of more rows, and with the code of both in
+// the loop of tiles their softmax is a memory tile's time long.  32 trees of 10 to 32
+// nodes over caches of up to 16000 tokens (16 query heads on 8, D = 128, 1.04 GB) take
+// 175 us, 88% of a plain copy's rate, with a row in one lane and one bf16 P; 188 with
+// the columns of up to 64 rows shared out between the warps, 221 with the halves of P
+// kept, 333 with both.  The output is off by sqrt 2 of its own rounding, as the pair
+// kernel's.
 // A tile whose end is past the last key is loaded, and multiplied with P,
 // only up to the next multiple of 16 keys; the softmax warps zero the V rows
 // between the last key and there, so that whatever bits the page holds behind
@@ -227,11 +234,12 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     const uint32_t pa = tmem + Gm::ColS + (np & 1) * BKV;
                     if (lead) {
                         umma_bf16_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
-                        umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2, dv, idesc_o, 1);
+                        if (!kPagedTree<Args>) umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2, dv, idesc_o, 1);
                         auto both = [&](int kk) {
                             umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o, 1);
-                            umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2 + kk * 8, dv + kk * 128, idesc_o,
-                                         1);
+                            if (!kPagedTree<Args>)
+                                umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2 + kk * 8, dv + kk * 128, idesc_o,
+                                             1);
                         };
                         if (steps == BKV / 16) {
 #pragma unroll
@@ -268,7 +276,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
         PagedItem p;
         for (uint32_t k = 0; ok && paged_take(a, ring, k, p, false, 940); ++k) {
             const int nt = p.tv1 - p.tv0;
-            const bool few = p.rows <= Gm::FewRows;
+            const bool few = !kPagedTree<Args> && p.rows <= Gm::FewRows;
             const int r = few ? lane : q * 32 + lane;   // row within the query tile
             const bool live = r < p.rows;
             const int frow = p.frow0 + (live ? r : 0);
@@ -351,6 +359,11 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                                        make_float2(a.scale_log2, a.scale_log2), make_float2(nm, nm));
                 const float2 p2 = make_float2(fast_exp2(d2.x), fast_exp2(d2.y));
                 acc = add2(acc, p2);
+                if constexpr (kPagedTree<Args>) {
+                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(p2.x, p2.y);
+                    hi = *reinterpret_cast<const uint32_t *>(&h2);
+                    return;
+                }
                 // p down to the bf16 below the one it is cut off to
                 const int px = __viaddmax_s32(__float_as_int(p2.x), -0x10000, 0) & ~0xFFFF;
                 const int py = __viaddmax_s32(__float_as_int(p2.y), -0x10000, 0) & ~0xFFFF;
@@ -376,7 +389,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 // first and last visible column
                 const int c_hi = !kPagedTree<Args> && a.causal ? min(valid - 1, pos - key0) : valid - 1;
                 int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-                // a tree's columns beyond that, a bit each (those of this warp, with few rows)
+                // a tree's columns, a bit each
                 uint32_t nodes[BKV / 32];
                 if constexpr (kPagedTree<Args>) {
                     // (the window cuts the cached keys alone)
@@ -384,9 +397,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     c_lo = min(c_lo, max(0, -node0));
 #pragma unroll
                     for (int w = 0; w < BKV / 32; ++w)
-                        nodes[w] = !border ? 0xFFFFFFFFu
-                                           : few ? (w == 0 ? paged_nodes(a, p, i, node0 + q * CH) : 0u)
-                                                 : paged_nodes(a, p, i, node0 + 32 * w);
+                        nodes[w] = border ? paged_nodes(a, p, i, node0 + 32 * w) : 0xFFFFFFFFu;
                 }
                 ok = mbar_wait_poll(&s_full[sb], (it >> 1) & 1u, a.ws, 942);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
@@ -405,7 +416,6 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         if (q * CH + c > c_hi || q * CH + c < c_lo) sr[c] = __float_as_uint(-INFINITY);
-                        if (kPagedTree<Args> && !(nodes[0] >> c & 1u)) sr[c] = __float_as_uint(-INFINITY);
                         rmax = fmaxf(rmax, __uint_as_float(sr[c]));
                     }
                     ok = refer(rmax * a.scale_log2);
@@ -462,7 +472,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                         for (int c = 0; c < 16; ++c)
                             weigh(sr[c0 + 2 * c], sr[c0 + 2 * c + 1], nm, acc, hi[c], lo[c]);
                         tmem_st16(ts + c0 / 2, hi);
-                        tmem_st16(ts + BKV / 2 + c0 / 2, lo);
+                        if (!kPagedTree<Args>) tmem_st16(ts + BKV / 2 + c0 / 2, lo);
                     }
                     l += acc.x + acc.y;
                     tmem_wait_st();

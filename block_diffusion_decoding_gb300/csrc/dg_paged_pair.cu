@@ -456,7 +456,11 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         const int wg = (warp - 4) >> 2;          // 0: even tiles, 1: odd tiles
         const int q = warp & 3;                  // TMEM lane quadrant of the warp
         const int rr = q * 32 + lane;            // row within this CTA's 128
-        const int row = r * 128 + rr;            // row within the query tile
+        // Rows of a query tile that each CTA has.  Trees, of which many fill part of a
+        // tile, share theirs out evenly, in whole warps: the CTA with more is waited for.
+        auto share = [](const PagedItem &p) -> int {
+            return kPagedTree<Args> ? min(128, (p.rows + 63) / 64 * 32) : 128;
+        };
         const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
         const uint32_t to = tmem + lane_off + Gm::ColO;
         uint32_t it = 0, parts = 0;              // tiles and parts before this part
@@ -469,7 +473,8 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         // 32 rows, each warpgroup half of every row; the lanes of a load lie
         // along the rows.
         auto load_q = [&](const PagedItem &p) {
-            if (r * 128 + q * 32 < p.rows) {
+            const int mine = share(p), row = r * mine + rr;
+            if (q * 32 < mine && r * mine + q * 32 < p.rows) {
                 constexpr int CPR = D / 16, RPL = 32 / CPR;   // chunks of a half row, rows per load
                 const int frow = p.frow0 + min(row, p.rows - 1);
                 const int i = frow / a.G;
@@ -485,7 +490,7 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
 #pragma unroll
                 for (int n = 0; n < CPR; ++n) {
                     const int rw = q * 32 + n * RPL + lane / CPR;   // row within this CTA's 128
-                    if (r * 128 + rw >= p.rows) v[n] = make_uint4(0, 0, 0, 0);
+                    if (r * mine + rw >= p.rows) v[n] = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4 *>(smem + Gm::OffQ + rw * 128 + (c >> 3) * Gm::QAtomBytes +
                                                (((c & 7) ^ (rw & 7)) << 4)) = v[n];
                 }
@@ -504,14 +509,15 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
         if (more && p.tv1 > p.tv0) load_q(p);
         while (more && ok) {
             const int nt = p.tv1 - p.tv0;
-            const bool live = row < p.rows;
+            const int mine = share(p), row = r * mine + rr;   // row within the query tile
+            const bool live = rr < mine && row < p.rows;
             if (p.kind == kPartFirst)
                 de = PagedDesc{p.last, p.rows, p.frow0, p.s0, p.g * a.G, de.part0, {0, 0}};
             else if (p.kind == kPartLater)
                 de.part0 = 1;
             const int frow = p.frow0 + (live ? row : 0);
             const int i = frow / a.G;
-            const bool busy = r * 128 + q * 32 < p.rows;   // the warp has a live row
+            const bool busy = q * 32 < mine && r * mine + q * 32 < p.rows;   // the warp has a live row
             float m_ref = -INFINITY, l = 0.f;    // reference of, and sum over, this group's tiles
             const int pos = paged_pos(a, p, i);
             const PagedSpecial special = paged_special<BKV>(a, p, paged_edge(a, p));
