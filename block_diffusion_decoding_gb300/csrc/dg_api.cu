@@ -1171,7 +1171,7 @@ int paged_attn_run(Args a, const PagedKernels<Args> &kernels, DeviceInfo::Paged 
     int rc = check_paged_cache(c, &page_stride);
     if (rc != DG_OK) return rc;
     if (T < 0 || Hq < 1 || window < 0 || (causal != 0 && causal != 1)) return DG_ERR_INVALID_ARG;
-    if (window > 0 && !causal && !kPagedTree<Args>) return DG_ERR_INVALID_ARG;
+    if (window > 0 && !causal) return DG_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale * 2.f)) return DG_ERR_INVALID_ARG;
     if (Hq % c->Hkv != 0 || Hq / c->Hkv > 128) return DG_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(T) * Hq > (1LL << 29)) return DG_ERR_UNSUPPORTED;
@@ -1493,7 +1493,7 @@ int dg_paged_tree_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_ne
     a.words = mask_words;
     a.positions = positions;
     return paged_attn_run(a, kTreeKernels, &DeviceInfo::tree, q, q_stride, k_new, k_stride, v_new,
-                          v_stride, out, out_stride, T, Hq, scale, 0, window, c, workspace,
+                          v_stride, out, out_stride, T, Hq, scale, 1, window, c, workspace,
                           workspace_bytes, stream);
 }
 

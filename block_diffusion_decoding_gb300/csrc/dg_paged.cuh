@@ -112,10 +112,10 @@ DG_BOTH PagedSeq<I> paged_seq(const Args &a, int b, int *bad = nullptr)
     s.cap = 0;
     s.mc = s.mt;
     if constexpr (kPagedTree<Args>) {
-        // every tile the same: all keys but those before any row's window
-        const int keys = s.kv + (a.has_new ? s.n : 0);
-        s.slope = 0;
-        s.x0 = G * (a.window > 0 ? paged_min(keys, s.n + a.window + BKV) : keys);
+        // a tree's root may see a window's keys and a tile's last row all nodes before it
+        const int before = paged_max(0, a.has_new ? s.kv : s.kv - s.n);
+        s.slope = ROWS;
+        s.x0 = G * (a.window > 0 ? paged_min(before, a.window + BKV) : before);
     } else if (!a.causal) {
         s.slope = 0;
         s.x0 = G * (s.kv + (a.has_new ? s.n : 0));
@@ -490,7 +490,7 @@ struct PagedWalk {
         p.rows = paged_min(ROWS, s.n * a.G - p.frow0);
         p.nkp = (s.kv + BKV - 1) / BKV;
         int hi, lo = 0;
-        if (kPagedTree<Args> || !a.causal) {
+        if (!a.causal) {
             hi = p.nkp + (a.has_new ? (s.n + BKV - 1) / BKV : 0);
         } else {
             const int i1 = (p.frow0 + p.rows - 1) / a.G;
@@ -576,7 +576,7 @@ struct __align__(16) PagedItem {
     int32_t tv0, tv1;        // key tiles of this part
     int32_t kind;            // kPart*
     int32_t last;            // kPartFirst: the unit with the item's last part
-    int32_t pad;
+    int32_t deepest;         // trees with a window: the last of the rows' positions, from the root's on
 };
 constexpr int kPagedItems = 4;
 constexpr int kPagedLoadSleep = 60;    // ns between a load warp's looks at a full ring
@@ -626,6 +626,16 @@ DG_DEVICE void paged_walk_in(const Args &a, int u, int units, PagedRing &ring, i
     ready();
     for (uint32_t k = 0;; ++k) {
         const int e = static_cast<int>(k % kPagedItems);
+        int deepest = 0;
+        if constexpr (kPagedTree<Args>) {
+            if (a.window > 0 && more) {
+                const int base = a.has_new ? p.kv : p.kv - p.n;
+                const int i1 = (p.frow0 + p.rows - 1) / a.G;
+                for (int i = p.frow0 / a.G + (static_cast<int>(threadIdx.x) & 31); i <= i1; i += 32)
+                    deepest = max(deepest, __ldg(a.positions + p.s0 + i) - base);
+                deepest = min(__reduce_max_sync(0xFFFFFFFFu, deepest), p.n - 1);
+            }
+        }
         const bool ok = mbar_wait_poll<false, 400>(&ring.empty[e], ((k / kPagedItems) & 1u) ^ 1u, a.ws,
                                                    where, kPagedWalkLimitNs);
         if (!__all_sync(0xFFFFFFFFu, ok)) return;
@@ -644,6 +654,7 @@ DG_DEVICE void paged_walk_in(const Args &a, int u, int units, PagedRing &ring, i
                 it.kind = p.whole ? kPartWhole : p.last >= 0 ? kPartFirst : kPartLater;
                 it.last = p.last;
             }
+            if constexpr (kPagedTree<Args>) it.deepest = deepest;
             ring.item[e] = it;
             mbar_arrive(&ring.full[e]);
         }
@@ -855,7 +866,7 @@ DG_DEVICE PagedEdge paged_edge(const Args &a, const PagedItem &p)
 {
     const int base = a.has_new ? p.kv : p.kv - p.n;
     // any node of a tree may be hidden from any row, and any row be the root
-    if constexpr (kPagedTree<Args>) return {base - 1, base + p.n - 1};
+    if constexpr (kPagedTree<Args>) return {base - 1, base + p.deepest};
     return {base + p.frow0 / a.G, base + (p.frow0 + p.rows - 1) / a.G};
 }
 template <class Args>
@@ -963,8 +974,8 @@ DG_DEVICE float paged_weight(const PagedArgs &a, const uint16_t *k, int64_t q_of
                  __uint_as_float(static_cast<uint32_t>(k[d]) << 16), s);
     return fast_exp2(fmaf(s, a.scale_log2, -m_ref));
 }
-// Token i of a part's sequence: its place among the keys, or (with a window) its
-// position in the tree, which lies among those of the tree's nodes.
+// Token i of a part's sequence: its place among the keys, or (trees with a window)
+// its position, which lies among the places of the tree's nodes.
 template <class Args>
 DG_DEVICE int paged_pos(const Args &a, const PagedItem &p, int i)
 {
@@ -973,8 +984,8 @@ DG_DEVICE int paged_pos(const Args &a, const PagedItem &p, int i)
         if (a.window > 0) return min(max(__ldg(a.positions + p.s0 + i), base), base + p.n - 1);
     return base + i;
 }
-// Whether token i sees nodes node .. node + 31 of its tree, a bit each; those
-// before the tree (node < 0) are cached keys.
+// Whether token i sees nodes node .. node + 31 of its tree, a bit each, as far as
+// they are not after it; those before the tree (node < 0) are cached keys.
 DG_DEVICE uint32_t paged_nodes(const PagedTreeArgs &a, const PagedItem &p, int i, int node)
 {
     const uint32_t *row = a.mask + static_cast<int64_t>(p.s0 + i) * a.words;
@@ -989,7 +1000,7 @@ DG_DEVICE bool paged_sees(const Args &a, const PagedItem &p, int i, int pos, int
 {
     if constexpr (kPagedTree<Args>) {
         const int base = a.has_new ? p.kv : p.kv - p.n;
-        if (key >= base) return paged_nodes(a, p, i, key - base) & 1u;
+        if (key >= base) return key <= base + i && (paged_nodes(a, p, i, key - base) & 1u);
         return a.window == 0 || key > pos - a.window;
     }
     return (!a.causal || key <= pos) && (a.window == 0 || key > pos - a.window);

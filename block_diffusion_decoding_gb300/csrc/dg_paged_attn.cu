@@ -318,7 +318,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 if (lane == 0) mbar_arrive(q_ready);
             }
             // position of this row, and the keys it sees
-            const int pos = paged_pos(a, p, i);
+            const int pos = paged_pos(a, p, i), last = kPagedTree<Args> ? (a.has_new ? p.kv : p.kv - p.n) + i : pos;
             const PagedEdge edge = paged_edge(a, p);
             const int buf = static_cast<int>(parts % 3u);
             float m_ref = -INFINITY, l = 0.f;
@@ -387,7 +387,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     if (border && paged_look<Gm>(v_tile, valid, threadIdx.x - 64)) zeroed[buf] = 1;
                 }
                 // first and last visible column
-                const int c_hi = !kPagedTree<Args> && a.causal ? min(valid - 1, pos - key0) : valid - 1;
+                const int c_hi = a.causal ? min(valid - 1, last - key0) : valid - 1;
                 int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
                 // a tree's columns, a bit each
                 uint32_t nodes[BKV / 32];

@@ -556,7 +556,8 @@ __device__ __forceinline__ void paged_pair_body(const CUtensorMap *map_k, const 
                         // first and last visible column
                         const int valid = paged_valid<BKV>(p, p.tv0 + j), key0 = paged_key0<BKV>(p, p.tv0 + j);
                         const int at = pos - key0;
-                        const int c_hi = !kPagedTree<Args> && a.causal ? min(valid - 1, at) : valid - 1;
+                        const int last = kPagedTree<Args> ? (a.has_new ? p.kv : p.kv - p.n) + i - key0 : at;
+                        const int c_hi = a.causal ? min(valid - 1, last) : valid - 1;
                         int c_lo = a.window > 0 ? max(at - a.window + 1, 0) : 0;
                         // (a tree's window cuts the cached keys alone)
                         if (kPagedTree<Args>)

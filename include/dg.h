@@ -296,9 +296,9 @@ int dg_tree_plan(const int32_t *parents, int T, int window, int appended, uint32
 
 /* dg_paged_attn for trees: node i of sequence b sees the keys before the     */
 /* tree, with window > 0 those at places after positions[q_start[b] + i] -     */
-/* window, and of the tree's own keys those whose bit is set in its row of    */
-/* mask (bits from n_b on are ignored; nodes past 32 mask_words are seen by    */
-/* nobody; the window does not look at the bits).  The tree's keys are k_new,  */
+/* window, and of the tree's own keys up to its own those whose bit is set in  */
+/* its row of mask (bits of later nodes are ignored; nodes past 32 mask_words  */
+/* are seen by nobody; the window does not look at the bits).  The tree's keys are k_new,  */
 /* v_new, or without them the last n_b cached ones.  A node that sees no key   */
 /* gets a row of zeros.  positions are read with a window alone (else may be  */
 /* NULL); one outside [base, base + n_b) counts as the nearest inside.        */

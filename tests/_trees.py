@@ -53,7 +53,7 @@ def attention(batch, mask, positions, window, fresh, stored):
             words = mask[t0 + i]
             seen = [j for j in range(max(0, base)) if not window or j > positions[t0 + i] - window]
             seen += [base + j for j in range(n)
-                     if base + j >= 0 and j < 32 * len(words) and words[j // 32] >> j % 32 & 1]
+                     if base + j >= 0 and j <= i and j < 32 * len(words) and words[j // 32] >> j % 32 & 1]
             for h in range(batch.Hq):
                 if not seen:
                     out[t0 + i, h] = 0

@@ -142,7 +142,8 @@ def test_attn_strides_and_wide_masks(monkeypatch, kernel):
 @pytest.mark.parametrize("kernel", ["single", "pair"])
 @pytest.mark.parametrize("fresh", [False, True])
 def test_attn_rows_that_see_nothing_and_bits_of_nobody(monkeypatch, kernel, fresh):
-    """No cached key and no bit: zeros; bits past the tree's nodes mean nothing; any pattern of bits is taken."""
+    """No cached key and no bit: zeros; bits of later nodes and past the tree's mean nothing; of the others any
+    pattern is taken."""
     monkeypatch.setenv("DG_PAGED_KERNEL", kernel)
     out = check_attn([6, 50], [0, 0], 4, 2, 128, 16, fresh=fresh, words=2,
                      mask=lambda rows: [[0, 0] if i % 3 == 0 else [x | 0xFFFFFFC0 if i < 6 else x, 0xFFFFFFFF if i < 6 else y]

@@ -1,5 +1,5 @@
 """The tree attention's work is divided into parts that are all of it, as the paged attention's: every key that a
-node at any position of its tree may see is in one part of every item."""
+node may see, at the depth of its index (further up a window's keys are earlier ones), is in one part of every item."""
 import pytest
 
 import tests._paged_division as division
@@ -18,8 +18,8 @@ def program(tmp_path_factory):
 
 
 def trees(seed, n, falling):
-    """The other test's batches; no causal mask, the windows stay."""
-    return [c[:7] + [0] + c[8:] for c in cases(seed, n, falling)]
+    """The other test's batches; a node sees none behind it, so that every batch is a causal one."""
+    return [c[:7] + [1] + c[8:] for c in cases(seed, n, falling)]
 
 
 def test_on_the_host(program):
