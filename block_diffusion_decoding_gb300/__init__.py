@@ -409,6 +409,7 @@ class PagedCache:
                                    k.stride(0) if n_pages > 1 else 0, n_pages, page_size,
                                    max_pages, B, Hkv, D)
         self.ref = ctypes.byref(self.args)
+        self.first = tuple((t.data_ptr(), t.shape, t.stride()) for t in (k, v))   # (see _layers)
 
 
 def qk_norm_rope(q, k, q_out, k_out, positions, p: HeadParams, stream=None):
@@ -541,15 +542,18 @@ def _layers(layers, cache: PagedCache, what: str):
     Hkv, D] whose first is the cache's (None: the cache's alone)."""
     if layers is None:
         return 1, 0
-    for t, first in zip(layers, (cache.k, cache.v)):
-        if t.dtype is not _BF16 or t.dim() != 5 or t.shape[1:] != first.shape or t.shape[0] < 1:
+    n = apart = None
+    for t, (address, shape, stride) in zip(layers, cache.first):
+        if t.dtype is not _BF16 or t.shape[1:] != shape:
             _refuse(what, "bf16 layers [layers, n_pages, page_size, Hkv, D] of the cache's shape are wanted")
-        if t.data_ptr() != first.data_ptr() or t.stride()[1:] != first.stride():
+        s = t.stride()
+        if t.data_ptr() != address or s[1:] != stride:
             _refuse(what, "the first layer is not the cache")
-    k, v = layers
-    if k.shape[0] != v.shape[0] or (k.shape[0] > 1 and k.stride(0) != v.stride(0)):
-        _refuse(what, "k's and v's layers are not alike")
-    return k.shape[0], k.stride(0) if k.shape[0] > 1 else 0
+        count, s0 = t.shape[0], s[0]
+        if count < 1 or n is not None and (count != n or n > 1 and s0 != apart):
+            _refuse(what, "k's and v's layers are not alike")
+        n, apart = count, s0
+    return n, apart if n > 1 else 0
 
 
 def paged_tree_commit_workspace() -> int:

@@ -1547,8 +1547,7 @@ int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const in
     if (T > 0 && (!tokens || !parents || !sampled)) return DG_ERR_INVALID_ARG;
     if (T > (1 << 29) || path_max > (1 << 20)) return DG_ERR_UNSUPPORTED;
     if ((rc = check_layers(c, page_stride, layers, layer_stride)) != DG_OK) return rc;
-    if (kv_len_out != c->kv_len && kv_len_out < c->kv_len + c->B && c->kv_len < kv_len_out + c->B)
-        return DG_ERR_INVALID_ARG;
+    if (kv_len_out < c->kv_len + c->B && c->kv_len < kv_len_out + c->B) return DG_ERR_INVALID_ARG;
     if ((rc = check_status_ws(workspace, workspace_bytes)) != DG_OK) return rc;
     DeviceInfo *di = nullptr;
     if ((rc = current_device_info(&di)) != DG_OK) return rc;
@@ -1578,14 +1577,10 @@ int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const in
     a.row = c->Hkv * c->D;
     a.ws = static_cast<WsHeader *>(workspace);
     cudaStream_t st = as_stream(stream);
-    const bool pdl = use_pdl(st);
-    const int64_t walks = (static_cast<int64_t>(c->B) * 32 + kTreeWalkThreads - 1) / kTreeWalkThreads;
-    DG_CUDA_TRY(launch_kernel(tree_walk_kernel, dim3(static_cast<unsigned>(walks)), dim3(kTreeWalkThreads), 0,
-                              st, pdl, a));
-    DG_LAUNCHED();
-    const int64_t units = 2LL * c->B * layers * ((a.row / 8 + kTreeMoveThreads - 1) / kTreeMoveThreads);
-    DG_CUDA_TRY(launch_kernel(tree_move_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(units, 16 * di->sms))),
-                              dim3(kTreeMoveThreads), 0, st, pdl, a));
+    const int64_t units = 2LL * c->B * layers * ((a.row / 8 + kTreeCommitThreads - 1) / kTreeCommitThreads);
+    DG_CUDA_TRY(launch_kernel(tree_commit_kernel,
+                              dim3(static_cast<unsigned>(std::min<int64_t>(units, 16 * di->sms))),
+                              dim3(kTreeCommitThreads), 0, st, use_pdl(st), a));
     DG_LAUNCHED();
     return DG_OK;
 }
@@ -1696,6 +1691,12 @@ int dg_paged_release(const dg_page_pool *pool, const dg_paged_cache *c, const in
     a.n = n;
     cudaStream_t st = as_stream(stream);
     const bool pdl = use_pdl(st);
+    // few pages: one CTA does both, in less than a second launch takes
+    if (static_cast<int64_t>(n) * a.max_pages + a.n_pages <= kReleaseSmall && n <= kPoolThreads) {
+        DG_CUDA_TRY(launch_kernel(paged_release_small_kernel, dim3(1), dim3(kPoolThreads), 0, st, pdl, a));
+        DG_LAUNCHED();
+        return DG_OK;
+    }
     DG_CUDA_TRY(launch_kernel(paged_release_kernel, dim3(n), dim3(kReleaseThreads), 0, st, pdl, a));
     DG_LAUNCHED();
     DG_CUDA_TRY(launch_kernel(paged_collect_kernel, dim3(1), dim3(kPoolThreads), 0, st, pdl, a));

@@ -223,6 +223,88 @@ __global__ void __launch_bounds__(kForkThreads) paged_fork_copy_kernel(PagePoolA
     }
 }
 
+namespace {
+
+// Gives a place's page back.
+DG_DEVICE void give_back(const PagePoolArgs &a, int32_t *place)
+{
+    const int page = *place;
+    if (page < 0) return;
+    *place = -1;
+    if (page >= a.n_pages) {
+        report_error(a.ws, DG_ERR_DEVICE, 1132);
+        return;
+    }
+    const int before = atomicSub(a.refs + page, 1);
+    if (before == 1) {
+        atomicExch(a.refs + page, kPageFreed);
+    } else if (before < 1) {                     // nobody's already
+        atomicAdd(a.refs + page, 1);
+        report_error(a.ws, DG_ERR_DEVICE, 1133);
+    }
+}
+
+// The pages that have been given back go onto the free ones, the lowest first.  One
+// CTA of kPoolThreads.
+DG_DEVICE void collect(const PagePoolArgs &a, int *sums)
+{
+    constexpr int Per = 8;                       // pages a thread looks at in a turn
+    int n_free = count_free(a);
+    for (int p0 = 0; p0 < a.n_pages; p0 += Per * kPoolThreads) {
+        const int first = p0 + Per * static_cast<int>(threadIdx.x);
+        uint32_t freed = 0;
+#pragma unroll
+        for (int e = 0; e < Per; ++e)
+            if (first + e < a.n_pages && __ldcg(a.refs + first + e) <= kPageFreed / 2) freed |= 1u << e;
+        int total;
+        int at = n_free + block_scan(__popc(freed), Per * kPoolThreads, sums, &total) - __popc(freed);
+        for (; freed != 0; freed &= freed - 1) {
+            const int page = first + __ffs(freed) - 1;
+            a.refs[page] = 0;
+            if (at < a.n_pages) a.free_pages[at] = page;
+            else report_error(a.ws, DG_ERR_DEVICE, 1134);
+            ++at;
+        }
+        n_free = min(n_free + total, a.n_pages);
+    }
+    if (threadIdx.x == 0) *a.n_free = n_free;
+}
+
+}  // namespace
+
+// Takes the pages of up to kPoolThreads sequences back, by one CTA.
+__global__ void __launch_bounds__(kPoolThreads) paged_release_small_kernel(PagePoolArgs a)
+{
+    __shared__ int sums[32];
+    __shared__ int s_seq[kPoolThreads];          // -1: not (or no longer) one
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x;
+    int seq = tid < a.n ? a.dst[tid] : -1;
+    s_seq[tid] = seq;
+    __syncthreads();
+    if (tid < a.n) {
+        bool bad = seq < 0 || seq >= a.B;
+        for (int j = 0; j < tid && !bad; ++j) bad = s_seq[j] == seq;
+        if (bad) {
+            report_error(a.ws, DG_ERR_DEVICE, 1131);
+            seq = -1;
+        } else {
+            a.kv_len[seq] = 0;
+        }
+    }
+    __syncthreads();
+    s_seq[tid] = seq;
+    __syncthreads();
+    for (int x = tid; x < a.n * a.max_pages; x += kPoolThreads) {
+        const int i = x / a.max_pages;
+        if (s_seq[i] >= 0)
+            give_back(a, a.page_table + static_cast<int64_t>(s_seq[i]) * a.max_pages + x - i * a.max_pages);
+    }
+    __syncthreads();
+    collect(a, sums);
+}
+
 // Takes a sequence's pages back, a block a sequence.
 __global__ void __launch_bounds__(kReleaseThreads) paged_release_kernel(PagePoolArgs a)
 {
@@ -238,51 +320,17 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_release_kernel(PagePool
         return;
     }
     int32_t *row = a.page_table + static_cast<int64_t>(seq) * a.max_pages;
-    for (int m = threadIdx.x; m < a.max_pages; m += kReleaseThreads) {
-        const int page = row[m];
-        if (page < 0) continue;
-        row[m] = -1;
-        if (page >= a.n_pages) {
-            report_error(a.ws, DG_ERR_DEVICE, 1132);
-            continue;
-        }
-        const int before = atomicSub(a.refs + page, 1);
-        if (before == 1) {
-            atomicExch(a.refs + page, kPageFreed);
-        } else if (before < 1) {                 // nobody's already
-            atomicAdd(a.refs + page, 1);
-            report_error(a.ws, DG_ERR_DEVICE, 1133);
-        }
-    }
+    for (int m = threadIdx.x; m < a.max_pages; m += kReleaseThreads) give_back(a, row + m);
     if (threadIdx.x == 0) a.kv_len[seq] = 0;
 }
 
-// The pages that the releases took back go onto the free ones, the lowest first.
+// The pages that the releases took back.
 __global__ void __launch_bounds__(kPoolThreads) paged_collect_kernel(PagePoolArgs a)
 {
-    constexpr int Per = 8;                       // pages a thread looks at in a turn
     __shared__ int sums[32];
     griddep_wait();
     griddep_launch_dependents();
-    int n_free = count_free(a);
-    for (int p0 = 0; p0 < a.n_pages; p0 += Per * kPoolThreads) {
-        const int first = p0 + Per * static_cast<int>(threadIdx.x);
-        uint32_t freed = 0;
-#pragma unroll
-        for (int e = 0; e < Per; ++e)
-            if (first + e < a.n_pages && a.refs[first + e] <= kPageFreed / 2) freed |= 1u << e;
-        int total;
-        int at = n_free + block_scan(__popc(freed), Per * kPoolThreads, sums, &total) - __popc(freed);
-        for (; freed != 0; freed &= freed - 1) {
-            const int page = first + __ffs(freed) - 1;
-            a.refs[page] = 0;
-            if (at < a.n_pages) a.free_pages[at] = page;
-            else report_error(a.ws, DG_ERR_DEVICE, 1134);
-            ++at;
-        }
-        n_free = min(n_free + total, a.n_pages);
-    }
-    if (threadIdx.x == 0) *a.n_free = n_free;
+    collect(a, sums);
 }
 
 }  // namespace dg

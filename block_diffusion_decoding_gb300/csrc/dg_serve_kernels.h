@@ -50,9 +50,8 @@ struct TreeCommitArgs {
     int row;                        // values of a token in a page: Hkv D
     WsHeader *ws;
 };
-constexpr int kTreeWalkThreads = 128, kTreeMoveThreads = 128;
-__global__ void tree_walk_kernel(TreeCommitArgs a);
-__global__ void tree_move_kernel(TreeCommitArgs a);
+constexpr int kTreeCommitThreads = 128;
+__global__ void tree_commit_kernel(TreeCommitArgs a);
 
 // ---------------------------------------------------------------- page pool
 struct PageForkJob {
@@ -76,9 +75,11 @@ constexpr int kPoolThreads = 1024;    // of the single-CTA kernels: sequences of
 constexpr int kForkThreads = 256;
 constexpr int kForkBytes = 32768;     // of a page that a block copies
 constexpr int kReleaseThreads = 256;
+constexpr int kReleaseSmall = 32768;  // places in tables and pages of a release by one CTA
 __global__ void paged_reserve_kernel(PagePoolArgs a);
 __global__ void paged_fork_kernel(PagePoolArgs a);
 __global__ void paged_fork_copy_kernel(PagePoolArgs a);
+__global__ void paged_release_small_kernel(PagePoolArgs a);
 __global__ void paged_release_kernel(PagePoolArgs a);
 __global__ void paged_collect_kernel(PagePoolArgs a);
 

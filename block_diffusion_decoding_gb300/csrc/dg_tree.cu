@@ -69,76 +69,106 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(TreePlanArg
     }
 }
 
-// The accepted path of each sequence, by a warp: from the root (its first node)
-// on to the first child whose token is the one sampled at its parent.
-__global__ void __launch_bounds__(kTreeWalkThreads) tree_walk_kernel(TreeCommitArgs a)
+// The accepted path of a sequence, and its keys' and values' moves to the places behind
+// the cached tokens: node path[j] to place j of the tree's.  A block has up to 128
+// times 16 bytes of every token, of the keys or the values of one layer.  Each block
+// walks the path for itself, which takes a read of the tree and some votes, less than
+// a launch; the first one of a sequence writes it down.  path[j] rises and is at least
+// j, so in the order of j no place is written before it has been read, and a thread
+// keeps that order by itself.
+// Bound by latency: lengths and tree, pages, tokens, one after another.  64 trees of up
+// to 32 nodes, 16 layers of 8 heads of 128 (9.2 MB): 8.2 us with the walk in a kernel of
+// its own.
+__global__ void __launch_bounds__(kTreeCommitThreads) tree_commit_kernel(TreeCommitArgs a)
 {
+    constexpr int Batch = 8;                     // tokens a thread has in flight
+    constexpr int Kept = 4;                      // nodes of the first 128 that a lane of the walk keeps
+    __shared__ int path[kTreeCommitThreads];
+    __shared__ int64_t from[kTreeCommitThreads], to[kTreeCommitThreads];   // (-1: no move)
+    __shared__ int found;
     griddep_wait();
     griddep_launch_dependents();
-    const int b = (blockIdx.x * kTreeWalkThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    if (b >= a.B) return;
-    const int r0 = __ldg(a.q_start + b), r1 = __ldg(a.q_start + b + 1), k0 = a.kv_len[b];
-    const Rows s = rows_of(a.q_start, b, a.T);
-    const int kv = min(max(k0, 0), a.max_kv);
-    const int base = kv - s.n;
-    if (lane == 0 && (r0 != s.s0 || r1 != s.s0 + s.n || kv != k0 || base < 0))
-        report_error(a.ws, DG_ERR_DEVICE, 1111);
-    int32_t *path = a.path + static_cast<int64_t>(b) * a.path_max;
-    int n = 0, next = -1;
-    if (s.n > 0 && base >= 0) {
-        int at = 0;
-        for (;;) {
-            if (lane == 0) path[n] = at;
-            ++n;
-            next = __ldg(a.sampled + s.s0 + at);
-            if (n == a.path_max) break;
-            int child = -1;
-            for (int c0 = at + 1; c0 < s.n && child < 0; c0 += 32) {
-                const int c = c0 + lane;
-                const bool fits = c < s.n && __ldg(a.parents + s.s0 + c) == at && __ldg(a.tokens + s.s0 + c) == next;
-                const uint32_t any = __ballot_sync(0xFFFFFFFFu, fits);
-                if (any != 0) child = c0 + __ffs(any) - 1;
-            }
-            if (child < 0) break;
-            at = child;
-        }
-    }
-    for (int j = n + lane; j < a.path_max; j += 32) path[j] = 0;
-    if (lane == 0) {
-        a.n_path[b] = n;
-        a.next[b] = next;
-        a.kv_out[b] = n > 0 ? base + n : kv;
-    }
-}
-
-// Moves the accepted nodes' keys and values of every layer to the places behind the
-// cached tokens: node path[j] to place j of the tree's.  path[j] rises and is at
-// least j, so in the order of j no place is written before it has been read; a
-// thread has 16 bytes of every token and keeps that order by itself.
-__global__ void __launch_bounds__(kTreeMoveThreads) tree_move_kernel(TreeCommitArgs a)
-{
-    constexpr int Batch = 8;
-    __shared__ int64_t from[kTreeMoveThreads], to[kTreeMoveThreads];   // (-1: no such page)
-    griddep_wait();
-    griddep_launch_dependents();
-    const int chunks = (a.row / 8 + kTreeMoveThreads - 1) / kTreeMoveThreads;
+    const int lane = threadIdx.x & 31;
+    const int chunks = (a.row / 8 + kTreeCommitThreads - 1) / kTreeCommitThreads;
     const int64_t units = static_cast<int64_t>(a.B) * a.layers * 2 * chunks;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int c = static_cast<int>(unit % chunks) * kTreeMoveThreads + threadIdx.x;
+        const int c = static_cast<int>(unit % chunks) * kTreeCommitThreads + threadIdx.x;
         const int64_t rest = unit / chunks;
         const int kind = static_cast<int>(rest & 1);
         const int layer = static_cast<int>((rest >> 1) % a.layers);
         const int b = static_cast<int>((rest >> 1) / a.layers);
-        const int n = a.n_path[b];
-        const int base = a.kv_out[b] - n;
-        const int32_t *path = a.path + static_cast<int64_t>(b) * a.path_max;
-        if (n == 0 || path[n - 1] == n - 1) continue;     // nothing, or all in place
+        const bool scribe = rest == static_cast<int64_t>(b) * a.layers * 2 && unit % chunks == 0;
+        const int r0 = __ldg(a.q_start + b), r1 = __ldg(a.q_start + b + 1), k0 = __ldg(a.kv_len + b);
+        const int s0 = min(max(r0, 0), a.T), n = min(max(r1, s0), a.T) - s0;
+        const int kv = min(max(k0, 0), a.max_kv), base = kv - n;
+        const bool can = n > 0 && base >= 0;
+        if (scribe && threadIdx.x == 0 && (r0 != s0 || r1 != s0 + n || kv != k0 || base < 0))
+            report_error(a.ws, DG_ERR_DEVICE, 1111);
+        int parent[Kept], token[Kept], drawn[Kept];
+        if (threadIdx.x < 32 && can) {
+#pragma unroll
+            for (int e = 0; e < Kept; ++e) {
+                const int i = 32 * e + lane;
+                parent[e] = i < n ? __ldg(a.parents + s0 + i) : -1;
+                token[e] = i < n ? __ldg(a.tokens + s0 + i) : 0;
+                drawn[e] = i < n ? __ldg(a.sampled + s0 + i) : 0;
+            }
+        }
         uint16_t *pool = (kind ? a.v : a.k) + layer * a.layer_stride;
-        for (int j0 = 0; j0 < n; j0 += kTreeMoveThreads) {
-            const int m = min(kTreeMoveThreads, n - j0);
-            __syncthreads();                              // the offsets before have been read
+        int at = -1, taken = 0;                  // the walk's: last node, tokens; of warp 0
+        int next = -1;
+        bool more = can;
+        for (int j0 = 0; more || j0 == 0; j0 += kTreeCommitThreads) {
+            __syncthreads();                     // the batch before has been moved
+            if (threadIdx.x < 32) {
+                int m = 0;
+                while (more && m < kTreeCommitThreads) {
+                    int child = -1;
+                    if (at < 0) {
+                        child = 0;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < Kept; ++e) {
+                            const bool fits = 32 * e + lane > at && 32 * e + lane < n && parent[e] == at && token[e] == next;
+                            const uint32_t any = __ballot_sync(0xFFFFFFFFu, fits);
+                            if (child < 0 && any != 0) child = 32 * e + __ffs(any) - 1;
+                        }
+                        for (int i0 = max(at + 1, 32 * Kept); i0 < n && child < 0; i0 += 32) {
+                            const int i = i0 + lane;
+                            const bool fits = i < n && __ldg(a.parents + s0 + i) == at && __ldg(a.tokens + s0 + i) == next;
+                            const uint32_t any = __ballot_sync(0xFFFFFFFFu, fits);
+                            if (any != 0) child = i0 + __ffs(any) - 1;
+                        }
+                    }
+                    if (child < 0) {
+                        more = false;
+                        break;
+                    }
+                    at = child;
+                    if (at < 32 * Kept) {
+#pragma unroll
+                        for (int e = 0; e < Kept; ++e) {
+                            const int x = __shfl_sync(0xFFFFFFFFu, drawn[e], at & 31);
+                            if (at >> 5 == e) next = x;
+                        }
+                    } else {
+                        next = __ldg(a.sampled + s0 + at);
+                    }
+                    if (lane == 0) {
+                        path[m] = at;
+                        if (scribe) a.path[static_cast<int64_t>(b) * a.path_max + taken] = at;
+                    }
+                    ++m;
+                    if (++taken == a.path_max) more = false;
+                }
+                if (lane == 0) found = more ? -m : m;      // (the last batch: not negative)
+            }
+            __syncthreads();
+            const int count = found;
+            const int m = abs(count);
+            more = count < 0;
             if (static_cast<int>(threadIdx.x) < m) {
-                const int j = j0 + threadIdx.x;
+                const int j = j0 + threadIdx.x, node = path[threadIdx.x];
                 auto place = [&](int key) -> int64_t {
                     const int page = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + key / a.page_size);
                     if (page < 0 || page >= a.n_pages) {
@@ -147,26 +177,33 @@ __global__ void __launch_bounds__(kTreeMoveThreads) tree_move_kernel(TreeCommitA
                     }
                     return page * a.page_stride + static_cast<int64_t>(key % a.page_size) * a.row;
                 };
-                const bool moves = path[j] != j;
-                from[threadIdx.x] = moves ? place(base + path[j]) : -1;
-                to[threadIdx.x] = moves ? place(base + j) : -1;
+                from[threadIdx.x] = node != j ? place(base + node) : -1;
+                to[threadIdx.x] = node != j ? place(base + j) : -1;
             }
             __syncthreads();
-            if (c >= a.row / 8) continue;
-            for (int j = 0; j < m; j += Batch) {
-                uint4 x[Batch];
+            if (c < a.row / 8) {
+                for (int j = 0; j < m; j += Batch) {
+                    uint4 x[Batch];
 #pragma unroll
-                for (int e = 0; e < Batch; ++e) {
-                    x[e] = make_uint4(0, 0, 0, 0);
-                    if (j + e < m && from[j + e] >= 0)
-                        x[e] = *reinterpret_cast<const uint4 *>(pool + from[j + e] + 8 * c);
+                    for (int e = 0; e < Batch; ++e) {
+                        x[e] = make_uint4(0, 0, 0, 0);
+                        if (j + e < m && from[j + e] >= 0)
+                            x[e] = *reinterpret_cast<const uint4 *>(pool + from[j + e] + 8 * c);
+                    }
+#pragma unroll
+                    for (int e = 0; e < Batch; ++e)
+                        if (j + e < m && to[j + e] >= 0) *reinterpret_cast<uint4 *>(pool + to[j + e] + 8 * c) = x[e];
                 }
-#pragma unroll
-                for (int e = 0; e < Batch; ++e)
-                    if (j + e < m && to[j + e] >= 0) *reinterpret_cast<uint4 *>(pool + to[j + e] + 8 * c) = x[e];
             }
         }
-        __syncthreads();
+        if (scribe && threadIdx.x < 32) {
+            for (int j = taken + lane; j < a.path_max; j += 32) a.path[static_cast<int64_t>(b) * a.path_max + j] = 0;
+            if (lane == 0) {
+                a.n_path[b] = taken;
+                a.next[b] = next;
+                a.kv_out[b] = taken > 0 ? base + taken : kv;
+            }
+        }
     }
 }
 

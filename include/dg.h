@@ -318,7 +318,8 @@ int dg_paged_tree_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_ne
 /*   path [B, path_max]   the accepted nodes, 0 past their end                 */
 /*   n_path [B]           how many (0: the sequence has no new tokens)         */
 /*   next [B]             what was sampled at the last one (-1: none)          */
-/*   kv_len_out [B]       base + n_path, the cache's new length; may be kv_len */
+/*   kv_len_out [B]       base + n_path, the cache's new length (not kv_len     */
+/*                        itself)                                              */
 /* Keys and values of the accepted nodes move to the places base .. base +     */
 /* n_path - 1 of the sequence's pages, in all layers: layer l's pages are k +  */
 /* l * layer_stride and v + l * layer_stride.  Every other byte of the cache   */

@@ -221,3 +221,19 @@ def test_corrupt_counts_are_reported():
     dg.paged_release(p.pool, i32([1]), p.ws)
     assert dg.read_device_status(p.ws, clear=True) == 7
     status_ok(p.ws)
+
+
+def test_release_of_many():
+    """More sequences, or places, than one CTA takes back; the same one twice among them."""
+    r = random.Random(5)
+    p = Pool(1300, 4000, 30, 16)
+    p.check(p.reserve([r.choice([0, 5, 40, 60]) for _ in range(1300)]))
+    p.check(p.release(r.sample(range(1300), 700)))
+    p.check(p.reserve([r.choice([0, 5, 20]) for _ in range(1300)]))
+    seqs = r.sample(range(1300), 1200)
+    assert p.release(seqs + [seqs[3], 1300]) == 7
+    p.check(7)
+    p = Pool(3, 40000, 20000, 16)
+    p.check(p.reserve([16 * 9000, 16 * 19999, 16]))
+    p.check(p.release([1]))
+    p.check(p.release([2, 0]))

@@ -282,19 +282,18 @@ def test_commit(n, kv, Hkv, D, page, layers, path_max, pad, interleaved):
     assert moved > 0 or len(n) == 1
 
 
-def test_commit_long_paths_and_lengths_in_place():
-    """A path longer than a block's turn; kv_len_out is kv_len itself; one layer without `layers`."""
+def test_commit_long_paths():
+    """A path longer than a block's turn; one layer without `layers`."""
     n, kv = [400], [21]
     b, k, v, kd, vd, c, trees, tokens, sampled, flat, out, ws, total = commit_case(n, kv, 1, 128, 32, 1, 380, 4)
     trees = [[-1, 0] + list(range(1, 399))]
     trees[0][2] = 0                                              # node 1 is passed by: everything moves
     tokens, sampled = [[7] * 400], [[7] * 400]
     tokens[0][1] = 8
-    out[3] = c.kv_len
     dg.paged_tree_commit(flat(tokens), flat(trees), flat(sampled), c, *out, ws)
     status_ok(ws)
     path = [0] + list(range(2, 381))
-    assert out[0][0].tolist() == path and c.kv_len.tolist() == [21 + 380] and out[2].tolist() == [7]
+    assert out[0][0].tolist() == path and out[3].tolist() == [21 + 380] and out[2].tolist() == [7]
     places = [(b.table[0, x // 32].item(), x % 32) for x in range(421)]
     rows = [k[0, places[21 + i][0], places[21 + i][1]].clone() for i in path]
     for j, row in enumerate(rows):

@@ -106,7 +106,7 @@ def test_commit_refuses(lib):
                      (dict(path=None), INVALID), (dict(n_path=None), INVALID), (dict(next=None), INVALID),
                      (dict(lens=None), INVALID), (dict(T=-1), INVALID), (dict(path_max=0), INVALID),
                      (dict(path_max=1 << 21), UNSUPPORTED), (dict(T=1 << 30), UNSUPPORTED),
-                     (dict(lens=GOOD + 4096 + 4), INVALID), (dict(ws=None), WORKSPACE), (dict(n=255), WORKSPACE),
+                     (dict(lens=GOOD + 4096 + 4), INVALID), (dict(lens=GOOD + 4096), INVALID), (dict(ws=None), WORKSPACE), (dict(n=255), WORKSPACE),
                      (dict(ws=GOOD + 8), ALIGNMENT)):
         assert commit(lib, **kw) == code, kw
 
@@ -149,6 +149,7 @@ def test_binding_checks_its_tensors(lib):
     c.v = torch.zeros_like(c.k)
     both = torch.zeros(2, 4, 3, 16, 2, 128, dtype=torch.bfloat16)
     c.k, c.v = both[0, 0], both[1, 0]
+    c.first = tuple((t.data_ptr(), t.shape, t.stride()) for t in (c.k, c.v))
     assert dg._layers(None, c, "x") == (1, 0)
     assert dg._layers((both[0], both[1]), c, "x") == (4, c.k.numel())
     assert dg._layers((both[0, :1], both[1, :1]), c, "x") == (1, 0)
