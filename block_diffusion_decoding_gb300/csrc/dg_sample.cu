@@ -11,10 +11,9 @@
 //                groups whose maximum reaches a value that the cut lies above are read
 //                again for the tokens above it, which are sorted and summed by one CTA.
 //                For top-k the value is the k-th largest of the groups' maxima;
-//   top-p        the weights, rounded, are summed in bins of 1/32 of a factor of 2; the
+//   top-p        the weights, rounded, are summed in bins of 1/8 of a factor of 2; the
 //                tokens of the bin that holds the cut (or of a part of it) are sorted, as
-//                above, beside the exact sum of what lies above it; then as without a
-//                filter;
+//                above, beside the exact sums of the row and of what lies above them;
 //   the rest     (a larger k, cuts that lie elsewhere) the cut is found by counting: the
 //                tokens fall into 1024 bins by their distance from the maximum, those
 //                of the bin it lies in into 1024 again, then by their bits; the exact
@@ -38,8 +37,8 @@ namespace {
 constexpr int kBins = 1024;
 constexpr int kBinsThread = kBins / kSampleThreads;
 constexpr float kBinsLog2 = 16.f;        // of the search by counting: bins to a factor of 2 in weight
-constexpr float kMassLog2 = 32.f;        // of top-p's bins of weights
-constexpr float kMassOne = 8192.f;       // a weight at its bin's upper end, in these
+constexpr float kMassOne = 8192.f;       // a weight at its bin's upper end, in sums of rounded ones
+constexpr int kMassBins = 256;           // of top-p's: 8 to a factor of 2
 constexpr int kGroups = 8;               // groups of a thread's tokens
 constexpr int kList = 1536;              // tokens that are sorted at most
 constexpr int kListMost = 1024;          // of which top-k's k
@@ -54,7 +53,7 @@ constexpr int kMoves = 1 << 14;
 struct Found {
     int bin;                             // -1: the target lies past the last one
     uint32_t count, before;              // tokens in it, and above it
-    float mass;                          // weight above it
+    float mass, all;                     // weight above it, and of all bins
     bool reached;                        // (with rounded weights: else the last one with a token)
 };
 
@@ -73,6 +72,7 @@ struct alignas(16) SampleShared {
     union {
         struct {
             uint64_t above[2][kSegments];   // by segment: weight above the cut
+            uint64_t whole[kSegments];      // (once a row)
             uint32_t ties[2][kSegments];    // and tokens at it
             uint64_t row_above[kSampleRows];
             uint32_t row_ties[kSampleRows];
@@ -226,10 +226,11 @@ __device__ __noinline__ uint64_t weight_in_double(float x, float m, float ch, fl
 // c x is taken in units of 1/32: P, its nearest whole number, comes out of one
 // multiply-add with a large constant, exactly; what is left of it, |r| <= 1/64, of a
 // second, rounded at 2^-31, and c's low half with it.  Then 2^(j / 32) from a table
-// and 2^r = 1 + y by its series, y rounded at 2^-28.  The reference is the maximum's
-// own P, so the largest weight lies within 2^(1/64) of 1 and a row of equal logits
-// has equal ones, with nothing cut off.  Where |c x| is too large for that (2^16 and
-// more), the same in 64-bit arithmetic.
+// (turned so that P's own low bits find it) and 2^r = 1 + y by its series, to r^3 (the
+// next term is below 2^-30), y rounded at 2^-28.  The reference is the maximum's own P,
+// so the largest weight lies within 2^(1/64) of 1 and a row of equal logits has equal
+// ones, with nothing cut off.  Where |c x| is too large for that (2^16 and more), the
+// same in 64-bit arithmetic.
 struct Weights {
     float ch, cl, floor;
     int ref;
@@ -247,6 +248,8 @@ struct Weights {
         ref = __float_as_int(fmaf(max, ch, 393216.f));   // 1.5 x 2^18: a unit in the last place is 1/32
         wide = !(fabsf(max) * ch < 65536.f);
     }
+    // What the table holds at place p.
+    DG_DEVICE uint32_t turned(int p) const { return kExpTable[(p - ref) & 31]; }
     DG_DEVICE double c() const { return static_cast<double>(ch) + static_cast<double>(cl); }
     // ln of what a weight of 2^53 stands for beside exp((x - max) / T) = 1
     DG_DEVICE double shift() const
@@ -255,33 +258,41 @@ struct Weights {
         const double at = static_cast<double>(__int_as_float(ref) - 393216.f);
         return (at - static_cast<double>(m) * c()) * 0.6931471805599453;
     }
-    // The maximum's weight beside its reference (2^53), a factor next to 1.
-    DG_DEVICE float most() const
-    {
-        if (wide) return 1.f;
-        const float P = __int_as_float(ref) - 393216.f;
-        return exp2f(fmaf(m, cl, fmaf(m, ch, -P)));
-    }
     DG_DEVICE uint64_t operator()(float x, const uint32_t *table) const
     {
         return wide ? in_double(x) : fast(x, table);
     }
+    // P as an integer: 32 to a factor of 2, `ref` for the largest.
+    DG_DEVICE int unit(float x) const { return __float_as_int(fmaf(fmaxf(x, floor), ch, 393216.f)); }
     DG_DEVICE uint64_t fast(float x, const uint32_t *table) const
+    {
+        int p;
+        return fast(x, table, p);
+    }
+    DG_DEVICE uint64_t fast(float x, const uint32_t *table, int &p) const
     {
         const float y = fmaxf(x, floor);
         const float P = fmaf(y, ch, 393216.f);
-        const float Pf = P - 393216.f;
-        float r = fmaf(y, ch, -Pf);
+        p = __float_as_int(P);
+        float r = fmaf(y, ch, 393216.f - P);
         r = fmaf(y, cl, r);
-        const int i = __float_as_int(P) - ref;
-        float s = fmaf(r, 0.0096181291f, 0.055504109f);  // ln2^4 / 24, ln2^3 / 6
-        s = fmaf(r, s, 0.24022651f);                     // ln2^2 / 2
+        float s = fmaf(r, 0.055504109f, 0.24022651f);    // ln2^3 / 6, ln2^2 / 2
         s = fmaf(r, s, 0.69314718f);
         const float B = fmaf(r, s, 0.046875f);           // 1.5 x 2^-5: in units of 2^-28
-        const uint32_t T = table[i & 31];
-        const int yi = __float_as_int(B) - __float_as_int(0.046875f);
-        const uint32_t w = T + static_cast<uint32_t>(__mulhi(static_cast<int>(T), yi << 4));
-        return static_cast<uint64_t>(w) << (kLaneBits - 30) >> (31 - i >> 5);   // (0 .. 61)
+        const uint32_t T = table[p & 31];
+        const int yi = static_cast<int>(static_cast<uint32_t>(__float_as_int(B)) * 16u -
+                                        static_cast<uint32_t>(__float_as_int(0.046875f)) * 16u);
+        uint32_t w;                                      // T (1 + y)
+        asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(w) : "r"(T), "r"(yi));
+        return static_cast<uint64_t>(w) << (kLaneBits - 30) >> (ref + 31 - p >> 5);   // (0 .. 61)
+    }
+    // Its weight beside that of unit q, which is not far above, in units of 1 / kMassOne.
+    DG_DEVICE uint32_t beside(float x, int q) const
+    {
+        const float r = fmaf(fmaxf(x, floor), ch, 393216.f - __int_as_float(q));
+        const float w = fmaf(r, fmaf(r, fmaf(r, 0.055504109f, 0.24022651f), 0.69314718f), 1.f);
+        return static_cast<uint32_t>(__float_as_int(fmaf(w, kMassOne, 12582912.f)) -
+                                     __float_as_int(12582912.f));    // (1.5 x 2^23: to a whole number)
     }
     DG_DEVICE uint64_t in_double(float x) const { return weight_in_double(x, m, ch, cl); }
 };
@@ -333,6 +344,7 @@ __device__ __noinline__ void end_nucleus(const SampleArgs &a, SampleShared &sh, 
 template <class T>
 struct Sampler {
     static constexpr int E = Vec<T>::N;
+    static constexpr int kAhead = E == 4 ? 2 : 1;   // 16 bytes that a pass has on their way
     const SampleArgs &a;
     SampleShared &sh;
     const T *base;                       // the row, from the 16 bytes on that it begins in
@@ -358,6 +370,11 @@ struct Sampler {
     {
         flat = m == INFINITY;
         if (!flat) weight.init(m, t);
+    }
+    // The weights' table, once the maximum is known; before the next barrier.
+    DG_DEVICE void lay_table()
+    {
+        if (threadIdx.x < 32) sh.table[threadIdx.x] = flat ? 0 : weight.turned(static_cast<int>(threadIdx.x));
     }
     DG_DEVICE Row handed() const { return Row{row, m, t, (turn & 1) | (hist_turn & 1) << 1 | (sum_turn & 1) << 2}; }
 
@@ -415,6 +432,27 @@ struct Sampler {
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 if (r + e < r1) f(v[e], r + e);
+        }
+    }
+    // The same for all rows, N ahead of those at work.
+    template <int N, class F>
+    DG_DEVICE void rows_ahead(F f) const
+    {
+        uint4 v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < a.rows_warp) v[e] = load(warp, e, lane);
+#pragma unroll 1
+        for (int r = 0; r < a.rows_warp; r += N) {
+            uint4 now[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                now[e] = v[e];
+                if (r + N + e < a.rows_warp) v[e] = load(warp, r + N + e, lane);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (r + e < a.rows_warp) f(now[e], r + e);
         }
     }
     // f(x, row of the warp, number in the 16 bytes) for each of this thread's tokens.
@@ -494,10 +532,10 @@ struct Sampler {
         return hist;
     }
     // The bin in which the tokens reach `target` in number, or with `Mass` (counts
-    // weighed by of_bin) target_mass in weight; where rounded sums stay short of that,
+    // weighed by of_bin) target_mass in weight, or `part` of all of it; where rounded sums stay short of that,
     // the last one that is not empty.
     template <bool Mass, class F>
-    DG_DEVICE Found find(uint32_t target, float target_mass, F of_bin)
+    DG_DEVICE Found find(uint32_t target, float target_mass, F of_bin, float part = 0.f)
     {
         const int buf = hist_turn++ & 1;
         if (threadIdx.x == 0) {
@@ -543,10 +581,16 @@ struct Sampler {
             sh.scan_f[warp] = f_end;
         }
         __syncthreads();
-        for (int w = 0; w < warp; ++w) {
-            n_end += sh.scan_u[w];
-            f_end += sh.scan_f[w];
+        float f_all = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSampleWarps; ++w) {
+            if (w < warp) {
+                n_end += sh.scan_u[w];
+                f_end += sh.scan_f[w];
+            }
+            f_all += sh.scan_f[w];
         }
+        if (part > 0.f) target_mass = part * f_all;
         if (n_sum > 0) {
             if (Mass ? f_end >= target_mass : n_end >= target) atomicMin(&sh.claim, static_cast<int>(threadIdx.x));
             if (Mass) atomicMax(&sh.last, static_cast<int>(threadIdx.x));
@@ -554,14 +598,14 @@ struct Sampler {
         __syncthreads();
         const bool reached = sh.claim < kSampleThreads;
         if (static_cast<int>(threadIdx.x) == (reached ? sh.claim : max(sh.last, 0))) {
-            Found got{-1, 0, 0, 0.f, reached};
+            Found got{-1, 0, 0, 0.f, f_all, reached};
             uint32_t n_before = n_end - n_sum;
             float f_before = f_end - f_sum;
             bool stop = false;
 #pragma unroll
             for (int e = 0; e < kBinsThread; ++e) {
                 if (n[e] > 0 && !stop) {
-                    got = Found{b + e, n[e], n_before, f_before, reached};
+                    got = Found{b + e, n[e], n_before, f_before, f_all, reached};
                     stop = reached && (Mass ? f_before + f[e] >= target_mass : n_before + n[e] >= target);
                 }
                 n_before += n[e];
@@ -658,33 +702,41 @@ struct Sampler {
         uint32_t ties;                    // tokens at the cut
         int buf;
     };
-    // Hands a lane's sums out by segment (a warp's stretch of the row) and adds them up.
-    DG_DEVICE Sums gather(uint64_t above, uint32_t ties)
+    // Hands a lane's sums out by segment (a warp's stretch of the row) and adds them up;
+    // with Whole another one, whose sum alone is wanted.  more_above: in the sums' units.
+    template <bool Whole = false>
+    DG_DEVICE Sums gather(uint64_t above, uint32_t ties, uint64_t *whole = nullptr, uint64_t more_above = 0)
     {
-        above >>= kDrop;
+        above = (above >> kDrop) + more_above;
         ties = __reduce_add_sync(kAll, ties);
+        uint64_t more = Whole ? *whole >> kDrop : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             above += __shfl_xor_sync(kAll, above, o);
+            if (Whole) more += __shfl_xor_sync(kAll, more, o);
         }
         const int buf = sum_turn++ & 1;
         const int at = rank * kSampleWarps + warp;
         if (lane < ctas) {
             st_cluster64(mapa_shared(smem_u32(&sh.above[buf][at]), lane), above);
+            if (Whole) st_cluster64(mapa_shared(smem_u32(&sh.whole[at]), lane), more);
             st_cluster32(mapa_shared(smem_u32(&sh.ties[buf][at]), lane), ties);
         }
         sync();
-        above = 0;
+        above = more = 0;
         ties = 0;
         for (int k = lane; k < ctas * kSampleWarps; k += 32) {
             above += sh.above[buf][k];
+            if (Whole) more += sh.whole[k];
             ties += sh.ties[buf][k];
         }
         ties = __reduce_add_sync(kAll, ties);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             above += __shfl_xor_sync(kAll, above, o);
+            if (Whole) more += __shfl_xor_sync(kAll, more, o);
         }
+        if (Whole) *whole = more;
         return Sums{above, ties, buf};
     }
     // Of the whole row.
@@ -694,7 +746,7 @@ struct Sampler {
         if (flat || weight.wide) {
             each([&](float x, int, int) { above += w_of(x); });
         } else {
-            rows<2>(0, a.rows_warp, [&](const uint4 &v, int) {
+            rows_ahead<kAhead>([&](const uint4 &v, int) {
                 float x[E];
                 Vec<T>::unpack(v, x);
 #pragma unroll
@@ -1062,84 +1114,147 @@ struct Sampler {
     }
 
     // ------------------------------------------------------------ top-p alone
-    // The part p of the row's weight: the cut's tokens and those next to it, by their bin,
-    // are listed and sorted by the first CTA, beside the exact weight of those above.
-    // False: the row has to go the long way.
+    DG_DEVICE int sub_bin(float x, float top, float scale) const
+    {
+        return min(max(static_cast<int>(fmaf(-x, weight.ch, top) * scale), 0), kBins - 1);
+    }
+    // The part p of the row's weight.  The weights, rounded, are summed in bins, 4 of the
+    // weights' units each, a place a lane so that no two meet; then the whole weight
+    // exactly, and of the tokens above the bins that the cut may lie in, which are listed
+    // and sorted by the first CTA.  False: the row has to go the long way.
     DG_DEVICE bool draw_nucleus(float p, float u)
     {
         constexpr float kSlack = 2e-4f;          // (the bins' weights are off by less than 1e-4)
-        const float s1 = weight.ch * kMassLog2;
-        uint32_t *hist = clear();
-        uint64_t all = 0;
-        each([&](float x, int, int) {
-            all += w_of(x);
-            const float y = (m - x) * s1;
-            if (!(y < static_cast<float>(kBins))) return;
-            const int b = static_cast<int>(y);
-            const float f = y - static_cast<float>(b);
-            // (its weight beside that of the bin's upper end, 2^(-f / 32))
-            atomicAdd(hist + b, static_cast<uint32_t>(fmaf(fmaf(f, fmaf(f, 2.3459e-4f, -0.0216608f), 1.f), kMassOne, 0.5f)));
-        });
-        all = gather(all, 0).above;
-        const float target = p * (static_cast<float>(all) * (1.f / 8796093022208.f) / weight.most());
-        auto of_bin = [](int b) -> float { return exp2f(-b / kMassLog2) * (1.f / kMassOne); };
-        const Found hi = find<true>(0, target * (1.f + kSlack), of_bin);
-        if (!hi.reached) return false;
-        const float below = static_cast<float>(hi.bin + 1);
-        auto upto = [&](float x) -> bool { return x > -INFINITY && !((m - x) * s1 >= below); };
-        if (hi.before + hi.count < static_cast<uint32_t>(kMassOne * 0.9f * kList)) {
-            each_of(upto, [&](const uint4 &v, int w, int r, int l) {
-                float x[E];
-                Vec<T>::unpack(v, x);
-                uint32_t hits = 0;
+        if (weight.wide) return false;
+        uint32_t *lanes = &sh.hist[0][0];        // [bin][lane]
+        static_assert(offsetof(SampleShared, hist) == 0 && offsetof(SampleShared, gather) >= kMassBins * 32 * 4,
+                      "hist, list and mass are the bins' room");
+        static_assert(kMassBins == kSampleThreads, "a thread adds a bin up");
+        for (int k = threadIdx.x; k < kMassBins * 32; k += kSampleThreads) lanes[k] = 0;
+        __syncthreads();
+        const int ref = weight.ref;
+        rows_ahead<kAhead>([&](const uint4 &v, int) {
+            float x[E];
+            Vec<T>::unpack(v, x);
 #pragma unroll
-                for (int e = 0; e < E; ++e) hits |= upto(x[e]) ? 1u << e : 0u;
-                list(x, hits, w, r, l);
-            });
-            const int n = join_lists();
-            if (n > kList) return false;
-            if (rank == 0) end_listed<T>(a, sh, handed(), n, 0, p, all, -INFINITY, u);
-            return true;
+            for (int e = 0; e < E; ++e) {
+                const int b = (ref - weight.unit(x[e])) >> 2;
+                if (b < kMassBins) atomicAdd(lanes + b * 32 + lane, weight.beside(x[e], ref - 4 * b));
+            }
+        });
+        __syncthreads();
+        uint32_t mine = 0;
+#pragma unroll 8
+        for (int l = 0; l < 32; ++l) mine += lanes[threadIdx.x * 32 + ((l + lane) & 31)];   // (spread over the banks)
+        __syncthreads();
+        uint32_t *hist = sh.hist[hist_turn & 1];
+        for (int k = threadIdx.x; k < kBins; k += kSampleThreads) hist[k] = k == static_cast<int>(threadIdx.x) ? mine : 0;
+        auto of_bin = [](int b) -> float { return exp2f(-b / 8.f) * (1.f / kMassOne); };
+        const Found hi = find<true>(0, 0.f, of_bin, p * (1.f + kSlack));
+        if (!hi.reached) return false;
+        // (a token's rounded weight is at least 0.92 of kMassOne, at most 1.01)
+        const bool all_listed = hi.before + hi.count < static_cast<uint32_t>(kMassOne * 0.85f * kList);
+        int from = 0, first_sub = 0, last_sub = kBins - 1;
+        float mass_from = 0.f;                   // (rounded, above bin `from`)
+        float top = 0.f, scale = 0.f;            // bins of the bins: their upper end, how many to a factor of 2
+        auto of_sub = [&](int b) -> float {
+            const float end = static_cast<float>(ref - __float_as_int(top + 393216.f)) / 32.f;
+            return exp2f(-(end + (static_cast<float>(b) + 0.5f) / scale));
+        };
+        bool split = false;                      // the bins hold more than the CTAs can list
+        if (!all_listed) {
+            --hist_turn;                         // (once more in the same histogram)
+            const Found lo = find<true>(0, 0.f, of_bin, p * (1.f - kSlack));
+            from = lo.bin;
+            mass_from = lo.mass;
+            top = __int_as_float(ref - 4 * from + 1) - 393216.f;
+            scale = kBins * 8.f / static_cast<float>(hi.bin - from + 2);
+            split = hi.before + hi.count - lo.before > static_cast<uint32_t>(kMassOne * 0.65f * kList) * ctas;
+            if (split) {
+                hist = clear();
+                rows_ahead<kAhead>([&](const uint4 &v, int) {
+                    float x[E];
+                    Vec<T>::unpack(v, x);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int b = (ref - weight.unit(x[e])) >> 2;
+                        if (b >= from && b <= hi.bin) atomicAdd(hist + sub_bin(x[e], top, scale), 1u);
+                    }
+                });
+                const Found hi2 = find<true>(0, p * (1.f + kSlack) * hi.all - mass_from, of_sub);
+                --hist_turn;
+                const Found lo2 = find<true>(0, p * (1.f - kSlack) * hi.all - mass_from, of_sub);
+                if (!hi2.reached || hi2.before + hi2.count - lo2.before > kList) return false;
+                first_sub = lo2.bin;
+                last_sub = hi2.bin;
+            }
         }
-        --hist_turn;                             // (once more in the same histogram)
-        const Found lo = find<true>(0, target * (1.f - kSlack), of_bin);
-        const float from = static_cast<float>(lo.bin), scale = static_cast<float>(kBins) / (below - from);
-        auto sub_bin = [&](float y) -> int { return min(static_cast<int>((y - from) * scale), kBins - 1); };
-        int first_bin = 0, last_bin = kBins - 1;
-        if (hi.before + hi.count - lo.before > static_cast<uint32_t>(kMassOne * 0.8f * kList)) {
-            // too many: the same once more for these alone
-            hist = clear();
-            each([&](float x, int, int) {
-                const float y = (m - x) * s1;
-                if (y >= from && y < below) atomicAdd(hist + sub_bin(y), 1u);
-            });
-            auto of_sub = [&](int b) -> float {
-                return exp2f(-(from + (static_cast<float>(b) + 0.5f) / scale) / kMassLog2);
-            };
-            const Found hi2 = find<true>(0, target * (1.f + kSlack) - lo.mass, of_sub);
-            --hist_turn;
-            const Found lo2 = find<true>(0, target * (1.f - kSlack) - lo.mass, of_sub);
-            if (!hi2.reached || hi2.before + hi2.count - lo2.before > kList) return false;
-            first_bin = lo2.bin;
-            last_bin = hi2.bin;
-        }
-        uint64_t above = 0;
-        rows<2>(0, a.rows_warp, [&](const uint4 &v, int r) {
+        uint64_t above = 0, all = 0, listed_above = 0;
+        rows_ahead<kAhead>([&](const uint4 &v, int r) {
             float x[E];
             Vec<T>::unpack(v, x);
             uint32_t hits = 0;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float y = (m - x[e]) * s1;
-                if (!(y < below)) continue;
-                const int b = y >= from ? sub_bin(y) : -1;
-                if (b >= first_bin && b <= last_bin) hits |= 1u << e;
-                else if (b < first_bin) above += w_of(x[e]);
+                int unit;
+                const uint64_t w = weight.fast(x[e], sh.table, unit);
+                all += w;
+                const int b = (ref - unit) >> 2;
+                if (b > hi.bin) continue;
+                int side = b < from ? -1 : 0;
+                if (split && side == 0) {
+                    const int sub = sub_bin(x[e], top, scale);
+                    side = sub < first_sub ? -1 : sub > last_sub ? 1 : 0;
+                }
+                if (side < 0) above += w;
+                hits |= side == 0 ? 1u << e : 0u;
             }
             list(x, hits, warp, r, lane);
         });
-        const Sums s = gather(above, 0);
+        if (!all_listed && !split) {
+            // Each CTA has its part of the bins' tokens; those that the cut cannot be among
+            // are told apart by bins of their own, and leave the list.
+            hist = clear();
+            const int n = static_cast<int>(min(sh.listed, static_cast<uint32_t>(kList)));
+            const bool lost = sh.listed > kList;
+            for (int e = threadIdx.x; e < n; e += kSampleThreads)
+                atomicAdd(hist + sub_bin(value_of(sh.list[e]), top, scale), 1u);
+            const Found hi2 = find<true>(0, p * (1.f + kSlack) * hi.all - mass_from, of_sub);
+            --hist_turn;
+            const Found lo2 = find<true>(0, p * (1.f - kSlack) * hi.all - mass_from, of_sub);
+            if (largest(lost ? 1 : 0, 0).x != 0 || !hi2.reached) return false;
+            if (threadIdx.x < kSampleWarps) sh.mass[threadIdx.x] = 0;
+            __syncthreads();
+            const uint32_t size = E * 32 * a.rows_warp;
+            uint64_t key[kList / kSampleThreads];
+#pragma unroll
+            for (int e = 0; e < kList / kSampleThreads; ++e) {
+                const int at = e * kSampleThreads + threadIdx.x;
+                key[e] = at < n ? sh.list[at] : 0;
+                if (at >= n) continue;
+                const float x = value_of(key[e]);
+                const int b = sub_bin(x, top, scale);
+                if (b >= lo2.bin && b <= hi2.bin) continue;
+                if (b < lo2.bin)                 // above them after all
+                    atomicAdd(reinterpret_cast<unsigned long long *>(sh.mass) +
+                                  (static_cast<uint32_t>(key[e]) / size - rank * kSampleWarps),
+                              static_cast<unsigned long long>(w_of(x) >> kDrop));
+                key[e] = 0;
+            }
+            __syncthreads();
+            if (threadIdx.x == 0) sh.listed = 0;
+            if (lane == 0) listed_above = sh.mass[warp];
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kList / kSampleThreads; ++e)
+                if (key[e] != 0) sh.list[atomicAdd(&sh.listed, 1u)] = key[e];
+        }
+        const Sums s = gather<true>(above, 0, &all, listed_above);
         const int n = join_lists();
+        if (n <= kList && n > 0 && all_listed) {
+            if (rank == 0) end_listed<T>(a, sh, handed(), n, 0, p, all, -INFINITY, u);
+            return true;
+        }
         if (n > kList || n == 0) return false;
         const uint64_t need = part_of(all, p, true);
         if (rank == 0) {
@@ -1222,7 +1337,6 @@ struct Sampler {
         const float low = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.f;
         const float u = __ldg(a.u + row);
         if (threadIdx.x == 0) sh.listed = sh.todo = 0;
-        if (threadIdx.x < 32) sh.table[threadIdx.x] = kExpTable[threadIdx.x];
         __syncwarp();
         if (ctas > 1) cluster_arrive_all();                  // (the others' shared memory: only once they run)
         uint32_t hi = 0, lo = 0;
@@ -1271,6 +1385,8 @@ struct Sampler {
         }
         t = fminf(fmaxf(t, 7.8886091e-31f), 1.2676506e30f);  // 2^-100, 2^100
         ready();
+        lay_table();
+        __syncthreads();
         const bool some = k > 0 && k < a.V, part = p < 1.f;
         if (!some && !part && !(low > 0.f)) {
             const Sums s = sums_all();
@@ -1351,7 +1467,7 @@ struct Sampler {
             whole = s.above;
             if (by_k.v > -INFINITY) whole += times(w_of(by_k.v), min(by_k.first, s.ties));
             if (!flat)
-                v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 8796093022208.f) / weight.most()),
+                v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 8796093022208.f) * exp2f(static_cast<float>(weight.shift() * 1.4426950408889634))),
                                           by_k.v).v);
         }
         Sums s = sums(v);
