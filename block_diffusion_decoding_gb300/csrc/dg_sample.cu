@@ -1415,7 +1415,7 @@ struct Sampler {
                     if (x > -INFINITY) atomicAdd(hist + max(0, min(static_cast<int>((m - x) * scale), kBins - 1)), 1u);
                 };
                 // (below half of the maxima there are many more tokens than maxima)
-                if (2 * k <= ctas * kSampleThreads * min(kGroups, a.rows_warp)) {
+                if (2 * k <= ctas * kSampleThreads * (a.rows_warp / rows_group())) {
 #pragma unroll 1
                     for (int g = 0; g < kGroups; ++g) count(sh.group[g][threadIdx.x]);
                 } else {
