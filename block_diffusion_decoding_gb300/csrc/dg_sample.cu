@@ -250,13 +250,11 @@ struct Weights {
     }
     // What the table holds at place p.
     DG_DEVICE uint32_t turned(int p) const { return kExpTable[(p - ref) & 31]; }
-    DG_DEVICE double c() const { return static_cast<double>(ch) + static_cast<double>(cl); }
-    // ln of what a weight of 2^53 stands for beside exp((x - max) / T) = 1
-    DG_DEVICE double shift() const
+    // log2 of what a weight of 2^53 stands for beside exp((x - max) / T) = 1, at most
+    // 1/64 (what the multiply-add cuts off is below 2^-31)
+    DG_DEVICE float shift() const
     {
-        if (wide) return 0.;
-        const double at = static_cast<double>(__int_as_float(ref) - 393216.f);
-        return (at - static_cast<double>(m) * c()) * 0.6931471805599453;
+        return wide ? 0.f : -fmaf(m, cl, fmaf(m, ch, 393216.f - __int_as_float(ref)));
     }
     DG_DEVICE uint64_t operator()(float x, const uint32_t *table) const
     {
@@ -297,13 +295,48 @@ struct Weights {
     DG_DEVICE uint64_t in_double(float x) const { return weight_in_double(x, m, ch, cl); }
 };
 
-// A drawn token's logprob: (x - m) / T less ln of `all`, of which 2^kSumBits stands for
-// e^shift of the largest weight.  (Once a row, by one thread.)
-__device__ __noinline__ float logprob_of(float x, float m, float ch, float cl, uint64_t all, double shift)
+// a + b and what its rounding cut off
+DG_DEVICE float2 two_sum(float a, float b)
 {
-    const double at = (static_cast<double>(x) - static_cast<double>(m)) *
-                      (static_cast<double>(ch) + static_cast<double>(cl));
-    return static_cast<float>(at * 0.6931471805599453 - (log(static_cast<double>(all)) - kSumBits * 0.6931471805599453 + shift));
+    const float s = a + b, part = s - a;
+    return make_float2(s, (a - (s - part)) + (b - part));
+}
+// n / d in two floats
+DG_DEVICE float2 two_div(float n_hi, float n_lo, float d_hi, float d_lo)
+{
+    const float q = n_hi / d_hi;
+    return make_float2(q, (fmaf(-q, d_lo, fmaf(-q, d_hi, n_hi)) + n_lo) / d_hi);
+}
+
+// A drawn token's logprob: (x - m) / t less ln of `all`, of which 2^kSumBits stands for
+// 2^shift of the largest weight.  One thread does this at the end of a row's way, so
+// its latency counts: sums of two floats, off by less than 2^-28 beside the result's
+// own rounding, in place of arithmetic in 64 bits (1.5 us of a row's 14).  With
+// all = 2^n g, g about 1, ln g = 2 (s + s^3 / 3 + ...), s = (g - 1) / (g + 1), |s| < 0.172.
+__device__ __noinline__ float logprob_of(float x, float m, float t, uint64_t all, float shift)
+{
+    constexpr float kLn2 = 0.693145752f, kLn2Low = 1.42860677e-6f;   // (the first: 16 bits)
+    int n = 63 - __clzll(static_cast<long long>(all));
+    const uint64_t top = all << (63 - n);                            // g 2^63
+    float g = static_cast<float>(static_cast<uint32_t>(top >> 40)) * 1.1920929e-7f;
+    float low = static_cast<float>(static_cast<uint32_t>(top >> 16) & 0xFFFFFFu) * 7.1054274e-15f;
+    if (g > 1.41421354f) {
+        g *= 0.5f;
+        low *= 0.5f;
+        ++n;
+    }
+    const float2 above = two_sum(g, 1.f);
+    const float2 s = two_div(g - 1.f, low, above.x, above.y + low);
+    const float q = s.x * s.x;
+    const float series = fmaf(q, fmaf(q, fmaf(q, fmaf(q, 0.181818182f, 0.222222222f), 0.285714286f), 0.4f), 0.666666667f);
+    // (halves: x - m may be past the largest number)
+    const float2 d = two_sum(0.5f * x, -0.5f * m);
+    const float2 at = two_div(d.x, d.y, t, 0.f);
+    if (!(at.x > -1e37f)) return -INFINITY;
+    const float e = static_cast<float>(n - kSumBits);
+    const float2 one = two_sum(2.f * at.x, -e * kLn2);
+    const float2 two = two_sum(one.x, -2.f * s.x);
+    return two.x + (two.y + one.y + 2.f * at.y - 2.f * s.y - fmaf(e, kLn2Low, fmaf(shift, 0.69314718f, series * q * s.x)));
 }
 
 // What a row's CTA hands on to the out-of-line end of its way to a token.
@@ -474,10 +507,20 @@ struct Sampler {
         constexpr int N = 4;
         uint16_t *todo = reinterpret_cast<uint16_t *>(sh.mass);
         static_assert(sizeof(sh.mass) >= kGroups * kSampleThreads * sizeof(uint16_t), "a place for every group");
-#pragma unroll 1
-        for (int g = 0; g < kGroups; ++g)
-            if (wanted(sh.group[g][threadIdx.x]))
-                todo[atomicAdd(&sh.todo, 1u)] = static_cast<uint16_t>(g * kSampleThreads + threadIdx.x);
+        uint32_t want = 0;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) want |= wanted(sh.group[g][threadIdx.x]) ? 1u << g : 0u;
+        uint32_t slot = __popc(want);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(kAll, slot, o);
+            if (lane >= o) slot += x;
+        }
+        uint32_t at0 = 0;
+        if (lane == 31 && slot > 0) at0 = atomicAdd(&sh.todo, slot);
+        slot += __shfl_sync(kAll, at0, 31) - __popc(want);
+        for (; want != 0; want &= want - 1)
+            todo[slot++] = static_cast<uint16_t>((__ffs(want) - 1) * kSampleThreads + threadIdx.x);
         __syncthreads();
         const int rg = rows_group(), n = static_cast<int>(sh.todo) * rg;
 #pragma unroll 1
@@ -935,8 +978,8 @@ struct Sampler {
     {
         a.token[row] = token;
         if (a.logprob == nullptr) return;
-        if (flat) a.logprob[row] = logprob_of(0.f, 0.f, 0.f, 0.f, all, 0.);
-        else a.logprob[row] = logprob_of(value, m, weight.ch, weight.cl, all, weight.shift());
+        if (flat) a.logprob[row] = logprob_of(0.f, 0.f, 1.f, all, 0.f);
+        else a.logprob[row] = logprob_of(value, m, t, all, weight.shift());
     }
 
     // ------------------------------------------------------------ few tokens
@@ -1030,6 +1073,10 @@ struct Sampler {
     // `least`.
     DG_DEVICE void draw_listed(int n, int k, float p, uint64_t all, float least, float u)
     {
+        if (n <= kSampleThreads) {
+            draw_few(n, k, p, all, least, u);
+            return;
+        }
         sort_values(n);
         const int most = k > 0 ? min(k, n) : n;
         // the weights in that order and their sums; a thread has `per` neighbours
@@ -1078,6 +1125,49 @@ struct Sampler {
             }
             at += w;
         }
+    }
+
+    // The same for at most a token a thread: its place in either order is the number of
+    // those before it, counted out.
+    DG_DEVICE void draw_few(int n, int k, float p, uint64_t all, float least, float u)
+    {
+        const int e = threadIdx.x;
+        uint64_t key = 0;
+        if (e < n) {
+            key = sh.list[e];
+            int before = 0;
+#pragma unroll 8
+            for (int o = 0; o < n; ++o) before += sh.list[o] < key ? 1 : 0;
+            sh.moved[before] = key;
+            sh.mass[before] = w_of(value_of(key)) >> kDrop;
+        }
+        __syncthreads();
+        const int most = k > 0 ? min(k, n) : n;
+        uint64_t w = 0, listed;
+        if (e < n) key = sh.moved[e];
+        if (e < most) w = sh.mass[e];
+        const uint64_t before = scan(w, &listed) - w;
+        const uint64_t need = p < 1.f ? part_of(k > 0 ? listed : all, p, true) : ~0ull;
+        const bool keeps = e < most && (e == 0 || (before < need && value_of(key) >= least));
+        uint32_t *index = reinterpret_cast<uint32_t *>(sh.list);
+        const uint32_t at = keeps ? static_cast<uint32_t>(key) : ~0u;
+        index[e] = at;                           // (nobody looks at the list any more)
+        const int kept = __syncthreads_count(keeps);
+        if (e == kept - 1) sh.all = before + w;
+        __syncthreads();
+        if (!keeps) return;
+        const uint64_t part = sh.all;
+        const uint64_t rem = min(u < 1.f ? part_of(part, u, false) : part - 1, part - 1);
+        uint64_t sum = 0;
+        bool first = true;
+#pragma unroll 8
+        for (int o = 0; o < kept; ++o) {
+            const bool lower = index[o] < at;
+            sum += lower ? sh.mass[o] : 0;
+            first &= !lower;
+        }
+        // (rem == 0: the first one, however light)
+        if (rem == 0 ? first : sum <= rem && rem < sum + w) say(static_cast<int>(at) - skew, value_of(key), part);
     }
 
     // Lists a thread's hits among 16 bytes' tokens.
@@ -1337,6 +1427,7 @@ struct Sampler {
         const float low = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.f;
         const float u = __ldg(a.u + row);
         if (threadIdx.x == 0) sh.listed = sh.todo = 0;
+        for (int k = threadIdx.x; k < kBins; k += kSampleThreads) sh.hist[0][k] = 0;
         __syncwarp();
         if (ctas > 1) cluster_arrive_all();                  // (the others' shared memory: only once they run)
         uint32_t hi = 0, lo = 0;
@@ -1386,9 +1477,9 @@ struct Sampler {
         t = fminf(fmaxf(t, 7.8886091e-31f), 1.2676506e30f);  // 2^-100, 2^100
         ready();
         lay_table();
-        __syncthreads();
         const bool some = k > 0 && k < a.V, part = p < 1.f;
         if (!some && !part && !(low > 0.f)) {
+            __syncthreads();
             const Sums s = sums_all();
             end_draw<T>(a, sh, handed(), -INFINITY, 0, s.above, s.ties, s.buf, u);
             return true;
@@ -1410,7 +1501,7 @@ struct Sampler {
             float scale = 0.f, limit = INFINITY;
             if (list_k) {
                 scale = static_cast<float>(kBins) / (m - of_order(~ends.y));
-                uint32_t *hist = clear();
+                uint32_t *hist = sh.hist[0];
                 auto count = [&](float x) {
                     if (x > -INFINITY) atomicAdd(hist + max(0, min(static_cast<int>((m - x) * scale), kBins - 1)), 1u);
                 };
@@ -1444,6 +1535,7 @@ struct Sampler {
                 return true;
             }
         }
+        __syncthreads();
         if (!flat && part && !some && !(low > 0.f)) {
             end_nucleus<T>(a, sh, handed(), p, u);
             return true;
@@ -1467,7 +1559,7 @@ struct Sampler {
             whole = s.above;
             if (by_k.v > -INFINITY) whole += times(w_of(by_k.v), min(by_k.first, s.ties));
             if (!flat)
-                v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 8796093022208.f) * exp2f(static_cast<float>(weight.shift() * 1.4426950408889634))),
+                v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 8796093022208.f) * exp2f(weight.shift())),
                                           by_k.v).v);
         }
         Sums s = sums(v);
