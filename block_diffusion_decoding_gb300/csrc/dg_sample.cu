@@ -84,9 +84,9 @@ struct alignas(16) SampleShared {
     uint32_t table[32];
     float scan_f[kSampleWarps];
     uint32_t scan_u[kSampleWarps];
-    Found found;
+    Found found[2];
     Cut cut;
-    int claim, last;
+    int claim[2], last;
     int seg, tie_prefix;
     uint64_t rem, all;
     uint32_t listed, base, todo;
@@ -575,14 +575,16 @@ struct Sampler {
         return hist;
     }
     // The bin in which the tokens reach `target` in number, or with `Mass` (counts
-    // weighed by of_bin) target_mass in weight, or `part` of all of it; where rounded sums stay short of that,
-    // the last one that is not empty.
-    template <bool Mass, class F>
-    DG_DEVICE Found find(uint32_t target, float target_mass, F of_bin, float part = 0.f)
+    // weighed by of_bin) each of N weights, part[i] of `of` (of < 0: of all of theirs)
+    // less `less`; where rounded sums stay short of that, the last one that is not empty.
+    // Into sh.found[i].
+    template <bool Mass, int N, class F>
+    DG_DEVICE void find_each(uint32_t target, const float (&part)[N], float of, float less, F of_bin)
     {
         const int buf = hist_turn++ & 1;
         if (threadIdx.x == 0) {
-            sh.claim = kSampleThreads;
+#pragma unroll
+            for (int i = 0; i < N; ++i) sh.claim[i] = kSampleThreads;
             sh.last = -1;
         }
         sync();
@@ -591,14 +593,27 @@ struct Sampler {
         float f[kBinsThread];
 #pragma unroll
         for (int e = 0; e < kBinsThread; ++e) n[e] = 0;
-        for (int k = 0; k < ctas; ++k) {
-            uint4 v;
-            if (ctas == 1) v = *reinterpret_cast<const uint4 *>(&sh.hist[buf][b]);
-            else v = ld_cluster4(mapa_shared(smem_u32(&sh.hist[buf][b]), k));
-            n[0] += v.x;
-            n[1] += v.y;
-            n[2] += v.z;
-            n[3] += v.w;
+        if (ctas == 1) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(&sh.hist[buf][b]);
+            n[0] = v.x, n[1] = v.y, n[2] = v.z, n[3] = v.w;
+        } else {
+            constexpr int Ahead = 4;
+            const uint32_t at = smem_u32(&sh.hist[buf][b]);
+            for (int k0 = 0; k0 < ctas; k0 += Ahead) {
+                uint4 v[Ahead];
+#pragma unroll
+                for (int k = 0; k < Ahead; ++k) {
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (k0 + k < ctas) v[k] = ld_cluster4(mapa_shared(at, k0 + k));
+                }
+#pragma unroll
+                for (int k = 0; k < Ahead; ++k) {
+                    n[0] += v[k].x;
+                    n[1] += v[k].y;
+                    n[2] += v[k].z;
+                    n[3] += v[k].w;
+                }
+            }
         }
         uint32_t n_sum = 0;
         float f_sum = 0.f;
@@ -633,14 +648,19 @@ struct Sampler {
             }
             f_all += sh.scan_f[w];
         }
-        if (part > 0.f) target_mass = part * f_all;
-        if (n_sum > 0) {
-            if (Mass ? f_end >= target_mass : n_end >= target) atomicMin(&sh.claim, static_cast<int>(threadIdx.x));
-            if (Mass) atomicMax(&sh.last, static_cast<int>(threadIdx.x));
+        float aim[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            aim[i] = part[i] * (of < 0.f ? f_all : of) - less;
+            if (n_sum > 0 && (Mass ? f_end >= aim[i] : n_end >= target))
+                atomicMin(&sh.claim[i], static_cast<int>(threadIdx.x));
         }
+        if (Mass && n_sum > 0) atomicMax(&sh.last, static_cast<int>(threadIdx.x));
         __syncthreads();
-        const bool reached = sh.claim < kSampleThreads;
-        if (static_cast<int>(threadIdx.x) == (reached ? sh.claim : max(sh.last, 0))) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool reached = sh.claim[i] < kSampleThreads;
+            if (static_cast<int>(threadIdx.x) != (reached ? sh.claim[i] : max(sh.last, 0))) continue;
             Found got{-1, 0, 0, 0.f, f_all, reached};
             uint32_t n_before = n_end - n_sum;
             float f_before = f_end - f_sum;
@@ -649,16 +669,22 @@ struct Sampler {
             for (int e = 0; e < kBinsThread; ++e) {
                 if (n[e] > 0 && !stop) {
                     got = Found{b + e, n[e], n_before, f_before, f_all, reached};
-                    stop = reached && (Mass ? f_before + f[e] >= target_mass : n_before + n[e] >= target);
+                    stop = reached && (Mass ? f_before + f[e] >= aim[i] : n_before + n[e] >= target);
                 }
                 n_before += n[e];
                 f_before += f[e];
             }
             if (!reached && !Mass) got.bin = -1;
-            sh.found = got;
+            sh.found[i] = got;
         }
         __syncthreads();
-        return sh.found;
+    }
+    template <bool Mass, class F>
+    DG_DEVICE Found find(uint32_t target, float target_mass, F of_bin)
+    {
+        const float part[1] = {target_mass};
+        find_each<Mass>(target, part, 1.f, 0.f, of_bin);
+        return sh.found[0];
     }
 
     // Where the tokens reach k in number or, with `Mass`, `target` in weight, of those
@@ -1240,7 +1266,9 @@ struct Sampler {
         uint32_t *hist = sh.hist[hist_turn & 1];
         for (int k = threadIdx.x; k < kBins; k += kSampleThreads) hist[k] = k == static_cast<int>(threadIdx.x) ? mine : 0;
         auto of_bin = [](int b) -> float { return exp2f(-b / 8.f) * (1.f / kMassOne); };
-        const Found hi = find<true>(0, 0.f, of_bin, p * (1.f + kSlack));
+        const float parts[2] = {p * (1.f + kSlack), p * (1.f - kSlack)};
+        find_each<true>(0, parts, -1.f, 0.f, of_bin);
+        const Found hi = sh.found[0];
         if (!hi.reached) return false;
         // (a token's rounded weight is at least 0.92 of kMassOne, at most 1.01)
         const bool all_listed = hi.before + hi.count < static_cast<uint32_t>(kMassOne * 0.85f * kList);
@@ -1253,8 +1281,7 @@ struct Sampler {
         };
         bool split = false;                      // the bins hold more than the CTAs can list
         if (!all_listed) {
-            --hist_turn;                         // (once more in the same histogram)
-            const Found lo = find<true>(0, 0.f, of_bin, p * (1.f - kSlack));
+            const Found lo = sh.found[1];
             from = lo.bin;
             mass_from = lo.mass;
             top = __int_as_float(ref - 4 * from + 1) - 393216.f;
@@ -1271,9 +1298,8 @@ struct Sampler {
                         if (b >= from && b <= hi.bin) atomicAdd(hist + sub_bin(x[e], top, scale), 1u);
                     }
                 });
-                const Found hi2 = find<true>(0, p * (1.f + kSlack) * hi.all - mass_from, of_sub);
-                --hist_turn;
-                const Found lo2 = find<true>(0, p * (1.f - kSlack) * hi.all - mass_from, of_sub);
+                find_each<true>(0, parts, hi.all, mass_from, of_sub);
+                const Found hi2 = sh.found[0], lo2 = sh.found[1];
                 if (!hi2.reached || hi2.before + hi2.count - lo2.before > kList) return false;
                 first_sub = lo2.bin;
                 last_sub = hi2.bin;
@@ -1309,9 +1335,8 @@ struct Sampler {
             const bool lost = sh.listed > kList;
             for (int e = threadIdx.x; e < n; e += kSampleThreads)
                 atomicAdd(hist + sub_bin(value_of(sh.list[e]), top, scale), 1u);
-            const Found hi2 = find<true>(0, p * (1.f + kSlack) * hi.all - mass_from, of_sub);
-            --hist_turn;
-            const Found lo2 = find<true>(0, p * (1.f - kSlack) * hi.all - mass_from, of_sub);
+            find_each<true>(0, parts, hi.all, mass_from, of_sub);
+            const Found hi2 = sh.found[0], lo2 = sh.found[1];
             if (largest(lost ? 1 : 0, 0).x != 0 || !hi2.reached) return false;
             if (threadIdx.x < kSampleWarps) sh.mass[threadIdx.x] = 0;
             __syncthreads();
