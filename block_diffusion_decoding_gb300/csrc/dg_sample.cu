@@ -37,7 +37,8 @@ namespace {
 constexpr int kBins = 1024;
 constexpr int kBinsThread = kBins / kSampleThreads;
 constexpr float kBinsLog2 = 16.f;        // of the search by counting: bins to a factor of 2 in weight
-constexpr float kMassOne = 8192.f;       // a weight at its bin's upper end, in sums of rounded ones
+constexpr float kMassOne = 8192.f;       // a weight where its bin stands for it, in sums of rounded ones
+constexpr float kEighths = 1572864.f;    // 1.5 x 2^20: a unit in the last place is 1/8
 constexpr int kMassBins = 256;           // of top-p's: 8 to a factor of 2
 constexpr int kGroups = 8;               // groups of a thread's tokens
 constexpr int kList = 1536;              // tokens that are sorted at most
@@ -260,18 +261,21 @@ struct Weights {
     {
         return wide ? in_double(x) : fast(x, table);
     }
-    // P as an integer: 32 to a factor of 2, `ref` for the largest.
-    DG_DEVICE int unit(float x) const { return __float_as_int(fmaf(fmaxf(x, floor), ch, 393216.f)); }
-    DG_DEVICE uint64_t fast(float x, const uint32_t *table) const
+    // c x to the nearest 1/8, in the last places of a number near 2^20.
+    DG_DEVICE float eighths(float x) const { return fmaf(fmaxf(x, floor), ch, kEighths); }
+    // Its weight beside that of its nearest eighth, in units of 1 / kMassOne: |r| <= 1/16,
+    // the series to r^2 with r^3's nearest line, off by 4e-6 and the rounding.
+    DG_DEVICE uint32_t beside(float x, float at) const
     {
-        int p;
-        return fast(x, table, p);
+        const float r = fmaf(fmaxf(x, floor), ch, kEighths - at);
+        const float w = fmaf(r, fmaf(r, 0.24022651f * kMassOne, 0.69330979f * kMassOne), 12582912.f + kMassOne);
+        return static_cast<uint32_t>(__float_as_int(w) - __float_as_int(12582912.f));   // (1.5 x 2^23: to a whole number)
     }
-    DG_DEVICE uint64_t fast(float x, const uint32_t *table, int &p) const
+    DG_DEVICE uint64_t fast(float x, const uint32_t *table) const
     {
         const float y = fmaxf(x, floor);
         const float P = fmaf(y, ch, 393216.f);
-        p = __float_as_int(P);
+        const int p = __float_as_int(P);
         float r = fmaf(y, ch, 393216.f - P);
         r = fmaf(y, cl, r);
         float s = fmaf(r, 0.055504109f, 0.24022651f);    // ln2^3 / 6, ln2^2 / 2
@@ -283,14 +287,6 @@ struct Weights {
         uint32_t w;                                      // T (1 + y)
         asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(w) : "r"(T), "r"(yi));
         return static_cast<uint64_t>(w) << (kLaneBits - 30) >> (ref + 31 - p >> 5);   // (0 .. 61)
-    }
-    // Its weight beside that of unit q, which is not far above, in units of 1 / kMassOne.
-    DG_DEVICE uint32_t beside(float x, int q) const
-    {
-        const float r = fmaf(fmaxf(x, floor), ch, 393216.f - __int_as_float(q));
-        const float w = fmaf(r, fmaf(r, fmaf(r, 0.055504109f, 0.24022651f), 0.69314718f), 1.f);
-        return static_cast<uint32_t>(__float_as_int(fmaf(w, kMassOne, 12582912.f)) -
-                                     __float_as_int(12582912.f));    // (1.5 x 2^23: to a whole number)
     }
     DG_DEVICE uint64_t in_double(float x) const { return weight_in_double(x, m, ch, cl); }
 };
@@ -1234,8 +1230,8 @@ struct Sampler {
     {
         return min(max(static_cast<int>(fmaf(-x, weight.ch, top) * scale), 0), kBins - 1);
     }
-    // The part p of the row's weight.  The weights, rounded, are summed in bins, 4 of the
-    // weights' units each, a place a lane so that no two meet; then the whole weight
+    // The part p of the row's weight.  The weights, rounded, are summed in bins, by their
+    // logarithm's nearest 1/8, a place a lane so that no two meet; then the whole weight
     // exactly, and of the tokens above the bins that the cut may lie in, which are listed
     // and sorted by the first CTA.  False: the row has to go the long way.
     DG_DEVICE bool draw_nucleus(float p, float u)
@@ -1248,14 +1244,15 @@ struct Sampler {
         static_assert(kMassBins == kSampleThreads, "a thread adds a bin up");
         for (int k = threadIdx.x; k < kMassBins * 32; k += kSampleThreads) lanes[k] = 0;
         __syncthreads();
-        const int ref = weight.ref;
+        const float ref = weight.eighths(m);
         rows_ahead<kAhead>([&](const uint4 &v, int) {
             float x[E];
             Vec<T>::unpack(v, x);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int b = (ref - weight.unit(x[e])) >> 2;
-                if (b < kMassBins) atomicAdd(lanes + b * 32 + lane, weight.beside(x[e], ref - 4 * b));
+                const float at = weight.eighths(x[e]);
+                const int b = __float_as_int(ref) - __float_as_int(at);
+                if (b < kMassBins) atomicAdd(lanes + b * 32 + lane, weight.beside(x[e], at));
             }
         });
         __syncthreads();
@@ -1270,21 +1267,23 @@ struct Sampler {
         find_each<true>(0, parts, -1.f, 0.f, of_bin);
         const Found hi = sh.found[0];
         if (!hi.reached) return false;
-        // (a token's rounded weight is at least 0.92 of kMassOne, at most 1.01)
+        // (a token's rounded weight is at least 0.95 of kMassOne, at most 1.05)
         const bool all_listed = hi.before + hi.count < static_cast<uint32_t>(kMassOne * 0.85f * kList);
         int from = 0, first_sub = 0, last_sub = kBins - 1;
         float mass_from = 0.f;                   // (rounded, above bin `from`)
         float top = 0.f, scale = 0.f;            // bins of the bins: their upper end, how many to a factor of 2
         auto of_sub = [&](int b) -> float {
-            const float end = static_cast<float>(ref - __float_as_int(top + 393216.f)) / 32.f;
-            return exp2f(-(end + (static_cast<float>(b) + 0.5f) / scale));
+            return exp2f(top - (ref - kEighths) - (static_cast<float>(b) + 0.5f) / scale);
         };
         bool split = false;                      // the bins hold more than the CTAs can list
+        const float last_at = ref - static_cast<float>(hi.bin) / 8.f;
+        float first_at = INFINITY;               // (of the bins `from` and hi.bin)
         if (!all_listed) {
             const Found lo = sh.found[1];
             from = lo.bin;
+            first_at = ref - static_cast<float>(from) / 8.f;
             mass_from = lo.mass;
-            top = __int_as_float(ref - 4 * from + 1) - 393216.f;
+            top = ref - kEighths - static_cast<float>(from) / 8.f + 0.0625f;
             scale = kBins * 8.f / static_cast<float>(hi.bin - from + 2);
             split = hi.before + hi.count - lo.before > static_cast<uint32_t>(kMassOne * 0.65f * kList) * ctas;
             if (split) {
@@ -1294,8 +1293,8 @@ struct Sampler {
                     Vec<T>::unpack(v, x);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        const int b = (ref - weight.unit(x[e])) >> 2;
-                        if (b >= from && b <= hi.bin) atomicAdd(hist + sub_bin(x[e], top, scale), 1u);
+                        const float at = weight.eighths(x[e]);
+                        if (at <= first_at && at >= last_at) atomicAdd(hist + sub_bin(x[e], top, scale), 1u);
                     }
                 });
                 find_each<true>(0, parts, hi.all, mass_from, of_sub);
@@ -1312,12 +1311,11 @@ struct Sampler {
             uint32_t hits = 0;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                int unit;
-                const uint64_t w = weight.fast(x[e], sh.table, unit);
+                const uint64_t w = weight.fast(x[e], sh.table);
                 all += w;
-                const int b = (ref - unit) >> 2;
-                if (b > hi.bin) continue;
-                int side = b < from ? -1 : 0;
+                const float at = weight.eighths(x[e]);
+                if (at < last_at) continue;
+                int side = at > first_at ? -1 : 0;
                 if (split && side == 0) {
                     const int sub = sub_bin(x[e], top, scale);
                     side = sub < first_sub ? -1 : sub > last_sub ? 1 : 0;
