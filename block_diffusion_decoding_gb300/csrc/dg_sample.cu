@@ -1249,10 +1249,11 @@ struct Sampler {
             float x[E];
             Vec<T>::unpack(v, x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
+            for (int e = 0; e < E; ++e) {        // (no branch: the tokens' latencies overlap)
                 const float at = weight.eighths(x[e]);
                 const int b = __float_as_int(ref) - __float_as_int(at);
-                if (b < kMassBins) atomicAdd(lanes + b * 32 + lane, weight.beside(x[e], at));
+                const uint32_t w = weight.beside(x[e], at);
+                atomicAdd(lanes + min(b, kMassBins - 1) * 32 + lane, b < kMassBins ? w : 0);
             }
         });
         __syncthreads();
@@ -1314,14 +1315,18 @@ struct Sampler {
                 const uint64_t w = weight.fast(x[e], sh.table);
                 all += w;
                 const float at = weight.eighths(x[e]);
-                if (at < last_at) continue;
-                int side = at > first_at ? -1 : 0;
-                if (split && side == 0) {
+                above += at > first_at ? w : 0;
+                hits |= at <= first_at && at >= last_at ? 1u << e : 0u;
+            }
+            if (split && hits != 0) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (!(hits >> e & 1u)) continue;
                     const int sub = sub_bin(x[e], top, scale);
-                    side = sub < first_sub ? -1 : sub > last_sub ? 1 : 0;
+                    if (sub >= first_sub && sub <= last_sub) continue;
+                    hits &= ~(1u << e);
+                    if (sub < first_sub) above += weight.fast(x[e], sh.table);
                 }
-                if (side < 0) above += w;
-                hits |= side == 0 ? 1u << e : 0u;
             }
             list(x, hits, warp, r, lane);
         });
