@@ -573,8 +573,8 @@ struct Sampler {
     // The bin in which the tokens reach `target` in number, or with `Mass` (counts
     // weighed by of_bin) each of N weights, part[i] of `of` (of < 0: of all of theirs)
     // less `less`; where rounded sums stay short of that, the last one that is not empty.
-    // Into sh.found[i].
-    template <bool Mass, int N, class F>
+    // Into sh.found[i].  Bins: of those that are in use.
+    template <bool Mass, int Bins, int N, class F>
     DG_DEVICE void find_each(uint32_t target, const float (&part)[N], float of, float less, F of_bin)
     {
         const int buf = hist_turn++ & 1;
@@ -589,11 +589,12 @@ struct Sampler {
         float f[kBinsThread];
 #pragma unroll
         for (int e = 0; e < kBinsThread; ++e) n[e] = 0;
-        if (ctas == 1) {
+        if (b >= Bins) {
+        } else if (ctas == 1) {
             const uint4 v = *reinterpret_cast<const uint4 *>(&sh.hist[buf][b]);
             n[0] = v.x, n[1] = v.y, n[2] = v.z, n[3] = v.w;
         } else {
-            constexpr int Ahead = 4;
+            constexpr int Ahead = 8;
             const uint32_t at = smem_u32(&sh.hist[buf][b]);
             for (int k0 = 0; k0 < ctas; k0 += Ahead) {
                 uint4 v[Ahead];
@@ -679,7 +680,7 @@ struct Sampler {
     DG_DEVICE Found find(uint32_t target, float target_mass, F of_bin)
     {
         const float part[1] = {target_mass};
-        find_each<Mass>(target, part, 1.f, 0.f, of_bin);
+        find_each<Mass, kBins>(target, part, 1.f, 0.f, of_bin);
         return sh.found[0];
     }
 
@@ -1262,10 +1263,10 @@ struct Sampler {
         for (int l = 0; l < 32; ++l) mine += lanes[threadIdx.x * 32 + ((l + lane) & 31)];   // (spread over the banks)
         __syncthreads();
         uint32_t *hist = sh.hist[hist_turn & 1];
-        for (int k = threadIdx.x; k < kBins; k += kSampleThreads) hist[k] = k == static_cast<int>(threadIdx.x) ? mine : 0;
+        hist[threadIdx.x] = mine;
         auto of_bin = [](int b) -> float { return exp2f(-b / 8.f) * (1.f / kMassOne); };
         const float parts[2] = {p * (1.f + kSlack), p * (1.f - kSlack)};
-        find_each<true>(0, parts, -1.f, 0.f, of_bin);
+        find_each<true, kMassBins>(0, parts, -1.f, 0.f, of_bin);
         const Found hi = sh.found[0];
         if (!hi.reached) return false;
         // (a token's rounded weight is at least 0.95 of kMassOne, at most 1.05)
@@ -1298,7 +1299,7 @@ struct Sampler {
                         if (at <= first_at && at >= last_at) atomicAdd(hist + sub_bin(x[e], top, scale), 1u);
                     }
                 });
-                find_each<true>(0, parts, hi.all, mass_from, of_sub);
+                find_each<true, kBins>(0, parts, hi.all, mass_from, of_sub);
                 const Found hi2 = sh.found[0], lo2 = sh.found[1];
                 if (!hi2.reached || hi2.before + hi2.count - lo2.before > kList) return false;
                 first_sub = lo2.bin;
@@ -1338,7 +1339,7 @@ struct Sampler {
             const bool lost = sh.listed > kList;
             for (int e = threadIdx.x; e < n; e += kSampleThreads)
                 atomicAdd(hist + sub_bin(value_of(sh.list[e]), top, scale), 1u);
-            find_each<true>(0, parts, hi.all, mass_from, of_sub);
+            find_each<true, kBins>(0, parts, hi.all, mass_from, of_sub);
             const Found hi2 = sh.found[0], lo2 = sh.found[1];
             if (largest(lost ? 1 : 0, 0).x != 0 || !hi2.reached) return false;
             if (threadIdx.x < kSampleWarps) sh.mass[threadIdx.x] = 0;
