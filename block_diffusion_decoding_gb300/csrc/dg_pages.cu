@@ -3,8 +3,11 @@
 //
 // free_pages [0, n_free) are the pages of nobody, a stack: handed out from its end.
 // refs counts the sequences that hold a page; a sequence holds the pages of the first
-// places of its row of the table, the places behind them are negative.  Which page goes where depends on the
-// arguments alone: the decisions are made by one CTA in the order of the sequences.
+// places of its row of the table, the places behind them are negative.  Which page goes
+// where depends on the arguments alone: the decisions are made by one CTA in the order of
+// the sequences, by prefix sums of what each one needs, and only counts that no order
+// changes are added by atomics.  All of it but the copies is bound by latency: a few reads
+// that depend on one another, 2 to 4 us, beside which the host's 5 for a launch counts.
 #include "dg_serve_kernels.h"
 
 namespace dg {
@@ -57,7 +60,8 @@ constexpr int32_t kPageFreed = -(1 << 30);   // refs of a page that a release ha
 
 }  // namespace
 
-// Pages for the tokens that the next append brings, a sequence a thread.
+// Pages for the tokens that the next append brings, a sequence a thread; then a thread a
+// page handed out, which looks its sequence up among the sums.
 __global__ void __launch_bounds__(kPoolThreads) paged_reserve_kernel(PagePoolArgs a)
 {
     __shared__ int sums[32];
@@ -168,7 +172,10 @@ __global__ void __launch_bounds__(kPoolThreads) paged_fork_kernel(PagePoolArgs a
 
 // The forks' tables, the counts of the pages they share, and the copies of their
 // last, unfinished pages in every layer: a block a fork's table, or kForkBytes of a
-// page.
+// page, 128 bytes of it on their way in each thread.  Bound by memory: 128 forks of 8
+// prompts, 16 layers of 8 heads of 128, 0.55 GB read and written, 55 us by itself (10
+// TB/s: what was read, and part of what was written, stays in L2) and 72 with the
+// decisions and the release that follows them.
 __global__ void __launch_bounds__(kForkThreads) paged_fork_copy_kernel(PagePoolArgs a)
 {
     constexpr int Batch = 8;
@@ -245,27 +252,44 @@ DG_DEVICE void give_back(const PagePoolArgs &a, int32_t *place)
 }
 
 // The pages that have been given back go onto the free ones, the lowest first.  One
-// CTA of kPoolThreads.
+// CTA of kPoolThreads; neighbouring threads look at neighbouring pages.
 DG_DEVICE void collect(const PagePoolArgs &a, int *sums)
 {
     constexpr int Per = 8;                       // pages a thread looks at in a turn
+    constexpr int Warps = kPoolThreads / 32;
+    __shared__ int s_before[Per * Warps];        // pages given back, by 32 of them
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int n_free = count_free(a);
     for (int p0 = 0; p0 < a.n_pages; p0 += Per * kPoolThreads) {
-        const int first = p0 + Per * static_cast<int>(threadIdx.x);
-        uint32_t freed = 0;
+        int32_t refs[Per];
 #pragma unroll
-        for (int e = 0; e < Per; ++e)
-            if (first + e < a.n_pages && __ldcg(a.refs + first + e) <= kPageFreed / 2) freed |= 1u << e;
+        for (int e = 0; e < Per; ++e) {
+            const int page = p0 + e * kPoolThreads + tid;
+            refs[e] = page < a.n_pages ? __ldcg(a.refs + page) : 0;
+        }
+        uint32_t freed[Per];
+#pragma unroll
+        for (int e = 0; e < Per; ++e) {
+            freed[e] = __ballot_sync(0xFFFFFFFFu, refs[e] <= kPageFreed / 2);
+            if (lane == 0) s_before[e * Warps + warp] = __popc(freed[e]);
+        }
+        __syncthreads();
+        const int count = tid < Per * Warps ? s_before[tid] : 0;
         int total;
-        int at = n_free + block_scan(__popc(freed), Per * kPoolThreads, sums, &total) - __popc(freed);
-        for (; freed != 0; freed &= freed - 1) {
-            const int page = first + __ffs(freed) - 1;
+        const int end = block_scan(count, Per * kPoolThreads, sums, &total);
+        if (tid < Per * Warps) s_before[tid] = end - count;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < Per; ++e) {
+            if (!(freed[e] >> lane & 1u)) continue;
+            const int page = p0 + e * kPoolThreads + tid;
+            const int at = n_free + s_before[e * Warps + warp] + __popc(freed[e] & ((1u << lane) - 1u));
             a.refs[page] = 0;
             if (at < a.n_pages) a.free_pages[at] = page;
             else report_error(a.ws, DG_ERR_DEVICE, 1134);
-            ++at;
         }
         n_free = min(n_free + total, a.n_pages);
+        __syncthreads();                         // (before the next turn's counts)
     }
     if (threadIdx.x == 0) *a.n_free = n_free;
 }
@@ -305,7 +329,8 @@ __global__ void __launch_bounds__(kPoolThreads) paged_release_small_kernel(PageP
     collect(a, sums);
 }
 
-// Takes a sequence's pages back, a block a sequence.
+// Takes a sequence's pages back, blockIdx.x its place in the list: up to 16 blocks share
+// a long table (2 sequences of 4096 places: 15.5 us with one each).
 __global__ void __launch_bounds__(kReleaseThreads) paged_release_kernel(PagePoolArgs a)
 {
     griddep_wait();
@@ -316,12 +341,13 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_release_kernel(PagePool
     for (int j = threadIdx.x; j < i; j += kReleaseThreads) twice |= a.dst[j] == seq;
     const bool bad = seq < 0 || seq >= a.B;
     if (__syncthreads_or(twice) || bad) {
-        if (threadIdx.x == 0) report_error(a.ws, DG_ERR_DEVICE, 1131);
+        if (blockIdx.y == 0 && threadIdx.x == 0) report_error(a.ws, DG_ERR_DEVICE, 1131);
         return;
     }
     int32_t *row = a.page_table + static_cast<int64_t>(seq) * a.max_pages;
-    for (int m = threadIdx.x; m < a.max_pages; m += kReleaseThreads) give_back(a, row + m);
-    if (threadIdx.x == 0) a.kv_len[seq] = 0;
+    for (int m = blockIdx.y * kReleaseThreads + threadIdx.x; m < a.max_pages; m += gridDim.y * kReleaseThreads)
+        give_back(a, row + m);
+    if (blockIdx.y == 0 && threadIdx.x == 0) a.kv_len[seq] = 0;
 }
 
 // The pages that the releases took back.

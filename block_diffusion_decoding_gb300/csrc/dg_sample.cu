@@ -21,6 +21,24 @@
 // A row is a cluster's; its CTAs exchange maxima, bins and sums through each other's
 // shared memory.
 //
+// What bounds it is not the one read of the logits that it cannot do without (the first
+// pass; the later ones find much of the row in L2), but instructions and, where rows are
+// few, barriers and latencies in a row.  On one GB300, us, beside that read at a copy's
+// rate:
+//                                    floor  greedy  none  top-k  top-k and top-p  top-p
+//   1 row of 16384 bf16                0.0     8     12     11         14           24
+//   1 of 262144 fp32                   0.2     8     16     17         17           41
+//   64 of 262144 fp32                  9.9    17     44     37         35          103
+//   1024 of 151643 bf16               45.8    80    225    124        115          532
+// (calls back to back; 6 of the small ones is the host's time).  An exact weight takes 24
+// instructions, of which 10 are its 64-bit shift and sum: the pass of 1024 rows that sums
+// them issues 57% of the time.  Eight groups a thread: with 4 the wanted groups' tokens
+// are twice as many to read again, with 16 the maxima take 16 KB.  Tried and no better:
+// the row a few pieces ahead through asynchronous copies to shared memory (none 225 ->
+// 233, top-p on one row 46 -> 45, a batch 94 -> 91), prefetches of a row into L2 (115 ->
+// 133), fewer CTAs an SM to spread clusters (no change where there is room, up to half as
+// fast where there is none), both policies for the clusters' places (no change).
+//
 // The exact weights exp((x - max) / T) are 64-bit fixed-point numbers with a relative
 // error of about 2^-29 (see Weights): a token's place among the sums of a whole
 // vocabulary would be lost in 32 bits, and sums of integers do not depend on their

@@ -75,7 +75,7 @@ constexpr int kPoolThreads = 1024;    // of the single-CTA kernels: sequences of
 constexpr int kForkThreads = 256;
 constexpr int kForkBytes = 32768;     // of a page that a block copies
 constexpr int kReleaseThreads = 256;
-constexpr int kReleaseSmall = 32768;  // places in tables and pages of a release by one CTA
+constexpr int kReleaseSmall = 4096;  // places in tables and pages of a release by one CTA
 __global__ void paged_reserve_kernel(PagePoolArgs a);
 __global__ void paged_fork_kernel(PagePoolArgs a);
 __global__ void paged_fork_copy_kernel(PagePoolArgs a);

@@ -20,7 +20,11 @@ DG_DEVICE Rows rows_of(const int32_t *q_start, int b, int T)
 }  // namespace
 
 // A node sees itself and its ancestors: a thread walks up its node's parents, whose
-// indices fall, and so meets the mask's words in falling order.
+// indices fall, and so meets the mask's words in falling order.  Bound by latency, the
+// search for the row's sequence and a read for each ancestor, which its neighbours' walks
+// have brought into L1: 2.6 us for a tree of 16 nodes, 5.5 for 256 of up to 64, within the
+// 6.2 us that a call from Python takes (in shared memory the parents would cost a barrier
+// and be read as often).
 __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(TreePlanArgs a)
 {
     griddep_wait();
@@ -77,8 +81,9 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(TreePlanArg
 // j, so in the order of j no place is written before it has been read, and a thread
 // keeps that order by itself.
 // Bound by latency: lengths and tree, pages, tokens, one after another.  64 trees of up
-// to 32 nodes, 16 layers of 8 heads of 128 (9.2 MB): 8.2 us with the walk in a kernel of
-// its own.
+// to 32 nodes, 16 layers of 8 heads of 128 (9.2 MB): 8.4 us, one tree of 16, two layers:
+// 6.5; with the walk in a kernel of its own 8.2 and 6.4, and a second launch, 3 us of the
+// host's, whose time the calls back to back are.
 __global__ void __launch_bounds__(kTreeCommitThreads) tree_commit_kernel(TreeCommitArgs a)
 {
     constexpr int Batch = 8;                     // tokens a thread has in flight

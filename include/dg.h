@@ -43,11 +43,13 @@
  *     DG_LM_KERNEL (single | duo | fused), DG_LM_BN (tile width),
  *     DG_LM_EPI (8 | 16: epilogue warps of the 2-SM kernel, bf16 operands),
  *     DG_ATTN_KERNEL (single | pair), DG_ATTN_SPLITS (key splits),
- *     DG_ATTN_RESERVE (SMs kept for the attention in dg_canvas_step) and
- *     DG_PAGED_KERNEL (single | pair) force a choice; a choice the shapes do
+ *     DG_ATTN_RESERVE (SMs kept for the attention in dg_canvas_step),
+ *     DG_PAGED_KERNEL (single | pair) and DG_SAMPLE_CTAS (1 .. 16: CTAs that
+ *     share a row of logits) force a choice; a choice the shapes do
  *     not allow is ignored.  Results do not depend on the choice beyond
  *     floating-point summation order (paged attention: and the rounding of the
- *     softmax weights, one bf16 in the pair kernel, two in the single one; the
+ *     softmax weights, one bf16 in the pair kernel and in both of the trees',
+ *     two in the other single one; the
  *     pair kernel takes batches of more than 128 rows of a kv head, tokens x
  *     its query heads, a sequence on average, so the last bits of a token's
  *     row depend on what else is in its batch).
