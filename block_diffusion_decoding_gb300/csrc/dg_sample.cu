@@ -30,14 +30,13 @@
 //   1 of 262144 fp32                   0.2     8     16     17         17           41
 //   64 of 262144 fp32                  9.9    17     44     37         35          103
 //   1024 of 151643 bf16               45.8    80    225    124        115          532
-// (calls back to back; 6 of the small ones is the host's time).  An exact weight takes 24
-// instructions, of which 10 are its 64-bit shift and sum: the pass of 1024 rows that sums
-// them issues 57% of the time.  Eight groups a thread: with 4 the wanted groups' tokens
-// are twice as many to read again, with 16 the maxima take 16 KB.  Tried and no better:
-// the row a few pieces ahead through asynchronous copies to shared memory (none 225 ->
-// 233, top-p on one row 46 -> 45, a batch 94 -> 91), prefetches of a row into L2 (115 ->
-// 133), fewer CTAs an SM to spread clusters (no change where there is room, up to half as
-// fast where there is none), both policies for the clusters' places (no change).
+// (calls back to back, 6 us of which are the host's).  Without a filter a token takes 36
+// instructions in all, on 57% of the issue slots (512 rows of 151643, in a profile).
+// Tried and no better: the row a few pieces ahead through asynchronous copies to shared
+// memory (the last line's 225 -> 233; top-p on one row 46.4 -> 44.7), prefetches of the
+// rows to come into L2 (its 122, then, -> 133), fewer CTAs an SM, to spread clusters (no
+// change for few rows; top-p on 64 rows 109 with 4, 156 with 2), both policies for the
+// clusters' places (no change).
 //
 // The exact weights exp((x - max) / T) are 64-bit fixed-point numbers with a relative
 // error of about 2^-29 (see Weights): a token's place among the sums of a whole

@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(TreePlanArg
 // keeps that order by itself.
 // Bound by latency: lengths and tree, pages, tokens, one after another.  64 trees of up
 // to 32 nodes, 16 layers of 8 heads of 128 (9.2 MB): 8.4 us, one tree of 16, two layers:
-// 6.5; with the walk in a kernel of its own 8.2 and 6.4, and a second launch, 3 us of the
-// host's, whose time the calls back to back are.
+// 6.5; with the walk in a kernel of its own the 64 took 8.2, and a second launch of the
+// host's time, which the calls back to back are.
 __global__ void __launch_bounds__(kTreeCommitThreads) tree_commit_kernel(TreeCommitArgs a)
 {
     constexpr int Batch = 8;                     // tokens a thread has in flight
