@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kPoolThreads) paged_fork_kernel(PagePoolArgs a
 // last, unfinished pages in every layer: a block a fork's table, or kForkBytes of a
 // page, 128 bytes of it on their way in each thread.  Bound by memory: 128 forks of 8
 // prompts, 16 layers of 8 heads of 128, 0.55 GB read and written, 55 us by itself (10
-// TB/s: what was read, and part of what was written, stays in L2) and 72 with the
+// TB/s: what was read, and part of what was written, stays in L2) and 66 with the
 // decisions and the release that follows them.
 __global__ void __launch_bounds__(kForkThreads) paged_fork_copy_kernel(PagePoolArgs a)
 {

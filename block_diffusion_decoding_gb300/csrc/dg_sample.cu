@@ -26,14 +26,14 @@
 // few, barriers and latencies in a row.  On one GB300, us, beside that read at a copy's
 // rate:
 //                                    floor  greedy  none  top-k  top-k and top-p  top-p
-//   1 row of 16384 bf16                0.0     8     12     11         14           24
+//   1 row of 16384 bf16                0.0     8     12     11         14           23
 //   1 of 262144 fp32                   0.2     8     16     17         17           41
-//   64 of 262144 fp32                  9.9    17     44     37         35          103
-//   1024 of 151643 bf16               45.8    80    225    124        115          532
+//   64 of 262144 fp32                  9.9    17     45     37         35          102
+//   1024 of 151643 bf16               45.8    74    223    120        114          527
 // (calls back to back, 6 us of which are the host's).  Without a filter a token takes 36
 // instructions in all, on 57% of the issue slots (512 rows of 151643, in a profile).
 // Tried and no better: the row a few pieces ahead through asynchronous copies to shared
-// memory (the last line's 225 -> 233; top-p on one row 46.4 -> 44.7), prefetches of the
+// memory (the last line's none 225 -> 233; top-p on one row 46.4 -> 44.7), prefetches of the
 // rows to come into L2 (its 122, then, -> 133), fewer CTAs an SM, to spread clusters (no
 // change for few rows; top-p on 64 rows 109 with 4, 156 with 2), both policies for the
 // clusters' places (no change).
