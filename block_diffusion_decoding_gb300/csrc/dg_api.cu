@@ -1067,8 +1067,6 @@ PagedWs paged_ws(int units, int rows, int D)
 }
 
 // ---------------------------------------------------------------- drafted trees, page pool
-constexpr int kMaskWords = 128;
-
 int check_status_ws(const void *workspace, size_t bytes, size_t need = sizeof(WsHeader))
 {
     if (workspace == nullptr || bytes < need) return DG_ERR_WORKSPACE;
@@ -1681,7 +1679,7 @@ int dg_paged_release(const dg_page_pool *pool, const dg_paged_cache *c, const in
                      void *workspace, size_t workspace_bytes, void *stream)
 {
     if (n < 0) return DG_ERR_INVALID_ARG;
-    if (n > (1 << 20)) return DG_ERR_UNSUPPORTED;
+    if (n > (1 << 16)) return DG_ERR_UNSUPPORTED;   // (each is compared with those before it)
     PagePoolArgs a{};
     const int rc = pool_args(a, pool, c, workspace, workspace_bytes, sizeof(WsHeader));
     if (rc != DG_OK) return rc;

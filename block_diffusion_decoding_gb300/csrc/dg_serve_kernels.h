@@ -37,6 +37,7 @@ struct TreePlanArgs {
     WsHeader *ws;
 };
 constexpr int kTreePlanThreads = 128;
+constexpr int kMaskWords = 128;       // of a row of the mask at most
 __global__ void tree_plan_kernel(TreePlanArgs a);
 
 struct TreeCommitArgs {

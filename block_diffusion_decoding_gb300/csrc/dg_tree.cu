@@ -49,7 +49,8 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(TreePlanArg
     int w = a.words - 1, depth = 0;
     uint32_t bits = 0;
     if (i >= 32 * a.words) report_error(a.ws, DG_ERR_DEVICE, 1102);
-    for (int at = i; at >= 0; ++depth) {
+    // (a mask has room for no path that is longer, and a chain of any length ends soon)
+    for (int at = i; at >= 0 && depth < 32 * kMaskWords; ++depth) {
         for (; w > at >> 5; --w) {
             row[w] = bits;
             bits = 0;

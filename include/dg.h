@@ -287,8 +287,9 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
 /*     fewer than `window` edges away.                                         */
 /* mask [T, mask_words] and positions [T], device.  Rows of nobody stay as    */
 /* they were.  A parent that is not a lower index or -1 counts as -1; a node  */
-/* past 32 mask_words is not in the mask (not seen by itself either); lengths */
-/* and rows are cut as the attention cuts them; each records DG_ERR_DEVICE.   */
+/* past 32 mask_words is not in the mask (not seen by itself either), and a   */
+/* path is followed for 4096 nodes; lengths and rows are cut as the attention */
+/* cuts them; each records DG_ERR_DEVICE.                                     */
 /* workspace: 256 bytes, for the status word.                                 */
 /* Supported: 1 <= mask_words <= 128; T == 0 is allowed.                      */
 size_t dg_tree_plan_workspace(void);
@@ -358,7 +359,7 @@ int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const in
 /* 16-byte aligned (its rows need not be).  Weights and their sums are 64-bit   */
 /* fixed-point numbers, 2^-43 of the largest, weights with a relative error of  */
 /* 2^-28: results do not depend on the order of any sum.  Needs no workspace.   */
-/* Supported: R * 16 < 2^31; V <= 393216.  R == 0 is allowed.                   */
+/* Supported: R <= 2^26; V <= 393216.  R == 0 is allowed.                       */
 #define DG_LOGITS_BF16 0
 #define DG_LOGITS_FP32 1
 int dg_sample_logits(const void *logits, int type, int64_t row_stride, int R, int V,
@@ -406,7 +407,7 @@ int dg_paged_fork(const dg_page_pool *pool, const dg_paged_cache *c, int layers,
 /* Takes back the pages of sequences seqs [n] (device): refs - 1 each, their    */
 /* places in the table -1, kv_len 0.  Pages that nobody holds any more join the */
 /* free ones at the end, the lowest id first.  An index outside [0, B) or given */
-/* before is skipped, and recorded.  n == 0 is allowed.                         */
+/* before is skipped, and recorded.  Supported: n <= 65536 (0 is allowed).      */
 size_t dg_paged_release_workspace(void);
 int dg_paged_release(const dg_page_pool *pool, const dg_paged_cache *c, const int32_t *seqs, int n,
                      void *workspace, size_t workspace_bytes, void *stream);

@@ -242,3 +242,35 @@ def test_frequencies_follow_the_weights():
     w = torch.softmax(x[0].double(), 0)
     n = torch.bincount(token.cpu().long(), minlength=6)
     assert (n - 10000 * w).abs().max() <= 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("ctas", ["1", "2", "8", "16"])
+def test_ways_and_clusters(monkeypatch, ctas, dtype):
+    """Every way to a token on clusters of every kind: nuclei from a few tokens to nearly all, in logits that lie so
+    close that bins of bins hold too many; lists about as long as a CTA has threads, and as they may be."""
+    monkeypatch.setenv("DG_SAMPLE_CTAS", ctas)
+    V = 60007
+    for spread in (0.001, 0.03, 0.3, 1.0, 3.0, 12.0):
+        x = logits(5, V, int(spread * 1000), dtype, spread=spread)
+        check(x, T=[1.0, 0.9, 1.1, 1.0, 0.5], p=[0.1, 0.5, 0.9, 0.999, 0.7])
+        check(x, p=[0.9, 0.5, 1.0, 0.1, 0.9], low=[0.2, 0.0, 0.5, 0.9, 0.01])
+    x = logits(7, V, 1, dtype)
+    for k in ([254, 255, 256, 257, 258, 300, 2], [1000, 1023, 1024, 1025, 1500, 30000, 60006]):
+        check(x, k=k)
+        check(x, k=k, p=[0.3, 0.9, 0.95, 0.5, 1.0, 0.8, 0.6], low=[0, 0.01, 0, 0.001, 0.1, 0, 0])
+    check(x, T=[1.0, 0.5, 2.0, 1.0, 0.7, 1.5, 1.0])
+
+
+def test_logprob_far_from_the_largest():
+    """A token's log probability where it is large, at temperatures of every size, and where x - m leaves fp32."""
+    V = 40
+    x = torch.zeros(8, V)
+    x[:, 0] = torch.tensor([30.0, -30.0, 1e4, -1e4, 3e38, 1e-3, 5.0, 2.0 ** 20])
+    x[:, 1:] = x[:, :1] - torch.tensor([20.0, 25.0, 0.0, 1e-2, 0.0, 1e-30, 3.0, 16.0])[:, None]
+    T = [1.0, 1.5, 1e-2, 1e-3, 1e30, 1e-28, 0.25, 1.0]
+    for u in (0.0, 0.25, 0.999, 1.0 - 2.0 ** -24):
+        check(x, T=T, u=torch.full((8,), u))
+    y = x.clone()
+    y[:, 1:] = torch.tensor([-3e38] * 8)[:, None]        # whose weight is nothing beside the first's
+    check(y, T=T, u=torch.full((8,), 0.5), exact=True)

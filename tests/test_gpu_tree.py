@@ -417,3 +417,17 @@ def test_verification_step_in_a_graph():
                     assert same_bits(k[layer, table[s, j // page].item(), j % page], row)
     held = [p for s in range(B) for p in table[s, :-(-(lens[s].item() + n) // page)].tolist()]
     assert len(set(held)) == len(held)
+
+
+def test_plan_follows_a_long_chain_for_4096_nodes():
+    """A chain that no mask has room for, as a prompt beside trees would be, ends soon, and is reported."""
+    n = 5000
+    b = Batch([n], [1], [1], 1, 1, 128, 16)
+    c = dg.PagedCache(b.k.to(DEV), b.v.to(DEV), torch.zeros(1, 512, dtype=torch.int32, device=DEV), i32([9]), b.q_start.to(DEV))
+    mask, positions = torch.zeros(n, 128, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    ws = dg.workspace(dg.tree_plan_workspace(), DEV)
+    dg.tree_plan(i32(range(-1, n - 1)), c, mask, ws, positions=positions)
+    assert dg.read_device_status(ws, clear=True) == 7
+    assert positions.tolist() == [9 + min(i, 4095) for i in range(n)]
+    want, _ = _trees.plan([list(range(-1, 4095))], [9], 128)
+    assert torch.equal(mask[:4096].cpu(), _trees.as_int32(want))
