@@ -441,13 +441,24 @@ struct Sampler {
         else cluster_sync_all();
     }
 
-    // 16 bytes of the row (-inf past its ends).
+    // 16 bytes of the row (-inf past its ends).  Stream: not to be kept in L1, of which
+    // little is left beside the shared memory.  Top-p's passes gain from it (64 fp32 rows of
+    // 262144, mixed: 83 -> 73 us; 256, top-p: 354 -> 294), those of fp32 rows do all (maxima
+    // 56 -> 54, sums 146 -> 141); the maxima of bf16 rows do by themselves (80 -> 72), but
+    // whatever follows them is slower by as much (sums 225 -> 233).
+    template <bool Stream = false>
     DG_DEVICE uint4 load(int w, int r, int l) const
     {
         constexpr uint32_t Low = E == 8 ? 0xFF80FF80u : 0xFF800000u;
         const int first = place(w, r, l, 0);
-        if (first >= skew && first + E <= a.V + skew) return __ldg(reinterpret_cast<const uint4 *>(base + first));
         uint4 v = make_uint4(Low, Low, Low, Low);
+        if (first >= skew && first + E <= a.V + skew) {
+            if (!Stream) return __ldg(reinterpret_cast<const uint4 *>(base + first));
+            asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                : "l"(base + first));
+            return v;
+        }
         if (first + E > skew && first < a.V + skew) {
             alignas(16) T x[E];
             *reinterpret_cast<uint4 *>(x) = v;
@@ -466,7 +477,7 @@ struct Sampler {
     DG_DEVICE int rows_group() const { return (a.rows_warp + kGroups - 1) / kGroups; }
 
     // f(16 bytes, row of the warp) for rows r0 .. r1 - 1.
-    template <int N, class F>
+    template <int N, bool Stream, class F>
     DG_DEVICE void rows(int r0, int r1, F f) const
     {
 #pragma unroll 1
@@ -474,27 +485,27 @@ struct Sampler {
             uint4 v[N];
 #pragma unroll
             for (int e = 0; e < N; ++e)
-                if (r + e < r1) v[e] = load(warp, r + e, lane);
+                if (r + e < r1) v[e] = load<Stream>(warp, r + e, lane);
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 if (r + e < r1) f(v[e], r + e);
         }
     }
     // The same for all rows, N ahead of those at work.
-    template <int N, class F>
+    template <int N, bool Stream, class F>
     DG_DEVICE void rows_ahead(F f) const
     {
         uint4 v[N];
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            if (e < a.rows_warp) v[e] = load(warp, e, lane);
+            if (e < a.rows_warp) v[e] = load<Stream>(warp, e, lane);
 #pragma unroll 1
         for (int r = 0; r < a.rows_warp; r += N) {
             uint4 now[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 now[e] = v[e];
-                if (r + N + e < a.rows_warp) v[e] = load(warp, r + N + e, lane);
+                if (r + N + e < a.rows_warp) v[e] = load<Stream>(warp, r + N + e, lane);
             }
 #pragma unroll
             for (int e = 0; e < N; ++e)
@@ -505,7 +516,7 @@ struct Sampler {
     template <class F>
     DG_DEVICE void each(F f) const
     {
-        rows<2>(0, a.rows_warp, [&](const uint4 &v, int r) {
+        rows<2, false>(0, a.rows_warp, [&](const uint4 &v, int r) {
             float x[E];
             Vec<T>::unpack(v, x);
 #pragma unroll
@@ -829,7 +840,7 @@ struct Sampler {
         if (flat || weight.wide) {
             each([&](float x, int, int) { above += w_of(x); });
         } else {
-            rows_ahead<kAhead>([&](const uint4 &v, int) {
+            rows_ahead<kAhead, E == 4>([&](const uint4 &v, int) {
                 float x[E];
                 Vec<T>::unpack(v, x);
 #pragma unroll
@@ -843,7 +854,7 @@ struct Sampler {
     {
         uint64_t above = 0;
         uint32_t ties = 0;
-        rows<2>(0, a.rows_warp, [&](const uint4 &raw, int) {
+        rows<2, false>(0, a.rows_warp, [&](const uint4 &raw, int) {
             float x[E];
             Vec<T>::unpack(raw, x);
 #pragma unroll
@@ -1263,7 +1274,7 @@ struct Sampler {
         for (int k = threadIdx.x; k < kMassBins * 32; k += kSampleThreads) lanes[k] = 0;
         __syncthreads();
         const float ref = weight.eighths(m);
-        rows_ahead<kAhead>([&](const uint4 &v, int) {
+        rows_ahead<kAhead, true>([&](const uint4 &v, int) {
             float x[E];
             Vec<T>::unpack(v, x);
 #pragma unroll
@@ -1307,7 +1318,7 @@ struct Sampler {
             split = hi.before + hi.count - lo.before > static_cast<uint32_t>(kMassOne * 0.65f * kList) * ctas;
             if (split) {
                 hist = clear();
-                rows_ahead<kAhead>([&](const uint4 &v, int) {
+                rows_ahead<kAhead, true>([&](const uint4 &v, int) {
                     float x[E];
                     Vec<T>::unpack(v, x);
 #pragma unroll
@@ -1324,7 +1335,7 @@ struct Sampler {
             }
         }
         uint64_t above = 0, all = 0, listed_above = 0;
-        rows_ahead<kAhead>([&](const uint4 &v, int r) {
+        rows_ahead<kAhead, true>([&](const uint4 &v, int r) {
             float x[E];
             Vec<T>::unpack(v, x);
             uint32_t hits = 0;
@@ -1479,7 +1490,7 @@ struct Sampler {
         uint32_t hi = 0, lo = 0;
         typename Vec<T>::Most most = Vec<T>::none();
         int g = 0, left = rows_group();
-        rows<8>(0, a.rows_warp, [&](const uint4 &v, int r) {
+        rows<8, E == 4>(0, a.rows_warp, [&](const uint4 &v, int r) {
             Vec<T>::most(most, v);
             if (--left > 0 && r + 1 < a.rows_warp) return;
             const float x = Vec<T>::value(most);
