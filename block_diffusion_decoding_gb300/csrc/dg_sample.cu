@@ -4,7 +4,7 @@
 // What is kept of a row is a prefix of its tokens in the order (logit falling, index
 // rising): all above a value, the cut, and the first few of those that equal it.  So
 // a vocabulary is not sorted.  Every way to the token begins with one pass over the
-// row, in which a thread takes the maximum of each of its kGroups groups of tokens.
+// row, in which a thread takes the maximum of each of its groups of tokens.
 //   no filter    the weights are summed, a stretch of the row a warp; the token is
 //                looked for in the stretch that the random number falls into;
 //   few kept     (top-k of up to kListMost, what min-p leaves, a small nucleus) the
@@ -57,7 +57,7 @@ constexpr float kBinsLog2 = 16.f;        // of the search by counting: bins to a
 constexpr float kMassOne = 8192.f;       // a weight where its bin stands for it, in sums of rounded ones
 constexpr float kEighths = 1572864.f;    // 1.5 x 2^20: a unit in the last place is 1/8
 constexpr int kMassBins = 256;           // of top-p's: 8 to a factor of 2
-constexpr int kGroups = 8;               // groups of a thread's tokens
+constexpr int kGroupBytes = 32;          // of the maxima of a thread's groups: 8, of bf16 tokens 16
 constexpr int kList = 1536;              // tokens that are sorted at most
 constexpr int kListMost = 1024;          // of which top-k's k
 constexpr int kLaneBits = 53;            // a weight of 1 in a lane's sums: up to 1600 tokens
@@ -94,7 +94,7 @@ struct alignas(16) SampleShared {
             uint32_t ties[2][kSegments];    // and tokens at it
             uint64_t row_above[kSampleRows];
             uint32_t row_ties[kSampleRows];
-            float group[kGroups][kSampleThreads];   // maxima
+            uint8_t group[kGroupBytes * kSampleThreads];   // maxima, as the tokens' type
         };
         uint64_t moved[kList];            // the list while it is sorted
     };
@@ -187,6 +187,7 @@ struct Vec<float> {
     }
     DG_DEVICE static float value(Most m) { return m; }
     DG_DEVICE static float widen(float x) { return x; }
+    DG_DEVICE static float narrow(float x) { return x; }
 };
 template <>
 struct Vec<uint16_t> {
@@ -209,6 +210,8 @@ struct Vec<uint16_t> {
     }
     DG_DEVICE static float value(Most m) { return fmaxf(__low2float(m), __high2float(m)); }
     DG_DEVICE static float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+    // (of what is a bf16 number)
+    DG_DEVICE static uint16_t narrow(float x) { return static_cast<uint16_t>(__float_as_uint(x) >> 16); }
 };
 
 // floor(f S) for f in [0, 1), a float's 24 bits times 64 (up: the next whole number
@@ -390,6 +393,7 @@ __device__ __noinline__ void end_nucleus(const SampleArgs &a, SampleShared &sh, 
 template <class T>
 struct Sampler {
     static constexpr int E = Vec<T>::N;
+    static constexpr int kGroups = kGroupBytes / sizeof(T);
     static constexpr int kAhead = E == 4 ? 2 : 1;   // 16 bytes that a pass has on their way
     const SampleArgs &a;
     SampleShared &sh;
@@ -475,6 +479,7 @@ struct Sampler {
         return (((rank * kSampleWarps + w) * a.rows_warp + r) * 32 + l) * E + e;
     }
     DG_DEVICE int rows_group() const { return (a.rows_warp + kGroups - 1) / kGroups; }
+    DG_DEVICE T &group(int g) const { return reinterpret_cast<T *>(sh.group)[g * kSampleThreads + threadIdx.x]; }
 
     // f(16 bytes, row of the warp) for rows r0 .. r1 - 1.
     template <int N, bool Stream, class F>
@@ -533,7 +538,7 @@ struct Sampler {
         static_assert(sizeof(sh.mass) >= kGroups * kSampleThreads * sizeof(uint16_t), "a place for every group");
         uint32_t want = 0;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) want |= wanted(sh.group[g][threadIdx.x]) ? 1u << g : 0u;
+        for (int g = 0; g < kGroups; ++g) want |= wanted(Vec<T>::widen(group(g))) ? 1u << g : 0u;
         uint32_t slot = __popc(want);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1494,13 +1499,14 @@ struct Sampler {
             Vec<T>::most(most, v);
             if (--left > 0 && r + 1 < a.rows_warp) return;
             const float x = Vec<T>::value(most);
-            sh.group[g++][threadIdx.x] = x;
+            group(g++) = Vec<T>::narrow(x);
             hi = max(hi, order_of(x));
             if (x > -INFINITY) lo = max(lo, ~order_of(x));
             most = Vec<T>::none();
             left = rows_group();
         });
-        for (; g < kGroups; ++g) sh.group[g][threadIdx.x] = -INFINITY;
+        const int groups = g;
+        for (; g < kGroups; ++g) group(g) = Vec<T>::narrow(-INFINITY);
         __syncwarp();
         if (ctas > 1) cluster_wait_all();
         const uint2 ends = largest(hi, lo);
@@ -1565,7 +1571,7 @@ struct Sampler {
                 // (below half of the maxima there are many more tokens than maxima)
                 if (2 * k <= ctas * kSampleThreads * (a.rows_warp / rows_group())) {
 #pragma unroll 1
-                    for (int g = 0; g < kGroups; ++g) count(sh.group[g][threadIdx.x]);
+                    for (int g = 0; g < groups; ++g) count(Vec<T>::widen(group(g)));
                 } else {
                     each([&](float x, int, int) { count(x); });
                 }
