@@ -186,6 +186,10 @@ struct Vec<float> {
                   fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
     DG_DEVICE static float value(Most m) { return m; }
+    DG_DEVICE static float at(const uint4 &v, int e)
+    {
+        return __uint_as_float(e < 2 ? (e < 1 ? v.x : v.y) : (e < 3 ? v.z : v.w));
+    }
     DG_DEVICE static float widen(float x) { return x; }
     DG_DEVICE static float narrow(float x) { return x; }
 };
@@ -209,6 +213,11 @@ struct Vec<uint16_t> {
         m = __hmax2(__hmax2(m, x[0]), __hmax2(x[1], __hmax2(x[2], x[3])));
     }
     DG_DEVICE static float value(Most m) { return fmaxf(__low2float(m), __high2float(m)); }
+    DG_DEVICE static float at(const uint4 &v, int e)
+    {
+        const uint32_t w = e < 4 ? (e < 2 ? v.x : v.y) : (e < 6 ? v.z : v.w);
+        return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+    }
     DG_DEVICE static float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
     // (of what is a bf16 number)
     DG_DEVICE static uint16_t narrow(float x) { return static_cast<uint16_t>(__float_as_uint(x) >> 16); }
@@ -528,38 +537,53 @@ struct Sampler {
             for (int e = 0; e < E; ++e) f(x[e], r, e);
         });
     }
-    // f(16 bytes, warp, row, lane) for those of the groups whose maximum is wanted,
-    // shared out evenly over the CTA's threads.  Once a row; all of them.
-    template <class W, class F>
-    DG_DEVICE void each_of(W wanted, F f)
+    // A place in a list for each of a lane's `n` tokens, the first of them; `count`: its
+    // length.  By a warp.
+    DG_DEVICE uint32_t places(uint32_t n, uint32_t *count) const
     {
-        constexpr int N = 4;
+        uint32_t end = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(kAll, end, o);
+            if (lane >= o) end += x;
+        }
+        uint32_t first = 0;
+        if (lane == 31 && end > 0) first = atomicAdd(count, end);
+        return __shfl_sync(kAll, first, 31) + end - n;
+    }
+    // The 16 bytes of the groups whose maximum is wanted, listed; how many they are.  Once
+    // a row.
+    template <class W>
+    DG_DEVICE int pick(W wanted)
+    {
         uint16_t *todo = reinterpret_cast<uint16_t *>(sh.mass);
         static_assert(sizeof(sh.mass) >= kGroups * kSampleThreads * sizeof(uint16_t), "a place for every group");
         uint32_t want = 0;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) want |= wanted(Vec<T>::widen(group(g))) ? 1u << g : 0u;
-        uint32_t slot = __popc(want);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(kAll, slot, o);
-            if (lane >= o) slot += x;
-        }
-        uint32_t at0 = 0;
-        if (lane == 31 && slot > 0) at0 = atomicAdd(&sh.todo, slot);
-        slot += __shfl_sync(kAll, at0, 31) - __popc(want);
+        uint32_t slot = places(__popc(want), &sh.todo);
         for (; want != 0; want &= want - 1)
             todo[slot++] = static_cast<uint16_t>((__ffs(want) - 1) * kSampleThreads + threadIdx.x);
         __syncthreads();
-        const int rg = rows_group(), n = static_cast<int>(sh.todo) * rg;
+        return static_cast<int>(sh.todo) * rows_group();
+    }
+    // f(N of those from place x0 on, a thread's, and where they are: warp, row, lane; where
+    // there is none 16 bytes of -inf), shared out evenly; a warp's threads go together.
+    template <int N, class F>
+    DG_DEVICE void picked(int n, F f)
+    {
+        const uint16_t *todo = reinterpret_cast<const uint16_t *>(sh.mass);
+        const int rg = rows_group();
 #pragma unroll 1
-        for (int x0 = threadIdx.x; x0 < n; x0 += N * kSampleThreads) {
+        for (int x0 = warp * 32; x0 < n; x0 += N * kSampleThreads) {
             uint4 v[N];
             int w[N], r[N], l[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const int x = x0 + e * kSampleThreads;
-                r[e] = a.rows_warp;
+                constexpr uint32_t Low = E == 8 ? 0xFF80FF80u : 0xFF800000u;
+                v[e] = make_uint4(Low, Low, Low, Low);
+                const int x = x0 + lane + e * kSampleThreads;
+                w[e] = r[e] = l[e] = 0;
                 if (x >= n) continue;
                 const int at = x / rg, id = todo[at];
                 r[e] = id / kSampleThreads * rg + x - at * rg;
@@ -567,10 +591,36 @@ struct Sampler {
                 l[e] = id % 32;
                 if (r[e] < a.rows_warp) v[e] = load(w[e], r[e], l[e]);
             }
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (r[e] < a.rows_warp) f(v[e], w[e], r[e], l[e]);
+            f(v, w, r, l);
         }
+    }
+    // The tokens that are wanted, listed.
+    template <class W>
+    DG_DEVICE void list_of(W wanted)
+    {
+        constexpr int N = 4;
+        picked<N>(pick(wanted), [&](const uint4 (&v)[N], const int (&w)[N], const int (&r)[N], const int (&l)[N]) {
+            uint32_t hits = 0;                       // of N * E tokens
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float x[E];
+                Vec<T>::unpack(v[i], x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) hits |= wanted(x[e]) ? 1u << (i * E + e) : 0u;
+            }
+            if (!__any_sync(kAll, hits != 0)) return;
+            uint32_t slot = places(__popc(hits), &sh.listed);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                for (uint32_t h = hits >> (i * E) & ((1u << E) - 1u); h != 0; h &= h - 1) {
+                    const int e = __ffs(h) - 1;
+                    if (slot < kList)
+                        sh.list[slot] = static_cast<uint64_t>(~order_of(Vec<T>::at(v[i], e))) << 32 |
+                                        static_cast<uint32_t>(place(w[i], r[i], l[i], e));
+                    ++slot;
+                }
+            }
+        });
     }
 
     // The largest of two values over the row's threads.
@@ -1522,13 +1572,18 @@ struct Sampler {
         }
         if (!(t > 0.f) || k == 1 || p <= 0.f) {              // the first of the largest
             uint32_t best = 0;
-            each_of([&](float x) -> bool { return x == m; }, [&](const uint4 &v, int w, int r, int l) {
-                float x[E];
-                Vec<T>::unpack(v, x);
+            constexpr int N = 4;
+            picked<N>(pick([&](float x) -> bool { return x == m; }),
+                      [&](const uint4 (&v)[N], const int (&w)[N], const int (&r)[N], const int (&l)[N]) {
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (x[e] == m) best = max(best, ~static_cast<uint32_t>(place(w, r, l, e)));
-            });
+                          for (int i = 0; i < N; ++i) {
+                              float x[E];
+                              Vec<T>::unpack(v[i], x);
+#pragma unroll
+                              for (int e = 0; e < E; ++e)
+                                  if (x[e] == m) best = max(best, ~static_cast<uint32_t>(place(w[i], r[i], l[i], e)));
+                          }
+                      });
             __syncwarp();
             best = largest(best, 0).x;
             if (lead) {
@@ -1583,14 +1638,7 @@ struct Sampler {
             auto wanted = [&](float x) -> bool {
                 return x >= from && x > -INFINITY && !((m - x) * scale >= limit);
             };
-            each_of(wanted, [&](const uint4 &v, int w, int r, int l) {
-                float x[E];
-                Vec<T>::unpack(v, x);
-                uint32_t hits = 0;
-#pragma unroll
-                for (int e = 0; e < E; ++e) hits |= wanted(x[e]) ? 1u << e : 0u;
-                list(x, hits, w, r, l);
-            });
+            list_of(wanted);
             const int n = join_lists();
             if (n <= kList) {
                 if (rank != 0) return false;
