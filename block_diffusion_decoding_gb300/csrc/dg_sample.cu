@@ -26,10 +26,10 @@
 // few, barriers and latencies in a row.  On one GB300, us, beside that read at a copy's
 // rate:
 //                                    floor  greedy  none  top-k  top-k and top-p  top-p
-//   1 row of 16384 bf16                0.0     8     12     11         14           23
-//   1 of 262144 fp32                   0.2     8     16     17         17           41
-//   64 of 262144 fp32                  9.9    17     45     37         35          102
-//   1024 of 151643 bf16               45.8    74    223    120        114          527
+//   1 row of 16384 bf16                0.0     8     12     12         14           22
+//   1 of 262144 fp32                   0.2     8     16     17         17           37
+//   64 of 262144 fp32                  9.9    16     43     36         33           96
+//   1024 of 151643 bf16               45.8    70    222    114        108          500
 // (calls back to back, 6 us of which are the host's).  Without a filter a token takes 36
 // instructions in all, on 57% of the issue slots (512 rows of 151643, in a profile).
 // Tried and no better: the row a few pieces ahead through asynchronous copies to shared
