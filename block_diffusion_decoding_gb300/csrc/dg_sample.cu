@@ -27,9 +27,9 @@
 // rate:
 //                                    floor  greedy  none  top-k  top-k and top-p  top-p
 //   1 row of 16384 bf16                0.0     8     12     12         14           22
-//   1 of 262144 fp32                   0.2     8     16     17         17           37
-//   64 of 262144 fp32                  9.9    16     43     36         33           96
-//   1024 of 151643 bf16               45.8    70    222    114        108          500
+//   1 of 262144 fp32                   0.2     8     15     17         17           37
+//   64 of 262144 fp32                  9.9    16     41     36         33           93
+//   1024 of 151643 bf16               45.8    70    210    114        108          484
 // (calls back to back, 6 us of which are the host's).  Without a filter a token takes 36
 // instructions in all, on 57% of the issue slots (512 rows of 151643, in a profile).
 // Tried and no better: the row a few pieces ahead through asynchronous copies to shared
@@ -274,7 +274,7 @@ struct Weights {
         m = max;
         ch = 1.442695041f / t;
         cl = (fmaf(-ch, t, 1.442695041f) + 1.92596299e-8f) / t;   // log2 e in two parts
-        floor = max - 60.f / ch;
+        floor = max - 57.f / ch;                         // (2^-53 is the last that counts)
         ref = __float_as_int(fmaf(max, ch, 393216.f));   // 1.5 x 2^18: a unit in the last place is 1/32
         wide = !(fabsf(max) * ch < 65536.f);
     }
@@ -311,11 +311,8 @@ struct Weights {
         s = fmaf(r, s, 0.69314718f);
         const float B = fmaf(r, s, 0.046875f);           // 1.5 x 2^-5: in units of 2^-28
         const uint32_t T = table[p & 31];
-        const int yi = static_cast<int>(static_cast<uint32_t>(__float_as_int(B)) * 16u -
-                                        static_cast<uint32_t>(__float_as_int(0.046875f)) * 16u);
-        uint32_t w;                                      // T (1 + y)
-        asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(w) : "r"(T), "r"(yi));
-        return static_cast<uint64_t>(w) << (kLaneBits - 30) >> (ref + 31 - p >> 5);   // (0 .. 61)
+        const uint32_t Y = __float_as_uint(B) - (__float_as_uint(0.046875f) - (1u << 28));   // 2^28 (1 + y)
+        return static_cast<uint64_t>(T) * Y >> (ref + 31 + 32 * (58 - kLaneBits) - p >> 5);  // (by 5 .. 63)
     }
     DG_DEVICE uint64_t in_double(float x) const { return weight_in_double(x, m, ch, cl); }
 };
