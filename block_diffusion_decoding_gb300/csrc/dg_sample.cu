@@ -27,13 +27,13 @@
 // rate:
 //                                    floor  greedy  none  top-k  top-k and top-p  top-p
 //   1 row of 16384 bf16                0.0     8     12     12         14           22
-//   1 of 262144 fp32                   0.2     8     15     17         17           37
-//   64 of 262144 fp32                  9.9    16     41     36         33           93
-//   1024 of 151643 bf16               45.8    70    210    114        108          484
-// (calls back to back, 6 us of which are the host's).  Without a filter a token takes 36
-// instructions in all, on 57% of the issue slots (512 rows of 151643, in a profile).
+//   1 of 262144 fp32                   0.2     8     15     17         17           35
+//   64 of 262144 fp32                  9.9    16     41     36         33           89
+//   1024 of 151643 bf16               45.8    70    210    114        108          469
+// (calls back to back, 6 us of which are the host's).  Without a filter a token takes 34
+// instructions in all, on 59% of the issue slots (512 rows of 151643, in a profile).
 // Tried and no better: the row a few pieces ahead through asynchronous copies to shared
-// memory (the last line's none 225 -> 233; top-p on one row 46.4 -> 44.7), prefetches of the
+// memory (the last line's none, then 225, -> 233; top-p on one row 46.4 -> 44.7), prefetches of the
 // rows to come into L2 (its 122, then, -> 133), fewer CTAs an SM, to spread clusters (no
 // change for few rows; top-p on 64 rows 109 with 4, 156 with 2), both policies for the
 // clusters' places (no change).
@@ -456,19 +456,21 @@ struct Sampler {
     // 262144, mixed: 83 -> 73 us; 256, top-p: 354 -> 294), those of fp32 rows do all (maxima
     // 56 -> 54, sums 146 -> 141); the maxima of bf16 rows do by themselves (80 -> 72), but
     // whatever follows them is slower by as much (sums 225 -> 233).
-    template <bool Stream = false>
-    DG_DEVICE uint4 load(int w, int r, int l) const
+    template <bool Stream>
+    DG_DEVICE static uint4 fetch(const T *p)
+    {
+        if (!Stream) return __ldg(reinterpret_cast<const uint4 *>(p));
+        uint4 v;
+        asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+            : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+            : "l"(p));
+        return v;
+    }
+    // ... that the row's first or last token is among, or none.
+    DG_DEVICE uint4 edge(int first) const
     {
         constexpr uint32_t Low = E == 8 ? 0xFF80FF80u : 0xFF800000u;
-        const int first = place(w, r, l, 0);
         uint4 v = make_uint4(Low, Low, Low, Low);
-        if (first >= skew && first + E <= a.V + skew) {
-            if (!Stream) return __ldg(reinterpret_cast<const uint4 *>(base + first));
-            asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                : "l"(base + first));
-            return v;
-        }
         if (first + E > skew && first < a.V + skew) {
             alignas(16) T x[E];
             *reinterpret_cast<uint4 *>(x) = v;
@@ -478,6 +480,30 @@ struct Sampler {
             v = *reinterpret_cast<const uint4 *>(x);
         }
         return v;
+    }
+    template <bool Stream = false>
+    DG_DEVICE uint4 load(int w, int r, int l) const
+    {
+        const int first = place(w, r, l, 0);
+        return first >= skew && first + E <= a.V + skew ? fetch<Stream>(base + first) : edge(first);
+    }
+    // The 16 bytes of each row of this thread's warp that are its own: whole ones in rows
+    // from .. to - 1.  Fewer instructions a load for more registers: top-p's passes gain
+    // (484 -> 469 us on 1024 bf16 rows of 151643), the others lose (maxima 72 -> 74, sums
+    // 210 -> 213).
+    struct Own {
+        const T *p;
+        int first, from, to;
+    };
+    DG_DEVICE Own own() const
+    {
+        const int first = place(warp, 0, lane, 0), left = a.V + skew - E - first;
+        return Own{base + first, first, first < skew ? 1 : 0, left >= 0 ? left / (32 * E) + 1 : 0};
+    }
+    template <bool Stream>
+    DG_DEVICE uint4 load(const Own &o, int r) const
+    {
+        return r >= o.from && r < o.to ? fetch<Stream>(o.p + r * (32 * E)) : edge(o.first + r * (32 * E));
     }
     // The first token of 16 bytes, `skew` early.
     DG_DEVICE int place(int w, int r, int l, int e) const
@@ -503,20 +529,20 @@ struct Sampler {
         }
     }
     // The same for all rows, N ahead of those at work.
-    template <int N, bool Stream, class F>
-    DG_DEVICE void rows_ahead(F f) const
+    template <int N, class F, class L>
+    DG_DEVICE void rows_ahead(F f, L load_row) const
     {
         uint4 v[N];
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            if (e < a.rows_warp) v[e] = load<Stream>(warp, e, lane);
+            if (e < a.rows_warp) v[e] = load_row(e);
 #pragma unroll 1
         for (int r = 0; r < a.rows_warp; r += N) {
             uint4 now[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 now[e] = v[e];
-                if (r + N + e < a.rows_warp) v[e] = load<Stream>(warp, r + N + e, lane);
+                if (r + N + e < a.rows_warp) v[e] = load_row(r + N + e);
             }
 #pragma unroll
             for (int e = 0; e < N; ++e)
@@ -892,12 +918,12 @@ struct Sampler {
         if (flat || weight.wide) {
             each([&](float x, int, int) { above += w_of(x); });
         } else {
-            rows_ahead<kAhead, E == 4>([&](const uint4 &v, int) {
+            rows_ahead<kAhead>([&](const uint4 &v, int) {
                 float x[E];
                 Vec<T>::unpack(v, x);
 #pragma unroll
                 for (int e = 0; e < E; ++e) above += weight.fast(x[e], sh.table);
-            });
+            }, [&](int r) -> uint4 { return load<E == 4>(warp, r, lane); });
         }
         return gather(above, 0);
     }
@@ -1326,7 +1352,9 @@ struct Sampler {
         for (int k = threadIdx.x; k < kMassBins * 32; k += kSampleThreads) lanes[k] = 0;
         __syncthreads();
         const float ref = weight.eighths(m);
-        rows_ahead<kAhead, true>([&](const uint4 &v, int) {
+        const Own mine_rows = own();
+        auto load_row = [&](int r) -> uint4 { return load<true>(mine_rows, r); };
+        rows_ahead<kAhead>([&](const uint4 &v, int) {
             float x[E];
             Vec<T>::unpack(v, x);
 #pragma unroll
@@ -1336,7 +1364,7 @@ struct Sampler {
                 const uint32_t w = weight.beside(x[e], at);
                 atomicAdd(lanes + min(b, kMassBins - 1) * 32 + lane, b < kMassBins ? w : 0);
             }
-        });
+        }, load_row);
         __syncthreads();
         uint32_t mine = 0;
 #pragma unroll 8
@@ -1370,7 +1398,7 @@ struct Sampler {
             split = hi.before + hi.count - lo.before > static_cast<uint32_t>(kMassOne * 0.65f * kList) * ctas;
             if (split) {
                 hist = clear();
-                rows_ahead<kAhead, true>([&](const uint4 &v, int) {
+                rows_ahead<kAhead>([&](const uint4 &v, int) {
                     float x[E];
                     Vec<T>::unpack(v, x);
 #pragma unroll
@@ -1378,7 +1406,7 @@ struct Sampler {
                         const float at = weight.eighths(x[e]);
                         if (at <= first_at && at >= last_at) atomicAdd(hist + sub_bin(x[e], top, scale), 1u);
                     }
-                });
+                }, load_row);
                 find_each<true, kBins>(0, parts, hi.all, mass_from, of_sub);
                 const Found hi2 = sh.found[0], lo2 = sh.found[1];
                 if (!hi2.reached || hi2.before + hi2.count - lo2.before > kList) return false;
@@ -1387,7 +1415,7 @@ struct Sampler {
             }
         }
         uint64_t above = 0, all = 0, listed_above = 0;
-        rows_ahead<kAhead, true>([&](const uint4 &v, int r) {
+        rows_ahead<kAhead>([&](const uint4 &v, int r) {
             float x[E];
             Vec<T>::unpack(v, x);
             uint32_t hits = 0;
@@ -1410,7 +1438,7 @@ struct Sampler {
                 }
             }
             list(x, hits, warp, r, lane);
-        });
+        }, load_row);
         if (!all_listed && !split) {
             // Each CTA has its part of the bins' tokens; those that the cut cannot be among
             // are told apart by bins of their own, and leave the list.
