@@ -1130,11 +1130,14 @@ int sample_kernels(DeviceInfo &di)
 
 // CTAs that share a row, and the 512-byte pieces of it that a warp of theirs reads.
 // Two things count: a row's time by itself, which more CTAs shorten while each warp has
-// a few pieces to read at once (one row of 151643 bf16 logits, no filter: 57 us with 1,
-// 36 with 2, 25 with 4, 20 with 8), and the clusters that are at work at a time, which
-// take turns from where they fill the GPU (1024 such rows: 246, 235, 260, 355; long
-// rows that are not shared leave fewer threads to each SM's memory traffic and more
-// of them in L2 at a time).  DG_SAMPLE_CTAS forces a number.
+// more than a few pieces to read at once (one row of 151643 bf16 logits, no filter: 47 us
+// with 1, 30 with 2, 20 with 4, 16.5 with 8; of 16384, top-k and top-p, 13.5, 15.1, 14.6,
+// 15.0), and the clusters that are at work at a time, which take turns from where they
+// fill the GPU (1024 rows of 151643: 220, 210, 240, 335; of 16384: 38, 58, 91, 175; long
+// rows that are not shared leave fewer threads to each SM's memory traffic and more of
+// them in L2 at a time).  16 pay where a warp still has 12 pieces and the CTAs an SM each
+// (1 row of 262144 fp32: 20.3 with 8, 15.6; 64 rows: 41 and 50).  DG_SAMPLE_CTAS forces a
+// number.
 int sample_cluster(int type, int64_t stride, int R, int V, int sms, int *rows_warp)
 {
     const int per = type == DG_LOGITS_BF16 ? 8 : 4;
@@ -1147,7 +1150,7 @@ int sample_cluster(int type, int64_t stride, int R, int V, int sms, int *rows_wa
         while (ctas < kSampleCluster && ctas < std::atoi(env)) ctas *= 2;
     } else {
         while (rows(ctas) > 64) ctas *= 2;
-        while (ctas < 8 && rows(2 * ctas) > 2 && 2LL * R * ctas <= kSampleCtas * sms) ctas *= 2;
+        while (ctas < 8 && rows(2 * ctas) > 4 && 2LL * R * ctas <= kSampleCtas * sms) ctas *= 2;
         if (ctas == 8 && rows(16) >= 12 && 16LL * R <= sms) ctas = 16;
     }
     *rows_warp = rows(ctas);

@@ -115,7 +115,7 @@ struct alignas(16) SampleShared {
 static_assert(offsetof(SampleShared, hist) % 16 == 0 && offsetof(SampleShared, list) % 8 == 0 &&
                   offsetof(SampleShared, gather) % 8 == 0 && offsetof(SampleShared, above) % 8 == 0 &&
                   offsetof(SampleShared, rem) % 8 == 0 && offsetof(SampleShared, all) % 8 == 0 &&
-                  offsetof(SampleShared, cut) % 4 == 0,
+                  offsetof(SampleShared, cut) % 4 == 0 && offsetof(SampleShared, group) % 4 == 0,
               "alignment");
 
 // round(2^(30 + j / 32))
