@@ -70,7 +70,7 @@ constexpr int kMoves = 1 << 14;
 
 struct Found {
     int bin;                             // -1: the target lies past the last one
-    uint32_t count, before;              // tokens in it, and above it
+    uint32_t count, before, total;       // tokens in it, above it, and in all bins
     float mass, all;                     // weight above it, and of all bins
     bool reached;                        // (with rounded weights: else the last one with a token)
 };
@@ -743,6 +743,7 @@ struct Sampler {
         }
         __syncthreads();
         float f_all = 0.f;
+        uint32_t n_all = 0;
 #pragma unroll
         for (int w = 0; w < kSampleWarps; ++w) {
             if (w < warp) {
@@ -750,6 +751,7 @@ struct Sampler {
                 f_end += sh.scan_f[w];
             }
             f_all += sh.scan_f[w];
+            n_all += sh.scan_u[w];
         }
         float aim[N];
 #pragma unroll
@@ -764,14 +766,14 @@ struct Sampler {
         for (int i = 0; i < N; ++i) {
             const bool reached = sh.claim[i] < kSampleThreads;
             if (static_cast<int>(threadIdx.x) != (reached ? sh.claim[i] : max(sh.last, 0))) continue;
-            Found got{-1, 0, 0, 0.f, f_all, reached};
+            Found got{-1, 0, 0, n_all, 0.f, f_all, reached};
             uint32_t n_before = n_end - n_sum;
             float f_before = f_end - f_sum;
             bool stop = false;
 #pragma unroll
             for (int e = 0; e < kBinsThread; ++e) {
                 if (n[e] > 0 && !stop) {
-                    got = Found{b + e, n[e], n_before, f_before, f_all, reached};
+                    got = Found{b + e, n[e], n_before, n_all, f_before, f_all, reached};
                     stop = reached && (Mass ? f_before + f[e] >= aim[i] : n_before + n[e] >= target);
                 }
                 n_before += n[e];
@@ -1641,25 +1643,44 @@ struct Sampler {
         if (!flat && (list_k || list_min)) {
             uint64_t all = 0;
             if (part && !some) all = sums_all().above;
-            float scale = 0.f, limit = INFINITY;
+            float scale = 0.f, limit = INFINITY, from = min_value;
             if (list_k) {
-                scale = static_cast<float>(kBins) / (m - of_order(~ends.y));
+                // What a mask of finite values leaves aside: weights below e^-750.  It may
+                // not widen the bins, nor count as groups that hold a token.
+                const float masked = m - fmaxf(1000.f, 750.f * t);
+                uint32_t lo = ends.y;
+                if (of_order(~lo) < masked) {
+                    lo = 0;
+                    for (int g = 0; g < groups; ++g) {
+                        const float x = Vec<T>::widen(group(g));
+                        if (x >= masked && x > -INFINITY) lo = max(lo, ~order_of(x));
+                    }
+                    lo = largest(lo, 0).x;
+                }
+                from = masked;
+                scale = static_cast<float>(kBins) / (m - of_order(~lo));
                 uint32_t *hist = sh.hist[0];
                 auto count = [&](float x) {
-                    if (x > -INFINITY) atomicAdd(hist + max(0, min(static_cast<int>((m - x) * scale), kBins - 1)), 1u);
+                    if (x >= masked && x > -INFINITY)
+                        atomicAdd(hist + max(0, min(static_cast<int>((m - x) * scale), kBins - 1)), 1u);
                 };
+                auto found = [&]() -> Found { return find<false>(k, 0.f, [](int) -> float { return 0.f; }); };
                 // (below half of the maxima there are many more tokens than maxima)
+                Found f;
+                f.total = 0;
                 if (2 * k <= ctas * kSampleThreads * (a.rows_warp / rows_group())) {
 #pragma unroll 1
                     for (int g = 0; g < groups; ++g) count(Vec<T>::widen(group(g)));
-                } else {
-                    each([&](float x, int, int) { count(x); });
+                    f = found();
                 }
-                const Found f = find<false>(k, 0.f, [](int) -> float { return 0.f; });
+                if (f.total < 2u * static_cast<uint32_t>(k)) {
+                    hist = clear();
+                    each([&](float x, int, int) { count(x); });
+                    f = found();
+                }
                 if (f.bin >= 0 && f.bin < kBins - 1) limit = static_cast<float>(f.bin + 1);
                 else scale = 0.f;                            // (all of them)
             }
-            const float from = list_min ? min_value : -INFINITY;
             auto wanted = [&](float x) -> bool {
                 return x >= from && x > -INFINITY && !((m - x) * scale >= limit);
             };

@@ -274,3 +274,19 @@ def test_logprob_far_from_the_largest():
     y = x.clone()
     y[:, 1:] = torch.tensor([-3e38] * 8)[:, None]        # whose weight is nothing beside the first's
     check(y, T=T, u=torch.full((8,), 0.5), exact=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value", [-1e4, -1e9, "min", -math.inf])
+@pytest.mark.parametrize("first,last", [(300, 20000), (0, 19000), (7000, 19900)])
+def test_masks_of_finite_values(dtype, value, first, last):
+    """Tokens ruled out by a large negative number or the type's lowest: fewer left than top-k asks for, all of them in
+    a few threads' groups; where the temperature lets such a token weigh something, it counts."""
+    x = logits(8, 20000, 3, dtype)
+    x[:, first:last] = torch.finfo(dtype).min if value == "min" else value
+    k = [1, 5, 250, 400, 1000, 1024, 19999, 120]
+    for T in (0.05, 1.0, 10.0, 50.0):
+        for u in (0.0, 0.3, 0.999):
+            check(x, T=[T] * 8, k=k, u=torch.full((8,), u))
+        check(x, T=[T] * 8, k=k, p=[0.9] * 8, low=[0.0, 0.01] * 4)
+        check(x, T=[T] * 8, p=[0.3, 0.9, 0.999, 1.0] * 2)
