@@ -438,6 +438,8 @@ struct Sampler {
     {
         return flat ? (x == m ? 1ull << kLaneBits : 0) : weight(x, sh.table);
     }
+    // The least logit that is ever drawn: further down weights are zeros of 64-bit floats.
+    DG_DEVICE float light() const { return flat ? m : fmaf(-745.13f, t, m); }
     // n tokens of weight w in the units of the sums
     DG_DEVICE static uint64_t times(uint64_t w, uint64_t n)
     {
@@ -1070,7 +1072,7 @@ struct Sampler {
                 Vec<T>::unpack(load(seg, k / 32, k % 32), x);
                 for (int e = 0; e < E; ++e) {
                     const bool tie = x[e] == v && v > -INFINITY;
-                    if (x[e] > v || (tie && prefix < kept)) {
+                    if ((x[e] > v || (tie && prefix < kept)) && x[e] >= light()) {
                         token = place(seg, k / 32, k % 32, e) - skew;
                         value = x[e];
                     }
@@ -1090,12 +1092,12 @@ struct Sampler {
             draw(v, kept, s, rem, all);
             return;
         }
-        // the first that is kept, however light
+        // the first that is kept and weighs anything
         uint32_t best = 0;
         float value = 0.f;
         each([&](float x, int r, int e) {
             const uint32_t at = ~static_cast<uint32_t>(place(warp, r, lane, e));
-            if ((x > v || (x == v && kept > 0)) && at > best) {
+            if ((x > v || (x == v && kept > 0)) && x >= light() && at > best) {
                 best = at;
                 value = x;
             }
@@ -1204,6 +1206,7 @@ struct Sampler {
     // `least`.
     DG_DEVICE void draw_listed(int n, int k, float p, uint64_t all, float least, float u)
     {
+        least = fmaxf(least, light());
         if (n <= kSampleThreads) {
             draw_few(n, k, p, all, least, u);
             return;

@@ -352,7 +352,9 @@ int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const in
 /* logprob = ln(its weight / the kept weight).  T <= 0 or NaN: the first token */
 /* of the order; T is cut to 2^-100 .. 2^100.  Tokens whose logit is minus     */
 /* infinity or NaN are never drawn (a row of them alone: token -1, logprob     */
-/* minus infinity); where m is infinite, the tokens that have it are all alike. */
+/* minus infinity), nor are those more than 745.13 T below m, whose weight is   */
+/* 0 in 64-bit floats; where m is infinite, the tokens that have it are all     */
+/* alike.                                                                       */
 /* logits [R, V] fp32 or bf16, rows row_stride elements apart (>= V, 0: V);    */
 /* temperature, top_k, top_p, min_p [R], each NULL for 1, 0, 1, 0; u [R] fp32   */
 /* in [0, 1); token [R] int32, logprob [R] fp32 or NULL.  All device; logits    */
