@@ -502,10 +502,9 @@ struct Sampler {
         const int first = place(warp, 0, lane, 0), left = a.V + skew - E - first;
         return Own{base + first, first, first < skew ? 1 : 0, left >= 0 ? left / (32 * E) + 1 : 0};
     }
-    template <bool Stream>
     DG_DEVICE uint4 load(const Own &o, int r) const
     {
-        return r >= o.from && r < o.to ? fetch<Stream>(o.p + r * (32 * E)) : edge(o.first + r * (32 * E));
+        return r >= o.from && r < o.to ? fetch<true>(o.p + r * (32 * E)) : edge(o.first + r * (32 * E));
     }
     // The first token of 16 bytes, `skew` early.
     DG_DEVICE int place(int w, int r, int l, int e) const
@@ -1358,7 +1357,7 @@ struct Sampler {
         __syncthreads();
         const float ref = weight.eighths(m);
         const Own mine_rows = own();
-        auto load_row = [&](int r) -> uint4 { return load<true>(mine_rows, r); };
+        auto load_row = [&](int r) -> uint4 { return load(mine_rows, r); };
         rows_ahead<kAhead>([&](const uint4 &v, int) {
             float x[E];
             Vec<T>::unpack(v, x);
