@@ -456,8 +456,8 @@ struct Sampler {
     // 16 bytes of the row (-inf past its ends).  Stream: not to be kept in L1, of which
     // little is left beside the shared memory.  Top-p's passes gain from it (64 fp32 rows of
     // 262144, mixed: 83 -> 73 us; 256, top-p: 354 -> 294), those of fp32 rows do all (maxima
-    // 56 -> 54, sums 146 -> 141); the maxima of bf16 rows do by themselves (80 -> 72), but
-    // whatever follows them is slower by as much (sums 225 -> 233).
+    // 56 -> 54, sums 146 -> 141); the maxima of bf16 rows do not (72 either way), and what
+    // follows them is slower (sums 210 -> 220).
     template <bool Stream>
     DG_DEVICE static uint4 fetch(const T *p)
     {
