@@ -335,8 +335,11 @@ DG_DEVICE float2 two_div(float n_hi, float n_lo, float d_hi, float d_lo)
 // its latency counts: sums of two floats, off by less than 2^-28 beside the result's
 // own rounding, in place of arithmetic in 64 bits (1.5 us of a row's 14).  With
 // all = 2^n g, g about 1, ln g = 2 (s + s^3 / 3 + ...), s = (g - 1) / (g + 1), |s| < 0.172.
-__device__ __noinline__ float logprob_of(float x, float m, float t, uint64_t all, float shift)
+// Where its own weight w is nearly all, from what is left of that, whose rounding the
+// result's size bounds: 0 for a token that is kept alone.
+__device__ __noinline__ float logprob_of(float x, float m, float t, uint64_t w, uint64_t all, float shift)
 {
+    if (all - w <= w >> 4) return -log1pf(static_cast<float>(all - w) / static_cast<float>(w));
     constexpr float kLn2 = 0.693145752f, kLn2Low = 1.42860677e-6f;   // (the first: 16 bits)
     int n = 63 - __clzll(static_cast<long long>(all));
     const uint64_t top = all << (63 - n);                            // g 2^63
@@ -1079,7 +1082,7 @@ struct Sampler {
                 }
             }
         }
-        say(token, value, all);
+        say(token, value, w_of(value) >> kDrop, all);
     }
 
     // The draw from all that lies above v and `kept` of the tokens at v, summed by s.
@@ -1103,15 +1106,16 @@ struct Sampler {
         });
         const uint32_t mine = best;
         best = largest(best, 0).x;
-        if (mine == best && best != 0) say(static_cast<int>(~best) - skew, value, all);   // (one thread has it)
+        if (mine == best && best != 0) say(static_cast<int>(~best) - skew, value, w_of(value) >> kDrop, all);   // (one has it)
     }
 
-    DG_DEVICE void say(int token, float value, uint64_t all) const
+    // w: its weight in the sums' units, as it is counted in `all`.
+    DG_DEVICE void say(int token, float value, uint64_t w, uint64_t all) const
     {
         a.token[row] = token;
         if (a.logprob == nullptr) return;
-        if (flat) a.logprob[row] = logprob_of(0.f, 0.f, 1.f, all, 0.f);
-        else a.logprob[row] = logprob_of(value, m, t, all, weight.shift());
+        if (flat) a.logprob[row] = logprob_of(0.f, 0.f, 1.f, w, all, 0.f);
+        else a.logprob[row] = logprob_of(value, m, t, w, all, weight.shift());
     }
 
     // ------------------------------------------------------------ few tokens
@@ -1254,7 +1258,7 @@ struct Sampler {
             // (rem == 0: the first one, however light)
             if (rem == 0 ? e == 0 : at <= rem && rem < at + w) {
                 const int place = static_cast<int>(sh.list[e] >> 32);
-                say(place - skew, Vec<T>::widen(base[place]), part);
+                say(place - skew, Vec<T>::widen(base[place]), w, part);
             }
             at += w;
         }
@@ -1300,7 +1304,7 @@ struct Sampler {
             first &= !lower;
         }
         // (rem == 0: the first one, however light)
-        if (rem == 0 ? first : sum <= rem && rem < sum + w) say(static_cast<int>(at) - skew, value_of(key), part);
+        if (rem == 0 ? first : sum <= rem && rem < sum + w) say(static_cast<int>(at) - skew, value_of(key), w, part);
     }
 
     // Lists a thread's hits among 16 bytes' tokens.

@@ -290,3 +290,34 @@ def test_masks_of_finite_values(dtype, value, first, last):
             check(x, T=[T] * 8, k=k, u=torch.full((8,), u))
         check(x, T=[T] * 8, k=k, p=[0.9] * 8, low=[0.0, 0.01] * 4)
         check(x, T=[T] * 8, p=[0.3, 0.9, 0.999, 1.0] * 2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_logprob_of_a_token_that_is_nearly_all(dtype):
+    """0 for a token that is kept alone, by whichever filter; else off by its own rounding, the others' weights' (2^-28 of
+    themselves, which is the result's size) and what all 41 are cut off by, each by up to 2^-43: 41 x 2^-43 < 2^-37."""
+    for V in (1, 50, 3001, 151643):
+        x = logits(6, V, 3, dtype)
+        u = torch.full((6,), 0.7, device=DEV)
+        token, logprob = torch.zeros(6, dtype=torch.int32, device=DEV), torch.full((6,), 5.0, device=DEV)
+        t, p, low = (torch.full((6,), v, device=DEV) for v in (1e-4, 1e-6, 1.0))
+        k = torch.full((6,), 300, dtype=torch.int32, device=DEV)
+        x[torch.arange(6), torch.arange(6) * (V // 7)] = 20.0           # one that leads (bf16 has ties)
+        xd = x.to(DEV)
+        for args in (dict(temperature=t), dict(top_p=p), dict(top_p=p, top_k=k), dict(min_p=low), dict(temperature=t, top_k=k),
+                     dict(min_p=low, top_p=p)):
+            dg.sample_logits(xd, token, u, logprob=logprob.fill_(5.0), **args)
+            assert (logprob == 0).all() and token.tolist() == [r * (V // 7) for r in range(6)], (V, list(args))
+    x = torch.full((16, 41), -math.inf)
+    x[:, 0] = 0.0
+    for r in range(16):
+        x[r, 1:] = -3.0 - 1.5 * r
+    x = x.to(dtype)
+    u = torch.zeros(16, device=DEV)
+    token, logprob = torch.ones(16, dtype=torch.int32, device=DEV), torch.zeros(16, device=DEV)
+    for args in (dict(), dict(top_k=torch.full((16,), 40, dtype=torch.int32, device=DEV))):
+        dg.sample_logits(x.to(DEV), token, u, logprob=logprob, **args)
+        n = 39 if args else 40
+        want = -torch.log1p(n * torch.exp(x[:, 1].double()))
+        assert (token == 0).all()
+        assert ((logprob.cpu().double() - want).abs() <= want.abs() * 2 ** -21 + 2 ** -37 + 2 ** -26 * (want < -0.06)).all(), (logprob, want)
