@@ -42,6 +42,7 @@
 // error of about 2^-29 (see Weights): a token's place among the sums of a whole
 // vocabulary would be lost in 32 bits, and sums of integers do not depend on their
 // order.
+#include <cfloat>
 #include <cstddef>
 
 #include "dg_paged_device.cuh"
@@ -797,7 +798,7 @@ struct Sampler {
     }
 
     // Where the tokens reach k in number or, with `Mass`, `target` in weight, of those
-    // from `floor_v` on.  Tokens of weight 0 do not count; none: there are too few.
+    // from `floor_v` on.  Tokens too light to be drawn do not count; none: there are too few.
     // With `Mass` it may be one of the cut's neighbours (the weights are rounded).
     template <bool Mass>
     DG_DEVICE Cut select(uint32_t k, float target, float floor_v)
@@ -819,31 +820,40 @@ struct Sampler {
         });
         const Found f1 =
             find<Mass>(k, target, [&](int b) -> float { return exp2f(-b / kBinsLog2) * (1.f / kMassOne); });
-        if (f1.bin < 0) return Cut{-INFINITY, 0, 0};
-        // that bin's tokens by their place in it
+        // Past the last bin, 64 factors of 2 below the largest, tokens add nothing to a sum of
+        // weights, but they are of the first k: those are found by their bits alone.
+        const bool past = !Mass && f1.bin < 0;
+        if (f1.bin < 0 && !past) return Cut{-INFINITY, 0, 0};
+        // else that bin's tokens by their place in it
         const float b1 = static_cast<float>(f1.bin);
         auto y2_of = [&](float y) -> int { return min(static_cast<int>((y - b1) * kBins), kBins - 1); };
         auto inside = [&](float x, float y) -> bool {
             return x >= floor_v && y < static_cast<float>(kBins) && static_cast<int>(y) == f1.bin;
         };
-        hist = clear();
-        each([&](float x, int, int) {
-            const float y = y_of(x);
-            if (inside(x, y)) atomicAdd(hist + y2_of(y), 1u);
-        });
         uint32_t before = Mass ? 0 : f1.before;
         float above = f1.mass;
-        const Found f2 = find<Mass>(k - before, target - above, [&](int b) -> float {
-            return exp2f(-(b1 + (static_cast<float>(b) + 0.5f) * (1.f / kBins)) / kBinsLog2);
-        });
-        if (f2.bin < 0) return Cut{-INFINITY, 0, 0};
+        Found f2{};
+        if (past) {
+            floor_v = fmaxf(floor_v, fmaxf(light(), -FLT_MAX));
+            before = f1.total;
+        } else {
+            hist = clear();
+            each([&](float x, int, int) {
+                const float y = y_of(x);
+                if (inside(x, y)) atomicAdd(hist + y2_of(y), 1u);
+            });
+            f2 = find<Mass>(k - before, target - above, [&](int b) -> float {
+                return exp2f(-(b1 + (static_cast<float>(b) + 0.5f) * (1.f / kBins)) / kBinsLog2);
+            });
+            if (f2.bin < 0) return Cut{-INFINITY, 0, 0};
+            before += f2.before;
+            above += f2.mass;
+        }
         // and by their bits
-        before += f2.before;
-        above += f2.mass;
         uint32_t hi = 0, lo = 0, ties = f2.count;
         each([&](float x, int, int) {
             const float y = y_of(x);
-            if (inside(x, y) && y2_of(y) == f2.bin) {
+            if (past ? x >= floor_v && !(y < static_cast<float>(kBins)) : inside(x, y) && y2_of(y) == f2.bin) {
                 hi = max(hi, order_of(x));
                 lo = max(lo, ~order_of(x));
             }
@@ -851,7 +861,8 @@ struct Sampler {
         const uint2 ends = largest(hi, lo);
         hi = ends.x;
         lo = ~ends.y;
-        while (hi > lo) {
+        if (hi < lo) return Cut{-INFINITY, 0, 0};            // (none past the last bin)
+        while (hi > lo || past) {                            // (those have not been counted)
             const int shift = max(0, 22 - __clz(hi - lo));
             hist = clear();
             each([&](float x, int, int) {

@@ -1,0 +1,43 @@
+"""GPU tests of dg_sample_logits where its filters' borders lie far down the row, or among tokens that weigh next to
+nothing."""
+import math
+
+import pytest
+import torch
+
+import block_diffusion_decoding_gb300 as dg
+from tests._paged import DEV
+from tests.test_gpu_sample import check, logits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("ctas", [None, "1", "16"])
+def test_top_k_holds_for_u_of_zero(monkeypatch, ctas, dtype):
+    """k above 1024, the k-th token more than 64 factors of 2 below the largest: u = 0 draws the first token of the
+    vocabulary among the first k, however light, and none behind them."""
+    if ctas is not None:
+        monkeypatch.setenv("DG_SAMPLE_CTAS", ctas)
+    x = logits(8, 20000, 11, dtype)
+    k = [1025, 1100, 1500, 2000, 3000, 4000, 5000, 19999]
+    zero = torch.zeros(8)
+    for T in (0.02, 0.05, 0.1, 0.3):
+        got = check(x, T=[T] * 8, k=k, u=zero, exact=True).tolist()
+        for r in range(7):
+            assert got[r] in torch.sort(x[r], descending=True, stable=True).indices[:k[r]].tolist(), (T, r)
+        check(x, T=[T] * 8, k=k, u=zero, low=[1e-30, 1e-36, 0.0, 1e-20] * 2, exact=True)
+        check(x, T=[T] * 8, k=k, u=torch.full((8,), 0.4), p=[0.9, 1.0] * 4)
+        check(x, T=[T] * 8, k=k, u=torch.ones(8))
+    if dtype is torch.float32:                           # (weights by 64-bit arithmetic)
+        check(x + 1e5, T=[0.05] * 8, k=k, u=zero, exact=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_top_k_among_more_equal_tokens_than_are_sorted(dtype):
+    """The k-th token among thousands of its value, which a list does not hold: the first of them by index are kept."""
+    x = logits(8, 20000, 12, dtype, spread=1.5).round()
+    k = [1000, 1024, 900, 700, 500, 1023, 2, 1500]
+    for T in (0.02, 0.05, 1.0):
+        for u in (0.0, 0.5, 1.0):
+            check(x, T=[T] * 8, k=k, u=torch.full((8,), u), exact=u == 0.0)
