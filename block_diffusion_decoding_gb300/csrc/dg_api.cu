@@ -1113,7 +1113,7 @@ int pool_args(PagePoolArgs &a, const dg_page_pool *pool, const dg_paged_cache *c
 }
 
 // ---------------------------------------------------------------- draws from logits
-constexpr int kSampleMaxV = 393216;      // 2^19 tokens' weights fit the sums
+constexpr int kSampleMaxV = 393216;      // tokens whose weights fit a sum (kWeightBits)
 
 int sample_kernels(DeviceInfo &di)
 {

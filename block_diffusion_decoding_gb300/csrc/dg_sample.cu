@@ -41,7 +41,7 @@
 // The exact weights exp((x - max) / T) are 64-bit fixed-point numbers with a relative
 // error of about 2^-29 (see Weights): a token's place among the sums of a whole
 // vocabulary would be lost in 32 bits, and sums of integers do not depend on their
-// order.
+// order, nor on the number of CTAs that share a row.
 #include <cfloat>
 #include <cstddef>
 
@@ -61,9 +61,9 @@ constexpr int kMassBins = 256;           // of top-p's: 8 to a factor of 2
 constexpr int kGroupBytes = 32;          // of the maxima of a thread's groups: 8, of bf16 tokens 16
 constexpr int kList = 1536;              // tokens that are sorted at most
 constexpr int kListMost = 1024;          // of which top-k's k
-constexpr int kLaneBits = 53;            // a weight of 1 in a lane's sums: up to 1600 tokens
-constexpr int kSumBits = 43;             // in all others: up to 2^19
-constexpr int kDrop = kLaneBits - kSumBits;
+// A weight of 1, up to 393216 of which (and of 2^(1/64), see Weights) fit a sum.  Each one
+// is cut off to this by itself: a sum is the same however its tokens are shared out.
+constexpr int kWeightBits = 45;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // Neighbours that top-p's cut is moved over at most.  The rounded weights put it
 // within 1e-5 of the row's weight, a few tokens of any vocabulary.
@@ -250,10 +250,10 @@ __device__ __noinline__ uint64_t weight_in_double(float x, float m, float ch, fl
 {
     const double t = (static_cast<double>(x) - static_cast<double>(m)) *
                      (static_cast<double>(ch) + static_cast<double>(cl));
-    return t > -60. ? static_cast<uint64_t>(exp2(t) * 9007199254740992.) : 0;
+    return t > -60. ? static_cast<uint64_t>(exp2(t) * 35184372088832.) : 0;   // 2^kWeightBits
 }
 
-// Weights 2^(c x - reference), c = log2 e / T, as 64-bit integers, 2^53 for 1.
+// Weights 2^(c x - reference), c = log2 e / T, as 64-bit integers, 2^kWeightBits for 1.
 // c x is taken in units of 1/32: P, its nearest whole number, comes out of one
 // multiply-add with a large constant, exactly; what is left of it, |r| <= 1/64, of a
 // second, rounded at 2^-31, and c's low half with it.  Then 2^(j / 32) from a table
@@ -275,13 +275,13 @@ struct Weights {
         m = max;
         ch = 1.442695041f / t;
         cl = (fmaf(-ch, t, 1.442695041f) + 1.92596299e-8f) / t;   // log2 e in two parts
-        floor = max - 57.f / ch;                         // (2^-53 is the last that counts)
+        floor = max - 48.f / ch;                         // (2^-45 is the last that counts)
         ref = __float_as_int(fmaf(max, ch, 393216.f));   // 1.5 x 2^18: a unit in the last place is 1/32
         wide = !(fabsf(max) * ch < 65536.f);
     }
     // What the table holds at place p.
     DG_DEVICE uint32_t turned(int p) const { return kExpTable[(p - ref) & 31]; }
-    // log2 of what a weight of 2^53 stands for beside exp((x - max) / T) = 1, at most
+    // log2 of what a weight of 2^kWeightBits stands for beside exp((x - max) / T) = 1, at most
     // 1/64 (what the multiply-add cuts off is below 2^-31)
     DG_DEVICE float shift() const
     {
@@ -313,7 +313,7 @@ struct Weights {
         const float B = fmaf(r, s, 0.046875f);           // 1.5 x 2^-5: in units of 2^-28
         const uint32_t T = table[p & 31];
         const uint32_t Y = __float_as_uint(B) - (__float_as_uint(0.046875f) - (1u << 28));   // 2^28 (1 + y)
-        return static_cast<uint64_t>(T) * Y >> (ref + 31 + 32 * (58 - kLaneBits) - p >> 5);  // (by 5 .. 63)
+        return static_cast<uint64_t>(T) * Y >> (ref + 31 + 32 * (58 - kWeightBits) - p >> 5);  // (by 13 .. 62)
     }
     DG_DEVICE uint64_t in_double(float x) const { return weight_in_double(x, m, ch, cl); }
 };
@@ -331,7 +331,7 @@ DG_DEVICE float2 two_div(float n_hi, float n_lo, float d_hi, float d_lo)
     return make_float2(q, (fmaf(-q, d_lo, fmaf(-q, d_hi, n_hi)) + n_lo) / d_hi);
 }
 
-// A drawn token's logprob: (x - m) / t less ln of `all`, of which 2^kSumBits stands for
+// A drawn token's logprob: (x - m) / t less ln of `all`, of which 2^kWeightBits stands for
 // 2^shift of the largest weight.  One thread does this at the end of a row's way, so
 // its latency counts: sums of two floats, off by less than 2^-28 beside the result's
 // own rounding, in place of arithmetic in 64 bits (1.5 us of a row's 14).  With
@@ -359,7 +359,7 @@ __device__ __noinline__ float logprob_of(float x, float m, float t, uint64_t w, 
     const float2 d = two_sum(0.5f * x, -0.5f * m);
     const float2 at = two_div(d.x, d.y, t, 0.f);
     if (!(at.x > -1e37f)) return -INFINITY;
-    const float e = static_cast<float>(n - kSumBits);
+    const float e = static_cast<float>(n - kWeightBits);
     const float2 one = two_sum(2.f * at.x, -e * kLn2);
     const float2 two = two_sum(one.x, -2.f * s.x);
     return two.x + (two.y + one.y + 2.f * at.y - 2.f * s.y - fmaf(e, kLn2Low, fmaf(shift, 0.69314718f, series * q * s.x)));
@@ -440,15 +440,10 @@ struct Sampler {
 
     DG_DEVICE uint64_t w_of(float x) const
     {
-        return flat ? (x == m ? 1ull << kLaneBits : 0) : weight(x, sh.table);
+        return flat ? (x == m ? 1ull << kWeightBits : 0) : weight(x, sh.table);
     }
     // The least logit that is ever drawn: further down weights are zeros of 64-bit floats.
     DG_DEVICE float light() const { return flat ? m : fmaf(-745.13f, t, m); }
-    // n tokens of weight w in the units of the sums
-    DG_DEVICE static uint64_t times(uint64_t w, uint64_t n)
-    {
-        return n * (w >> kDrop) + (n * (w & ((1u << kDrop) - 1)) >> kDrop);
-    }
 
     // A barrier of the row's threads.
     DG_DEVICE void sync() const
@@ -892,13 +887,13 @@ struct Sampler {
         int buf;
     };
     // Hands a lane's sums out by segment (a warp's stretch of the row) and adds them up;
-    // with Whole another one, whose sum alone is wanted.  more_above: in the sums' units.
+    // with Whole another one, whose sum alone is wanted.
     template <bool Whole = false>
     DG_DEVICE Sums gather(uint64_t above, uint32_t ties, uint64_t *whole = nullptr, uint64_t more_above = 0)
     {
-        above = (above >> kDrop) + more_above;
+        above += more_above;
         ties = __reduce_add_sync(kAll, ties);
-        uint64_t more = Whole ? *whole >> kDrop : 0;
+        uint64_t more = Whole ? *whole : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             above += __shfl_xor_sync(kAll, above, o);
@@ -975,17 +970,16 @@ struct Sampler {
         }
         before -= ties;
         const int64_t left = kept - tie_prefix - before;
-        const uint64_t mine = above + times(w, left <= 0 ? 0 : left < ties ? left : ties);
+        const uint64_t mine = above + w * static_cast<uint64_t>(left <= 0 ? 0 : left < ties ? left : ties);
         uint64_t end = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint64_t x = __shfl_up_sync(kAll, end, o);
             if (lane >= o) end += x;
         }
-        const uint32_t past = __ballot_sync(kAll, end > rem && mine > 0), any = __ballot_sync(kAll, mine > 0);
-        const int at = past != 0 ? __ffs(past) - 1 : any != 0 ? 31 - __clz(any) : 0;
-        const uint64_t begin = __shfl_sync(kAll, end - mine, at), size = __shfl_sync(kAll, mine, at);
-        rem = past != 0 ? rem - begin : size > 0 ? size - 1 : 0;     // (sums round off: the last one)
+        // (all of them weigh more than rem: the parts' sums are exact)
+        const int at = __ffs(__ballot_sync(kAll, end > rem) | 1u << 31) - 1;
+        rem -= __shfl_sync(kAll, end - mine, at);
         tie_prefix += __shfl_sync(kAll, before, at);
         return at;
     }
@@ -1038,7 +1032,6 @@ struct Sampler {
                 if (x[e] > v) above += w_of(x[e]);
                 ties += x[e] == v && v > -INFINITY ? 1u : 0u;
             }
-            above >>= kDrop;
         };
         for (int r = warp; r < a.rows_warp; r += kSampleWarps) {
             uint64_t above;
@@ -1076,30 +1069,15 @@ struct Sampler {
             token = place(seg, r, l, e) - skew;
             value = x[e];
             sum += w;
-            if (sum > rem << kDrop) break;
+            if (sum > rem) break;
         }
-        if (token < 0) {
-            // (parts too small to count beside the rest: the segment's last kept token)
-            prefix = sh.tie_prefix;
-            for (int k = 0; k < a.rows_warp * 32; ++k) {
-                Vec<T>::unpack(load(seg, k / 32, k % 32), x);
-                for (int e = 0; e < E; ++e) {
-                    const bool tie = x[e] == v && v > -INFINITY;
-                    if ((x[e] > v || (tie && prefix < kept)) && x[e] >= light()) {
-                        token = place(seg, k / 32, k % 32, e) - skew;
-                        value = x[e];
-                    }
-                    prefix += tie ? 1 : 0;
-                }
-            }
-        }
-        say(token, value, w_of(value) >> kDrop, all);
+        say(token, value, w_of(value), all);
     }
 
     // The draw from all that lies above v and `kept` of the tokens at v, summed by s.
     DG_DEVICE void draw_from(float v, int64_t kept, const Sums &s, float u)
     {
-        const uint64_t all = s.above + times(v > -INFINITY ? w_of(v) : 0, kept);
+        const uint64_t all = s.above + (v > -INFINITY ? w_of(v) : 0) * kept;
         const uint64_t rem = min(u < 1.f ? part_of(all, u, false) : all - 1, all - 1);
         if (rem > 0) {
             draw(v, kept, s, rem, all);
@@ -1117,7 +1095,7 @@ struct Sampler {
         });
         const uint32_t mine = best;
         best = largest(best, 0).x;
-        if (mine == best && best != 0) say(static_cast<int>(~best) - skew, value, w_of(value) >> kDrop, all);   // (one has it)
+        if (mine == best && best != 0) say(static_cast<int>(~best) - skew, value, w_of(value), all);   // (one has it)
     }
 
     // w: its weight in the sums' units, as it is counted in `all`.
@@ -1231,7 +1209,7 @@ struct Sampler {
         int per = (most + kSampleThreads - 1) / kSampleThreads, first = threadIdx.x * per;
         uint64_t sum = 0, listed, part;
         for (int e = first; e < min(first + per, most); ++e) {
-            const uint64_t w = w_of(value_of(sh.list[e])) >> kDrop;
+            const uint64_t w = w_of(value_of(sh.list[e]));
             sh.mass[e] = w;
             sum += w;
         }
@@ -1287,7 +1265,7 @@ struct Sampler {
 #pragma unroll 8
             for (int o = 0; o < n; ++o) before += sh.list[o] < key ? 1 : 0;
             sh.moved[before] = key;
-            sh.mass[before] = w_of(value_of(key)) >> kDrop;
+            sh.mass[before] = w_of(value_of(key));
         }
         __syncthreads();
         const int most = k > 0 ? min(k, n) : n;
@@ -1484,7 +1462,7 @@ struct Sampler {
                 if (b < lo2.bin)                 // above them after all
                     atomicAdd(reinterpret_cast<unsigned long long *>(sh.mass) +
                                   (static_cast<uint32_t>(key[e]) / size - rank * kSampleWarps),
-                              static_cast<unsigned long long>(w_of(x) >> kDrop));
+                              static_cast<unsigned long long>(w_of(x)));
                 key[e] = 0;
             }
             __syncthreads();
@@ -1511,11 +1489,11 @@ struct Sampler {
             sort_values(n);
             const int per = (n + kSampleThreads - 1) / kSampleThreads, first = threadIdx.x * per;
             uint64_t sum = 0, listed;
-            for (int e = first; e < min(first + per, n); ++e) sum += w_of(value_of(sh.list[e])) >> kDrop;
+            for (int e = first; e < min(first + per, n); ++e) sum += w_of(value_of(sh.list[e]));
             uint64_t before = s.above + scan(sum, &listed) - sum;
             for (int e = first; e < min(first + per, n); ++e) {
                 const float x = value_of(sh.list[e]);
-                const uint64_t w = w_of(x) >> kDrop;
+                const uint64_t w = w_of(x);
                 if (before < need && before + w >= need) {
                     uint32_t ties = 1;
                     for (int o = e - 1; o >= 0 && value_of(sh.list[o]) == x; --o) ++ties;
@@ -1529,7 +1507,7 @@ struct Sampler {
             const int kept = static_cast<int>(cut.ties), size = E * 32 * a.rows_warp;
             for (int e = threadIdx.x; e < kept; e += kSampleThreads)
                 atomicAdd(reinterpret_cast<unsigned long long *>(segment) + static_cast<uint32_t>(sh.list[e]) / size,
-                          static_cast<unsigned long long>(w_of(value_of(sh.list[e])) >> kDrop));
+                          static_cast<unsigned long long>(w_of(value_of(sh.list[e]))));
             __syncthreads();
             if (warp == 0 && kept > 0) {
                 const uint64_t kept_all = sh.all;
@@ -1731,9 +1709,9 @@ struct Sampler {
         if (part) {
             const Sums s = sums(by_k.v);
             whole = s.above;
-            if (by_k.v > -INFINITY) whole += times(w_of(by_k.v), min(by_k.first, s.ties));
+            if (by_k.v > -INFINITY) whole += w_of(by_k.v) * min(by_k.first, s.ties);
             if (!flat)
-                v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 8796093022208.f) * exp2f(weight.shift())),
+                v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 35184372088832.f) * exp2f(weight.shift())),
                                           by_k.v).v);
         }
         Sums s = sums(v);
@@ -1749,12 +1727,12 @@ struct Sampler {
                     if (x > v) up = max(up, ~order_of(x));
                 });
                 v = of_order(~largest(up, 0).x);
-            } else if (s.above + times(wv, kept) >= need || !(v > least)) {
+            } else if (s.above + wv * kept >= need || !(v > least)) {
                 // the fewest at the cut that reach it
                 const uint64_t short_of = need > s.above ? need - s.above : 0;
                 int64_t n = 0;
                 for (int64_t step = 1 << 20; step > 0; step >>= 1)
-                    if (n + step <= kept && times(wv, n + step) < short_of) n += step;
+                    if (n + step <= kept && wv * (n + step) < short_of) n += step;
                 kept = min(kept, n + 1);
                 break;
             } else {                                         // one down

@@ -358,9 +358,11 @@ int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const in
 /* logits [R, V] fp32 or bf16, rows row_stride elements apart (>= V, 0: V);    */
 /* temperature, top_k, top_p, min_p [R], each NULL for 1, 0, 1, 0; u [R] fp32   */
 /* in [0, 1); token [R] int32, logprob [R] fp32 or NULL.  All device; logits    */
-/* 16-byte aligned (its rows need not be).  Weights and their sums are 64-bit   */
-/* fixed-point numbers, 2^-43 of the largest, weights with a relative error of  */
-/* 2^-28: results do not depend on the order of any sum.  Needs no workspace.   */
+/* 16-byte aligned (its rows need not be).  Weights are 64-bit fixed-point      */
+/* numbers with a relative error of 2^-28, each cut off to 2^-45 of the         */
+/* largest, and their sums are exact: results depend neither on the order of    */
+/* any sum nor on how a row is shared out, so not on what else is in its batch. */
+/* Needs no workspace.                                                          */
 /* Supported: R <= 2^26; V <= 393216.  R == 0 is allowed.                       */
 #define DG_LOGITS_BF16 0
 #define DG_LOGITS_FP32 1

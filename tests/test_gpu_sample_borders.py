@@ -41,3 +41,39 @@ def test_top_k_among_more_equal_tokens_than_are_sorted(dtype):
     for T in (0.02, 0.05, 1.0):
         for u in (0.0, 0.5, 1.0):
             check(x, T=[T] * 8, k=k, u=torch.full((8,), u), exact=u == 0.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_split_of_a_row_changes_no_bit(monkeypatch, dtype):
+    """Tokens and log probabilities are the same for any number of CTAs a row, and for a row alone and in a batch."""
+    V, R = 150001, 12
+    x = logits(R, V, 21, dtype)
+    x[4:8] = x[4:8] * 0.1 - 30.0                         # one token, and many that weigh next to nothing
+    x[4:8, 777] = 1.0
+    x[8:10] = -31.0
+    x[8:10, 100000] = 0.0
+    xd = x.to(DEV)
+    f = lambda v: torch.tensor(v, device=DEV)  # noqa: E731
+    ways = [dict(), dict(top_p=f([0.9, 0.5, 0.99, 0.9999] * 3)), dict(min_p=f([0.01, 1e-12, 0.0, 1e-5] * 3)),
+            dict(top_k=f([50, 1024, 1500, 100000] * 3).int(), top_p=f([0.95] * R))]
+
+    def draw(x, u, args):
+        token = torch.full((x.shape[0],), -9, dtype=torch.int32, device=DEV)
+        logprob = torch.full((x.shape[0],), 5.0, device=DEV)
+        dg.sample_logits(x, token, u, logprob=logprob, **args)
+        return token.tolist(), logprob.view(torch.int32).tolist()
+
+    g = torch.Generator().manual_seed(1)
+    for way in ways:
+        for u in [torch.rand(R, generator=g) for _ in range(4)] + [torch.zeros(R), torch.full((R,), 1 - 2.0 ** -24)]:
+            u = u.to(DEV)
+            got = []
+            for ctas in ("1", "2", "4", "8", "16"):
+                monkeypatch.setenv("DG_SAMPLE_CTAS", ctas)
+                got.append(draw(xd, u, way))
+            monkeypatch.delenv("DG_SAMPLE_CTAS")
+            got.append(draw(xd, u, way))
+            for r in range(R):
+                one = draw(xd[r:r + 1].clone(), u[r:r + 1].clone(), {n: t[r:r + 1].clone() for n, t in way.items()})
+                assert (one[0][0], one[1][0]) == (got[0][0][r], got[0][1][r]), (list(way), r)
+            assert all(a == got[0] for a in got), list(way)
