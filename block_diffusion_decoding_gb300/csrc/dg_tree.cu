@@ -32,7 +32,9 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(TreePlanArg
     const int t = blockIdx.x * kTreePlanThreads + threadIdx.x;
     if (t < a.B) {
         const int r0 = __ldg(a.q_start + t), r1 = __ldg(a.q_start + t + 1), kv = __ldg(a.kv_len + t);
-        if (r0 < 0 || r1 < r0 || r1 > a.T || kv < 0 || kv > a.max_kv) report_error(a.ws, DG_ERR_DEVICE, 1101);
+        // (lengths that count the nodes are at least as many)
+        if (r0 < 0 || r1 < r0 || r1 > a.T || kv < (a.appended ? r1 - r0 : 0) || kv > a.max_kv)
+            report_error(a.ws, DG_ERR_DEVICE, 1101);
     }
     if (t >= a.T) return;
     // the last sequence that begins at or before this row
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(TreePlanArg
     }
     if (a.positions != nullptr) {
         const int kv = min(max(__ldg(a.kv_len + lo), 0), a.max_kv);
-        a.positions[t] = (a.appended ? kv - s.n : kv) + depth - 1;
+        a.positions[t] = max(a.appended ? kv - s.n : kv, 0) + depth - 1;
     }
 }
 

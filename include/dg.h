@@ -289,7 +289,8 @@ int dg_paged_attn(const uint16_t *q, int64_t q_stride, const uint16_t *k_new, in
 /* they were.  A parent that is not a lower index or -1 counts as -1; a node  */
 /* past 32 mask_words is not in the mask (not seen by itself either), and a   */
 /* path is followed for 4096 nodes; lengths and rows are cut as the attention */
-/* cuts them; each records DG_ERR_DEVICE.                                     */
+/* cuts them, and a base below 0 (kv_len[b] < n_b where it counts them) counts */
+/* as 0; each records DG_ERR_DEVICE.                                          */
 /* workspace: 256 bytes, for the status word.                                 */
 /* Supported: 1 <= mask_words <= 128; T == 0 is allowed.                      */
 size_t dg_tree_plan_workspace(void);
