@@ -65,9 +65,11 @@ constexpr int kListMost = 1024;          // of which top-k's k
 // is cut off to this by itself: a sum is the same however its tokens are shared out.
 constexpr int kWeightBits = 45;
 constexpr unsigned kAll = 0xFFFFFFFFu;
-// Neighbours that top-p's cut is moved over at most.  The rounded weights put it
-// within 1e-5 of the row's weight, a few tokens of any vocabulary.
-constexpr int kMoves = 1 << 14;
+// Tokens that top-p's cut of fp32 rows is moved over before it is looked for further off.
+// The rounded weights put it within 1e-5 of the row's weight: mostly where it is or beside
+// it, but where p is next to 1 that may be thousands of light tokens (2000 of 262144
+// normal logits times 3, p = 0.99995: 20 ms token by token, 0.39 as it is).
+constexpr int kNeighbours = 2;
 
 struct Found {
     int bin;                             // -1: the target lies past the last one
@@ -1696,6 +1698,21 @@ struct Sampler {
         return true;
     }
 
+    // The values that a token may have by their place in the order, which the lower bits of a
+    // bf16 number's order do not change.
+    static constexpr int kUnused = E == 8 ? 16 : 0;
+    DG_DEVICE static uint32_t place_in_order(float v) { return order_of(v) >> kUnused; }
+    DG_DEVICE static float value_in_order(uint32_t at)
+    {
+        return of_order(E == 8 ? at << 16 | (at >> 15 ? 0u : 0xFFFFu) : at);
+    }
+    // The least of them that is not below x.
+    DG_DEVICE static float value_from(float x)
+    {
+        const uint32_t o = order_of(x);
+        if (E == 4) return x;
+        return of_order(o >> 31 ? (o + 0xFFFFu) & ~0xFFFFu : o | 0xFFFFu);
+    }
     // The cuts by counting: top-k's, min-p's, top-p's; the highest is the one.
     DG_DEVICE void draw_counted(int k, float p, float min_value, float u)
     {
@@ -1703,7 +1720,7 @@ struct Sampler {
         Cut by_k{-INFINITY, 0, 0};
         if (flat) by_k = Cut{m, k > 0 ? static_cast<uint32_t>(k) : ~0u, 0};
         else if (k > 0) by_k = select<false>(k, 0.f, -INFINITY);
-        const float least = fmaxf(by_k.v, min_value);
+        const float least = value_from(fmaxf(by_k.v, min_value));
         float v = least;
         uint64_t whole = 0;                                  // what top-p is the part of
         if (part) {
@@ -1714,20 +1731,20 @@ struct Sampler {
                 v = fmaxf(v, select<true>(0, p * (static_cast<float>(whole) * (1.f / 35184372088832.f) * exp2f(weight.shift())),
                                           by_k.v).v);
         }
+        // Top-p's cut by exact sums, from v on.  By its place in the order it is one of lo .. hi,
+        // which each sum narrows: by steps that grow (in fp32 rows, whose tokens are far apart
+        // there, after a few neighbours), then by halves, 45 sums at most.
+        uint32_t at = place_in_order(v), lo = place_in_order(least), hi = place_in_order(m);
+        uint32_t step = E == 8 ? 1 : 1 << 12;
         Sums s = sums(v);
         int64_t kept;
         for (int moves = 0;; ++moves) {
             const uint64_t wv = v > -INFINITY ? w_of(v) : 0;
             kept = v == by_k.v ? min(by_k.first, s.ties) : s.ties;
-            if (!part || moves == kMoves) break;
+            if (!part) break;
             const uint64_t need = part_of(whole, p, true);
-            if (s.above >= need && s.above > 0) {            // reached before: one up
-                uint32_t up = 0;
-                each([&](float x, int, int) {
-                    if (x > v) up = max(up, ~order_of(x));
-                });
-                v = of_order(~largest(up, 0).x);
-            } else if (s.above + wv * kept >= need || !(v > least)) {
+            const bool up = s.above >= need;                 // reached before
+            if (lo >= hi || (!up && (s.above + wv * kept >= need || !(v > least)))) {
                 // the fewest at the cut that reach it
                 const uint64_t short_of = need > s.above ? need - s.above : 0;
                 int64_t n = 0;
@@ -1735,15 +1752,23 @@ struct Sampler {
                     if (n + step <= kept && wv * (n + step) < short_of) n += step;
                 kept = min(kept, n + 1);
                 break;
-            } else {                                         // one down
-                uint32_t down = 0;
-                each([&](float x, int, int) {
-                    if (x < v && x >= least) down = max(down, order_of(x));
-                });
-                down = largest(down, 0).x;
-                if (down == 0 || of_order(down) == -INFINITY) break;
-                v = of_order(down);
             }
+            if (up) lo = at + 1;
+            else hi = at - 1;
+            if (E == 4 && moves < kNeighbours) {
+                uint32_t near = 0;
+                each([&](float x, int, int) {
+                    if (up ? x > v : x < v && x >= least) near = max(near, up ? ~order_of(x) : order_of(x));
+                });
+                near = largest(near, 0).x;
+                at = (up ? ~near : near) >> kUnused;
+            } else {
+                const uint32_t half = hi > lo ? (hi - lo) / 2 : 0;
+                at = up ? lo + min(half, step) : hi - min(half, step);
+                step = min(step, 1u << 28) * 4;
+            }
+            at = min(max(at, lo), max(lo, hi));
+            v = value_in_order(at);
             s = sums(v);
         }
         end_draw<T>(a, sh, handed(), v, kept, s.above, s.ties, s.buf, u);

@@ -43,6 +43,33 @@ def test_top_k_among_more_equal_tokens_than_are_sorted(dtype):
             check(x, T=[T] * 8, k=k, u=torch.full((8,), u), exact=u == 0.0)
 
 
+def test_top_p_next_to_one_in_a_long_tail():
+    """One token that is nearly all, and hundreds of thousands beside it: 2^-24 of the whole weight are thousands of
+    them, and top-p's border lies among them.  The time is bounded too: a border is found by halving, not token by
+    token."""
+    V, rows = 262144, [(-24, 0.3, 0.999995), (-26, 0.5, 0.999999), (-20, 1.0, 0.99995), (-22, 0.1, 0.99999),
+                       (-26, 0.5, 1 - 2.0 ** -24), (-24, 0.3, 0.9999999), (-18, 0.01, 0.999), (-23, 2.0, 0.9999)]
+    R = len(rows)
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(R, V, generator=g) * torch.tensor([s for _, s, _ in rows])[:, None]
+    x += torch.tensor([float(m) for m, _, _ in rows])[:, None]
+    x[torch.arange(R), torch.randint(V, (R,), generator=g)] = 0.0
+    p = [p for _, _, p in rows]
+    for u in (1.0, 1.0 - 2.0 ** -24, 1.0 - 2.0 ** -23, 1.0 - 2.0 ** -21, 0.5, 0.0):
+        check(x, p=p, u=torch.full((R,), u))
+        check(x, p=p, u=torch.full((R,), u), k=[200000, 0] * 4, low=[0.0, 0.0, 1e-14, 1e-11] * 2)
+    check(x.bfloat16(), p=p, u=torch.ones(R))
+    xd, token = x.to(DEV), torch.zeros(R, dtype=torch.int32, device=DEV)
+    pd, ud = torch.tensor(p, device=DEV), torch.full((R,), 0.5, device=DEV)
+    at = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for _ in range(2):
+        at[0].record()
+        dg.sample_logits(xd, token, ud, top_p=pd)
+        at[1].record()
+    torch.cuda.synchronize()
+    assert at[0].elapsed_time(at[1]) < 20.0              # (some 50 passes of 10 us)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_the_split_of_a_row_changes_no_bit(monkeypatch, dtype):
     """Tokens and log probabilities are the same for any number of CTAs a row, and for a row alone and in a batch."""
