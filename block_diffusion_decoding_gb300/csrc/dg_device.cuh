@@ -111,6 +111,16 @@ DG_DEVICE void griddep_launch_dependents()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// An address as it is known here: a load from it, volatile or not, is behind every
+// volatile asm before this (griddep_wait), for which the compiler has no other reason
+// where the load is an asm without side effects.
+template <class T>
+DG_DEVICE T *behind_waits(T *p)
+{
+    asm volatile("" : "+l"(p) : : "memory");
+    return p;
+}
+
 // ------------------------------------------------------------------------
 // mbarrier
 // ------------------------------------------------------------------------

@@ -425,7 +425,7 @@ struct Sampler {
     {
         const int64_t at = row * a.stride;
         skew = static_cast<int>(at & (E - 1));
-        base = static_cast<const T *>(a.logits) + (at - skew);
+        base = behind_waits(static_cast<const T *>(a.logits) + (at - skew));
         ready();
     }
     DG_DEVICE void ready()
@@ -458,7 +458,9 @@ struct Sampler {
     // little is left beside the shared memory.  Top-p's passes gain from it (64 fp32 rows of
     // 262144, mixed: 83 -> 73 us; 256, top-p: 354 -> 294), those of fp32 rows do all (maxima
     // 56 -> 54, sums 146 -> 141); the maxima of bf16 rows do not (72 either way), and what
-    // follows them is slower (sums 210 -> 220).
+    // follows them is slower (sums 210 -> 220).  As a volatile load, in the order of all
+    // other accesses, it costs top-p's passes 8 to 13% (64 fp32 rows of 262144, p = 0.9: 82
+    // and 93): what it has to stay behind is the wait for the kernel that wrote the logits.
     template <bool Stream>
     DG_DEVICE static uint4 fetch(const T *p)
     {
@@ -466,7 +468,7 @@ struct Sampler {
         uint4 v;
         asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-            : "l"(p));
+            : "l"(p));                           // (an address that is known behind the wait alone)
         return v;
     }
     // ... that the row's first or last token is among, or none.
