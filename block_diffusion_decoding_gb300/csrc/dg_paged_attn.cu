@@ -30,13 +30,15 @@
 // an infinite value stays the infinity it is.  This kernel serves few rows, whose
 // time is the memory's, so the second product is free, and the output is off by
 // little more than its own rounding (with one bf16 P by sqrt 2 of that).
-// Trees take neither way: their items are of more rows, and with the code of both in
-// the loop of tiles their softmax is a memory tile's time long.  32 trees of 10 to 32
+// Trees keep the halves but do not share columns: their items are of more rows, and the
+// code of both ways in the loop of tiles costs more than it gives.  32 trees of 10 to 32
 // nodes over caches of up to 16000 tokens (16 query heads on 8, D = 128, 1.04 GB) take
-// 175 us, 88% of a plain copy's rate, with a row in one lane and one bf16 P; 188 with
-// the columns of up to 64 rows shared out between the warps, 221 with the halves of P
-// kept, 333 with both.  The output is off by sqrt 2 of its own rounding, as the pair
-// kernel's.
+// 175-178 us, 86% of a plain copy's rate; 197 with the sharing.  A tree's mask words are
+// read where a tile needs them: kept in registers across the wait for its scores they
+// cost the whole loop (221 and 240 in those two forms).  One bf16 P takes 170, and 12.4
+// in place of 14.6 for one tree of 16 nodes over 300 keys, whose three tiles wait for the
+// second product; its output is off by 2.3e-3 of its size, this by 1.7e-3, as the plain
+// form's rounded once.
 // A tile whose end is past the last key is loaded, and multiplied with P,
 // only up to the next multiple of 16 keys; the softmax warps zero the V rows
 // between the last key and there, so that whatever bits the page holds behind
@@ -234,12 +236,11 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     const uint32_t pa = tmem + Gm::ColS + (np & 1) * BKV;
                     if (lead) {
                         umma_bf16_ts(tmem + Gm::ColO, pa, dv, idesc_o, jp != 0);
-                        if (!kPagedTree<Args>) umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2, dv, idesc_o, 1);
+                        umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2, dv, idesc_o, 1);
                         auto both = [&](int kk) {
                             umma_bf16_ts(tmem + Gm::ColO, pa + kk * 8, dv + kk * 128, idesc_o, 1);
-                            if (!kPagedTree<Args>)
-                                umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2 + kk * 8, dv + kk * 128, idesc_o,
-                                             1);
+                            umma_bf16_ts(tmem + Gm::ColO, pa + BKV / 2 + kk * 8, dv + kk * 128, idesc_o,
+                                         1);
                         };
                         if (steps == BKV / 16) {
 #pragma unroll
@@ -359,11 +360,6 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                                        make_float2(a.scale_log2, a.scale_log2), make_float2(nm, nm));
                 const float2 p2 = make_float2(fast_exp2(d2.x), fast_exp2(d2.y));
                 acc = add2(acc, p2);
-                if constexpr (kPagedTree<Args>) {
-                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(p2.x, p2.y);
-                    hi = *reinterpret_cast<const uint32_t *>(&h2);
-                    return;
-                }
                 // p down to the bf16 below the one it is cut off to
                 const int px = __viaddmax_s32(__float_as_int(p2.x), -0x10000, 0) & ~0xFFFF;
                 const int py = __viaddmax_s32(__float_as_int(p2.y), -0x10000, 0) & ~0xFFFF;
@@ -389,16 +385,9 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                 // first and last visible column
                 const int c_hi = a.causal ? min(valid - 1, last - key0) : valid - 1;
                 int c_lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-                // a tree's columns, a bit each
-                uint32_t nodes[BKV / 32];
-                if constexpr (kPagedTree<Args>) {
-                    // (the window cuts the cached keys alone)
-                    const int node0 = key0 - (a.has_new ? p.kv : p.kv - p.n);
-                    c_lo = min(c_lo, max(0, -node0));
-#pragma unroll
-                    for (int w = 0; w < BKV / 32; ++w)
-                        nodes[w] = border ? paged_nodes(a, p, i, node0 + 32 * w) : 0xFFFFFFFFu;
-                }
+                // (a tree's window cuts the cached keys alone)
+                const int node0 = key0 - (a.has_new ? p.kv : p.kv - p.n);
+                if (kPagedTree<Args>) c_lo = min(c_lo, max(0, -node0));
                 ok = mbar_wait_poll(&s_full[sb], (it >> 1) & 1u, a.ws, 942);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
@@ -452,8 +441,12 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                     if constexpr (kPagedTree<Args>) {
                         if (border) {
 #pragma unroll
-                            for (int c = 0; c < BKV; ++c)
-                                if (!(nodes[c / 32] >> (c & 31) & 1u)) sr[c] = __float_as_uint(-INFINITY);
+                            for (int w = 0; w < BKV / 32; ++w) {
+                                const uint32_t nodes = paged_nodes(a, p, i, node0 + 32 * w);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (!(nodes >> c & 1u)) sr[32 * w + c] = __float_as_uint(-INFINITY);
+                            }
                         }
                     }
                     // the scale is positive, so the scaled maximum is the maximum scaled
@@ -472,7 +465,7 @@ __device__ __forceinline__ void paged_attn_body(const CUtensorMap *map_k, const 
                         for (int c = 0; c < 16; ++c)
                             weigh(sr[c0 + 2 * c], sr[c0 + 2 * c + 1], nm, acc, hi[c], lo[c]);
                         tmem_st16(ts + c0 / 2, hi);
-                        if (!kPagedTree<Args>) tmem_st16(ts + BKV / 2 + c0 / 2, lo);
+                        tmem_st16(ts + BKV / 2 + c0 / 2, lo);
                     }
                     l += acc.x + acc.y;
                     tmem_wait_st();

@@ -47,10 +47,9 @@
  *     DG_PAGED_KERNEL (single | pair) and DG_SAMPLE_CTAS (1 .. 16: CTAs that
  *     share a row of logits) force a choice; a choice the shapes do
  *     not allow is ignored.  Results do not depend on the choice beyond
- *     floating-point summation order (paged attention: and the rounding of the
- *     softmax weights, one bf16 in the pair kernel and in both of the trees',
- *     two in the other single one; the
- *     pair kernel takes batches of more than 128 rows of a kv head, tokens x
+ *     floating-point summation order (paged attention, trees' included: and the
+ *     rounding of the softmax weights, one bf16 in the pair kernel, two in the
+ *     single one; the pair kernel takes batches of more than 128 rows of a kv head, tokens x
  *     its query heads, a sequence on average, so the last bits of a token's
  *     row depend on what else is in its batch).
  */
