@@ -104,3 +104,18 @@ def test_the_split_of_a_row_changes_no_bit(monkeypatch, dtype):
                 one = draw(xd[r:r + 1].clone(), u[r:r + 1].clone(), {n: t[r:r + 1].clone() for n, t in way.items()})
                 assert (one[0][0], one[1][0]) == (got[0][0][r], got[0][1][r]), (list(way), r)
             assert all(a == got[0] for a in got), list(way)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [262145, 393216])
+def test_sums_of_the_longest_rows_hold(V, dtype):
+    """Equal logits fill a row's sum to its last bit: token floor(u V) of whole numbers, by every way, at temperatures
+    that put the largest weight at either end of its range."""
+    R = 6
+    x = torch.full((R, V), -3.296875, dtype=dtype)
+    T = [0.77, 1.0, 0.3, 3.1, 1.7, 0.9]
+    for u in (torch.arange(R) / 8.0 + 2.0 ** -10, torch.full((R,), 1 - 2.0 ** -24), torch.zeros(R)):
+        check(x, T=T, u=u, exact=True)
+        check(x, T=T, u=u, p=[0.5, 0.75, 0.3, 0.9, 0.99, 0.999969482421875], exact=True)
+        check(x, T=T, u=u, k=[1025, 2000, 100000, V - 1, 1, 300000], exact=True)
+        check(x, T=T, u=u, k=[1025, 2000, 100000, V - 1, 1, 300000], p=[0.5] * R, low=[0.5] * R, exact=True)
