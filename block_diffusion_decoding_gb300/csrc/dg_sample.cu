@@ -24,14 +24,18 @@
 // What bounds it is not the one read of the logits that it cannot do without (the first
 // pass; the later ones find much of the row in L2), but instructions and, where rows are
 // few, barriers and latencies in a row.  On one GB300, us, beside that read at a copy's
-// rate:
-//                                    floor  greedy  none  top-k  top-k and top-p  top-p
-//   1 row of 16384 bf16                0.0     8     12     12         14           22
-//   1 of 262144 fp32                   0.2     8     15     17         17           35
-//   64 of 262144 fp32                  9.9    16     41     36         33           89
-//   1024 of 151643 bf16               45.8    70    210    114        108          469
-// (calls back to back, 6 us of which are the host's).  Without a filter a token takes 34
-// instructions in all, on 59% of the issue slots (512 rows of 151643, in a profile).
+// rate, normal logits times 3:
+//                         floor  greedy  none  k 50  k 50, p 0.9  p 0.9  min-p 0.05  k 5000  p 0.99995
+//   1 row of 16384 bf16     0.0     7     11    10       10         28        9         37       80
+//   1 of 262144 fp32        0.2     6     15    15       15         40       13         50      375
+//   64 of 262144 fp32       9.9    16     40    27       28         80       26        121     1031
+//   1024 of 151643 bf16    45.8    71    206   100       99        462       98        585     1839
+// (calls back to back, 6 us of which are the host's).  The last two are cut by counting.
+// Without a filter a token takes 34 instructions in all, on 60% of the issue slots (512
+// rows of 151643, in a profile); greedy rows wait for memory, and at a block's end for one
+// another, with 44% of an SM's warps there (64 registers), on 38% of the slots.  Where the
+// list is of one value, 1500 equal logits, its sort compares each with all: 1 row of 16384,
+// k = 1000, 44 in place of 21.
 // Tried and no better: the row a few pieces ahead through asynchronous copies to shared
 // memory (the last line's none, then 225, -> 233; top-p on one row 46.4 -> 44.7), prefetches of the
 // rows to come into L2 (its 122, then, -> 133), fewer CTAs an SM, to spread clusters (no

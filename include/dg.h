@@ -340,9 +340,11 @@ int dg_paged_tree_commit(const int32_t *tokens, const int32_t *parents, const in
                          int32_t *kv_len_out, void *workspace, size_t workspace_bytes,
                          void *stream);
 
-/* Draws a token from each row of logits.  With x the row's logits, m the     */
-/* largest, w_i = exp((x_i - m) / T), and its tokens in the order (logit       */
-/* falling, index rising), kept are the tokens in all of                       */
+/* Draws a token from each row of logits, which are the caller's: its model's  */
+/* hidden states times the head's weight, by a matrix product of its own (the  */
+/* steps below fold the head into their sampler and write no logits).  With x   */
+/* the row's logits, m the largest, w_i = exp((x_i - m) / T), and its tokens in  */
+/* the order (logit falling, index rising), kept are the tokens in all of        */
 /*   the first top_k of the order (top_k <= 0: all);                           */
 /*   the shortest prefix of those whose weight is at least top_p of theirs     */
 /*     (top_p >= 1: all; <= 0: the first token);                               */
